@@ -1,6 +1,8 @@
 // The C ABI (include/wq.h): argument validation, per-shape dispatch, TMA descriptor
 // encoding, status strings and the device error word.
 #include <atomic>
+#include <cmath>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/wq.h"
@@ -541,7 +543,8 @@ wq_status wq_read_error_flags(uint32_t* out) {
   if (cudaDeviceSynchronize() != cudaSuccess) return WQ_ERR_CUDA;
   *out = wq::gemv_read_and_clear_error() | wq::gemm_tc_read_and_clear_error() |
          wq::gptq_read_and_clear_error() | wq::gptq_factor_read_and_clear_error() |
-         wq::selftest_read_and_clear_error() | wq::fp8_read_and_clear_error();
+         wq::selftest_read_and_clear_error() | wq::fp8_read_and_clear_error() |
+         wq::rope_read_and_clear_error() | wq::attn_read_and_clear_error() | wq::lora_read_and_clear_error();
   return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
@@ -552,6 +555,243 @@ wq_status wq_selftest_wait_timeout(uint32_t limit_us, uint32_t* timed_out, void*
   if (st != WQ_OK) return st;
   return from_cuda(wq::run_selftest_wait(static_cast<uint64_t>(limit_us) * 1000ull, timed_out,
                                          static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ the attention block
+static bool dtype_ok(wq_dtype t) { return t == WQ_DTYPE_BF16 || t == WQ_DTYPE_F16; }
+
+static bool page_ok(int64_t page_size) {
+  return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128;
+}
+
+// Two byte ranges share a byte.
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+static wq_status check_rope(wq_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, const uint16_t* Q,
+                            int64_t q_stride, const uint16_t* K, int64_t k_stride, const uint16_t* q_weight,
+                            const uint16_t* k_weight, float eps, const float* cos_sin, int64_t max_pos, int64_t rot,
+                            int interleaved, const int32_t* positions, uint16_t* Qo) {
+  if (!dtype_ok(dtype) || (interleaved != 0 && interleaved != 1) || !(eps >= 0.f) || !std::isfinite(eps)) return WQ_ERR_ARG;
+  if (!Q || !K || !cos_sin || !positions || !Qo) return WQ_ERR_NULL;
+  if (T < 1 || T > (1LL << 30) || Hq < 1 || Hkv < 1 || Hq > (1 << 16) || Hkv > (1 << 16)) return WQ_ERR_SHAPE;
+  if (d != 64 && d != 128 && d != 256) return WQ_ERR_SHAPE;
+  if (rot < 16 || rot > d || rot % 16 != 0 || max_pos < 1 || max_pos > (1LL << 30)) return WQ_ERR_SHAPE;
+  if (q_stride < Hq * d || k_stride < Hkv * d || q_stride % 8 != 0 || k_stride % 8 != 0 || q_stride > (1LL << 40) ||
+      k_stride > (1LL << 40))
+    return WQ_ERR_SHAPE;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(cos_sin) || !aligned16(positions) || !aligned16(Qo) ||
+      (q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)))
+    return WQ_ERR_ALIGN;
+  const size_t q_bytes = (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2;
+  if (overlap(Q, q_bytes, Qo, static_cast<size_t>(T) * Hq * d * 2) && !(Qo == Q && (q_stride == Hq * d || T == 1)))
+    return WQ_ERR_ARG;
+  return WQ_OK;
+}
+
+static wq::RopeArgs rope_args(int64_t T, int64_t Hq, int64_t Hkv, int64_t d, const uint16_t* Q, int64_t q_stride,
+                              const uint16_t* K, int64_t k_stride, const uint16_t* q_weight, const uint16_t* k_weight,
+                              float eps, const float* cos_sin, int64_t max_pos, int64_t rot, int interleaved,
+                              const int32_t* positions, uint16_t* Qo) {
+  wq::RopeArgs a{};
+  a.Q = Q, a.K = K;
+  a.q_stride = q_stride, a.k_stride = k_stride;
+  a.q_weight = q_weight, a.k_weight = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_pos = static_cast<int>(max_pos), a.rot = static_cast<int>(rot), a.interleaved = interleaved;
+  a.positions = positions;
+  a.Qo = Qo;
+  a.T = static_cast<int>(T), a.Hq = static_cast<int>(Hq), a.Hkv = static_cast<int>(Hkv), a.d = static_cast<int>(d);
+  return a;
+}
+
+wq_status wq_qk_norm_rope(wq_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, const uint16_t* Q,
+                          int64_t q_stride, const uint16_t* K, int64_t k_stride, const uint16_t* q_weight,
+                          const uint16_t* k_weight, float eps, const float* cos_sin, int64_t max_pos, int64_t rot,
+                          int interleaved, const int32_t* positions, uint16_t* Qo, uint16_t* Ko, void* stream) {
+  wq_status st = check_rope(dtype, T, Hq, Hkv, d, Q, q_stride, K, k_stride, q_weight, k_weight, eps, cos_sin, max_pos,
+                            rot, interleaved, positions, Qo);
+  if (st != WQ_OK) return st;
+  if (!Ko) return WQ_ERR_NULL;
+  if (!aligned16(Ko)) return WQ_ERR_ALIGN;
+  const size_t q_in = (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2;
+  const size_t k_in = (static_cast<size_t>(T - 1) * k_stride + Hkv * d) * 2;
+  const size_t q_out = static_cast<size_t>(T) * Hq * d * 2, k_out = static_cast<size_t>(T) * Hkv * d * 2;
+  if (overlap(K, k_in, Ko, k_out) && !(Ko == K && (k_stride == Hkv * d || T == 1))) return WQ_ERR_ARG;
+  if (overlap(Q, q_in, Ko, k_out) || overlap(Qo, q_out, Ko, k_out) || overlap(K, k_in, Qo, q_out)) return WQ_ERR_ARG;
+  st = check_device_cached();
+  if (st != WQ_OK) return st;
+  wq::RopeArgs a = rope_args(T, Hq, Hkv, d, Q, q_stride, K, k_stride, q_weight, k_weight, eps, cos_sin, max_pos, rot,
+                             interleaved, positions, Qo);
+  a.Ko = Ko;
+  return from_cuda(wq::launch_qk_norm_rope(dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
+wq_status wq_qk_norm_rope_cache(wq_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, const uint16_t* Q,
+                                int64_t q_stride, const uint16_t* K, int64_t k_stride, const uint16_t* V,
+                                int64_t v_stride, const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                                const float* cos_sin, int64_t max_pos, int64_t rot, int interleaved,
+                                const int32_t* positions, uint16_t* Qo, uint16_t* k_cache, uint16_t* v_cache,
+                                int64_t pages, int64_t page_size, const int32_t* slots, void* stream) {
+  wq_status st = check_rope(dtype, T, Hq, Hkv, d, Q, q_stride, K, k_stride, q_weight, k_weight, eps, cos_sin, max_pos,
+                            rot, interleaved, positions, Qo);
+  if (st != WQ_OK) return st;
+  if (!V || !k_cache || !v_cache || !slots) return WQ_ERR_NULL;
+  if (v_stride < Hkv * d || v_stride % 8 != 0 || v_stride > (1LL << 40)) return WQ_ERR_SHAPE;
+  if (!page_ok(page_size) || pages < 1 || pages > 0x7fffffffLL / page_size) return WQ_ERR_SHAPE;
+  if (!aligned16(V) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(slots)) return WQ_ERR_ALIGN;
+  const size_t q_in = (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2, q_out = static_cast<size_t>(T) * Hq * d * 2;
+  const size_t k_in = (static_cast<size_t>(T - 1) * k_stride + Hkv * d) * 2;
+  const size_t v_in = (static_cast<size_t>(T - 1) * v_stride + Hkv * d) * 2;
+  const size_t pool = static_cast<size_t>(pages) * page_size * Hkv * d * 2;
+  if (overlap(K, k_in, Qo, q_out) || overlap(V, v_in, Qo, q_out)) return WQ_ERR_ARG;
+  for (const uint16_t* c : {k_cache, v_cache})
+    if (overlap(Q, q_in, c, pool) || overlap(K, k_in, c, pool) || overlap(V, v_in, c, pool) || overlap(Qo, q_out, c, pool))
+      return WQ_ERR_ARG;
+  if (overlap(k_cache, pool, v_cache, pool)) return WQ_ERR_ARG;
+  st = check_device_cached();
+  if (st != WQ_OK) return st;
+  wq::RopeArgs a = rope_args(T, Hq, Hkv, d, Q, q_stride, K, k_stride, q_weight, k_weight, eps, cos_sin, max_pos, rot,
+                             interleaved, positions, Qo);
+  a.V = V, a.v_stride = v_stride;
+  a.k_cache = k_cache, a.v_cache = v_cache;
+  a.pages = pages, a.page_size = static_cast<int>(page_size);
+  a.slots = slots;
+  return from_cuda(wq::launch_qk_norm_rope(dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
+static bool attn_shape_ok(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new) {
+  return T >= 1 && T <= (1 << 24) && R >= 1 && R <= (1 << 24) && Hkv >= 1 && Hq >= 1 && Hq <= 1024 && Hq % Hkv == 0 &&
+         (d == 64 || d == 128) && max_new >= 1 && max_new <= T;
+}
+
+size_t wq_attn_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new) {
+  if (!attn_shape_ok(T, R, Hq, Hkv, d, max_new)) return 0;
+  return wq::attn_workspace_bytes(T, R, Hq, Hkv, d, max_new);
+}
+
+wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_stride, int64_t T, int64_t R, int64_t Hq,
+                                int64_t Hkv, int64_t d, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,
+                                int64_t page_size, const int32_t* prefix_pages, int64_t prefix_len,
+                                const int32_t* block_table, int64_t max_blocks, const int32_t* suffix_lens,
+                                const int32_t* q_start, int64_t max_new, float scale, uint16_t* O, float* lse,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dtype) || !(scale > 0.f) || !std::isfinite(scale)) return WQ_ERR_ARG;
+  if (!Q || !k_cache || !v_cache || !O) return WQ_ERR_NULL;
+  if (!attn_shape_ok(T, R, Hq, Hkv, d, max_new) || q_stride < Hq * d || q_stride % 8 != 0 || q_stride > (1LL << 40))
+    return WQ_ERR_SHAPE;
+  if (!page_ok(page_size) || pages < 1 || pages > 0x7fffffffLL / Hkv) return WQ_ERR_SHAPE;
+  if (prefix_len < 0 || prefix_len > (1LL << 30) || max_blocks < 0 || max_blocks > (1LL << 30) / page_size)
+    return WQ_ERR_SHAPE;
+  if (!q_start && (T != R || max_new != 1)) return WQ_ERR_SHAPE;
+  if ((prefix_len > 0 && !prefix_pages) || (max_blocks > 0 && (!block_table || !suffix_lens))) return WQ_ERR_NULL;
+  const auto odd4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+  if (!aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(O) || odd4(lse) || odd4(prefix_pages) ||
+      odd4(block_table) || odd4(suffix_lens) || odd4(q_start))
+    return WQ_ERR_ALIGN;
+  if (overlap(Q, (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2, O, static_cast<size_t>(T) * Hq * d * 2))
+    return WQ_ERR_ARG;
+  if (!workspace || ws_bytes < wq::attn_workspace_bytes(T, R, Hq, Hkv, d, max_new)) return WQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WQ_ERR_ALIGN;
+  wq_status st = check_device_cached();
+  if (st != WQ_OK) return st;
+  wq::AttnArgs a{};
+  a.Q = Q, a.q_stride = q_stride;
+  a.T = static_cast<int>(T), a.R = static_cast<int>(R), a.Hq = static_cast<int>(Hq), a.Hkv = static_cast<int>(Hkv);
+  a.d = static_cast<int>(d);
+  a.k_cache = k_cache, a.v_cache = v_cache;
+  a.pages = pages, a.page_size = static_cast<int>(page_size);
+  a.prefix_pages = prefix_pages, a.prefix_len = static_cast<int>(prefix_len);
+  a.block_table = block_table, a.max_blocks = static_cast<int>(max_blocks), a.suffix_lens = suffix_lens;
+  a.q_start = q_start, a.max_new = static_cast<int>(max_new);
+  a.scale = scale;
+  a.O = O, a.lse = lse;
+  return from_cuda(wq::launch_attn_shared_prefix(dtype, a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+static bool lora_shape_ok(int64_t M, int64_t K, int64_t N, int64_t r) {
+  return M >= 1 && N >= 1 && K >= 8 && K % 8 == 0 && r >= 8 && r <= 128 && r % 8 == 0 && M <= (1 << 24) &&
+         N <= (1 << 24) && K <= (1 << 24);
+}
+
+static wq_status check_lora(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint16_t* A, const uint16_t* B,
+                            int64_t L, int64_t r, const int32_t* ranks, const int32_t* adapter, const float* scales,
+                            const uint16_t* Y) {
+  if (!X || !A || !B || !adapter || !scales || !Y) return WQ_ERR_NULL;
+  if (!lora_shape_ok(M, K, N, r) || L < 1 || L > (1 << 24)) return WQ_ERR_SHAPE;
+  const auto odd4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+  if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || odd4(ranks) || odd4(adapter) || odd4(scales))
+    return WQ_ERR_ALIGN;
+  return WQ_OK;
+}
+
+size_t wq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
+  if (!lora_shape_ok(M, K, N, r)) return 0;
+  return wq::kWsHeaderBytes + wq::lora_scratch_bytes(M, K, N, r);
+}
+
+wq_status wq_lora_add(wq_dtype dtype, const uint16_t* base, const uint16_t* X, int64_t M, int64_t K, int64_t N,
+                      const uint16_t* A, const uint16_t* B, int64_t L, int64_t r, const int32_t* ranks,
+                      const int32_t* adapter, const float* scales, uint16_t* Y, void* workspace, size_t ws_bytes,
+                      void* stream) {
+  if (!dtype_ok(dtype)) return WQ_ERR_ARG;
+  if (!base) return WQ_ERR_NULL;
+  wq_status st = check_lora(X, M, K, N, A, B, L, r, ranks, adapter, scales, Y);
+  if (st != WQ_OK) return st;
+  if (!aligned16(base)) return WQ_ERR_ALIGN;
+  const size_t y_bytes = static_cast<size_t>(M) * N * 2;
+  if ((base != Y && overlap(base, y_bytes, Y, y_bytes)) || overlap(X, static_cast<size_t>(M) * K * 2, Y, y_bytes))
+    return WQ_ERR_ARG;
+  if (!workspace || ws_bytes < wq_lora_workspace_bytes(M, K, N, r)) return WQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WQ_ERR_ALIGN;
+  st = check_device_cached();
+  if (st != WQ_OK) return st;
+  const wq::LoraArgs a{base, X, A, B, static_cast<int>(M), static_cast<int>(K), static_cast<int>(N), static_cast<int>(L),
+                       static_cast<int>(r), ranks, adapter, scales, Y};
+  void* scratch = static_cast<uint8_t*>(workspace) + wq::kWsHeaderBytes;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = wq::launch_lora_shrink(dtype, a, scratch, s);
+  if (e != cudaSuccess) return WQ_ERR_CUDA;
+  return from_cuda(wq::launch_lora_expand(dtype, a, scratch, s));
+}
+
+// The layer's own workspace (or the shared header, where that is longer), then the adapters' scratch.
+static size_t lora_scratch_offset(wq_fmt fmt, int64_t M, int64_t K, int64_t N) {
+  const size_t need = wq_gemm_workspace_bytes(fmt, M, K, N);
+  return round_up256(need > wq::kWsHeaderBytes ? need : wq::kWsHeaderBytes);
+}
+
+size_t wq_gemm_w4a16_lora_workspace_bytes(wq_fmt fmt, int64_t M, int64_t K, int64_t N, int64_t r) {
+  if ((fmt != WQ_FMT_INT4_G128_ASYM && fmt != WQ_FMT_MXFP4) || !lora_shape_ok(M, K, N, r)) return 0;
+  return lora_scratch_offset(fmt, M, K, N) + wq::lora_scratch_bytes(M, K, N, r);
+}
+
+wq_status wq_gemm_w4a16_lora(wq_fmt fmt, const uint16_t* X, int64_t M, int64_t K, int64_t N, const int32_t* Wq,
+                             const void* scales, const uint16_t* zeros, const uint16_t* A, const uint16_t* B, int64_t L,
+                             int64_t r, const int32_t* ranks, const int32_t* adapter, const float* lora_scales,
+                             uint16_t* Y, void* workspace, size_t ws_bytes, void* stream) {
+  wq_status st = check_linear_args(fmt, X, M, K, N, Wq, scales, zeros, Y);
+  if (st != WQ_OK) return st;
+  st = check_lora(X, M, K, N, A, B, L, r, ranks, adapter, lora_scales, Y);
+  if (st != WQ_OK) return st;
+  if (overlap(X, static_cast<size_t>(M) * K * 2, Y, static_cast<size_t>(M) * N * 2)) return WQ_ERR_ARG;
+  if (!workspace || ws_bytes < wq_gemm_w4a16_lora_workspace_bytes(fmt, M, K, N, r)) return WQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WQ_ERR_ALIGN;
+  st = check_device_cached();
+  if (st != WQ_OK) return st;
+  const wq::LoraArgs a{Y, X, A, B, static_cast<int>(M), static_cast<int>(K), static_cast<int>(N), static_cast<int>(L),
+                       static_cast<int>(r), ranks, adapter, lora_scales, Y};
+  const size_t off = lora_scratch_offset(fmt, M, K, N);
+  void* scratch = static_cast<uint8_t*>(workspace) + off;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = wq::launch_lora_shrink(WQ_DTYPE_BF16, a, scratch, s);
+  if (e != cudaSuccess) return WQ_ERR_CUDA;
+  st = wq_gemm_w4a16(fmt, X, M, K, N, Wq, scales, zeros, Y, workspace, off, stream);
+  if (st != WQ_OK) return st;
+  return from_cuda(wq::launch_lora_expand(WQ_DTYPE_BF16, a, scratch, s));
 }
 
 wq_status wq_check_device(void) { return check_device_cached(); }

@@ -20,6 +20,7 @@ enum : uint32_t {
   kErrDrain = 1u << 4,        // TMA drain at exit gave up
   kErrSelftestWait = 1u << 5, // the diagnostic wait of wq_selftest_wait_timeout ran out (expected)
   kErrNotPositiveDefinite = 1u << 6,  // GPTQ factor: a Cholesky pivot of H was not positive
+  kErrIndex = 1u << 7,        // an index read on the device lies outside its range (entry skipped or clamped)
 };
 
 // About two seconds of polling, measured on the global nanosecond timer.

@@ -12,6 +12,8 @@ namespace wq {
 
 // Format codes (same values as wq_fmt in include/wq.h).
 enum Fmt : int { kInt4G128 = 0, kMxfp4 = 1 };
+// 16-bit element types of the attention-block operators (same values as wq_dtype).
+enum Dtype : int { kBf16 = 0, kF16 = 1 };
 
 // Epilogue of the linear layer.  kEpiSwiglu: the weight is the fused gate+up projection of
 // 2F rows with gate and up rows interleaved in blocks of 8 (row 16q + i is gate row 8q + i,
@@ -128,6 +130,63 @@ cudaError_t launch_mx_weights_to_e4m3(const int32_t* Wq, const uint8_t* scales, 
 cudaError_t launch_quant_w4a4_act(const uint16_t* X, int64_t M, int64_t K, uint8_t* X8, float* sx,
                                   cudaStream_t stream);
 cudaError_t run_selftest_wait(uint64_t limit_ns, uint32_t* timed_out_host, cudaStream_t stream);
+
+// rope.cu -- head norm + position rotation of queries and keys, with the cache write.  Strides in
+// elements; `slots` null: K goes to Ko [T, Hkv, d], else K and V go to the pages of the cache.
+struct RopeArgs {
+  const uint16_t *Q, *K, *V;
+  int64_t q_stride, k_stride, v_stride;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  const float* cos_sin;
+  int max_pos, rot, interleaved;
+  const int32_t* positions;
+  uint16_t *Qo, *Ko;
+  uint16_t *k_cache, *v_cache;
+  const int32_t* slots;
+  int64_t pages;
+  int page_size;
+  int T, Hq, Hkv, d;
+};
+cudaError_t launch_qk_norm_rope(int dtype, const RopeArgs& a, cudaStream_t stream);
+uint32_t rope_read_and_clear_error();
+
+// attn.cu -- attention of a batch sharing a prefix, over a cache kept in pages
+struct AttnArgs {
+  const uint16_t* Q;
+  int64_t q_stride;
+  int T, R, Hq, Hkv, d;
+  const uint16_t *k_cache, *v_cache;
+  int64_t pages;
+  int page_size;
+  const int32_t* prefix_pages;
+  int prefix_len;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* suffix_lens;
+  const int32_t* q_start;
+  int max_new;
+  float scale;
+  uint16_t* O;
+  float* lse;
+};
+size_t attn_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new);
+cudaError_t launch_attn_shared_prefix(int dtype, const AttnArgs& a, void* ws, cudaStream_t stream);
+uint32_t attn_read_and_clear_error();
+
+// lora.cu -- low-rank adapters of many requests beside a shared projection: the shrink
+// V = X A^T into the scratch, then the expand Y = base + s V B^T
+struct LoraArgs {
+  const uint16_t *base, *X, *A, *B;
+  int M, K, N, L, r;
+  const int32_t *ranks, *adapter;
+  const float* scales;
+  uint16_t* Y;
+};
+size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
+cudaError_t launch_lora_shrink(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream);
+cudaError_t launch_lora_expand(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream);
+uint32_t lora_read_and_clear_error();
 
 // layout.cu -- row re-layout of the stacked gate+up weight
 cudaError_t launch_interleave_gate_up(const void* src, void* dst, int64_t F, int64_t row_bytes, cudaStream_t stream);

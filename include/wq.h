@@ -350,7 +350,7 @@ const char* wq_status_str(wq_status s);
 
 /*
  * Reads (and clears) the device-side error word of the current device: 0 when no bounded
- * wait ran out since the last read.  Synchronizes the device.  When a decode kernel's split-K
+ * wait ran out (and no index read on the device lay outside its range) since the last read.  Synchronizes the device.  When a decode kernel's split-K
  * wait ran out (bit 1 << 3), it also zeroes the scratch array of wq_gemv_w4a16_noalloc.
  */
 wq_status wq_read_error_flags(uint32_t* out);
@@ -435,6 +435,123 @@ wq_status wq_mxfp4_weights_to_e4m3(const int32_t* Wq, const uint8_t* scales, int
 wq_status wq_quantize_w4a4_activations(const uint16_t* X, int64_t M, int64_t K, uint8_t* Xq8, float* s_x,
                                        void* stream);
 wq_status wq_gemm_w4a4_mxfp4(const uint16_t* X, int64_t M, int64_t K, int64_t N, const uint8_t* Wq8, const float* s_w,
+                             uint16_t* Y, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The attention block around the quantized projections, for serving many requests at once:
+ * low-rank adapters beside a projection, the norm and rotation of queries and keys with the
+ * write to a cache in pages, and attention of a batch that shares a prefix.
+ *
+ * Common to the three
+ *   - dtype: the 16-bit type of every uint16_t array of the call (bf16 or IEEE fp16).
+ *   - A cache is two arrays k_cache, v_cache [pages, Hkv, page_size, d]; token `at` of page `p`
+ *     has slot number p * page_size + at.  page_size is 16, 32, 64 or 128.
+ *   - Indices that live on the device (positions, slots, adapters, pages, lengths) are checked
+ *     by the kernels: one outside its range never makes a kernel leave its arrays; bit 1 << 7 of
+ *     the error word (wq_read_error_flags) is set and the outputs that depend on the index are
+ *     unspecified.
+ *   - Sums, softmax statistics and norms are float32; outputs are rounded to dtype once.
+ *   - Results do not depend on what else runs on the device: no floating-point atomics.
+ */
+typedef enum { WQ_DTYPE_BF16 = 0, WQ_DTYPE_F16 = 1 } wq_dtype;
+
+/*
+ * Norm of every query and key head and rotation by the token's position, one pass:
+ *   x' = x / sqrt(mean(x^2) + eps) * w    over the head's d elements (weight NULL: x' = x);
+ *   with (c, s) the table's row at the token's position, each pair (a, b) of the head's first
+ *   `rot` elements becomes (a c - b s, b c + a s); the other d - rot elements stay x'.
+ *   interleaved = 0: pairs (i, i + rot/2);  interleaved = 1: pairs (2i, 2i + 1).
+ * The norm, the rotation and both products are float32, rounded to dtype once at the end.
+ *   Q [T, Hq, d], K [T, Hkv, d], V [T, Hkv, d]: a token's heads are contiguous, tokens are
+ *     q_stride / k_stride / v_stride elements apart (so the three may be parts of one fused
+ *     projection output); strides are multiples of 8 and at least the token's own size.
+ *   q_weight, k_weight [d] dtype, each may be NULL.
+ *   cos_sin [max_pos, rot] float32: rot/2 cosines, then rot/2 sines.   positions [T] int32.
+ *   Qo [T, Hq, d], Ko [T, Hkv, d] contiguous outputs.  Qo may be Q itself when q_stride ==
+ *     Hq d (Ko likewise); other overlaps are not allowed.
+ * wq_qk_norm_rope_cache writes keys (after norm and rotation) and values (as they are) to the
+ * cache instead: token t goes to slot slots[t] (int32); a negative slot writes neither (padding
+ * rows of a captured batch); slots of one call are distinct.
+ * Errors: WQ_ERR_ARG (dtype, interleaved, eps < 0 or not finite); WQ_ERR_NULL; WQ_ERR_SHAPE
+ *   unless T, Hq, Hkv, max_pos >= 1, d is 64, 128 or 256, rot % 16 == 0 with 16 <= rot <= d,
+ *   strides as above, pages >= 1, pages * page_size <= 2^31 - 1; WQ_ERR_ALIGN; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.
+ */
+wq_status wq_qk_norm_rope(wq_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, const uint16_t* Q,
+                          int64_t q_stride, const uint16_t* K, int64_t k_stride, const uint16_t* q_weight,
+                          const uint16_t* k_weight, float eps, const float* cos_sin, int64_t max_pos, int64_t rot,
+                          int interleaved, const int32_t* positions, uint16_t* Qo, uint16_t* Ko, void* stream);
+wq_status wq_qk_norm_rope_cache(wq_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, const uint16_t* Q,
+                                int64_t q_stride, const uint16_t* K, int64_t k_stride, const uint16_t* V,
+                                int64_t v_stride, const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                                const float* cos_sin, int64_t max_pos, int64_t rot, int interleaved,
+                                const int32_t* positions, uint16_t* Qo, uint16_t* k_cache, uint16_t* v_cache,
+                                int64_t pages, int64_t page_size, const int32_t* slots, void* stream);
+
+/*
+ * Attention of R requests that share a prefix of prefix_len tokens, each with its own further
+ * tokens (its suffix), over a cache in pages; the prefix's keys and values are read once for
+ * all requests:
+ *   O[t, h] = sum_j p_j v_j,  p = softmax_j(scale q[t, h] . k_j),  lse[t, h] = ln sum_j e^(scale q . k_j)
+ * over the prefix's keys and those of the request's own keys the token may see.  Query head h
+ * uses key/value head h / (Hq / Hkv).  The n new tokens of a request are the last n of its own
+ * keys (already in the cache): new token i sees own keys j <= suffix_lens[r] - n + i.  A row
+ * that sees no key (no prefix, no own key) gives O = 0 and lse = -inf.
+ *   Q [T, Hq, d]: tokens q_stride elements apart (a multiple of 8, at least Hq d).
+ *   q_start [R + 1] int32: request r's new tokens are rows q_start[r] .. q_start[r + 1] - 1 of
+ *     Q, at most max_new of them, ascending from 0 to T.  NULL: one token a request (T == R,
+ *     max_new == 1).
+ *   prefix_pages [ceil(prefix_len / page_size)] int32 (NULL when prefix_len is 0).
+ *   block_table [R, max_blocks] int32: the pages of the requests' own tokens (entries past a
+ *     request's length are not read); suffix_lens [R] int32, at most max_blocks * page_size.
+ *     max_blocks 0: no request has own keys, both may be NULL.
+ *   Cache rows past a length are not used, whatever they hold.
+ *   O [T, Hq, d] dtype, lse [T, Hq] float32 (may be NULL): contiguous outputs, distinct from Q.
+ *   workspace / ws_bytes: at least wq_attn_workspace_bytes(...) bytes, under the workspace rules
+ *     of wq_gemm_workspace_bytes (it starts with the same header, left at zero).
+ * Errors: WQ_ERR_ARG (dtype; scale not positive and finite); WQ_ERR_NULL; WQ_ERR_SHAPE unless
+ *   T, R, Hq, Hkv, pages, max_new >= 1, Hq % Hkv == 0, d is 64 or 128, page_size as above,
+ *   prefix_len, max_blocks >= 0, prefix_len and max_blocks * page_size <= 2^30, pages * Hkv <=
+ *   2^31 - 1, T <= 2^24, Hq <= 1024; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.
+ */
+size_t wq_attn_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new);
+wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_stride, int64_t T, int64_t R, int64_t Hq,
+                                int64_t Hkv, int64_t d, const uint16_t* k_cache, const uint16_t* v_cache, int64_t pages,
+                                int64_t page_size, const int32_t* prefix_pages, int64_t prefix_len,
+                                const int32_t* block_table, int64_t max_blocks, const int32_t* suffix_lens,
+                                const int32_t* q_start, int64_t max_new, float scale, uint16_t* O, float* lse,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Low-rank adapters of many requests at once beside a shared projection:
+ *   Y[m] = base[m] + scales[a] (X[m] A[a]^T) B[a]^T,  a = adapter[m];   a = -1: Y[m] = base[m].
+ *   base [M, N] dtype: the projection's output; Y [M, N] may be base itself.
+ *   X [M, K]; A [L, r, K], B [L, N, r] dtype: L adapters of up to r ranks.
+ *   ranks [L] int32 (may be NULL: all r): adapter a's own rank; its rows of A and columns of B
+ *     from there on must hold zeros (the kernels skip whole blocks of 8 of them).
+ *   adapter [M] int32, -1 .. L - 1: rows of one request need not be neighbours, but are served
+ *     best when they are.    scales [L] float32.
+ *   workspace / ws_bytes: at least wq_lora_workspace_bytes(M, K, N, r) bytes, under the workspace
+ *     rules of wq_gemm_workspace_bytes (it starts with the same header).
+ * Errors: WQ_ERR_ARG (dtype); WQ_ERR_NULL; WQ_ERR_SHAPE unless M, N, L >= 1, K >= 8, K % 8 == 0,
+ *   r % 8 == 0, 8 <= r <= 128, each of M, N, K, L <= 2^24; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH;
+ *   WQ_ERR_CUDA.
+ */
+size_t wq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
+wq_status wq_lora_add(wq_dtype dtype, const uint16_t* base, const uint16_t* X, int64_t M, int64_t K, int64_t N,
+                      const uint16_t* A, const uint16_t* B, int64_t L, int64_t r, const int32_t* ranks,
+                      const int32_t* adapter, const float* scales, uint16_t* Y, void* workspace, size_t ws_bytes,
+                      void* stream);
+
+/*
+ * The quantized layer with adapters: Y = wq_gemm_w4a16(X, Wq) + the adapters' product, bf16.
+ * The layer's output is rounded to bf16 before the adapters' product is added to it in float32.
+ * Arguments and errors as wq_gemm_w4a16 and wq_lora_add; workspace / ws_bytes at least
+ * wq_gemm_w4a16_lora_workspace_bytes(fmt, M, K, N, r).
+ */
+size_t wq_gemm_w4a16_lora_workspace_bytes(wq_fmt fmt, int64_t M, int64_t K, int64_t N, int64_t r);
+wq_status wq_gemm_w4a16_lora(wq_fmt fmt, const uint16_t* X, int64_t M, int64_t K, int64_t N, const int32_t* Wq,
+                             const void* scales, const uint16_t* zeros, const uint16_t* A, const uint16_t* B, int64_t L,
+                             int64_t r, const int32_t* ranks, const int32_t* adapter, const float* lora_scales,
                              uint16_t* Y, void* workspace, size_t ws_bytes, void* stream);
 
 /* WQ_OK when the current device is a GB300-class part (compute capability 10.3). */

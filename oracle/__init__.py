@@ -37,4 +37,4 @@ Pins (tests/test_oracle_pins.py, tests/golden/): the pages' worked example and
 asserts, closed forms, brute force on tiny inputs, invariants and special
 cases.  Every function here is pinned; none is "parity unpinned".
 """
-from . import uniform, int4_g128, mxfp4, linear, swiglu, gptq, awq, fp8, w4a4  # noqa: F401
+from . import uniform, int4_g128, mxfp4, linear, swiglu, gptq, awq, fp8, w4a4, attention_block  # noqa: F401
