@@ -46,6 +46,20 @@ cudaError_t make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_4d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[4],
+                         const uint64_t (&strides_bytes)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle,
+                         CUtensorMapL2promotion promo) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {strides_bytes[0], strides_bytes[1], strides_bytes[2]};
+  const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, dtype, 4, const_cast<void*>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promo,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 CUcontext current_context() {
   using CtxGetCurrentFn = CUresult (*)(CUcontext*);
   static CtxGetCurrentFn fn = nullptr;
@@ -664,7 +678,7 @@ wq_status wq_qk_norm_rope_cache(wq_dtype dtype, int64_t T, int64_t Hq, int64_t H
 }
 
 static bool attn_shape_ok(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new) {
-  return T >= 1 && T <= (1 << 24) && R >= 1 && R <= (1 << 24) && Hkv >= 1 && Hq >= 1 && Hq <= 1024 && Hq % Hkv == 0 &&
+  return T >= 1 && T <= (1 << 24) && R >= 1 && R <= (1 << 24) && Hkv >= 1 && Hq >= 1 && Hq <= 1024 && Hq % Hkv == 0 && Hq / Hkv <= 128 &&
          (d == 64 || d == 128) && max_new >= 1 && max_new <= T;
 }
 

@@ -43,6 +43,11 @@ cudaError_t make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void
                          uint64_t dim1, uint64_t stride1_bytes, uint32_t box0, uint32_t box1,
                          CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo);
 
+// The same with 4 dimensions; strides_bytes[i] is the stride of dimension i + 1.
+cudaError_t make_tmap_4d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[4],
+                         const uint64_t (&strides_bytes)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle,
+                         CUtensorMapL2promotion promo);
+
 int device_sm_count();
 
 // The calling thread's current CUDA context (driver entry point, no libcuda link), or

@@ -84,4 +84,27 @@ __device__ __forceinline__ void tc_mma_ss_f8f6f4(uint32_t d_tmem, uint64_t a_des
       : "memory");
 }
 
+// D[tmem] (+)= A[smem desc] * B[smem desc], 16-bit operands (both fp16 or both bf16).
+__device__ __forceinline__ void tc_mma_ss_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory matrix descriptor of an operand whose M or N index is contiguous (rows of 64
+// elements = 128 bytes, one row per k, 128-byte swizzle): groups of 8 k are 1024 B apart, and the
+// next 64 elements of the contiguous index start `chunk_bytes` further on.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t chunk_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
+  d |= static_cast<uint64_t>(chunk_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
 }  // namespace wq

@@ -509,7 +509,7 @@ wq_status wq_qk_norm_rope_cache(wq_dtype dtype, int64_t T, int64_t Hq, int64_t H
  *   workspace / ws_bytes: at least wq_attn_workspace_bytes(...) bytes, under the workspace rules
  *     of wq_gemm_workspace_bytes (it starts with the same header, left at zero).
  * Errors: WQ_ERR_ARG (dtype; scale not positive and finite); WQ_ERR_NULL; WQ_ERR_SHAPE unless
- *   T, R, Hq, Hkv, pages, max_new >= 1, Hq % Hkv == 0, d is 64 or 128, page_size as above,
+ *   T, R, Hq, Hkv, pages, max_new >= 1, Hq % Hkv == 0, Hq / Hkv <= 128, d is 64 or 128, page_size as above,
  *   prefix_len, max_blocks >= 0, prefix_len and max_blocks * page_size <= 2^30, pages * Hkv <=
  *   2^31 - 1, T <= 2^24, Hq <= 1024; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.
  */
