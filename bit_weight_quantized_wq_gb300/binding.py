@@ -613,102 +613,36 @@ def gemm_w4a4_mxfp4(X, Wq8, sw, out=None, workspace=None, stream=None):
 
 
 # ------------------------------------------------------------------ the attention block
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+# These calls are marshalled by _marshal.so (csrc/marshal.cpp): the same checks as above, compiled.
+_marshal_module = None
 
 
-def _dtype16(t, name):
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError("%s must be bfloat16 or float16, got %s" % (name, t.dtype))
-    return code
+def _m():
+    global _marshal_module
+    if _marshal_module is None:
+        load_library()
+        from . import _marshal
+        _marshal_module = _marshal
+    return _marshal_module
 
 
-def _same(t, ref, name, shape=None, dtype=None, contiguous=True):
-    """``t`` on ``ref``'s CUDA device with the given shape and dtype (default: ``ref``'s dtype)."""
-    d = t.get_device()
-    if d < 0 or d != ref.get_device():
-        raise ValueError("%s must be on the same CUDA device as the other tensors" % name)
-    want = ref.dtype if dtype is None else dtype
-    if t.dtype is not want:
-        raise ValueError("%s must be %s, got %s" % (name, want, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    if contiguous and not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+def _on_stream(stream, f, tensors, *args):
+    """The call ``f(*args)`` on ``stream``: outputs and workspace are made under it, and the allocator
+    is told that ``tensors`` are in use there."""
+    with torch.cuda.stream(stream):
+        out = f(*args)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return out
 
 
-def _heads(t, name):
-    """Token stride of a [T, heads, d] tensor whose heads are contiguous within a token."""
-    if t.dim() != 3 or t.numel() == 0:
-        raise ValueError("%s must be [T, heads, d], none of them 0" % name)
-    T, h, d = t.shape
-    st = t.stride()
-    if st[2] != 1 or (h > 1 and st[1] != d):
-        raise ValueError("%s: a token's heads must be contiguous" % name)
-    return st[0] if T > 1 else h * d
-
-
-class _On:
-    """The stream of a call and what must outlive it.  With ``stream`` given, new tensors are
-    made under it, so the allocator never hands their memory out before that stream is done with it;
-    ``used`` tells the allocator the same of tensors that belong to other streams."""
-
-    def __init__(self, stream, device_index):
-        self.stream = stream
-        self.index = device_index
-        self.handle = stream.cuda_stream if stream is not None else _raw_stream(device_index)
-
-    def empty(self, shape, dtype):
-        device = torch.device("cuda", self.index)
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-
-    def workspace(self, nbytes, given):
-        if given is not None:
-            if given.get_device() != self.index or not given.is_contiguous():
-                raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
-            return given
-        key = ("cuda:%d" % self.index, self.handle)
-        ws = _default_ws.get(key)
-        if ws is None:
-            ws = _default_ws[key] = Workspace(torch.device("cuda", self.index))
-        if ws.buf is not None and ws.buf.numel() >= nbytes:
-            return ws.buf
-        if self.stream is None:
-            return ws.get(nbytes)
-        with torch.cuda.stream(self.stream):
-            return ws.get(nbytes)
-
-    def used(self, *tensors):
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-
-
-def _raw_stream(index):
-    if _raw_current_stream is not None:
-        return _raw_current_stream(index)
-    return torch.cuda.current_stream(index).cuda_stream
-
-
-def _rope_inputs(Q, K, positions, cos_sin, q_weight, k_weight):
-    dt = _dtype16(Q, "Q")
-    if Q.get_device() < 0:
-        raise ValueError("Q must be a CUDA tensor")
-    qs, ks = _heads(Q, "Q"), _heads(K, "K")
-    T, Hq, d = Q.shape
-    _same(K, Q, "K", (T, K.shape[1], d), contiguous=False)
-    _same(positions, Q, "positions", (T,), torch.int32)
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [positions, rot]")
-    _same(cos_sin, Q, "cos_sin", None, torch.float32)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _same(w, Q, name, (d,))
-    return dt, T, Hq, K.shape[1], d, qs, ks
+def _pair(out, names):
+    if out is None:
+        return None, None
+    if len(out) != 2:
+        raise ValueError("out must be two tensors (%s)" % names)
+    return out
 
 
 def qk_norm_rope(Q, K, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None,
@@ -716,32 +650,13 @@ def qk_norm_rope(Q, K, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-
     """Norm of every query and key head (with its weight; none where the weight is None), then the
     rotation of the first ``rot = cos_sin.shape[1]`` elements of a head by the token's position:
     (Q' [T, Hq, d], K' [T, Hkv, d]).  Q and K may be parts of a fused projection output (a token's
-    heads contiguous).  cos_sin float32 [positions, rot]: rot/2 cosines, then rot/2 sines.
-    ``out`` may be (Q', K'); contiguous Q and K may be their own outputs."""
-    dt, T, Hq, Hkv, d, qs, ks = _rope_inputs(Q, K, positions, cos_sin, q_weight, k_weight)
-    on = _On(stream, Q.get_device())
-    if out is None:
-        out = on.empty((T, Hq, d), Q.dtype), on.empty((T, Hkv, d), Q.dtype)
-    else:
-        if len(out) != 2:
-            raise ValueError("out must be two tensors (Q', K')")
-        _same(out[0], Q, "out Q", (T, Hq, d))
-        _same(out[1], Q, "out K", (T, Hkv, d))
-    on.used(Q, K, positions, cos_sin, q_weight, k_weight, *out)
-    _check(_fn("wq_qk_norm_rope")(dt, T, Hq, Hkv, d, Q.data_ptr(), qs, K.data_ptr(), ks, _ptr(q_weight), _ptr(k_weight),
-                                  eps, cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(interleaved),
-                                  positions.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), on.handle),
-           "wq_qk_norm_rope")
-    return tuple(out)
-
-
-def _cache(k_cache, v_cache, ref, heads=None, d=None):
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, Hkv, page_size, d]")
-    pages, h, page, e = k_cache.shape
-    _same(k_cache, ref, "k_cache", (pages, h if heads is None else heads, page, e if d is None else d))
-    _same(v_cache, ref, "v_cache", k_cache.shape)
-    return pages, page
+    heads contiguous).  positions int32 [T]; cos_sin float32 [positions, rot]: rot/2 cosines, then
+    rot/2 sines.  ``out`` may be (Q', K'); contiguous Q and K may be their own outputs."""
+    qo, ko = _pair(out, "Q', K'")
+    args = (Q, K, positions, cos_sin, q_weight, k_weight, eps, interleaved, qo, ko)
+    if stream is None:
+        return _m().qk_norm_rope(*args)
+    return _on_stream(stream, _m().qk_norm_rope, (Q, K, positions, cos_sin, q_weight, k_weight, qo, ko), *args)
 
 
 def qk_norm_rope_cache(Q, K, V, positions, cos_sin, k_cache, v_cache, slots, q_weight=None, k_weight=None, eps=1e-6,
@@ -749,23 +664,11 @@ def qk_norm_rope_cache(Q, K, V, positions, cos_sin, k_cache, v_cache, slots, q_w
     """``qk_norm_rope`` that writes the keys, and the values as they are, to a cache in pages
     (k_cache, v_cache [pages, Hkv, page_size, d]): token t goes to slot slots[t] = page * page_size
     + place (int32; negative: not written).  Returns Q' [T, Hq, d]."""
-    dt, T, Hq, Hkv, d, qs, ks = _rope_inputs(Q, K, positions, cos_sin, q_weight, k_weight)
-    vs = _heads(V, "V")
-    _same(V, Q, "V", (T, Hkv, d), contiguous=False)
-    pages, page = _cache(k_cache, v_cache, Q, Hkv, d)
-    _same(slots, Q, "slots", (T,), torch.int32)
-    on = _On(stream, Q.get_device())
-    if out is None:
-        out = on.empty((T, Hq, d), Q.dtype)
-    else:
-        _same(out, Q, "out", (T, Hq, d))
-    on.used(Q, K, V, positions, cos_sin, k_cache, v_cache, slots, q_weight, k_weight, out)
-    _check(_fn("wq_qk_norm_rope_cache")(dt, T, Hq, Hkv, d, Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs,
-                                        _ptr(q_weight), _ptr(k_weight), eps, cos_sin.data_ptr(), cos_sin.shape[0],
-                                        cos_sin.shape[1], int(interleaved), positions.data_ptr(), out.data_ptr(),
-                                        k_cache.data_ptr(), v_cache.data_ptr(), pages, page, slots.data_ptr(),
-                                        on.handle), "wq_qk_norm_rope_cache")
-    return out
+    args = (Q, K, positions, cos_sin, q_weight, k_weight, eps, interleaved, V, k_cache, v_cache, slots, out)
+    if stream is None:
+        return _m().qk_norm_rope_cache(*args)
+    return _on_stream(stream, _m().qk_norm_rope_cache,
+                      (Q, K, V, positions, cos_sin, k_cache, v_cache, slots, q_weight, k_weight, out), *args)
 
 
 def attn_shared_prefix(Q, k_cache, v_cache, prefix_pages, prefix_len, block_table, suffix_lens, q_start=None, max_new=1,
@@ -777,72 +680,12 @@ def attn_shared_prefix(Q, k_cache, v_cache, prefix_pages, prefix_len, block_tabl
     tokens the last of them (both None: no own tokens).  q_start int32 [R + 1]: where each request's
     new tokens start in Q, at most ``max_new`` each (None: one each).  scale defaults to 1/sqrt(d).
     Returns (O [T, Hq, d], lse float32 [T, Hq])."""
-    dt = _dtype16(Q, "Q")
-    if Q.get_device() < 0:
-        raise ValueError("Q must be a CUDA tensor")
-    qs = _heads(Q, "Q")
-    T, Hq, d = Q.shape
-    pages, page = _cache(k_cache, v_cache, Q, None, d)
-    Hkv = k_cache.shape[1]
-    if q_start is not None:
-        _same(q_start, Q, "q_start", None, torch.int32)
-        R = q_start.numel() - 1
-        if q_start.dim() != 1:
-            raise ValueError("q_start must be [R + 1]")
-    else:
-        R = T
-    if (block_table is None) != (suffix_lens is None):
-        raise ValueError("block_table and suffix_lens go together")
-    blocks = 0
-    if block_table is not None:
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [R, blocks]")
-        blocks = block_table.shape[1]
-        _same(block_table, Q, "block_table", (R, blocks), torch.int32)
-        _same(suffix_lens, Q, "suffix_lens", (R,), torch.int32)
-    if prefix_len:
-        if prefix_pages is None:
-            raise ValueError("prefix_pages is required when prefix_len > 0")
-        _same(prefix_pages, Q, "prefix_pages", None, torch.int32)
-        if prefix_pages.dim() != 1 or prefix_pages.numel() * page < prefix_len:
-            raise ValueError("prefix_pages must hold prefix_len tokens")
-    on = _On(stream, Q.get_device())
-    if out is None:
-        out = on.empty((T, Hq, d), Q.dtype), on.empty((T, Hq), torch.float32)
-    else:
-        if len(out) != 2:
-            raise ValueError("out must be two tensors (O, lse)")
-        _same(out[0], Q, "out O", (T, Hq, d))
-        _same(out[1], Q, "out lse", (T, Hq), torch.float32)
-    ws = on.workspace(_fn("wq_attn_workspace_bytes")(T, R, Hq, Hkv, d, max_new), workspace)
-    on.used(Q, k_cache, v_cache, prefix_pages, block_table, suffix_lens, q_start, *out)
-    if workspace is not None:
-        on.used(workspace)
-    _check(_fn("wq_attn_shared_prefix")(dt, Q.data_ptr(), qs, T, R, Hq, Hkv, d, k_cache.data_ptr(), v_cache.data_ptr(),
-                                        pages, page, _ptr(prefix_pages), prefix_len, _ptr(block_table), blocks,
-                                        _ptr(suffix_lens), _ptr(q_start), max_new,
-                                        d ** -0.5 if scale is None else scale, out[0].data_ptr(), out[1].data_ptr(),
-                                        _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), on.handle),
-           "wq_attn_shared_prefix")
-    return tuple(out)
-
-
-def _lora_inputs(X, A, B, adapter, scales, ranks):
-    if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
-        raise ValueError("X must be [M, K], A [L, r, K] and B [L, N, r]")
-    if X.get_device() < 0:
-        raise ValueError("X must be a CUDA tensor")
-    M, K = X.shape
-    L, r = A.shape[0], A.shape[1]
-    N = B.shape[1]
-    _same(X, X, "X")
-    _same(A, X, "A", (L, r, K))
-    _same(B, X, "B", (L, N, r))
-    _same(adapter, X, "adapter", (M,), torch.int32)
-    _same(scales, X, "scales", (L,), torch.float32)
-    if ranks is not None:
-        _same(ranks, X, "ranks", (L,), torch.int32)
-    return M, K, N, L, r
+    o, lse = _pair(out, "O, lse")
+    args = (Q, k_cache, v_cache, prefix_pages, prefix_len, block_table, suffix_lens, q_start, max_new, scale, o, lse, workspace)
+    if stream is None:
+        return _m().attn_shared_prefix(*args)
+    return _on_stream(stream, _m().attn_shared_prefix,
+                      (Q, k_cache, v_cache, prefix_pages, block_table, suffix_lens, q_start, o, lse, workspace), *args)
 
 
 def lora_add(base, X, A, B, adapter, scales, ranks=None, out=None, workspace=None, stream=None):
@@ -850,40 +693,17 @@ def lora_add(base, X, A, B, adapter, scales, ranks=None, out=None, workspace=Non
     low-rank adapters of many requests beside one projection.  base [M, N], X [M, K], A [L, r, K],
     B [L, N, r] (one 16-bit dtype), adapter int32 [M], scales float32 [L], ranks int32 [L] (the
     adapters' own ranks, zeros beyond them).  ``out`` may be base itself."""
-    dt = _dtype16(X, "X")
-    M, K, N, L, r = _lora_inputs(X, A, B, adapter, scales, ranks)
-    _same(base, X, "base", (M, N))
-    on = _On(stream, X.get_device())
-    if out is None:
-        out = on.empty((M, N), X.dtype)
-    else:
-        _same(out, X, "out", (M, N))
-    ws = on.workspace(_fn("wq_lora_workspace_bytes")(M, K, N, r), workspace)
-    on.used(base, X, A, B, adapter, scales, ranks, out, workspace)
-    _check(_fn("wq_lora_add")(dt, base.data_ptr(), X.data_ptr(), M, K, N, A.data_ptr(), B.data_ptr(), L, r, _ptr(ranks),
-                              adapter.data_ptr(), scales.data_ptr(), out.data_ptr(), _ptr(ws),
-                              0 if ws is None else ws.numel() * ws.element_size(), on.handle), "wq_lora_add")
-    return out
+    args = (X, A, B, adapter, scales, ranks, base, out, workspace)
+    if stream is None:
+        return _m().lora_add(*args)
+    return _on_stream(stream, _m().lora_add, args, *args)
 
 
 def gemm_w4a16_lora(fmt, X, Wq, scales, zeros, A, B, adapter, lora_scales, ranks=None, out=None, workspace=None,
                     stream=None):
     """The quantized layer with adapters, Y = ``gemm_w4a16`` + the product of ``lora_add`` (bf16)."""
-    f = fmt if fmt.__class__ is int else _FMT_NAMES[fmt]
-    M, K, N, d = _inputs(f, X, Wq, scales, zeros)
-    _, _, Nb, L, r = _lora_inputs(X, A, B, adapter, lora_scales, ranks)
-    if Nb != N:
-        raise ValueError("B must be [L, N, r] with Wq's N")
-    on = _On(stream, d)
-    if out is None:
-        out = on.empty((M, N), _BF16)
-    else:
-        _same(out, X, "out", (M, N))
-    ws = on.workspace(_fn("wq_gemm_w4a16_lora_workspace_bytes")(f, M, K, N, r), workspace)
-    on.used(X, Wq, scales, zeros, A, B, adapter, lora_scales, ranks, out, workspace)
-    _check(_fn("wq_gemm_w4a16_lora")(f, X.data_ptr(), M, K, N, Wq.data_ptr(), scales.data_ptr(), _ptr(zeros),
-                                     A.data_ptr(), B.data_ptr(), L, r, _ptr(ranks), adapter.data_ptr(),
-                                     lora_scales.data_ptr(), out.data_ptr(), _ptr(ws),
-                                     0 if ws is None else ws.numel() * ws.element_size(), on.handle),
-           "wq_gemm_w4a16_lora")
-    return out
+    args = (X, A, B, adapter, lora_scales, ranks, _fmt(fmt), Wq, scales, zeros, out, workspace)
+    if stream is None:
+        return _m().gemm_w4a16_lora(*args)
+    return _on_stream(stream, _m().gemm_w4a16_lora,
+                      (X, Wq, scales, zeros, A, B, adapter, lora_scales, ranks, out, workspace), *args)

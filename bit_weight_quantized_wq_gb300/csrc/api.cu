@@ -679,12 +679,12 @@ wq_status wq_qk_norm_rope_cache(wq_dtype dtype, int64_t T, int64_t Hq, int64_t H
 
 static bool attn_shape_ok(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new) {
   return T >= 1 && T <= (1 << 24) && R >= 1 && R <= (1 << 24) && Hkv >= 1 && Hq >= 1 && Hq <= 1024 && Hq % Hkv == 0 && Hq / Hkv <= 128 &&
-         (d == 64 || d == 128) && max_new >= 1 && max_new <= T;
+         (d == 64 || d == 128) && max_new >= 1;
 }
 
 size_t wq_attn_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new) {
   if (!attn_shape_ok(T, R, Hq, Hkv, d, max_new)) return 0;
-  return wq::attn_workspace_bytes(T, R, Hq, Hkv, d, max_new);
+  return wq::attn_workspace_bytes(T, R, Hq, Hkv, d, max_new < T ? max_new : T);
 }
 
 wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_stride, int64_t T, int64_t R, int64_t Hq,
@@ -708,6 +708,7 @@ wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_str
     return WQ_ERR_ALIGN;
   if (overlap(Q, (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2, O, static_cast<size_t>(T) * Hq * d * 2))
     return WQ_ERR_ARG;
+  if (max_new > T) max_new = T;
   if (!workspace || ws_bytes < wq::attn_workspace_bytes(T, R, Hq, Hkv, d, max_new)) return WQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return WQ_ERR_ALIGN;
   wq_status st = check_device_cached();

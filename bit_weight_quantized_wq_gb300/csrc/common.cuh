@@ -96,6 +96,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
   }
 }
 
+// The same wait for short hand-offs on a kernel's critical path: the limit (4e9 SM cycles, about
+// two seconds) is read on the SM's own cycle counter, and only after 64 polls -- the nanosecond
+// timer of mbar_wait takes long enough to read to delay the wake-up.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > 4000000000ll) {
+      atomicOr(err, code);
+      return false;
+    }
+  }
+  return true;
+}
+
 // The same bounded wait with the limit given in nanoseconds.
 __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code,
                                               uint64_t limit_ns) {
