@@ -53,9 +53,9 @@ namespace {
 
 constexpr int kRows = 128;            // rows per lane
 constexpr int kTile = 64;             // keys per tile
-constexpr int kThreads = 384;         // 2 lanes x 4 softmax warps; TMA warp, a product warp a lane, scheduler
+constexpr int kThreads = 512;         // 2 lanes x 4 softmax warps; two TMA warps, a product warp a lane, scheduler
 constexpr int kWarps = kThreads / 32;
-constexpr int kWTma = 8, kWMma = 9, kWSched = 11;
+constexpr int kWTma = 8, kWMma = 10, kWSched = 12;   // warps from 13 on only take part in the set-up
 constexpr int kItems = 4;             // items the scheduler is ahead of the other warps
 constexpr int kTmemCols = 512;        // two S of 64 columns a lane, then O of 128 a lane
 constexpr int kColO = 256;
@@ -80,10 +80,10 @@ template <int D>
 struct Smem {
   static constexpr int kTileBytes = kTile * D * 2;      // a K or V tile: [D / 64][64 keys][128 B]
   static constexpr int kQBytes = kRows * D * 2;         // a Q tile: [D / 64][128 rows][128 B]
-  static constexpr int kStages = D == 128 ? 10 : 16;    // K and V tiles in flight
-  uint8_t kv[kStages][kTileBytes];
+  static constexpr int kStages = D == 128 ? 5 : 8;      // K tiles, and V tiles, in flight
+  uint8_t kv[2][kStages][kTileBytes];                   // rings of K and of V tiles
   uint8_t q[2][kQBytes];
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[2][kStages], empty[2][kStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], p_full[2][2];                  // [lane][buffer]
   uint64_t pv_done[2], o_full[2], o_empty[2], drain[2];
@@ -105,6 +105,7 @@ struct __align__(16) TokenRecord {
 struct Params {
   AttnArgs a;
   int G, tb;                 // query heads per key/value head; tokens per lane tile (kRows / G)
+  int log_page;              // log2 of the page size
   int n_prefix;              // prefix items
   int prefix_tiles;
   int q_rows_suffix;         // rows a suffix lane tile can have (its partial's row capacity)
@@ -225,9 +226,8 @@ struct Walk {
   }
 };
 
-// Order in which an item's n key tiles reach shared memory: the K of the first `ahead` tiles, then
-// V0, K(ahead), V1, K(ahead + 1), ...: each lane has the scores of two tiles under way (rows mode:
-// tiles 0 and 1; keys mode: its own first two of tiles 0 to 3).
+// Tiles by which a lane's S = Q K^T runs ahead of its O += P V: two tiles of its own, which are in
+// rows mode the next two, in keys mode two of the next four.
 __device__ __forceinline__ int k_ahead(bool rows) { return rows ? 2 : 4; }
 
 // A wait of a whole warp: every lane waits (bounded), and all of them go on or none.
@@ -287,14 +287,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     // K, V and Q tiles are given back by both lanes' product warps
-    for (int s = 0; s < NS; ++s) mbar_init(&sm.full[s], 1), mbar_init(&sm.empty[s], 2);
     for (int i = 0; i < 2; ++i) {
+      for (int s = 0; s < NS; ++s) mbar_init(&sm.full[i][s], 1), mbar_init(&sm.empty[i][s], 2);
       mbar_init(&sm.q_full[i], 1), mbar_init(&sm.q_empty[i], 2);
       for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[i][b], 1), mbar_init(&sm.p_full[i][b], 4);
       mbar_init(&sm.pv_done[i], 1), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.o_empty[i], 4);
       mbar_init(&sm.drain[i], 1);
     }
-    for (int i = 0; i < kItems; ++i) mbar_init(&sm.item_full[i], 1), mbar_init(&sm.item_empty[i], 11);
+    for (int i = 0; i < kItems; ++i) mbar_init(&sm.item_full[i], 1), mbar_init(&sm.item_empty[i], 12);
     fence_barrier_init();
   }
   if (warp == kWMma) {
@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const bool work = total > 0;
   const int prefix_cost = static_cast<int>(prefix_long > kMaxLine ? 0 : prefix_long);
-  const int share = max(kWKeys, static_cast<int>((total + p.ctas - 1) / p.ctas));
+  // at least a tile for each lane
+  const int share = max(2 * kWKeys, static_cast<int>((total + p.ctas - 1) / p.ctas));
   const int b0 = blockIdx.x * share;
   if (work) {
     int run = prefix_cost, run_items = 0;
@@ -393,84 +394,99 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Item* it = &sm.items[n_items % kItems];
     return ok && it->hi > 0 ? it : nullptr;
   };
+  // The one after it, without leaving it (waits for the scheduler, which is up to kItems ahead).
+  const auto peek_item = [&]() -> const Item* {
+    const uint32_t i = n_items + 1;
+    ok = warp_wait(&sm.item_full[i % kItems], (i / kItems) & 1, kErrWaitFull);
+    const Item* it = &sm.items[i % kItems];
+    return ok && it->hi > 0 ? it : nullptr;
+  };
   const auto item_done = [&] {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.item_empty[n_items % kItems]);
     ++n_items;
   };
 
-  if (warp == kWTma) {
-    // -------------------------------------------------------------------- TMA producer
+  if (warp == kWTma || warp == kWTma + 1) {
+    // -------------------------------------------------------------------- TMA producers: Q and K, V
+    // A load of 16-row pages is eight copies a tile, each some 40 cycles to issue, so K and V have a
+    // warp each.  One elected lane issues; the page numbers come to it by shuffles.
+    const bool keys = warp == kWTma;
     const uint64_t pol_keep = l2_policy_evict_last(), pol_once = l2_policy_evict_first();
-    const int page = p.a.page_size, box = min(page, kTile), boxes = kTile / box, per_page = page / box;
-    // lane i < boxes * CH loads box i % boxes of chunk i / boxes of each tile
-    const int my_box = lane % boxes, my_chunk = lane / boxes;
+    // boxes of 2^lb rows, 2^lt of them a tile, 2^lp of them a page
+    const int lb = min(p.log_page, 6), box = 1 << lb, lt = 6 - lb, boxes = 1 << lt, lp = p.log_page - lb;
+    const CUtensorMap* map = keys ? &tk : &tv;
+    const int ring = keys ? 0 : 1;
     uint32_t ord = 0, qord = 0;
-    while (const Item* it = next_item()) {
+    // Page numbers: lane i holds that of box base + i of the segment, read 32 boxes ahead and, for the
+    // first 32 boxes, while the segment before is being loaded.
+    const auto boxes_of = [&](const Item* it) { return min(((it->len + box - 1) >> lb) - (it->lo << lt), (it->hi - it->lo) << lt); };
+    const auto page_ids = [&](const Item* it, int n_boxes, int base) {
+      const int32_t* list = it->r < 0 ? p.a.prefix_pages : p.a.block_table + static_cast<int64_t>(it->r) * p.a.max_blocks;
+      return base + lane < n_boxes ? __ldg(list + (((it->lo << lt) + base + lane) >> lp)) : 0;
+    };
+    const Item* it = next_item();
+    int ids = it ? page_ids(it, boxes_of(it), 0) : 0;
+    while (it) {
       const int lo = it->lo, n = it->hi - lo, kvh = it->kvh;
       const bool prefix = it->r < 0, rows = it->ntok > p.tb;
-      // Q: one 128-row tile, or one per lane
-      const int box_tok = prefix ? p.tb : min(p.tb, p.a.max_new);
-      for (int i = 0; i < (rows ? 2 : 1) && ok; ++i, ++qord) {
-        const int s = qord & 1;
-        ok = warp_wait(&sm.q_empty[s], ((qord >> 1) & 1) ^ 1, kErrWaitEmpty);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.q_full[s], box_tok * p.G * 128 * CH);
-          for (int c = 0; c < CH; ++c)
-            tma_load_4d(&sm.q[s][c * kQChunk], prefix ? &tq_p : &tq_s, 0, c, kvh * p.G, it->tok0 + i * p.tb, &sm.q_full[s],
-                        pol_keep);
-        }
-        __syncwarp();
-      }
-      if (!ok) break;
-      const int32_t* list = prefix ? p.a.prefix_pages : p.a.block_table + static_cast<int64_t>(it->r) * p.a.max_blocks;
       const uint64_t pol = prefix ? pol_keep : pol_once;
-      const int n_boxes = ceil_div(it->len, box);
-      // Row of the tensor map, page * Hkv + head, of this lane's box of tile j; -1: zero fill.
-      const auto page_id = [&](int j) {
-        const int i = (lo + j) * boxes + my_box;
-        if (j >= n || i >= n_boxes) return -1;
-        const int id = __ldg(list + i / per_page);
-        if (id < 0 || id >= p.a.pages) {
-          atomicOr(&g_attn_err, kErrIndex);
-          return -1;
+      const int n_boxes = boxes_of(it);                // of this segment
+      const Item* after = peek_item();
+      if (!ok) break;
+      const int ids_after = after ? page_ids(after, boxes_of(after), 0) : 0;
+      int ids_next = page_ids(it, n_boxes, 32);
+      if (keys) {   // Q: one 128-row tile, or one per lane
+        const int box_tok = prefix ? p.tb : min(p.tb, p.a.max_new);
+        for (int i = 0; i < (rows ? 2 : 1) && ok; ++i, ++qord) {
+          const int s = qord & 1;
+          ok = warp_wait(&sm.q_empty[s], ((qord >> 1) & 1) ^ 1, kErrWaitEmpty);
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&sm.q_full[s], box_tok * p.G * 128 * CH);
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+              tma_load_4d(&sm.q[s][c * kQChunk], prefix ? &tq_p : &tq_s, 0, c, kvh * p.G, it->tok0 + i * p.tb, &sm.q_full[s],
+                          pol_keep);
+          }
+          __syncwarp();
         }
-        return id * p.a.Hkv + kvh;
-      };
-      const auto load = [&](const CUtensorMap* map, int j, int id) {
-        const int s = ord % NS;
-        if (!warp_wait(&sm.empty[s], ((ord / NS) & 1) ^ 1, kErrWaitEmpty)) return false;
-        const int i0 = (lo + j) * boxes, here = min(boxes, n_boxes - i0);
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], here * box * 128 * CH);
-        __syncwarp();
-        if (my_chunk < CH && my_box < here)
-          tma_load_4d(&sm.kv[s][my_chunk * kKvChunk + my_box * box * 128], map, 0, ((i0 + my_box) % per_page) * box, my_chunk, id,
-                      &sm.full[s], pol);
-        ++ord;
-        return true;
-      };
-      // page numbers are read ahead of their use: K runs `ahead` tiles before V
-      const int ahead = k_ahead(rows);
-      int id[5];
-#pragma unroll
-      for (int k = 0; k < 5; ++k) id[k] = page_id(k);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (ok && k < ahead && k < n) ok = load(&tk, k, id[k]);
+        if (!ok) break;
+      }
 #pragma unroll 1
-      for (int j = 0; ok && j < n; ++j) {
-        const int id5 = page_id(j + 5);
-        ok = load(&tv, j, id[0]);
-        if (ok && j + ahead < n) ok = load(&tk, j + ahead, rows ? id[2] : id[4]);
-        id[0] = id[1], id[1] = id[2], id[2] = id[3], id[3] = id[4], id[4] = id5;
+      for (int j = 0; j < n; ++j, ++ord) {
+        const int s = ord % NS, b0 = j << lt, here = min(boxes, n_boxes - b0);
+        // rows of the tensor map, page * Hkv + head; -1: zero fill
+        int row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int id = __shfl_sync(0xffffffffu, ids, (b0 + i) & 31);
+          row[i] = id < 0 || id >= p.a.pages ? -1 : id * p.a.Hkv + kvh;
+          if (row[i] < 0 && i < here && lane == 0) atomicOr(&g_attn_err, kErrIndex);
+        }
+        const int row0 = (((lo << lt) + b0) & ((1 << lp) - 1)) << lb;   // pages of 128: one box a tile, half a page
+        ok = warp_wait(&sm.empty[ring][s], ((ord / NS) & 1) ^ 1, kErrWaitEmpty);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.full[ring][s], (here << lb) * 128 * CH);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < here) {
+#pragma unroll
+              for (int c = 0; c < CH; ++c)
+                tma_load_4d(&sm.kv[ring][s][c * kKvChunk + ((i << lb) * 128)], map, 0, row0, c, row[i], &sm.full[ring][s], pol);
+            }
+        }
+        __syncwarp();
+        if (((b0 + boxes) & 31) == 0) ids = ids_next, ids_next = page_ids(it, n_boxes, b0 + boxes + 32);
       }
       if (!ok) break;
       item_done();
+      it = after, ids = ids_after;
     }
     // drain: the last fill of each slot has landed before the CTA's memory goes
     for (uint32_t i = ord > NS ? ord - NS : 0; i < ord; ++i)
-      mbar_wait_short(&sm.full[i % NS], (i / NS) & 1, &g_attn_err, kErrDrain);
+      mbar_wait_short(&sm.full[ring][i % NS], (i / NS) & 1, &g_attn_err, kErrDrain);
     for (uint32_t i = qord > 2 ? qord - 2 : 0; i < qord; ++i)
       mbar_wait_short(&sm.q_full[i & 1], (i >> 1) & 1, &g_attn_err, kErrDrain);
   } else if (warp == kWSched) {
@@ -487,17 +503,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sm.item_full[i % kItems]);
       }
     }
-  } else if (warp >= kWMma) {
+  } else if (warp == kWMma || warp == kWMma + 1) {
     // -------------------------------------------------------------------- products of lane l
     const int l = warp - kWMma;
-    const bool leader = lane == 0;
     constexpr uint32_t fmt = F16 ? 0u : 1u;
     constexpr uint32_t id_qk = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kTile >> 3) << 17) | ((kRows >> 4) << 24);
     constexpr uint32_t id_pv = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((D >> 3) << 17) | ((kRows >> 4) << 24);
     const uint32_t t_s = tmem + 128 * l, t_o = tmem + kColO + 128 * l;
-    const uint64_t k0 = smem_desc_sw128(smem_u32(&sm.kv[0][0])), v0 = smem_desc_sw128_mn(smem_u32(&sm.kv[0][0]), kKvChunk);
+    const uint64_t k0 = smem_desc_sw128(smem_u32(&sm.kv[0][0][0])), v0 = smem_desc_sw128_mn(smem_u32(&sm.kv[1][0][0]), kKvChunk);
     const uint64_t q0 = smem_desc_sw128(smem_u32(&sm.q[0][0]));
-    uint32_t ord = 0, qord = 0, o_cnt = 0;
+    uint32_t k_ord = 0, v_ord = 0, qord = 0, o_cnt = 0;
     uint32_t s_cnt = 0, p_cnt = 0;            // tiles of this lane whose S was issued / whose P was taken
     // Every slot of the rings is waited for and given back once by each lane, also where only the
     // other lane uses it: a wait by parity is only sound if no phase of the slot is left out.
@@ -508,70 +523,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qd = q0 + ((qord + (rows ? l : 0)) & 1) * (S::kQBytes >> 4);
       for (int i = 0; i < nq && ok; ++i) ok = warp_wait(&sm.q_full[(qord + i) & 1], ((qord + i) >> 1) & 1, kErrWaitFull);
       if (!ok) break;
-      const auto next_kv = [&] {                // the next slot of the ring is filled
-        ok = warp_wait(&sm.full[ord % NS], (ord / NS) & 1, kErrWaitFull);
-        return ok;
-      };
-      const auto give_back = [&] {              // a tile of the other lane
-        if (leader) mbar_arrive(&sm.empty[ord % NS]);
-        __syncwarp();
-        ++ord;
-      };
       const auto qk = [&](int j) {              // S = Q K(j)^T
-        if (!next_kv()) return;
-        if (!rows && (j & 1) != l) return give_back();
-        const uint64_t kd = k0 + (ord % NS) * (S::kTileBytes >> 4);
+        const uint32_t sl = k_ord % NS;
+        ok = warp_wait(&sm.full[0][sl], (k_ord / NS) & 1, kErrWaitFull);
+        if (!ok) return;
+        ++k_ord;
+        if (!rows && (j & 1) != l) {            // a tile of the other lane
+          if (elect_one()) mbar_arrive(&sm.empty[0][sl]);
+          __syncwarp();
+          return;
+        }
+        const uint64_t kd = k0 + sl * (S::kTileBytes >> 4);
         const uint32_t b = s_cnt & 1, t = t_s + 64 * b;
         tc_fence_after();
-        if (leader) {
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4 * CH; ++k)
             tc_mma_ss_f16(t, qd + (((k >> 2) * kQChunk + 32 * (k & 3)) >> 4), kd + (((k >> 2) * kKvChunk + 32 * (k & 3)) >> 4),
                           id_qk, k ? 1u : 0u);
           tc_commit(&sm.s_full[l][b]);
-          tc_commit(&sm.empty[ord % NS]);
+          tc_commit(&sm.empty[0][sl]);
         }
         __syncwarp();
-        ++s_cnt, ++ord;
+        ++s_cnt;
       };
       const auto pv = [&](int j) {              // O += P(j) V(j)
-        if (!next_kv()) return;
-        if (!rows && (j & 1) != l) return give_back();
+        const uint32_t sl = v_ord % NS;
+        ok = warp_wait(&sm.full[1][sl], (v_ord / NS) & 1, kErrWaitFull);
+        if (!ok) return;
+        ++v_ord;
+        if (!rows && (j & 1) != l) {
+          if (elect_one()) mbar_arrive(&sm.empty[1][sl]);
+          __syncwarp();
+          return;
+        }
         const bool first = rows ? j == 0 : j < 2, last = j + (rows ? 1 : 2) >= n;
         // first: the lane's previous item has left the output columns
         if (first) ok = warp_wait(&sm.o_empty[l], (o_cnt++ & 1) ^ 1, kErrWaitAccum);
         const uint32_t b = p_cnt & 1, t = t_s + 64 * b;
         ok = ok && warp_wait(&sm.p_full[l][b], (p_cnt >> 1) & 1, kErrWaitFull);
         if (!ok) return;
-        const uint64_t vd = v0 + (ord % NS) * (S::kTileBytes >> 4);
+        const uint64_t vd = v0 + sl * (S::kTileBytes >> 4);
         tc_fence_after();
-        if (leader) {
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
             tc_mma_ts(t_o, t + 8 * k, vd + ((k * 2048) >> 4), id_pv, (first && k == 0) ? 0u : 1u);
           tc_commit(&sm.pv_done[l]);
           if (last) tc_commit(&sm.o_full[l]);
-          tc_commit(&sm.empty[ord % NS]);
+          tc_commit(&sm.empty[1][sl]);
         }
         __syncwarp();
-        ++p_cnt, ++ord;
+        ++p_cnt;
       };
-      for (int j = 0; j < ahead && j < n && ok; ++j) qk(j);
 #pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
-        pv(j);
-        if (ok && j + ahead < n) qk(j + ahead);
+      for (int j = 0; j < n + ahead && ok; ++j) {
+        if (j >= ahead) pv(j - ahead);
+        if (ok && j < n) qk(j);
       }
       if (!ok) break;
-      if (leader)
+      if (elect_one())
         for (int i = 0; i < nq; ++i) tc_commit(&sm.q_empty[(qord + i) & 1]);
       qord += nq;
       item_done();
     }
-    // every product and commit of this warp has completed before tensor memory and barriers go
-    if (leader) tc_commit(&sm.drain[l]);
+    // every product and commit of this warp (elect.sync names the same lane each time) has completed before tensor memory and barriers go
+    if (elect_one()) tc_commit(&sm.drain[l]);
     mbar_wait_short(&sm.drain[l], 0, &g_attn_err, kErrDrain);
-  } else {
+  } else if (warp < kWTma) {
     // -------------------------------------------------------------------- softmax, one row a thread
     const int l = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -580,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.a.scale * 1.4426950408889634f;
     const uint64_t c2 = pair(__float_as_uint(c), __float_as_uint(c));
     const int tok = row / p.G;
-    uint32_t cnt = 0, o_cnt = 0, ord_end = 0;   // tiles of this lane so far; ring places of all items so far
+    uint32_t cnt = 0, o_cnt = 0, v_end = 0;     // tiles of this lane so far; V tiles of all items so far
     while (const Item* it = next_item()) {
       const int lo = it->lo, n = it->hi - lo, len = it->len;
       const bool prefix = it->r < 0, rows = it->ntok > p.tb;
@@ -590,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // keys this row sees
       const int lim = !valid ? 0 : (prefix ? len : min(max(it->lim0 + tok_item, 0), len));
       float m = -INFINITY, sum = 0.f;           // m in units of log2, already times c
-      ord_end += 2 * n;
+      v_end += n;
       const int j0 = rows ? 0 : l, step = rows ? 1 : 2;
 #pragma unroll 1
       for (int j = j0; j < n; j += step, ++cnt) {
@@ -634,16 +653,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
               const uint64_t keep2 = pair(__float_as_uint(keep), __float_as_uint(keep));
 #pragma unroll
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tmem_ld32(t_o + 32 * q, o);
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(t_o + 16 * q, o);
                 tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
+                for (int e = 0; e < 16; e += 2) {
                   const float2 f = unpair(mul_pair(pair(o[e], o[e + 1]), keep2));
                   o[e] = __float_as_uint(f.x), o[e + 1] = __float_as_uint(f.y);
                 }
-                tmem_st32(t_o + 32 * q, o);
+                tmem_st16(t_o + 16 * q, o);
               }
             }
           }
@@ -670,11 +689,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // their weight 0 times a NaN would not be 0 (in rows mode both lanes write the same zeros,
         // each before its own product).  Only an item's last tile has such rows.
         if (key0 + kTile > len) {
-          const uint32_t vo = ord_end - 1;
-          ok = warp_wait(&sm.full[vo % NS], (vo / NS) & 1, kErrWaitFull);
+          const uint32_t vo = v_end - 1;
+          ok = warp_wait(&sm.full[1][vo % NS], (vo / NS) & 1, kErrWaitFull);
           if (!ok) break;
           if ((row & 63) >= len - key0 && (row >> 6) < CH) {
-            uint4* z = reinterpret_cast<uint4*>(&sm.kv[vo % NS][(row >> 6) * kKvChunk + (row & 63) * 128]);
+            uint4* z = reinterpret_cast<uint4*>(&sm.kv[1][vo % NS][(row >> 6) * kKvChunk + (row & 63) * 128]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] = make_uint4(0, 0, 0, 0);
           }
@@ -723,25 +742,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the segments of each row, in line order: one warp a row, the lanes over its elements.
+// Joins the segments of each row: W warps a row take its segments in turn (in line order), the
+// lanes over the row's elements, and the first of them adds up what they found.
 constexpr int kJoinWarps = 8;
-template <bool F16, int D>
+template <bool F16, int D, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_constant__ Params p) {
   using V = typename std::conditional<D == 128, float4, float2>::type;
   constexpr int E = D / 32;
+  __shared__ float part[kJoinWarps][32][E + 2];
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long row_out = static_cast<long long>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
+  const long long row_out = static_cast<long long>(blockIdx.x) * (kJoinWarps / W) + warp / W;
   const int t = static_cast<int>(row_out / p.a.Hq);
   const int h = static_cast<int>(row_out - static_cast<long long>(t) * p.a.Hq), kvh = h / p.G, g = h - kvh * p.G;
-  if (t >= p.a.T) return;
   pdl_wait();
+  const bool here = t < p.a.T;
   const int share = __ldcg(p.share);
-  const int4 rec = __ldcg(reinterpret_cast<const int4*>(p.token + t));
-  const int i_tok = __ldcg(&p.token[t].i);
+  const int4 rec = here ? __ldcg(reinterpret_cast<const int4*>(p.token + t)) : make_int4(0, 0, 0, 1);
+  const int i_tok = here ? __ldcg(&p.token[t].i) : 0;
   if (share == 0) return;                               // the requests do not cover the tokens
 
-  // The segments of one run of keys: slots first .. first + count - 1 by way of slot().
+  // The segments of one run of keys: row of segment i of the run in the partial arrays.
   struct Run {
     int cap, row, first, count, step;
     __device__ long long at(int i) const { return static_cast<long long>(first + i * step) * cap + row; }
@@ -763,22 +784,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
   };
   const Run run_p = find(t, p.a.T, p.prefix_tiles, 0, 0, kRows);
   const Run run_s = find(i_tok, rec.w, ceil_div(rec.z, kTile), rec.x, rec.y, p.q_rows_suffix);
-  const int n = run_p.count + run_s.count;
+  const int n = here ? run_p.count + run_s.count : 0;
   float top = -INFINITY, total = 0.f;
   float o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int base = 0; base < n; base += 32) {
-    const int i = base + lane;
-    const int which = i < run_p.count ? 0 : 1, k = which ? i - run_p.count : i;
+  for (int base = 0; base * W < n; base += 32) {
+    const int i = (base + lane) * W + w0;               // this lane's segment
+    const bool in_p = i < run_p.count;
+    const long long at = in_p ? run_p.at(i) : run_s.at(i - run_p.count);
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (i < n) ml = __ldcg(reinterpret_cast<const float2*>(which ? p.ml_s : p.ml_p) + (which ? run_s.at(k) : run_p.at(k)));
+    if (i < n) ml = __ldcg(reinterpret_cast<const float2*>(in_p ? p.ml_p : p.ml_s) + at);
+    // an empty segment (no tile, or nothing seen) has sum 0 and maybe no output: weight 0, not read
+    uint32_t live = __ballot_sync(0xffffffffu, ml.y != 0.f);
     float m2 = fmaxf(top, ml.x);
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, w));
-    const float at = m2 == -INFINITY ? 0.f : m2, keep = exp2_approx(top - at);
-    // an empty segment (no tile, or nothing seen) has sum 0 and maybe no output: weight 0, not read
-    const float wt = ml.y == 0.f ? 0.f : exp2_approx(ml.x - at);
+    const float ref = m2 == -INFINITY ? 0.f : m2, keep = exp2_approx(top - ref);
+    const float wt = ml.y == 0.f ? 0.f : exp2_approx(ml.x - ref);
     float add = ml.y == 0.f ? 0.f : ml.y * wt;
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) add += __shfl_xor_sync(0xffffffffu, add, w);
@@ -786,19 +809,51 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
     total = total * keep + add;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= keep;
-    const uint32_t live = __ballot_sync(0xffffffffu, ml.y != 0.f);
-    const int here = min(32, n - base);
-#pragma unroll 4
-    for (int j = 0; j < here; ++j) {
-      const float f = __shfl_sync(0xffffffffu, wt, j);
-      if (!((live >> j) & 1u)) continue;
-      const int ij = base + j, wh = ij < run_p.count ? 0 : 1, kj = wh ? ij - run_p.count : ij;
-      const V v = __ldcg(reinterpret_cast<const V*>((wh ? p.po_s : p.po_p) + (wh ? run_s.at(kj) : run_p.at(kj)) * D) + lane);
-      const float* vf = reinterpret_cast<const float*>(&v);
+    while (live) {                                      // four segments' loads under way at a time
+      V v[4];
+      float f[4];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(vf[e], f, o[e]);
+      for (int u = 0; u < 4; ++u) {
+        const int j = live ? __ffs(live) - 1 : 0;
+        const bool some = live != 0;
+        f[u] = some ? __shfl_sync(0xffffffffu, wt, j) : 0.f;
+        const long long aj = __shfl_sync(0xffffffffu, at, j);
+        const bool pj = __shfl_sync(0xffffffffu, static_cast<int>(in_p), j);
+        float* z = reinterpret_cast<float*>(&v[u]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) z[e] = 0.f;
+        if (some) v[u] = __ldcg(reinterpret_cast<const V*>((pj ? p.po_p : p.po_s) + aj * D) + lane);
+        live &= live - 1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float* vf = reinterpret_cast<const float*>(&v[u]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(vf[e], f[u], o[e]);
+      }
     }
   }
+  if constexpr (W > 1) {
+    part[warp][lane][0] = top, part[warp][lane][1] = total;
+#pragma unroll
+    for (int e = 0; e < E; ++e) part[warp][lane][2 + e] = o[e];
+    __syncthreads();
+    if (w0 != 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = fmaxf(top, part[warp + w][lane][0]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    total = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = exp2_approx(part[warp + w][lane][0] - ref);
+      total = fmaf(part[warp + w][lane][1], f, total);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(part[warp + w][lane][2 + e], f, o[e]);
+    }
+  }
+  if (!here) return;
   const float inv = total == 0.f ? 0.f : 1.f / total;
   uint16_t* dst = p.a.O + row_out * D + E * lane;
   if constexpr (D == 128)
@@ -848,6 +903,8 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
   Params p{};
   p.a = a;
   p.G = l.G, p.tb = l.tb;
+  p.log_page = 4;
+  while ((1 << p.log_page) < a.page_size) ++p.log_page;
   p.prefix_tiles = (a.prefix_len + kTile - 1) / kTile;
   p.n_prefix = p.prefix_tiles ? l.n_prefix : 0;
   p.q_rows_suffix = l.rows_s;
@@ -877,9 +934,15 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(k_attn<F16, D>, dim3(l.ctas), kThreads, smem, stream, tq_p, tq_s, tk, tv, p);
   if (e != cudaSuccess) return e;
+  // Few rows have many segments each (the prefix is spread over all SMs): more warps a row.
   const long long rows = static_cast<long long>(a.T) * a.Hq;
-  return launch_pdl(k_attn_join<F16, D>, dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0,
-                    stream, p);
+  const auto join = [&](void (*kern)(Params), int w) {
+    const long long per = kJoinWarps / w;
+    return launch_pdl(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), kJoinWarps * 32, 0, stream, p);
+  };
+  if (rows <= 2048) return join(k_attn_join<F16, D, 8>, 8);
+  if (rows <= 8192) return join(k_attn_join<F16, D, 2>, 2);
+  return join(k_attn_join<F16, D, 1>, 1);
 }
 
 }  // namespace
