@@ -53,14 +53,16 @@ namespace {
 
 constexpr int kRows = 128;            // rows per lane
 constexpr int kTile = 64;             // keys per tile
-constexpr int kThreads = 512;         // 2 lanes x 4 softmax warps; two TMA warps, a product warp a lane, scheduler
+constexpr int kThreads = 512;         // 2 lanes x 4 softmax warps; K, V and Q copies, a product warp a lane, scheduler
 constexpr int kWarps = kThreads / 32;
-constexpr int kWTma = 8, kWMma = 10, kWSched = 12;   // warps from 13 on only take part in the set-up
+constexpr int kWTma = 8, kWMma = 10, kWSched = 12, kWQ = 13;   // the last two warps only take part in the set-up
+// Registers a thread: 128 at launch; the softmax warps take what the other eight give up.
+constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr int kItems = 4;             // items the scheduler is ahead of the other warps
 constexpr int kTmemCols = 512;        // two S of 64 columns a lane, then O of 128 a lane
 constexpr int kColO = 256;
 // Weights on the line: a key tile in either mode, and an item's own cost.
-constexpr int kWRows = 4, kWKeys = 4, kWItem = 4;
+constexpr int kWRows = 6, kWKeys = 3, kWItem = 6;
 constexpr long long kMaxLine = 1ll << 30;
 constexpr float kLazy = 8.f;          // rescale when the maximum grew by more than 2^8
 
@@ -106,6 +108,7 @@ struct Params {
   AttnArgs a;
   int G, tb;                 // query heads per key/value head; tokens per lane tile (kRows / G)
   int log_page;              // log2 of the page size
+  int p_rts, p_full, p_head; // prefix: row tiles of a head, line length of a full one, of a head
   int n_prefix;              // prefix items
   int prefix_tiles;
   int q_rows_suffix;         // rows a suffix lane tile can have (its partial's row capacity)
@@ -140,7 +143,9 @@ __device__ __forceinline__ Request request(const AttnArgs& a, int r) {
 }
 
 // Items of ntok tokens: row tiles, and the tokens of tile rt.
-__device__ __forceinline__ int row_tiles(const Params& p, int ntok) { return ceil_div(ntok, 2 * p.tb); }
+__device__ __forceinline__ int row_tiles(const Params& p, int ntok) {
+  return ntok <= 2 * p.tb ? (ntok > 0 ? 1 : 0) : ceil_div(ntok, 2 * p.tb);
+}
 __device__ __forceinline__ int tile_tokens(const Params& p, int ntok, int rt) { return min(2 * p.tb, ntok - rt * 2 * p.tb); }
 __device__ __forceinline__ int weight(const Params& p, int tokens) { return tokens > p.tb ? kWRows : kWKeys; }
 // Line length of all row tiles of one head (T is int or, where it may be too long, long long).
@@ -154,7 +159,8 @@ __device__ __forceinline__ L head_cost(const Params& p, int ntok, int tiles) {
 // First tile of an item (line start s, tiles n of weight w) that starts at or after position b.
 // Tile t therefore belongs to the CTA whose share holds position s + t w.
 __device__ __forceinline__ int tile_at(int b, int s, int n, int w) {
-  return b <= s ? 0 : min(n, static_cast<int>(static_cast<uint32_t>(b - s + w - 1) / static_cast<uint32_t>(w)));
+  const uint32_t x = static_cast<uint32_t>(b - s + w - 1);
+  return b <= s ? 0 : min(n, static_cast<int>(w == kWRows ? x / kWRows : x / kWKeys));
 }
 
 // Walks over the items of one CTA's share (the scheduler warp).
@@ -172,11 +178,10 @@ struct Walk {
     b1 = b0 + share;
     h = p.a.Hkv, t = 0, pline = 0, pitem = 0;
     if (b0 < prefix_cost) {
-      const int hc = prefix_cost / p.a.Hkv, rts = p.n_prefix / p.a.Hkv, full = p.prefix_tiles * kWRows + kWItem;
-      h = b0 / hc;
-      t = min((b0 - h * hc) / full, rts - 1);
-      pline = h * hc + t * full;
-      pitem = h * rts + t;
+      h = b0 / p.p_head;
+      t = p.p_rts == 1 ? 0 : min((b0 - h * p.p_head) / p.p_full, p.p_rts - 1);
+      pline = h * p.p_head + t * p.p_full;
+      pitem = h * p.p_rts + t;
     }
     r = r0, line = r0_line, item = r0_item, kvh = 0, rt = 0;
     if (r < p.a.R) q = request(p.a, r);
@@ -294,14 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.pv_done[i], 1), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.o_empty[i], 4);
       mbar_init(&sm.drain[i], 1);
     }
-    for (int i = 0; i < kItems; ++i) mbar_init(&sm.item_full[i], 1), mbar_init(&sm.item_empty[i], 12);
+    for (int i = 0; i < kItems; ++i) mbar_init(&sm.item_full[i], 1), mbar_init(&sm.item_empty[i], 13);
     fence_barrier_init();
   }
   if (warp == kWMma) {
     tmem_alloc(&sm.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kWTma && lane == 0) {
+  if (warp == kWQ && lane == 0) {
     tma_prefetch_desc(&tq_p), tma_prefetch_desc(&tq_s), tma_prefetch_desc(&tk), tma_prefetch_desc(&tv);
   }
   pdl_launch_dependents();
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---------------------------------------------------------------- the line: its length, and
   // the request in which this CTA's share begins
-  const long long prefix_long = p.a.Hkv * head_cost<long long>(p, p.a.T, p.prefix_tiles);
+  const long long prefix_long = static_cast<long long>(p.a.Hkv) * p.p_head;
   long long mine = 0;
   bool bad = false;
   Request q0;                             // request threadIdx.x, kept for the scan
@@ -407,64 +412,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     ++n_items;
   };
 
+  if (warp >= kWTma) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kWTma || warp == kWTma + 1) {
-    // -------------------------------------------------------------------- TMA producers: Q and K, V
-    // A load of 16-row pages is eight copies a tile, each some 40 cycles to issue, so K and V have a
-    // warp each.  One elected lane issues; the page numbers come to it by shuffles.
-    const bool keys = warp == kWTma;
+    // -------------------------------------------------------------------- TMA producers: K, V
+    // With pages of 16 tokens a tile is eight copies, and each takes some 40 cycles to issue, so K
+    // and V (and Q) have a warp each.  One elected lane issues; the page numbers come to it by
+    // shuffles.
+    const CUtensorMap* map = warp == kWTma ? &tk : &tv;
+    const int ring = warp - kWTma;
     const uint64_t pol_keep = l2_policy_evict_last(), pol_once = l2_policy_evict_first();
     // boxes of 2^lb rows, 2^lt of them a tile, 2^lp of them a page
-    const int lb = min(p.log_page, 6), box = 1 << lb, lt = 6 - lb, boxes = 1 << lt, lp = p.log_page - lb;
-    const CUtensorMap* map = keys ? &tk : &tv;
-    const int ring = keys ? 0 : 1;
-    uint32_t ord = 0, qord = 0;
+    const int lb = min(p.log_page, 6), lt = 6 - lb, lp = p.log_page - lb;
+    uint32_t ord = 0;
     // Page numbers: lane i holds that of box base + i of the segment, read 32 boxes ahead and, for the
     // first 32 boxes, while the segment before is being loaded.
-    const auto boxes_of = [&](const Item* it) { return min(((it->len + box - 1) >> lb) - (it->lo << lt), (it->hi - it->lo) << lt); };
+    const auto boxes_of = [&](const Item* it) {
+      return min(((it->len + (1 << lb) - 1) >> lb) - (it->lo << lt), (it->hi - it->lo) << lt);
+    };
     const auto page_ids = [&](const Item* it, int n_boxes, int base) {
       const int32_t* list = it->r < 0 ? p.a.prefix_pages : p.a.block_table + static_cast<int64_t>(it->r) * p.a.max_blocks;
       return base + lane < n_boxes ? __ldg(list + (((it->lo << lt) + base + lane) >> lp)) : 0;
     };
+    // their rows of the tensor map, page * Hkv + head; -1: zero fill
+    const auto map_row = [&](int id, int kvh) {
+      if (static_cast<uint32_t>(id) < static_cast<uint32_t>(p.a.pages)) return id * p.a.Hkv + kvh;
+      atomicOr(&g_attn_err, kErrIndex);
+      return -1;
+    };
     const Item* it = next_item();
-    int ids = it ? page_ids(it, boxes_of(it), 0) : 0;
+    int raw = it ? page_ids(it, boxes_of(it), 0) : 0;
     while (it) {
-      const int lo = it->lo, n = it->hi - lo, kvh = it->kvh;
-      const bool prefix = it->r < 0, rows = it->ntok > p.tb;
-      const uint64_t pol = prefix ? pol_keep : pol_once;
-      const int n_boxes = boxes_of(it);                // of this segment
+      const int first = it->lo << lt, n = it->hi - it->lo, kvh = it->kvh, n_boxes = boxes_of(it);
+      const uint64_t pol = it->r < 0 ? pol_keep : pol_once;
+      int row = map_row(raw, kvh), raw_next = n_boxes > 32 ? page_ids(it, n_boxes, 32) : 0;
       const Item* after = peek_item();
       if (!ok) break;
-      const int ids_after = after ? page_ids(after, boxes_of(after), 0) : 0;
-      int ids_next = page_ids(it, n_boxes, 32);
-      if (keys) {   // Q: one 128-row tile, or one per lane
-        const int box_tok = prefix ? p.tb : min(p.tb, p.a.max_new);
-        for (int i = 0; i < (rows ? 2 : 1) && ok; ++i, ++qord) {
-          const int s = qord & 1;
-          ok = warp_wait(&sm.q_empty[s], ((qord >> 1) & 1) ^ 1, kErrWaitEmpty);
-          if (!ok) break;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&sm.q_full[s], box_tok * p.G * 128 * CH);
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-              tma_load_4d(&sm.q[s][c * kQChunk], prefix ? &tq_p : &tq_s, 0, c, kvh * p.G, it->tok0 + i * p.tb, &sm.q_full[s],
-                          pol_keep);
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-      }
+      raw = after ? page_ids(after, boxes_of(after), 0) : 0;
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++ord) {
-        const int s = ord % NS, b0 = j << lt, here = min(boxes, n_boxes - b0);
-        // rows of the tensor map, page * Hkv + head; -1: zero fill
-        int row[4];
+        const int s = ord % NS, b0 = j << lt, here = min(1 << lt, n_boxes - b0);
+        const int in_page = ((first + b0) & ((1 << lp) - 1)) << lb;    // pages of 128: one box a tile, half a page
+        int rows[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int id = __shfl_sync(0xffffffffu, ids, (b0 + i) & 31);
-          row[i] = id < 0 || id >= p.a.pages ? -1 : id * p.a.Hkv + kvh;
-          if (row[i] < 0 && i < here && lane == 0) atomicOr(&g_attn_err, kErrIndex);
-        }
-        const int row0 = (((lo << lt) + b0) & ((1 << lp) - 1)) << lb;   // pages of 128: one box a tile, half a page
+        for (int i = 0; i < 4; ++i) rows[i] = __shfl_sync(0xffffffffu, row, (b0 + i) & 31);
         ok = warp_wait(&sm.empty[ring][s], ((ord / NS) & 1) ^ 1, kErrWaitEmpty);
         if (!ok) break;
         if (elect_one()) {
@@ -474,19 +465,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i < here) {
 #pragma unroll
               for (int c = 0; c < CH; ++c)
-                tma_load_4d(&sm.kv[ring][s][c * kKvChunk + ((i << lb) * 128)], map, 0, row0, c, row[i], &sm.full[ring][s], pol);
+                tma_load_4d(&sm.kv[ring][s][c * kKvChunk + ((i << lb) * 128)], map, 0, in_page, c, rows[i], &sm.full[ring][s],
+                            pol);
             }
         }
         __syncwarp();
-        if (((b0 + boxes) & 31) == 0) ids = ids_next, ids_next = page_ids(it, n_boxes, b0 + boxes + 32);
+        if (((b0 + (1 << lt)) & 31) == 0 && j + 1 < n) {
+          row = map_row(raw_next, kvh);
+          raw_next = page_ids(it, n_boxes, b0 + (1 << lt) + 32);
+        }
       }
       if (!ok) break;
       item_done();
-      it = after, ids = ids_after;
+      it = after;
     }
     // drain: the last fill of each slot has landed before the CTA's memory goes
     for (uint32_t i = ord > NS ? ord - NS : 0; i < ord; ++i)
       mbar_wait_short(&sm.full[ring][i % NS], (i / NS) & 1, &g_attn_err, kErrDrain);
+  } else if (warp == kWQ) {
+    // -------------------------------------------------------------------- TMA producer: Q
+    const uint64_t pol_keep = l2_policy_evict_last();
+    uint32_t qord = 0;
+    while (const Item* it = next_item()) {   // one 128-row tile, or one per lane
+      const bool prefix = it->r < 0;
+      const int box_tok = prefix ? p.tb : min(p.tb, p.a.max_new);
+      for (int i = 0; i < (it->ntok > p.tb ? 2 : 1); ++i, ++qord) {
+        const int s = qord & 1;
+        ok = warp_wait(&sm.q_empty[s], ((qord >> 1) & 1) ^ 1, kErrWaitEmpty);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.q_full[s], box_tok * p.G * 128 * CH);
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            tma_load_4d(&sm.q[s][c * kQChunk], prefix ? &tq_p : &tq_s, 0, c, it->kvh * p.G, it->tok0 + i * p.tb, &sm.q_full[s],
+                        pol_keep);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      item_done();
+    }
     for (uint32_t i = qord > 2 ? qord - 2 : 0; i < qord; ++i)
       mbar_wait_short(&sm.q_full[i & 1], (i >> 1) & 1, &g_attn_err, kErrDrain);
   } else if (warp == kWSched) {
@@ -590,7 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every product and commit of this warp (elect.sync names the same lane each time) has completed before tensor memory and barriers go
     if (elect_one()) tc_commit(&sm.drain[l]);
     mbar_wait_short(&sm.drain[l], 0, &g_attn_err, kErrDrain);
-  } else if (warp < kWTma) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------------- softmax, one row a thread
     const int l = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -907,6 +927,16 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
   while ((1 << p.log_page) < a.page_size) ++p.log_page;
   p.prefix_tiles = (a.prefix_len + kTile - 1) / kTile;
   p.n_prefix = p.prefix_tiles ? l.n_prefix : 0;
+  // The line is 32 bits on the device; a prefix alone that passes it is refused (kMaxLine / 4 tiles
+  // of rows: 2^28 / 8 heads / 128 rows and 2^21 keys, for example).
+  const long long full = static_cast<long long>(p.prefix_tiles) * kWRows + kWItem;
+  const int span = 2 * p.tb;
+  p.p_rts = (a.T + span - 1) / span;
+  const int last = a.T - (p.p_rts - 1) * span;
+  const long long head = p.prefix_tiles
+      ? (p.p_rts - 1) * full + static_cast<long long>(p.prefix_tiles) * (last > p.tb ? kWRows : kWKeys) + kWItem : 0;
+  if (head * a.Hkv > kMaxLine) return cudaErrorInvalidValue;
+  p.p_full = static_cast<int>(full), p.p_head = static_cast<int>(head);
   p.q_rows_suffix = l.rows_s;
   p.ctas = l.ctas;
   p.token = reinterpret_cast<TokenRecord*>(ws + l.token);

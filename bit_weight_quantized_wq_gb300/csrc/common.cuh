@@ -98,9 +98,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
 
 // The same wait for short hand-offs on a kernel's critical path: the limit (4e9 SM cycles, about
 // two seconds) is read on the SM's own cycle counter -- the nanosecond timer of mbar_wait takes long
-// enough to read to delay the wake-up -- and everything past the first poll is out of line, so that
-// a kernel with many waits stays small.
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
+// enough to read to delay the wake-up.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
+  if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (clock64() - t0 > 4000000000ll) {
@@ -109,9 +109,6 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
     }
   }
   return true;
-}
-__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
-  return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, err, code);
 }
 
 // The same bounded wait with the limit given in nanoseconds.
