@@ -728,7 +728,7 @@ wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_str
 }
 
 static bool lora_shape_ok(int64_t M, int64_t K, int64_t N, int64_t r) {
-  return M >= 1 && N >= 1 && K >= 8 && K % 8 == 0 && r >= 8 && r <= 128 && r % 8 == 0 && M <= (1 << 24) &&
+  return M >= 1 && N >= 1 && K >= 8 && K % 8 == 0 && r >= 8 && r <= 128 && r % 8 == 0 && M <= (1 << 22) &&
          N <= (1 << 24) && K <= (1 << 24);
 }
 

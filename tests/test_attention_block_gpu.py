@@ -392,6 +392,10 @@ LORA = [  # M, K, N, r, L, adapters of the rows
     (1000, 256, 320, 16, 6, "runs"),
     (513, 640, 250, 8, 4, "mixed"),
     (40, 128, 64, 16, 2, "none"),
+    (1500, 256, 200, 64, 5, "runs"),
+    (2100, 136, 72, 96, 9, "mixed"),
+    (1025, 2048, 64, 8, 1, "one"),
+    (1100, 512, 41, 128, 40, "each"),
 ]
 
 
