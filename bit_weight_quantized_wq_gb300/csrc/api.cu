@@ -736,7 +736,7 @@ static wq_status check_lora(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
                             int64_t L, int64_t r, const int32_t* ranks, const int32_t* adapter, const float* scales,
                             const uint16_t* Y) {
   if (!X || !A || !B || !adapter || !scales || !Y) return WQ_ERR_NULL;
-  if (!lora_shape_ok(M, K, N, r) || L < 1 || L > (1 << 24)) return WQ_ERR_SHAPE;
+  if (!lora_shape_ok(M, K, N, r) || L < 1 || L * r > 0x7fffff00LL || L > (1 << 24)) return WQ_ERR_SHAPE;
   const auto odd4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
   if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || odd4(ranks) || odd4(adapter) || odd4(scales))
     return WQ_ERR_ALIGN;

@@ -18,6 +18,7 @@
 
 #include "elem16.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace wq {
 
@@ -99,6 +100,15 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
+
+// 16 bytes global -> this thread's own place in shared memory, zeros where !on; groups complete in
+// order.  Only the thread that copied reads the place, so its own wait is all the ordering needed.
+__device__ __forceinline__ void copy16(void* dst, const uint16_t* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Steps of 32 of the contracted index that slice i of n takes.
 __device__ __forceinline__ void slice(int steps, int i, int n, int& lo, int& hi) {
@@ -196,100 +206,231 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
   if (n > 1) cluster_sync();                  // the others have read this CTA's sums
 }
 
-// Many rows: a cluster for each 128 rows (and each 64 ranks); a warp has 32 rows and half of the
-// CTA's slice of K, and runs through the adapters of its rows.  Four warps read the same A, from L1.
-constexpr int kTileRows = 128;
+// Many rows: a cluster for each 128 rows (and each 64 ranks), its CTAs a slice of K each, on the
+// tensor cores: tcgen05.mma with X [128 rows, 64 k] and A [ranks, 64 k] by TMA (128-byte swizzle), one
+// accumulator in tensor memory for each adapter that occurs in the rows, two adapters a pass over
+// the slice.  Three stages of 32 KB and two CTAs an SM keep some 150 KB of loads under way; the
+// same contraction on mma.sync, with A prefetched one step ahead, waited for L2 at every step.
+constexpr int kTileRows = 128, kTileStages = 3, kTilePass = 2;
+constexpr int kTileLd = 64 + 4;
+struct TileSmem {
+  union {
+    struct {
+      uint8_t x[kTileStages][kTileRows * 128];
+      uint8_t a[kTileStages][kTilePass][64 * 128];
+    } ring;
+    float red[kTileRows * kTileLd];            // after the last product
+  };
+  uint64_t full[kTileStages], empty[kTileStages], acc_full[2], acc_empty[2], drain;
+  int id[kTileRows];                           // adapter of each row
+  int found[kTileRows];                        // the different ones, in order of their first row
+  int n_found[4];
+  uint32_t tmem_base;
+};
+
 template <bool F16>
-__global__ void __launch_bounds__(256) k_lora_shrink_tile(const LoraArgs p, uint16_t* V) {
-  constexpr int W = 64, RB = 2, NT = 8, LD = W + 4;
-  __shared__ float red[kTileRows * LD];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int part = warp >> 2, r0 = (warp & 3) * 32;            // K half, first row in the tile
+__global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ta,
+                                                          const LoraArgs p, uint16_t* V, int box_ranks) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  TileSmem& sm = *reinterpret_cast<TileSmem*>(smem_raw + smem_align_pad(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTileStages; ++s) mbar_init(&sm.full[s], 1), mbar_init(&sm.empty[s], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.acc_full[i], 1), mbar_init(&sm.acc_empty[i], 4);
+    mbar_init(&sm.drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, 256);            // two sets of two accumulators of 64 columns
+    tmem_relinquish();
+  }
   pdl_wait();
   pdl_launch_dependents();
-  const int m0 = blockIdx.y * kTileRows + r0, j0 = blockIdx.z * W;
-  const int mine = row_adapter(p, m0 + lane);
-  float acc[RB][NT][4];
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[b][t][e] = 0.f;
-  int lo, hi;
-  slice((p.K + 31) / 32, blockIdx.x * 2 + part, gridDim.x * 2, lo, hi);
-  for (uint32_t todo = leaders(mine); todo; todo &= todo - 1) {
-    const int a = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
-    const uint32_t rows = __ballot_sync(0xffffffffu, mine == a) >> g;
-    const uint32_t on = (rows & 1u) | ((rows >> 7) & 2u) | ((rows >> 14) & 4u) | ((rows >> 21) & 8u);
-    const int tiles = min(NT, (adapter_rank(p, a) - j0) / 8);
-    if (tiles > 0)
-      shrink_loop<F16, RB, NT, 1>(acc, p, p.X + static_cast<int64_t>(m0) * p.K,
-                                  p.A + (static_cast<int64_t>(a) * p.r + j0) * p.K, on, tiles, lo, hi);
-  }
-#pragma unroll
-  for (int h = 1; h >= 0; --h) {               // half 1 writes, half 0 adds its own
-    if (part == h) {
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            float2* d = reinterpret_cast<float2*>(red + (r0 + 16 * b + 4 * e + g) * LD + 8 * t + 2 * q);
-            const float2 o = h ? make_float2(0.f, 0.f) : *d;
-            *d = make_float2(acc[b][t][e] + o.x, acc[b][t][e + 1] + o.y);
-          }
-    }
+  const int m0 = blockIdx.y * kTileRows, j0 = blockIdx.z * 64;
+  const int row = (warp & 3) * 32 + lane;      // warps 2 .. 5: a row a thread, its tensor-memory lane
+  int mine = -1;
+  if (warp >= 2) sm.id[row] = mine = row_adapter(p, m0 + row);
+  __syncthreads();
+  int place = -1;                              // of this row's adapter in `found`
+  {
+    bool leads = mine >= 0;
+    int first = row;
+    if (warp >= 2 && mine >= 0)
+      for (int i = 0; i < row; ++i)
+        if (sm.id[i] == mine) {
+          leads = false, first = i;
+          break;
+        }
+    const uint32_t lead = __ballot_sync(0xffffffffu, leads);
+    if (warp >= 2 && lane == 0) sm.n_found[warp & 3] = __popc(lead);
     __syncthreads();
+    if (warp >= 2 && leads) {
+      place = __popc(lead & ((1u << lane) - 1));
+      for (int w = 0; w < (warp & 3); ++w) place += sm.n_found[w];
+      sm.found[place] = mine;
+      sm.id[row] = -2 - place;                 // followers look it up
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp >= 2 && mine >= 0 && !leads) place = -2 - sm.id[first];
+  }
+  const int found = sm.n_found[0] + sm.n_found[1] + sm.n_found[2] + sm.n_found[3];
+  const int passes = (found + kTilePass - 1) / kTilePass;
+  int lo, hi;
+  slice((p.K + 63) / 64, blockIdx.x, gridDim.x, lo, hi);
+  const uint32_t tmem = sm.tmem_base;
+  float res[64];
+#pragma unroll
+  for (int e = 0; e < 64; ++e) res[e] = 0.f;
+
+  if (warp == 0) {
+    uint32_t ord = 0;
+    bool ok = true;
+    const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+    for (int ps = 0; ps < passes && ok; ++ps) {
+      const int n = min(kTilePass, found - ps * kTilePass);
+      for (int s = lo; s < hi; ++s, ++ord) {
+        const int st = ord % kTileStages;
+        ok = __all_sync(0xffffffffu, mbar_wait_short(&sm.empty[st], ((ord / kTileStages) & 1) ^ 1, &g_lora_err, kErrWaitEmpty));
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.full[st], kTileRows * 128 + n * box_ranks * 128);
+          tma_load_2d(sm.ring.x[st], &tx, s * 64, m0, &sm.full[st], passes > 1 ? keep : once);
+          for (int d = 0; d < n; ++d)
+            tma_load_2d(sm.ring.a[st][d], &ta, s * 64, sm.found[ps * kTilePass + d] * p.r + j0, &sm.full[st], keep);
+        }
+        __syncwarp();
+      }
+    }
+    for (uint32_t i = ord > kTileStages ? ord - kTileStages : 0; i < ord; ++i)
+      mbar_wait_short(&sm.full[i % kTileStages], (i / kTileStages) & 1, &g_lora_err, kErrDrain);
+  } else if (warp == 1) {
+    constexpr uint32_t fmt = F16 ? 0u : 1u;
+    const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(box_ranks >> 3) << 17) | ((kTileRows >> 4) << 24);
+    uint32_t ord = 0;
+    bool ok = true;
+    for (int ps = 0; ps < passes && ok; ++ps) {
+      const int n = min(kTilePass, found - ps * kTilePass), set = ps & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait_short(&sm.acc_empty[set], ((ps >> 1) & 1) ^ 1, &g_lora_err, kErrWaitAccum));
+      for (int s = lo; s < hi && ok; ++s, ++ord) {
+        const int st = ord % kTileStages;
+        ok = __all_sync(0xffffffffu, mbar_wait_short(&sm.full[st], (ord / kTileStages) & 1, &g_lora_err, kErrWaitFull));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t xd = smem_desc_sw128(smem_u32(sm.ring.x[st]));
+          for (int d = 0; d < n; ++d) {
+            const uint64_t ad = smem_desc_sw128(smem_u32(sm.ring.a[st][d]));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_ss_f16(tmem + 128 * set + 64 * d, xd + 2 * k, ad + 2 * k, idesc, (s > lo || k) ? 1u : 0u);
+          }
+          tc_commit(&sm.empty[st]);
+        }
+        __syncwarp();
+      }
+      if (ok && elect_one()) tc_commit(&sm.acc_full[set]);
+      __syncwarp();
+    }
+    if (elect_one()) tc_commit(&sm.drain);     // nothing under way any more, whatever happened
+    mbar_wait_short(&sm.drain, 0, &g_lora_err, kErrDrain);
+  } else {
+    for (int ps = 0; ps < passes; ++ps) {
+      const int n = min(kTilePass, found - ps * kTilePass), set = ps & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_short(&sm.acc_full[set], (ps >> 1) & 1, &g_lora_err, kErrWaitAccum))) break;
+      tc_fence_after();
+      for (int d = 0; d < n && lo < hi; ++d) {
+        const bool own = place == ps * kTilePass + d;
+        if (!__any_sync(0xffffffffu, own)) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+          tmem_ld32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 * set + 64 * d + 32 * h, v);
+          tc_wait_ld();
+          if (own)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) res[32 * h + e] = __uint_as_float(v[e]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.acc_empty[set]);
+    }
+  }
+  __syncwarp();
+  __syncthreads();                             // the ring is idle: its memory holds the sums now
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+  if (warp >= 2) {
+    float4* d = reinterpret_cast<float4*>(sm.red + row * kTileLd);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) d[e] = make_float4(res[4 * e], res[4 * e + 1], res[4 * e + 2], res[4 * e + 3]);
   }
   const uint32_t n = gridDim.x;
   if (n > 1) cluster_sync();
+  else __syncthreads();
   // each CTA of the cluster finishes its share of the rows, a warp a row at a time
-  for (int row = cluster_rank() * 8 + warp; row < kTileRows; row += 8 * n) {
-    const int m = blockIdx.y * kTileRows + row;
+  for (int r = cluster_rank() * 6 + warp; r < kTileRows; r += 6 * n) {
+    const int m = m0 + r;
     const int a = row_adapter(p, m);
     if (a < 0) continue;
     const float s = __ldg(p.scales + a);
     const int rank = adapter_rank(p, a) - j0;
     float2 v = make_float2(0.f, 0.f);
     for (uint32_t c = 0; c < n; ++c) {
-      const float* src = red + row * LD + 2 * lane;
+      const float* src = sm.red + r * kTileLd + 2 * lane;
       v.x += n > 1 ? ld_cluster(src, c) : src[0];
       v.y += n > 1 ? ld_cluster(src + 1, c) : src[1];
     }
     if (2 * lane < rank)
       *reinterpret_cast<uint32_t*>(V + static_cast<int64_t>(m) * p.r + j0 + 2 * lane) = pack2<F16>(v.x * s, v.y * s);
   }
-  if (n > 1) cluster_sync();
+  if (n > 1) cluster_sync();                   // the others have read this CTA's sums
 }
 
-// The expand: a warp has 16 rows and 64 output columns.  Output tile t of 8 columns stands for the
-// columns 32 (t / 4) + 8 (c / 2) + 2 (t % 4) + c % 2, c = 0 .. 7, so that a lane's results of four
-// tiles are 8 neighbouring columns: base and Y move 16 bytes a lane.
-constexpr int kCols = 64;
+// The expand: a warp has 16 rows, 32 output columns and every `subsets`-th adapter of those rows
+// (their rows are its own to write; rows without an adapter are the first warp's).  Output tile t
+// of 8 columns stands for the columns 8 (c / 2) + 2 t + c % 2, c = 0 .. 7, so that a lane's results
+// of four tiles are 8 neighbouring columns: base and Y move 16 bytes a lane.
+constexpr int kCols = 32;
 template <bool F16, int CH>     // CH: chunks of 32 ranks
-__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uint16_t* V, int row_warps) {
+__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uint16_t* V, int log_rows, int log_subsets) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int col_warps = (blockDim.x >> 5) / row_warps;
-  const int m0 = (blockIdx.y * row_warps + warp % row_warps) * 16;
-  const int n0 = (blockIdx.x * col_warps + warp / row_warps) * kCols;
+  // warps of a CTA: row blocks first (they share B through L1), then subsets, then columns
+  const int subset = (warp >> log_rows) & ((1 << log_subsets) - 1);
+  const int m0 = ((blockIdx.y << log_rows) + (warp & ((1 << log_rows) - 1))) * 16;
+  const int col_warps = (blockDim.x >> 5) >> (log_rows + log_subsets);
+  const int n0 = (blockIdx.x * col_warps + (warp >> (log_rows + log_subsets))) * kCols;
   pdl_launch_dependents();
   if (m0 >= p.M || n0 >= p.N) return;          // whole warps
   const int mine = lane < 16 ? row_adapter(p, m0 + lane) : -1;
-  uint32_t todo = leaders(mine);
+  uint32_t todo = 0;                           // this subset's leading rows
+  {
+    uint32_t lead = leaders(mine);
+    for (int i = 0; lead; ++i, lead &= lead - 1)
+      if ((i & ((1 << log_subsets) - 1)) == subset) todo |= lead & (0u - lead);
+  }
+  // the leading row of each of the two rows this lane holds, and whether they are this warp's
+  const uint32_t same = __match_any_sync(0xffffffffu, mine);
+  const int first = __ffs(same) - 1;
+  const bool own_row = mine >= 0 ? ((todo >> first) & 1u) != 0 : subset == 0;
+  if (!__any_sync(0xffffffffu, lane < 16 && own_row)) return;
+  const uint32_t own_rows = __ballot_sync(0xffffffffu, lane < 16 && own_row);
   // B of one adapter and chunk of ranks: column of tile t, 8 ranks a lane
-  const auto load_b = [&](uint4 (&b)[8], int a, int rank, int ch) {
+  const auto load_b = [&](uint4 (&b)[4], int a, int rank, int ch) {
     const int k = 32 * ch + 8 * q;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int n = n0 + 32 * (t >> 2) + 8 * (g >> 1) + 2 * (t & 3) + (g & 1);
+    for (int t = 0; t < 4; ++t) {
+      const int n = n0 + 8 * (g >> 1) + 2 * t + (g & 1);
       b[t] = make_uint4(0, 0, 0, 0);
       if (k < rank && n < p.N) b[t] = ld_shared_operand(p.B + (static_cast<int64_t>(a) * p.N + n) * p.r + k);
     }
   };
   int a = 0, rank = 0;
-  uint4 b[8];
+  uint4 b[4];
   if (todo) {
     a = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
     rank = adapter_rank(p, a);
@@ -297,31 +438,25 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
   }
   pdl_wait();
   const int id[2] = {__shfl_sync(0xffffffffu, mine, g), __shfl_sync(0xffffffffu, mine, g + 8)};
-  uint4 v[CH][2];
+  const bool own[2] = {((own_rows >> g) & 1u) != 0, ((own_rows >> (g + 8)) & 1u) != 0};
+  uint4 v[CH][2], base[2];
+  const bool vec = p.N % 8 == 0;
+  const int n = n0 + 8 * q;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int own = id[h] >= 0 ? adapter_rank(p, id[h]) : 0;
+    const int m = m0 + 8 * h + g;
+    const int ranks = own[h] && id[h] >= 0 ? adapter_rank(p, id[h]) : 0;
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
       v[ch][h] = make_uint4(0, 0, 0, 0);
-      if (32 * ch + 8 * q < own)
-        v[ch][h] = __ldcg(reinterpret_cast<const uint4*>(V + static_cast<int64_t>(m0 + 8 * h + g) * p.r + 32 * ch + 8 * q));
+      if (32 * ch + 8 * q < ranks)
+        v[ch][h] = __ldcg(reinterpret_cast<const uint4*>(V + static_cast<int64_t>(m) * p.r + 32 * ch + 8 * q));
     }
+    if (vec && own[h] && m < p.M && n < p.N) base[h] = *reinterpret_cast<const uint4*>(p.base + static_cast<int64_t>(m) * p.N + n);
   }
-  const bool vec = p.N % 8 == 0;
-  uint4 base[2][2];                            // [row half][32 columns]
-  if (vec) {
+  float acc[4][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int m = m0 + 8 * h + g, n = n0 + 32 * c + 8 * q;
-        if (m < p.M && n < p.N) base[h][c] = *reinterpret_cast<const uint4*>(p.base + static_cast<int64_t>(m) * p.N + n);
-      }
-  }
-  float acc[8][4];
-#pragma unroll
-  for (int t = 0; t < 8; ++t)
+  for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
   while (todo) {
@@ -331,48 +466,152 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      uint4 nb[8];
+      uint4 nb[4];
       if (ch + 1 < CH) load_b(nb, a, rank, ch + 1);
       else load_b(nb, next, next_rank, 0);
       const uint4 lo = id[0] == a ? v[ch][0] : zero, hi = id[1] == a ? v[ch][1] : zero;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) mma_k32<F16>(acc[t], lo, hi, b[t]);
+      for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], lo, hi, b[t]);
 #pragma unroll
-      for (int t = 0; t < 8; ++t) b[t] = nb[t];
+      for (int t = 0; t < 4; ++t) b[t] = nb[t];
     }
     a = next, rank = next_rank;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int m = m0 + 8 * h + g;
-    if (m >= p.M) continue;
+    if (m >= p.M || !own[h]) continue;
+    const int64_t at = static_cast<int64_t>(m) * p.N + n;
+    if (vec) {
+      if (n >= p.N) continue;
+      uint32_t w[4] = {base[h].x, base[h].y, base[h].z, base[h].w};
+      if (id[h] >= 0) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int n = n0 + 32 * c + 8 * q;
-      const int64_t at = static_cast<int64_t>(m) * p.N + n;
-      if (vec) {
-        if (n >= p.N) continue;
-        uint32_t w[4] = {base[h][c].x, base[h][c].y, base[h][c].z, base[h][c].w};
-        if (id[h] >= 0) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const float2 f = unpack2<F16>(w[t]);
-            w[t] = pack2<F16>(f.x + acc[4 * c + t][2 * h], f.y + acc[4 * c + t][2 * h + 1]);
-          }
+        for (int t = 0; t < 4; ++t) {
+          const float2 f = unpack2<F16>(w[t]);
+          w[t] = pack2<F16>(f.x + acc[t][2 * h], f.y + acc[t][2 * h + 1]);
         }
-        *reinterpret_cast<uint4*>(p.Y + at) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int64_t i = at + 2 * t + e;
-            if (n + 2 * t + e >= p.N) continue;
-            p.Y[i] = id[h] >= 0 ? round1<F16>(load1<F16>(p.base + i) + acc[4 * c + t][2 * h + e]) : p.base[i];
-          }
       }
+      *reinterpret_cast<uint4*>(p.Y + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t i = at + 2 * t + e;
+          if (n + 2 * t + e >= p.N) continue;
+          p.Y[i] = id[h] >= 0 ? round1<F16>(load1<F16>(p.base + i) + acc[t][2 * h + e]) : p.base[i];
+        }
     }
   }
+}
+
+// The expand of many rows: a warp keeps its 16 rows and walks over `span` column tiles, so that the
+// row set-up is done once and the next tiles' base (a queue of kBaseQueue tiles a thread in shared
+// memory) and B (the next step's, in registers) are under way while a tile is computed.
+constexpr int kBaseQueue = 6;
+template <bool F16, int CH>
+__global__ void __launch_bounds__(256) k_lora_expand_run(const LoraArgs p, const uint16_t* V, int span) {
+  __shared__ uint4 base_queue[kBaseQueue][2][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int m0 = (blockIdx.y * 8 + warp) * 16;
+  const int tiles = (p.N + kCols - 1) / kCols;
+  const int lo = blockIdx.x * span, hi = min(lo + span, tiles);
+  pdl_launch_dependents();
+  if (m0 >= p.M) return;                       // whole warps
+  const int mine = lane < 16 ? row_adapter(p, m0 + lane) : -1;
+  const uint32_t lead = leaders(mine);
+  const int id[2] = {__shfl_sync(0xffffffffu, mine, g), __shfl_sync(0xffffffffu, mine, g + 8)};
+  const auto load_b = [&](uint4 (&b)[4], int a, int rank, int ch, int ct) {
+    const int k = 32 * ch + 8 * q, n0 = ct * kCols + 8 * (g >> 1) + (g & 1);
+    const uint16_t* src = p.B + (static_cast<int64_t>(a) * p.N + n0) * p.r + k;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      b[t] = make_uint4(0, 0, 0, 0);
+      if (k < rank && n0 + 2 * t < p.N) b[t] = ld_shared_operand(src + static_cast<int64_t>(2 * t) * p.r);
+    }
+  };
+  const auto fetch_base = [&](int ct, int at) {
+    const int n = ct * kCols + 8 * q;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = m0 + 8 * h + g;
+      const bool on = ct < hi && m < p.M && n < p.N;
+      copy16(&base_queue[at][h][threadIdx.x], on ? p.base + static_cast<int64_t>(m) * p.N + n : p.base, on);
+    }
+    copy_commit();
+  };
+  int a0 = 0, rank0 = 0;
+  uint4 b[4];
+  if (lead) {
+    a0 = __shfl_sync(0xffffffffu, mine, __ffs(lead) - 1);
+    rank0 = adapter_rank(p, a0);
+    load_b(b, a0, rank0, 0, lo);
+  }
+  pdl_wait();
+  for (int i = 0; i < kBaseQueue - 1; ++i) fetch_base(lo + i, i);
+  uint4 v[CH][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int ranks = id[h] >= 0 ? adapter_rank(p, id[h]) : 0;
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      v[ch][h] = make_uint4(0, 0, 0, 0);
+      if (32 * ch + 8 * q < ranks)
+        v[ch][h] = __ldcg(reinterpret_cast<const uint4*>(V + static_cast<int64_t>(m0 + 8 * h + g) * p.r + 32 * ch + 8 * q));
+    }
+  }
+  int at = 0;
+#pragma unroll 1
+  for (int ct = lo; ct < hi; ++ct) {
+    fetch_base(ct + kBaseQueue - 1, at == 0 ? kBaseQueue - 1 : at - 1);
+    float acc[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+    int a = a0, rank = rank0;
+    uint32_t todo = lead;
+    while (todo) {
+      todo &= todo - 1;
+      // the next adapter of the block, or the first one of the next tile
+      const int next = todo ? __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1) : a0;
+      const int next_rank = todo ? adapter_rank(p, next) : rank0;
+      const int next_ct = todo ? ct : min(ct + 1, hi - 1);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch) {
+        uint4 nb[4];
+        if (ch + 1 < CH) load_b(nb, a, rank, ch + 1, ct);
+        else load_b(nb, next, next_rank, 0, next_ct);
+        const uint4 x0 = id[0] == a ? v[ch][0] : zero, x1 = id[1] == a ? v[ch][1] : zero;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], x0, x1, b[t]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) b[t] = nb[t];
+      }
+      a = next, rank = next_rank;
+    }
+    copy_wait<kBaseQueue - 1>();
+    const int n = ct * kCols + 8 * q;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = m0 + 8 * h + g;
+      const uint4 y = base_queue[at][h][threadIdx.x];
+      uint32_t w[4] = {y.x, y.y, y.z, y.w};
+      if (id[h] >= 0) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float2 f = unpack2<F16>(w[t]);
+          w[t] = pack2<F16>(f.x + acc[t][2 * h], f.y + acc[t][2 * h + 1]);
+        }
+      }
+      if (m < p.M && n < p.N)
+        *reinterpret_cast<uint4*>(p.Y + static_cast<int64_t>(m) * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    at = at + 1 == kBaseQueue ? 0 : at + 1;
+  }
+  copy_wait<0>();
 }
 
 // Launch with programmatic serialization, and clusters of `cluster` CTAs along x.
@@ -398,6 +637,8 @@ cudaError_t launch_cluster(void (*kern)(P...), dim3 grid, unsigned threads, size
 
 // Up to this many rows a cluster for each leading row; above, for each 128 rows.
 constexpr int kRowsMax = 1024;
+// From this many rows on the expand walks over column tiles.
+constexpr int kRunRows = 256;
 
 template <bool F16, int NT>
 cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
@@ -420,23 +661,48 @@ cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
     if (a.r <= 64) return launch_rows<F16, 8>(a, V, stream);
     return launch_rows<F16, 16>(a, V, stream);
   }
-  const int tiles = (a.M + kTileRows - 1) / kTileRows, steps = (a.K + 31) / 32;
-  unsigned c = 1;
-  while (c < 8 && tiles * c < 2u * device_sm_count() && steps >= static_cast<int>(2 * c) * 8) c *= 2;
-  return launch_cluster(k_lora_shrink_tile<F16>, dim3(c, tiles, (a.r + 63) / 64), 256, 0, c, stream, a, V);
+  const int tiles = (a.M + kTileRows - 1) / kTileRows, steps = (a.K + 63) / 64;
+  unsigned c = 1;                              // two CTAs an SM, at least four steps of 64 each
+  while (c < 8 && static_cast<int>(tiles * c) < 2 * device_sm_count() && steps >= static_cast<int>(2 * c) * 4) c *= 2;
+  const int box_ranks = std::min(64, (a.r + 15) / 16 * 16);
+  const CUtensorMapDataType dt = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap tx, ta;
+  cudaError_t e = make_tmap_2d(&tx, dt, a.X, a.K, a.M, static_cast<uint64_t>(a.K) * 2, 64, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  if (e == cudaSuccess)
+    e = make_tmap_2d(&ta, dt, a.A, a.K, static_cast<uint64_t>(a.L) * a.r, static_cast<uint64_t>(a.K) * 2, 64, box_ranks,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  constexpr size_t smem = sizeof(TileSmem) + 1024;
+  if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(k_lora_shrink_tile<F16>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(k_lora_shrink_tile<F16>, dim3(c, tiles, (a.r + 63) / 64), 192, smem, c, stream, tx, ta, a, V, box_ranks);
 }
 
 template <bool F16>
 cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, cudaStream_t stream) {
-  const int blocks = (a.M + 15) / 16, cols = (a.N + kCols - 1) / kCols;
-  // 8 warps a CTA: as many row blocks as there are (they share B through L1), then columns
-  int rw = 1;
-  while (rw < 8 && rw < blocks) rw *= 2;
-  const int cw = 8 / rw;
-  const dim3 grid((cols + cw - 1) / cw, (blocks + rw - 1) / rw);
-  if (a.r <= 32) return launch_pdl(k_lora_expand<F16, 1>, grid, 256, 0, stream, a, V, rw);
-  if (a.r <= 64) return launch_pdl(k_lora_expand<F16, 2>, grid, 256, 0, stream, a, V, rw);
-  return launch_pdl(k_lora_expand<F16, 4>, grid, 256, 0, stream, a, V, rw);
+  const int64_t blocks = (a.M + 15) / 16, cols = (a.N + kCols - 1) / kCols;
+  if (a.M > kRunRows && a.N % 8 == 0) {        // rows of one request are neighbours: few adapters a block
+    const int64_t tiles128 = (a.M + 127) / 128;
+    // enough CTAs for four an SM, and at least 8 column tiles each
+    int64_t span = cols * tiles128 / (4 * device_sm_count());
+    span = std::max<int64_t>(8, std::min<int64_t>(span, 64));
+    const dim3 grid(static_cast<unsigned>((cols + span - 1) / span), static_cast<unsigned>(tiles128));
+    const int sp = static_cast<int>(span);
+    if (a.r <= 32) return launch_pdl(k_lora_expand_run<F16, 1>, grid, 256, 0, stream, a, V, sp);
+    if (a.r <= 64) return launch_pdl(k_lora_expand_run<F16, 2>, grid, 256, 0, stream, a, V, sp);
+    return launch_pdl(k_lora_expand_run<F16, 4>, grid, 256, 0, stream, a, V, sp);
+  }
+  // Subsets of the adapters: while there are few warps for the SMs, up to the adapters a block can
+  // hold.  Row blocks: as many as there are.  8 warps a CTA.
+  int ls = 0, lr = 0;
+  const int most = std::min(std::min(a.M, 16), a.L);
+  while (ls < 3 && a.M <= kRunRows && (1 << ls) < most && (blocks * cols << ls) < 24ll * device_sm_count()) ++ls;
+  while (lr + ls < 3 && (1 << lr) < blocks) ++lr;
+  const int64_t cw = 8 >> (lr + ls);
+  const dim3 grid(static_cast<unsigned>((cols + cw - 1) / cw), static_cast<unsigned>((blocks + (1 << lr) - 1) >> lr));
+  if (a.r <= 32) return launch_pdl(k_lora_expand<F16, 1>, grid, 256, 0, stream, a, V, lr, ls);
+  if (a.r <= 64) return launch_pdl(k_lora_expand<F16, 2>, grid, 256, 0, stream, a, V, lr, ls);
+  return launch_pdl(k_lora_expand<F16, 4>, grid, 256, 0, stream, a, V, lr, ls);
 }
 
 }  // namespace

@@ -533,7 +533,7 @@ wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_str
  *   workspace / ws_bytes: at least wq_lora_workspace_bytes(M, K, N, r) bytes, under the workspace
  *     rules of wq_gemm_workspace_bytes (it starts with the same header).
  * Errors: WQ_ERR_ARG (dtype); WQ_ERR_NULL; WQ_ERR_SHAPE unless M, N, L >= 1, K >= 8, K % 8 == 0,
- *   r % 8 == 0, 8 <= r <= 128, M <= 2^22, N, K, L <= 2^24; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH;
+ *   r % 8 == 0, 8 <= r <= 128, M <= 2^22, N, K, L <= 2^24, L r < 2^31 - 256; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH;
  *   WQ_ERR_CUDA.
  */
 size_t wq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
