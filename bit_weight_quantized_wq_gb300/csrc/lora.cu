@@ -391,228 +391,279 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
   if (n > 1) cluster_sync();                   // the others have read this CTA's sums
 }
 
-// The expand: a warp has 16 rows, 32 output columns and every `subsets`-th adapter of those rows
-// (their rows are its own to write; rows without an adapter are the first warp's).  Output tile t
-// of 8 columns stands for the columns 8 (c / 2) + 2 t + c % 2, c = 0 .. 7, so that a lane's results
-// of four tiles are 8 neighbouring columns: base and Y move 16 bytes a lane.
+// The expand: a warp has 16 rows, 32 output columns at a time, and every `subsets`-th adapter of
+// those rows (their rows are its own to write; rows without an adapter are the first warp's).
+// Output tile t of 8 columns stands for the columns 8 (c / 2) + 2 t + c % 2, c = 0 .. 7, so that a
+// lane's results of four tiles are 8 neighbouring columns: base and Y move 16 bytes a lane.
+//   B (32 columns and 32 ranks a step) and base come through queues in shared memory, each thread
+//   its own place, so that steps ahead are under way without registers: with B one step ahead in
+//   registers a decode batch of 48 adapters ran at 2.5 TB/s.
+//   `span` column tiles a warp: 1 for few rows; many rows keep their set-up over several.
 constexpr int kCols = 32;
+constexpr int kBQueue = 4, kBaseQueue = 4;   // see the waits below
 template <bool F16, int CH>     // CH: chunks of 32 ranks
-__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uint16_t* V, int log_rows, int log_subsets) {
+__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uint16_t* V, int log_rows, int log_subsets, int span) {
+  extern __shared__ __align__(16) uint8_t expand_smem[];
+  uint4* bq = reinterpret_cast<uint4*>(expand_smem) + threadIdx.x;              // [step][4][256]
+  uint4* baseq = bq + kBQueue * 4 * 256;                                        // [tile][2][256]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   // warps of a CTA: row blocks first (they share B through L1), then subsets, then columns
   const int subset = (warp >> log_rows) & ((1 << log_subsets) - 1);
   const int m0 = ((blockIdx.y << log_rows) + (warp & ((1 << log_rows) - 1))) * 16;
-  const int col_warps = (blockDim.x >> 5) >> (log_rows + log_subsets);
-  const int n0 = (blockIdx.x * col_warps + (warp >> (log_rows + log_subsets))) * kCols;
+  const int col_warps = 8 >> (log_rows + log_subsets);
+  const int ct0 = (blockIdx.x * col_warps + (warp >> (log_rows + log_subsets))) * span;
+  const int ct1 = min(ct0 + span, (p.N + kCols - 1) / kCols);
   pdl_launch_dependents();
-  if (m0 >= p.M || n0 >= p.N) return;          // whole warps
+  if (m0 >= p.M || ct0 >= ct1) return;         // whole warps
   const int mine = lane < 16 ? row_adapter(p, m0 + lane) : -1;
-  uint32_t todo = 0;                           // this subset's leading rows
+  const int my_rank = mine >= 0 ? adapter_rank(p, mine) : 0;
+  uint32_t list = 0;                           // this subset's leading rows
   {
     uint32_t lead = leaders(mine);
     for (int i = 0; lead; ++i, lead &= lead - 1)
-      if ((i & ((1 << log_subsets) - 1)) == subset) todo |= lead & (0u - lead);
+      if ((i & ((1 << log_subsets) - 1)) == subset) list |= lead & (0u - lead);
   }
-  // the leading row of each of the two rows this lane holds, and whether they are this warp's
-  const uint32_t same = __match_any_sync(0xffffffffu, mine);
-  const int first = __ffs(same) - 1;
-  const bool own_row = mine >= 0 ? ((todo >> first) & 1u) != 0 : subset == 0;
-  if (!__any_sync(0xffffffffu, lane < 16 && own_row)) return;
-  const uint32_t own_rows = __ballot_sync(0xffffffffu, lane < 16 && own_row);
-  // B of one adapter and chunk of ranks: column of tile t, 8 ranks a lane
-  const auto load_b = [&](uint4 (&b)[4], int a, int rank, int ch) {
-    const int k = 32 * ch + 8 * q;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int n = n0 + 8 * (g >> 1) + 2 * t + (g & 1);
-      b[t] = make_uint4(0, 0, 0, 0);
-      if (k < rank && n < p.N) b[t] = ld_shared_operand(p.B + (static_cast<int64_t>(a) * p.N + n) * p.r + k);
-    }
-  };
-  int a = 0, rank = 0;
-  uint4 b[4];
-  if (todo) {
-    a = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
-    rank = adapter_rank(p, a);
-    load_b(b, a, rank, 0);                     // on its way while the shrink finishes
-  }
-  pdl_wait();
-  const int id[2] = {__shfl_sync(0xffffffffu, mine, g), __shfl_sync(0xffffffffu, mine, g + 8)};
-  const bool own[2] = {((own_rows >> g) & 1u) != 0, ((own_rows >> (g + 8)) & 1u) != 0};
-  uint4 v[CH][2], base[2];
-  const bool vec = p.N % 8 == 0;
-  const int n = n0 + 8 * q;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int m = m0 + 8 * h + g;
-    const int ranks = own[h] && id[h] >= 0 ? adapter_rank(p, id[h]) : 0;
-#pragma unroll
-    for (int ch = 0; ch < CH; ++ch) {
-      v[ch][h] = make_uint4(0, 0, 0, 0);
-      if (32 * ch + 8 * q < ranks)
-        v[ch][h] = __ldcg(reinterpret_cast<const uint4*>(V + static_cast<int64_t>(m) * p.r + 32 * ch + 8 * q));
-    }
-    if (vec && own[h] && m < p.M && n < p.N) base[h] = *reinterpret_cast<const uint4*>(p.base + static_cast<int64_t>(m) * p.N + n);
-  }
-  float acc[4][4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-  while (todo) {
-    todo &= todo - 1;
-    const int next = todo ? __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1) : a;
-    const int next_rank = todo ? adapter_rank(p, next) : 0;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int ch = 0; ch < CH; ++ch) {
-      uint4 nb[4];
-      if (ch + 1 < CH) load_b(nb, a, rank, ch + 1);
-      else load_b(nb, next, next_rank, 0);
-      const uint4 lo = id[0] == a ? v[ch][0] : zero, hi = id[1] == a ? v[ch][1] : zero;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], lo, hi, b[t]);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) b[t] = nb[t];
-    }
-    a = next, rank = next_rank;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int m = m0 + 8 * h + g;
-    if (m >= p.M || !own[h]) continue;
-    const int64_t at = static_cast<int64_t>(m) * p.N + n;
-    if (vec) {
-      if (n >= p.N) continue;
-      uint32_t w[4] = {base[h].x, base[h].y, base[h].z, base[h].w};
-      if (id[h] >= 0) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float2 f = unpack2<F16>(w[t]);
-          w[t] = pack2<F16>(f.x + acc[t][2 * h], f.y + acc[t][2 * h + 1]);
-        }
-      }
-      *reinterpret_cast<uint4*>(p.Y + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int64_t i = at + 2 * t + e;
-          if (n + 2 * t + e >= p.N) continue;
-          p.Y[i] = id[h] >= 0 ? round1<F16>(load1<F16>(p.base + i) + acc[t][2 * h + e]) : p.base[i];
-        }
-    }
-  }
-}
+  const int first = __ffs(__match_any_sync(0xffffffffu, mine)) - 1;
+  const bool own_row = lane < 16 && (mine >= 0 ? ((list >> first) & 1u) != 0 : subset == 0);
+  const uint32_t own_rows = __ballot_sync(0xffffffffu, own_row);
+  if (!own_rows) return;
 
-// The expand of many rows: a warp keeps its 16 rows and walks over `span` column tiles, so that the
-// row set-up is done once and the next tiles' base (a queue of kBaseQueue tiles a thread in shared
-// memory) and B (the next step's, in registers) are under way while a tile is computed.
-constexpr int kBaseQueue = 6;
-template <bool F16, int CH>
-__global__ void __launch_bounds__(256) k_lora_expand_run(const LoraArgs p, const uint16_t* V, int span) {
-  __shared__ uint4 base_queue[kBaseQueue][2][256];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int m0 = (blockIdx.y * 8 + warp) * 16;
-  const int tiles = (p.N + kCols - 1) / kCols;
-  const int lo = blockIdx.x * span, hi = min(lo + span, tiles);
-  pdl_launch_dependents();
-  if (m0 >= p.M) return;                       // whole warps
-  const int mine = lane < 16 ? row_adapter(p, m0 + lane) : -1;
-  const uint32_t lead = leaders(mine);
-  const int id[2] = {__shfl_sync(0xffffffffu, mine, g), __shfl_sync(0xffffffffu, mine, g + 8)};
-  const auto load_b = [&](uint4 (&b)[4], int a, int rank, int ch, int ct) {
-    const int k = 32 * ch + 8 * q, n0 = ct * kCols + 8 * (g >> 1) + (g & 1);
-    const uint16_t* src = p.B + (static_cast<int64_t>(a) * p.N + n0) * p.r + k;
+  // The steps: column tile, leading row, chunk of ranks -- walked twice, by the copies and, kBQueue
+  // steps behind, by the products.
+  struct Step {
+    int ct, ch;
+    uint32_t todo;                             // leading rows from this step's on
+  };
+  const auto next_step = [&](Step& s) {
+    if (++s.ch < CH) return;
+    s.ch = 0;
+    s.todo &= s.todo - 1;
+    if (!s.todo) s.todo = list, ++s.ct;
+  };
+  Step fs{ct0, 0, list};
+  int f_at = 0;
+  const auto fetch_b = [&] {
+    if (fs.ct < ct1 && list) {
+      const int i = __ffs(fs.todo) - 1;
+      const int a = __shfl_sync(0xffffffffu, mine, i), rank = __shfl_sync(0xffffffffu, my_rank, i);
+      const int k = 32 * fs.ch + 8 * q, n = fs.ct * kCols + 8 * (g >> 1) + (g & 1);
+      const uint16_t* src = p.B + (static_cast<int64_t>(a) * p.N + n) * p.r + k;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      b[t] = make_uint4(0, 0, 0, 0);
-      if (k < rank && n0 + 2 * t < p.N) b[t] = ld_shared_operand(src + static_cast<int64_t>(2 * t) * p.r);
+      for (int t = 0; t < 4; ++t) {
+        const bool on = k < rank && n + 2 * t < p.N;
+        copy16(bq + (f_at * 4 + t) * 256, on ? src + static_cast<int64_t>(2 * t) * p.r : p.B, on);
+      }
+      next_step(fs);
+      f_at = f_at + 1 == kBQueue ? 0 : f_at + 1;
     }
   };
+  const bool vec = p.N % 8 == 0;
+  const bool own[2] = {((own_rows >> g) & 1u) != 0, ((own_rows >> (g + 8)) & 1u) != 0};
   const auto fetch_base = [&](int ct, int at) {
     const int n = ct * kCols + 8 * q;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int m = m0 + 8 * h + g;
-      const bool on = ct < hi && m < p.M && n < p.N;
-      copy16(&base_queue[at][h][threadIdx.x], on ? p.base + static_cast<int64_t>(m) * p.N + n : p.base, on);
+      const bool on = vec && own[h] && ct < ct1 && m < p.M && n < p.N;
+      copy16(baseq + (at * 2 + h) * 256, on ? p.base + static_cast<int64_t>(m) * p.N + n : p.base, on);
     }
-    copy_commit();
   };
-  int a0 = 0, rank0 = 0;
-  uint4 b[4];
-  if (lead) {
-    a0 = __shfl_sync(0xffffffffu, mine, __ffs(lead) - 1);
-    rank0 = adapter_rank(p, a0);
-    load_b(b, a0, rank0, 0, lo);
+  // Groups of copies, by number: 0 .. Q - 2 the first steps' B, on its way while the shrink finishes;
+  // Q - 1 the first tiles' bases; Q + s, at step s, the B of step s + Q - 1 and, at a tile's first
+  // step, the base of the tile Q - 1 tiles on.
+#pragma unroll
+  for (int i = 0; i < kBQueue - 1; ++i) {
+    fetch_b();
+    copy_commit();
   }
   pdl_wait();
-  for (int i = 0; i < kBaseQueue - 1; ++i) fetch_base(lo + i, i);
+#pragma unroll
+  for (int i = 0; i < kBaseQueue - 1; ++i) fetch_base(ct0 + i, i);
+  copy_commit();
+  const int id[2] = {__shfl_sync(0xffffffffu, mine, g), __shfl_sync(0xffffffffu, mine, g + 8)};
+  const int ranks[2] = {__shfl_sync(0xffffffffu, my_rank, g), __shfl_sync(0xffffffffu, my_rank, g + 8)};
   uint4 v[CH][2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int ranks = id[h] >= 0 ? adapter_rank(p, id[h]) : 0;
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
       v[ch][h] = make_uint4(0, 0, 0, 0);
-      if (32 * ch + 8 * q < ranks)
+      if (own[h] && 32 * ch + 8 * q < ranks[h])
         v[ch][h] = __ldcg(reinterpret_cast<const uint4*>(V + static_cast<int64_t>(m0 + 8 * h + g) * p.r + 32 * ch + 8 * q));
     }
-  }
-  int at = 0;
+  const int steps = max(1, __popc(list) * CH);   // a tile
+  int b_at = 0, base_at = 0;
 #pragma unroll 1
-  for (int ct = lo; ct < hi; ++ct) {
-    fetch_base(ct + kBaseQueue - 1, at == 0 ? kBaseQueue - 1 : at - 1);
+  for (int ct = ct0; ct < ct1; ++ct) {
+    fetch_base(ct + kBaseQueue - 1, base_at == 0 ? kBaseQueue - 1 : base_at - 1);
     float acc[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-    int a = a0, rank = rank0;
-    uint32_t todo = lead;
-    while (todo) {
-      todo &= todo - 1;
-      // the next adapter of the block, or the first one of the next tile
-      const int next = todo ? __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1) : a0;
-      const int next_rank = todo ? adapter_rank(p, next) : rank0;
-      const int next_ct = todo ? ct : min(ct + 1, hi - 1);
+#pragma unroll 1
+    for (uint32_t todo = list; todo; todo &= todo - 1) {
+      const int a = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
       const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
-        uint4 nb[4];
-        if (ch + 1 < CH) load_b(nb, a, rank, ch + 1, ct);
-        else load_b(nb, next, next_rank, 0, next_ct);
+        fetch_b();
+        copy_commit();
+        copy_wait<kBQueue - 1>();              // groups up to s + 1: the B of step s among them
         const uint4 x0 = id[0] == a ? v[ch][0] : zero, x1 = id[1] == a ? v[ch][1] : zero;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], x0, x1, b[t]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) b[t] = nb[t];
+        for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], x0, x1, bq[(b_at * 4 + t) * 256]);
+        b_at = b_at + 1 == kBQueue ? 0 : b_at + 1;
       }
-      a = next, rank = next_rank;
     }
-    copy_wait<kBaseQueue - 1>();
+    if (!list) {
+      copy_commit();
+      copy_wait<kBQueue - 1>();
+    }
+    // This tile's base: tile i, of T steps a tile, has group Q + (i - Q + 1) T at most, and groups up
+    // to (i + 1) T are here; only the first tiles' group Q - 1 may be later.
+    if ((ct - ct0 + 1) * steps < kBQueue - 1) copy_wait<1>();
     const int n = ct * kCols + 8 * q;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int m = m0 + 8 * h + g;
-      const uint4 y = base_queue[at][h][threadIdx.x];
+      if (m >= p.M || !own[h]) continue;
+      const int64_t at = static_cast<int64_t>(m) * p.N + n;
+      if (vec) {
+        if (n >= p.N) continue;
+        const uint4 y = baseq[(base_at * 2 + h) * 256];
+        uint32_t w[4] = {y.x, y.y, y.z, y.w};
+        if (id[h] >= 0) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const float2 f = unpack2<F16>(w[t]);
+            w[t] = pack2<F16>(f.x + acc[t][2 * h], f.y + acc[t][2 * h + 1]);
+          }
+        }
+        *reinterpret_cast<uint4*>(p.Y + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int64_t i = at + 2 * t + e;
+            if (n + 2 * t + e >= p.N) continue;
+            p.Y[i] = id[h] >= 0 ? round1<F16>(load1<F16>(p.base + i) + acc[t][2 * h + e]) : p.base[i];
+          }
+      }
+    }
+    base_at = base_at + 1 == kBaseQueue ? 0 : base_at + 1;
+  }
+  copy_wait<0>();
+}
+constexpr size_t kExpandSmem = static_cast<size_t>(kBQueue * 4 + kBaseQueue * 2) * 256 * 16;
+
+// The expand of many rows: a warp has 32 rows (so that each B it loads serves two products) and
+// walks over `span` column tiles of 32, the next step's B in registers (from L1: the CTA's 8 warps
+// read the same columns) and the next tiles' base in a queue in shared memory.
+constexpr int kRunQueue = 5;
+template <bool F16, int CH>
+__global__ void __launch_bounds__(256) k_lora_expand_run(const LoraArgs p, const uint16_t* V, int span) {
+  extern __shared__ __align__(16) uint8_t run_smem[];
+  uint4* baseq = reinterpret_cast<uint4*>(run_smem) + threadIdx.x;              // [tile][4][256]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int m0 = (blockIdx.y * 8 + warp) * 32;
+  const int ct0 = blockIdx.x * span, ct1 = min(ct0 + span, p.N / kCols + (p.N % kCols ? 1 : 0));
+  pdl_launch_dependents();
+  if (m0 >= p.M) return;                       // whole warps
+  const int mine = row_adapter(p, m0 + lane);
+  const int my_rank = mine >= 0 ? adapter_rank(p, mine) : 0;
+  const uint32_t list = leaders(mine);
+  int id[4], ranks[4];                         // of rows g, g + 8, g + 16, g + 24
+#pragma unroll
+  for (int i = 0; i < 4; ++i) id[i] = __shfl_sync(0xffffffffu, mine, 8 * i + g), ranks[i] = __shfl_sync(0xffffffffu, my_rank, 8 * i + g);
+  const auto load_b = [&](uint4 (&b)[4], int lead, int ch, int ct) {
+    const int a = __shfl_sync(0xffffffffu, mine, lead), rank = __shfl_sync(0xffffffffu, my_rank, lead);
+    const int k = 32 * ch + 8 * q, n0 = ct * kCols + 8 * (g >> 1) + (g & 1);
+    const uint16_t* src = p.B + (static_cast<int64_t>(a) * p.N + n0) * p.r + k;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      b[t] = make_uint4(0, 0, 0, 0);
+      if (k < rank && n0 + 2 * t < p.N) b[t] = ld_shared_operand(src + 2 * t * p.r);
+    }
+  };
+  const uint16_t* base0 = p.base + static_cast<int64_t>(m0 + g) * p.N + 8 * q;
+  const auto fetch_base = [&](int ct, int at) {
+    const bool in = ct < ct1 && ct * kCols + 8 * q < p.N;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool on = in && m0 + 8 * i + g < p.M;
+      copy16(baseq + (at * 4 + i) * 256, on ? base0 + static_cast<int64_t>(8 * i) * p.N + ct * kCols : p.base, on);
+    }
+    copy_commit();
+  };
+  uint4 b[4];
+  if (list) load_b(b, __ffs(list) - 1, 0, ct0);
+  pdl_wait();
+#pragma unroll
+  for (int i = 0; i < kRunQueue - 1; ++i) fetch_base(ct0 + i, i);
+  uint4 v[CH][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      v[ch][i] = make_uint4(0, 0, 0, 0);
+      if (32 * ch + 8 * q < ranks[i])
+        v[ch][i] = __ldcg(reinterpret_cast<const uint4*>(V + static_cast<int64_t>(m0 + 8 * i + g) * p.r + 32 * ch + 8 * q));
+    }
+  int at = 0;
+#pragma unroll 1
+  for (int ct = ct0; ct < ct1; ++ct) {
+    fetch_base(ct + kRunQueue - 1, at == 0 ? kRunQueue - 1 : at - 1);
+    float acc[2][4][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[h][t][e] = 0.f;
+#pragma unroll 1
+    for (uint32_t todo = list; todo;) {
+      const int lead = __ffs(todo) - 1, a = __shfl_sync(0xffffffffu, mine, lead);
+      todo &= todo - 1;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch) {
+        uint4 nb[4];                           // the next chunk, adapter or tile
+        if (ch + 1 < CH) load_b(nb, lead, ch + 1, ct);
+        else load_b(nb, todo ? __ffs(todo) - 1 : __ffs(list) - 1, 0, todo ? ct : min(ct + 1, ct1 - 1));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x0 = id[2 * h] == a ? v[ch][2 * h] : zero, x1 = id[2 * h + 1] == a ? v[ch][2 * h + 1] : zero;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[h][t], x0, x1, b[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) b[t] = nb[t];
+      }
+    }
+    copy_wait<kRunQueue - 1>();
+    const int n = ct * kCols + 8 * q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + 8 * i + g;
+      const uint4 y = baseq[(at * 4 + i) * 256];
       uint32_t w[4] = {y.x, y.y, y.z, y.w};
-      if (id[h] >= 0) {
+      if (id[i] >= 0) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const float2 f = unpack2<F16>(w[t]);
-          w[t] = pack2<F16>(f.x + acc[t][2 * h], f.y + acc[t][2 * h + 1]);
+          w[t] = pack2<F16>(f.x + acc[i >> 1][t][2 * (i & 1)], f.y + acc[i >> 1][t][2 * (i & 1) + 1]);
         }
       }
       if (m < p.M && n < p.N)
         *reinterpret_cast<uint4*>(p.Y + static_cast<int64_t>(m) * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    at = at + 1 == kBaseQueue ? 0 : at + 1;
+    at = at + 1 == kRunQueue ? 0 : at + 1;
   }
   copy_wait<0>();
 }
+constexpr size_t kRunSmem = static_cast<size_t>(kRunQueue) * 4 * 256 * 16;
 
 // Launch with programmatic serialization, and clusters of `cluster` CTAs along x.
 template <typename... P, typename... A>
@@ -681,28 +732,40 @@ cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
 template <bool F16>
 cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, cudaStream_t stream) {
   const int64_t blocks = (a.M + 15) / 16, cols = (a.N + kCols - 1) / kCols;
-  if (a.M > kRunRows && a.N % 8 == 0) {        // rows of one request are neighbours: few adapters a block
-    const int64_t tiles128 = (a.M + 127) / 128;
-    // enough CTAs for four an SM, and at least 8 column tiles each
-    int64_t span = cols * tiles128 / (4 * device_sm_count());
-    span = std::max<int64_t>(8, std::min<int64_t>(span, 64));
-    const dim3 grid(static_cast<unsigned>((cols + span - 1) / span), static_cast<unsigned>(tiles128));
-    const int sp = static_cast<int>(span);
-    if (a.r <= 32) return launch_pdl(k_lora_expand_run<F16, 1>, grid, 256, 0, stream, a, V, sp);
-    if (a.r <= 64) return launch_pdl(k_lora_expand_run<F16, 2>, grid, 256, 0, stream, a, V, sp);
-    return launch_pdl(k_lora_expand_run<F16, 4>, grid, 256, 0, stream, a, V, sp);
-  }
-  // Subsets of the adapters: while there are few warps for the SMs, up to the adapters a block can
-  // hold.  Row blocks: as many as there are.  8 warps a CTA.
+  const int sms = device_sm_count();
   int ls = 0, lr = 0;
-  const int most = std::min(std::min(a.M, 16), a.L);
-  while (ls < 3 && a.M <= kRunRows && (1 << ls) < most && (blocks * cols << ls) < 24ll * device_sm_count()) ++ls;
+  int64_t span = 1;
+  if (a.M > kRunRows && a.N % 8 == 0) {
+    // rows of one request are neighbours: few adapters a block.  One wave of two CTAs an SM.
+    const int64_t row_ctas = (a.M + 255) / 256, across = std::max<int64_t>(1, 2 * sms / row_ctas);
+    span = std::max<int64_t>(4, (cols + across - 1) / across);
+    const dim3 grid(static_cast<unsigned>((cols + span - 1) / span), static_cast<unsigned>(row_ctas));
+    const auto launch = [&](void (*kern)(LoraArgs, const uint16_t*, int)) {
+      const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), kRunSmem);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(kern, grid, 256, kRunSmem, stream, a, V, static_cast<int>(span));
+    };
+    if (a.r <= 32) return launch(k_lora_expand_run<F16, 1>);
+    if (a.r <= 64) return launch(k_lora_expand_run<F16, 2>);
+    return launch(k_lora_expand_run<F16, 4>);
+  }
+  // Subsets of the adapters, up to those that a block can hold, while there are few warps for the
+  // SMs (many rows: rows of one request are neighbours, no subsets).  Row blocks: as many as there
+  // are.  8 warps a CTA, and column tiles enough for one wave of two CTAs an SM.
+  const int most = a.M > kRunRows ? 1 : std::min(std::min(a.M, 16), a.L);
+  while (ls < 3 && (1 << ls) < most && (blocks * cols << ls) < 24ll * sms) ++ls;
   while (lr + ls < 3 && (1 << lr) < blocks) ++lr;
-  const int64_t cw = 8 >> (lr + ls);
-  const dim3 grid(static_cast<unsigned>((cols + cw - 1) / cw), static_cast<unsigned>((blocks + (1 << lr) - 1) >> lr));
-  if (a.r <= 32) return launch_pdl(k_lora_expand<F16, 1>, grid, 256, 0, stream, a, V, lr, ls);
-  if (a.r <= 64) return launch_pdl(k_lora_expand<F16, 2>, grid, 256, 0, stream, a, V, lr, ls);
-  return launch_pdl(k_lora_expand<F16, 4>, grid, 256, 0, stream, a, V, lr, ls);
+  span = std::min<int64_t>(8, std::max<int64_t>(1, ((blocks * cols << ls) + 16 * sms - 1) / (16 * sms)));
+  const int64_t per = (8 >> (lr + ls)) * span;
+  const dim3 grid(static_cast<unsigned>((cols + per - 1) / per), static_cast<unsigned>((blocks + (1 << lr) - 1) >> lr));
+  const auto launch = [&](void (*kern)(LoraArgs, const uint16_t*, int, int, int)) {
+    const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), kExpandSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, grid, 256, kExpandSmem, stream, a, V, lr, ls, static_cast<int>(span));
+  };
+  if (a.r <= 32) return launch(k_lora_expand<F16, 1>);
+  if (a.r <= 64) return launch(k_lora_expand<F16, 2>);
+  return launch(k_lora_expand<F16, 4>);
 }
 
 }  // namespace
