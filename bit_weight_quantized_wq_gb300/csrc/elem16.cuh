@@ -38,6 +38,53 @@ __device__ __forceinline__ uint16_t round1(float v) {
   else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Pairs of floats in a 64-bit register: two operations an instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair_f(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+// Two packed 16-bit elements as such a pair.
+template <bool F16>
+__device__ __forceinline__ uint64_t unpack_pair(uint32_t v) {
+  if constexpr (F16) {
+    const float2 f = unpack2<true>(v);
+    return pair_f(f.x, f.y);
+  } else {
+    return pair(v << 16, v & 0xffff0000u);
+  }
+}
+
+// 16 bytes global -> this thread's own place in shared memory, zeros where !on; groups complete in
+// order.  Only the thread that copied reads the place, so its own wait is all the ordering needed.
+__device__ __forceinline__ void copy16(void* dst, const uint16_t* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Launch with programmatic stream serialization: the CTAs may start while the previous kernel
 // of the stream drains; the kernel reads and writes global memory only after pdl_wait().
 template <typename... P, typename... A>

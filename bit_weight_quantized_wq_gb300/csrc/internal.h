@@ -150,7 +150,7 @@ struct RopeArgs {
   uint16_t *k_cache, *v_cache;
   const int32_t* slots;
   int64_t pages;
-  int page_size;
+  int page_size, log_page;   // log_page: set by the launch
   int T, Hq, Hkv, d;
 };
 cudaError_t launch_qk_norm_rope(int dtype, const RopeArgs& a, cudaStream_t stream);

@@ -101,15 +101,6 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
   return v;
 }
 
-// 16 bytes global -> this thread's own place in shared memory, zeros where !on; groups complete in
-// order.  Only the thread that copied reads the place, so its own wait is all the ordering needed.
-__device__ __forceinline__ void copy16(void* dst, const uint16_t* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // Steps of 32 of the contracted index that slice i of n takes.
 __device__ __forceinline__ void slice(int steps, int i, int n, int& lo, int& hi) {
   lo = static_cast<int>(static_cast<int64_t>(steps) * i / n);

@@ -6,11 +6,11 @@
 //   pair (a, b) of the first `rot` elements -> (a c - b s, b c + a s), c and s from the row of
 //   the table at the token's position; the rest of the head unrotated.
 //
-// Bandwidth-bound: every element is read once and written once.  A thread holds 8 consecutive
-// elements (one 16-byte access) and d / 8 neighbouring lanes hold a head, so the sum of squares
-// and the partner of a half-split pair come by shuffles.  A thread keeps its place in the head
-// and walks over heads of one token, so that its cos / sin values (64 bytes a thread, four times
-// its data) are loaded once per token and not once per head.
+// Bandwidth-bound: every element is read once and written once.  A thread holds two 16-byte pieces
+// of a head, chosen so that both elements of each pair are its own (half-split pairs: pieces j and
+// j + rot/16; adjacent pairs: any, j and j + d/16), and d / 16 neighbouring lanes hold a head, so
+// only the sum of squares takes shuffles.  With one piece a thread and the partners by shuffles the
+// instructions, not the bytes, set the time.
 #include "elem16.cuh"
 #include "internal.h"
 
@@ -29,152 +29,237 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 
-// D: head elements.  HPT: heads a thread takes (all of one token).
-template <bool F16, int D, int HPT>
-__global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a) {
-  constexpr int TPH = D / 8;                     // threads per head
-  constexpr int HPB = kRopeThreads / TPH;        // heads per pass of a block
-  pdl_launch_dependents();
-  pdl_wait();
-  const int t = blockIdx.x;
-  const int c = threadIdx.x % TPH;               // this thread's 8 elements: 8c .. 8c + 7
-  const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv;   // Q heads, K heads, then V heads
-  const int row0 = blockIdx.y * (HPB * HPT) + threadIdx.x / TPH;
+// Source of element 8 c of a row (query heads, key heads, then value heads) of token t.
+template <int D>
+__device__ __forceinline__ const uint16_t* row_source(const RopeArgs& a, int64_t t, int row) {
+  if (row < a.Hq) return a.Q + t * a.q_stride + static_cast<int64_t>(row) * D;
+  if (row < a.Hq + a.Hkv) return a.K + t * a.k_stride + static_cast<int64_t>(row - a.Hq) * D;
+  return a.V + t * a.v_stride + static_cast<int64_t>(row - a.Hq - a.Hkv) * D;
+}
 
-  int slot = 0;
-  if (a.slots) {
-    slot = __ldg(a.slots + t);
-    if (static_cast<int64_t>(slot) >= a.pages * a.page_size) {
-      if (threadIdx.x == 0) atomicOr(&g_rope_err, kErrIndex);
-      slot = -1;
-    }
-  }
-  uint4 x[HPT];
-#pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    const int row = row0 + i * HPB;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const uint16_t* src;
-      if (row < a.Hq) src = a.Q + t * a.q_stride + static_cast<int64_t>(row) * D;
-      else if (row < a.Hq + a.Hkv) src = a.K + t * a.k_stride + static_cast<int64_t>(row - a.Hq) * D;
-      else src = a.V + t * a.v_stride + static_cast<int64_t>(row - a.Hq - a.Hkv) * D;
-      x[i] = *reinterpret_cast<const uint4*>(src + 8 * c);
-    }
-  }
+// Position of token t, forced into the table; slot, or -1 where nothing is written.
+__device__ __forceinline__ int token_position(const RopeArgs& a, int64_t t) {
   int pos = __ldg(a.positions + t);
   if (static_cast<uint32_t>(pos) >= static_cast<uint32_t>(a.max_pos)) {
-    if (threadIdx.x == 0) atomicOr(&g_rope_err, kErrIndex);
+    atomicOr(&g_rope_err, kErrIndex);
     pos = min(max(pos, 0), a.max_pos - 1);
   }
-  // cos / sin of this thread's elements.  Half-split pairs (i, i + rot/2): element e uses index
-  // e mod rot/2.  Adjacent pairs (2i, 2i + 1): element e uses index e / 2.
-  const int half = a.rot >> 1;
-  const bool turned = 8 * c < a.rot;             // rot is a multiple of 16
-  float cs[8], sn[8];
-  if (turned) {
-    const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.rot;
-    if (a.interleaved) {
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
-      const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
-      const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        cs[2 * e] = cs[2 * e + 1] = cc[e];
-        sn[2 * e] = sn[2 * e + 1] = ss[e];
-      }
-    } else {
-      const int i0 = 8 * c < half ? 8 * c : 8 * c - half;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i0) + q);
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + i0) + q);
-        cs[4 * q] = cv.x, cs[4 * q + 1] = cv.y, cs[4 * q + 2] = cv.z, cs[4 * q + 3] = cv.w;
-        sn[4 * q] = sv.x, sn[4 * q + 1] = sv.y, sn[4 * q + 2] = sv.z, sn[4 * q + 3] = sv.w;
-      }
-      if (8 * c < half) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sn[e] = -sn[e];   // first of the pair: a c - b s
-      }
-    }
+  return pos;
+}
+__device__ __forceinline__ int token_slot(const RopeArgs& a, int64_t t) {
+  if (!a.slots) return 0;
+  const int slot = __ldg(a.slots + t);
+  if (static_cast<int64_t>(slot) >= a.pages * a.page_size) {
+    atomicOr(&g_rope_err, kErrIndex);
+    return -1;
   }
-  // lane holding the other half of a half-split pair (rot/2 is a multiple of 8)
-  const int lane = threadIdx.x & 31;
-  const int mate = a.interleaved || !turned ? lane : (8 * c < half ? lane + half / 8 : lane - half / 8);
+  return slot;
+}
 
+// A thread's pieces of a head (in units of 8 elements), and whether they are turned.  Neighbouring
+// threads have neighbouring pieces.
+struct Pieces {
+  int a, b;
+  bool turn_a, turn_b;
+};
+template <int D>
+__device__ __forceinline__ Pieces pieces(const RopeArgs& p, int j) {
+  const int n = p.rot >> 4;                    // threads with half-split pairs
+  if (p.interleaved) return {j, j + D / 16, 8 * j < p.rot, 8 * j + D / 2 < p.rot};
+  if (j < n) return {j, j + n, true, true};
+  return {j + n, j + D / 16, false, false};    // past rot: the first half of the rest, and the second
+}
+
+// cos / sin of a thread's 8 pairs.
+struct Turn {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void load_turn(Turn& u, const RopeArgs& a, int pos, const Pieces& pc) {
+  const float* row = a.cos_sin + static_cast<int64_t>(pos) * a.rot;
 #pragma unroll
-  for (int i = 0; i < HPT; ++i) {
-    const int row = row0 + i * HPB;
-    const bool is_q = row < a.Hq, is_v = row >= a.Hq + a.Hkv;
-    float f[8];
-    {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 v = unpack2<F16>(w[q]);
-        f[2 * q] = v.x;
-        f[2 * q + 1] = v.y;
-      }
-    }
-    const uint16_t* weight = is_q ? a.q_weight : a.k_weight;
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(f[e], f[e], sum);
-#pragma unroll
-    for (int o = TPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (weight && row < rows && !is_v) {
-      const float inv = rsqrtf(sum * (1.f / D) + a.eps);
-      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(weight + 8 * c));
-      const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 v = unpack2<F16>(w[q]);
-        f[2 * q] *= inv * v.x;
-        f[2 * q + 1] *= inv * v.y;
-      }
-    }
-    float g[8];
-    if (a.interleaved) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        g[2 * e] = -f[2 * e + 1];
-        g[2 * e + 1] = f[2 * e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = __shfl_sync(0xffffffffu, f[e], mate);
-    }
-    if (turned && !is_v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = fmaf(g[e], sn[e], f[e] * cs[e]);
-    }
-    if (row >= rows) continue;
-    const uint4 y = is_v ? x[i] : make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]),
-                                              pack2<F16>(f[6], f[7]));
-    uint16_t* dst;
-    if (is_q) {
-      dst = a.Qo + (static_cast<int64_t>(t) * a.Hq + row) * D;
-    } else {
-      const int h = is_v ? row - a.Hq - a.Hkv : row - a.Hq;
-      if (a.slots) {
-        if (slot < 0) continue;
-        const int page = slot / a.page_size, at = slot % a.page_size;
-        dst = (is_v ? a.v_cache : a.k_cache) + ((static_cast<int64_t>(page) * a.Hkv + h) * a.page_size + at) * D;
-      } else {
-        dst = a.Ko + (static_cast<int64_t>(t) * a.Hkv + h) * D;
-      }
-    }
-    *reinterpret_cast<uint4*>(dst + 8 * c) = y;
+  for (int q = 0; q < 2; ++q) {
+    if (!(q ? pc.turn_b : pc.turn_a)) continue;
+    const int i = a.interleaved ? 4 * (q ? pc.b : pc.a) : 8 * pc.a + 4 * q;
+    const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i));
+    const float4 sv = __ldg(reinterpret_cast<const float4*>(row + (a.rot >> 1) + i));
+    u.c[4 * q] = cv.x, u.c[4 * q + 1] = cv.y, u.c[4 * q + 2] = cv.z, u.c[4 * q + 3] = cv.w;
+    u.s[4 * q] = sv.x, u.s[4 * q + 1] = sv.y, u.s[4 * q + 2] = sv.z, u.s[4 * q + 3] = sv.w;
   }
+}
+
+template <bool F16>
+__device__ __forceinline__ void unpack_piece(uint64_t (&f)[4], const uint4& x) {
+  f[0] = unpack_pair<F16>(x.x), f[1] = unpack_pair<F16>(x.y), f[2] = unpack_pair<F16>(x.z), f[3] = unpack_pair<F16>(x.w);
+}
+template <bool F16>
+__device__ __forceinline__ uint4 pack_piece(const uint64_t (&f)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float2 v = unpair(f[q]);
+    w[q] = pack2<F16>(v.x, v.y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Two pieces of a head: norm, rotation, rounding.  All lanes of the warp take part.
+template <bool F16, int D>
+__device__ __forceinline__ void turn_pieces(const RopeArgs& a, uint4& xa, uint4& xb, const Turn& u, const uint16_t* weight,
+                                            const Pieces& pc, bool is_v) {
+  uint64_t fa[4], fb[4];
+  unpack_piece<F16>(fa, xa);
+  unpack_piece<F16>(fb, xb);
+  if (a.q_weight || a.k_weight) {              // the same for the whole grid
+    uint64_t sq = mul_pair(fa[0], fa[0]), sq2 = mul_pair(fb[0], fb[0]);
+#pragma unroll
+    for (int q = 1; q < 4; ++q) sq = fma_pair(fa[q], fa[q], sq), sq2 = fma_pair(fb[q], fb[q], sq2);
+    const float2 s2 = unpair(add_pair(sq, sq2));
+    float sum = s2.x + s2.y;
+#pragma unroll
+    for (int o = D / 32; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (weight && !is_v) {
+      const float inv = rsqrtf(sum * (1.f / D) + a.eps);
+      const uint64_t i2 = pair_f(inv, inv);
+      uint64_t wa[4], wb[4];
+      unpack_piece<F16>(wa, __ldg(reinterpret_cast<const uint4*>(weight) + pc.a));
+      unpack_piece<F16>(wb, __ldg(reinterpret_cast<const uint4*>(weight) + pc.b));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        fa[q] = mul_pair(fa[q], mul_pair(wa[q], i2));
+        fb[q] = mul_pair(fb[q], mul_pair(wb[q], i2));
+      }
+    }
+  }
+  if (is_v) return;
+  if (a.interleaved) {
+    if (pc.turn_a) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 x = unpair(fa[q]);
+        fa[q] = pair_f(fmaf(-x.y, u.s[q], x.x * u.c[q]), fmaf(x.x, u.s[q], x.y * u.c[q]));
+      }
+    }
+    if (pc.turn_b) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 x = unpair(fb[q]);
+        fb[q] = pair_f(fmaf(-x.y, u.s[4 + q], x.x * u.c[4 + q]), fmaf(x.x, u.s[4 + q], x.y * u.c[4 + q]));
+      }
+    }
+  } else if (pc.turn_a) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t c = pair_f(u.c[2 * q], u.c[2 * q + 1]), s = pair_f(u.s[2 * q], u.s[2 * q + 1]);
+      const uint64_t n = pair_f(-u.s[2 * q], -u.s[2 * q + 1]), x = fa[q];
+      fa[q] = fma_pair(fb[q], n, mul_pair(x, c));
+      fb[q] = fma_pair(x, s, mul_pair(fb[q], c));
+    }
+  }
+  xa = pack_piece<F16>(fa);
+  xb = pack_piece<F16>(fb);
+}
+
+// Where a row goes; null where it is not written.
+template <int D>
+__device__ __forceinline__ uint16_t* row_target(const RopeArgs& a, int64_t t, int row, int slot) {
+  if (row < a.Hq) return a.Qo + (t * a.Hq + row) * D;
+  const bool is_v = row >= a.Hq + a.Hkv;
+  const int h = is_v ? row - a.Hq - a.Hkv : row - a.Hq;
+  if (!a.slots) return a.Ko + (t * a.Hkv + h) * D;
+  if (slot < 0) return nullptr;
+  const int64_t page = slot >> a.log_page;
+  const int at = slot & (a.page_size - 1);
+  return (is_v ? a.v_cache : a.k_cache) + (((page * a.Hkv + h) << a.log_page) + at) * D;
+}
+
+// Few tokens: one head a thread, nothing kept; the call is over in one round of loads.
+template <bool F16, int D>
+__global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a) {
+  constexpr int TPH = D / 16;                  // threads per head
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t = blockIdx.x, j = threadIdx.x % TPH;
+  const Pieces pc = pieces<D>(a, j);
+  const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv, row = blockIdx.y * (kRopeThreads / TPH) + threadIdx.x / TPH;
+  uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+  if (row < rows) {
+    const uint4* src = reinterpret_cast<const uint4*>(row_source<D>(a, t, row));
+    xa = src[pc.a], xb = src[pc.b];
+  }
+  const int slot = token_slot(a, t), pos = token_position(a, t);
+  Turn u;
+  load_turn(u, a, pos, pc);
+  turn_pieces<F16, D>(a, xa, xb, u, row < a.Hq ? a.q_weight : a.k_weight, pc, row >= a.Hq + a.Hkv);
+  uint4* dst = row < rows ? reinterpret_cast<uint4*>(row_target<D>(a, t, row, slot)) : nullptr;
+  if (dst) dst[pc.a] = xa, dst[pc.b] = xb;
+}
+
+// Many tokens: a grid that fills the SMs once walks over tokens, a pass of heads at a time; the rows
+// of the next passes come through a queue in shared memory (each thread its own places: no barrier),
+// the next token's cos / sin are in registers.  With a block for each token's share, 8 blocks an SM
+// waited for two dependent rounds of loads each: 3.9 TB/s at 8192 tokens of 80 heads.
+constexpr int kWalkThreads = 128, kWalkQueue = 8, kWalkCtas = 6;     // CTAs an SM
+template <bool F16, int D>
+__global__ void __launch_bounds__(kWalkThreads, kWalkCtas) k_qk_norm_rope_walk(const RopeArgs a, int passes) {
+  constexpr int TPH = D / 16, HPB = kWalkThreads / TPH;
+  __shared__ uint4 queue[kWalkQueue][2][kWalkThreads];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int j = threadIdx.x % TPH, r0 = threadIdx.x / TPH, step = gridDim.x;
+  const Pieces pc = pieces<D>(a, j);
+  const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv;
+  int ft = blockIdx.x, fpass = 0, f_at = 0;    // the next pass to fetch
+  const auto fetch = [&] {
+    if (ft < a.T) {
+      const int row = fpass * HPB + r0;
+      const bool on = row < rows;
+      const uint16_t* src = on ? row_source<D>(a, ft, row) : a.Q;
+      copy16(&queue[f_at][0][threadIdx.x], on ? src + 8 * pc.a : src, on);
+      copy16(&queue[f_at][1][threadIdx.x], on ? src + 8 * pc.b : src, on);
+      if (++fpass == passes) fpass = 0, ft += step;
+      f_at = (f_at + 1) % kWalkQueue;
+    }
+    copy_commit();
+  };
+  int t = blockIdx.x;
+#pragma unroll
+  for (int i = 0; i < kWalkQueue - 1; ++i) fetch();
+  Turn now, next;
+  int slot = token_slot(a, t);
+  load_turn(now, a, token_position(a, t), pc);
+  int pos_next = t + step < a.T ? token_position(a, t + step) : 0;
+  int at = 0;
+#pragma unroll 1
+  for (; t < a.T; t += step) {
+    int slot_next = 0;
+    if (t + step < a.T) {
+      load_turn(next, a, pos_next, pc);
+      slot_next = token_slot(a, t + step);
+      if (t + 2ll * step < a.T) pos_next = token_position(a, t + 2ll * step);
+    }
+#pragma unroll 1
+    for (int row = r0, pass = 0; pass < passes; ++pass, row += HPB) {
+      fetch();
+      copy_wait<kWalkQueue - 1>();
+      uint4 xa = queue[at][0][threadIdx.x], xb = queue[at][1][threadIdx.x];
+      turn_pieces<F16, D>(a, xa, xb, now, row < a.Hq ? a.q_weight : a.k_weight, pc, row >= a.Hq + a.Hkv);
+      uint4* dst = row < rows ? reinterpret_cast<uint4*>(row_target<D>(a, t, row, slot)) : nullptr;
+      if (dst) dst[pc.a] = xa, dst[pc.b] = xb;
+      at = (at + 1) % kWalkQueue;
+    }
+    now = next, slot = slot_next;
+  }
+  copy_wait<0>();
 }
 
 template <bool F16, int D>
 cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t stream) {
-  constexpr int HPB = kRopeThreads / (D / 8);
-  const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv;
-  const auto grid = [&](int hpt) { return dim3(a.T, (rows + HPB * hpt - 1) / (HPB * hpt)); };
-  if (a.T < 512) return launch_pdl(k_qk_norm_rope<F16, D, 1>, grid(1), kRopeThreads, 0, stream, a);
-  return launch_pdl(k_qk_norm_rope<F16, D, 4>, grid(4), kRopeThreads, 0, stream, a);
+  constexpr int TPH = D / 16, HPB = kRopeThreads / TPH;
+  static_assert(kRopeThreads == kWalkThreads, "both take the same heads a pass");
+  const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv, passes = (rows + HPB - 1) / HPB;
+  const int fill = kWalkCtas * device_sm_count();
+  if (a.T < fill) return launch_pdl(k_qk_norm_rope<F16, D>, dim3(a.T, passes), kRopeThreads, 0, stream, a);
+  return launch_pdl(k_qk_norm_rope_walk<F16, D>, dim3(fill), kWalkThreads, 0, stream, a, passes);
 }
 
 template <bool F16>
@@ -186,7 +271,10 @@ cudaError_t launch_rope_d(const RopeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_qk_norm_rope(int dtype, const RopeArgs& a, cudaStream_t stream) {
+cudaError_t launch_qk_norm_rope(int dtype, const RopeArgs& args, cudaStream_t stream) {
+  RopeArgs a = args;
+  a.log_page = 0;
+  while (a.slots && (1 << a.log_page) < a.page_size) ++a.log_page;
   return dtype == kF16 ? launch_rope_d<true>(a, stream) : launch_rope_d<false>(a, stream);
 }
 
