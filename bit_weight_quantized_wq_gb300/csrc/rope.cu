@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a)
   if (dst) dst[pc.a] = xa, dst[pc.b] = xb;
 }
 
-// Many tokens: a grid that fills the SMs once walks over tokens, a pass of heads at a time; the rows
-// of the next passes come through a queue in shared memory (each thread its own places: no barrier),
+// Many tokens: a grid that fills the SMs once divides the (token, pass of heads) units evenly; the rows
+// of the next units come through a queue in shared memory (each thread its own places: no barrier),
 // the next token's cos / sin are in registers.  With a block for each token's share, 8 blocks an SM
 // waited for two dependent rounds of loads each: 3.9 TB/s at 8192 tokens of 80 heads.
 constexpr int kWalkThreads = 128, kWalkQueue = 8, kWalkCtas = 6;     // CTAs an SM
@@ -205,40 +205,46 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) k_qk_norm_rope_walk(c
   __shared__ uint4 queue[kWalkQueue][2][kWalkThreads];
   pdl_launch_dependents();
   pdl_wait();
-  const int j = threadIdx.x % TPH, r0 = threadIdx.x / TPH, step = gridDim.x;
+  const int j = threadIdx.x % TPH, r0 = threadIdx.x / TPH;
   const Pieces pc = pieces<D>(a, j);
   const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv;
-  int ft = blockIdx.x, fpass = 0, f_at = 0;    // the next pass to fetch
+  // this CTA's share of all (token, pass) units
+  const int64_t units = static_cast<int64_t>(a.T) * passes;
+  const int64_t lo = units * blockIdx.x / gridDim.x;
+  int left = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - lo);
+  int t = static_cast<int>(lo / passes), pass = static_cast<int>(lo - static_cast<int64_t>(t) * passes);
+  int ft = t, fpass = pass, fleft = left, f_at = 0;      // the next unit to fetch
   const auto fetch = [&] {
-    if (ft < a.T) {
+    if (fleft > 0) {
       const int row = fpass * HPB + r0;
       const bool on = row < rows;
       const uint16_t* src = on ? row_source<D>(a, ft, row) : a.Q;
       copy16(&queue[f_at][0][threadIdx.x], on ? src + 8 * pc.a : src, on);
       copy16(&queue[f_at][1][threadIdx.x], on ? src + 8 * pc.b : src, on);
-      if (++fpass == passes) fpass = 0, ft += step;
+      --fleft;
+      if (++fpass == passes) fpass = 0, ++ft;
       f_at = (f_at + 1) % kWalkQueue;
     }
     copy_commit();
   };
-  int t = blockIdx.x;
 #pragma unroll
   for (int i = 0; i < kWalkQueue - 1; ++i) fetch();
   Turn now, next;
   int slot = token_slot(a, t);
   load_turn(now, a, token_position(a, t), pc);
-  int pos_next = t + step < a.T ? token_position(a, t + step) : 0;
+  int pos_next = t + 1 < a.T ? token_position(a, t + 1) : 0;
   int at = 0;
 #pragma unroll 1
-  for (; t < a.T; t += step) {
+  for (; left > 0; ++t, pass = 0) {
     int slot_next = 0;
-    if (t + step < a.T) {
+    if (t + 1 < a.T) {
       load_turn(next, a, pos_next, pc);
-      slot_next = token_slot(a, t + step);
-      if (t + 2ll * step < a.T) pos_next = token_position(a, t + 2ll * step);
+      slot_next = token_slot(a, t + 1);
+      if (t + 2 < a.T) pos_next = token_position(a, t + 2);
     }
 #pragma unroll 1
-    for (int row = r0, pass = 0; pass < passes; ++pass, row += HPB) {
+    for (; pass < passes && left > 0; ++pass, --left) {
+      const int row = pass * HPB + r0;
       fetch();
       copy_wait<kWalkQueue - 1>();
       uint4 xa = queue[at][0][threadIdx.x], xb = queue[at][1][threadIdx.x];
@@ -258,7 +264,8 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t stream) {
   static_assert(kRopeThreads == kWalkThreads, "both take the same heads a pass");
   const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv, passes = (rows + HPB - 1) / HPB;
   const int fill = kWalkCtas * device_sm_count();
-  if (a.T < fill) return launch_pdl(k_qk_norm_rope<F16, D>, dim3(a.T, passes), kRopeThreads, 0, stream, a);
+  // from about eight units a CTA on the walk's set-up pays
+  if (static_cast<int64_t>(a.T) * passes < 4ll * fill) return launch_pdl(k_qk_norm_rope<F16, D>, dim3(a.T, passes), kRopeThreads, 0, stream, a);
   return launch_pdl(k_qk_norm_rope_walk<F16, D>, dim3(fill), kWalkThreads, 0, stream, a, passes);
 }
 
