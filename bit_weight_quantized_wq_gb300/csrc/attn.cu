@@ -62,9 +62,9 @@ constexpr int kRegsSoftmax = 168, kRegsOther = 88;
 constexpr int kItems = 4;             // items the scheduler is ahead of the other warps
 constexpr int kTmemCols = 512;        // two S of 64 columns a lane, then O of 128 a lane
 constexpr int kColO = 256;
-// Weights on the line: a key tile in either mode, and an item's own cost (about 1840, 1300 and
-// 3500 SM cycles, measured on long and on short items).
-constexpr int kWRows = 6, kWKeys = 4, kWItem = 11;
+// Weights on the line, in units of about 200 SM cycles: a key tile in rows mode, in keys mode with
+// more than 32 rows (all softmax warps at work) and with up to 32; an item's own cost, alike.
+constexpr int kWRows = 10, kWKeys = 8, kWFew = 5, kWItemRows = 20, kWItem = 16;
 constexpr long long kMaxLine = 1ll << 30;
 constexpr float kLazy = 8.f;          // rescale when the maximum grew by more than 2^8
 
@@ -93,7 +93,7 @@ struct Smem {
   uint64_t pv_done[2], o_full[2], o_empty[2], drain[2];
   uint64_t item_full[kItems], item_empty[kItems];
   Item items[kItems];
-  long long scan[kWarps];
+  long long scan[kWarps], scan_rest[kWarps];
   int scan_items[kWarps];
   int r0, r0_line, r0_item;
   uint32_t tmem_base;
@@ -117,8 +117,12 @@ struct Params {
   int ctas;
   TokenRecord* token;        // [T]
   int* share;                // line units a CTA; 0: nothing to join
-  float *po_p, *ml_p;        // prefix partials: [segment][lane][128][D], [segment][lane][128][2]
-  float *po_s, *ml_s;        // suffix partials, with q_rows_suffix rows
+  // Prefix partials: [segment][lane][128 / 8][D / 4][8][4] and [segment][lane][128][2]; suffix
+  // partials with q_rows_suffix (a multiple of 8) for 128.  Rows go in eights, four columns at a
+  // time, so that a warp with a row a thread writes whole 128-byte lines, and so does one that
+  // reads eight rows.
+  float *po_p, *ml_p;
+  float *po_s, *ml_s;
 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -128,11 +132,9 @@ struct Request {
   int first, n, len;
   bool bad_n, bad_len;
 };
-__device__ __forceinline__ Request request(const AttnArgs& a, int r) {
+__device__ __forceinline__ Request checked(const AttnArgs& a, int r, int first, int end, int len) {
   Request q;
-  q.first = a.q_start ? __ldg(a.q_start + r) : r;
-  const int end = a.q_start ? __ldg(a.q_start + r + 1) : r + 1;
-  q.len = a.max_blocks ? __ldg(a.suffix_lens + r) : 0;
+  q.first = first, q.len = len;
   q.n = end - q.first;
   // requests cover the tokens from 0 to T without gaps
   q.bad_n = q.first < 0 || end < q.first || end > a.T || q.n > a.max_new || (r == 0 && q.first != 0) ||
@@ -143,26 +145,36 @@ __device__ __forceinline__ Request request(const AttnArgs& a, int r) {
   q.len = min(max(q.len, 0), cap);
   return q;
 }
+__device__ __forceinline__ Request request(const AttnArgs& a, int r) {
+  return checked(a, r, a.q_start ? __ldg(a.q_start + r) : r, a.q_start ? __ldg(a.q_start + r + 1) : r + 1,
+                 a.max_blocks ? __ldg(a.suffix_lens + r) : 0);
+}
 
 // Items of ntok tokens: row tiles, and the tokens of tile rt.
 __device__ __forceinline__ int row_tiles(const Params& p, int ntok) {
   return ntok <= 2 * p.tb ? (ntok > 0 ? 1 : 0) : ceil_div(ntok, 2 * p.tb);
 }
 __device__ __forceinline__ int tile_tokens(const Params& p, int ntok, int rt) { return min(2 * p.tb, ntok - rt * 2 * p.tb); }
-__device__ __forceinline__ int weight(const Params& p, int tokens) { return tokens > p.tb ? kWRows : kWKeys; }
+__device__ __forceinline__ int tile_weight(const Params& p, int tokens) {
+  return tokens > p.tb ? kWRows : (tokens * p.G > 32 ? kWKeys : kWFew);
+}
+__device__ __forceinline__ int item_weight(const Params& p, int tokens) { return tokens > p.tb ? kWItemRows : kWItem; }
+// Line length of an item in rows mode.
+__device__ __forceinline__ int full_cost(int tiles) { return tiles * kWRows + kWItemRows; }
 // Line length of all row tiles of one head (T is int or, where it may be too long, long long).
 template <typename L>
 __device__ __forceinline__ L head_cost(const Params& p, int ntok, int tiles) {
   const int rts = row_tiles(p, ntok);
   if (rts == 0 || tiles == 0) return 0;
-  return static_cast<L>(rts - 1) * (static_cast<L>(tiles) * kWRows + kWItem) +
-         static_cast<L>(tiles) * weight(p, tile_tokens(p, ntok, rts - 1)) + kWItem;
+  const int last = tile_tokens(p, ntok, rts - 1);
+  return static_cast<L>(rts - 1) * (static_cast<L>(tiles) * kWRows + kWItemRows) +
+         static_cast<L>(tiles) * tile_weight(p, last) + item_weight(p, last);
 }
 // First tile of an item (line start s, tiles n of weight w) that starts at or after position b.
 // Tile t therefore belongs to the CTA whose share holds position s + t w.
 __device__ __forceinline__ int tile_at(int b, int s, int n, int w) {
   const uint32_t x = static_cast<uint32_t>(b - s + w - 1);
-  return b <= s ? 0 : min(n, static_cast<int>(w == kWRows ? x / kWRows : x / kWKeys));
+  return b <= s ? 0 : min(n, static_cast<int>(w == kWRows ? x / kWRows : (w == kWKeys ? x / kWKeys : x / kWFew)));
 }
 
 // Walks over the items of one CTA's share (the scheduler warp).
@@ -172,7 +184,8 @@ struct Walk {
   int h, t, pline, pitem; // next prefix item and its line position
   int r, kvh, rt, item;   // next suffix item
   int line;               // its line position
-  Request q, nq;          // request r and, read ahead, r + 1
+  Request q;              // request r
+  int raw[3];             // of request r + 1, read ahead: where it ends, the next one's end, own keys
 
   __device__ Walk(const Params& p_, int share, int prefix_cost, int r0, int r0_line, int r0_item)
       : p(p_), cta(blockIdx.x) {
@@ -187,21 +200,29 @@ struct Walk {
     }
     r = r0, line = r0_line, item = r0_item, kvh = 0, rt = 0;
     if (r < p.a.R) q = request(p.a, r);
-    if (r + 1 < p.a.R) nq = request(p.a, r + 1);
+    read_ahead();
+  }
+
+  __device__ void read_ahead() {
+    if (r + 1 < p.a.R) {
+      raw[0] = p.a.q_start ? __ldg(p.a.q_start + r + 1) : r + 1;
+      raw[1] = p.a.q_start ? __ldg(p.a.q_start + r + 2) : r + 2;
+      raw[2] = p.a.max_blocks ? __ldg(p.a.suffix_lens + r + 1) : 0;
+    }
   }
 
   __device__ bool next(Item& it) {
     while (h < p.a.Hkv) {
       if (pline >= b1) return false;
       it.ntok = tile_tokens(p, p.a.T, t);
-      const int w = weight(p, it.ntok);
+      const int w = tile_weight(p, it.ntok);
       it.kvh = h, it.r = -1;
       it.lo = tile_at(b0, pline, p.prefix_tiles, w), it.hi = tile_at(b1, pline, p.prefix_tiles, w);
       it.len = p.a.prefix_len;
       it.tok0 = t * 2 * p.tb;
       it.lim0 = p.a.prefix_len;
       it.seg = cta + pitem;
-      pline += p.prefix_tiles * w + kWItem;
+      pline += p.prefix_tiles * w + item_weight(p, it.ntok);
       ++pitem;
       if (it.tok0 + 2 * p.tb >= p.a.T) t = 0, ++h;
       else ++t;
@@ -211,20 +232,20 @@ struct Walk {
       const int tiles = ceil_div(q.len, kTile), rts = row_tiles(p, q.n);
       if (tiles == 0 || rts == 0 || kvh == p.a.Hkv) {
         ++r, kvh = 0, rt = 0;
-        q = nq;
-        if (r + 1 < p.a.R) nq = request(p.a, r + 1);
+        if (r < p.a.R) q = checked(p.a, r, raw[0], raw[1], raw[2]);
+        read_ahead();
         continue;
       }
       if (line >= b1) return false;
       it.ntok = tile_tokens(p, q.n, rt);
-      const int w = weight(p, it.ntok);
+      const int w = tile_weight(p, it.ntok);
       it.kvh = kvh, it.r = r;
       it.lo = tile_at(b0, line, tiles, w), it.hi = tile_at(b1, line, tiles, w);
       it.len = q.len;
       it.tok0 = q.first + rt * 2 * p.tb;
       it.lim0 = q.len - q.n + rt * 2 * p.tb + 1;
       it.seg = cta + item;
-      line += tiles * w + kWItem;
+      line += tiles * w + item_weight(p, it.ntok);
       ++item;
       if (++rt == rts) rt = 0, ++kvh;
       if (it.lo < it.hi) return true;
@@ -289,26 +310,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
 
   // ---------------------------------------------------------------- the line: its length, and
-  // the request in which this CTA's share begins
+  // the request in which this CTA's share begins.  A thread has a request; more requests than
+  // threads go in further rounds, their total first.
   const long long prefix_long = static_cast<long long>(p.a.Hkv) * p.p_head;
-  long long mine = 0;
+  Request q0{0, 0, 0, false, false};
   bool bad = false;
-  Request q0;                             // request threadIdx.x, kept for the scan
+  long long c0 = 0, rest = 0;
+  int n0 = 0;
   for (int r = threadIdx.x; r < p.a.R; r += kThreads) {
     const Request q = request(p.a, r);
-    if (r == threadIdx.x) q0 = q;
+    const int tiles = ceil_div(q.len, kTile);
+    const long long c = p.a.Hkv * head_cost<long long>(p, q.n, tiles);
     bad |= q.bad_n;
     if (blockIdx.x == 0 && (q.bad_n || q.bad_len)) atomicOr(&g_attn_err, kErrIndex);
-    mine += p.a.Hkv * head_cost<long long>(p, q.n, ceil_div(q.len, kTile));
+    if (r == threadIdx.x) q0 = q, c0 = c, n0 = tiles ? p.a.Hkv * row_tiles(p, q.n) : 0;
+    else rest += c;
   }
+  long long ic = c0;                      // inclusive scans over the warp
+  int in = n0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sm.scan[warp] = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long uc = __shfl_up_sync(0xffffffffu, ic, o);
+    const int un = __shfl_up_sync(0xffffffffu, in, o);
+    if (lane >= o) ic += uc, in += un;
+  }
+  if (p.a.R > kThreads) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+  }
+  if (lane == 31) sm.scan[warp] = ic, sm.scan_items[warp] = in, sm.scan_rest[warp] = rest;
   if (threadIdx.x == 0) sm.r0 = p.a.R, sm.r0_line = 0, sm.r0_item = 0;
   bad = __syncthreads_or(bad);
-  long long total = prefix_long;
+  long long total = prefix_long, at_long = prefix_long, run_long = prefix_long;
+  int item = 0, run_items = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
+  for (int w = 0; w < kWarps; ++w) {
+    const long long wc = sm.scan[w];
+    total += wc + (p.a.R > kThreads ? sm.scan_rest[w] : 0);
+    run_long += wc, run_items += sm.scan_items[w];
+    if (w < warp) at_long += wc, item += sm.scan_items[w];
+  }
   if (total > kMaxLine) {                 // too long for the line's 32 bits: reported, nothing computed
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_attn_err, kErrIndex);
     bad = true;
@@ -317,45 +358,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool work = total > 0;
   const int prefix_cost = static_cast<int>(prefix_long > kMaxLine ? 0 : prefix_long);
   // at least a tile for each lane
-  const int share = max(2 * kWKeys, static_cast<int>((total + p.ctas - 1) / p.ctas));
+  const int share = max(2 * kWRows, static_cast<int>((static_cast<uint32_t>(total) + p.ctas - 1) / static_cast<uint32_t>(p.ctas)));
   const int b0 = blockIdx.x * share;
+  const auto place = [&](int r, const Request& q, int at, int c, int first_item) {
+    if (blockIdx.x == 0)
+      for (int i = 0; i < q.n; ++i) p.token[q.first + i] = TokenRecord{at, first_item, q.len, q.n, i, {0, 0, 0}};
+    // the first request whose items reach past b0
+    if ((at <= b0 && b0 < at + c) || (r == 0 && b0 < prefix_cost)) sm.r0 = r, sm.r0_line = at, sm.r0_item = first_item;
+  };
   if (work) {
-    int run = prefix_cost, run_items = 0;
-    for (int base = 0; base < p.a.R; base += kThreads) {
+    if (static_cast<int>(threadIdx.x) < p.a.R)
+      place(threadIdx.x, q0, static_cast<int>(at_long + ic - c0), static_cast<int>(c0), item + in - n0);
+    int run = static_cast<int>(run_long);
+    for (int base = kThreads; base < p.a.R; base += kThreads) {
       const int r = base + threadIdx.x;
       int c = 0, n = 0;
-      Request q;
+      Request q{0, 0, 0, false, false};
       if (r < p.a.R) {
-        q = base ? request(p.a, r) : q0;
+        q = request(p.a, r);
         const int tiles = ceil_div(q.len, kTile);
         c = p.a.Hkv * head_cost<int>(p, q.n, tiles);
         n = tiles ? p.a.Hkv * row_tiles(p, q.n) : 0;
       }
-      int ic = c, in = n;
+      int sc = c, sn = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int uc = __shfl_up_sync(0xffffffffu, ic, o), un = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) ic += uc, in += un;
+        const int uc = __shfl_up_sync(0xffffffffu, sc, o), un = __shfl_up_sync(0xffffffffu, sn, o);
+        if (lane >= o) sc += uc, sn += un;
       }
       __syncthreads();
-      if (lane == 31) sm.scan[warp] = ic, sm.scan_items[warp] = in;
+      if (lane == 31) sm.scan[warp] = sc, sm.scan_items[warp] = sn;
       __syncthreads();
-      int at = run + ic - c, item = run_items + in - n;
+      int at = run + sc - c, first_item = run_items + sn - n;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const int wc = static_cast<int>(sm.scan[w]), wi = sm.scan_items[w];
-        if (w < warp) at += wc, item += wi;
+        if (w < warp) at += wc, first_item += wi;
         run += wc, run_items += wi;
       }
-      if (r < p.a.R) {
-        if (blockIdx.x == 0)
-          for (int i = 0; i < q.n; ++i) {
-            TokenRecord rec{at, item, q.len, q.n, i, {0, 0, 0}};
-            p.token[q.first + i] = rec;
-          }
-        // the first request whose items reach past b0
-        if ((at <= b0 && b0 < at + c) || (r == 0 && b0 < prefix_cost)) sm.r0 = r, sm.r0_line = at, sm.r0_item = item;
-      }
+      if (r < p.a.R) place(r, q, at, c, first_item);
     }
   } else if (!bad && blockIdx.x == 0) {
     // nobody sees any key: the join still writes every row's 0 and -inf
@@ -702,13 +743,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // ---------------------------------------------------------------- the segment's partial
       const int cap = prefix ? kRows : p.q_rows_suffix;
-      const long long slot = (2ll * it->seg + l) * cap + row;
+      const long long slot = 2ll * it->seg + l;
       if (j0 < n) {
         ok = warp_wait(&sm.o_full[l], o_cnt++ & 1, kErrWaitAccum);
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          float4* po = reinterpret_cast<float4*>(prefix ? p.po_p : p.po_s) + slot * (D / 4);
+          float4* po = reinterpret_cast<float4*>(prefix ? p.po_p : p.po_s) + (slot * (cap >> 3) + (row >> 3)) * (2 * D) + (row & 7);
           uint32_t o[D / 32][32];
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) tmem_ld32(t_o + 32 * q, o[q]);
@@ -721,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < D / 32; ++q)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                po[8 * q + e] = make_float4(__uint_as_float(o[q][4 * e]), __uint_as_float(o[q][4 * e + 1]),
+                po[8 * (8 * q + e)] = make_float4(__uint_as_float(o[q][4 * e]), __uint_as_float(o[q][4 * e + 1]),
                                             __uint_as_float(o[q][4 * e + 2]), __uint_as_float(o[q][4 * e + 3]));
           }
         } else {
@@ -730,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&sm.o_empty[l]);
         }
       }
-      if (valid) reinterpret_cast<float2*>(prefix ? p.ml_p : p.ml_s)[slot] = make_float2(m, sum);
+      if (valid) reinterpret_cast<float2*>(prefix ? p.ml_p : p.ml_s)[slot * cap + row] = make_float2(m, sum);
       item_done();
     }
   }
@@ -742,127 +783,154 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the segments of each row: W warps a row take its segments in turn (in line order), the
-// lanes over the row's elements, and the first of them adds up what they found.
+// Joins the segments of each row.  A warp has eight consecutive rows of one key/value head (row =
+// token * G + query head of the group) and a C-th of their columns: lane 8c + i has row i and a
+// quarter (c) of those columns.  W warps take the rows' segments in turn, and the first of them adds
+// up what they found.
 constexpr int kJoinWarps = 8;
-template <bool F16, int D, int W>
+template <bool F16, int D, int W, int C>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_constant__ Params p) {
-  using V = typename std::conditional<D == 128, float4, float2>::type;
-  constexpr int E = D / 32;
-  __shared__ float part[kJoinWarps][32][E + 2];
+  constexpr int E = D / 4 / C;                          // columns of a lane
+  extern __shared__ float part[];                       // [E + 2][warp][32]
+  __shared__ float weights[kJoinWarps][32][8];
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
-  const long long row_out = static_cast<long long>(blockIdx.x) * (kJoinWarps / W) + warp / W;
-  const int t = static_cast<int>(row_out / p.a.Hq);
-  const int h = static_cast<int>(row_out - static_cast<long long>(t) * p.a.Hq), kvh = h / p.G, g = h - kvh * p.G;
-  pdl_wait();
+  const int row_all = (blockIdx.x * (kJoinWarps / W) + warp / W) * 8 + (lane & 7), kvh = blockIdx.y;
+  const int t = row_all / p.G, g = row_all - t * p.G, col = (blockIdx.z * 4 + (lane >> 3)) * (E / 4);   // first group of four columns
   const bool here = t < p.a.T;
+  pdl_wait();
   const int share = __ldcg(p.share);
   const int4 rec = here ? __ldcg(reinterpret_cast<const int4*>(p.token + t)) : make_int4(0, 0, 0, 1);
   const int i_tok = here ? __ldcg(&p.token[t].i) : 0;
   if (share == 0) return;                               // the requests do not cover the tokens
 
-  // The segments of one run of keys: row of segment i of the run in the partial arrays.
+  // The segments of one run of keys that hold the row: slots first, first + step, ...
   struct Run {
-    int cap, row, first, count, step;
-    __device__ long long at(int i) const { return static_cast<long long>(first + i * step) * cap + row; }
+    int first, count, step, row;
   };
-  const auto find = [&](int tok, int ntok_all, int tiles, int line, int ordinal, int cap) {
-    Run r{cap, 0, 0, 0, 1};
+  const auto find = [&](int tok, int ntok_all, int tiles, int line, int head, int ordinal) {
+    Run r{0, 0, 1, 0};
     if (tiles == 0) return r;
-    const int span = 2 * p.tb, rt = tok / span, rts = row_tiles(p, ntok_all), ntok = tile_tokens(p, ntok_all, rt);
+    const int span = 2 * p.tb, rt = ntok_all <= span ? 0 : tok / span, ntok = tile_tokens(p, ntok_all, rt);
     const bool rows = ntok > p.tb;
-    const int w = rows ? kWRows : kWKeys;
-    const int s = line + kvh * head_cost<int>(p, ntok_all, tiles) + rt * (tiles * kWRows + kWItem);
+    const int w = tile_weight(p, ntok);
+    const int s = line + kvh * head + (rt ? rt * full_cost(tiles) : 0);
     const int c0 = s / share, c1 = (s + (tiles - 1) * w) / share;
     const int in_tile = tok - rt * span, half = in_tile >= p.tb ? 1 : 0;
     r.row = (in_tile - half * p.tb) * p.G + g;
-    r.first = 2 * (c0 + ordinal + kvh * rts + rt) + (rows ? half : 0);
+    r.first = 2 * (c0 + ordinal + kvh * row_tiles(p, ntok_all) + rt) + (rows ? half : 0);
     r.count = (c1 - c0 + 1) * (rows ? 1 : 2);
     r.step = rows ? 2 : 1;                              // keys mode: both lanes' slots hold the row
     return r;
   };
-  const Run run_p = find(t, p.a.T, p.prefix_tiles, 0, 0, kRows);
-  const Run run_s = find(i_tok, rec.w, ceil_div(rec.z, kTile), rec.x, rec.y, p.q_rows_suffix);
-  const int n = here ? run_p.count + run_s.count : 0;
+  const int tiles_s = ceil_div(rec.z, kTile);
+  const Run run_p = find(t, p.a.T, here ? p.prefix_tiles : 0, 0, p.p_head, 0);
+  const Run run_s = find(i_tok, rec.w, here ? tiles_s : 0, rec.x, head_cost<int>(p, rec.w, tiles_s), rec.y);
+  const int n = run_p.count + run_s.count;
+  const auto slot = [&](int i, bool& in_p) {
+    in_p = i < run_p.count;
+    return in_p ? run_p.first + i * run_p.step : run_s.first + (i - run_p.count) * run_s.step;
+  };
+  // Rounds of 32 segments: their statistics first (eight loads a lane, all under way at once), the
+  // weights into shared memory, then the outputs, whose loads wait for nothing.
+  float(*wt)[8] = weights[warp];
   float top = -INFINITY, total = 0.f;
-  float o[E];
+  float4 o[E / 4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int base = 0; base * W < n; base += 32) {
-    const int i = (base + lane) * W + w0;               // this lane's segment
-    const bool in_p = i < run_p.count;
-    const long long at = in_p ? run_p.at(i) : run_s.at(i - run_p.count);
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (i < n) ml = __ldcg(reinterpret_cast<const float2*>(in_p ? p.ml_p : p.ml_s) + at);
-    // an empty segment (no tile, or nothing seen) has sum 0 and maybe no output: weight 0, not read
-    uint32_t live = __ballot_sync(0xffffffffu, ml.y != 0.f);
-    float m2 = fmaxf(top, ml.x);
+  for (int e = 0; e < E / 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int most = __reduce_max_sync(0xffffffffu, n);
+  for (int base = w0; base < most; base += 32 * W) {
+    float2 ml[8];
+    float m2 = top;
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, w));
+    for (int k = 0; k < 8; ++k) {
+      const int i = base + (4 * k + (lane >> 3)) * W;
+      bool in_p;
+      const long long s = slot(i, in_p);
+      ml[k] = i < n ? __ldcg(reinterpret_cast<const float2*>(in_p ? p.ml_p : p.ml_s) +
+                             s * (in_p ? kRows : p.q_rows_suffix) + (in_p ? run_p.row : run_s.row))
+                    : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m2 = fmaxf(m2, ml[k].x);
+    m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, 8));
+    m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, 16));
     const float ref = m2 == -INFINITY ? 0.f : m2, keep = exp2_approx(top - ref);
-    const float wt = ml.y == 0.f ? 0.f : exp2_approx(ml.x - ref);
-    float add = ml.y == 0.f ? 0.f : ml.y * wt;
+    float add = 0.f;
+    __syncwarp();
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) add += __shfl_xor_sync(0xffffffffu, add, w);
+    for (int k = 0; k < 8; ++k) {
+      // no tile, or nothing seen: maybe no output either, so weight 0 means not read
+      const float f = ml[k].y == 0.f ? 0.f : exp2_approx(ml[k].x - ref);
+      if (f != 0.f) add = fmaf(ml[k].y, f, add);
+      wt[4 * k + (lane >> 3)][lane & 7] = f;
+    }
+    __syncwarp();
+    add += __shfl_xor_sync(0xffffffffu, add, 8);
+    add += __shfl_xor_sync(0xffffffffu, add, 16);
     top = m2;
-    total = total * keep + add;
+    total = fmaf(total, keep, add);
+    if (base != w0) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= keep;
-    while (live) {                                      // four segments' loads under way at a time
-      V v[4];
-      float f[4];
+      for (int e = 0; e < E / 4; ++e) o[e].x *= keep, o[e].y *= keep, o[e].z *= keep, o[e].w *= keep;
+    }
+    const int here_n = min(32, (most - base + W - 1) / W);
+#pragma unroll(E >= 16 ? 2 : 8)
+    for (int k = 0; k < here_n; ++k) {
+      const float f = wt[k][lane & 7];
+      bool in_p;
+      const long long s = slot(base + k * W, in_p);
+      const int cap8 = in_p ? kRows / 8 : p.q_rows_suffix >> 3, row = in_p ? run_p.row : run_s.row;
+      const float4* src = reinterpret_cast<const float4*>(in_p ? p.po_p : p.po_s) + (s * cap8 + (row >> 3)) * (2 * D) + (row & 7) + col * 8;
+      // without a branch, so that several segments' loads are under way: a row without this segment
+      // loads some line of the workspace and drops it
+      const bool live = f != 0.f;
+      if (!live) src = reinterpret_cast<const float4*>(p.po_s);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = live ? __ffs(live) - 1 : 0;
-        const bool some = live != 0;
-        f[u] = some ? __shfl_sync(0xffffffffu, wt, j) : 0.f;
-        const long long aj = __shfl_sync(0xffffffffu, at, j);
-        const bool pj = __shfl_sync(0xffffffffu, static_cast<int>(in_p), j);
-        float* z = reinterpret_cast<float*>(&v[u]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) z[e] = 0.f;
-        if (some) v[u] = __ldcg(reinterpret_cast<const V*>((pj ? p.po_p : p.po_s) + aj * D) + lane);
-        live &= live - 1;
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float* vf = reinterpret_cast<const float*>(&v[u]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(vf[e], f[u], o[e]);
+      for (int e = 0; e < E / 4; ++e) {
+        const float4 v = __ldcg(src + 8 * e);
+        o[e].x = fmaf(live ? v.x : 0.f, f, o[e].x), o[e].y = fmaf(live ? v.y : 0.f, f, o[e].y);
+        o[e].z = fmaf(live ? v.z : 0.f, f, o[e].z), o[e].w = fmaf(live ? v.w : 0.f, f, o[e].w);
       }
     }
   }
   if constexpr (W > 1) {
-    part[warp][lane][0] = top, part[warp][lane][1] = total;
+    const auto at = [&](int k, int w) -> float& { return part[(k * kJoinWarps + w) * 32 + lane]; };
+    at(0, warp) = top, at(1, warp) = total;
 #pragma unroll
-    for (int e = 0; e < E; ++e) part[warp][lane][2 + e] = o[e];
+    for (int e = 0; e < E / 4; ++e)
+      at(2 + 4 * e, warp) = o[e].x, at(3 + 4 * e, warp) = o[e].y, at(4 + 4 * e, warp) = o[e].z, at(5 + 4 * e, warp) = o[e].w;
     __syncthreads();
     if (w0 != 0) return;
 #pragma unroll
-    for (int w = 1; w < W; ++w) top = fmaxf(top, part[warp + w][lane][0]);
-    const float ref = top == -INFINITY ? 0.f : top;
+    for (int w = 1; w < W; ++w) top = fmaxf(top, at(0, warp + w));
+    const float all = top == -INFINITY ? 0.f : top;
     total = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-#pragma unroll
+    for (int e = 0; e < E / 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
     for (int w = 0; w < W; ++w) {
-      const float f = exp2_approx(part[warp + w][lane][0] - ref);
-      total = fmaf(part[warp + w][lane][1], f, total);
+      const float f = exp2_approx(at(0, warp + w) - all);
+      total = fmaf(at(1, warp + w), f, total);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(part[warp + w][lane][2 + e], f, o[e]);
+      for (int e = 0; e < E / 4; ++e) {
+        o[e].x = fmaf(at(2 + 4 * e, warp + w), f, o[e].x), o[e].y = fmaf(at(3 + 4 * e, warp + w), f, o[e].y);
+        o[e].z = fmaf(at(4 + 4 * e, warp + w), f, o[e].z), o[e].w = fmaf(at(5 + 4 * e, warp + w), f, o[e].w);
+      }
     }
   }
   if (!here) return;
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  uint16_t* dst = p.a.O + row_out * D + E * lane;
-  if constexpr (D == 128)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack2<F16>(o[0] * inv, o[1] * inv);
-  if (lane == 0 && p.a.lse)
+  const long long row_out = static_cast<long long>(t) * p.a.Hq + kvh * p.G + g;
+  uint2* dst = reinterpret_cast<uint2*>(p.a.O + row_out * D + 4 * col);
+#pragma unroll
+  for (int e = 0; e < E / 4; ++e)
+    dst[e] = make_uint2(pack2<F16>(o[e].x * inv, o[e].y * inv), pack2<F16>(o[e].z * inv, o[e].w * inv));
+  if (lane < 8 && blockIdx.z == 0 && p.a.lse)
     p.a.lse[row_out] = total == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(total)) * 0.6931471805599453f;
 }
+template <int D>
+constexpr size_t kJoinSmem = static_cast<size_t>(D / 4 + 2) * kJoinWarps * 32 * 4;   // C = 1
 
 struct Layout {
   int G, tb, n_prefix, rows_s, ctas;
@@ -879,7 +947,7 @@ Layout layout(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t 
   // requests' row tiles: no more than one each and one more for every full tile of tokens
   const int64_t tiles_each = (max_new + span - 1) / span;
   const int64_t n_suffix = Hkv * std::min(R * tiles_each, R + T / span);
-  l.rows_s = static_cast<int>(std::min<int64_t>(kRows, max_new * l.G));
+  l.rows_s = static_cast<int>(std::min<int64_t>(kRows, (max_new * l.G + 7) / 8 * 8));
   size_t off = kWsHeaderBytes;
   const auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -909,12 +977,13 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
   p.n_prefix = p.prefix_tiles ? l.n_prefix : 0;
   // The line is 32 bits on the device; a prefix alone that passes it is refused (kMaxLine / 4 tiles
   // of rows: 2^28 / 8 heads / 128 rows and 2^21 keys, for example).
-  const long long full = static_cast<long long>(p.prefix_tiles) * kWRows + kWItem;
+  const long long full = static_cast<long long>(p.prefix_tiles) * kWRows + kWItemRows;
   const int span = 2 * p.tb;
   p.p_rts = (a.T + span - 1) / span;
   const int last = a.T - (p.p_rts - 1) * span;
   const long long head = p.prefix_tiles
-      ? (p.p_rts - 1) * full + static_cast<long long>(p.prefix_tiles) * (last > p.tb ? kWRows : kWKeys) + kWItem : 0;
+      ? (p.p_rts - 1) * full + static_cast<long long>(p.prefix_tiles) * (last > p.tb ? kWRows : (last * p.G > 32 ? kWKeys : kWFew)) +
+            (last > p.tb ? kWItemRows : kWItem) : 0;
   if (head * a.Hkv > kMaxLine) return cudaErrorInvalidValue;
   p.p_full = static_cast<int>(full), p.p_head = static_cast<int>(head);
   p.q_rows_suffix = l.rows_s;
@@ -945,14 +1014,20 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
   e = launch_pdl(k_attn<F16, D>, dim3(l.ctas), kThreads, smem, stream, tq_p, tq_s, tk, tv, p);
   if (e != cudaSuccess) return e;
   // Few rows have many segments each (the prefix is spread over all SMs): more warps a row.
-  const long long rows = static_cast<long long>(a.T) * a.Hq;
-  const auto join = [&](void (*kern)(Params), int w) {
-    const long long per = kJoinWarps / w;
-    return launch_pdl(kern, dim3(static_cast<unsigned>((rows + per - 1) / per)), kJoinWarps * 32, 0, stream, p);
+  const int blocks = (a.T * p.G + 7) / 8;               // of eight rows of a head
+  const auto join = [&](void (*kern)(Params), int w, int c) {
+    const int per = kJoinWarps / w;
+    return launch_pdl(kern, dim3((blocks + per - 1) / per, a.Hkv, c), kJoinWarps * 32, w > 1 ? kJoinSmem<D> : 0, stream, p);
   };
-  if (rows <= 2048) return join(k_attn_join<F16, D, 8>, 8);
-  if (rows <= 8192) return join(k_attn_join<F16, D, 2>, 2);
-  return join(k_attn_join<F16, D, 1>, 1);
+  // W C warps for each eight rows of a head, as long as they fit the SMs at once (32 an SM).
+  const long long warps = static_cast<long long>(blocks) * a.Hkv, fit = 32ll * l.ctas;
+  constexpr int C = D == 128 ? 4 : 2;
+  if (warps * 8 * C <= fit) return join(k_attn_join<F16, D, 8, C>, 8, C);
+  if (warps * 8 * 2 <= fit) return join(k_attn_join<F16, D, 8, 2>, 8, 2);
+  if (warps * 4 * 2 <= fit) return join(k_attn_join<F16, D, 4, 2>, 4, 2);
+  if (warps * 2 * 2 <= fit) return join(k_attn_join<F16, D, 2, 2>, 2, 2);
+  if (warps * 2 <= fit) return join(k_attn_join<F16, D, 1, 2>, 1, 2);
+  return join(k_attn_join<F16, D, 1, 1>, 1, 1);
 }
 
 }  // namespace
