@@ -90,7 +90,7 @@ def _compile_marshal() -> str:
 def _link_marshal(obj: str) -> None:
     tmp = MARSHAL + ".tmp"
     r = subprocess.run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libwq.so", "-Wl,-rpath,$ORIGIN", "-L" + _torch_flags()[1],
-                        "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python"], capture_output=True, text=True)
+                        "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link of _marshal.so failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, MARSHAL)

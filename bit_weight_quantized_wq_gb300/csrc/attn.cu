@@ -199,8 +199,10 @@ struct Walk {
       pitem = h * p.p_rts + t;
     }
     r = r0, line = r0_line, item = r0_item, kvh = 0, rt = 0;
-    if (r < p.a.R) q = request(p.a, r);
-    read_ahead();
+    if (h == p.a.Hkv && r < p.a.R) {
+      q = request(p.a, r);
+      read_ahead();
+    }
   }
 
   __device__ void read_ahead() {
@@ -226,6 +228,10 @@ struct Walk {
       ++pitem;
       if (it.tok0 + 2 * p.tb >= p.a.T) t = 0, ++h;
       else ++t;
+      if (h == p.a.Hkv && r < p.a.R) {         // on to the requests
+        q = request(p.a, r);
+        read_ahead();
+      }
       if (it.lo < it.hi) return true;
     }
     while (r < p.a.R) {
@@ -343,8 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   bad = __syncthreads_or(bad);
   long long total = prefix_long, at_long = prefix_long, run_long = prefix_long;
   int item = 0, run_items = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  const int with_requests = min(kWarps, (p.a.R + 31) / 32);
+#pragma unroll 4
+  for (int w = 0; w < with_requests; ++w) {
     const long long wc = sm.scan[w];
     total += wc + (p.a.R > kThreads ? sm.scan_rest[w] : 0);
     run_long += wc, run_items += sm.scan_items[w];
