@@ -89,6 +89,9 @@ ROPE = [  # T, Hq, Hkv, d, rot, interleaved, norm
     (64, 16, 16, 64, 32, False, True),
     (600, 8, 1, 128, 32, False, True),
     (515, 7, 7, 64, 48, True, True),
+    (1100, 64, 8, 64, 64, True, True),          # enough units for the kernel that walks over them
+    (1301, 33, 3, 128, 96, False, True),
+    (1000, 17, 4, 256, 128, False, False),
 ]
 
 
@@ -116,7 +119,7 @@ def test_rope(B, dtype, T, Hq, Hkv, d, rot, interleaved, norm):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
-@pytest.mark.parametrize("T,Hq,Hkv,d", [(1, 8, 2, 128), (50, 4, 4, 64), (9, 16, 2, 256), (700, 6, 2, 128)])
+@pytest.mark.parametrize("T,Hq,Hkv,d", [(1, 8, 2, 128), (50, 4, 4, 64), (9, 16, 2, 256), (700, 6, 2, 128), (1500, 24, 4, 128)])
 def test_rope_cache(B, dtype, page, T, Hq, Hkv, d):
     """From the parts of a fused projection output into a cache; padding rows are not written, and
     neither is any other slot."""
@@ -257,6 +260,9 @@ ATTN = [  # new tokens, prefix, own lengths, Hq, Hkv
     ([1] * 70, 333, [1 + 3 * i for i in range(70)], 8, 2),
     ([1] * 3, 4200, [700, 2, 1500], 8, 1),
     ([2] * 20, 1025, [5 + 7 * i for i in range(20)], 16, 1),
+    ([1] * 1100, 70, [i % 5 for i in range(1100)], 2, 1),  # more requests than one round of the set-up
+    ([1, 0, 3], 200, [1, 0, 64], 128, 1),                 # 128 query heads on one
+    ([1, 2], 150, [64, 65], 9, 3),                        # tiles that end exactly, and one key later
 ]
 
 
@@ -283,6 +289,32 @@ def test_attn_one_token_each_without_q_start_strided_q_no_own_keys(B):
                 B.attn_shared_prefix(q, b.kc, b.vc, b.args[0], 700, None, None, scale=128 ** -0.5)):
         assert torch.equal(got[0], o) and torch.equal(got[1], lse)
     b.check((o, lse))
+
+
+def test_attn_workspace_header_stays_zero_and_serves_other_calls(B):
+    """One zeroed workspace for an attention call, a quantized layer and adapters in turn."""
+    import torch
+    b = Batch(81, [1, 2], 700, [100, 30], 8, 2, 64, 16, "bf16")
+    K, N, M = 512, 256, 3
+    pk = int4_g128.quantize(inputs.weights(5, N, K, 0.05))
+    d = [torch.from_numpy(np.ascontiguousarray(p)).cuda() for p in pk]
+    xb, xf = inputs.activations(6, M, K)
+    X = torch.from_numpy(xb.view(np.int16)).cuda().view(torch.bfloat16)
+    (a, w, s), _ = _adapter_set(3, 2, 16, K, N, "bf16")
+    ad = torch.tensor([1, -1, 0], dtype=torch.int32, device="cuda")
+    lib = B.load_library()
+    need = max(lib.wq_attn_workspace_bytes(3, 2, 8, 2, 64, 2), lib.wq_gemm_w4a16_lora_workspace_bytes(0, M, K, N, 16),
+               lib.wq_lora_workspace_bytes(M, K, N, 16))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(3):
+        b.check(b.run(B, workspace=ws))
+        y = B.gemm_w4a16("int4_g128", X, *d, workspace=ws)
+        got = y, B.lora_add(y, X, a, w, ad, s, workspace=ws), B.gemm_w4a16_lora("int4_g128", X, *d, a, w, ad, s, workspace=ws)
+        assert torch.equal(got[1], got[2])
+        first = got if first is None else first
+        assert all(torch.equal(p, q) for p, q in zip(got, first))
+        assert int(ws[:64 * 1024 + 10 * 1024 * 1024].count_nonzero()) == 0
 
 
 def test_attn_large_scores_and_shifted_scores(B):
