@@ -570,3 +570,14 @@ def test_calls_are_captured_in_a_graph(B):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, want) and torch.equal(y2, y)
+
+
+def test_the_three_together_as_one_block(B):
+    """The example: a shared prompt prefilled, then requests with adapters decoding behind it."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "shared_prefix_block.py")
+    spec = importlib.util.spec_from_file_location("shared_prefix_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main() < 0.02
