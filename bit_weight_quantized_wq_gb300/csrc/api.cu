@@ -701,6 +701,7 @@ wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_str
   if (prefix_len < 0 || prefix_len > (1LL << 30) || max_blocks < 0 || max_blocks > (1LL << 30) / page_size)
     return WQ_ERR_SHAPE;
   if (!q_start && (T != R || max_new != 1)) return WQ_ERR_SHAPE;
+  if (!wq::attn_prefix_fits(T, Hq, Hkv, prefix_len)) return WQ_ERR_SHAPE;
   if ((prefix_len > 0 && !prefix_pages) || (max_blocks > 0 && (!block_table || !suffix_lens))) return WQ_ERR_NULL;
   const auto odd4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
   if (!aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(O) || odd4(lse) || odd4(prefix_pages) ||

@@ -155,10 +155,12 @@ __device__ __forceinline__ int row_tiles(const Params& p, int ntok) {
   return ntok <= 2 * p.tb ? (ntok > 0 ? 1 : 0) : ceil_div(ntok, 2 * p.tb);
 }
 __device__ __forceinline__ int tile_tokens(const Params& p, int ntok, int rt) { return min(2 * p.tb, ntok - rt * 2 * p.tb); }
-__device__ __forceinline__ int tile_weight(const Params& p, int tokens) {
-  return tokens > p.tb ? kWRows : (tokens * p.G > 32 ? kWKeys : kWFew);
+// Rows mode or keys mode of an item of so many tokens.
+__host__ __device__ inline bool rows_mode(int tb, int tokens) { return tokens > tb; }
+__host__ __device__ inline int tile_weight(int tb, int G, int tokens) {
+  return rows_mode(tb, tokens) ? kWRows : (tokens * G > 32 ? kWKeys : kWFew);
 }
-__device__ __forceinline__ int item_weight(const Params& p, int tokens) { return tokens > p.tb ? kWItemRows : kWItem; }
+__host__ __device__ inline int item_weight(int tb, int tokens) { return rows_mode(tb, tokens) ? kWItemRows : kWItem; }
 // Line length of an item in rows mode.
 __device__ __forceinline__ int full_cost(int tiles) { return tiles * kWRows + kWItemRows; }
 // Line length of all row tiles of one head (T is int or, where it may be too long, long long).
@@ -168,7 +170,7 @@ __device__ __forceinline__ L head_cost(const Params& p, int ntok, int tiles) {
   if (rts == 0 || tiles == 0) return 0;
   const int last = tile_tokens(p, ntok, rts - 1);
   return static_cast<L>(rts - 1) * (static_cast<L>(tiles) * kWRows + kWItemRows) +
-         static_cast<L>(tiles) * tile_weight(p, last) + item_weight(p, last);
+         static_cast<L>(tiles) * tile_weight(p.tb, p.G, last) + item_weight(p.tb, last);
 }
 // First tile of an item (line start s, tiles n of weight w) that starts at or after position b.
 // Tile t therefore belongs to the CTA whose share holds position s + t w.
@@ -217,14 +219,14 @@ struct Walk {
     while (h < p.a.Hkv) {
       if (pline >= b1) return false;
       it.ntok = tile_tokens(p, p.a.T, t);
-      const int w = tile_weight(p, it.ntok);
+      const int w = tile_weight(p.tb, p.G, it.ntok);
       it.kvh = h, it.r = -1;
       it.lo = tile_at(b0, pline, p.prefix_tiles, w), it.hi = tile_at(b1, pline, p.prefix_tiles, w);
       it.len = p.a.prefix_len;
       it.tok0 = t * 2 * p.tb;
       it.lim0 = p.a.prefix_len;
       it.seg = cta + pitem;
-      pline += p.prefix_tiles * w + item_weight(p, it.ntok);
+      pline += p.prefix_tiles * w + item_weight(p.tb, it.ntok);
       ++pitem;
       if (it.tok0 + 2 * p.tb >= p.a.T) t = 0, ++h;
       else ++t;
@@ -244,14 +246,14 @@ struct Walk {
       }
       if (line >= b1) return false;
       it.ntok = tile_tokens(p, q.n, rt);
-      const int w = tile_weight(p, it.ntok);
+      const int w = tile_weight(p.tb, p.G, it.ntok);
       it.kvh = kvh, it.r = r;
       it.lo = tile_at(b0, line, tiles, w), it.hi = tile_at(b1, line, tiles, w);
       it.len = q.len;
       it.tok0 = q.first + rt * 2 * p.tb;
       it.lim0 = q.len - q.n + rt * 2 * p.tb + 1;
       it.seg = cta + item;
-      line += tiles * w + item_weight(p, it.ntok);
+      line += tiles * w + item_weight(p.tb, it.ntok);
       ++item;
       if (++rt == rts) rt = 0, ++kvh;
       if (it.lo < it.hi) return true;
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (const Item* it = next_item()) {   // one 128-row tile, or one per lane
       const bool prefix = it->r < 0;
       const int box_tok = prefix ? p.tb : min(p.tb, p.a.max_new);
-      for (int i = 0; i < (it->ntok > p.tb ? 2 : 1); ++i, ++qord) {
+      for (int i = 0; i < (rows_mode(p.tb, it->ntok) ? 2 : 1); ++i, ++qord) {
         const int s = qord & 1;
         ok = warp_wait(&sm.q_empty[s], ((qord >> 1) & 1) ^ 1, kErrWaitEmpty);
         if (!ok) break;
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // other lane uses it: a wait by parity is only sound if no phase of the slot is left out.
     while (const Item* it = next_item()) {
       const int n = it->hi - it->lo;
-      const bool rows = it->ntok > p.tb;
+      const bool rows = rows_mode(p.tb, it->ntok);
       const int nq = rows ? 2 : 1, ahead = k_ahead(rows), flip = n_items & 1;
       const uint64_t qd = q0 + ((qord + (rows ? l : 0)) & 1) * (S::kQBytes >> 4);
       for (int i = 0; i < nq && ok; ++i) ok = warp_wait(&sm.q_full[(qord + i) & 1], ((qord + i) >> 1) & 1, kErrWaitFull);
@@ -646,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t cnt = 0, o_cnt = 0, v_end = 0;     // tiles of this lane so far; V tiles of all items so far
     while (const Item* it = next_item()) {
       const int lo = it->lo, n = it->hi - lo, len = it->len;
-      const bool prefix = it->r < 0, rows = it->ntok > p.tb;
+      const bool prefix = it->r < 0, rows = rows_mode(p.tb, it->ntok);
       const int tok_item = tok + (rows && l ? p.tb : 0);
       const bool valid = tok < p.tb && tok_item < it->ntok;
       const bool active = __any_sync(0xffffffffu, valid);
@@ -819,8 +821,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
     Run r{0, 0, 1, 0};
     if (tiles == 0) return r;
     const int span = 2 * p.tb, rt = ntok_all <= span ? 0 : tok / span, ntok = tile_tokens(p, ntok_all, rt);
-    const bool rows = ntok > p.tb;
-    const int w = tile_weight(p, ntok);
+    const bool rows = rows_mode(p.tb, ntok);
+    const int w = tile_weight(p.tb, p.G, ntok);
     const int s = line + kvh * head + (rt ? rt * full_cost(tiles) : 0);
     const int c0 = s / share, c1 = (s + (tiles - 1) * w) / share;
     const int in_tile = tok - rt * span, half = in_tile >= p.tb ? 1 : 0;
@@ -972,6 +974,19 @@ Layout layout(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t 
   return l;
 }
 
+// The prefix's items on the line: row tiles of a head, the length of a full one and of all of them.
+struct PrefixLine {
+  int row_tiles;
+  long long full, head;
+  PrefixLine(int64_t T, int64_t prefix_len, int tb, int G) {
+    const int64_t tiles = (prefix_len + kTile - 1) / kTile, span = 2 * tb;
+    row_tiles = static_cast<int>((T + span - 1) / span);
+    const int last = static_cast<int>(T - (row_tiles - 1) * span);
+    full = tiles * kWRows + kWItemRows;
+    head = tiles ? (row_tiles - 1) * full + tiles * tile_weight(tb, G, last) + item_weight(tb, last) : 0;
+  }
+};
+
 template <bool F16, int D>
 cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
   const Layout l = layout(a.T, a.R, a.Hq, a.Hkv, D, a.max_new);
@@ -982,17 +997,8 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
   while ((1 << p.log_page) < a.page_size) ++p.log_page;
   p.prefix_tiles = (a.prefix_len + kTile - 1) / kTile;
   p.n_prefix = p.prefix_tiles ? l.n_prefix : 0;
-  // The line is 32 bits on the device; a prefix alone that passes it is refused (kMaxLine / 4 tiles
-  // of rows: 2^28 / 8 heads / 128 rows and 2^21 keys, for example).
-  const long long full = static_cast<long long>(p.prefix_tiles) * kWRows + kWItemRows;
-  const int span = 2 * p.tb;
-  p.p_rts = (a.T + span - 1) / span;
-  const int last = a.T - (p.p_rts - 1) * span;
-  const long long head = p.prefix_tiles
-      ? (p.p_rts - 1) * full + static_cast<long long>(p.prefix_tiles) * (last > p.tb ? kWRows : (last * p.G > 32 ? kWKeys : kWFew)) +
-            (last > p.tb ? kWItemRows : kWItem) : 0;
-  if (head * a.Hkv > kMaxLine) return cudaErrorInvalidValue;
-  p.p_full = static_cast<int>(full), p.p_head = static_cast<int>(head);
+  const PrefixLine line(a.T, a.prefix_len, p.tb, p.G);
+  p.p_rts = line.row_tiles, p.p_full = static_cast<int>(line.full), p.p_head = static_cast<int>(line.head);
   p.q_rows_suffix = l.rows_s;
   p.ctas = l.ctas;
   p.token = reinterpret_cast<TokenRecord*>(ws + l.token);
@@ -1041,6 +1047,11 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
 
 size_t attn_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new) {
   return layout(T, R, Hq, Hkv, d, max_new).bytes;
+}
+
+bool attn_prefix_fits(int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_len) {
+  const int G = static_cast<int>(Hq / Hkv);
+  return PrefixLine(T, prefix_len, kRows / G, G).head <= kMaxLine / Hkv;
 }
 
 cudaError_t launch_attn_shared_prefix(int dtype, const AttnArgs& a, void* ws, cudaStream_t stream) {

@@ -176,6 +176,7 @@ struct AttnArgs {
   float* lse;
 };
 size_t attn_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new);
+bool attn_prefix_fits(int64_t T, int64_t Hq, int64_t Hkv, int64_t prefix_len);
 cudaError_t launch_attn_shared_prefix(int dtype, const AttnArgs& a, void* ws, cudaStream_t stream);
 uint32_t attn_read_and_clear_error();
 

@@ -504,14 +504,22 @@ wq_status wq_qk_norm_rope_cache(wq_dtype dtype, int64_t T, int64_t Hq, int64_t H
  *   block_table [R, max_blocks] int32: the pages of the requests' own tokens (entries past a
  *     request's length are not read); suffix_lens [R] int32, at most max_blocks * page_size.
  *     max_blocks 0: no request has own keys, both may be NULL.
- *   Cache rows past a length are not used, whatever they hold.
+ *   Cache rows past a length are not used, whatever they hold.  Rows within it are: a value
+ *   that is infinite or NaN reaches every row that sees it, and of the request's own new tokens
+ *   also those before it (their weight for it is 0, and 0 times it is NaN).
  *   O [T, Hq, d] dtype, lse [T, Hq] float32 (may be NULL): contiguous outputs, distinct from Q.
  *   workspace / ws_bytes: at least wq_attn_workspace_bytes(...) bytes, under the workspace rules
  *     of wq_gemm_workspace_bytes (it starts with the same header, left at zero).
  * Errors: WQ_ERR_ARG (dtype; scale not positive and finite); WQ_ERR_NULL; WQ_ERR_SHAPE unless
  *   T, R, Hq, Hkv, pages, max_new >= 1, Hq % Hkv == 0, Hq / Hkv <= 128, d is 64 or 128, page_size as above,
  *   prefix_len, max_blocks >= 0, prefix_len and max_blocks * page_size <= 2^30, pages * Hkv <=
- *   2^31 - 1, T <= 2^24, Hq <= 1024; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.
+ *   2^31 - 1, T <= 2^24, Hq <= 1024, and the work on the prefix fits one call, Hkv * ceil(T / (2 b)) *
+ *   (10 ceil(prefix_len / 64) + 20) <= 2^30 with b = 128 / (Hq / Hkv) rounded down; WQ_ERR_ALIGN;
+ *   WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.  The work on the prefix and on the
+ *   requests' own keys together (counted alike, from lengths that only the device knows) is held to
+ *   2^30 too: past it, and where q_start does not cover the tokens, the error word gets the bit of
+ *   an index out of range and O is not written.  (One request of 200000 new tokens, 32 heads on 8,
+ *   is within it.)
  */
 size_t wq_attn_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new);
 wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_stride, int64_t T, int64_t R, int64_t Hq,

@@ -143,6 +143,14 @@ def test_attn_refusals(lib):
     assert lib.wq_attn_workspace_bytes(4, 4, 8, 3, 128, 1) == 0
 
 
+def test_attn_refuses_more_prefix_work_than_one_call_holds(lib):
+    """Hq = Hkv = 8: row tiles of 256 tokens.  8 * ceil(T / 256) * (10 ceil(P / 64) + 20) <= 2^30."""
+    T = 256 * 16
+    most = 64 * (((1 << 30) // 8 // 16 - 20) // 10)
+    assert _attn(lib, Hq=8, Hkv=8, qs=8 * 128, T=T, q0=_p(9), P=most + 64, pages=64) == 2
+    assert _attn(lib, Hq=8, Hkv=8, qs=8 * 128, T=T, q0=_p(9), P=most, pages=64) != 2
+
+
 def _lora(lib, **kw):
     a = dict(dtype=0, base=_p(0), X=_p(1), M=4, K=128, N=64, A=_p(2), B=_p(3), L=2, r=16, ranks=None, ad=_p(4), s=_p(5),
              Y=_p(6), ws=_p(7), wsb=1 << 40)
