@@ -101,6 +101,20 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
   return v;
 }
 
+// The sum, in the CTAs' order, of the floats at p in the n <= 8 CTAs of the cluster; all loads under way
+// at once (one after the other they took some 300 cycles each).
+__device__ __forceinline__ float sum_cluster(const float* p, uint32_t n) {
+  float part[8];
+#pragma unroll
+  for (uint32_t c = 0; c < 8; ++c)
+    if (c < n) part[c] = ld_cluster(p, c);
+  float v = part[0];
+#pragma unroll
+  for (uint32_t c = 1; c < 8; ++c)
+    if (c < n) v += part[c];
+  return v;
+}
+
 // Steps of 32 of the contracted index that slice i of n takes.
 __device__ __forceinline__ void slice(int steps, int i, int n, int& lo, int& hi) {
   lo = static_cast<int>(static_cast<int64_t>(steps) * i / n);
@@ -190,8 +204,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
   for (int i = threadIdx.x * n + cluster_rank(); i < 16 * W; i += blockDim.x * n) {
     const int row = i / W, j = i % W;
     if (!((rows >> row) & 1u) || j >= rank) continue;
-    float v = 0.f;
-    for (uint32_t c = 0; c < n; ++c) v += n > 1 ? ld_cluster(red + i, c) : red[i];
+    const float v = n > 1 ? sum_cluster(red + i, n) : red[i];
     V[static_cast<int64_t>(m0 + row) * p.r + j] = round1<F16>(v * s);
   }
   if (n > 1) cluster_sync();                  // the others have read this CTA's sums
@@ -213,8 +226,8 @@ struct TileSmem {
     float red[kTileRows * kTileLd];            // after the last product
   };
   uint64_t full[kTileStages], empty[kTileStages], acc_full[2], acc_empty[2], drain;
-  int id[kTileRows];                           // adapter of each row
-  int found[kTileRows];                        // the different ones, in order of their first row
+  int lead[4][32], place[4][32], n_lead[4];    // a warp's leading rows: adapter, place in `found`
+  int found[kTileRows];                        // the different adapters, in order of their first row
   int n_found[4];
   uint32_t tmem_base;
 };
@@ -239,32 +252,39 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
   pdl_launch_dependents();
   const int m0 = blockIdx.y * kTileRows, j0 = blockIdx.z * 64;
   const int row = (warp & 3) * 32 + lane;      // warps 2 .. 5: a row a thread, its tensor-memory lane
-  int mine = -1;
-  if (warp >= 2) sm.id[row] = mine = row_adapter(p, m0 + row);
-  __syncthreads();
+  const int mine = warp >= 2 ? row_adapter(p, m0 + row) : -1;
+  // The different adapters in order of their first row: within a warp by a match, then the leaders of
+  // warp w look for themselves among those of the warps before it.
   int place = -1;                              // of this row's adapter in `found`
   {
-    bool leads = mine >= 0;
-    int first = row;
-    if (warp >= 2 && mine >= 0)
-      for (int i = 0; i < row; ++i)
-        if (sm.id[i] == mine) {
-          leads = false, first = i;
-          break;
-        }
-    const uint32_t lead = __ballot_sync(0xffffffffu, leads);
-    if (warp >= 2 && lane == 0) sm.n_found[warp & 3] = __popc(lead);
+    const uint32_t lead = leaders(mine), same = __match_any_sync(0xffffffffu, mine);
+    const bool leads = (lead >> lane) & 1u;
+    const int nth = __popc(lead & ((1u << lane) - 1));
+    if (warp >= 2) {
+      if (leads) sm.lead[warp & 3][nth] = mine;
+      if (lane == 0) sm.n_lead[warp & 3] = __popc(lead);
+    }
     __syncthreads();
-    if (warp >= 2 && leads) {
-      place = __popc(lead & ((1u << lane) - 1));
+    int before = -1;                           // 32 w + i: warp w's i-th leader has it already
+    if (warp >= 2 && leads)
+      for (int w = 0; w < (warp & 3) && before < 0; ++w)
+        for (int i = 0; i < sm.n_lead[w] && before < 0; ++i)
+          if (sm.lead[w][i] == mine) before = 32 * w + i;
+    const uint32_t fresh = __ballot_sync(0xffffffffu, leads && before < 0);
+    if (warp >= 2 && lane == 0) sm.n_found[warp & 3] = __popc(fresh);
+    __syncthreads();
+    if ((fresh >> lane) & 1u) {
+      place = __popc(fresh & ((1u << lane) - 1));
       for (int w = 0; w < (warp & 3); ++w) place += sm.n_found[w];
       sm.found[place] = mine;
-      sm.id[row] = -2 - place;                 // followers look it up
     }
+    if (warp >= 2 && leads) sm.place[warp & 3][nth] = place;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp >= 2 && mine >= 0 && !leads) place = -2 - sm.id[first];
+    if (before >= 0) place = sm.place[before >> 5][before & 31];
+    place = __shfl_sync(0xffffffffu, place, __ffs(same) - 1);
+    if (mine < 0) place = -1;
   }
   const int found = sm.n_found[0] + sm.n_found[1] + sm.n_found[2] + sm.n_found[3];
   const int passes = (found + kTilePass - 1) / kTilePass;
@@ -370,12 +390,8 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
     if (a < 0) continue;
     const float s = __ldg(p.scales + a);
     const int rank = adapter_rank(p, a) - j0;
-    float2 v = make_float2(0.f, 0.f);
-    for (uint32_t c = 0; c < n; ++c) {
-      const float* src = sm.red + r * kTileLd + 2 * lane;
-      v.x += n > 1 ? ld_cluster(src, c) : src[0];
-      v.y += n > 1 ? ld_cluster(src + 1, c) : src[1];
-    }
+    const float* src = sm.red + r * kTileLd + 2 * lane;
+    const float2 v = n > 1 ? make_float2(sum_cluster(src, n), sum_cluster(src + 1, n)) : make_float2(src[0], src[1]);
     if (2 * lane < rank)
       *reinterpret_cast<uint32_t*>(V + static_cast<int64_t>(m) * p.r + j0 + 2 * lane) = pack2<F16>(v.x * s, v.y * s);
   }
