@@ -771,7 +771,7 @@ wq_status wq_lora_add(wq_dtype dtype, const uint16_t* base, const uint16_t* X, i
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = wq::launch_lora_shrink(dtype, a, scratch, s);
   if (e != cudaSuccess) return WQ_ERR_CUDA;
-  return from_cuda(wq::launch_lora_expand(dtype, a, scratch, s));
+  return from_cuda(wq::launch_lora_expand(dtype, a, scratch, true, s));
 }
 
 // The layer's own workspace (or the shared header, where that is longer), then the adapters' scratch.
@@ -807,7 +807,7 @@ wq_status wq_gemm_w4a16_lora(wq_fmt fmt, const uint16_t* X, int64_t M, int64_t K
   if (e != cudaSuccess) return WQ_ERR_CUDA;
   st = wq_gemm_w4a16(fmt, X, M, K, N, Wq, scales, zeros, Y, workspace, off, stream);
   if (st != WQ_OK) return st;
-  return from_cuda(wq::launch_lora_expand(WQ_DTYPE_BF16, a, scratch, s));
+  return from_cuda(wq::launch_lora_expand(WQ_DTYPE_BF16, a, scratch, false, s));
 }
 
 wq_status wq_check_device(void) { return check_device_cached(); }

@@ -191,7 +191,8 @@ struct LoraArgs {
 };
 size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
 cudaError_t launch_lora_shrink(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream);
-cudaError_t launch_lora_expand(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream);
+// base_ready: the base was written before the shrink was launched, not by a kernel after it
+cudaError_t launch_lora_expand(int dtype, const LoraArgs& a, void* scratch, bool base_ready, cudaStream_t stream);
 uint32_t lora_read_and_clear_error();
 
 // layout.cu -- row re-layout of the stacked gate+up weight

@@ -15,6 +15,7 @@
 // memory and are added in a fixed order.  V is kept in the element type (rounded once, after the
 // scale): it is an operand of the second product, which takes 16 bits.
 #include <algorithm>
+#include <type_traits>
 
 #include "elem16.cuh"
 #include "internal.h"
@@ -101,18 +102,21 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
   return v;
 }
 
-// The sum, in the CTAs' order, of the floats at p in the n <= 8 CTAs of the cluster; all loads under way
-// at once (one after the other they took some 300 cycles each).
+// The sum, in the CTAs' order, of the floats at p in the n (2, 4 or 8) CTAs of the cluster; all
+// loads under way at once (one after the other they took some 300 cycles each).
 __device__ __forceinline__ float sum_cluster(const float* p, uint32_t n) {
-  float part[8];
+  const auto sum = [&](auto count) {
+    float part[decltype(count)::value];
 #pragma unroll
-  for (uint32_t c = 0; c < 8; ++c)
-    if (c < n) part[c] = ld_cluster(p, c);
-  float v = part[0];
+    for (uint32_t c = 0; c < decltype(count)::value; ++c) part[c] = ld_cluster(p, c);
+    float v = part[0];
 #pragma unroll
-  for (uint32_t c = 1; c < 8; ++c)
-    if (c < n) v += part[c];
-  return v;
+    for (uint32_t c = 1; c < decltype(count)::value; ++c) v += part[c];
+    return v;
+  };
+  if (n == 8) return sum(std::integral_constant<uint32_t, 8>{});
+  if (n == 4) return sum(std::integral_constant<uint32_t, 4>{});
+  return sum(std::integral_constant<uint32_t, 2>{});
 }
 
 // Steps of 32 of the contracted index that slice i of n takes.
@@ -203,9 +207,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
   const float s = __ldg(p.scales + a);
   for (int i = threadIdx.x * n + cluster_rank(); i < 16 * W; i += blockDim.x * n) {
     const int row = i / W, j = i % W;
-    if (!((rows >> row) & 1u) || j >= rank) continue;
-    const float v = n > 1 ? sum_cluster(red + i, n) : red[i];
-    V[static_cast<int64_t>(m0 + row) * p.r + j] = round1<F16>(v * s);
+    if (!((rows >> row) & 1u) || j >= p.r) continue;
+    float v = 0.f;                            // past the rank: the expand of many rows takes all r
+    if (j < rank) v = (n > 1 ? sum_cluster(red + i, n) : red[i]) * s;
+    V[static_cast<int64_t>(m0 + row) * p.r + j] = round1<F16>(v);
   }
   if (n > 1) cluster_sync();                  // the others have read this CTA's sums
 }
@@ -217,6 +222,44 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
 // same contraction on mma.sync, with A prefetched one step ahead, waited for L2 at every step.
 constexpr int kTileRows = 128, kTileStages = 3, kTilePass = 2;
 constexpr int kTileLd = 64 + 4;
+// The different adapters of 128 rows, in order of their first row.
+struct Found {
+  int lead[4][32], place[4][32], n_lead[4];    // a warp's leading rows: adapter, place in `id`
+  int id[kTileRows];
+  int n[4];
+  __device__ __forceinline__ int count() const { return n[0] + n[1] + n[2] + n[3]; }
+};
+// Fills `f`, and gives each row's place in it (-1: none).  All threads of the CTA; rw: 0 .. 3 for the
+// four warps that have a row a thread, else -1.  Within a warp by a match; then the leaders of warp rw
+// look for themselves among those of the warps before it.
+__device__ __forceinline__ int find_adapters(Found& f, int rw, int mine) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t lead = leaders(mine), same = __match_any_sync(0xffffffffu, mine);
+  const bool leads = rw >= 0 && ((lead >> lane) & 1u);
+  const int nth = __popc(lead & ((1u << lane) - 1));
+  if (leads) f.lead[rw][nth] = mine;
+  if (rw >= 0 && lane == 0) f.n_lead[rw] = __popc(lead);
+  __syncthreads();
+  int before = -1, place = -1;                 // 32 w + i: warp w's i-th leader has it already
+  if (leads)
+    for (int w = 0; w < rw && before < 0; ++w)
+      for (int i = 0; i < f.n_lead[w] && before < 0; ++i)
+        if (f.lead[w][i] == mine) before = 32 * w + i;
+  const uint32_t fresh = __ballot_sync(0xffffffffu, leads && before < 0);
+  if (rw >= 0 && lane == 0) f.n[rw] = __popc(fresh);
+  __syncthreads();
+  if ((fresh >> lane) & 1u) {
+    place = __popc(fresh & ((1u << lane) - 1));
+    for (int w = 0; w < rw; ++w) place += f.n[w];
+    f.id[place] = mine;
+  }
+  if (leads) f.place[rw][nth] = place;
+  __syncthreads();
+  if (before >= 0) place = f.place[before >> 5][before & 31];
+  place = __shfl_sync(0xffffffffu, place, __ffs(same) - 1);
+  return mine < 0 ? -1 : place;
+}
+
 struct TileSmem {
   union {
     struct {
@@ -226,9 +269,7 @@ struct TileSmem {
     float red[kTileRows * kTileLd];            // after the last product
   };
   uint64_t full[kTileStages], empty[kTileStages], acc_full[2], acc_empty[2], drain;
-  int lead[4][32], place[4][32], n_lead[4];    // a warp's leading rows: adapter, place in `found`
-  int found[kTileRows];                        // the different adapters, in order of their first row
-  int n_found[4];
+  Found who;
   uint32_t tmem_base;
 };
 
@@ -253,40 +294,10 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
   const int m0 = blockIdx.y * kTileRows, j0 = blockIdx.z * 64;
   const int row = (warp & 3) * 32 + lane;      // warps 2 .. 5: a row a thread, its tensor-memory lane
   const int mine = warp >= 2 ? row_adapter(p, m0 + row) : -1;
-  // The different adapters in order of their first row: within a warp by a match, then the leaders of
-  // warp w look for themselves among those of the warps before it.
-  int place = -1;                              // of this row's adapter in `found`
-  {
-    const uint32_t lead = leaders(mine), same = __match_any_sync(0xffffffffu, mine);
-    const bool leads = (lead >> lane) & 1u;
-    const int nth = __popc(lead & ((1u << lane) - 1));
-    if (warp >= 2) {
-      if (leads) sm.lead[warp & 3][nth] = mine;
-      if (lane == 0) sm.n_lead[warp & 3] = __popc(lead);
-    }
-    __syncthreads();
-    int before = -1;                           // 32 w + i: warp w's i-th leader has it already
-    if (warp >= 2 && leads)
-      for (int w = 0; w < (warp & 3) && before < 0; ++w)
-        for (int i = 0; i < sm.n_lead[w] && before < 0; ++i)
-          if (sm.lead[w][i] == mine) before = 32 * w + i;
-    const uint32_t fresh = __ballot_sync(0xffffffffu, leads && before < 0);
-    if (warp >= 2 && lane == 0) sm.n_found[warp & 3] = __popc(fresh);
-    __syncthreads();
-    if ((fresh >> lane) & 1u) {
-      place = __popc(fresh & ((1u << lane) - 1));
-      for (int w = 0; w < (warp & 3); ++w) place += sm.n_found[w];
-      sm.found[place] = mine;
-    }
-    if (warp >= 2 && leads) sm.place[warp & 3][nth] = place;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (before >= 0) place = sm.place[before >> 5][before & 31];
-    place = __shfl_sync(0xffffffffu, place, __ffs(same) - 1);
-    if (mine < 0) place = -1;
-  }
-  const int found = sm.n_found[0] + sm.n_found[1] + sm.n_found[2] + sm.n_found[3];
+  tc_fence_before();
+  const int place = find_adapters(sm.who, warp >= 2 ? warp & 3 : -1, mine);
+  tc_fence_after();
+  const int found = sm.who.count();
   const int passes = (found + kTilePass - 1) / kTilePass;
   int lo, hi;
   slice((p.K + 63) / 64, blockIdx.x, gridDim.x, lo, hi);
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
           mbar_arrive_expect_tx(&sm.full[st], kTileRows * 128 + n * box_ranks * 128);
           tma_load_2d(sm.ring.x[st], &tx, s * 64, m0, &sm.full[st], passes > 1 ? keep : once);
           for (int d = 0; d < n; ++d)
-            tma_load_2d(sm.ring.a[st][d], &ta, s * 64, sm.found[ps * kTilePass + d] * p.r + j0, &sm.full[st], keep);
+            tma_load_2d(sm.ring.a[st][d], &ta, s * 64, sm.who.id[ps * kTilePass + d] * p.r + j0, &sm.full[st], keep);
         }
         __syncwarp();
       }
@@ -391,9 +402,10 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
     const float s = __ldg(p.scales + a);
     const int rank = adapter_rank(p, a) - j0;
     const float* src = sm.red + r * kTileLd + 2 * lane;
-    const float2 v = n > 1 ? make_float2(sum_cluster(src, n), sum_cluster(src + 1, n)) : make_float2(src[0], src[1]);
-    if (2 * lane < rank)
-      *reinterpret_cast<uint32_t*>(V + static_cast<int64_t>(m) * p.r + j0 + 2 * lane) = pack2<F16>(v.x * s, v.y * s);
+    float2 v = n > 1 ? make_float2(sum_cluster(src, n), sum_cluster(src + 1, n)) : make_float2(src[0], src[1]);
+    v = 2 * lane < rank ? make_float2(v.x * s, v.y * s) : make_float2(0.f, 0.f);
+    if (2 * lane < p.r - j0)
+      *reinterpret_cast<uint32_t*>(V + static_cast<int64_t>(m) * p.r + j0 + 2 * lane) = pack2<F16>(v.x, v.y);
   }
   if (n > 1) cluster_sync();                   // the others have read this CTA's sums
 }
@@ -565,112 +577,191 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
 }
 constexpr size_t kExpandSmem = static_cast<size_t>(kBQueue * 4 + kBaseQueue * 2) * 256 * 16;
 
-// The expand of many rows: a warp has 32 rows (so that each B it loads serves two products) and
-// walks over `span` column tiles of 32, the next step's B in registers (from L1: the CTA's 8 warps
-// read the same columns) and the next tiles' base in a queue in shared memory.
-constexpr int kRunQueue = 5;
-template <bool F16, int CH>
-__global__ void __launch_bounds__(256) k_lora_expand_run(const LoraArgs p, const uint16_t* V, int span) {
-  extern __shared__ __align__(16) uint8_t run_smem[];
-  uint4* baseq = reinterpret_cast<uint4*>(run_smem) + threadIdx.x;              // [tile][4][256]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int m0 = (blockIdx.y * 8 + warp) * 32;
-  const int ct0 = blockIdx.x * span, ct1 = min(ct0 + span, p.N / kCols + (p.N % kCols ? 1 : 0));
-  pdl_launch_dependents();
-  if (m0 >= p.M) return;                       // whole warps
-  const int mine = row_adapter(p, m0 + lane);
-  const int my_rank = mine >= 0 ? adapter_rank(p, mine) : 0;
-  const uint32_t list = leaders(mine);
-  int id[4], ranks[4];                         // of rows g, g + 8, g + 16, g + 24
-#pragma unroll
-  for (int i = 0; i < 4; ++i) id[i] = __shfl_sync(0xffffffffu, mine, 8 * i + g), ranks[i] = __shfl_sync(0xffffffffu, my_rank, 8 * i + g);
-  const auto load_b = [&](uint4 (&b)[4], int lead, int ch, int ct) {
-    const int a = __shfl_sync(0xffffffffu, mine, lead), rank = __shfl_sync(0xffffffffu, my_rank, lead);
-    const int k = 32 * ch + 8 * q, n0 = ct * kCols + 8 * (g >> 1) + (g & 1);
-    const uint16_t* src = p.B + (static_cast<int64_t>(a) * p.N + n0) * p.r + k;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      b[t] = make_uint4(0, 0, 0, 0);
-      if (k < rank && n0 + 2 * t < p.N) b[t] = ld_shared_operand(src + 2 * t * p.r);
-    }
-  };
-  const uint16_t* base0 = p.base + static_cast<int64_t>(m0 + g) * p.N + 8 * q;
-  const auto fetch_base = [&](int ct, int at) {
-    const bool in = ct < ct1 && ct * kCols + 8 * q < p.N;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool on = in && m0 + 8 * i + g < p.M;
-      copy16(baseq + (at * 4 + i) * 256, on ? base0 + static_cast<int64_t>(8 * i) * p.N + ct * kCols : p.base, on);
-    }
-    copy_commit();
-  };
-  uint4 b[4];
-  if (list) load_b(b, __ffs(list) - 1, 0, ct0);
-  pdl_wait();
-#pragma unroll
-  for (int i = 0; i < kRunQueue - 1; ++i) fetch_base(ct0 + i, i);
-  uint4 v[CH][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int ch = 0; ch < CH; ++ch) {
-      v[ch][i] = make_uint4(0, 0, 0, 0);
-      if (32 * ch + 8 * q < ranks[i])
-        v[ch][i] = __ldcg(reinterpret_cast<const uint4*>(V + static_cast<int64_t>(m0 + 8 * i + g) * p.r + 32 * ch + 8 * q));
-    }
-  int at = 0;
-#pragma unroll 1
-  for (int ct = ct0; ct < ct1; ++ct) {
-    fetch_base(ct + kRunQueue - 1, at == 0 ? kRunQueue - 1 : at - 1);
-    float acc[2][4][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[h][t][e] = 0.f;
-#pragma unroll 1
-    for (uint32_t todo = list; todo;) {
-      const int lead = __ffs(todo) - 1, a = __shfl_sync(0xffffffffu, mine, lead);
-      todo &= todo - 1;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int ch = 0; ch < CH; ++ch) {
-        uint4 nb[4];                           // the next chunk, adapter or tile
-        if (ch + 1 < CH) load_b(nb, lead, ch + 1, ct);
-        else load_b(nb, todo ? __ffs(todo) - 1 : __ffs(list) - 1, 0, todo ? ct : min(ct + 1, ct1 - 1));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 x0 = id[2 * h] == a ? v[ch][2 * h] : zero, x1 = id[2 * h + 1] == a ? v[ch][2 * h + 1] : zero;
-#pragma unroll
-          for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[h][t], x0, x1, b[t]);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) b[t] = nb[t];
-      }
-    }
-    copy_wait<kRunQueue - 1>();
-    const int n = ct * kCols + 8 * q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = m0 + 8 * i + g;
-      const uint4 y = baseq[(at * 4 + i) * 256];
-      uint32_t w[4] = {y.x, y.y, y.z, y.w};
-      if (id[i] >= 0) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float2 f = unpack2<F16>(w[t]);
-          w[t] = pack2<F16>(f.x + acc[i >> 1][t][2 * (i & 1)], f.y + acc[i >> 1][t][2 * (i & 1) + 1]);
-        }
-      }
-      if (m < p.M && n < p.N)
-        *reinterpret_cast<uint4*>(p.Y + static_cast<int64_t>(m) * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    at = at + 1 == kRunQueue ? 0 : at + 1;
+// The expand of many rows: a CTA has 128 rows and walks over `span` tiles of 64 columns on the tensor
+// cores.  acc = V [128 rows, r] B^T [r, 64 columns], one accumulator in tensor memory for each adapter that
+// occurs in the rows, two adapters a pass; base, by TMA, is added to in its place in shared memory and
+// stored from there by TMA.  Warps 0 .. 3 have a row a thread, the others copy base, issue the products
+// and copy B.  Four tiles of base and two CTAs an SM keep some 100 KB under way.
+constexpr int kExCols = 64, kExBase = 4, kExB = 3;
+template <int CR>                              // chunks of 64 ranks
+struct ExpandSmem {
+  uint8_t base[kExBase][kTileRows * 128];
+  uint8_t v[CR][kTileRows * 128];
+  uint8_t b[kExB][CR][kExCols * 128];
+  uint64_t base_full[kExBase], base_empty[kExBase], b_full[kExB], b_empty[kExB], v_full, acc_full[2], acc_empty[2], drain;
+  Found who;
+  uint32_t tmem_base;
+};
+
+template <bool F16, int CR>
+__global__ void __launch_bounds__(224) k_lora_expand_tile(const __grid_constant__ CUtensorMap tbase, const __grid_constant__ CUtensorMap ty,
+                                                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb,
+                                                          const LoraArgs p, int span, int base_ready) {
+  using S = ExpandSmem<CR>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw + smem_align_pad(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kExBase; ++i) mbar_init(&sm.base_full[i], 1), mbar_init(&sm.base_empty[i], 1);
+    for (int i = 0; i < kExB; ++i) mbar_init(&sm.b_full[i], 1), mbar_init(&sm.b_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.acc_full[i], 1), mbar_init(&sm.acc_empty[i], 4);
+    mbar_init(&sm.v_full, 1), mbar_init(&sm.drain, 1);
+    fence_barrier_init();
   }
-  copy_wait<0>();
+  if (warp == 5) {
+    tmem_alloc(&sm.tmem_base, 256);            // two sets of two accumulators of 64 columns
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  const int m0 = blockIdx.y * kTileRows, row = threadIdx.x;
+  const int ct0 = blockIdx.x * span, tiles = min(span, (p.N + kExCols - 1) / kExCols - ct0);
+  // adapter and ranks are the caller's: the shrink, this kernel's predecessor, has waited for them
+  const int mine = warp < 4 ? row_adapter(p, m0 + row) : -1;
+  tc_fence_before();
+  const int place = find_adapters(sm.who, warp < 4 ? warp : -1, mine);
+  tc_fence_after();
+  const int found = sm.who.count(), passes = (found + kTilePass - 1) / kTilePass;
+  const uint32_t tmem = sm.tmem_base;
+  bool ok = true;
+  const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
+    return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, &g_lora_err, code));
+  };
+  if (warp == 4) {
+    // -------------------------------------------------------------------- base
+    if (!base_ready) pdl_wait();
+    const uint64_t once = l2_policy_evict_normal();
+    int i = 0;
+    for (; i < tiles; ++i) {
+      const int s = i % kExBase;
+      if (!wait(&sm.base_empty[s], ((i / kExBase) & 1) ^ 1, kErrWaitEmpty)) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sm.base_full[s], kTileRows * 128);
+        tma_load_2d(sm.base[s], &tbase, (ct0 + i) * kExCols, m0, &sm.base_full[s], once);
+      }
+      __syncwarp();
+    }
+    // every copy has landed before the memory goes
+    const int issued = i;
+    for (i = max(issued - kExBase, 0); i < issued; ++i) wait(&sm.base_full[i % kExBase], (i / kExBase) & 1, kErrDrain);
+  } else if (warp == 6) {
+    // -------------------------------------------------------------------- B
+    const uint64_t keep = l2_policy_evict_last();
+    int ord = 0;
+    for (int i = 0; i < tiles && ok; ++i)
+      for (int d = 0; d < found; ++d, ++ord) {
+        const int s = ord % kExB;
+        ok = wait(&sm.b_empty[s], ((ord / kExB) & 1) ^ 1, kErrWaitEmpty);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&sm.b_full[s], CR * kExCols * 128);
+#pragma unroll
+          for (int c = 0; c < CR; ++c)
+            tma_load_4d(sm.b[s][c], &tb, 64 * c, (ct0 + i) * kExCols, sm.who.id[d], 0, &sm.b_full[s], keep);
+        }
+        __syncwarp();
+      }
+    for (int i = max(ord - kExB, 0); i < ord; ++i) wait(&sm.b_full[i % kExB], (i / kExB) & 1, kErrDrain);
+  } else if (warp == 5) {
+    // -------------------------------------------------------------------- V, products
+    pdl_wait();
+    if (found) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sm.v_full, CR * kTileRows * 128);
+#pragma unroll
+        for (int c = 0; c < CR; ++c) tma_load_2d(sm.v[c], &tv, 64 * c, m0, &sm.v_full, l2_policy_evict_first());
+      }
+      __syncwarp();
+      ok = wait(&sm.v_full, 0, kErrWaitFull);
+    }
+    constexpr uint32_t fmt = F16 ? 0u : 1u;
+    constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kExCols >> 3) << 17) | ((kTileRows >> 4) << 24);
+    const int steps = (p.r + 15) / 16;         // past r both operands are filled with zeros
+    uint32_t ord = 0, cnt = 0;
+    for (int i = 0; i < tiles && ok; ++i)
+      for (int ps = 0; ps < passes && ok; ++ps, ++cnt) {
+        const int n = min(kTilePass, found - ps * kTilePass), set = cnt & 1;
+        ok = wait(&sm.acc_empty[set], ((cnt >> 1) & 1) ^ 1, kErrWaitAccum);
+        for (int d = 0; d < n && ok; ++d, ++ord) {
+          const int s = ord % kExB;
+          ok = wait(&sm.b_full[s], (ord / kExB) & 1, kErrWaitFull);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            for (int k = 0; k < steps; ++k)
+              tc_mma_ss_f16(tmem + 128 * set + 64 * d, smem_desc_sw128(smem_u32(sm.v[k >> 2])) + 2 * (k & 3),
+                            smem_desc_sw128(smem_u32(sm.b[s][k >> 2])) + 2 * (k & 3), idesc, k ? 1u : 0u);
+            tc_commit(&sm.b_empty[s]);
+          }
+          __syncwarp();
+        }
+        if (ok && elect_one()) tc_commit(&sm.acc_full[set]);
+        __syncwarp();
+      }
+    if (elect_one()) tc_commit(&sm.drain);     // nothing under way any more, whatever happened
+    wait(&sm.drain, 0, kErrDrain);
+  } else {
+    // -------------------------------------------------------------------- base + acc, a row a thread
+    // After a wait that ran out the loop goes on without waiting, so that the four warps still meet.
+    uint32_t cnt = 0;
+    for (int i = 0; i < tiles; ++i) {
+      const int s = i % kExBase;
+      uint32_t acc[64];
+      for (int ps = 0; ps < passes; ++ps, ++cnt) {
+        const int n = min(kTilePass, found - ps * kTilePass), set = cnt & 1;
+        if (ok) ok = wait(&sm.acc_full[set], (cnt >> 1) & 1, kErrWaitAccum);
+        tc_fence_after();
+        for (int d = 0; d < n; ++d) {
+          const bool own = place == ps * kTilePass + d;
+          if (!__any_sync(0xffffffffu, own)) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+            tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + 128 * set + 64 * d + 32 * h, v);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (own) acc[32 * h + e] = v[e];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.acc_empty[set]);
+      }
+      if (ok) ok = wait(&sm.base_full[s], (i / kExBase) & 1, kErrWaitFull);
+      if (place >= 0) {                        // the others keep their base, bit for bit
+        uint8_t* at = sm.base[s] + row * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint4* q = reinterpret_cast<uint4*>(at + ((c ^ (row & 7)) << 4));
+          const uint4 y = *q;
+          uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const float2 f = unpack2<F16>(w[t]);
+            w[t] = pack2<F16>(f.x + __uint_as_float(acc[8 * c + 2 * t]), f.y + __uint_as_float(acc[8 * c + 2 * t + 1]));
+          }
+          *q = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(1, 128);
+      if (warp == 0 && elect_one()) {
+        if (ok) tma_store_2d(&ty, sm.base[s], (ct0 + i) * kExCols, m0);
+        bulk_commit();
+        bulk_wait_read<1>();                   // the tile before has left its slot
+        if (i > 0) mbar_arrive(&sm.base_empty[(i - 1) % kExBase]);
+      }
+      __syncwarp();
+    }
+    if (warp == 0 && elect_one()) bulk_wait<0>();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
 }
-constexpr size_t kRunSmem = static_cast<size_t>(kRunQueue) * 4 * 256 * 16;
 
 // Launch with programmatic serialization, and clusters of `cluster` CTAs along x.
 template <typename... P, typename... A>
@@ -693,10 +784,13 @@ cudaError_t launch_cluster(void (*kern)(P...), dim3 grid, unsigned threads, size
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Up to this many rows a cluster for each leading row; above, for each 128 rows.
-constexpr int kRowsMax = 1024;
-// From this many rows on the expand walks over column tiles.
-constexpr int kRunRows = 256;
+// Up to this many rows the kernels on mma.sync, by the adapters that lead in each 16 rows; above, those
+// on tcgen05, by 128 rows.  K 4096, N 4096 or 8192, in us, mma.sync / tcgen05:
+//   shrink (with the same expand): 512 rows of 8 adapters 16.6 / 18.2, 1024 rows 26.6 / 22.6, 1024 rows
+//     of rank 64 28.4 / 19.8; 512 rows that are each another's adapter of 48 85 / 115, 1024 rows 158 / 161
+//   expand (with the same shrink): 257 rows 12.1 / 13.1, 512 rows 16.3 / 16.6, 1024 rows 26.9 / 26.6,
+//     2048 rows of rank 64 29.2 / 22.1, 4001 rows 67 / 43; 2048 rows interleaved over 64 adapters 163 / 194
+constexpr int kFewRows = 512;
 
 template <bool F16, int NT>
 cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
@@ -714,7 +808,7 @@ cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
 
 template <bool F16>
 cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
-  if (a.M <= kRowsMax) {
+  if (a.M <= kFewRows) {
     if (a.r <= 32) return launch_rows<F16, 4>(a, V, stream);
     if (a.r <= 64) return launch_rows<F16, 8>(a, V, stream);
     return launch_rows<F16, 16>(a, V, stream);
@@ -737,29 +831,39 @@ cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
 }
 
 template <bool F16>
-cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, cudaStream_t stream) {
+cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cudaStream_t stream) {
   const int64_t blocks = (a.M + 15) / 16, cols = (a.N + kCols - 1) / kCols;
   const int sms = device_sm_count();
   int ls = 0, lr = 0;
   int64_t span = 1;
-  if (a.M > kRunRows && a.N % 8 == 0) {
-    // rows of one request are neighbours: few adapters a block.  One wave of two CTAs an SM.
-    const int64_t row_ctas = (a.M + 255) / 256, across = std::max<int64_t>(1, 2 * sms / row_ctas);
-    span = std::max<int64_t>(4, (cols + across - 1) / across);
-    const dim3 grid(static_cast<unsigned>((cols + span - 1) / span), static_cast<unsigned>(row_ctas));
-    const auto launch = [&](void (*kern)(LoraArgs, const uint16_t*, int)) {
-      const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(kern), kRunSmem);
-      if (e != cudaSuccess) return e;
-      return launch_pdl(kern, grid, 256, kRunSmem, stream, a, V, static_cast<int>(span));
+  if (a.M > kFewRows && a.N % 8 == 0) {
+    // one wave: two CTAs an SM, with more than 64 ranks one
+    const int64_t row_ctas = (a.M + kTileRows - 1) / kTileRows, tiles = (a.N + kExCols - 1) / kExCols;
+    const int64_t across = std::max<int64_t>(1, (a.r <= 64 ? 2 : 1) * sms / row_ctas);
+    span = (tiles + across - 1) / across;
+    const dim3 grid(static_cast<unsigned>((tiles + span - 1) / span), static_cast<unsigned>(row_ctas));
+    const CUtensorMapDataType dt = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t n = a.N, r = a.r;
+    CUtensorMap tbase, ty, tv, tb;
+    cudaError_t e = make_tmap_2d(&tbase, dt, a.base, n, a.M, n * 2, kExCols, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (e == cudaSuccess) e = make_tmap_2d(&ty, dt, a.Y, n, a.M, n * 2, kExCols, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+    if (e == cudaSuccess) e = make_tmap_2d(&tv, dt, V, r, a.M, r * 2, 64, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    const uint64_t bd[4] = {r, n, static_cast<uint64_t>(a.L), 1}, bs[3] = {r * 2, n * r * 2, n * r * 2 * a.L};
+    const uint32_t bb[4] = {64, kExCols, 1, 1};
+    if (e == cudaSuccess) e = make_tmap_4d(&tb, dt, a.B, bd, bs, bb, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    if (e != cudaSuccess) return e;
+    const auto launch = [&](auto kern, size_t smem) {
+      const cudaError_t se = set_smem_attr_once(reinterpret_cast<const void*>(kern), smem);
+      if (se != cudaSuccess) return se;
+      return launch_pdl(kern, grid, 224, smem, stream, tbase, ty, tv, tb, a, static_cast<int>(span), base_ready ? 1 : 0);
     };
-    if (a.r <= 32) return launch(k_lora_expand_run<F16, 1>);
-    if (a.r <= 64) return launch(k_lora_expand_run<F16, 2>);
-    return launch(k_lora_expand_run<F16, 4>);
+    if (a.r <= 64) return launch(k_lora_expand_tile<F16, 1>, sizeof(ExpandSmem<1>) + 1024);
+    return launch(k_lora_expand_tile<F16, 2>, sizeof(ExpandSmem<2>) + 1024);
   }
   // Subsets of the adapters, up to those that a block can hold, while there are few warps for the
-  // SMs (many rows: rows of one request are neighbours, no subsets).  Row blocks: as many as there
-  // are.  8 warps a CTA, and column tiles enough for one wave of two CTAs an SM.
-  const int most = a.M > kRunRows ? 1 : std::min(std::min(a.M, 16), a.L);
+  // SMs.  Row blocks: as many as there are.  8 warps a CTA, and column tiles enough for one wave of two
+  // CTAs an SM.
+  const int most = std::min(std::min(a.M, 16), a.L);
   while (ls < 3 && (1 << ls) < most && (blocks * cols << ls) < 24ll * sms) ++ls;
   while (lr + ls < 3 && (1 << lr) < blocks) ++lr;
   span = std::min<int64_t>(8, std::max<int64_t>(1, ((blocks * cols << ls) + 16 * sms - 1) / (16 * sms)));
@@ -788,9 +892,9 @@ cudaError_t launch_lora_shrink(int dtype, const LoraArgs& a, void* scratch, cuda
   return dtype == kF16 ? shrink_t<true>(a, V, stream) : shrink_t<false>(a, V, stream);
 }
 
-cudaError_t launch_lora_expand(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream) {
+cudaError_t launch_lora_expand(int dtype, const LoraArgs& a, void* scratch, bool base_ready, cudaStream_t stream) {
   const uint16_t* V = static_cast<const uint16_t*>(scratch);
-  return dtype == kF16 ? expand_t<true>(a, V, stream) : expand_t<false>(a, V, stream);
+  return dtype == kF16 ? expand_t<true>(a, V, base_ready, stream) : expand_t<false>(a, V, base_ready, stream);
 }
 
 }  // namespace wq
