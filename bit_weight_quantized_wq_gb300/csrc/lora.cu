@@ -459,18 +459,30 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
     s.todo &= s.todo - 1;
     if (!s.todo) s.todo = list, ++s.ct;
   };
+  // The walk of the copies costs as much as the products: a row's lane keeps where its adapter's B
+  // begins, a lane where its four columns are in the tile.
   Step fs{ct0, 0, list};
   int f_at = 0;
+  const int64_t b_of = mine >= 0 ? static_cast<int64_t>(mine) * p.N * p.r : 0;
+  const int c_lane = 8 * (g >> 1) + (g & 1), r2 = 2 * p.r;
   const auto fetch_b = [&] {
     if (fs.ct < ct1 && list) {
       const int i = __ffs(fs.todo) - 1;
-      const int a = __shfl_sync(0xffffffffu, mine, i), rank = __shfl_sync(0xffffffffu, my_rank, i);
-      const int k = 32 * fs.ch + 8 * q, n = fs.ct * kCols + 8 * (g >> 1) + (g & 1);
-      const uint16_t* src = p.B + (static_cast<int64_t>(a) * p.N + n) * p.r + k;
+      const int rank = __shfl_sync(0xffffffffu, my_rank, i);
+      const int64_t of = __shfl_sync(0xffffffffu, b_of, i);
+      const int k = 32 * fs.ch + 8 * q, n = fs.ct * kCols + c_lane;
+      const uint16_t* src = p.B + of + (static_cast<int64_t>(n) * p.r + k);
+      uint4* dst = bq + f_at * (4 * 256);
+      const bool in = k < rank;
+      if ((fs.ct + 1) * kCols <= p.N) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const bool on = k < rank && n + 2 * t < p.N;
-        copy16(bq + (f_at * 4 + t) * 256, on ? src + static_cast<int64_t>(2 * t) * p.r : p.B, on);
+        for (int t = 0; t < 4; ++t) copy16(dst + t * 256, in ? src + t * r2 : p.B, in);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const bool on = in && n + 2 * t < p.N;
+          copy16(dst + t * 256, on ? src + t * r2 : p.B, on);
+        }
       }
       next_step(fs);
       f_at = f_at + 1 == kBQueue ? 0 : f_at + 1;
