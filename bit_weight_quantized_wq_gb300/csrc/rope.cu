@@ -264,8 +264,11 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t stream) {
   static_assert(kRopeThreads == kWalkThreads, "both take the same heads a pass");
   const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv, passes = (rows + HPB - 1) / HPB;
   const int fill = kWalkCtas * device_sm_count();
-  // from about eight units a CTA on the walk's set-up pays
-  if (static_cast<int64_t>(a.T) * passes < 4ll * fill) return launch_pdl(k_qk_norm_rope<F16, D>, dim3(a.T, passes), kRopeThreads, 0, stream, a);
+  // From eight units a CTA on the walk's set-up pays.  Without / with it, in us: 40 heads of 128, 1024
+  // tokens (3 units a CTA) 6.3 / 7.4, 2047 (7) 11.2 / 11.5, 4096 (13) 24.6 / 22.5; 80 heads, 1024 tokens (6)
+  // 9.1 / 9.5, 2047 (11) 19.0 / 18.1, 4096 (22) 38.1 / 33.8; 48 heads of 64, 2047 tokens (4) 7.0 / 8.1, 4096 (9)
+  // 13.1 / 13.1.
+  if (static_cast<int64_t>(a.T) * passes < 8ll * fill) return launch_pdl(k_qk_norm_rope<F16, D>, dim3(a.T, passes), kRopeThreads, 0, stream, a);
   return launch_pdl(k_qk_norm_rope_walk<F16, D>, dim3(fill), kWalkThreads, 0, stream, a, passes);
 }
 
