@@ -591,71 +591,120 @@ constexpr size_t kExpandSmem = static_cast<size_t>(kBQueue * 4 + kBaseQueue * 2)
 
 // The expand of many rows: a CTA has 128 rows and walks over `span` tiles of 64 columns on the tensor
 // cores.  acc = V [128 rows, r] B^T [r, 64 columns], one accumulator in tensor memory for each adapter that
-// occurs in the rows, two adapters a pass; base, by TMA, is added to in its place in shared memory and
-// stored from there by TMA.  Warps 0 .. 3 have a row a thread, the others copy base, issue the products
-// and copy B.  Four tiles of base and two CTAs an SM keep some 100 KB under way.
+// occurs in the rows; base comes by TMA, is added to in its place in shared memory and
+// leaves from there by TMA.  Two groups of four warps (a row a thread) take the tiles in turn, each with
+// two accumulators of its own; the other warps move base and Y, issue the products, and copy B.  Two CTAs
+// an SM (one with more than 64 ranks).
 constexpr int kExCols = 64, kExBase = 4, kExB = 3;
+constexpr int kExThreads = 352, kExWBase = 8, kExWMma = 9;   // warps 0 .. 7 add; 10: B
 template <int CR>                              // chunks of 64 ranks
 struct ExpandSmem {
   uint8_t base[kExBase][kTileRows * 128];
   uint8_t v[CR][kTileRows * 128];
   uint8_t b[kExB][CR][kExCols * 128];
-  uint64_t base_full[kExBase], base_empty[kExBase], b_full[kExB], b_empty[kExB], v_full, acc_full[2], acc_empty[2], drain;
+  uint64_t base_full[kExBase], added[kExBase], b_full[kExB], b_empty[kExB], v_full, acc_full[2][2], acc_empty[2][2], drain;
   Found who;
+  int place[kTileRows];                        // of each row's adapter in `who`
   uint32_t tmem_base;
 };
 
 template <bool F16, int CR>
-__global__ void __launch_bounds__(224) k_lora_expand_tile(const __grid_constant__ CUtensorMap tbase, const __grid_constant__ CUtensorMap ty,
-                                                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb,
-                                                          const LoraArgs p, int span, int base_ready) {
+__global__ void __launch_bounds__(kExThreads, CR == 1 ? 2 : 1)
+    k_lora_expand_tile(const __grid_constant__ CUtensorMap tbase, const __grid_constant__ CUtensorMap ty,
+                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb, const LoraArgs p, int span,
+                       int base_ready) {
   using S = ExpandSmem<CR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + smem_align_pad(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kExBase; ++i) mbar_init(&sm.base_full[i], 1), mbar_init(&sm.base_empty[i], 1);
+    for (int i = 0; i < kExBase; ++i) mbar_init(&sm.base_full[i], 1), mbar_init(&sm.added[i], 4);
     for (int i = 0; i < kExB; ++i) mbar_init(&sm.b_full[i], 1), mbar_init(&sm.b_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.acc_full[i], 1), mbar_init(&sm.acc_empty[i], 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.acc_full[i >> 1][i & 1], 1), mbar_init(&sm.acc_empty[i >> 1][i & 1], 4);
     mbar_init(&sm.v_full, 1), mbar_init(&sm.drain, 1);
     fence_barrier_init();
   }
-  if (warp == 5) {
-    tmem_alloc(&sm.tmem_base, 256);            // two sets of two accumulators of 64 columns
+  if (warp == kExWMma) {
+    tmem_alloc(&sm.tmem_base, 256);            // two accumulators of 64 columns a group
     tmem_relinquish();
   }
   pdl_launch_dependents();
-  const int m0 = blockIdx.y * kTileRows, row = threadIdx.x;
+  const int m0 = blockIdx.y * kTileRows, row = threadIdx.x & (kTileRows - 1);
   const int ct0 = blockIdx.x * span, tiles = min(span, (p.N + kExCols - 1) / kExCols - ct0);
   // adapter and ranks are the caller's: the shrink, this kernel's predecessor, has waited for them
   const int mine = warp < 4 ? row_adapter(p, m0 + row) : -1;
+  int place = find_adapters(sm.who, warp < 4 ? warp : -1, mine);
+  if (warp < 4) sm.place[row] = place;
   tc_fence_before();
-  const int place = find_adapters(sm.who, warp < 4 ? warp : -1, mine);
+  __syncthreads();
   tc_fence_after();
-  const int found = sm.who.count(), passes = (found + kTilePass - 1) / kTilePass;
+  const int found = sm.who.count();
   const uint32_t tmem = sm.tmem_base;
   bool ok = true;
   const auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t code) {
     return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, &g_lora_err, code));
   };
-  if (warp == 4) {
-    // -------------------------------------------------------------------- base
+  if (warp == kExWBase) {
+    // -------------------------------------------------------------------- base in, Y out
     if (!base_ready) pdl_wait();
-    const uint64_t once = l2_policy_evict_normal();
-    int i = 0;
-    for (; i < tiles; ++i) {
-      const int s = i % kExBase;
-      if (!wait(&sm.base_empty[s], ((i / kExBase) & 1) ^ 1, kErrWaitEmpty)) break;
+    const uint64_t normal = l2_policy_evict_normal();
+    const auto load = [&](int i) {
+      mbar_arrive_expect_tx(&sm.base_full[i % kExBase], kTileRows * 128);
+      tma_load_2d(sm.base[i % kExBase], &tbase, (ct0 + i) * kExCols, m0, &sm.base_full[i % kExBase], normal);
+    };
+    int issued = min(tiles, kExBase);
+    if (elect_one())
+      for (int i = 0; i < issued; ++i) load(i);
+    __syncwarp();
+    for (int i = 0; i < tiles; ++i) {
+      if (!wait(&sm.added[i % kExBase], (i / kExBase) & 1, kErrWaitFull)) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&sm.base_full[s], kTileRows * 128);
-        tma_load_2d(sm.base[s], &tbase, (ct0 + i) * kExCols, m0, &sm.base_full[s], once);
+        tma_store_2d(&ty, sm.base[i % kExBase], (ct0 + i) * kExCols, m0);
+        bulk_commit();
+        bulk_wait_read<0>();                   // the tile has left its slot
+        if (issued < tiles) load(issued);
       }
       __syncwarp();
+      issued = min(issued + 1, tiles);
     }
+    if (elect_one()) bulk_wait<0>();
     // every copy has landed before the memory goes
-    const int issued = i;
-    for (i = max(issued - kExBase, 0); i < issued; ++i) wait(&sm.base_full[i % kExBase], (i / kExBase) & 1, kErrDrain);
-  } else if (warp == 6) {
+    for (int i = max(issued - kExBase, 0); i < issued; ++i) wait(&sm.base_full[i % kExBase], (i / kExBase) & 1, kErrDrain);
+  } else if (warp == kExWMma) {
+    // -------------------------------------------------------------------- V, products
+    pdl_wait();
+    if (found) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sm.v_full, CR * kTileRows * 128);
+#pragma unroll
+        for (int c = 0; c < CR; ++c) tma_load_2d(sm.v[c], &tv, 64 * c, m0, &sm.v_full, l2_policy_evict_first());
+      }
+      __syncwarp();
+      ok = wait(&sm.v_full, 0, kErrWaitFull);
+    }
+    constexpr uint32_t fmt = F16 ? 0u : 1u;
+    constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kExCols >> 3) << 17) | ((kTileRows >> 4) << 24);
+    const int steps = (p.r + 15) / 16;         // past r both operands are filled with zeros
+    uint32_t ord = 0;
+    for (int i = 0; i < tiles && ok; ++i)
+      for (int d = 0; d < found; ++d, ++ord) {
+        const int s = ord % kExB, grp = i & 1;
+        const uint32_t use = static_cast<uint32_t>(i >> 1) * found + d, buf = use & 1;   // of this group's
+        ok = wait(&sm.acc_empty[grp][buf], ((use >> 1) & 1) ^ 1, kErrWaitAccum) && wait(&sm.b_full[s], (ord / kExB) & 1, kErrWaitFull);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          for (int k = 0; k < steps; ++k)
+            tc_mma_ss_f16(tmem + 128 * grp + 64 * buf, smem_desc_sw128(smem_u32(sm.v[k >> 2])) + 2 * (k & 3),
+                          smem_desc_sw128(smem_u32(sm.b[s][k >> 2])) + 2 * (k & 3), idesc, k ? 1u : 0u);
+          tc_commit(&sm.b_empty[s]);
+          tc_commit(&sm.acc_full[grp][buf]);
+        }
+        __syncwarp();
+      }
+    if (elect_one()) tc_commit(&sm.drain);     // nothing under way any more, whatever happened
+    wait(&sm.drain, 0, kErrDrain);
+  } else if (warp > kExWMma) {
     // -------------------------------------------------------------------- B
     const uint64_t keep = l2_policy_evict_last();
     int ord = 0;
@@ -673,103 +722,56 @@ __global__ void __launch_bounds__(224) k_lora_expand_tile(const __grid_constant_
         __syncwarp();
       }
     for (int i = max(ord - kExB, 0); i < ord; ++i) wait(&sm.b_full[i % kExB], (i / kExB) & 1, kErrDrain);
-  } else if (warp == 5) {
-    // -------------------------------------------------------------------- V, products
-    pdl_wait();
-    if (found) {
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&sm.v_full, CR * kTileRows * 128);
-#pragma unroll
-        for (int c = 0; c < CR; ++c) tma_load_2d(sm.v[c], &tv, 64 * c, m0, &sm.v_full, l2_policy_evict_first());
-      }
-      __syncwarp();
-      ok = wait(&sm.v_full, 0, kErrWaitFull);
-    }
-    constexpr uint32_t fmt = F16 ? 0u : 1u;
-    constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kExCols >> 3) << 17) | ((kTileRows >> 4) << 24);
-    const int steps = (p.r + 15) / 16;         // past r both operands are filled with zeros
-    uint32_t ord = 0, cnt = 0;
-    for (int i = 0; i < tiles && ok; ++i)
-      for (int ps = 0; ps < passes && ok; ++ps, ++cnt) {
-        const int n = min(kTilePass, found - ps * kTilePass), set = cnt & 1;
-        ok = wait(&sm.acc_empty[set], ((cnt >> 1) & 1) ^ 1, kErrWaitAccum);
-        for (int d = 0; d < n && ok; ++d, ++ord) {
-          const int s = ord % kExB;
-          ok = wait(&sm.b_full[s], (ord / kExB) & 1, kErrWaitFull);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            for (int k = 0; k < steps; ++k)
-              tc_mma_ss_f16(tmem + 128 * set + 64 * d, smem_desc_sw128(smem_u32(sm.v[k >> 2])) + 2 * (k & 3),
-                            smem_desc_sw128(smem_u32(sm.b[s][k >> 2])) + 2 * (k & 3), idesc, k ? 1u : 0u);
-            tc_commit(&sm.b_empty[s]);
-          }
-          __syncwarp();
-        }
-        if (ok && elect_one()) tc_commit(&sm.acc_full[set]);
-        __syncwarp();
-      }
-    if (elect_one()) tc_commit(&sm.drain);     // nothing under way any more, whatever happened
-    wait(&sm.drain, 0, kErrDrain);
   } else {
     // -------------------------------------------------------------------- base + acc, a row a thread
-    // After a wait that ran out the loop goes on without waiting, so that the four warps still meet.
-    uint32_t cnt = 0;
-    for (int i = 0; i < tiles; ++i) {
+    const int group = warp >> 2;
+    place = sm.place[row];
+    uint32_t use = 0;
+    for (int i = group; i < tiles && ok; i += 2) {
       const int s = i % kExBase;
-      uint32_t acc[64];
-      for (int ps = 0; ps < passes; ++ps, ++cnt) {
-        const int n = min(kTilePass, found - ps * kTilePass), set = cnt & 1;
-        if (ok) ok = wait(&sm.acc_full[set], (cnt >> 1) & 1, kErrWaitAccum);
+      ok = wait(&sm.base_full[s], (i / kExBase) & 1, kErrWaitFull);
+      for (int d = 0; d < found; ++d, ++use) {
+        const uint32_t buf = use & 1;
+        ok = wait(&sm.acc_full[group][buf], (use >> 1) & 1, kErrWaitAccum);
+        if (!ok) break;
         tc_fence_after();
-        for (int d = 0; d < n; ++d) {
-          const bool own = place == ps * kTilePass + d;
-          if (!__any_sync(0xffffffffu, own)) continue;
+        const bool own = place == d;
+        if (__any_sync(0xffffffffu, own)) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t v[32];
-            tmem_ld32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + 128 * set + 64 * d + 32 * h, v);
+            tmem_ld32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 128 * group + 64 * buf + 32 * h, v);
             tc_wait_ld();
+            if (own) {                         // rows without an adapter keep their base, bit for bit
+              uint8_t* at = sm.base[s] + row * 128;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (own) acc[32 * h + e] = v[e];
+              for (int c = 0; c < 4; ++c) {
+                uint4* q = reinterpret_cast<uint4*>(at + (((4 * h + c) ^ (row & 7)) << 4));
+                const uint4 y = *q;
+                uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                  const float2 f = unpack2<F16>(w[t]);
+                  w[t] = pack2<F16>(f.x + __uint_as_float(v[8 * c + 2 * t]), f.y + __uint_as_float(v[8 * c + 2 * t + 1]));
+                }
+                *q = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.acc_empty[set]);
+        if (lane == 0) mbar_arrive(&sm.acc_empty[group][buf]);
       }
-      if (ok) ok = wait(&sm.base_full[s], (i / kExBase) & 1, kErrWaitFull);
-      if (place >= 0) {                        // the others keep their base, bit for bit
-        uint8_t* at = sm.base[s] + row * 128;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4* q = reinterpret_cast<uint4*>(at + ((c ^ (row & 7)) << 4));
-          const uint4 y = *q;
-          uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const float2 f = unpack2<F16>(w[t]);
-            w[t] = pack2<F16>(f.x + __uint_as_float(acc[8 * c + 2 * t]), f.y + __uint_as_float(acc[8 * c + 2 * t + 1]));
-          }
-          *q = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+      if (!ok) break;
       fence_proxy_async_smem();
-      named_bar_sync(1, 128);
-      if (warp == 0 && elect_one()) {
-        if (ok) tma_store_2d(&ty, sm.base[s], (ct0 + i) * kExCols, m0);
-        bulk_commit();
-        bulk_wait_read<1>();                   // the tile before has left its slot
-        if (i > 0) mbar_arrive(&sm.base_empty[(i - 1) % kExBase]);
-      }
       __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.added[s]);
     }
-    if (warp == 0 && elect_one()) bulk_wait<0>();
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kExWMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
@@ -867,7 +869,7 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
     const auto launch = [&](auto kern, size_t smem) {
       const cudaError_t se = set_smem_attr_once(reinterpret_cast<const void*>(kern), smem);
       if (se != cudaSuccess) return se;
-      return launch_pdl(kern, grid, 224, smem, stream, tbase, ty, tv, tb, a, static_cast<int>(span), base_ready ? 1 : 0);
+      return launch_pdl(kern, grid, kExThreads, smem, stream, tbase, ty, tv, tb, a, static_cast<int>(span), base_ready ? 1 : 0);
     };
     if (a.r <= 64) return launch(k_lora_expand_tile<F16, 1>, sizeof(ExpandSmem<1>) + 1024);
     return launch(k_lora_expand_tile<F16, 2>, sizeof(ExpandSmem<2>) + 1024);
