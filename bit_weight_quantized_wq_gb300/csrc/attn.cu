@@ -30,6 +30,15 @@
 // turns, and the tensor core idled.
 // The running maximum is only followed when it grows by more than 2^8 (the output in tensor memory
 // is then rescaled); until then P is at most 2^8, which float32 sums and 16-bit P carry as well.
+// S has one product of N = 64 a K16 step, which takes the time that reading Q from shared memory takes
+// (some 70 cycles), not the tensor core's 32: the tensor pipe bounds rows mode at about two thirds of its
+// rate.  2048 rows on 8 heads over 32768 keys: 234 us, 1174 TFLOP/s.  N = 128 (two key tiles) halves that time,
+// but needs both score buffers of a lane at once, and the lane then waits for its own products: 284 us;
+// with the pair's second P in shared memory, so that the wait ends when the scores are in registers, 298 us
+// (P V with both operands in shared memory and V transposed takes some 150 cycles a step).
+// Keys mode is bound by the bytes: 262144 keys, 8 rows on 8 heads, 164 us, 6.6 TB/s; 64 requests over 16384 keys
+// of their own 326 us, 6.6 TB/s.  Short calls are bound by the chain of dependent loads, waits and launches:
+// 2 requests over 500 + 40 keys 12.4 us, of which the second kernel some 4.
 // P is rounded to the cache's type for the second product (the tensor core takes both operands in
 // one type); the sum of P is kept unrounded in float32.
 #include <algorithm>
@@ -63,7 +72,10 @@ constexpr int kItems = 4;             // items the scheduler is ahead of the oth
 constexpr int kTmemCols = 512;        // two S of 64 columns a lane, then O of 128 a lane
 constexpr int kColO = 256;
 // Weights on the line, in units of about 200 SM cycles: a key tile in rows mode, in keys mode with
-// more than 32 rows (all softmax warps at work) and with up to 32; an item's own cost, alike.
+// more than 32 rows (all softmax warps at work) and with up to 32; an item's own cost, alike.  With all tiles
+// alike and items free: 128 requests, 64 heads, over 8192 + up to 2048 keys 142 us instead of 112; 48 requests
+// of up to 4 new tokens, heads of 64, 43 instead of 31; one weight up or down by 1 moves these by 1 to 5%
+// either way.
 constexpr int kWRows = 10, kWKeys = 8, kWFew = 5, kWItemRows = 20, kWItem = 16;
 constexpr long long kMaxLine = 1ll << 30;
 constexpr float kLazy = 8.f;          // rescale when the maximum grew by more than 2^8
@@ -155,7 +167,10 @@ __device__ __forceinline__ int row_tiles(const Params& p, int ntok) {
   return ntok <= 2 * p.tb ? (ntok > 0 ? 1 : 0) : ceil_div(ntok, 2 * p.tb);
 }
 __device__ __forceinline__ int tile_tokens(const Params& p, int ntok, int rt) { return min(2 * p.tb, ntok - rt * 2 * p.tb); }
-// Rows mode or keys mode of an item of so many tokens.
+// Rows mode or keys mode of an item of so many tokens.  More rows than a lane holds would read K and V
+// twice in keys mode.  Rows mode for one lane's rows leaves the other lane idle; rows / keys mode, heads
+// of 128, in us: 1 token of 32 heads on 8 over 32768 keys 40.1 / 35.4, 16 tokens of 64 heads 45.0 / 40.3, 32
+// requests over 8192 + up to 700 33.8 / 28.4, 64 requests over up to 4096 of their own 114.6 / 93.9.
 __host__ __device__ inline bool rows_mode(int tb, int tokens) { return tokens > tb; }
 __host__ __device__ inline int tile_weight(int tb, int G, int tokens) {
   return rows_mode(tb, tokens) ? kWRows : (tokens * G > 32 ? kWKeys : kWFew);
@@ -1042,7 +1057,9 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
     const int per = kJoinWarps / w;
     return launch_pdl(kern, dim3((blocks + per - 1) / per, a.Hkv, c), kJoinWarps * 32, w > 1 ? kJoinSmem<D> : 0, stream, p);
   };
-  // W C warps for each eight rows of a head, as long as they fit the SMs at once (32 an SM).
+  // W C warps for each eight rows of a head, as long as they fit the SMs at once (32 an SM).  One warp / this
+  // rule / always 8 C, in us: 2 requests over 8192 keys 38 / 18 / 18, 32 requests over 8192 + up to 700 51 / 28 /
+  // 28, 128 requests 66 / 58 / 64, 256 requests of 64 heads over 32768 + up to 1024 295 / 292 / 327.
   const long long warps = static_cast<long long>(blocks) * a.Hkv, fit = 32ll * l.ctas;
   constexpr int C = D == 128 ? 4 : 2;
   if (warps * 8 * C <= fit) return join(k_attn_join<F16, D, 8, C>, 8, C);

@@ -1,19 +1,27 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   Y[m] = base[m] + s[a] (X[m] A[a]^T) B[a]^T,   a = adapter[m];  a = -1: Y[m] = base[m].
 //
-// Two kernels: the shrink V = s X A^T [M, r], and the expand Y = base + V B^T.  Both are bound by
-// bytes (a decode batch by the adapters' A and B, a prefill batch by X, base and Y), so the
-// contractions run on mma.sync m16n8k16 straight from global memory into registers: no operand is
-// staged, every load is 16 bytes a lane.
+// Two kernels, the shrink V = s X A^T [M, r] and the expand Y = base + V B^T, each in a form for few rows and
+// one for many (many_rows, below).  All are bound by bytes: a decode batch by the adapters' A and B, a prefill
+// batch by X, base and Y.
+//
+// Few rows: mma.sync m16n8k16 with the operands straight from global memory (A, B of the shrink; the
+// expand's B through per-thread queues); every load is 16 bytes a lane.
 //   Both operands are contiguous along the contracted index.  A lane holds 8 neighbouring values of
 //   it (one load) and gives four to each of two products; which k a fragment slot stands for is
 //   free as long as both operands agree.
 //   Rows of different adapters share a 16-row block: for each adapter that occurs in it (the lowest
 //   of its rows leads), the products run with the rows of all others set to zero, into the same
 //   accumulators.
+// Many rows: tcgen05 with TMA on tiles of 128 rows, an accumulator for each adapter that occurs in them; each
+// row takes its own.
 // The sum over K is split over warps and over the CTAs of a cluster; partial sums meet in shared
 // memory and are added in a fixed order.  V is kept in the element type (rounded once, after the
 // scale): it is an operand of the second product, which takes 16 bits.
+//
+// Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.4 us (launches and dependent loads); 64 rows of
+// 48 adapters of rank 32 on 4096 x 28672 24.4 us, 3.6 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
+// 47.0 us, 4.5 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -125,25 +133,23 @@ __device__ __forceinline__ void slice(int steps, int i, int n, int& lo, int& hi)
   hi = static_cast<int>(static_cast<int64_t>(steps) * (i + 1) / n);
 }
 
-// acc[b][t] += X rows (16 b + g, + 8) . A row (8 t + g) over steps [lo, hi) of 32, for the rows that
-// `on` marks (bits 2b: row 16 b + g, 2b + 1: row 16 b + g + 8); NT tiles of 8 ranks, `tiles` live.
-template <bool F16, int RB, int NT, int U>
-__device__ __forceinline__ void shrink_loop(float (&acc)[RB][NT][4], const LoraArgs& p, const uint16_t* x, const uint16_t* a,
+// acc[t] += X rows (g, g + 8) . A row (8 t + g) over steps [lo, hi) of 32, for the rows that `on` marks (bit 0:
+// row g, bit 1: row g + 8); NT tiles of 8 ranks, `tiles` live; U steps' loads under way at a time.
+template <bool F16, int NT, int U>
+__device__ __forceinline__ void shrink_loop(float (&acc)[NT][4], const LoraArgs& p, const uint16_t* x, const uint16_t* a,
                                             uint32_t on, int tiles, int lo, int hi) {
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   for (int s = lo; s < hi; s += U) {
-    uint4 xv[U][RB][2], av[U][NT];
+    uint4 xv[U][2], av[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = (s + u) * 32 + 8 * q;
       const bool in = s + u < hi && k < p.K;
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          xv[u][b][h] = make_uint4(0, 0, 0, 0);
-          if (in && ((on >> (2 * b + h)) & 1u)) xv[u][b][h] = ld_stream(x + static_cast<int64_t>(16 * b + 8 * h + g) * p.K + k);
-        }
+      for (int h = 0; h < 2; ++h) {
+        xv[u][h] = make_uint4(0, 0, 0, 0);
+        if (in && ((on >> h) & 1u)) xv[u][h] = ld_stream(x + static_cast<int64_t>(8 * h + g) * p.K + k);
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         av[u][t] = make_uint4(0, 0, 0, 0);
@@ -154,14 +160,13 @@ __device__ __forceinline__ void shrink_loop(float (&acc)[RB][NT][4], const LoraA
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        if (t < tiles)
-#pragma unroll
-          for (int b = 0; b < RB; ++b) mma_k32<F16>(acc[b][t], xv[u][b][0], xv[u][b][1], av[u][t]);
+        if (t < tiles) mma_k32<F16>(acc[t], xv[u][0], xv[u][1], av[u][t]);
   }
 }
 
 // Few rows: one cluster for each row that leads its adapter in its 16-row block; 8 warps a CTA, each
-// a slice of K.
+// a slice of K.  12 us by itself for 48 adapters of rank 32, K 4096 (10 MB of A): adapter, rank and A are
+// loads that wait for one another, and the cluster meets twice.
 constexpr int kRowWarps = 8;
 template <bool F16, int NT>
 __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraArgs p, uint16_t* V) {
@@ -176,23 +181,23 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
   const int a = __shfl_sync(0xffffffffu, mine, m & 15);
   const int rank = adapter_rank(p, a), tiles = rank / 8;
   const uint32_t rows = __ballot_sync(0xffffffffu, mine == a);
-  float acc[1][NT][4];
+  float acc[NT][4];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[0][t][e] = 0.f;
+    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
   int lo, hi;
   slice((p.K + 31) / 32, blockIdx.x * kRowWarps + warp, gridDim.x * kRowWarps, lo, hi);
   const uint32_t on = ((rows >> g) & 1u) | (((rows >> (g + 8)) & 1u) << 1);
-  shrink_loop<F16, 1, NT, NT <= 4 ? 4 : 2>(acc, p, p.X + static_cast<int64_t>(m0) * p.K,
+  shrink_loop<F16, NT, NT <= 4 ? 4 : 2>(acc, p, p.X + static_cast<int64_t>(m0) * p.K,
                                             p.A + static_cast<int64_t>(a) * p.r * p.K, on, tiles, lo, hi);
   constexpr int W = 8 * NT;
   float* part = red + warp * 16 * W;
   const int q = lane & 3;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    *reinterpret_cast<float2*>(part + g * W + 8 * t + 2 * q) = make_float2(acc[0][t][0], acc[0][t][1]);
-    *reinterpret_cast<float2*>(part + (g + 8) * W + 8 * t + 2 * q) = make_float2(acc[0][t][2], acc[0][t][3]);
+    *reinterpret_cast<float2*>(part + g * W + 8 * t + 2 * q) = make_float2(acc[t][0], acc[t][1]);
+    *reinterpret_cast<float2*>(part + (g + 8) * W + 8 * t + 2 * q) = make_float2(acc[t][2], acc[t][3]);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 16 * W; i += blockDim.x) {
@@ -219,7 +224,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
 // tensor cores: tcgen05.mma with X [128 rows, 64 k] and A [ranks, 64 k] by TMA (128-byte swizzle), one
 // accumulator in tensor memory for each adapter that occurs in the rows, two adapters a pass over
 // the slice.  Three stages of 32 KB and two CTAs an SM keep some 150 KB of loads under way; the
-// same contraction on mma.sync, with A prefetched one step ahead, waited for L2 at every step.
+// same contraction on mma.sync, with A prefetched one step ahead, waited for L2 at every step.  24 us by
+// itself at 4001 rows, K 8192, rank 64: 72 MB, 3.0 TB/s; a CTA has only 16 steps of 64 between its start
+// and the cluster's sum.
 constexpr int kTileRows = 128, kTileStages = 3, kTilePass = 2;
 constexpr int kTileLd = 64 + 4;
 // The different adapters of 128 rows, in order of their first row.
@@ -413,7 +420,8 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
 // The expand: a warp has 16 rows, 32 output columns at a time, and every `subsets`-th adapter of
 // those rows (their rows are its own to write; rows without an adapter are the first warp's).
 // Output tile t of 8 columns stands for the columns 8 (c / 2) + 2 t + c % 2, c = 0 .. 7, so that a
-// lane's results of four tiles are 8 neighbouring columns: base and Y move 16 bytes a lane.
+// lane's results of four tiles are 8 neighbouring columns: base and Y move 16 bytes a lane.  19 us by itself
+// for 64 rows of 48 adapters of rank 32, N 28672: 84 MB, 4.4 TB/s.
 //   B (32 columns and 32 ranks a step) and base come through queues in shared memory, each thread
 //   its own place, so that steps ahead are under way without registers: with B one step ahead in
 //   registers a decode batch of 48 adapters ran at 2.5 TB/s.
@@ -594,7 +602,8 @@ constexpr size_t kExpandSmem = static_cast<size_t>(kBQueue * 4 + kBaseQueue * 2)
 // occurs in the rows; base comes by TMA, is added to in its place in shared memory and
 // leaves from there by TMA.  Two groups of four warps (a row a thread) take the tiles in turn, each with
 // two accumulators of its own; the other warps move base and Y, issue the products, and copy B.  Two CTAs
-// an SM (one with more than 64 ranks).
+// an SM (one with more than 64 ranks).  26 us by itself at 4001 rows, N 8192, rank 64: 131 MB, 5.1 TB/s; with one
+// group, which held a tile's sums in registers until base was there, the whole call took 50 us instead of 47.
 constexpr int kExCols = 64, kExBase = 4, kExB = 3;
 constexpr int kExThreads = 352, kExWBase = 8, kExWMma = 9;   // warps 0 .. 7 add; 10: B
 template <int CR>                              // chunks of 64 ranks
@@ -798,17 +807,24 @@ cudaError_t launch_cluster(void (*kern)(P...), dim3 grid, unsigned threads, size
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Up to this many rows the kernels on mma.sync, by the adapters that lead in each 16 rows; above, those
-// on tcgen05, by 128 rows.  K 4096, N 4096 or 8192, in us, mma.sync / tcgen05:
-//   shrink (with the same expand): 512 rows of 8 adapters 16.6 / 18.2, 1024 rows 26.6 / 22.6, 1024 rows
-//     of rank 64 28.4 / 19.8; 512 rows that are each another's adapter of 48 85 / 115, 1024 rows 158 / 161
-//   expand (with the same shrink): 257 rows 12.1 / 13.1, 512 rows 16.3 / 16.6, 1024 rows 26.9 / 26.6,
-//     2048 rows of rank 64 29.2 / 22.1, 4001 rows 67 / 43; 2048 rows interleaved over 64 adapters 163 / 194
-constexpr int kFewRows = 512;
+// The kernels on tcgen05, by 128 rows, or those on mma.sync, by the adapters that lead in each 16 rows.  The
+// former cost a product and a pass over the rows for each adapter that occurs in 128 of them, which only the
+// device knows; at 32 rows an adapter or more, on average over all, it is few where requests' rows are
+// neighbours.  (Beyond kMostRows the grid of the latter's shrink would end.)  K 4096, N 4096 or 8192, in us,
+// mma.sync / tcgen05:
+//   shrink (with the expand that fits): 8 adapters, 257 rows 12.2 / 18.8, 512 rows 16.2 / 18.1, 1024 rows 25.3 / 21.2,
+//     1024 rows of rank 64 28.2 / 19.6, 2048 rows 46 / 21; 1024 rows that take 64 adapters in turn 134 / 164
+//   expand (with the shrink that fits): 8 adapters, 256 rows 11.9 / 14.2, 512 rows 16.2 / 16.2, 1024 rows 23.1 / 21.1,
+//     2048 rows of rank 64 27.8 / 21.2, 4001 rows 63 / 40; 64 adapters in turn, 1024 rows 131 / 164, 2048 rows 153 / 225
+constexpr int kFewRows = 512, kRowsAdapter = 32, kMostRows = 16384;
+bool many_rows(const LoraArgs& a) {
+  return a.M > kFewRows && (a.M / kRowsAdapter >= a.L || a.M > kMostRows);
+}
 
 template <bool F16, int NT>
 cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
-  // at least four steps of 32 a warp, up to 8 CTAs
+  // At least four steps of 32 a warp, up to 8 CTAs.  One CTA / this many (4), K 4096, in us: 3 rows
+  // 11.0 / 6.7, 16 rows of 16 adapters 11.9 / 7.4, 64 rows of 48 39 / 24 (N 28672), 200 rows 42.8 / 41.9.
   const int steps = (a.K + 31) / 32;
   unsigned c = 1;
   while (c < 8 && steps >= static_cast<int>(2 * c) * kRowWarps * 4) c *= 2;
@@ -822,13 +838,15 @@ cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
 
 template <bool F16>
 cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
-  if (a.M <= kFewRows) {
+  if (!many_rows(a)) {
     if (a.r <= 32) return launch_rows<F16, 4>(a, V, stream);
     if (a.r <= 64) return launch_rows<F16, 8>(a, V, stream);
     return launch_rows<F16, 16>(a, V, stream);
   }
   const int tiles = (a.M + kTileRows - 1) / kTileRows, steps = (a.K + 63) / 64;
-  unsigned c = 1;                              // two CTAs an SM, at least four steps of 64 each
+  // Two CTAs an SM, at least four steps of 64 each.  One CTA / this many, whole calls, K 4096, in us: 1024 rows
+  // 52 / 21 (8), 2048 rows of rank 64 41 / 21 (8), 4001 rows 61 / 40 (8).
+  unsigned c = 1;
   while (c < 8 && static_cast<int>(tiles * c) < 2 * device_sm_count() && steps >= static_cast<int>(2 * c) * 4) c *= 2;
   const int box_ranks = std::min(64, (a.r + 15) / 16 * 16);
   const CUtensorMapDataType dt = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -850,7 +868,7 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
   const int sms = device_sm_count();
   int ls = 0, lr = 0;
   int64_t span = 1;
-  if (a.M > kFewRows && a.N % 8 == 0) {
+  if (many_rows(a) && a.N % 8 == 0) {
     // one wave: two CTAs an SM, with more than 64 ranks one
     const int64_t row_ctas = (a.M + kTileRows - 1) / kTileRows, tiles = (a.N + kExCols - 1) / kExCols;
     const int64_t across = std::max<int64_t>(1, (a.r <= 64 ? 2 : 1) * sms / row_ctas);
@@ -876,7 +894,9 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
   }
   // Subsets of the adapters, up to those that a block can hold, while there are few warps for the
   // SMs.  Row blocks: as many as there are.  8 warps a CTA, and column tiles enough for one wave of two
-  // CTAs an SM.
+  // CTAs an SM.  No subsets / this rule / always all, K 4096, in us: 16 rows of 16 adapters, N 4096 11.0 / 7.4 /
+  // 7.4, N 28672 13.1 / 11.8 / 11.9; 64 rows of 48, N 4096 14.3 / 11.2 / 11.3, N 28672 24.5 / 24.3 / 34.0; 200 rows,
+  // N 14336 41.9 / 41.9 / 54.0.  One column tile a warp / this rule: 64 rows, N 28672 27.7 / 24.3.
   const int most = std::min(std::min(a.M, 16), a.L);
   while (ls < 3 && (1 << ls) < most && (blocks * cols << ls) < 24ll * sms) ++ls;
   while (lr + ls < 3 && (1 << lr) < blocks) ++lr;

@@ -10,7 +10,9 @@
 // of a head, chosen so that both elements of each pair are its own (half-split pairs: pieces j and
 // j + rot/16; adjacent pairs: any, j and j + d/16), and d / 16 neighbouring lanes hold a head, so
 // only the sum of squares takes shuffles.  With one piece a thread and the partners by shuffles the
-// instructions, not the bytes, set the time.
+// instructions, not the bytes, set the time (8192 tokens of 80 heads of 128: 88 us instead of 61).  Sums, norm and
+// rotation are float32; each output is rounded once.  8192 tokens, 80 heads, with cache: 60.6 us, 5.6 TB/s of 340 MB;
+// 2047 tokens, 40 heads: 9.4 us, 4.6 TB/s; one token: 2.0 us, a launch and two dependent loads.
 #include "elem16.cuh"
 #include "internal.h"
 

@@ -428,6 +428,10 @@ LORA = [  # M, K, N, r, L, adapters of the rows
     (2100, 136, 72, 96, 9, "mixed"),
     (1025, 2048, 64, 8, 1, "one"),
     (1100, 512, 41, 128, 40, "each"),
+    (1300, 512, 104, 128, 40, "each"),
+    (700, 256, 200, 24, 64, "runs"),
+    (16500, 64, 72, 8, 600, "each"),
+    (600, 1024, 328, 40, 2, "runs"),
 ]
 
 
