@@ -838,16 +838,20 @@ cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
 
 template <bool F16>
 cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
-  if (!many_rows(a)) {
+  // A small X leaves the tiles' clusters too little to share.  By 16 rows / by 128 rows, 8 adapters of rank 40, in
+  // us: 965 x 896 13.3 / 14.8, 1024 x 512 11.7 / 14.2, 1024 x 1024 13.6 / 13.6, 2048 x 1024 16.6 / 14.9, 4096 x 512
+  // 20.8 / 15.6, 1024 x 2048 16.5 / 15.1.
+  const bool small = static_cast<int64_t>(a.M) * a.K < (1 << 20);
+  if (!many_rows(a) || (small && a.M <= kMostRows)) {
     if (a.r <= 32) return launch_rows<F16, 4>(a, V, stream);
     if (a.r <= 64) return launch_rows<F16, 8>(a, V, stream);
     return launch_rows<F16, 16>(a, V, stream);
   }
   const int tiles = (a.M + kTileRows - 1) / kTileRows, steps = (a.K + 63) / 64;
-  // Two CTAs an SM, at least four steps of 64 each.  One CTA / this many, whole calls, K 4096, in us: 1024 rows
+  // Two CTAs an SM, at least two steps of 64 each (at least four: 4096 x 512 18.6 us instead of 15.6).  One CTA / this many, whole calls, K 4096, in us: 1024 rows
   // 52 / 21 (8), 2048 rows of rank 64 41 / 21 (8), 4001 rows 61 / 40 (8).
   unsigned c = 1;
-  while (c < 8 && static_cast<int>(tiles * c) < 2 * device_sm_count() && steps >= static_cast<int>(2 * c) * 4) c *= 2;
+  while (c < 8 && static_cast<int>(tiles * c) < 2 * device_sm_count() && steps >= static_cast<int>(2 * c) * 2) c *= 2;
   const int box_ranks = std::min(64, (a.r + 15) / 16 * 16);
   const CUtensorMapDataType dt = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap tx, ta;
