@@ -188,8 +188,9 @@ struct LoraArgs {
   const int32_t *ranks, *adapter;
   const float* scales;
   uint16_t* Y;
+  int lo;               // 0: a row of V is r wide; r: 2 r wide, what V's rounding left behind V
 };
-size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
+size_t lora_scratch_bytes(int64_t M, int64_t v_width);
 cudaError_t launch_lora_shrink(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream);
 // base_ready: the base was written before the shrink was launched, not by a kernel after it
 cudaError_t launch_lora_expand(int dtype, const LoraArgs& a, void* scratch, bool base_ready, cudaStream_t stream);

@@ -17,7 +17,9 @@
 // row takes its own.
 // The sum over K is split over warps and over the CTAs of a cluster; partial sums meet in shared
 // memory and are added in a fixed order.  V is kept in the element type (rounded once, after the
-// scale): it is an operand of the second product, which takes 16 bits.
+// scale): it is an operand of the second product, which takes 16 bits.  Where base itself comes rounded
+// from the quantized layer of the same call, V is kept in two such parts, itself and what its rounding
+// left (`lo`), so that base's rounding and the result's are the only ones that count.
 //
 // Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.4 us (launches and dependent loads); 64 rows of
 // 48 adapters of rank 32 on 4096 x 28672 24.4 us, 3.6 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
@@ -215,7 +217,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
     if (!((rows >> row) & 1u) || j >= p.r) continue;
     float v = 0.f;                            // past the rank: the expand of many rows takes all r
     if (j < rank) v = (n > 1 ? sum_cluster(red + i, n) : red[i]) * s;
-    V[static_cast<int64_t>(m0 + row) * p.r + j] = round1<F16>(v);
+    uint16_t* to = V + static_cast<int64_t>(m0 + row) * (p.r + p.lo) + j;
+    const uint32_t hi = pack2<F16>(v, 0.f);
+    to[0] = static_cast<uint16_t>(hi);
+    if (p.lo) to[p.lo] = round1<F16>(v - unpack2<F16>(hi).x);
   }
   if (n > 1) cluster_sync();                  // the others have read this CTA's sums
 }
@@ -411,8 +416,13 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
     const float* src = sm.red + r * kTileLd + 2 * lane;
     float2 v = n > 1 ? make_float2(sum_cluster(src, n), sum_cluster(src + 1, n)) : make_float2(src[0], src[1]);
     v = 2 * lane < rank ? make_float2(v.x * s, v.y * s) : make_float2(0.f, 0.f);
-    if (2 * lane < p.r - j0)
-      *reinterpret_cast<uint32_t*>(V + static_cast<int64_t>(m) * p.r + j0 + 2 * lane) = pack2<F16>(v.x, v.y);
+    if (2 * lane < p.r - j0) {
+      uint16_t* to = V + static_cast<int64_t>(m) * (p.r + p.lo) + j0 + 2 * lane;
+      const uint32_t hi = pack2<F16>(v.x, v.y);
+      const float2 f = unpack2<F16>(hi);
+      *reinterpret_cast<uint32_t*>(to) = hi;
+      if (p.lo) *reinterpret_cast<uint32_t*>(to + p.lo) = pack2<F16>(v.x - f.x, v.y - f.y);
+    }
   }
   if (n > 1) cluster_sync();                   // the others have read this CTA's sums
 }
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
 //   `span` column tiles a warp: 1 for few rows; many rows keep their set-up over several.
 constexpr int kCols = 32;
 constexpr int kBQueue = 4, kBaseQueue = 4;   // see the waits below
-template <bool F16, int CH>     // CH: chunks of 32 ranks
+template <bool F16, int CH, bool LO>     // CH: chunks of 32 ranks; LO: V in two parts
 __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uint16_t* V, int log_rows, int log_subsets, int span) {
   extern __shared__ __align__(16) uint8_t expand_smem[];
   uint4* bq = reinterpret_cast<uint4*>(expand_smem) + threadIdx.x;              // [step][4][256]
@@ -521,14 +531,18 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
   copy_commit();
   const int id[2] = {__shfl_sync(0xffffffffu, mine, g), __shfl_sync(0xffffffffu, mine, g + 8)};
   const int ranks[2] = {__shfl_sync(0xffffffffu, my_rank, g), __shfl_sync(0xffffffffu, my_rank, g + 8)};
-  uint4 v[CH][2];
+  uint4 v[CH][2], vl[LO ? CH : 1][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
       v[ch][h] = make_uint4(0, 0, 0, 0);
-      if (own[h] && 32 * ch + 8 * q < ranks[h])
-        v[ch][h] = __ldcg(reinterpret_cast<const uint4*>(V + static_cast<int64_t>(m0 + 8 * h + g) * p.r + 32 * ch + 8 * q));
+      if constexpr (LO) vl[ch][h] = v[ch][h];
+      if (own[h] && 32 * ch + 8 * q < ranks[h]) {
+        const uint16_t* from = V + static_cast<int64_t>(m0 + 8 * h + g) * (p.r + p.lo) + 32 * ch + 8 * q;
+        v[ch][h] = __ldcg(reinterpret_cast<const uint4*>(from));
+        if constexpr (LO) vl[ch][h] = __ldcg(reinterpret_cast<const uint4*>(from + p.lo));
+      }
     }
   const int steps = max(1, __popc(list) * CH);   // a tile
   int b_at = 0, base_at = 0;
@@ -552,6 +566,11 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
         const uint4 x0 = id[0] == a ? v[ch][0] : zero, x1 = id[1] == a ? v[ch][1] : zero;
 #pragma unroll
         for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], x0, x1, bq[(b_at * 4 + t) * 256]);
+        if constexpr (LO) {
+          const uint4 y0 = id[0] == a ? vl[ch][0] : zero, y1 = id[1] == a ? vl[ch][1] : zero;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], y0, y1, bq[(b_at * 4 + t) * 256]);
+        }
         b_at = b_at + 1 == kBQueue ? 0 : b_at + 1;
       }
     }
@@ -602,14 +621,16 @@ constexpr size_t kExpandSmem = static_cast<size_t>(kBQueue * 4 + kBaseQueue * 2)
 // occurs in the rows; base comes by TMA, is added to in its place in shared memory and
 // leaves from there by TMA.  Two groups of four warps (a row a thread) take the tiles in turn, each with
 // two accumulators of its own; the other warps move base and Y, issue the products, and copy B.  Two CTAs
-// an SM (one with more than 64 ranks).  26 us by itself at 4001 rows, N 8192, rank 64: 131 MB, 5.1 TB/s; with one
+// an SM (one with more than 64 ranks or V in two parts).  26 us by itself at 4001 rows, N 8192, rank 64: 131 MB, 5.1 TB/s; with one
 // group, which held a tile's sums in registers until base was there, the whole call took 50 us instead of 47.
+// A multiple of the groups: a slot of base is then always the same group's, which sees each of its phases.
 constexpr int kExCols = 64, kExBase = 4, kExB = 3;
+static_assert(kExBase % 2 == 0, "a wait by parity may not leave out a phase");
 constexpr int kExThreads = 352, kExWBase = 8, kExWMma = 9;   // warps 0 .. 7 add; 10: B
-template <int CR>                              // chunks of 64 ranks
+template <int CR, bool LO>                     // chunks of 64 ranks; V in two parts
 struct ExpandSmem {
   uint8_t base[kExBase][kTileRows * 128];
-  uint8_t v[CR][kTileRows * 128];
+  uint8_t v[LO ? 2 : 1][CR][kTileRows * 128];
   uint8_t b[kExB][CR][kExCols * 128];
   uint64_t base_full[kExBase], added[kExBase], b_full[kExB], b_empty[kExB], v_full, acc_full[2][2], acc_empty[2][2], drain;
   Found who;
@@ -617,12 +638,13 @@ struct ExpandSmem {
   uint32_t tmem_base;
 };
 
-template <bool F16, int CR>
-__global__ void __launch_bounds__(kExThreads, CR == 1 ? 2 : 1)
+template <bool F16, int CR, bool LO>
+__global__ void __launch_bounds__(kExThreads, CR == 1 && !LO ? 2 : 1)
     k_lora_expand_tile(const __grid_constant__ CUtensorMap tbase, const __grid_constant__ CUtensorMap ty,
-                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb, const LoraArgs p, int span,
-                       int base_ready) {
-  using S = ExpandSmem<CR>;
+                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tvl,
+                       const __grid_constant__ CUtensorMap tb, const LoraArgs p, int span, int base_ready) {
+  using S = ExpandSmem<CR, LO>;
+  constexpr int kParts = LO ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + smem_align_pad(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -684,9 +706,12 @@ __global__ void __launch_bounds__(kExThreads, CR == 1 ? 2 : 1)
     pdl_wait();
     if (found) {
       if (elect_one()) {
-        mbar_arrive_expect_tx(&sm.v_full, CR * kTileRows * 128);
+        mbar_arrive_expect_tx(&sm.v_full, kParts * CR * kTileRows * 128);
 #pragma unroll
-        for (int c = 0; c < CR; ++c) tma_load_2d(sm.v[c], &tv, 64 * c, m0, &sm.v_full, l2_policy_evict_first());
+        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+          for (int c = 0; c < CR; ++c)
+            tma_load_2d(sm.v[part][c], part ? &tvl : &tv, 64 * c, m0, &sm.v_full, l2_policy_evict_first());
       }
       __syncwarp();
       ok = wait(&sm.v_full, 0, kErrWaitFull);
@@ -703,9 +728,11 @@ __global__ void __launch_bounds__(kExThreads, CR == 1 ? 2 : 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          for (int k = 0; k < steps; ++k)
-            tc_mma_ss_f16(tmem + 128 * grp + 64 * buf, smem_desc_sw128(smem_u32(sm.v[k >> 2])) + 2 * (k & 3),
-                          smem_desc_sw128(smem_u32(sm.b[s][k >> 2])) + 2 * (k & 3), idesc, k ? 1u : 0u);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part)
+            for (int k = 0; k < steps; ++k)
+              tc_mma_ss_f16(tmem + 128 * grp + 64 * buf, smem_desc_sw128(smem_u32(sm.v[part][k >> 2])) + 2 * (k & 3),
+                            smem_desc_sw128(smem_u32(sm.b[s][k >> 2])) + 2 * (k & 3), idesc, (part || k) ? 1u : 0u);
           tc_commit(&sm.b_empty[s]);
           tc_commit(&sm.acc_full[grp][buf]);
         }
@@ -873,17 +900,19 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
   int ls = 0, lr = 0;
   int64_t span = 1;
   if (many_rows(a) && a.N % 8 == 0) {
-    // one wave: two CTAs an SM, with more than 64 ranks one
+    // one wave: two CTAs an SM, with more than 64 ranks or V in two parts one
     const int64_t row_ctas = (a.M + kTileRows - 1) / kTileRows, tiles = (a.N + kExCols - 1) / kExCols;
-    const int64_t across = std::max<int64_t>(1, (a.r <= 64 ? 2 : 1) * sms / row_ctas);
+    const int64_t across = std::max<int64_t>(1, (a.r <= 64 && !a.lo ? 2 : 1) * sms / row_ctas);
     span = (tiles + across - 1) / across;
     const dim3 grid(static_cast<unsigned>((tiles + span - 1) / span), static_cast<unsigned>(row_ctas));
     const CUtensorMapDataType dt = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t n = a.N, r = a.r;
-    CUtensorMap tbase, ty, tv, tb;
+    CUtensorMap tbase, ty, tv, tvl, tb;
+    const uint64_t v_stride = static_cast<uint64_t>(a.r + a.lo) * 2;
     cudaError_t e = make_tmap_2d(&tbase, dt, a.base, n, a.M, n * 2, kExCols, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (e == cudaSuccess) e = make_tmap_2d(&ty, dt, a.Y, n, a.M, n * 2, kExCols, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
-    if (e == cudaSuccess) e = make_tmap_2d(&tv, dt, V, r, a.M, r * 2, 64, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    if (e == cudaSuccess) e = make_tmap_2d(&tvl, dt, V + a.lo, r, a.M, v_stride, 64, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    if (e == cudaSuccess) e = make_tmap_2d(&tv, dt, V, r, a.M, v_stride, 64, kTileRows, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
     const uint64_t bd[4] = {r, n, static_cast<uint64_t>(a.L), 1}, bs[3] = {r * 2, n * r * 2, n * r * 2 * a.L};
     const uint32_t bb[4] = {64, kExCols, 1, 1};
     if (e == cudaSuccess) e = make_tmap_4d(&tb, dt, a.B, bd, bs, bb, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
@@ -891,10 +920,14 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
     const auto launch = [&](auto kern, size_t smem) {
       const cudaError_t se = set_smem_attr_once(reinterpret_cast<const void*>(kern), smem);
       if (se != cudaSuccess) return se;
-      return launch_pdl(kern, grid, kExThreads, smem, stream, tbase, ty, tv, tb, a, static_cast<int>(span), base_ready ? 1 : 0);
+      return launch_pdl(kern, grid, kExThreads, smem, stream, tbase, ty, tv, tvl, tb, a, static_cast<int>(span), base_ready ? 1 : 0);
     };
-    if (a.r <= 64) return launch(k_lora_expand_tile<F16, 1>, sizeof(ExpandSmem<1>) + 1024);
-    return launch(k_lora_expand_tile<F16, 2>, sizeof(ExpandSmem<2>) + 1024);
+    if (a.lo) {
+      if (a.r <= 64) return launch(k_lora_expand_tile<F16, 1, true>, sizeof(ExpandSmem<1, true>) + 1024);
+      return launch(k_lora_expand_tile<F16, 2, true>, sizeof(ExpandSmem<2, true>) + 1024);
+    }
+    if (a.r <= 64) return launch(k_lora_expand_tile<F16, 1, false>, sizeof(ExpandSmem<1, false>) + 1024);
+    return launch(k_lora_expand_tile<F16, 2, false>, sizeof(ExpandSmem<2, false>) + 1024);
   }
   // Subsets of the adapters, up to those that a block can hold, while there are few warps for the
   // SMs.  Row blocks: as many as there are.  8 warps a CTA, and column tiles enough for one wave of two
@@ -912,17 +945,15 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, grid, 256, kExpandSmem, stream, a, V, lr, ls, static_cast<int>(span));
   };
-  if (a.r <= 32) return launch(k_lora_expand<F16, 1>);
-  if (a.r <= 64) return launch(k_lora_expand<F16, 2>);
-  return launch(k_lora_expand<F16, 4>);
+  if (a.r <= 32) return launch(a.lo ? k_lora_expand<F16, 1, true> : k_lora_expand<F16, 1, false>);
+  if (a.r <= 64) return launch(a.lo ? k_lora_expand<F16, 2, true> : k_lora_expand<F16, 2, false>);
+  return launch(a.lo ? k_lora_expand<F16, 4, true> : k_lora_expand<F16, 4, false>);
 }
 
 }  // namespace
 
-size_t lora_scratch_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
-  (void)K;
-  (void)N;
-  return (static_cast<size_t>(M) * r * sizeof(uint16_t) + 255) / 256 * 256;
+size_t lora_scratch_bytes(int64_t M, int64_t v_width) {
+  return (static_cast<size_t>(M) * v_width * sizeof(uint16_t) + 255) / 256 * 256;
 }
 
 cudaError_t launch_lora_shrink(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream) {

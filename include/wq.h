@@ -552,7 +552,8 @@ wq_status wq_lora_add(wq_dtype dtype, const uint16_t* base, const uint16_t* X, i
 
 /*
  * The quantized layer with adapters: Y = wq_gemm_w4a16(X, Wq) + the adapters' product, bf16.
- * The layer's output is rounded to bf16 before the adapters' product is added to it in float32.
+ * The layer's output is rounded to bf16 before the adapters' product is added to it in float32; X A^T,
+ * which wq_lora_add rounds once to the element type, is kept in two parts here.
  * Arguments and errors as wq_gemm_w4a16 and wq_lora_add; workspace / ws_bytes at least
  * wq_gemm_w4a16_lora_workspace_bytes(fmt, M, K, N, r).
  */

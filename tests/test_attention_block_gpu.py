@@ -524,6 +524,25 @@ def test_quantized_layer_with_adapters(B, fmt, M):
     assert torch.equal(plain, B.gemm_w4a16(fmt, X, *d))     # the shared workspace's header is left at zero
 
 
+@pytest.mark.parametrize("M,r,L", [(1, 8, 1), (19, 16, 5), (64, 64, 9), (130, 104, 3), (700, 40, 6), (1300, 104, 40), (640, 64, 2)])
+def test_adapters_beside_a_quantized_layer_add_no_rounding_of_their_own(B, M, r, L):
+    """Given the layer's output, which is rounded to bf16, the sum is rounded once: V's own rounding is
+    carried along (it is left with u^2 of V, and float32 sums)."""
+    import torch
+    K, N = 512, 264
+    W = inputs.weights(11, N, K, 0.05)
+    d = [torch.from_numpy(np.ascontiguousarray(p)).cuda() for p in int4_g128.quantize(W)]
+    xb, xf = inputs.activations(M, M, K)
+    X = torch.from_numpy(xb.view(np.int16)).cuda().view(torch.bfloat16)
+    (a, b, s), (af, bf, sf) = _adapter_set(M, L, r, K, N, "bf16")
+    who = _who("mixed", M, L, M + 1)
+    y = B.gemm_w4a16_lora("int4_g128", X, *d, a, b, torch.from_numpy(who).cuda(), s)
+    base = _host(B.gemm_w4a16("int4_g128", X, *d))
+    delta, dabs = ab.adapters(xf, af, bf, who, sf)
+    ref, u = base + delta, U["bf16"]
+    _within(_host(y), ref, u * np.abs(ref) + (u * u + 1e-5) * dabs, "Y")
+
+
 # ------------------------------------------------------------------------- streams together
 def test_on_a_side_stream(B):
     """Every call on a stream that is not the current one, inputs made there just before."""
