@@ -438,6 +438,8 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
 //   `span` column tiles a warp: 1 for few rows; many rows keep their set-up over several.
 constexpr int kCols = 32;
 constexpr int kBQueue = 4, kBaseQueue = 4;   // see the waits below
+constexpr int kStageLd = 33;
+static_assert(8 * 16 * kStageLd * 4 <= kBaseQueue * 2 * 256 * 16, "the staged rows take the base queue's place");
 template <bool F16, int CH, bool LO>     // CH: chunks of 32 ranks; LO: V in two parts
 __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uint16_t* V, int log_rows, int log_subsets, int span) {
   extern __shared__ __align__(16) uint8_t expand_smem[];
@@ -506,14 +508,20 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
       f_at = f_at + 1 == kBQueue ? 0 : f_at + 1;
     }
   };
+  // N not a multiple of 8: rows begin anywhere, so a lane takes one column of each row; its base is on its
+  // way during the products, which come to the rows through shared memory (the base queue's place).  With
+  // eight columns a lane, in single elements, 494 rows of 11655 columns took 46 us instead of 33.
   const bool vec = p.N % 8 == 0;
+  float* stage = reinterpret_cast<float*>(expand_smem + sizeof(uint4) * kBQueue * 4 * 256) + warp * (16 * kStageLd);
+  const uint32_t adapted = __ballot_sync(0xffffffffu, mine >= 0);
   const bool own[2] = {((own_rows >> g) & 1u) != 0, ((own_rows >> (g + 8)) & 1u) != 0};
   const auto fetch_base = [&](int ct, int at) {
+    if (!vec) return;                          // the place is the staged rows'
     const int n = ct * kCols + 8 * q;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int m = m0 + 8 * h + g;
-      const bool on = vec && own[h] && ct < ct1 && m < p.M && n < p.N;
+      const bool on = own[h] && ct < ct1 && m < p.M && n < p.N;
       copy16(baseq + (at * 2 + h) * 256, on ? p.base + static_cast<int64_t>(m) * p.N + n : p.base, on);
     }
   };
@@ -554,6 +562,14 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+    const int col = ct * kCols + lane;
+    const int64_t first_at = static_cast<int64_t>(m0) * p.N + col;
+    uint16_t single[16];
+    if (!vec) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        single[r] = ((own_rows >> r) & 1u) && m0 + r < p.M && col < p.N ? p.base[first_at + static_cast<int64_t>(r) * p.N] : 0;
+    }
 #pragma unroll 1
     for (uint32_t todo = list; todo; todo &= todo - 1) {
       const int a = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
@@ -581,14 +597,12 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
     // This tile's base: tile i, of T steps a tile, has group Q + (i - Q + 1) T at most, and groups up
     // to (i + 1) T are here; only the first tiles' group Q - 1 may be later.
     if ((ct - ct0 + 1) * steps < kBQueue - 1) copy_wait<1>();
-    const int n = ct * kCols + 8 * q;
+    if (vec) {
+      const int n = ct * kCols + 8 * q;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int m = m0 + 8 * h + g;
-      if (m >= p.M || !own[h]) continue;
-      const int64_t at = static_cast<int64_t>(m) * p.N + n;
-      if (vec) {
-        if (n >= p.N) continue;
+      for (int h = 0; h < 2; ++h) {
+        const int m = m0 + 8 * h + g;
+        if (m >= p.M || !own[h] || n >= p.N) continue;
         const uint4 y = baseq[(base_at * 2 + h) * 256];
         uint32_t w[4] = {y.x, y.y, y.z, y.w};
         if (id[h] >= 0) {
@@ -598,17 +612,22 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
             w[t] = pack2<F16>(f.x + acc[t][2 * h], f.y + acc[t][2 * h + 1]);
           }
         }
-        *reinterpret_cast<uint4*>(p.Y + at) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
+        *reinterpret_cast<uint4*>(p.Y + static_cast<int64_t>(m) * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int64_t i = at + 2 * t + e;
-            if (n + 2 * t + e >= p.N) continue;
-            p.Y[i] = id[h] >= 0 ? round1<F16>(load1<F16>(p.base + i) + acc[t][2 * h + e]) : p.base[i];
-          }
-      }
+          for (int e = 0; e < 2; ++e) stage[(8 * h + g) * kStageLd + 8 * q + 2 * t + e] = acc[t][2 * h + e];
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (((own_rows >> r) & 1u) && m0 + r < p.M && col < p.N)
+          p.Y[first_at + static_cast<int64_t>(r) * p.N] =
+              (adapted >> r) & 1u ? round1<F16>(unpack2<F16>(single[r]).x + stage[r * kStageLd + lane]) : single[r];
+      __syncwarp();
     }
     base_at = base_at + 1 == kBaseQueue ? 0 : base_at + 1;
   }
