@@ -746,7 +746,7 @@ static wq_status check_lora(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
 
 size_t wq_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
   if (!lora_shape_ok(M, K, N, r)) return 0;
-  return wq::kWsHeaderBytes + wq::lora_scratch_bytes(M, r);
+  return wq::kWsHeaderBytes + wq::lora_scratch_bytes(M, 2 * r);
 }
 
 wq_status wq_lora_add(wq_dtype dtype, const uint16_t* base, const uint16_t* X, int64_t M, int64_t K, int64_t N,
@@ -766,7 +766,7 @@ wq_status wq_lora_add(wq_dtype dtype, const uint16_t* base, const uint16_t* X, i
   st = check_device_cached();
   if (st != WQ_OK) return st;
   const wq::LoraArgs a{base, X, A, B, static_cast<int>(M), static_cast<int>(K), static_cast<int>(N), static_cast<int>(L),
-                       static_cast<int>(r), ranks, adapter, scales, Y, 0};
+                       static_cast<int>(r), ranks, adapter, scales, Y, wq::lora_many_rows(M, L) ? 0 : static_cast<int>(r)};
   void* scratch = static_cast<uint8_t*>(workspace) + wq::kWsHeaderBytes;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = wq::launch_lora_shrink(dtype, a, scratch, s);

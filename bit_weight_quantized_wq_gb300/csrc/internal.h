@@ -190,6 +190,7 @@ struct LoraArgs {
   uint16_t* Y;
   int lo;               // 0: a row of V is r wide; r: 2 r wide, what V's rounding left behind V
 };
+bool lora_many_rows(int64_t M, int64_t L);     // the kernels for many rows take such a call
 size_t lora_scratch_bytes(int64_t M, int64_t v_width);
 cudaError_t launch_lora_shrink(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream);
 // base_ready: the base was written before the shrink was launched, not by a kernel after it

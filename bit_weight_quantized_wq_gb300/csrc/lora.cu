@@ -2,7 +2,7 @@
 //   Y[m] = base[m] + s[a] (X[m] A[a]^T) B[a]^T,   a = adapter[m];  a = -1: Y[m] = base[m].
 //
 // Two kernels, the shrink V = s X A^T [M, r] and the expand Y = base + V B^T, each in a form for few rows and
-// one for many (many_rows, below).  All are bound by bytes: a decode batch by the adapters' A and B, a prefill
+// one for many (lora_many_rows, below).  All are bound by bytes: a decode batch by the adapters' A and B, a prefill
 // batch by X, base and Y.
 //
 // Few rows: mma.sync m16n8k16 with the operands straight from global memory (A, B of the shrink; the
@@ -17,9 +17,9 @@
 // row takes its own.
 // The sum over K is split over warps and over the CTAs of a cluster; partial sums meet in shared
 // memory and are added in a fixed order.  V is kept in the element type (rounded once, after the
-// scale): it is an operand of the second product, which takes 16 bits.  Where base itself comes rounded
-// from the quantized layer of the same call, V is kept in two such parts, itself and what its rounding
-// left (`lo`), so that base's rounding and the result's are the only ones that count.
+// scale): it is an operand of the second product, which takes 16 bits.  For few rows, and where base itself
+// comes rounded from the quantized layer of the same call, V is kept in two such parts, itself and what
+// its rounding left (`lo`): base's rounding and the result's are then the only ones that count.
 //
 // Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.4 us (launches and dependent loads); 64 rows of
 // 48 adapters of rank 32 on 4096 x 28672 24.4 us, 3.6 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
@@ -863,10 +863,6 @@ cudaError_t launch_cluster(void (*kern)(P...), dim3 grid, unsigned threads, size
 //   expand (with the shrink that fits): 8 adapters, 256 rows 11.9 / 14.2, 512 rows 16.2 / 16.2, 1024 rows 23.1 / 21.1,
 //     2048 rows of rank 64 27.8 / 21.2, 4001 rows 63 / 40; 64 adapters in turn, 1024 rows 131 / 164, 2048 rows 153 / 225
 constexpr int kFewRows = 512, kRowsAdapter = 32, kMostRows = 16384;
-bool many_rows(const LoraArgs& a) {
-  return a.M > kFewRows && (a.M / kRowsAdapter >= a.L || a.M > kMostRows);
-}
-
 template <bool F16, int NT>
 cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
   // At least four steps of 32 a warp, up to 8 CTAs.  One CTA / this many (4), K 4096, in us: 3 rows
@@ -888,7 +884,7 @@ cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
   // us: 965 x 896 13.3 / 14.8, 1024 x 512 11.7 / 14.2, 1024 x 1024 13.6 / 13.6, 2048 x 1024 16.6 / 14.9, 4096 x 512
   // 20.8 / 15.6, 1024 x 2048 16.5 / 15.1.
   const bool small = static_cast<int64_t>(a.M) * a.K < (1 << 20);
-  if (!many_rows(a) || (small && a.M <= kMostRows)) {
+  if (!lora_many_rows(a.M, a.L) || (small && a.M <= kMostRows)) {
     if (a.r <= 32) return launch_rows<F16, 4>(a, V, stream);
     if (a.r <= 64) return launch_rows<F16, 8>(a, V, stream);
     return launch_rows<F16, 16>(a, V, stream);
@@ -918,7 +914,7 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
   const int sms = device_sm_count();
   int ls = 0, lr = 0;
   int64_t span = 1;
-  if (many_rows(a) && a.N % 8 == 0) {
+  if (lora_many_rows(a.M, a.L) && a.N % 8 == 0) {
     // one wave: two CTAs an SM, with more than 64 ranks or V in two parts one
     const int64_t row_ctas = (a.M + kTileRows - 1) / kTileRows, tiles = (a.N + kExCols - 1) / kExCols;
     const int64_t across = std::max<int64_t>(1, (a.r <= 64 && !a.lo ? 2 : 1) * sms / row_ctas);
@@ -970,6 +966,8 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
 }
 
 }  // namespace
+
+bool lora_many_rows(int64_t M, int64_t L) { return M > kFewRows && (M / kRowsAdapter >= L || M > kMostRows); }
 
 size_t lora_scratch_bytes(int64_t M, int64_t v_width) {
   return (static_cast<size_t>(M) * v_width * sizeof(uint16_t) + 255) / 256 * 256;
