@@ -21,9 +21,9 @@
 // comes rounded from the quantized layer of the same call, V is kept in two such parts, itself and what
 // its rounding left (`lo`): base's rounding and the result's are then the only ones that count.
 //
-// Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.4 us (launches and dependent loads); 64 rows of
-// 48 adapters of rank 32 on 4096 x 28672 24.4 us, 3.6 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
-// 47.0 us, 4.5 TB/s.
+// Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.8 us (launches and dependent loads); 64 rows of
+// 48 adapters of rank 32 on 4096 x 28672 25.2 us, 3.5 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
+// 47.3 us, 4.5 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -858,15 +858,15 @@ cudaError_t launch_cluster(void (*kern)(P...), dim3 grid, unsigned threads, size
 // device knows; at 32 rows an adapter or more, on average over all, it is few where requests' rows are
 // neighbours.  (Beyond kMostRows the grid of the latter's shrink would end.)  K 4096, N 4096 or 8192, in us,
 // mma.sync / tcgen05:
-//   shrink (with the expand that fits): 8 adapters, 257 rows 12.2 / 18.8, 512 rows 16.2 / 18.1, 1024 rows 25.3 / 21.2,
-//     1024 rows of rank 64 28.2 / 19.6, 2048 rows 46 / 21; 1024 rows that take 64 adapters in turn 134 / 164
-//   expand (with the shrink that fits): 8 adapters, 256 rows 11.9 / 14.2, 512 rows 16.2 / 16.2, 1024 rows 23.1 / 21.1,
-//     2048 rows of rank 64 27.8 / 21.2, 4001 rows 63 / 40; 64 adapters in turn, 1024 rows 131 / 164, 2048 rows 153 / 225
+//   shrink (with the expand that fits): 8 adapters, 257 rows 12.5 / 19.3, 512 rows 16.7 / 18.6, 1024 rows 25.3 / 21.3,
+//     1024 rows of rank 64 28.3 / 19.9, 2048 rows 46 / 21; 1024 rows that take 64 adapters in turn 102 / 133
+//   expand (with the shrink that fits): 8 adapters, 256 rows 12.3 / 14.9, 512 rows 16.8 / 17.9, 1024 rows 22.4 / 21.4,
+//     2048 rows of rank 64 28.4 / 21.1, 4001 rows 66 / 40; 64 adapters in turn, 1024 rows 102 / 190, 2048 rows 149 / 225
 constexpr int kFewRows = 512, kRowsAdapter = 32, kMostRows = 16384;
 template <bool F16, int NT>
 cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
   // At least four steps of 32 a warp, up to 8 CTAs.  One CTA / this many (4), K 4096, in us: 3 rows
-  // 11.0 / 6.7, 16 rows of 16 adapters 11.9 / 7.4, 64 rows of 48 39 / 24 (N 28672), 200 rows 42.8 / 41.9.
+  // 11.3 / 6.9, 16 rows of 16 adapters 12.1 / 8.0, 64 rows of 48 39.6 / 25.1 (N 28672), 200 rows 45.5 / 44.9.
   const int steps = (a.K + 31) / 32;
   unsigned c = 1;
   while (c < 8 && steps >= static_cast<int>(2 * c) * kRowWarps * 4) c *= 2;
@@ -946,9 +946,9 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
   }
   // Subsets of the adapters, up to those that a block can hold, while there are few warps for the
   // SMs.  Row blocks: as many as there are.  8 warps a CTA, and column tiles enough for one wave of two
-  // CTAs an SM.  No subsets / this rule / always all, K 4096, in us: 16 rows of 16 adapters, N 4096 11.0 / 7.4 /
-  // 7.4, N 28672 13.1 / 11.8 / 11.9; 64 rows of 48, N 4096 14.3 / 11.2 / 11.3, N 28672 24.5 / 24.3 / 34.0; 200 rows,
-  // N 14336 41.9 / 41.9 / 54.0.  One column tile a warp / this rule: 64 rows, N 28672 27.7 / 24.3.
+  // CTAs an SM.  No subsets / this rule / always all, K 4096, in us: 16 rows of 16 adapters, N 4096 11.2 / 8.0 /
+  // 8.1, N 28672 15.2 / 12.6 / 12.7; 64 rows of 48, N 4096 15.6 / 12.3 / 12.4, N 28672 26.9 / 25.1 / 34.9; 200 rows,
+  // N 14336 44.8 / 44.9 / 56.8.  One column tile a warp / this rule: 64 rows, N 28672 29.3 / 25.1.
   const int most = std::min(std::min(a.M, 16), a.L);
   while (ls < 3 && (1 << ls) < most && (blocks * cols << ls) < 24ll * sms) ++ls;
   while (lr + ls < 3 && (1 << lr) < blocks) ++lr;
