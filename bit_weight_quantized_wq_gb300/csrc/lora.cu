@@ -21,8 +21,8 @@
 // comes rounded from the quantized layer of the same call, V is kept in two such parts, itself and what
 // its rounding left (`lo`): base's rounding and the result's are then the only ones that count.
 //
-// Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.8 us (launches and dependent loads); 64 rows of
-// 48 adapters of rank 32 on 4096 x 28672 25.2 us, 3.5 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
+// Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.6 us (launches and dependent loads); 64 rows of
+// 48 adapters of rank 32 on 4096 x 28672 24.5 us, 3.6 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
 // 47.3 us, 4.5 TB/s.
 #include <algorithm>
 #include <type_traits>
@@ -80,15 +80,15 @@ __device__ __forceinline__ int row_adapter(const LoraArgs& p, int m) {
   }
   return a;
 }
-// Its rank rounded up to 8.
-__device__ __forceinline__ int adapter_rank(const LoraArgs& p, int a) {
-  int rank = p.ranks ? __ldg(p.ranks + a) : p.r;
+// Its rank, forced into range and rounded up to 8.
+__device__ __forceinline__ int checked_rank(const LoraArgs& p, int rank) {
   if (rank < 0 || rank > p.r) {
     atomicOr(&g_lora_err, kErrIndex);
     rank = min(max(rank, 0), p.r);
   }
   return (rank + 7) & ~7;
 }
+__device__ __forceinline__ int adapter_rank(const LoraArgs& p, int a) { return checked_rank(p, p.ranks ? __ldg(p.ranks + a) : p.r); }
 // Lanes whose adapter occurs in the warp's rows for the first time (lanes with -1 never lead).
 __device__ __forceinline__ uint32_t leaders(int a) {
   const uint32_t same = __match_any_sync(0xffffffffu, a);
@@ -177,11 +177,24 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
   pdl_wait();
   pdl_launch_dependents();                    // the expand may read all but V from here on
   const int m = blockIdx.y, m0 = m & ~15;
+  // Up to 128 adapters: their ranks come beside the rows' adapters, not after them (after / beside, in us: 16
+  // rows 8.1 / 7.9, 64 rows of 48 adapters 24.9 / 24.6, 200 rows 45.1 / 44.3).
+  const bool ahead = p.ranks && p.L <= 128;
+  int all_ranks[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) all_ranks[i] = ahead && lane + 32 * i < p.L ? __ldg(p.ranks + lane + 32 * i) : 0;
   const int mine = lane < 16 ? row_adapter(p, m0 + lane) : -1;
   const uint32_t lead = leaders(mine);
   if (!((lead >> (m & 15)) & 1u)) return;     // the same for all CTAs of the cluster
   const int a = __shfl_sync(0xffffffffu, mine, m & 15);
-  const int rank = adapter_rank(p, a), tiles = rank / 8;
+  int rank;
+  if (ahead) {
+    const int i = a >> 5;                     // the same in all lanes
+    rank = checked_rank(p, __shfl_sync(0xffffffffu, i == 0 ? all_ranks[0] : i == 1 ? all_ranks[1] : i == 2 ? all_ranks[2] : all_ranks[3], a & 31));
+  } else {
+    rank = adapter_rank(p, a);
+  }
+  const int tiles = rank / 8;
   const uint32_t rows = __ballot_sync(0xffffffffu, mine == a);
   float acc[NT][4];
 #pragma unroll
@@ -282,6 +295,8 @@ struct TileSmem {
   };
   uint64_t full[kTileStages], empty[kTileStages], acc_full[2], acc_empty[2], drain;
   Found who;
+  float scale[kTileRows];                      // of each row's adapter
+  int rank[kTileRows];                         // -1: no adapter
   uint32_t tmem_base;
 };
 
@@ -306,6 +321,10 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
   const int m0 = blockIdx.y * kTileRows, j0 = blockIdx.z * 64;
   const int row = (warp & 3) * 32 + lane;      // warps 2 .. 5: a row a thread, its tensor-memory lane
   const int mine = warp >= 2 ? row_adapter(p, m0 + row) : -1;
+  if (warp >= 2) {                             // for the end, when a row is any warp's
+    sm.scale[row] = mine >= 0 ? __ldg(p.scales + mine) : 0.f;
+    sm.rank[row] = mine >= 0 ? adapter_rank(p, mine) : -1;
+  }
   tc_fence_before();
   const int place = find_adapters(sm.who, warp >= 2 ? warp & 3 : -1, mine);
   tc_fence_after();
@@ -409,10 +428,9 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
   // each CTA of the cluster finishes its share of the rows, a warp a row at a time
   for (int r = cluster_rank() * 6 + warp; r < kTileRows; r += 6 * n) {
     const int m = m0 + r;
-    const int a = row_adapter(p, m);
-    if (a < 0) continue;
-    const float s = __ldg(p.scales + a);
-    const int rank = adapter_rank(p, a) - j0;
+    if (sm.rank[r] < 0) continue;
+    const float s = sm.scale[r];
+    const int rank = sm.rank[r] - j0;
     const float* src = sm.red + r * kTileLd + 2 * lane;
     float2 v = n > 1 ? make_float2(sum_cluster(src, n), sum_cluster(src + 1, n)) : make_float2(src[0], src[1]);
     v = 2 * lane < rank ? make_float2(v.x * s, v.y * s) : make_float2(0.f, 0.f);
