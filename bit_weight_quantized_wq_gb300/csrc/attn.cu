@@ -38,7 +38,7 @@
 // (P V with both operands in shared memory and V transposed takes some 150 cycles a step).
 // Keys mode is bound by the bytes: 262144 keys, 8 rows on 8 heads, 164 us, 6.6 TB/s; 64 requests over 16384 keys
 // of their own 326 us, 6.6 TB/s.  Short calls are bound by the chain of dependent loads, waits and launches:
-// 2 requests over 500 + 40 keys 12.4 us, of which the second kernel some 4.
+// 2 requests over 500 + 40 keys 11.7 us, of which the second kernel some 3.
 // P is rounded to the cache's type for the second product (the tensor core takes both operands in
 // one type); the sum of P is kept unrounded in float32.
 #include <algorithm>
@@ -169,8 +169,8 @@ __device__ __forceinline__ int row_tiles(const Params& p, int ntok) {
 __device__ __forceinline__ int tile_tokens(const Params& p, int ntok, int rt) { return min(2 * p.tb, ntok - rt * 2 * p.tb); }
 // Rows mode or keys mode of an item of so many tokens.  More rows than a lane holds would read K and V
 // twice in keys mode.  Rows mode for one lane's rows leaves the other lane idle; rows / keys mode, heads
-// of 128, in us: 1 token of 32 heads on 8 over 32768 keys 40.1 / 35.4, 16 tokens of 64 heads 45.0 / 40.3, 32
-// requests over 8192 + up to 700 33.8 / 28.4, 64 requests over up to 4096 of their own 114.6 / 93.9.
+// of 128, in us: 1 token of 32 heads on 8 over 32768 keys 39.0 / 33.7, 16 tokens of 64 heads 45.0 / 40.0, 32
+// requests over 8192 + up to 700 35.0 / 28.5, 64 requests over up to 4096 of their own 115.2 / 93.0.
 __host__ __device__ inline bool rows_mode(int tb, int tokens) { return tokens > tb; }
 __host__ __device__ inline int tile_weight(int tb, int G, int tokens) {
   return rows_mode(tb, tokens) ? kWRows : (tokens * G > 32 ? kWKeys : kWFew);
@@ -873,6 +873,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
 #pragma unroll
   for (int e = 0; e < E / 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int most = __reduce_max_sync(0xffffffffu, n);
+  const auto source = [&](int i) {                      // a lane's columns of segment i
+    bool in_p;
+    const long long s = slot(i, in_p);
+    const int cap8 = in_p ? kRows / 8 : p.q_rows_suffix >> 3, row = in_p ? run_p.row : run_s.row;
+    return reinterpret_cast<const float4*>(in_p ? p.po_p : p.po_s) + (s * cap8 + (row >> 3)) * (2 * D) + (row & 7) + col * 8;
+  };
+  // The first segments' outputs come beside the statistics, whether they will count or not: four where
+  // the warps are few (C = 4: 1 request over 500 keys 12.4 -> 11.6 us, 2 over 8192 17.9 -> 16.4, 16 over 8192 + up to
+  // 700 23.9 -> 21.9), else half as many (48 requests of up to 4 new tokens: 31.5 us with none, 31.0 with two, 32.4
+  // with four).
+  constexpr int kAhead = C == 4 ? 4 : E <= 16 ? 16 / E : 1;
+  float4 first[kAhead][E / 4];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const float4* src = w0 + k * W < n ? source(w0 + k * W) : reinterpret_cast<const float4*>(p.po_s);
+#pragma unroll
+    for (int e = 0; e < E / 4; ++e) first[k][e] = __ldcg(src + 8 * e);
+  }
   for (int base = w0; base < most; base += 32 * W) {
     float2 ml[8];
     float m2 = top;
@@ -909,23 +927,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
       for (int e = 0; e < E / 4; ++e) o[e].x *= keep, o[e].y *= keep, o[e].z *= keep, o[e].w *= keep;
     }
     const int here_n = min(32, (most - base + W - 1) / W);
-#pragma unroll(E >= 16 ? 2 : 8)
-    for (int k = 0; k < here_n; ++k) {
-      const float f = wt[k][lane & 7];
-      bool in_p;
-      const long long s = slot(base + k * W, in_p);
-      const int cap8 = in_p ? kRows / 8 : p.q_rows_suffix >> 3, row = in_p ? run_p.row : run_s.row;
-      const float4* src = reinterpret_cast<const float4*>(in_p ? p.po_p : p.po_s) + (s * cap8 + (row >> 3)) * (2 * D) + (row & 7) + col * 8;
-      // without a branch, so that several segments' loads are under way: a row without this segment
-      // loads some line of the workspace and drops it
+    const auto add_part = [&](const float4 (&v)[E / 4], float f) {
       const bool live = f != 0.f;
-      if (!live) src = reinterpret_cast<const float4*>(p.po_s);
 #pragma unroll
       for (int e = 0; e < E / 4; ++e) {
-        const float4 v = __ldcg(src + 8 * e);
-        o[e].x = fmaf(live ? v.x : 0.f, f, o[e].x), o[e].y = fmaf(live ? v.y : 0.f, f, o[e].y);
-        o[e].z = fmaf(live ? v.z : 0.f, f, o[e].z), o[e].w = fmaf(live ? v.w : 0.f, f, o[e].w);
+        o[e].x = fmaf(live ? v[e].x : 0.f, f, o[e].x), o[e].y = fmaf(live ? v[e].y : 0.f, f, o[e].y);
+        o[e].z = fmaf(live ? v[e].z : 0.f, f, o[e].z), o[e].w = fmaf(live ? v[e].w : 0.f, f, o[e].w);
       }
+    };
+    int k0 = 0;
+    if (base == w0) {
+      k0 = kAhead;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) add_part(first[k], wt[k][lane & 7]);
+    }
+#pragma unroll(E >= 16 ? 2 : 8)
+    for (int k = k0; k < here_n; ++k) {
+      const float f = wt[k][lane & 7];
+      // without a branch, so that several segments' loads are under way: a row without this segment
+      // loads some line of the workspace and drops it
+      const float4* src = f != 0.f ? source(base + k * W) : reinterpret_cast<const float4*>(p.po_s);
+      float4 v[E / 4];
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) v[e] = __ldcg(src + 8 * e);
+      add_part(v, f);
     }
   }
   if constexpr (W > 1) {
@@ -1058,8 +1083,8 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
     return launch_pdl(kern, dim3((blocks + per - 1) / per, a.Hkv, c), kJoinWarps * 32, w > 1 ? kJoinSmem<D> : 0, stream, p);
   };
   // W C warps for each eight rows of a head, as long as they fit the SMs at once (32 an SM).  One warp / this
-  // rule / always 8 C, in us: 2 requests over 8192 keys 38 / 18 / 18, 32 requests over 8192 + up to 700 51 / 28 /
-  // 28, 128 requests 66 / 58 / 64, 256 requests of 64 heads over 32768 + up to 1024 295 / 292 / 327.
+  // rule / always 8 C, in us: 2 requests over 8192 keys 30 / 16 / 16, 32 requests over 8192 + up to 700 43 / 28 /
+  // 28, 128 requests 62 / 58 / 70, 256 requests of 64 heads over 32768 + up to 1024 291 / 293 / 349.
   const long long warps = static_cast<long long>(blocks) * a.Hkv, fit = 32ll * l.ctas;
   constexpr int C = D == 128 ? 4 : 2;
   if (warps * 8 * C <= fit) return join(k_attn_join<F16, D, 8, C>, 8, C);
