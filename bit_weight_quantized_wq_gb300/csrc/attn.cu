@@ -384,11 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     run_long += wc, run_items += sm.scan_items[w];
     if (w < warp) at_long += wc, item += sm.scan_items[w];
   }
-  if (total > kMaxLine) {                 // too long for the line's 32 bits: reported, nothing computed
+  if (total > kMaxLine) {                 // too long for the line's 32 bits: reported
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_attn_err, kErrIndex);
     bad = true;
-    total = 0;
   }
+  // Nothing is computed then, nor where a q_start does not cover the tokens once each: the workspace's
+  // partials are counted for requests whose new tokens add up to T.
+  if (bad) total = 0;
   const bool work = total > 0;
   const int prefix_cost = static_cast<int>(prefix_long > kMaxLine ? 0 : prefix_long);
   // at least a tile for each lane

@@ -604,3 +604,25 @@ def test_the_three_together_as_one_block(B):
     example = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(example)
     assert example.main() < 0.02
+
+
+# --------------------------------------------------- what a call must not reach, drop or keep
+def test_attn_requests_that_overlap_compute_nothing(B):
+    """q_start that goes back and forth: each request by itself is in range, but together they have more
+    tokens, and more partials, than the workspace is counted for (550 slots of own keys where it has 312).
+    Nothing is computed: outputs and the bytes past the workspace's size keep what they held."""
+    import torch
+    T, R, Hq, Hkv, d = 640, 10, 32, 8, 64
+    b = Batch(101, [T // R] * R, 70, [T] * R, Hq, Hkv, d, 16, "bf16")
+    need = B.load_library().wq_attn_workspace_bytes(T, R, Hq, Hkv, d, T)
+    ws = torch.zeros(3 * need, dtype=torch.uint8, device="cuda")
+    ws[need:] = 0xA5
+    o, lse = torch.full((T, Hq, d), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((T, Hq), 3.0, device="cuda")
+    kw = dict(max_new=T, out=(o, lse), workspace=ws)
+    for q0 in ([0, T] * (R // 2) + [T], [0] + [T, 0] * ((R - 1) // 2) + [0, T], [0, T, T - 1] + [T] * (R - 2)):
+        b.run(B, q_start=torch.tensor(q0, dtype=torch.int32, device="cuda"), **kw)
+        assert B.read_error_flags() == 1 << 7, q0
+        assert (ws[need:] == 0xA5).all() and (o == 3).all() and (lse == 3).all(), q0
+    want = b.run(B)
+    got = b.run(B, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (ws[need:] == 0xA5).all()
