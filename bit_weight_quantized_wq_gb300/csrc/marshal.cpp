@@ -18,6 +18,7 @@
 #include <stdexcept>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "../../include/wq.h"
 
@@ -105,7 +106,8 @@ struct On {
     // straight to the caching allocator: the dispatcher's way there costs most of a microsecond more
     return at::detail::empty_cuda(shape, dtype, c10::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
   }
-  // The caller's workspace, or the zeroed one kept for this stream, grown when a call needs more.
+  // The caller's workspace, or the zeroed one kept for this stream, grown when a call needs more.  One
+  // that a captured call took stays when a larger one takes its place: the graph holds its address.
   at::Tensor workspace(PyObject* given, size_t bytes) const {
     if (given != Py_None) {
       const at::Tensor& t = tensor(given, "workspace");
@@ -113,15 +115,26 @@ struct On {
         refuse("workspace must be a contiguous CUDA tensor on the inputs' device");
       return t;
     }
-    static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>;   // outlives the interpreter's tear-down
-    at::Tensor& t = (*kept)[{dev, stream}];
-    if (!t.defined() || static_cast<size_t>(t.numel()) < bytes) {
-      cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-      if (cudaStreamIsCapturing(stream, &st) != cudaSuccess || st != cudaStreamCaptureStatusNone)
+    struct Kept {
+      at::Tensor now;
+      bool captured = false;
+      std::vector<at::Tensor> before;
+    };
+    static auto* all = new std::map<std::pair<int, cudaStream_t>, Kept>;   // outlives the interpreter's tear-down
+    Kept& k = (*all)[{dev, stream}];
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    bool capturing = true;
+    if (cudaStreamIsCapturing(stream, &st) == cudaSuccess) capturing = st != cudaStreamCaptureStatusNone;
+    else cudaGetLastError();                   // the default stream while another one is captured: the call itself will say so
+    if (!k.now.defined() || static_cast<size_t>(k.now.numel()) < bytes) {
+      if (capturing)
         refuse("no workspace of this size on this stream yet: make one call of this size before capturing, or pass one");
-      t = at::zeros({static_cast<int64_t>((bytes + 255) / 256 * 256)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+      at::Tensor grown = at::zeros({static_cast<int64_t>((bytes + 255) / 256 * 256)}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+      if (k.captured) k.before.push_back(k.now);
+      k.now = std::move(grown), k.captured = false;
     }
-    return t;
+    k.captured |= capturing;
+    return k.now;
   }
 };
 

@@ -626,3 +626,43 @@ def test_attn_requests_that_overlap_compute_nothing(B):
     want = b.run(B)
     got = b.run(B, **kw)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (ws[need:] == 0xA5).all()
+
+
+def test_a_captured_graph_keeps_the_workspace_it_was_captured_with(B):
+    """Capture a small batch, then run a larger one on the same stream, which needs more workspace, and fill
+    what the allocator hands out next: the graph's replay gives the same outputs and touches none of it."""
+    import torch
+    small, large = (Batch(111 + n, [1] * n, 300, [10 + i for i in range(n)], 8, 2, 128, 16, "bf16") for n in (2, 64))
+    (a, w, s), _ = _adapter_set(3, 2, 16, 1024, 96, "bf16")
+    stream = torch.cuda.Stream()
+
+    def step(b):
+        n = b.q.shape[0]
+        o, lse = b.run(B)
+        ad = torch.arange(n, dtype=torch.int32, device="cuda") % 3 - 1
+        return o, lse, B.lora_add(torch.ones(n, 96, dtype=torch.bfloat16, device="cuda"), o.view(n, -1), a, w, ad, s)
+
+    lib = B.load_library()
+    sizes = [lib.wq_attn_workspace_bytes(2, 2, 8, 2, 128, 1), lib.wq_lora_workspace_bytes(2, 1024, 96, 16)]
+    with torch.cuda.stream(stream):
+        want = [x.clone() for x in step(small)]
+    stream.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        got = step(small)
+    with torch.cuda.stream(stream):
+        step(large)
+        others = [torch.full(((n + 255) // 256 * 256,), 0xA5, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    stream.synchronize()
+    for x in got:
+        x.zero_()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert all((t == 0xA5).all() for t in others)
+    with torch.cuda.stream(stream):                       # and the larger workspace serves the smaller call
+        again = step(small)
+    stream.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(again, want))
