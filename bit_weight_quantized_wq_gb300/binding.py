@@ -264,18 +264,29 @@ def gemm_workspace_bytes(fmt, M: int, K: int, N: int) -> int:
     return int(load_library().wq_gemm_workspace_bytes(_fmt(fmt), M, K, N))
 
 
+_capturing = torch.cuda.is_current_stream_capturing
+
+
 class Workspace:
-    """A zero-initialised device scratch buffer that grows on demand (one per stream)."""
+    """A zero-initialised device scratch buffer that grows on demand (one per stream).  A buffer handed
+    out during a graph capture is kept when a larger one takes its place: the graph holds its address."""
 
     def __init__(self, device=None):
         self.device = torch.device("cuda") if device is None else torch.device(device)
         self.buf = None
+        self._captured = False      # buf was handed out during a capture
+        self._before = []           # buffers that captured graphs go on using
 
     def get(self, nbytes: int):
         if nbytes == 0:
             return None
+        capturing = self.device.type == "cuda" and _capturing()
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(((nbytes + 255) // 256) * 256, dtype=torch.uint8, device=self.device)
+            grown = torch.zeros(((nbytes + 255) // 256) * 256, dtype=torch.uint8, device=self.device)
+            if self._captured:
+                self._before.append(self.buf)
+            self.buf, self._captured = grown, False
+        self._captured |= capturing
         return self.buf
 
 

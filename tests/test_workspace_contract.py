@@ -95,3 +95,49 @@ def test_one_workspace_across_shapes_and_epilogues(B):
                 assert_close(y_to_host(t), ref[:, lo:hi], "call %d (QKV)" % i)
         assert _header_zero(ws) == 0, "call %d left split-K counters or partial sums non-zero" % i
     assert B.read_error_flags() == 0
+
+
+def test_a_captured_graph_keeps_its_workspace(B):
+    """A layer captured in a graph, then a call that needs a larger workspace on the same stream: the
+    graph's replay gives the same bits and writes to nothing that was allocated since."""
+    import torch
+    pk = _pack("int4_g128", inputs.weights(31, 256, 4096, 0.05))
+    q, s, z = _dev("int4_g128", pk)
+    xb, _ = inputs.activations(32, 2, 4096)
+    X = x_to_dev(xb)
+    Xl = x_to_dev(inputs.activations(33, 900, 4096)[0])
+    small, large = B.gemm_workspace_bytes("int4_g128", 2, 4096, 256), B.gemm_workspace_bytes("int4_g128", 900, 4096, 256)
+    assert 0 < small < large
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        want = B.gemm_w4a16("int4_g128", X, q, s, z).clone()
+    stream.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        got = B.gemm_w4a16("int4_g128", X, q, s, z)
+    with torch.cuda.stream(stream):
+        B.gemm_w4a16("int4_g128", Xl, q, s, z)
+        others = [torch.full(((small + 255) // 256 * 256,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    stream.synchronize()
+    got.zero_()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all((t == 0xA5).all() for t in others)
+    assert B.read_error_flags() == 0
+
+
+def test_a_replaced_workspace_is_given_back_unless_a_capture_took_it(B):
+    import weakref
+    import torch
+    ws = B.Workspace()
+    first = weakref.ref(ws.get(4096))
+    ws.get(8192)
+    assert first() is None
+    second = weakref.ref(ws.buf)
+    stream = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        ws.get(8192).add_(1)
+    ws.get(1 << 20)
+    assert second() is not None and ws.buf is not second()
