@@ -914,8 +914,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      // no tile, or nothing seen: maybe no output either, so weight 0 means not read
-      const float f = ml[k].y == 0.f ? 0.f : exp2_approx(ml[k].x - ref);
+      // no tile, or nothing seen: maybe no output either, so weight 0 means not read.  A sum that is NaN counts
+      // whatever the weight: NaN scores raise no maximum, which may be -inf, or far below the row's.
+      const bool nan = ml[k].y != ml[k].y;
+      const float f = ml[k].y == 0.f ? 0.f : nan ? ml[k].y : exp2_approx(ml[k].x - ref);
       if (f != 0.f) add = fmaf(ml[k].y, f, add);
       wt[4 * k + (lane >> 3)][lane & 7] = f;
     }

@@ -506,7 +506,8 @@ wq_status wq_qk_norm_rope_cache(wq_dtype dtype, int64_t T, int64_t Hq, int64_t H
  *     max_blocks 0: no request has own keys, both may be NULL.
  *   Cache rows past a length are not used, whatever they hold.  Rows within it are: a value
  *   that is infinite or NaN reaches every row that sees it, and of the request's own new tokens
- *   also those before it (their weight for it is 0, and 0 times it is NaN).
+ *   also those before it (their weight for it is 0, and 0 times it is NaN).  A query or key that
+ *   makes a score NaN makes O and lse of the rows that see it NaN.
  *   O [T, Hq, d] dtype, lse [T, Hq] float32 (may be NULL): contiguous outputs, distinct from Q.
  *   workspace / ws_bytes: at least wq_attn_workspace_bytes(...) bytes, under the workspace rules
  *     of wq_gemm_workspace_bytes (it starts with the same header, left at zero).

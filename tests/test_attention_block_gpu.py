@@ -666,3 +666,36 @@ def test_a_captured_graph_keeps_the_workspace_it_was_captured_with(B):
         again = step(small)
     stream.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(again, want))
+
+
+@pytest.mark.parametrize("dtype,d,requests", [("bf16", 128, 3), ("f16", 64, 3), ("bf16", 64, 340), ("f16", 128, 340)])
+@pytest.mark.parametrize("where", ["query", "only own key", "only own key, no prefix", "a run of keys", "beside a far lower score"])
+def test_attn_nan_scores_reach_every_row_that_sees_them(B, where, dtype, d, requests):
+    """A NaN score makes its rows NaN, lse too, however the line of keys is cut; all other rows keep their bits."""
+    import torch
+    lens = {"query": [40, 700, 3], "a run of keys": [9000, 64, 5], "beside a far lower score": [20, 2, 30]}.get(where, [20, 1, 30])
+    prefix = 0 if where.endswith("no prefix") else 500
+    Hq, Hkv = (8, 2) if requests == 3 else (32, 8)       # many rows are joined by other kernels than few
+    b = Batch(91, [1] * requests, prefix, lens + [1] * (requests - 3), Hq, Hkv, d, 16, dtype)
+    if where == "beside a far lower score":
+        b.q[1, :4] = 8.0
+        b.kc[int(b.table[1][0]), 0, 1] = -64.0
+    clean = [x.clone() for x in b.run(B)]
+    if requests == 3:
+        b.check(clean)
+    if where == "query":
+        b.q[1, 2, 5] = float("nan")
+        rows = [(1, 2)]
+    elif where == "a run of keys":
+        for j in range(640, 1280):
+            b.kc[int(b.table[0][j // 16]), 1, j % 16] = float("nan")
+        rows = [(0, h) for h in range(4, 8)]
+    else:
+        b.kc[int(b.table[1][0]), 0, 0] = float("nan")
+        rows = [(1, h) for h in range(4)]
+    o, lse = b.run(B)
+    hit = torch.zeros(requests, Hq, dtype=torch.bool, device="cuda")
+    for t, h in rows:
+        hit[t, h] = True
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
