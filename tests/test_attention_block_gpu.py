@@ -699,3 +699,23 @@ def test_attn_nan_scores_reach_every_row_that_sees_them(B, where, dtype, d, requ
         hit[t, h] = True
     assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
     assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
+@pytest.mark.parametrize("dtype,d,requests", [("bf16", 128, 3), ("f16", 64, 340)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_attn_nan_and_infinite_values_of_far_lower_scores(B, value, dtype, d, requests):
+    """A value that is NaN or infinite reaches its rows also where its weight is too small for float32 (0 times
+    it is NaN), in a segment of its own as in one with other keys."""
+    import torch
+    Hq, Hkv = (8, 2) if requests == 3 else (32, 8)
+    b = Batch(95, [1] * requests, 500, [20, 1, 30] + [1] * (requests - 3), Hq, Hkv, d, 16, dtype)
+    page = int(b.table[1][0])
+    b.q[1, :4] = 8.0
+    b.kc[page, 0, 0] = -64.0                   # score -4096 and below
+    clean = [x.clone() for x in b.run(B)]
+    b.vc[page, 0, 0, 7] = value
+    o, lse = b.run(B)
+    hit = torch.zeros(requests, Hq, d, dtype=torch.bool, device="cuda")
+    hit[1, :4, 7] = True
+    assert not torch.isfinite(o[hit]).any()
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse, clean[1])
