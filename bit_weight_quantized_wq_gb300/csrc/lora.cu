@@ -11,8 +11,7 @@
 //   it (one load) and gives four to each of two products; which k a fragment slot stands for is
 //   free as long as both operands agree.
 //   Rows of different adapters share a 16-row block: for each adapter that occurs in it (the lowest
-//   of its rows leads), the products run with the rows of all others set to zero, into the same
-//   accumulators.
+//   of its rows leads) the products run for all 16 rows, and its own rows take them.
 // Many rows: tcgen05 with TMA on tiles of 128 rows, an accumulator for each adapter that occurs in them; each
 // row takes its own.
 // The sum over K is split over warps and over the CTAs of a cluster; partial sums meet in shared
@@ -588,26 +587,46 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
       for (int r = 0; r < 16; ++r)
         single[r] = ((own_rows >> r) & 1u) && m0 + r < p.M && col < p.N ? p.base[first_at + static_cast<int64_t>(r) * p.N] : 0;
     }
+    // An adapter's product runs for all 16 rows, and its own rows take it, so that an infinity or a NaN in its B
+    // reaches no other's.  They take it when the next adapter's B is there: at once, the products' latency showed
+    // (64 rows of 48 adapters, whole call: 26.7 us instead of 24.9).
+    float prod[4][4];
+    int of = -2;                               // no row's adapter
+    const auto take = [&] {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][e] = id[e >> 1] == of ? prod[t][e] : acc[t][e];
+    };
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) prod[t][e] = 0.f;
 #pragma unroll 1
     for (uint32_t todo = list; todo; todo &= todo - 1) {
-      const int a = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
-      const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
         fetch_b();
         copy_commit();
         copy_wait<kBQueue - 1>();              // groups up to s + 1: the B of step s among them
-        const uint4 x0 = id[0] == a ? v[ch][0] : zero, x1 = id[1] == a ? v[ch][1] : zero;
+        if (ch == 0) {
+          take();
+          of = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], x0, x1, bq[(b_at * 4 + t) * 256]);
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) prod[t][e] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) mma_k32<F16>(prod[t], v[ch][0], v[ch][1], bq[(b_at * 4 + t) * 256]);
         if constexpr (LO) {
-          const uint4 y0 = id[0] == a ? vl[ch][0] : zero, y1 = id[1] == a ? vl[ch][1] : zero;
 #pragma unroll
-          for (int t = 0; t < 4; ++t) mma_k32<F16>(acc[t], y0, y1, bq[(b_at * 4 + t) * 256]);
+          for (int t = 0; t < 4; ++t) mma_k32<F16>(prod[t], vl[ch][0], vl[ch][1], bq[(b_at * 4 + t) * 256]);
         }
         b_at = b_at + 1 == kBQueue ? 0 : b_at + 1;
       }
     }
+    take();
     if (!list) {
       copy_commit();
       copy_wait<kBQueue - 1>();

@@ -719,3 +719,26 @@ def test_attn_nan_and_infinite_values_of_far_lower_scores(B, value, dtype, d, re
     hit[1, :4, 7] = True
     assert not torch.isfinite(o[hit]).any()
     assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse, clean[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,N,r,L,kind", [(5, 128, 64, 8, 3, "mixed"), (16, 512, 256, 16, 16, "each"), (64, 256, 96, 40, 48, "each"),
+                                            (40, 128, 33, 72, 20, "each"), (200, 128, 9001, 16, 5, "mixed"),
+                                            (300, 128, 8200, 40, 4, "runs"), (1100, 1024, 72, 64, 6, "mixed")])
+def test_lora_one_adapters_infinities_stay_its_own(B, M, K, N, r, L, kind, dtype):
+    import torch
+    (a, b, s), _ = _adapter_set(M, L, r, K, N, dtype)
+    x, _ = _rand(M + 50, (M, K), dtype)
+    base, _ = _rand(M + 60, (M, N), dtype)
+    who = _who(kind, M, L, M)
+    who[M // 2] = 1
+    ad = torch.from_numpy(who).cuda()
+    good = B.lora_add(base, x, a, b, ad, s)
+    b[1, 3, 2], b[1, 5, 1], b[1, N - 1, r - 1] = float("inf"), float("nan"), float("-inf")
+    y = B.lora_add(base, x, a, b, ad, s)
+    mine = ad == 1
+    assert torch.equal(y[~mine], good[~mine])
+    broken = [3, 5, N - 1]
+    assert not torch.isfinite(y[mine][:, broken]).any()
+    rest = [n for n in range(N) if n not in broken]
+    assert torch.equal(y[mine][:, rest], good[mine][:, rest])
