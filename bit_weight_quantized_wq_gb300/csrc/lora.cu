@@ -79,15 +79,18 @@ __device__ __forceinline__ int row_adapter(const LoraArgs& p, int m) {
   }
   return a;
 }
-// Its rank, forced into range and rounded up to 8.
+// Its rank, forced into range.
 __device__ __forceinline__ int checked_rank(const LoraArgs& p, int rank) {
   if (rank < 0 || rank > p.r) {
     atomicOr(&g_lora_err, kErrIndex);
     rank = min(max(rank, 0), p.r);
   }
-  return (rank + 7) & ~7;
+  return rank;
 }
 __device__ __forceinline__ int adapter_rank(const LoraArgs& p, int a) { return checked_rank(p, p.ranks ? __ldg(p.ranks + a) : p.r); }
+__device__ __forceinline__ int up8(int rank) { return (rank + 7) & ~7; }
+// What v's rounding to `hi` left: nothing where that is infinite (inf - inf would make the sum of the parts NaN).
+__device__ __forceinline__ float rest(float v, float hi) { return fabsf(hi) == INFINITY ? 0.f : v - hi; }
 // Lanes whose adapter occurs in the warp's rows for the first time (lanes with -1 never lead).
 __device__ __forceinline__ uint32_t leaders(int a) {
   const uint32_t same = __match_any_sync(0xffffffffu, a);
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
   } else {
     rank = adapter_rank(p, a);
   }
-  const int tiles = rank / 8;
+  const int tiles = up8(rank) / 8;
   const uint32_t rows = __ballot_sync(0xffffffffu, mine == a);
   float acc[NT][4];
 #pragma unroll
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
     uint16_t* to = V + static_cast<int64_t>(m0 + row) * (p.r + p.lo) + j;
     const uint32_t hi = pack2<F16>(v, 0.f);
     to[0] = static_cast<uint16_t>(hi);
-    if (p.lo) to[p.lo] = round1<F16>(v - unpack2<F16>(hi).x);
+    if (p.lo) to[p.lo] = round1<F16>(rest(v, unpack2<F16>(hi).x));
   }
   if (n > 1) cluster_sync();                  // the others have read this CTA's sums
 }
@@ -432,13 +435,13 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
     const int rank = sm.rank[r] - j0;
     const float* src = sm.red + r * kTileLd + 2 * lane;
     float2 v = n > 1 ? make_float2(sum_cluster(src, n), sum_cluster(src + 1, n)) : make_float2(src[0], src[1]);
-    v = 2 * lane < rank ? make_float2(v.x * s, v.y * s) : make_float2(0.f, 0.f);
+    v = make_float2(2 * lane < rank ? v.x * s : 0.f, 2 * lane + 1 < rank ? v.y * s : 0.f);
     if (2 * lane < p.r - j0) {
       uint16_t* to = V + static_cast<int64_t>(m) * (p.r + p.lo) + j0 + 2 * lane;
       const uint32_t hi = pack2<F16>(v.x, v.y);
       const float2 f = unpack2<F16>(hi);
       *reinterpret_cast<uint32_t*>(to) = hi;
-      if (p.lo) *reinterpret_cast<uint32_t*>(to + p.lo) = pack2<F16>(v.x - f.x, v.y - f.y);
+      if (p.lo) *reinterpret_cast<uint32_t*>(to + p.lo) = pack2<F16>(rest(v.x, f.x), rest(v.y, f.y));
     }
   }
   if (n > 1) cluster_sync();                   // the others have read this CTA's sums
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
   pdl_launch_dependents();
   if (m0 >= p.M || ct0 >= ct1) return;         // whole warps
   const int mine = lane < 16 ? row_adapter(p, m0 + lane) : -1;
-  const int my_rank = mine >= 0 ? adapter_rank(p, mine) : 0;
+  const int my_rank = mine >= 0 ? up8(adapter_rank(p, mine)) : 0;
   uint32_t list = 0;                           // this subset's leading rows
   {
     uint32_t lead = leaders(mine);

@@ -742,3 +742,22 @@ def test_lora_one_adapters_infinities_stay_its_own(B, M, K, N, r, L, kind, dtype
     assert not torch.isfinite(y[mine][:, broken]).any()
     rest = [n for n in range(N) if n not in broken]
     assert torch.equal(y[mine][:, rest], good[mine][:, rest])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,rank", [(4, 64, 8), (4, 64, 5), (700, 2048, 13)])
+def test_lora_infinite_inner_products(B, M, K, rank, dtype):
+    """An infinity in X gives an infinite sum where the definition does, not NaN: neither from what an infinite
+    value's rounding leaves, nor from the zeros past an adapter's rank."""
+    import torch
+    r = (rank + 7) // 8 * 8
+    (a, b, s), _ = _adapter_set(7, 2, r, K, 48, dtype)
+    a[:, :, 0], b = 0.5, b.abs() + 0.01
+    a[:, rank:], b[:, :, rank:] = 0, 0
+    x, _ = _rand(8, (M, K), dtype)
+    x[2, 0] = float("inf")
+    base, _ = _rand(9, (M, 48), dtype)
+    ad = torch.ones(M, dtype=torch.int32, device="cuda")
+    ad[0], ad[1] = 0, -1
+    y = B.lora_add(base, x, a, b, ad, s, ranks=torch.tensor([rank, rank], dtype=torch.int32, device="cuda"))
+    assert (y[2] == float("inf")).all() and torch.isfinite(y[torch.arange(M) != 2]).all()
