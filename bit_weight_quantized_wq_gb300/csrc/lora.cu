@@ -19,6 +19,9 @@
 // scale): it is an operand of the second product, which takes 16 bits.  For few rows, and where base itself
 // comes rounded from the quantized layer of the same call, V is kept in two such parts, itself and what
 // its rounding left (`lo`): base's rounding and the result's are then the only ones that count.
+// fp16 has no room for inner products from 65520 on, where Y may well be ordinary: each row of V, by halves of
+// 64 ranks, is kept divided by a power of two that brings its largest value below 2^15 (1 where it is already),
+// and the expand multiplies its sums by it in float32.
 //
 // Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.6 us (launches and dependent loads); 64 rows of
 // 48 adapters of rank 32 on 4096 x 28672 24.5 us, 3.6 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
@@ -91,6 +94,33 @@ __device__ __forceinline__ int adapter_rank(const LoraArgs& p, int a) { return c
 __device__ __forceinline__ int up8(int rank) { return (rank + 7) & ~7; }
 // What v's rounding to `hi` left: nothing where that is infinite (inf - inf would make the sum of the parts NaN).
 __device__ __forceinline__ float rest(float v, float hi) { return fabsf(hi) == INFINITY ? 0.f : v - hi; }
+// fp16: the power of two by which a row of V is divided, from the largest finite size in each lane.  All lanes.
+__device__ __forceinline__ float row_power(float most) {
+  if (!__any_sync(0xffffffffu, most >= 32768.f)) return 1.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  return __uint_as_float(((__float_as_uint(most) >> 23) - 14) << 23);      // most is in 2^14 .. 2^15 of it
+}
+__device__ __forceinline__ float inverse_power(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+__device__ __forceinline__ float finite_size(float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.f; }
+// The rows' powers follow V in the scratch: [2][M], by halves of 64 ranks.
+__host__ __device__ inline int64_t v_elements(const LoraArgs& p) { return (static_cast<int64_t>(p.M) * (p.r + p.lo) + 7) / 8 * 8; }
+__device__ __forceinline__ float* powers(const LoraArgs& p, uint16_t* V) { return reinterpret_cast<float*>(V + v_elements(p)); }
+__device__ __forceinline__ const float* powers(const LoraArgs& p, const uint16_t* V) { return reinterpret_cast<const float*>(V + v_elements(p)); }
+// 8 fp16 values times a power of two of at most 1.
+__device__ __forceinline__ void scale_f16(uint4& x, float by) {
+  const auto each = [&](uint32_t& w) {
+    const float2 f = unpack2<true>(w);
+    w = pack2<true>(f.x * by, f.y * by);
+  };
+  each(x.x), each(x.y), each(x.z), each(x.w);
+}
+// Row m's, of all its ranks.
+__device__ __forceinline__ float row_power(const LoraArgs& p, const uint16_t* V, int m) {
+  const float* at = powers(p, V) + m;
+  const float a = __ldcg(at);
+  return p.r > 64 ? fmaxf(a, __ldcg(at + p.M)) : a;
+}
 // Lanes whose adapter occurs in the warp's rows for the first time (lanes with -1 never lead).
 __device__ __forceinline__ uint32_t leaders(int a) {
   const uint32_t same = __match_any_sync(0xffffffffu, a);
@@ -171,9 +201,12 @@ __device__ __forceinline__ void shrink_loop(float (&acc)[NT][4], const LoraArgs&
 // Few rows: one cluster for each row that leads its adapter in its 16-row block; 8 warps a CTA, each
 // a slice of K.  12 us by itself for 48 adapters of rank 32, K 4096 (10 MB of A): adapter, rank and A are
 // loads that wait for one another, and the cluster meets twice.
+// Two CTAs an SM are asked for so that the compiler keeps a step's loads in registers, all under way; left to
+// itself it took 86 to 114 registers, by what else stood in the kernel, and loaded in turns (13 rows of rank 48,
+// K 4992: 13.9 us instead of 9.9; 64 rows of rank 32: 23.1 instead of 22.5).
 constexpr int kRowWarps = 8;
 template <bool F16, int NT>
-__global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraArgs p, uint16_t* V) {
+__global__ void __launch_bounds__(32 * kRowWarps, NT <= 8 ? 2 : 1) k_lora_shrink_rows(const LoraArgs p, uint16_t* V) {
   extern __shared__ float red[];              // [warp][16][8 NT], then the CTA's sum over [0]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
   pdl_wait();
@@ -227,15 +260,30 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_lora_shrink_rows(const LoraA
   if (n > 1) cluster_sync();
   else __syncthreads();
   const float s = __ldg(p.scales + a);
-  for (int i = threadIdx.x * n + cluster_rank(); i < 16 * W; i += blockDim.x * n) {
-    const int row = i / W, j = i % W;
-    if (!((rows >> row) & 1u) || j >= p.r) continue;
-    float v = 0.f;                            // past the rank: the expand of many rows takes all r
-    if (j < rank) v = (n > 1 ? sum_cluster(red + i, n) : red[i]) * s;
-    uint16_t* to = V + static_cast<int64_t>(m0 + row) * (p.r + p.lo) + j;
-    const uint32_t hi = pack2<F16>(v, 0.f);
-    to[0] = static_cast<uint16_t>(hi);
-    if (p.lo) to[p.lo] = round1<F16>(rest(v, unpack2<F16>(hi).x));
+  for (int row = cluster_rank() + n * warp; row < 16; row += n * kRowWarps) {     // a warp a row
+    if (!((rows >> row) & 1u)) continue;
+    float v[W / 32], most = 0.f;
+#pragma unroll
+    for (int c = 0; c < W / 32; ++c) {
+      const int j = 32 * c + lane;
+      v[c] = 0.f;                             // past the rank: the expand of many rows takes all r
+      if (j < rank) v[c] = (n > 1 ? sum_cluster(red + row * W + j, n) : red[row * W + j]) * s;
+      if constexpr (F16) most = fmaxf(most, finite_size(v[c]));
+    }
+    if constexpr (F16) {
+      const float up = row_power(most);
+#pragma unroll
+      for (int c = 0; c < W / 32; ++c) v[c] *= inverse_power(up);
+      if (lane < 2) powers(p, V)[static_cast<int64_t>(lane) * p.M + m0 + row] = up;
+    }
+    uint16_t* to = V + static_cast<int64_t>(m0 + row) * (p.r + p.lo) + lane;
+#pragma unroll
+    for (int c = 0; c < W / 32; ++c) {
+      if (32 * c + lane >= p.r) continue;
+      const uint32_t hi = pack2<F16>(v[c], 0.f);
+      to[32 * c] = static_cast<uint16_t>(hi);
+      if (p.lo) to[32 * c + p.lo] = round1<F16>(rest(v[c], unpack2<F16>(hi).x));
+    }
   }
   if (n > 1) cluster_sync();                  // the others have read this CTA's sums
 }
@@ -436,6 +484,11 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
     const float* src = sm.red + r * kTileLd + 2 * lane;
     float2 v = n > 1 ? make_float2(sum_cluster(src, n), sum_cluster(src + 1, n)) : make_float2(src[0], src[1]);
     v = make_float2(2 * lane < rank ? v.x * s : 0.f, 2 * lane + 1 < rank ? v.y * s : 0.f);
+    if constexpr (F16) {
+      const float up = row_power(fmaxf(finite_size(v.x), finite_size(v.y))), down = inverse_power(up);
+      v.x *= down, v.y *= down;
+      if (lane == 0) powers(p, V)[static_cast<int64_t>(blockIdx.z) * p.M + m] = up;
+    }
     if (2 * lane < p.r - j0) {
       uint16_t* to = V + static_cast<int64_t>(m) * (p.r + p.lo) + j0 + 2 * lane;
       const uint32_t hi = pack2<F16>(v.x, v.y);
@@ -461,7 +514,7 @@ constexpr int kBQueue = 4, kBaseQueue = 4;   // see the waits below
 constexpr int kStageLd = 33;
 static_assert(8 * 16 * kStageLd * 4 <= kBaseQueue * 2 * 256 * 16, "the staged rows take the base queue's place");
 template <bool F16, int CH, bool LO>     // CH: chunks of 32 ranks; LO: V in two parts
-__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uint16_t* V, int log_rows, int log_subsets, int span) {
+__global__ void __launch_bounds__(256, CH * (LO ? 2 : 1) <= 2 ? 2 : 1) k_lora_expand(const LoraArgs p, const uint16_t* V, int log_rows, int log_subsets, int span) {
   extern __shared__ __align__(16) uint8_t expand_smem[];
   uint4* bq = reinterpret_cast<uint4*>(expand_smem) + threadIdx.x;              // [step][4][256]
   uint4* baseq = bq + kBQueue * 4 * 256;                                        // [tile][2][256]
@@ -559,6 +612,14 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
   copy_commit();
   const int id[2] = {__shfl_sync(0xffffffffu, mine, g), __shfl_sync(0xffffffffu, mine, g + 8)};
   const int ranks[2] = {__shfl_sync(0xffffffffu, my_rank, g), __shfl_sync(0xffffffffu, my_rank, g + 8)};
+  float half_up[2][CH == 4 ? 2 : 1];
+  if constexpr (F16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < (CH == 4 ? 2 : 1); ++c)
+        half_up[h][c] = own[h] && id[h] >= 0 ? __ldcg(powers(p, V) + static_cast<int64_t>(c) * p.M + m0 + 8 * h + g) : 1.f;
+  }
   uint4 v[CH][2], vl[LO ? CH : 1][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -572,6 +633,24 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
         if constexpr (LO) vl[ch][h] = __ldcg(reinterpret_cast<const uint4*>(from + p.lo));
       }
     }
+  // fp16: the power of two that the row's sums are multiplied by; halves of its ranks that were divided by
+  // different ones are brought to the larger
+  float up[2] = {1.f, 1.f};
+  if constexpr (F16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      up[h] = CH == 4 ? fmaxf(half_up[h][0], half_up[h][CH / 4]) : half_up[h][0];
+      if constexpr (CH == 4) {
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+          const float down = half_up[h][ch / 2] * inverse_power(up[h]);
+          if (down == 1.f) continue;
+          scale_f16(v[ch][h], down);
+          if constexpr (LO) scale_f16(vl[ch][h], down);
+        }
+      }
+    }
+  }
   const int steps = max(1, __popc(list) * CH);   // a tile
   int b_at = 0, base_at = 0;
 #pragma unroll 1
@@ -649,7 +728,8 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const float2 f = unpack2<F16>(w[t]);
-            w[t] = pack2<F16>(f.x + acc[t][2 * h], f.y + acc[t][2 * h + 1]);
+            if constexpr (F16) w[t] = pack2<F16>(fmaf(acc[t][2 * h], up[h], f.x), fmaf(acc[t][2 * h + 1], up[h], f.y));
+            else w[t] = pack2<F16>(f.x + acc[t][2 * h], f.y + acc[t][2 * h + 1]);
           }
         }
         *reinterpret_cast<uint4*>(p.Y + static_cast<int64_t>(m) * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -660,7 +740,7 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs p, const uin
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) stage[(8 * h + g) * kStageLd + 8 * q + 2 * t + e] = acc[t][2 * h + e];
+          for (int e = 0; e < 2; ++e) stage[(8 * h + g) * kStageLd + 8 * q + 2 * t + e] = acc[t][2 * h + e] * up[h];
       __syncwarp();
 #pragma unroll
       for (int r = 0; r < 16; ++r)
@@ -701,7 +781,7 @@ template <bool F16, int CR, bool LO>
 __global__ void __launch_bounds__(kExThreads, CR == 1 && !LO ? 2 : 1)
     k_lora_expand_tile(const __grid_constant__ CUtensorMap tbase, const __grid_constant__ CUtensorMap ty,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tvl,
-                       const __grid_constant__ CUtensorMap tb, const LoraArgs p, int span, int base_ready) {
+                       const __grid_constant__ CUtensorMap tb, const LoraArgs p, const uint16_t* V, int span, int base_ready) {
   using S = ExpandSmem<CR, LO>;
   constexpr int kParts = LO ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -773,7 +853,27 @@ __global__ void __launch_bounds__(kExThreads, CR == 1 && !LO ? 2 : 1)
             tma_load_2d(sm.v[part][c], part ? &tvl : &tv, 64 * c, m0, &sm.v_full, l2_policy_evict_first());
       }
       __syncwarp();
+      float half_up[4][2];                     // of rows lane, lane + 32, ...
+      if constexpr (F16 && CR == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            half_up[i][c] = sm.place[32 * i + lane] >= 0 ? __ldcg(powers(p, V) + static_cast<int64_t>(c) * p.M + m0 + 32 * i + lane) : 1.f;
+      }
       ok = wait(&sm.v_full, 0, kErrWaitFull);
+      if constexpr (F16 && CR == 2) {          // halves of a row's ranks that were divided by different powers
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float down = inverse_power(fmaxf(half_up[i][0], half_up[i][1]));
+          if (!ok || half_up[i][0] == half_up[i][1]) continue;
+          const int c = half_up[i][0] < half_up[i][1] ? 0 : 1;
+          for (int k = 0; k < kParts * 8; ++k)
+            scale_f16(*reinterpret_cast<uint4*>(sm.v[k >> 3][c] + (32 * i + lane) * 128 + 16 * (k & 7)), half_up[i][c] * down);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
     }
     constexpr uint32_t fmt = F16 ? 0u : 1u;
     constexpr uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((kExCols >> 3) << 17) | ((kTileRows >> 4) << 24);
@@ -821,6 +921,11 @@ __global__ void __launch_bounds__(kExThreads, CR == 1 && !LO ? 2 : 1)
     // -------------------------------------------------------------------- base + acc, a row a thread
     const int group = warp >> 2;
     place = sm.place[row];
+    float up = 1.f;
+    if constexpr (F16) {
+      pdl_wait();
+      if (place >= 0) up = row_power(p, V, m0 + row);
+    }
     uint32_t use = 0;
     for (int i = group; i < tiles && ok; i += 2) {
       const int s = i % kExBase;
@@ -847,7 +952,8 @@ __global__ void __launch_bounds__(kExThreads, CR == 1 && !LO ? 2 : 1)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                   const float2 f = unpack2<F16>(w[t]);
-                  w[t] = pack2<F16>(f.x + __uint_as_float(v[8 * c + 2 * t]), f.y + __uint_as_float(v[8 * c + 2 * t + 1]));
+                  const float a0 = __uint_as_float(v[8 * c + 2 * t]), a1 = __uint_as_float(v[8 * c + 2 * t + 1]);
+                  w[t] = F16 ? pack2<F16>(fmaf(a0, up, f.x), fmaf(a1, up, f.y)) : pack2<F16>(f.x + a0, f.y + a1);
                 }
                 *q = make_uint4(w[0], w[1], w[2], w[3]);
               }
@@ -975,7 +1081,7 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
     const auto launch = [&](auto kern, size_t smem) {
       const cudaError_t se = set_smem_attr_once(reinterpret_cast<const void*>(kern), smem);
       if (se != cudaSuccess) return se;
-      return launch_pdl(kern, grid, kExThreads, smem, stream, tbase, ty, tv, tvl, tb, a, static_cast<int>(span), base_ready ? 1 : 0);
+      return launch_pdl(kern, grid, kExThreads, smem, stream, tbase, ty, tv, tvl, tb, a, V, static_cast<int>(span), base_ready ? 1 : 0);
     };
     if (a.lo) {
       if (a.r <= 64) return launch(k_lora_expand_tile<F16, 1, true>, sizeof(ExpandSmem<1, true>) + 1024);
@@ -1009,8 +1115,9 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
 
 bool lora_many_rows(int64_t M, int64_t L) { return M > kFewRows && (M / kRowsAdapter >= L || M > kMostRows); }
 
+// V, then the rows' powers of two (fp16).
 size_t lora_scratch_bytes(int64_t M, int64_t v_width) {
-  return (static_cast<size_t>(M) * v_width * sizeof(uint16_t) + 255) / 256 * 256;
+  return (static_cast<size_t>(M) * v_width * sizeof(uint16_t) + 16 + static_cast<size_t>(M) * 2 * sizeof(float) + 255) / 256 * 256;
 }
 
 cudaError_t launch_lora_shrink(int dtype, const LoraArgs& a, void* scratch, cudaStream_t stream) {

@@ -537,8 +537,9 @@ wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_str
  *   X [M, K]; A [L, r, K], B [L, N, r] dtype: L adapters of up to r ranks.
  *   ranks [L] int32 (may be NULL: all r): adapter a's own rank; its rows of A and columns of B
  *     from there on must hold zeros (the kernels skip whole blocks of 8 of them).
- *   X A^T is rounded to the element type once when M > 512 and (M >= 32 L or M > 16384), and else, as in
- *     every wq_gemm_w4a16_lora, kept in two parts of it.
+ *   scales[a] X A^T is rounded to the element type once when M > 512 and (M >= 32 L or M > 16384), and else, as
+ *     in every wq_gemm_w4a16_lora, kept in two parts of it.  In fp16 a power of two a row keeps it in range, so
+ *     only Y itself can overflow.
  *   adapter [M] int32, -1 .. L - 1: rows of one request need not be neighbours, but are served
  *     best when they are.    scales [L] float32.
  *   workspace / ws_bytes: at least wq_lora_workspace_bytes(M, K, N, r) bytes, under the workspace

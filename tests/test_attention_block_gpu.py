@@ -761,3 +761,26 @@ def test_lora_infinite_inner_products(B, M, K, rank, dtype):
     ad[0], ad[1] = 0, -1
     y = B.lora_add(base, x, a, b, ad, s, ranks=torch.tensor([rank, rank], dtype=torch.int32, device="cuda"))
     assert (y[2] == float("inf")).all() and torch.isfinite(y[torch.arange(M) != 2]).all()
+
+
+@pytest.mark.parametrize("M,K,N,r,L,kind", [(3, 256, 64, 8, 2, "mixed"), (16, 512, 256, 16, 16, "each"), (40, 512, 33, 72, 3, "mixed"),
+                                            (130, 264, 640, 128, 3, "runs"), (700, 256, 200, 24, 6, "runs"),
+                                            (1100, 1024, 328, 64, 7, "runs"), (1100, 1024, 41, 96, 7, "runs"),
+                                            (1300, 1032, 104, 128, 9, "runs")])
+def test_lora_f16_inner_products_beyond_the_type(B, M, K, N, r, L, kind):
+    """s X A^T from some 10^2 to 10^7, by row and by half of the ranks, with B small: the result is ordinary."""
+    import torch
+    a = torch.randn((L, r, K), generator=torch.Generator().manual_seed(M)) * K ** -0.5
+    a[:, :r // 2] *= torch.tensor([1.0, 200.0, 0.01])[torch.arange(L) % 3][:, None, None]
+    b = torch.randn((L, N, r), generator=torch.Generator().manual_seed(M + 1)) * 2e-4
+    a, b = a.half(), b.half()
+    s = 0.25 + torch.rand(L, generator=torch.Generator().manual_seed(M + 2))
+    x = (torch.randn((M, K), generator=torch.Generator().manual_seed(M + 3))
+         * torch.tensor([1.0, 3e3, 1.2e4, 30.0])[torch.arange(M) % 4][:, None]).half()
+    base, basef = _rand(M + 60, (M, N), "f16")
+    who = _who(kind, M, L, M)
+    y = B.lora_add(base, x.cuda(), a.cuda(), b.cuda(), torch.from_numpy(who).cuda(), s.cuda())
+    delta, dabs = ab.adapters(x.double().numpy(), a.double().numpy(), b.double().numpy(), who, s.double().numpy())
+    ref, u = basef + delta, U["f16"]
+    assert np.abs(ref).max() < 60000
+    _within(_host(y), ref, u * np.abs(ref) + (u + 1e-5) * dabs, "Y")
