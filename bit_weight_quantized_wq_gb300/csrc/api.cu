@@ -578,6 +578,9 @@ static bool page_ok(int64_t page_size) {
   return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128;
 }
 
+// Index and scale arrays are read 4 bytes at a time.
+static bool odd4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
 // Two byte ranges share a byte.
 static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -596,7 +599,7 @@ static wq_status check_rope(wq_dtype dtype, int64_t T, int64_t Hq, int64_t Hkv, 
   if (q_stride < Hq * d || k_stride < Hkv * d || q_stride % 8 != 0 || k_stride % 8 != 0 || q_stride > (1LL << 40) ||
       k_stride > (1LL << 40))
     return WQ_ERR_SHAPE;
-  if (!aligned16(Q) || !aligned16(K) || !aligned16(cos_sin) || !aligned16(positions) || !aligned16(Qo) ||
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(cos_sin) || odd4(positions) || !aligned16(Qo) ||
       (q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)))
     return WQ_ERR_ALIGN;
   const size_t q_bytes = (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2;
@@ -656,7 +659,7 @@ wq_status wq_qk_norm_rope_cache(wq_dtype dtype, int64_t T, int64_t Hq, int64_t H
   if (!V || !k_cache || !v_cache || !slots) return WQ_ERR_NULL;
   if (v_stride < Hkv * d || v_stride % 8 != 0 || v_stride > (1LL << 40)) return WQ_ERR_SHAPE;
   if (!page_ok(page_size) || pages < 1 || pages > 0x7fffffffLL / page_size) return WQ_ERR_SHAPE;
-  if (!aligned16(V) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(slots)) return WQ_ERR_ALIGN;
+  if (!aligned16(V) || !aligned16(k_cache) || !aligned16(v_cache) || odd4(slots)) return WQ_ERR_ALIGN;
   const size_t q_in = (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2, q_out = static_cast<size_t>(T) * Hq * d * 2;
   const size_t k_in = (static_cast<size_t>(T - 1) * k_stride + Hkv * d) * 2;
   const size_t v_in = (static_cast<size_t>(T - 1) * v_stride + Hkv * d) * 2;
@@ -703,7 +706,6 @@ wq_status wq_attn_shared_prefix(wq_dtype dtype, const uint16_t* Q, int64_t q_str
   if (!q_start && (T != R || max_new != 1)) return WQ_ERR_SHAPE;
   if (!wq::attn_prefix_fits(T, Hq, Hkv, prefix_len)) return WQ_ERR_SHAPE;
   if ((prefix_len > 0 && !prefix_pages) || (max_blocks > 0 && (!block_table || !suffix_lens))) return WQ_ERR_NULL;
-  const auto odd4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
   if (!aligned16(Q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(O) || odd4(lse) || odd4(prefix_pages) ||
       odd4(block_table) || odd4(suffix_lens) || odd4(q_start))
     return WQ_ERR_ALIGN;
@@ -738,7 +740,6 @@ static wq_status check_lora(const uint16_t* X, int64_t M, int64_t K, int64_t N, 
                             const uint16_t* Y) {
   if (!X || !A || !B || !adapter || !scales || !Y) return WQ_ERR_NULL;
   if (!lora_shape_ok(M, K, N, r) || L < 1 || L * r > 0x7fffff00LL || L > (1 << 24)) return WQ_ERR_SHAPE;
-  const auto odd4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
   if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || odd4(ranks) || odd4(adapter) || odd4(scales))
     return WQ_ERR_ALIGN;
   return WQ_OK;

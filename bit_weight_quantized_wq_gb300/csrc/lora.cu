@@ -203,7 +203,7 @@ __device__ __forceinline__ void shrink_loop(float (&acc)[NT][4], const LoraArgs&
 // loads that wait for one another, and the cluster meets twice.
 // Two CTAs an SM are asked for so that the compiler keeps a step's loads in registers, all under way; left to
 // itself it took 86 to 114 registers, by what else stood in the kernel, and loaded in turns (13 rows of rank 48,
-// K 4992: 13.9 us instead of 9.9; 64 rows of rank 32: 23.1 instead of 22.5).
+// K 4992: 13.9 us instead of 9.6; 64 rows of rank 32: 23.1 instead of 22.5).
 constexpr int kRowWarps = 8;
 template <bool F16, int NT>
 __global__ void __launch_bounds__(32 * kRowWarps, NT <= 8 ? 2 : 1) k_lora_shrink_rows(const LoraArgs p, uint16_t* V) {

@@ -446,6 +446,7 @@ wq_status wq_gemm_w4a4_mxfp4(const uint16_t* X, int64_t M, int64_t K, int64_t N,
  *   - dtype: the 16-bit type of every uint16_t array of the call (bf16 or IEEE fp16).
  *   - A cache is two arrays k_cache, v_cache [pages, Hkv, page_size, d]; token `at` of page `p`
  *     has slot number p * page_size + at.  page_size is 16, 32, 64 or 128.
+ *   - Arrays are 16-byte aligned; those of int32, the adapters' scales and lse 4-byte.
  *   - Indices that live on the device (positions, slots, adapters, pages, lengths) are checked
  *     by the kernels: one outside its range never makes a kernel leave its arrays; bit 1 << 7 of
  *     the error word (wq_read_error_flags) is set and the outputs that depend on the index are

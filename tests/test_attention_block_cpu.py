@@ -175,3 +175,10 @@ def test_lora_refusals(lib):
     need = lib.wq_gemm_w4a16_lora_workspace_bytes(0, 4, 128, 64, 16)
     assert need > lib.wq_gemm_workspace_bytes(0, 4, 128, 64)
     assert lib.wq_gemm_w4a16_lora_workspace_bytes(7, 4, 128, 64, 16) == 0
+
+
+def test_rope_index_arrays_are_refused_only_off_4_bytes(lib):
+    """The accepted addresses get as far as the check for overlaps, which refuses these calls (nothing is launched)."""
+    for odd in (4, 8, 12):
+        assert _rope(lib, pos=_p(3, odd), Qo=_p(0, 1024)) == 7 and _rope_cache(lib, slots=_p(4, odd), vc=_p(2)) == 7
+    assert _rope(lib, pos=_p(3, 2), Qo=_p(0, 1024)) == 3 and _rope_cache(lib, slots=_p(4, 1), vc=_p(2)) == 3

@@ -784,3 +784,20 @@ def test_lora_f16_inner_products_beyond_the_type(B, M, K, N, r, L, kind):
     ref, u = basef + delta, U["f16"]
     assert np.abs(ref).max() < 60000
     _within(_host(y), ref, u * np.abs(ref) + (u + 1e-5) * dabs, "Y")
+
+
+def test_rope_positions_and_slots_need_their_own_alignment_only(B):
+    import torch
+    q, _ = _rand(1, (5, 2, 64), "bf16")
+    k, _ = _rand(2, (5, 1, 64), "bf16")
+    kc, vc = torch.zeros(2, 2, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    kc2, vc2 = torch.zeros(2, 2, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    tab = _table(16, 64)
+    pos = torch.tensor([9, 3, 5, 1, 0, 7], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([0, 0, 0, 17, 4, 31, -1, 2], dtype=torch.int32, device="cuda")
+    want = B.qk_norm_rope(q, k, pos[1:].clone(), tab)
+    got = B.qk_norm_rope(q, k, pos[1:], tab)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    want = B.qk_norm_rope_cache(q, k, k, pos[1:].clone(), tab, kc, vc, slots[3:].clone())
+    got = B.qk_norm_rope_cache(q, k, k, pos[1:], tab, kc2, vc2, slots[3:])
+    assert torch.equal(got, want) and torch.equal(kc2, kc) and torch.equal(vc2, vc)
