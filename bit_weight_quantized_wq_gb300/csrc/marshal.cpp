@@ -61,6 +61,15 @@ double number(PyObject* o, const char* name) {
   return v;
 }
 
+int truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be true or false");
+  }
+  return v;
+}
+
 // `t` on device `dev` with the given type and shape, contiguous.
 void need(const at::Tensor& t, const char* name, int dev, at::ScalarType dtype, at::IntArrayRef shape, bool contiguous = true) {
   if (!t.is_cuda() || t.get_device() != dev)
@@ -165,7 +174,7 @@ Rope rope_inputs(PyObject* const* a) {
   r.positions = tensor(a[2], "positions"), r.cos_sin = tensor(a[3], "cos_sin");
   r.wq = optional(a[4], "q_weight"), r.wk = optional(a[5], "k_weight");
   r.eps = static_cast<float>(number(a[6], "eps"));
-  r.interleaved = PyObject_IsTrue(a[7]) == 1;
+  r.interleaved = truth(a[7], "interleaved");
   r.dt = dtype16(r.Q, "Q");
   r.qs = head_stride(r.Q, "Q"), r.ks = head_stride(r.K, "K");
   r.T = r.Q.size(0), r.Hq = r.Q.size(1), r.d = r.Q.size(2), r.Hkv = r.K.size(1);

@@ -801,3 +801,11 @@ def test_rope_positions_and_slots_need_their_own_alignment_only(B):
     want = B.qk_norm_rope_cache(q, k, k, pos[1:].clone(), tab, kc, vc, slots[3:].clone())
     got = B.qk_norm_rope_cache(q, k, k, pos[1:], tab, kc2, vc2, slots[3:])
     assert torch.equal(got, want) and torch.equal(kc2, kc) and torch.equal(vc2, vc)
+
+
+def test_rope_refuses_a_pairing_that_is_no_truth_value(B):
+    import torch
+    q, _ = _rand(1, (3, 2, 64), "bf16")
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        B.qk_norm_rope(q, q, pos, _table(8, 64), interleaved=np.array([True, False]))
