@@ -31,3 +31,37 @@ def assert_close(y, ref, what="", extra=None):
         raise AssertionError("%s: %d of %d outputs outside tolerance; worst at %s: y=%r ref=%r"
                              % (what, int(bad.sum()), bad.size, i, y[i], ref[i]))
     return float((err / lim).max()) if err.size else 0.0
+
+
+def kernels_of(graph):
+    """Names of the kernels that a captured torch.cuda.CUDAGraph(keep_graph=True) launches, from the driver's
+    graph queries."""
+    import ctypes
+
+    cu = ctypes.CDLL("libcuda.so.1")
+
+    class Params(ctypes.Structure):               # CUDA_KERNEL_NODE_PARAMS_v2
+        _fields_ = ([("func", ctypes.c_void_p)] + [(n, ctypes.c_uint) for n in ("gx", "gy", "gz", "bx", "by", "bz", "smem")]
+                    + [(n, ctypes.c_void_p) for n in ("params", "extra", "kern", "ctx")])
+
+    def call(name, *args):
+        assert getattr(cu, name)(*args) == 0, name
+
+    g, n = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    call("cuGraphGetNodes", g, None, ctypes.byref(n))
+    nodes = (ctypes.c_void_p * n.value)()
+    call("cuGraphGetNodes", g, nodes, ctypes.byref(n))
+    names = []
+    for node in nodes:
+        kind = ctypes.c_int(-1)
+        call("cuGraphNodeGetType", ctypes.c_void_p(node), ctypes.byref(kind))
+        if kind.value != 0:
+            continue
+        p, s = Params(), ctypes.c_char_p()
+        call("cuGraphKernelNodeGetParams_v2", ctypes.c_void_p(node), ctypes.byref(p))
+        if p.kern:
+            call("cuKernelGetName", ctypes.byref(s), ctypes.c_void_p(p.kern))
+        else:
+            call("cuFuncGetName", ctypes.byref(s), ctypes.c_void_p(p.func))
+        names.append(s.value.decode())
+    return names

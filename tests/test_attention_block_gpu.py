@@ -18,7 +18,7 @@ import pytest
 from bit_weight_quantized_wq_gb300 import inputs
 from oracle import attention_block as ab
 from oracle import int4_g128, linear, mxfp4
-from tests._util import TOL
+from tests._util import TOL, kernels_of
 
 pytestmark = pytest.mark.gpu
 
@@ -809,3 +809,67 @@ def test_rope_refuses_a_pairing_that_is_no_truth_value(B):
     pos = torch.zeros(3, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         B.qk_norm_rope(q, q, pos, _table(8, 64), interleaved=np.array([True, False]))
+
+
+# ------------------------------------------------- the many-row adapter kernels, by their names
+def _kernels(f):
+    """The adapter kernels that a call launches (the call, once more, captured in a graph)."""
+    import torch
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        f()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g, stream=stream):
+        f()
+    torch.cuda.synchronize()
+    return [n for n in ("k_lora_shrink_tile", "k_lora_shrink_rows", "k_lora_expand_tile", "k_lora_expand")
+            if any(n + "I" in k for k in kernels_of(g))]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,N,r,L,kind", [(1100, 1096, 328, 64, 7, "runs"), (2100, 1032, 72, 96, 9, "mixed"),
+                                            (1300, 2048, 104, 128, 40, "each"), (1025, 1032, 48, 24, 3, "runs"),
+                                            (4100, 520, 264, 40, 5, "runs"), (1100, 1024, 41, 104, 6, "mixed")])
+def test_lora_many_rows_on_the_tensor_cores(B, M, K, N, r, L, kind, dtype):
+    """Ranks beyond 64 (two parts of the grid), K that ends inside a step, several adapters a tile, several CTAs a
+    cluster, ranks of their own: each on the kernels for many rows, whatever their rules become."""
+    import torch
+    ranks = [max(1, r - 5 * (i % 3)) for i in range(L)]
+    (a, b, s), (af, bf, sf) = _adapter_set(M, L, r, K, N, dtype, ranks)
+    x, xf = _rand(M + 50, (M, K), dtype)
+    base, basef = _rand(M + 60, (M, N), dtype)
+    who = _who(kind, M, L, M)
+    ad, rk = torch.from_numpy(who).cuda(), torch.tensor(ranks, dtype=torch.int32, device="cuda")
+    call = lambda: B.lora_add(base, x, a, b, ad, s, ranks=rk)
+    assert _kernels(call) == ["k_lora_shrink_tile", "k_lora_expand_tile" if N % 8 == 0 else "k_lora_expand"]
+    y = call()
+    delta, dabs = ab.adapters(xf, af, bf, who, sf)
+    ref, u = basef + delta, U[dtype]
+    _within(_host(y), ref, u * np.abs(ref) + (u + 1e-5) * dabs, "Y")
+    assert np.array_equal(_host(y)[who < 0], basef[who < 0])
+    assert torch.equal(y, B.lora_add(base, x, a, b, ad, s)) and torch.equal(y, call())
+    assert torch.equal(y, B.lora_add(base, x, a, b, ad, s, ranks=rk, out=base))
+
+
+@pytest.mark.parametrize("fmt", ["int4_g128", "mxfp4"])
+@pytest.mark.parametrize("M,K,N,r,L", [(1300, 1024, 264, 104, 5), (2100, 512, 136, 24, 3)])
+def test_adapters_beside_a_quantized_layer_on_the_tensor_cores(B, fmt, M, K, N, r, L):
+    """V in two parts through the kernels for many rows: the sum of the layer's output and the adapters' product
+    is rounded once."""
+    import torch
+    W = inputs.weights(13, N, K, 0.05)
+    pk = int4_g128.quantize(W) if fmt == "int4_g128" else mxfp4.quantize(W)
+    d = [torch.from_numpy(np.ascontiguousarray(p)).cuda() for p in pk] + [None] * (3 - len(pk))
+    xb, xf = inputs.activations(M, M, K)
+    X = torch.from_numpy(xb.view(np.int16)).cuda().view(torch.bfloat16)
+    (a, b, s), (af, bf, sf) = _adapter_set(M, L, r, K, N, "bf16")
+    who = _who("runs", M, L, M + 1)
+    ad = torch.from_numpy(who).cuda()
+    call = lambda: B.gemm_w4a16_lora(fmt, X, *d, a, b, ad, s)
+    assert _kernels(call) == ["k_lora_shrink_tile", "k_lora_expand_tile"]
+    y = call()
+    base = _host(B.gemm_w4a16(fmt, X, *d))
+    delta, dabs = ab.adapters(xf, af, bf, who, sf)
+    ref, u = base + delta, U["bf16"]
+    _within(_host(y), ref, u * np.abs(ref) + (u * u + 1e-5) * dabs, "Y")
+    assert torch.equal(y, call())
