@@ -873,3 +873,16 @@ def test_adapters_beside_a_quantized_layer_on_the_tensor_cores(B, fmt, M, K, N, 
     ref, u = base + delta, U["bf16"]
     _within(_host(y), ref, u * np.abs(ref) + (u * u + 1e-5) * dabs, "Y")
     assert torch.equal(y, call())
+
+
+# --------------------------------------------------------------------- prompts through attention
+@pytest.mark.parametrize("dtype,d,page", [("bf16", 128, 16), ("f16", 64, 128)])
+@pytest.mark.parametrize("news,prefix,lens,Hq,Hkv", [([700], 0, [700], 8, 2), ([300, 1, 129], 200, [420, 5, 129], 4, 1),
+                                                     ([513], 65, [513], 6, 2)])
+def test_attn_prompts_of_several_row_tiles(B, dtype, d, page, news, prefix, lens, Hq, Hkv):
+    """Requests whose new tokens fill several row tiles (of 64 tokens here and more), causal across them."""
+    b = Batch(121, news, prefix, lens, Hq, Hkv, d, page, dtype)
+    got = b.run(B)
+    b.check(got)
+    again = b.run(B)
+    assert (again[0] == got[0]).all() and (again[1] == got[1]).all()
