@@ -194,10 +194,9 @@ def gptq_int4_g128(W: torch.Tensor, U: torch.Tensor, stream=None):
     return Wq, scales, zeros
 
 
-def _gptq_workspace(K, dev, workspace):
-    need = int(load_library().wq_gptq_workspace_bytes(K))
+def _gptq_workspace(K, dev, workspace, stream):
     if workspace is None:
-        return torch.empty((need,), dtype=torch.uint8, device=dev)
+        return _scratch(dev, int(load_library().wq_gptq_workspace_bytes(K)), stream)
     if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on X's device")
     return workspace
@@ -208,7 +207,7 @@ def gptq_factor(X: torch.Tensor, workspace=None, stream=None):
     activations X float32 [n, K] (CUDA), computed on the device in float64."""
     _need(X, torch.float32, "X")
     n, K = X.shape
-    ws = _gptq_workspace(K, X.device, workspace)
+    ws = _gptq_workspace(K, X.device, workspace, stream)
     U = torch.empty((K, K), dtype=torch.float32, device=X.device)
     _check(load_library().wq_gptq_factor(_ptr(X), n, K, _ptr(U), _ptr(ws), ws.numel(), _stream(stream, X.device)),
            "wq_gptq_factor")
@@ -224,7 +223,7 @@ def gptq_int4_g128_calib(W: torch.Tensor, X: torch.Tensor, workspace=None, strea
     if X.dim() != 2 or X.shape[1] != K or X.device != W.device:
         raise ValueError("X must be [n, K] on W's device")
     n = X.shape[0]
-    ws = _gptq_workspace(K, W.device, workspace)
+    ws = _gptq_workspace(K, W.device, workspace, stream)
     Wq = torch.empty((N, K // 8), dtype=torch.int32, device=W.device)
     scales = torch.empty((N, K // 128), dtype=torch.float16, device=W.device)
     zeros = torch.empty((N, K // 128), dtype=torch.float16, device=W.device)
@@ -253,7 +252,7 @@ def awq_int4_g128(W: torch.Tensor, X: torch.Tensor, workspace=None, stream=None)
     losses = torch.empty((21,), dtype=torch.float64, device=dev)
     lib = load_library()
     if workspace is None:
-        workspace = torch.empty((int(lib.wq_awq_workspace_bytes(N, K, n)),), dtype=torch.uint8, device=dev)
+        workspace = _scratch(dev, int(lib.wq_awq_workspace_bytes(N, K, n)), stream)
     _check(lib.wq_awq_int4_g128(_ptr(W), N, K, _ptr(X), n, _ptr(Wq), _ptr(scales), _ptr(zeros), _ptr(s), _ptr(a),
                                 _ptr(losses), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                 _stream(stream, dev)), "wq_awq_int4_g128")
@@ -293,14 +292,26 @@ class Workspace:
 _default_ws = {}
 
 
-def _workspace_for(device, nbytes, workspace):
+def _workspace_for(device, nbytes, workspace, stream=None):
+    """The caller's workspace, or the one kept for the stream that the call runs on."""
     if workspace is not None:
         return workspace
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _workspace_for(device, nbytes, None)
     key = (str(device), torch.cuda.current_stream(device).cuda_stream)
     ws = _default_ws.get(key)
     if ws is None:
         ws = _default_ws[key] = Workspace(device)
     return ws.get(nbytes)
+
+
+def _scratch(device, nbytes, stream=None):
+    """Scratch of one call, from the allocator's memory of the stream that the call runs on."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _scratch(device, nbytes)
+    return torch.empty(((nbytes + 255) // 256) * 256, dtype=torch.uint8, device=device)
 
 
 _fns = {}
@@ -370,7 +381,7 @@ def _linear(cname: str, fmt, X, Wq, scales, zeros, out, workspace, stream, swigl
     # a caller's workspace is checked by the library itself (WQ_ERR_WORKSPACE when too small)
     if workspace is not None and (workspace.get_device() != d or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on X's device")
-    ws = workspace if workspace is not None else _workspace_for(X.device, gemm_workspace_bytes(f, M, K, N), None)
+    ws = workspace if workspace is not None else _workspace_for(X.device, gemm_workspace_bytes(f, M, K, N), None, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     if stream is not None:
         sh = stream.cuda_stream
@@ -480,7 +491,7 @@ def gemm_w4a16_qkv(fmt, X, Wq, scales, zeros=None, Nq=None, Nkv=None, out=None, 
                 for i, (n, nm) in enumerate(((Nq, "Q"), (Nkv, "K"), (Nkv, "V"))))
     if workspace is not None and (workspace.get_device() != d or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on X's device")
-    ws = workspace if workspace is not None else _workspace_for(dev, gemm_workspace_bytes(f, M, K, N), None)
+    ws = workspace if workspace is not None else _workspace_for(dev, gemm_workspace_bytes(f, M, K, N), None, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _fn("wq_gemm_w4a16_qkv")(f, X.data_ptr(), M, K, Nq, Nkv, Wq.data_ptr(), scales.data_ptr(),
                                    None if zeros is None else zeros.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
@@ -573,7 +584,7 @@ def gemm_w8a8_fp8(X, Wq, sw, out=None, workspace=None, stream=None):
     Y = _output(out, M, N, X.get_device(), "out")
     lib = load_library()
     need = lib.wq_gemm_w8a8_fp8_workspace_bytes(M, K)
-    ws = workspace if workspace is not None else Workspace(X.device).get(need)
+    ws = workspace if workspace is not None else _scratch(X.device, need, stream)
     _check(lib.wq_gemm_w8a8_fp8(_ptr(X), M, K, N, _ptr(Wq), _ptr(sw), _ptr(Y), _ptr(ws), ws.numel(),
                                 _stream(stream, X.device)), "wq_gemm_w8a8_fp8")
     return Y
@@ -617,7 +628,7 @@ def gemm_w4a4_mxfp4(X, Wq8, sw, out=None, workspace=None, stream=None):
     Y = _output(out, M, N, X.get_device(), "out")
     lib = load_library()
     need = lib.wq_gemm_w8a8_fp8_workspace_bytes(M, K)
-    ws = workspace if workspace is not None else Workspace(X.device).get(need)
+    ws = workspace if workspace is not None else _scratch(X.device, need, stream)
     _check(lib.wq_gemm_w4a4_mxfp4(_ptr(X), M, K, N, _ptr(Wq8), _ptr(sw), _ptr(Y), _ptr(ws), ws.numel(),
                                   _stream(stream, X.device)), "wq_gemm_w4a4_mxfp4")
     return Y

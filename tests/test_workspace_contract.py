@@ -141,3 +141,31 @@ def test_a_replaced_workspace_is_given_back_unless_a_capture_took_it(B):
         ws.get(8192).add_(1)
     ws.get(1 << 20)
     assert second() is not None and ws.buf is not second()
+
+
+def test_calls_on_a_given_stream_have_scratch_of_their_own(B):
+    """stream=...: the workspace kept is that stream's, and what a call allocates for itself is not handed out
+    again on the current stream while the call still runs."""
+    import torch
+    pk = _pack("int4_g128", inputs.weights(41, 256, 4096, 0.05))
+    q, s, z = _dev("int4_g128", pk)
+    X = x_to_dev(inputs.activations(42, 2, 4096)[0])
+    want = B.gemm_w4a16("int4_g128", X, q, s, z)
+    W8, sw = B.quantize_fp8_weights(torch.randn(256, 4096, generator=torch.Generator().manual_seed(1)).cuda())
+    want8 = B.gemm_w8a8_fp8(X, W8, sw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = B.gemm_w4a16("int4_g128", X, q, s, z, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    kept = {k[1]: w.buf.data_ptr() for k, w in B._default_ws.items() if w.buf is not None}
+    assert kept[side.cuda_stream] != kept[torch.cuda.current_stream().cuda_stream]
+    y = torch.empty_like(want8)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20000000)                          # the call's kernels wait; its scratch is given up at once
+    B.gemm_w8a8_fp8(X, W8, sw, out=y, stream=side)
+    size = B.load_library().wq_gemm_w8a8_fp8_workspace_bytes(2, 4096)
+    others = [torch.full((size,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want8) and all((t == 0xA5).all() for t in others)
+    assert B.read_error_flags() == 0
