@@ -275,18 +275,33 @@ class Workspace:
         self.buf = None
         self._captured = False      # buf was handed out during a capture
         self._before = []           # buffers that captured graphs go on using
+        self._graph = (0, None)     # a capture, and the buffer made in it
+
+    def _zeros(self, nbytes):
+        return torch.zeros(((nbytes + 255) // 256) * 256, dtype=torch.uint8, device=self.device)
 
     def get(self, nbytes: int):
         if nbytes == 0:
             return None
         capturing = self.device.type == "cuda" and _capturing()
         if self.buf is None or self.buf.numel() < nbytes:
-            grown = torch.zeros(((nbytes + 255) // 256) * 256, dtype=torch.uint8, device=self.device)
+            if capturing:
+                return self._in_capture(nbytes)
+            grown = self._zeros(nbytes)
             if self._captured:
                 self._before.append(self.buf)
             self.buf, self._captured = grown, False
         self._captured |= capturing
         return self.buf
+
+    def _in_capture(self, nbytes):
+        """A buffer made during a capture is zeroed when that graph is replayed, not now: it serves the
+        calls of that capture only."""
+        capture = _m().capture_id(torch.cuda.current_stream(self.device).cuda_stream)
+        if self._graph[0] != capture or self._graph[1].numel() < nbytes:
+            self._graph = (capture, self._zeros(nbytes))
+            self._before.append(self._graph[1])
+        return self._graph[1]
 
 
 _default_ws = {}

@@ -353,6 +353,16 @@ PyObject* gemm_lora(PyObject* const* a, Py_ssize_t n) {
   return THPVariable_Wrap(y);
 }
 
+// Raw stream -> the number of the graph capture that it takes part in, 0: none.
+PyObject* capture_id(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 1);
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(integer(a[0], "stream")), &st, &id) != cudaSuccess)
+    throw std::runtime_error("cudaStreamGetCaptureInfo failed");
+  return PyLong_FromUnsignedLongLong(st == cudaStreamCaptureStatusNone ? 0 : id);
+}
+
 // No C++ exception leaves a Python entry.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -371,7 +381,7 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define WQ_ENTRY(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {WQ_ENTRY("qk_norm_rope", rope), WQ_ENTRY("qk_norm_rope_cache", rope_cache),
                          WQ_ENTRY("attn_shared_prefix", attn), WQ_ENTRY("lora_add", lora_add),
-                         WQ_ENTRY("gemm_w4a16_lora", gemm_lora), {nullptr, nullptr, 0, nullptr}};
+                         WQ_ENTRY("gemm_w4a16_lora", gemm_lora), WQ_ENTRY("capture_id", capture_id), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

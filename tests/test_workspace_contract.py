@@ -169,3 +169,37 @@ def test_calls_on_a_given_stream_have_scratch_of_their_own(B):
     torch.cuda.synchronize()
     assert torch.equal(y, want8) and all((t == 0xA5).all() for t in others)
     assert B.read_error_flags() == 0
+
+
+def test_a_workspace_made_during_a_capture_serves_that_capture_only(B):
+    """Its zeros are written when the graph is replayed: another capture, or a call at once, that took it
+    would find whatever the memory held."""
+    import torch
+    ws, stream = B.Workspace(), torch.cuda.Stream()
+    taken = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            first, second, larger = ws.get(4096), ws.get(2048), ws.get(8192)
+            larger.add_(1)
+        assert second.data_ptr() == first.data_ptr() and larger.data_ptr() != first.data_ptr()
+        taken.append((g, first.data_ptr(), larger.data_ptr()))
+    now = ws.get(4096)
+    assert len({p for t in taken for p in t[1:]} | {now.data_ptr()}) == 5 and int(now.count_nonzero()) == 0
+    # a layer captured without a call before it, then called at once, then replayed
+    q, s, z = _dev("int4_g128", _pack("int4_g128", inputs.weights(51, 256, 4096, 0.05)))
+    X = x_to_dev(inputs.activations(52, 2, 4096)[0])
+    want = B.gemm_w4a16("int4_g128", X, q, s, z)
+    torch.cuda.synchronize()
+    fresh, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    B._default_ws.pop((str(X.device), fresh.cuda_stream), None)
+    with torch.cuda.graph(g, stream=fresh):
+        y = B.gemm_w4a16("int4_g128", X, q, s, z)
+    with torch.cuda.stream(fresh):
+        at_once = B.gemm_w4a16("int4_g128", X, q, s, z)
+    fresh.synchronize()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(at_once, want) and torch.equal(y, want)
+    assert B.read_error_flags() == 0
