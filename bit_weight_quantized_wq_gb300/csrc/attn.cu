@@ -123,7 +123,6 @@ struct Params {
   int G, tb;                 // query heads per key/value head; tokens per lane tile (kRows / G)
   int log_page;              // log2 of the page size
   int p_rts, p_full, p_head; // prefix: row tiles of a head, line length of a full one, of a head
-  int n_prefix;              // prefix items
   int prefix_tiles;
   int q_rows_suffix;         // rows a suffix lane tile can have (its partial's row capacity)
   int ctas;
@@ -1052,7 +1051,6 @@ cudaError_t launch_t(const AttnArgs& a, uint8_t* ws, cudaStream_t stream) {
   p.log_page = 4;
   while ((1 << p.log_page) < a.page_size) ++p.log_page;
   p.prefix_tiles = (a.prefix_len + kTile - 1) / kTile;
-  p.n_prefix = p.prefix_tiles ? l.n_prefix : 0;
   const PrefixLine line(a.T, a.prefix_len, p.tb, p.G);
   p.p_rts = line.row_tiles, p.p_full = static_cast<int>(line.full), p.p_head = static_cast<int>(line.head);
   p.q_rows_suffix = l.rows_s;

@@ -28,11 +28,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 template <bool F16>
-__device__ __forceinline__ float load1(const uint16_t* p) {
-  if constexpr (F16) return __half2float(__ushort_as_half(*p));
-  else return __uint_as_float(static_cast<uint32_t>(*p) << 16);
-}
-template <bool F16>
 __device__ __forceinline__ uint16_t round1(float v) {
   if constexpr (F16) return __half_as_ushort(__float2half_rn(v));
   else return __bfloat16_as_ushort(__float2bfloat16_rn(v));

@@ -181,7 +181,7 @@ cudaError_t launch_attn_shared_prefix(int dtype, const AttnArgs& a, void* ws, cu
 uint32_t attn_read_and_clear_error();
 
 // lora.cu -- low-rank adapters of many requests beside a shared projection: the shrink
-// V = X A^T into the scratch, then the expand Y = base + s V B^T
+// V = s X A^T into the scratch, then the expand Y = base + V B^T
 struct LoraArgs {
   const uint16_t *base, *X, *A, *B;
   int M, K, N, L, r;
