@@ -913,12 +913,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      // No tile, or nothing seen: maybe no output either, so not read (-1).  A weight that is too small for
-      // float32 is 0 and read, since 0 times an infinity or a NaN is NaN.  A sum that is NaN counts whatever the
-      // weight: NaN scores raise no maximum, which may be -inf, or far below the row's.
-      const bool nan = ml[k].y != ml[k].y;
-      const float f = ml[k].y == 0.f ? -1.f : nan ? ml[k].y : exp2_approx(ml[k].x - ref);
-      if (!(f < 0.f)) add = fmaf(ml[k].y, f, add);
+      // No tile, or nothing seen: maybe no output either, so not read; the sign of its weight -0 says so.  A weight
+      // that is too small for float32 is 0 and read, since 0 times an infinity or a NaN is NaN.  A sum that is NaN
+      // counts whatever the weight: NaN scores raise no maximum, which may be -inf, or far below the row's.
+      const float f = ml[k].y == 0.f ? -0.f : ml[k].y != ml[k].y ? __uint_as_float(0x7fffffffu) : exp2_approx(ml[k].x - ref);
+      add = fmaf(ml[k].y, f, add);
       wt[4 * k + (lane >> 3)][lane & 7] = f;
     }
     __syncwarp();
@@ -931,9 +930,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
       for (int e = 0; e < E / 4; ++e) o[e].x *= keep, o[e].y *= keep, o[e].z *= keep, o[e].w *= keep;
     }
     const int here_n = min(32, (most - base + W - 1) / W);
-    const auto add_part = [&](const float4 (&v)[E / 4], float w) {
-      const bool live = !(w < 0.f);
-      const float f = live ? w : 0.f;
+    const auto add_part = [&](const float4 (&v)[E / 4], float f) {
+      const bool live = __float_as_int(f) >= 0;
 #pragma unroll
       for (int e = 0; e < E / 4; ++e) {
         o[e].x = fmaf(live ? v[e].x : 0.f, f, o[e].x), o[e].y = fmaf(live ? v[e].y : 0.f, f, o[e].y);
@@ -951,7 +949,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const __grid_cons
       const float f = wt[k][lane & 7];
       // without a branch, so that several segments' loads are under way: a row without this segment
       // loads some line of the workspace and drops it
-      const float4* src = !(f < 0.f) ? source(base + k * W) : reinterpret_cast<const float4*>(p.po_s);
+      const float4* src = __float_as_int(f) >= 0 ? source(base + k * W) : reinterpret_cast<const float4*>(p.po_s);
       float4 v[E / 4];
 #pragma unroll
       for (int e = 0; e < E / 4; ++e) v[e] = __ldcg(src + 8 * e);
