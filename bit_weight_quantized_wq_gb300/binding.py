@@ -263,7 +263,8 @@ def gemm_workspace_bytes(fmt, M: int, K: int, N: int) -> int:
     return int(load_library().wq_gemm_workspace_bytes(_fmt(fmt), M, K, N))
 
 
-_capturing = torch.cuda.is_current_stream_capturing
+# Asked on every call that takes a kept workspace (the public function is one more call around it).
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 
 
 class Workspace:
@@ -272,6 +273,7 @@ class Workspace:
 
     def __init__(self, device=None):
         self.device = torch.device("cuda") if device is None else torch.device(device)
+        self._on_gpu = self.device.type == "cuda"
         self.buf = None
         self._captured = False      # buf was handed out during a capture
         self._before = []           # buffers that captured graphs go on using
@@ -283,7 +285,7 @@ class Workspace:
     def get(self, nbytes: int):
         if nbytes == 0:
             return None
-        capturing = self.device.type == "cuda" and _capturing()
+        capturing = self._on_gpu and _capturing()
         if self.buf is None or self.buf.numel() < nbytes:
             if capturing:
                 return self._in_capture(nbytes)
@@ -307,17 +309,15 @@ class Workspace:
 _default_ws = {}
 
 
-def _workspace_for(device, nbytes, workspace, stream=None):
-    """The caller's workspace, or the one kept for the stream that the call runs on."""
-    if workspace is not None:
-        return workspace
+def _workspace_for(d, sh, nbytes, stream):
+    """The workspace kept for CUDA device ``d`` and the raw stream ``sh`` that the call runs on
+    (``stream``: the same as an object, where the caller gave one)."""
+    ws = _default_ws.get((d, sh))
+    if ws is None:
+        ws = _default_ws[d, sh] = Workspace(torch.device("cuda", d))
     if stream is not None:
         with torch.cuda.stream(stream):
-            return _workspace_for(device, nbytes, None)
-    key = (str(device), torch.cuda.current_stream(device).cuda_stream)
-    ws = _default_ws.get(key)
-    if ws is None:
-        ws = _default_ws[key] = Workspace(device)
+            return ws.get(nbytes)
     return ws.get(nbytes)
 
 
@@ -396,14 +396,9 @@ def _linear(cname: str, fmt, X, Wq, scales, zeros, out, workspace, stream, swigl
     # a caller's workspace is checked by the library itself (WQ_ERR_WORKSPACE when too small)
     if workspace is not None and (workspace.get_device() != d or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on X's device")
-    ws = workspace if workspace is not None else _workspace_for(X.device, gemm_workspace_bytes(f, M, K, N), None, stream)
+    sh = _stream(stream, X.device)
+    ws = workspace if workspace is not None else _workspace_for(d, sh, gemm_workspace_bytes(f, M, K, N), stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    if stream is not None:
-        sh = stream.cuda_stream
-    elif _raw_current_stream is not None:
-        sh = _raw_current_stream(d)
-    else:
-        sh = torch.cuda.current_stream(X.device).cuda_stream
     st = _fn(cname)(f, X.data_ptr(), M, K, N // 2 if swiglu else N, Wq.data_ptr(), scales.data_ptr(),
                     None if zeros is None else zeros.data_ptr(), out.data_ptr(),
                     None if ws is None else ws.data_ptr(), ws_bytes, sh)
@@ -506,12 +501,12 @@ def gemm_w4a16_qkv(fmt, X, Wq, scales, zeros=None, Nq=None, Nkv=None, out=None, 
                 for i, (n, nm) in enumerate(((Nq, "Q"), (Nkv, "K"), (Nkv, "V"))))
     if workspace is not None and (workspace.get_device() != d or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on X's device")
-    ws = workspace if workspace is not None else _workspace_for(dev, gemm_workspace_bytes(f, M, K, N), None, stream)
+    sh = _stream(stream, dev)
+    ws = workspace if workspace is not None else _workspace_for(d, sh, gemm_workspace_bytes(f, M, K, N), stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _fn("wq_gemm_w4a16_qkv")(f, X.data_ptr(), M, K, Nq, Nkv, Wq.data_ptr(), scales.data_ptr(),
                                    None if zeros is None else zeros.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
-                                   out[2].data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes,
-                                   _stream(stream, dev))
+                                   out[2].data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes, sh)
     if st:
         _check(st, "wq_gemm_w4a16_qkv")
     return out

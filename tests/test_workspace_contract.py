@@ -192,7 +192,7 @@ def test_a_workspace_made_during_a_capture_serves_that_capture_only(B):
     want = B.gemm_w4a16("int4_g128", X, q, s, z)
     torch.cuda.synchronize()
     fresh, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
-    B._default_ws.pop((str(X.device), fresh.cuda_stream), None)
+    B._default_ws.pop((X.get_device(), fresh.cuda_stream), None)
     with torch.cuda.graph(g, stream=fresh):
         y = B.gemm_w4a16("int4_g128", X, q, s, z)
     with torch.cuda.stream(fresh):
