@@ -36,8 +36,8 @@
 // but needs both score buffers of a lane at once, and the lane then waits for its own products: 284 us;
 // with the pair's second P in shared memory, so that the wait ends when the scores are in registers, 298 us
 // (P V with both operands in shared memory and V transposed takes some 150 cycles a step).
-// Keys mode is bound by the bytes: 262144 keys, 8 rows on 8 heads, 164 us, 6.6 TB/s; 64 requests over 16384 keys
-// of their own 326 us, 6.6 TB/s.  Short calls are bound by the chain of dependent loads, waits and launches:
+// Keys mode is bound by the bytes: 262144 keys, 8 rows on 8 heads, 164 us, 6.6 TB/s; 64 requests over up to
+// 16384 keys of their own (half of that on average), 64 heads on 8, 325 us, 6.6 TB/s.  Short calls are bound by the chain of dependent loads, waits and launches:
 // 2 requests over 500 + 40 keys 11.7 us, of which the second kernel some 3.
 // P is rounded to the cache's type for the second product (the tensor core takes both operands in
 // one type); the sum of P is kept unrounded in float32.

@@ -22,10 +22,13 @@
 // fp16 has no room for inner products from 65520 on, where Y may well be ordinary: each row of V, by halves of
 // 64 ranks, is kept divided by a power of two that brings its largest value below 2^15 (1 where it is already),
 // and the expand multiplies its sums by it in float32.
+// For many rows V is rounded once: in two parts there the expand has room for one CTA an SM only and takes twice
+// the products (4001 rows of rank 64, 8192 x 8192: 60.1 us instead of 47.6; 1024 rows, K 4096, N 4096, rank 16:
+// 19.6 instead of 18.3).  Y's error is then some 1.2 times that of its own rounding alone.
 //
-// Measured, whole calls, cold adapters: 3 rows 4096 x 4096 6.6 us (launches and dependent loads); 64 rows of
-// 48 adapters of rank 32 on 4096 x 28672 24.5 us, 3.6 TB/s; 4001 rows of 11 requests, rank 64, 8192 x 8192
-// 47.3 us, 4.5 TB/s.
+// Measured, whole calls in a graph, cold adapters (as all figures below): 3 rows 4096 x 4096 5.9 us (launches and
+// dependent loads); 64 rows of 48 adapters of rank 32 on 4096 x 28672 22.5 us, 3.9 TB/s; 4001 rows of 11
+// requests, rank 64, 8192 x 8192 47.3 us, 4.5 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -199,7 +202,7 @@ __device__ __forceinline__ void shrink_loop(float (&acc)[NT][4], const LoraArgs&
 }
 
 // Few rows: one cluster for each row that leads its adapter in its 16-row block; 8 warps a CTA, each
-// a slice of K.  12 us by itself for 48 adapters of rank 32, K 4096 (10 MB of A): adapter, rank and A are
+// a slice of K.  9 us by itself for 48 adapters of rank 32, K 4096 (10 MB of A): adapter, rank and A are
 // loads that wait for one another, and the cluster meets twice.
 // Two CTAs an SM are asked for so that the compiler keeps a step's loads in registers, all under way; left to
 // itself it took 86 to 114 registers, by what else stood in the kernel, and loaded in turns (13 rows of rank 48,
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, NT <= 8 ? 2 : 1) k_lora_shrink
   pdl_launch_dependents();                    // the expand may read all but V from here on
   const int m = blockIdx.y, m0 = m & ~15;
   // Up to 128 adapters: their ranks come beside the rows' adapters, not after them (after / beside, in us: 16
-  // rows 8.1 / 7.9, 64 rows of 48 adapters 24.9 / 24.6, 200 rows 45.1 / 44.3).
+  // rows 7.6 / 7.3, 64 rows of 48 adapters 22.7 / 22.4, 200 rows 40.6 / 39.9).
   const bool ahead = p.ranks && p.L <= 128;
   int all_ranks[4];
 #pragma unroll
@@ -503,8 +506,8 @@ __global__ void __launch_bounds__(192) k_lora_shrink_tile(const __grid_constant_
 // The expand: a warp has 16 rows, 32 output columns at a time, and every `subsets`-th adapter of
 // those rows (their rows are its own to write; rows without an adapter are the first warp's).
 // Output tile t of 8 columns stands for the columns 8 (c / 2) + 2 t + c % 2, c = 0 .. 7, so that a
-// lane's results of four tiles are 8 neighbouring columns: base and Y move 16 bytes a lane.  19 us by itself
-// for 64 rows of 48 adapters of rank 32, N 28672: 84 MB, 4.4 TB/s.
+// lane's results of four tiles are 8 neighbouring columns: base and Y move 16 bytes a lane.  21 us by itself
+// for 64 rows of 48 adapters of rank 32, N 28672: 84 MB, 4.1 TB/s.
 //   B (32 columns and 32 ranks a step) and base come through queues in shared memory, each thread
 //   its own place, so that steps ahead are under way without registers: with B one step ahead in
 //   registers a decode batch of 48 adapters ran at 2.5 TB/s.
@@ -583,7 +586,8 @@ __global__ void __launch_bounds__(256, CH * (LO ? 2 : 1) <= 2 ? 2 : 1) k_lora_ex
   };
   // N not a multiple of 8: rows begin anywhere, so a lane takes one column of each row; its base is on its
   // way during the products, which come to the rows through shared memory (the base queue's place).  With
-  // eight columns a lane, in single elements, 494 rows of 11655 columns took 46 us instead of 33.
+  // eight columns a lane, in single elements, 494 rows of 11655 columns took 1.4 times as long (25.1 us now, K
+  // 4096, rank 32).
   const bool vec = p.N % 8 == 0;
   float* stage = reinterpret_cast<float*>(expand_smem + sizeof(uint4) * kBQueue * 4 * 256) + warp * (16 * kStageLd);
   const uint32_t adapted = __ballot_sync(0xffffffffu, mine >= 0);
@@ -671,7 +675,7 @@ __global__ void __launch_bounds__(256, CH * (LO ? 2 : 1) <= 2 ? 2 : 1) k_lora_ex
     }
     // An adapter's product runs for all 16 rows, and its own rows take it, so that an infinity or a NaN in its B
     // reaches no other's.  They take it when the next adapter's B is there: at once, the products' latency showed
-    // (64 rows of 48 adapters, whole call: 26.7 us instead of 24.9).
+    // (64 rows of 48 adapters, whole call: 23.5 us instead of 22.6).
     float prod[4][4];
     int of = -2;                               // no row's adapter
     const auto take = [&] {
@@ -1002,17 +1006,19 @@ cudaError_t launch_cluster(void (*kern)(P...), dim3 grid, unsigned threads, size
 // The kernels on tcgen05, by 128 rows, or those on mma.sync, by the adapters that lead in each 16 rows.  The
 // former cost a product and a pass over the rows for each adapter that occurs in 128 of them, which only the
 // device knows; at 32 rows an adapter or more, on average over all, it is few where requests' rows are
-// neighbours.  (Beyond kMostRows the grid of the latter's shrink would end.)  K 4096, N 4096 or 8192, in us,
+// neighbours.  (Beyond kMostRows the grid of the latter's shrink would end.)  K 4096, in us,
 // mma.sync / tcgen05:
-//   shrink (with the expand that fits): 8 adapters, 257 rows 12.5 / 19.3, 512 rows 16.7 / 18.6, 1024 rows 25.3 / 21.3,
-//     1024 rows of rank 64 28.3 / 19.9, 2048 rows 46 / 21; 1024 rows that take 64 adapters in turn 102 / 133
-//   expand (with the shrink that fits): 8 adapters, 256 rows 12.3 / 14.9, 512 rows 16.8 / 17.9, 1024 rows 22.4 / 21.4,
-//     2048 rows of rank 64 28.4 / 21.1, 4001 rows 66 / 40; 64 adapters in turn, 1024 rows 102 / 190, 2048 rows 149 / 225
+//   shrink (with the expand that fits), N 4096: 8 adapters, 257 rows of rank 32 11.5 / 18.6, 512 rows of rank 16 13.3 /
+//     15.3, 1024 rows 22.2 / 18.7, 1024 rows of rank 64 28.6 / 19.7, 2048 rows 48.6 / 22.1; 1024 rows that take 64
+//     adapters in turn 90 / 137
+//   expand (with the shrink that fits), N 8192: 8 adapters, 256 rows of rank 16 11.0 / 13.2, 512 rows 16.3 / 16.9, 1024
+//     rows 23.1 / 21.9, 2048 rows of rank 64 46.4 / 28.3, 4001 rows 64.9 / 41.1; 64 adapters in turn, 1024 rows 113 /
+//     263, 2048 rows 209 / 317
 constexpr int kFewRows = 512, kRowsAdapter = 32, kMostRows = 16384;
 template <bool F16, int NT>
 cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
   // At least four steps of 32 a warp, up to 8 CTAs.  One CTA / this many (4), K 4096, in us: 3 rows
-  // 11.3 / 6.9, 16 rows of 16 adapters 12.1 / 8.0, 64 rows of 48 39.6 / 25.1 (N 28672), 200 rows 45.5 / 44.9.
+  // 7.6 / 5.9, 16 rows of 16 adapters 8.3 / 7.3, 64 rows of 48 25.8 / 22.4 (N 28672), 200 rows 34.9 / 39.9.
   const int steps = (a.K + 31) / 32;
   unsigned c = 1;
   while (c < 8 && steps >= static_cast<int>(2 * c) * kRowWarps * 4) c *= 2;
@@ -1027,8 +1033,8 @@ cudaError_t launch_rows(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
 template <bool F16>
 cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
   // A small X leaves the tiles' clusters too little to share.  By 16 rows / by 128 rows, 8 adapters of rank 40, in
-  // us: 965 x 896 13.3 / 14.8, 1024 x 512 11.7 / 14.2, 1024 x 1024 13.6 / 13.6, 2048 x 1024 16.6 / 14.9, 4096 x 512
-  // 20.8 / 15.6, 1024 x 2048 16.5 / 15.1.
+  // us: 965 x 896 12.5 / 13.6, 1024 x 512 10.9 / 12.6, 1024 x 1024 12.7 / 12.9, 2048 x 1024 16.5 / 14.5, 4096 x 512
+  // 20.5 / 14.8, 1024 x 2048 16.0 / 14.2.
   const bool small = static_cast<int64_t>(a.M) * a.K < (1 << 20);
   if (!lora_many_rows(a.M, a.L) || (small && a.M <= kMostRows)) {
     if (a.r <= 32) return launch_rows<F16, 4>(a, V, stream);
@@ -1036,8 +1042,9 @@ cudaError_t shrink_t(const LoraArgs& a, uint16_t* V, cudaStream_t stream) {
     return launch_rows<F16, 16>(a, V, stream);
   }
   const int tiles = (a.M + kTileRows - 1) / kTileRows, steps = (a.K + 63) / 64;
-  // Two CTAs an SM, at least two steps of 64 each (at least four: 4096 x 512 18.6 us instead of 15.6).  One CTA / this many, whole calls, K 4096, in us: 1024 rows
-  // 52 / 21 (8), 2048 rows of rank 64 41 / 21 (8), 4001 rows 61 / 40 (8).
+  // Two CTAs an SM, at least two steps of 64 each (at least four: 4096 x 512 16.2 us instead of 14.8).  One CTA /
+  // this many (8), whole calls, K 4096, N 8192, in us: 1024 rows 49.8 / 21.9, 2048 rows of rank 64 46.0 / 28.3, 4001
+  // rows 58.5 / 41.2.
   unsigned c = 1;
   while (c < 8 && static_cast<int>(tiles * c) < 2 * device_sm_count() && steps >= static_cast<int>(2 * c) * 2) c *= 2;
   const int box_ranks = std::min(64, (a.r + 15) / 16 * 16);
@@ -1092,9 +1099,9 @@ cudaError_t expand_t(const LoraArgs& a, const uint16_t* V, bool base_ready, cuda
   }
   // Subsets of the adapters, up to those that a block can hold, while there are few warps for the
   // SMs.  Row blocks: as many as there are.  8 warps a CTA, and column tiles enough for one wave of two
-  // CTAs an SM.  No subsets / this rule / always all, K 4096, in us: 16 rows of 16 adapters, N 4096 11.2 / 8.0 /
-  // 8.1, N 28672 15.2 / 12.6 / 12.7; 64 rows of 48, N 4096 15.6 / 12.3 / 12.4, N 28672 26.9 / 25.1 / 34.9; 200 rows,
-  // N 14336 44.8 / 44.9 / 56.8.  One column tile a warp / this rule: 64 rows, N 28672 29.3 / 25.1.
+  // CTAs an SM.  No subsets / this rule / always all, K 4096, in us: 16 rows of 16 adapters, N 4096 10.2 / 7.3 /
+  // 7.3, N 28672 14.4 / 11.8 / 11.8; 64 rows of 48, N 4096 14.7 / 11.3 / 11.3, N 28672 24.5 / 22.4 / 33.9; 200 rows,
+  // N 14336 39.8 / 39.9 / 52.8.  One column tile a warp / this rule: 64 rows, N 28672 26.9 / 22.4.
   const int most = std::min(std::min(a.M, 16), a.L);
   while (ls < 3 && (1 << ls) < most && (blocks * cols << ls) < 24ll * sms) ++ls;
   while (lr + ls < 3 && (1 << lr) < blocks) ++lr;

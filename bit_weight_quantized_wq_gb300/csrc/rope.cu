@@ -12,7 +12,8 @@
 // only the sum of squares takes shuffles.  With one piece a thread and the partners by shuffles the
 // instructions, not the bytes, set the time (8192 tokens of 80 heads of 128: 88 us instead of 61).  Sums, norm and
 // rotation are float32; each output is rounded once.  8192 tokens, 80 heads, with cache: 60.6 us, 5.6 TB/s of 340 MB;
-// 2047 tokens, 40 heads: 9.4 us, 4.6 TB/s; one token: 2.0 us, a launch and two dependent loads.
+// 2047 tokens, 40 heads, no cache: 9.4 us, 4.6 TB/s; one token: 2.0 us, a launch and two dependent loads (all in a
+// graph, inputs not in L2).
 #include "elem16.cuh"
 #include "internal.h"
 
@@ -266,10 +267,10 @@ cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t stream) {
   static_assert(kRopeThreads == kWalkThreads, "both take the same heads a pass");
   const int rows = a.Hq + (a.slots ? 2 : 1) * a.Hkv, passes = (rows + HPB - 1) / HPB;
   const int fill = kWalkCtas * device_sm_count();
-  // From eight units a CTA on the walk's set-up pays.  Without / with it, in us: 40 heads of 128, 1024
-  // tokens (3 units a CTA) 6.3 / 7.4, 2047 (7) 11.2 / 11.5, 4096 (13) 24.6 / 22.5; 80 heads, 1024 tokens (6)
-  // 9.1 / 9.5, 2047 (11) 19.0 / 18.1, 4096 (22) 38.1 / 33.8; 48 heads of 64, 2047 tokens (4) 7.0 / 8.1, 4096 (9)
-  // 13.1 / 13.1.
+  // From eight units a CTA on the walk's set-up pays.  Without / with it, in us, keys and values into the cache
+  // (measured as above): 32 + 8 heads of 128, 1024 tokens (3 units a CTA) 6.0 / 7.2, 2047 (7) 12.6 / 13.3, 4096 (13)
+  // 24.5 / 22.2; 64 + 8 heads, 1024 tokens (6) 9.6 / 9.8, 2047 (11) 19.4 / 18.2, 4096 (22) 38.0 / 33.4; 16 + 16 heads
+  // of 64, 2047 tokens (4) 7.0 / 7.8, 4096 (9) 15.7 / 14.9.  2047 tokens, 32 + 8 heads, no cache (6) 9.6 / 10.2.
   if (static_cast<int64_t>(a.T) * passes < 8ll * fill) return launch_pdl(k_qk_norm_rope<F16, D>, dim3(a.T, passes), kRopeThreads, 0, stream, a);
   return launch_pdl(k_qk_norm_rope_walk<F16, D>, dim3(fill), kWalkThreads, 0, stream, a, passes);
 }
