@@ -34,7 +34,7 @@ def assert_close(y, ref, what="", extra=None):
 
 
 def kernels_of(graph):
-    """Names of the kernels that a captured torch.cuda.CUDAGraph(keep_graph=True) launches, from the driver's
+    """Names of the kernels that a captured torch.cuda.CUDAGraph(keep_graph=True) launches, from CUDA's
     graph queries."""
     import ctypes
 
