@@ -37,6 +37,7 @@ EXPORTED = [
     "wq_gemm_w8a8_fp8", "wq_mxfp4_weights_to_e4m3", "wq_quantize_w4a4_activations", "wq_gemm_w4a4_mxfp4",
     "wq_qk_norm_rope", "wq_qk_norm_rope_cache", "wq_attn_workspace_bytes", "wq_attn_shared_prefix",
     "wq_lora_workspace_bytes", "wq_lora_add", "wq_gemm_w4a16_lora_workspace_bytes", "wq_gemm_w4a16_lora",
+    "wq_kv_append_e4m3", "wq_kv_read_e4m3", "wq_attn_e4m3_workspace_bytes", "wq_attn_e4m3",
 ]
 
 _lib = None
@@ -96,6 +97,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "wq_lora_add": (I32, [I32, P, P, I64, I64, I64, P, P, I64, I64, P, P, P, P, P, SZ, P]),
         "wq_gemm_w4a16_lora_workspace_bytes": (SZ, [I32, I64, I64, I64, I64]),
         "wq_gemm_w4a16_lora": (I32, [I32, P, I64, I64, I64, P, P, P, P, P, I64, I64, P, P, P, P, P, SZ, P]),
+        "wq_kv_append_e4m3": (I32, [I32, P, I64, P, I64, I64, I64, I64, I64, P, P, P, P, I64, I64, P, I64, P, P, I64, P]),
+        "wq_kv_read_e4m3": (I32, [I32, P, P, P, P, I64, I64, I64, I64, P, I64, P, I64, I64, P, P, P]),
+        "wq_attn_e4m3_workspace_bytes": (SZ, [I64] * 6),
+        "wq_attn_e4m3": (I32, [I32, P, I64, I64, I64, I64, I64, I64, P, P, P, P, I64, I64, P, I64, P, P, I64, F32, P, P, P,
+                               SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -739,3 +745,44 @@ def gemm_w4a16_lora(fmt, X, Wq, scales, zeros, A, B, adapter, lora_scales, ranks
         return _m().gemm_w4a16_lora(*args)
     return _on_stream(stream, _m().gemm_w4a16_lora,
                       (X, Wq, scales, zeros, A, B, adapter, lora_scales, ranks, out, workspace), *args)
+
+
+# ------------------------------------------------------------------ the cache in 8 bits
+def kv_append_e4m3(K, V, k_cache, v_cache, k_scales, v_scales, block_table, lens, q_start=None, max_new=1, stream=None):
+    """New keys and values quantized as they are written to a cache in pages: k_cache, v_cache uint8 [pages,
+    Hkv, page_size, d] (E4M3 codes), k_scales, v_scales uint8 [pages, Hkv] (E8M0: 2^(byte - 127), one for
+    each page and head).  K, V [T, Hkv, d] (a token's heads contiguous) are the last tokens of requests of
+    ``lens`` int32 [R] tokens in the pages block_table int32 [R, blocks]; q_start int32 [R + 1]: where each
+    request's new tokens start in K, at most ``max_new`` each (None: one each).  A page's scale is the lowest
+    power of two that holds it, starts afresh with its first place and otherwise grows, the codes that it
+    holds with it."""
+    args = (K, V, k_cache, v_cache, k_scales, v_scales, block_table, lens, q_start, max_new)
+    if stream is None:
+        return _m().kv_append_e4m3(*args)
+    return _on_stream(stream, _m().kv_append_e4m3, args[:9], *args)
+
+
+def kv_read_e4m3(k_cache, v_cache, k_scales, v_scales, block_table, starts, tokens, dtype=torch.bfloat16, out=None,
+                 stream=None):
+    """Tokens of such a cache read back, one request after the other: the first starts[r + 1] - starts[r]
+    tokens of request r (pages block_table[r]) to rows starts[r] .. of (K, V), each [tokens, Hkv, d] of
+    ``dtype`` (bfloat16 or float16).  starts int32 [R + 1]; rows behind its last are left as they were."""
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float16")
+    ko, vo = _pair(out, "K, V")
+    args = (k_cache, v_cache, k_scales, v_scales, block_table, starts, tokens, dtype is torch.float16, ko, vo)
+    if stream is None:
+        return _m().kv_read_e4m3(*args)
+    return _on_stream(stream, _m().kv_read_e4m3, args[:6] + (ko, vo), *args)
+
+
+def attn_e4m3(Q, k_cache, v_cache, k_scales, v_scales, block_table, lens, q_start=None, max_new=1, scale=None, out=None,
+              workspace=None, stream=None):
+    """Attention of a batch of requests over a cache that ``kv_append_e4m3`` wrote, the new tokens causal:
+    Q [T, Hq, d] (a token's heads contiguous), the other arguments as there.  scale defaults to 1/sqrt(d).
+    Returns (O [T, Hq, d], lse float32 [T, Hq])."""
+    o, lse = _pair(out, "O, lse")
+    args = (Q, k_cache, v_cache, k_scales, v_scales, block_table, lens, q_start, max_new, scale, o, lse, workspace)
+    if stream is None:
+        return _m().attn_e4m3(*args)
+    return _on_stream(stream, _m().attn_e4m3, args[:8] + (o, lse, workspace), *args)

@@ -558,7 +558,8 @@ wq_status wq_read_error_flags(uint32_t* out) {
   *out = wq::gemv_read_and_clear_error() | wq::gemm_tc_read_and_clear_error() |
          wq::gptq_read_and_clear_error() | wq::gptq_factor_read_and_clear_error() |
          wq::selftest_read_and_clear_error() | wq::fp8_read_and_clear_error() |
-         wq::rope_read_and_clear_error() | wq::attn_read_and_clear_error() | wq::lora_read_and_clear_error();
+         wq::rope_read_and_clear_error() | wq::attn_read_and_clear_error() | wq::lora_read_and_clear_error() |
+         wq::kv_read_and_clear_error() | wq::attn_e4m3_read_and_clear_error();
   return cudaGetLastError() == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
@@ -809,6 +810,128 @@ wq_status wq_gemm_w4a16_lora(wq_fmt fmt, const uint16_t* X, int64_t M, int64_t K
   st = wq_gemm_w4a16(fmt, X, M, K, N, Wq, scales, zeros, Y, workspace, off, stream);
   if (st != WQ_OK) return st;
   return from_cuda(wq::launch_lora_expand(WQ_DTYPE_BF16, a, scratch, false, s));
+}
+
+// ------------------------------------------------------------------ the cache in 8 bits
+namespace {
+struct Cache8 {
+  const uint8_t *k, *v, *ks, *vs;
+  int64_t pages, page_size, Hkv, d;
+  size_t codes() const { return static_cast<size_t>(pages) * Hkv * page_size * d; }
+  size_t scales() const { return static_cast<size_t>(pages) * Hkv; }
+  // A byte range shares a byte with the cache.
+  bool overlaps(const void* p, size_t n) const {
+    return overlap(p, n, k, codes()) || overlap(p, n, v, codes()) || overlap(p, n, ks, scales()) || overlap(p, n, vs, scales());
+  }
+};
+}  // namespace
+
+static wq_status check_cache8(const Cache8& c, int64_t T, int64_t R, const int32_t* block_table, int64_t max_blocks) {
+  if (!c.k || !c.v || !c.ks || !c.vs || !block_table) return WQ_ERR_NULL;
+  if (T < 1 || T > (1 << 24) || R < 1 || R > (1 << 24) || c.Hkv < 1 || c.Hkv > 1024 || (c.d != 64 && c.d != 128)) return WQ_ERR_SHAPE;
+  if (!page_ok(c.page_size) || c.pages < 1 || c.pages > 0x7fffffffLL / c.Hkv) return WQ_ERR_SHAPE;
+  if (max_blocks < 1 || max_blocks > (1LL << 30) / c.page_size) return WQ_ERR_SHAPE;
+  if (!aligned16(c.k) || !aligned16(c.v) || odd4(block_table)) return WQ_ERR_ALIGN;
+  return WQ_OK;
+}
+
+wq_status wq_kv_append_e4m3(wq_dtype dtype, const uint16_t* K, int64_t k_stride, const uint16_t* V, int64_t v_stride,
+                            int64_t T, int64_t R, int64_t Hkv, int64_t d, uint8_t* k_cache, uint8_t* v_cache,
+                            uint8_t* k_scales, uint8_t* v_scales, int64_t pages, int64_t page_size,
+                            const int32_t* block_table, int64_t max_blocks, const int32_t* lens, const int32_t* q_start,
+                            int64_t max_new, void* stream) {
+  if (!dtype_ok(dtype)) return WQ_ERR_ARG;
+  if (!K || !V || !lens) return WQ_ERR_NULL;
+  const Cache8 c{k_cache, v_cache, k_scales, v_scales, pages, page_size, Hkv, d};
+  wq_status st = check_cache8(c, T, R, block_table, max_blocks);
+  if (st != WQ_OK) return st;
+  if (k_stride < Hkv * d || v_stride < Hkv * d || k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride > (1LL << 40) ||
+      v_stride > (1LL << 40) || max_new < 1 || (!q_start && (T != R || max_new != 1)))
+    return WQ_ERR_SHAPE;
+  if (!aligned16(K) || !aligned16(V) || odd4(lens) || odd4(q_start)) return WQ_ERR_ALIGN;
+  if (c.overlaps(K, (static_cast<size_t>(T - 1) * k_stride + Hkv * d) * 2) ||
+      c.overlaps(V, (static_cast<size_t>(T - 1) * v_stride + Hkv * d) * 2) || overlap(k_cache, c.codes(), v_cache, c.codes()) ||
+      overlap(k_scales, c.scales(), v_scales, c.scales()) || overlap(k_cache, c.codes(), k_scales, c.scales()) ||
+      overlap(k_cache, c.codes(), v_scales, c.scales()) || overlap(v_cache, c.codes(), k_scales, c.scales()) ||
+      overlap(v_cache, c.codes(), v_scales, c.scales()))
+    return WQ_ERR_ARG;
+  st = check_device_cached();
+  if (st != WQ_OK) return st;
+  wq::KvAppendArgs a{};
+  a.K = K, a.V = V, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.k_cache = k_cache, a.v_cache = v_cache, a.k_scales = k_scales, a.v_scales = v_scales;
+  a.pages = pages, a.page_size = static_cast<int>(page_size);
+  a.block_table = block_table, a.max_blocks = static_cast<int>(max_blocks);
+  a.lens = lens, a.q_start = q_start;
+  a.T = static_cast<int>(T), a.R = static_cast<int>(R), a.Hkv = static_cast<int>(Hkv), a.d = static_cast<int>(d);
+  a.max_new = static_cast<int>(max_new < T ? max_new : T);
+  return from_cuda(wq::launch_kv_append(dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
+wq_status wq_kv_read_e4m3(wq_dtype dtype, const uint8_t* k_cache, const uint8_t* v_cache, const uint8_t* k_scales,
+                          const uint8_t* v_scales, int64_t pages, int64_t page_size, int64_t Hkv, int64_t d,
+                          const int32_t* block_table, int64_t max_blocks, const int32_t* starts, int64_t R, int64_t T,
+                          uint16_t* Ko, uint16_t* Vo, void* stream) {
+  if (!dtype_ok(dtype)) return WQ_ERR_ARG;
+  if (!starts || !Ko || !Vo) return WQ_ERR_NULL;
+  const Cache8 c{k_cache, v_cache, k_scales, v_scales, pages, page_size, Hkv, d};
+  wq_status st = check_cache8(c, T, R, block_table, max_blocks);
+  if (st != WQ_OK) return st;
+  if (!aligned16(Ko) || !aligned16(Vo) || odd4(starts)) return WQ_ERR_ALIGN;
+  const size_t out = static_cast<size_t>(T) * Hkv * d * 2;
+  if (c.overlaps(Ko, out) || c.overlaps(Vo, out) || overlap(Ko, out, Vo, out)) return WQ_ERR_ARG;
+  st = check_device_cached();
+  if (st != WQ_OK) return st;
+  wq::KvReadArgs a{};
+  a.k_cache = k_cache, a.v_cache = v_cache, a.k_scales = k_scales, a.v_scales = v_scales;
+  a.pages = pages, a.page_size = static_cast<int>(page_size);
+  a.block_table = block_table, a.max_blocks = static_cast<int>(max_blocks), a.starts = starts;
+  a.T = static_cast<int>(T), a.R = static_cast<int>(R), a.Hkv = static_cast<int>(Hkv), a.d = static_cast<int>(d);
+  a.Ko = Ko, a.Vo = Vo;
+  return from_cuda(wq::launch_kv_read(dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
+static bool attn8_shape_ok(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new) {
+  return attn_shape_ok(T, R, Hq, Hkv, d, max_new) && T * (Hq / Hkv) <= (1LL << 30);
+}
+
+size_t wq_attn_e4m3_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new) {
+  if (!attn8_shape_ok(T, R, Hq, Hkv, d, max_new)) return 0;
+  return wq::attn_e4m3_workspace_bytes(d);
+}
+
+wq_status wq_attn_e4m3(wq_dtype dtype, const uint16_t* Q, int64_t q_stride, int64_t T, int64_t R, int64_t Hq, int64_t Hkv,
+                       int64_t d, const uint8_t* k_cache, const uint8_t* v_cache, const uint8_t* k_scales,
+                       const uint8_t* v_scales, int64_t pages, int64_t page_size, const int32_t* block_table,
+                       int64_t max_blocks, const int32_t* lens, const int32_t* q_start, int64_t max_new, float scale,
+                       uint16_t* O, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(dtype) || !(scale > 0.f) || !std::isfinite(scale)) return WQ_ERR_ARG;
+  if (!Q || !O || !lens) return WQ_ERR_NULL;
+  if (!attn8_shape_ok(T, R, Hq, Hkv, d, max_new) || q_stride < Hq * d || q_stride % 8 != 0 || q_stride > (1LL << 40) ||
+      (!q_start && (T != R || max_new != 1)))
+    return WQ_ERR_SHAPE;
+  const Cache8 c{k_cache, v_cache, k_scales, v_scales, pages, page_size, Hkv, d};
+  wq_status st = check_cache8(c, T, R, block_table, max_blocks);
+  if (st != WQ_OK) return st;
+  if (!aligned16(Q) || !aligned16(O) || odd4(lse) || odd4(lens) || odd4(q_start)) return WQ_ERR_ALIGN;
+  const size_t out = static_cast<size_t>(T) * Hq * d * 2;
+  if (overlap(Q, (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2, O, out) || c.overlaps(O, out)) return WQ_ERR_ARG;
+  if (!workspace || ws_bytes < wq_attn_e4m3_workspace_bytes(T, R, Hq, Hkv, d, max_new)) return WQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WQ_ERR_ALIGN;
+  st = check_device_cached();
+  if (st != WQ_OK) return st;
+  wq::AttnE4m3Args a{};
+  a.Q = Q, a.q_stride = q_stride;
+  a.T = static_cast<int>(T), a.R = static_cast<int>(R), a.Hq = static_cast<int>(Hq), a.Hkv = static_cast<int>(Hkv);
+  a.d = static_cast<int>(d);
+  a.k_cache = k_cache, a.v_cache = v_cache, a.k_scales = k_scales, a.v_scales = v_scales;
+  a.pages = pages, a.page_size = static_cast<int>(page_size);
+  a.block_table = block_table, a.max_blocks = static_cast<int>(max_blocks);
+  a.lens = lens, a.q_start = q_start;
+  a.max_new = static_cast<int>(max_new < T ? max_new : T);
+  a.scale = scale;
+  a.O = O, a.lse = lse;
+  return from_cuda(wq::launch_attn_e4m3(dtype, a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 wq_status wq_check_device(void) { return check_device_cached(); }

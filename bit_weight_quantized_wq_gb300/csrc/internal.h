@@ -197,6 +197,52 @@ cudaError_t launch_lora_shrink(int dtype, const LoraArgs& a, void* scratch, cuda
 cudaError_t launch_lora_expand(int dtype, const LoraArgs& a, void* scratch, bool base_ready, cudaStream_t stream);
 uint32_t lora_read_and_clear_error();
 
+// kv_e4m3.cu -- the cache in 8 bits: new tokens quantized into their pages, tokens read back
+struct KvAppendArgs {
+  const uint16_t *K, *V;
+  int64_t k_stride, v_stride;
+  uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
+  int64_t pages;
+  int page_size, log_page;   // log_page: set by the launch
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t *lens, *q_start;
+  int T, R, Hkv, d, max_new;
+};
+cudaError_t launch_kv_append(int dtype, const KvAppendArgs& a, cudaStream_t stream);
+struct KvReadArgs {
+  const uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
+  int64_t pages;
+  int page_size, log_page;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* starts;
+  int T, R, Hkv, d;
+  uint16_t *Ko, *Vo;
+};
+cudaError_t launch_kv_read(int dtype, const KvReadArgs& a, cudaStream_t stream);
+uint32_t kv_read_and_clear_error();
+
+// attn_e4m3.cu -- attention over the cache in 8 bits
+struct AttnE4m3Args {
+  const uint16_t* Q;
+  int64_t q_stride;
+  int T, R, Hq, Hkv, d;
+  const uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
+  int64_t pages;
+  int page_size;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t *lens, *q_start;
+  int max_new;
+  float scale;
+  uint16_t* O;
+  float* lse;
+};
+size_t attn_e4m3_workspace_bytes(int64_t d);
+cudaError_t launch_attn_e4m3(int dtype, const AttnE4m3Args& a, void* ws, cudaStream_t stream);
+uint32_t attn_e4m3_read_and_clear_error();
+
 // layout.cu -- row re-layout of the stacked gate+up weight
 cudaError_t launch_interleave_gate_up(const void* src, void* dst, int64_t F, int64_t row_bytes, cudaStream_t stream);
 

@@ -1,0 +1,307 @@
+// The cache of keys and values in 8 bits: new tokens quantized as they are written to their pages, and
+// tokens read back in 16 bits.
+//
+//   e' = max(e, lowest exponent with amax <= 448 * 2^e')     per page and head; keys and values apart
+//   code = E4M3(x * 2^-e')                                   nearest, ties to even
+//
+// amax is over the call's tokens of the page; e counts where the page holds tokens before them, and when
+// e' > e those are re-encoded, code -> E4M3(code * 2^(e - e')).  With a power of two as the scale that is
+// a shift of exponents: it loses what falls below the lowest steps of E4M3 and nothing else, so a page
+// written token by token holds what one written at once holds, but for those steps.  (A free float32
+// scale rounds every code again at each growth.)
+#include <algorithm>
+
+#include "internal.h"
+#include "kv_e4m3.cuh"
+
+namespace wq {
+
+__device__ uint32_t g_kv_err;
+
+uint32_t kv_read_and_clear_error() {
+  uint32_t v = 0, z = 0;
+  cudaMemcpyFromSymbol(&v, g_kv_err, sizeof(v));
+  cudaMemcpyToSymbol(g_kv_err, &z, sizeof(z));
+  return v;
+}
+
+namespace {
+
+constexpr int kAppendThreads = 128;
+
+// A page that the call writes: request r's block, its new tokens' rows and places.
+struct Touched {
+  int row, count;        // first of the call's rows, number of rows
+  int place;             // of the first in the page; 0: the page starts afresh
+  int page;              // -1: none
+};
+
+// Pages that request r's new tokens lie in; `first` and `n`: its rows.
+__device__ __forceinline__ int touched_pages(const KvAppendArgs& a, int r, int& first, int& n, int& len, bool& bad) {
+  first = a.q_start ? __ldg(a.q_start + r) : r;
+  const int end = a.q_start ? __ldg(a.q_start + r + 1) : r + 1;
+  len = __ldg(a.lens + r);
+  n = end - first;
+  bad = first < 0 || end < first || end > a.T || n > a.max_new || len < 0 || len > a.max_blocks << a.log_page;
+  bad |= !bad && len > 0 && len < n;
+  if (bad || n == 0 || len == 0) return 0;     // length 0: a row that pads a batch
+  return ((len - 1) >> a.log_page) - ((len - n) >> a.log_page) + 1;
+}
+
+// The index-th page that the call writes, in the order of the requests.  All threads of the CTA.
+__device__ __forceinline__ Touched find_touched(const KvAppendArgs& a, int index) {
+  __shared__ int sums[kAppendThreads / 32];
+  __shared__ Touched out;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) out.page = -1;
+  int before = 0;
+  const bool checks = blockIdx.x == 0 && blockIdx.y == 0;    // one CTA looks at every request
+  for (int base = 0; base < a.R && (before <= index || checks); base += kAppendThreads) {
+    const int r = base + threadIdx.x;
+    int first = 0, n = 0, len = 0, c = 0;
+    if (r < a.R) {
+      bool bad;
+      c = touched_pages(a, r, first, n, len, bad);
+      if (bad && checks) atomicOr(&g_kv_err, kErrIndex);
+    }
+    int in = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += v;
+    }
+    if (lane == 31) sums[warp] = in;
+    __syncthreads();
+    int at = before + in - c;
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) {
+      if (w < warp) at += sums[w];
+      before += sums[w];
+    }
+    if (at <= index && index < at + c) {
+      const int start = len - n, block = (start >> a.log_page) + index - at, lo = max(start, block << a.log_page);
+      out.row = first + lo - start;
+      out.count = min(len, (block + 1) << a.log_page) - lo;
+      out.place = lo & (a.page_size - 1);
+      const int page = __ldg(a.block_table + static_cast<int64_t>(r) * a.max_blocks + block);
+      const bool fine = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
+      if (!fine) atomicOr(&g_kv_err, kErrIndex);
+      out.page = fine ? page : -1;
+    }
+    __syncthreads();
+  }
+  return out;
+}
+
+// The lowest exponent with amax <= 448 * 2^e = 1.75 * 2^(e + 8), kept in the range.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  if (amax <= 448.f * 5.421010862427522e-20f) return kScaleLow;     // 448 * 2^-64
+  const uint32_t bits = __float_as_uint(amax);
+  return min(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), kScaleHigh);
+}
+
+// N threads (a warp or the CTA) have a page of one head's keys or values: P pieces of 8 elements each.
+// Bound by the bytes (2 read, 1 written an element) for prompts, by launch and dependent loads for
+// decoding (starts and lengths, then the page and the tokens).
+template <bool F16, int D, int N, int P>
+__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs a) {
+  constexpr int kRow = D / 8;                  // pieces a token
+  constexpr uint32_t kInf = F16 ? 0x7c00u : 0x7f80u;
+  __shared__ uint32_t tops[kAppendThreads / 32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const Touched u = find_touched(a, blockIdx.x);
+  if (u.page < 0) return;
+  const int unit = blockIdx.y * (kAppendThreads / N) + threadIdx.x / N, j = threadIdx.x % N;
+  const bool on = unit < 2 * a.Hkv;            // with N = 128 always
+  const int head = on ? unit >> 1 : 0, is_v = unit & 1;
+  uint8_t* scale_at = (is_v ? a.v_scales : a.k_scales) + static_cast<int64_t>(u.page) * a.Hkv + head;
+  uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + ((static_cast<int64_t>(u.page) * a.Hkv + head) << a.log_page) * D;
+  const uint16_t* src = (is_v ? a.V : a.K) + u.row * (is_v ? a.v_stride : a.k_stride) + head * D;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const int pieces = on ? u.count * kRow : 0;
+  const uint32_t old_byte = *scale_at;
+  uint4 x[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int q = p * N + j;
+    x[p] = q < pieces ? __ldg(reinterpret_cast<const uint4*>(src + (q / kRow) * stride + (q % kRow) * 8)) : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t top2 = 0;                           // two magnitudes as 16-bit patterns, which order as the values do
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+    top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(x[p].x & 0x7fff7fffu, x[p].y & 0x7fff7fffu)),
+                    __vmaxu2(x[p].z & 0x7fff7fffu, x[p].w & 0x7fff7fffu));
+  const bool odd = max(top2 & 0xffffu, top2 >> 16) >= kInf;      // an infinity or a NaN among them
+  uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+  if (odd) {                                   // the largest finite one instead
+    top = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const uint32_t word = (&x[p].x)[w >> 1], m = (word >> (16 * (w & 1))) & 0x7fffu;
+        if (m < kInf) top = max(top, m);
+      }
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (N > 32) {
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) top = max(top, tops[w]);
+  }
+  const float amax = unpack2<F16>(top).x;
+  int e = scale_exponent(amax);
+  const int old = min(max(static_cast<int>(old_byte) - kScaleBias, kScaleLow), kScaleHigh);
+  if (u.place > 0) e = max(e, old);
+  if (!on) return;
+  __syncwarp();                                // every lane has read the old scale (N = 128: the barrier above)
+  if (j == 0) *scale_at = static_cast<uint8_t>(e + kScaleBias);
+  const float down = pow2_normal(-e);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int q = p * N + j;
+    if (q >= pieces) break;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 f = unpack2<F16>((&x[p].x)[i]);
+      f.x *= down, f.y *= down;
+      if (odd) {                               // infinities are kept as NaN, not as large numbers
+        if (isinf(f.x)) f.x = __uint_as_float(0x7fffffffu);
+        if (isinf(f.y)) f.y = __uint_as_float(0x7fffffffu);
+      }
+      w[i] = f32_to_e4m3x2(f.x, f.y);
+    }
+    *reinterpret_cast<uint2*>(dst + u.place * D + q * 8) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  }
+  if (u.place > 0 && e > old) {                // the page's scale has grown: tokens held already
+    const float shift = pow2_normal(max(old - e, -126));
+    for (int q = j; q < u.place * (D / 16); q += N) {
+      uint4* at = reinterpret_cast<uint4*>(dst) + q;
+      uint4 c = *at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t& w = (&c.x)[i];
+        const float2 lo = unpack2<true>(e4m3_low(w)), hi = unpack2<true>(e4m3_high(w));
+        w = f32_to_e4m3x2(lo.x * shift, lo.y * shift) | (f32_to_e4m3x2(hi.x * shift, hi.y * shift) << 16);
+      }
+      *at = c;
+    }
+  }
+}
+
+template <bool F16, int D>
+cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
+  const int64_t most = std::min<int64_t>(a.T, a.T / a.page_size + 2ll * a.R);      // pages that T tokens of R requests lie in
+  const int pieces = std::min(a.page_size, a.max_new) * D / 8;
+  if (pieces <= 4 * 32)
+    return launch_pdl(k_kv_append<F16, D, 32, 4>, dim3(static_cast<unsigned>(most), (2 * a.Hkv + 3) / 4), kAppendThreads, 0, stream, a);
+  const dim3 grid(static_cast<unsigned>(most), 2 * a.Hkv);
+  if (pieces <= 8 * 128) return launch_pdl(k_kv_append<F16, D, 128, 8>, grid, kAppendThreads, 0, stream, a);
+  return launch_pdl(k_kv_append<F16, D, 128, 16>, grid, kAppendThreads, 0, stream, a);
+}
+
+// ------------------------------------------------------------------------------- reading back
+constexpr int kReadThreads = 256, kReadTokens = 16, kReadAhead = 4;
+
+// A CTA has 16 rows of the output, K or V; a thread 16 elements at a time (16 bytes in, 32 out).
+template <bool F16, int D>
+__global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvReadArgs a) {
+  constexpr int kPieces = D / 16;
+  __shared__ int64_t where[kReadTokens];       // of each row: its token of head 0, counted in tokens of the cache; -1: none
+  __shared__ int pages[kReadTokens];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t0 = blockIdx.x * kReadTokens, count = min(kReadTokens, a.T - t0);
+  if (threadIdx.x < kReadTokens) where[threadIdx.x] = -1;
+  __syncthreads();
+  for (int r = threadIdx.x; r < a.R; r += kReadThreads) {
+    const int lo = __ldg(a.starts + r), hi = __ldg(a.starts + r + 1);
+    if (lo < 0 || hi < lo || hi > a.T) {
+      if (blockIdx.x == 0) atomicOr(&g_kv_err, kErrIndex);
+      continue;
+    }
+    for (int t = max(lo, t0); t < min(hi, t0 + count); ++t) {
+      const int pos = t - lo, block = pos >> a.log_page;
+      const int page = block < a.max_blocks ? __ldg(a.block_table + static_cast<int64_t>(r) * a.max_blocks + block) : -1;
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages)) {
+        atomicOr(&g_kv_err, kErrIndex);
+        continue;
+      }
+      pages[t - t0] = page;
+      where[t - t0] = ((static_cast<int64_t>(page) * a.Hkv) << a.log_page) + (pos & (a.page_size - 1));
+    }
+  }
+  __syncthreads();
+  const uint8_t* cache = blockIdx.y ? a.v_cache : a.k_cache;
+  const uint8_t* scales = blockIdx.y ? a.v_scales : a.k_scales;
+  uint16_t* out = (blockIdx.y ? a.Vo : a.Ko) + static_cast<int64_t>(t0) * a.Hkv * D;
+  const int per_token = a.Hkv * kPieces, units = count * per_token;
+  for (int base = threadIdx.x; base < units; base += kReadThreads * kReadAhead) {
+    uint4 c[kReadAhead];
+    uint32_t byte[kReadAhead];
+    bool on[kReadAhead];
+#pragma unroll
+    for (int i = 0; i < kReadAhead; ++i) {
+      const int u = base + i * kReadThreads, t = u / per_token, h = (u - t * per_token) / kPieces, piece = u % kPieces;
+      const int64_t at = u < units ? where[t] : -1;
+      on[i] = at >= 0;
+      c[i] = make_uint4(0, 0, 0, 0), byte[i] = kScaleBias;
+      if (on[i]) {
+        c[i] = __ldg(reinterpret_cast<const uint4*>(cache + (at + (static_cast<int64_t>(h) << a.log_page)) * D) + piece);
+        byte[i] = __ldg(scales + static_cast<int64_t>(pages[t]) * a.Hkv + h);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kReadAhead; ++i) {
+      if (!on[i]) continue;
+      const float s = scale_value(byte[i]);
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t word = (&c[i].x)[k >> 1];
+        float2 f = unpack2<true>(k & 1 ? e4m3_high(word) : e4m3_low(word));
+        f.x *= s, f.y *= s;
+        if (F16) {                             // past the type's largest value: that value (NaN stays NaN)
+          if (fabsf(f.x) > 65504.f) f.x = copysignf(65504.f, f.x);
+          if (fabsf(f.y) > 65504.f) f.y = copysignf(65504.f, f.y);
+        }
+        w[k] = pack2<F16>(f.x, f.y);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(base + i * kReadThreads) * 16);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+template <bool F16, int D>
+cudaError_t launch_read_t(const KvReadArgs& a, cudaStream_t stream) {
+  return launch_pdl(k_kv_read<F16, D>, dim3((a.T + kReadTokens - 1) / kReadTokens, 2), kReadThreads, 0, stream, a);
+}
+
+int log2_of(int page_size) {
+  int l = 0;
+  while ((1 << l) < page_size) ++l;
+  return l;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(int dtype, const KvAppendArgs& args, cudaStream_t stream) {
+  KvAppendArgs a = args;
+  a.log_page = log2_of(a.page_size);
+  if (dtype == kF16) return a.d == 64 ? launch_append_t<true, 64>(a, stream) : launch_append_t<true, 128>(a, stream);
+  return a.d == 64 ? launch_append_t<false, 64>(a, stream) : launch_append_t<false, 128>(a, stream);
+}
+
+cudaError_t launch_kv_read(int dtype, const KvReadArgs& args, cudaStream_t stream) {
+  KvReadArgs a = args;
+  a.log_page = log2_of(a.page_size);
+  if (dtype == kF16) return a.d == 64 ? launch_read_t<true, 64>(a, stream) : launch_read_t<true, 128>(a, stream);
+  return a.d == 64 ? launch_read_t<false, 64>(a, stream) : launch_read_t<false, 128>(a, stream);
+}
+
+}  // namespace wq

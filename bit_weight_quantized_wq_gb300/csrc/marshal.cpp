@@ -1,4 +1,4 @@
-// Argument marshalling of the attention-block operators for Python, compiled: a decode call's
+// Argument marshalling of the attention-block and 8-bit-cache operators for Python, compiled: a decode call's
 // kernels run for a few microseconds, and checking ten tensors attribute by attribute from Python
 // and passing thirty ctypes arguments took 20 and more (measured on the Grace host; about 5 here).
 // Checks types, devices, shapes and contiguity, allocates the outputs, finds the workspace of the
@@ -353,6 +353,115 @@ PyObject* gemm_lora(PyObject* const* a, Py_ssize_t n) {
   return THPVariable_Wrap(y);
 }
 
+// ------------------------------------------------------------------------------- the cache in 8 bits
+uint8_t* u8(const at::Tensor& t) { return static_cast<uint8_t*>(t.data_ptr()); }
+
+struct Cache8 {
+  at::Tensor k, v, ks, vs, table;
+  int64_t pages, Hkv, page, d, blocks;
+};
+
+// k_cache, v_cache, k_scales, v_scales, block_table
+Cache8 cache8(PyObject* const* a, int dev) {
+  Cache8 c;
+  c.k = tensor(a[0], "k_cache"), c.v = tensor(a[1], "v_cache");
+  c.ks = tensor(a[2], "k_scales"), c.vs = tensor(a[3], "v_scales"), c.table = tensor(a[4], "block_table");
+  dims(c.k, "k_cache", 4, "[pages, Hkv, page_size, d]");
+  c.pages = c.k.size(0), c.Hkv = c.k.size(1), c.page = c.k.size(2), c.d = c.k.size(3);
+  need(c.k, "k_cache", dev, at::kByte, c.k.sizes());
+  need(c.v, "v_cache", dev, at::kByte, c.k.sizes());
+  need(c.ks, "k_scales", dev, at::kByte, {c.pages, c.Hkv});
+  need(c.vs, "v_scales", dev, at::kByte, {c.pages, c.Hkv});
+  dims(c.table, "block_table", 2, "[R, blocks]");
+  need(c.table, "block_table", dev, at::kInt, c.table.sizes());
+  c.blocks = c.table.size(1);
+  return c;
+}
+
+// The requests' lengths and first rows: T tokens of table.size(0) requests.
+void rows_of(const at::Tensor& lens, const at::Tensor& q0, const Cache8& c, int dev, int64_t T) {
+  const int64_t R = c.table.size(0);
+  need(lens, "lens", dev, at::kInt, {R});
+  if (q0.defined()) need(q0, "q_start", dev, at::kInt, {R + 1});
+  else if (T != R) refuse("q_start is required unless there is one token a request");
+}
+
+// K, V, k_cache, v_cache, k_scales, v_scales, block_table, lens, q_start, max_new
+PyObject* kv_append(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 10);
+  const at::Tensor &K = tensor(a[0], "K"), &V = tensor(a[1], "V"), &lens = tensor(a[7], "lens");
+  const at::Tensor q0 = optional(a[8], "q_start");
+  const wq_dtype dt = dtype16(K, "K");
+  const int64_t ks = head_stride(K, "K"), vs = head_stride(V, "V"), T = K.size(0);
+  const On on(K);
+  const Cache8 c = cache8(a + 2, on.dev);
+  need(K, "K", on.dev, K.scalar_type(), {T, c.Hkv, c.d}, false);
+  need(V, "V", on.dev, K.scalar_type(), {T, c.Hkv, c.d}, false);
+  rows_of(lens, q0, c, on.dev, T);
+  done(wq_kv_append_e4m3(dt, u16(K), ks, u16(V), vs, T, c.table.size(0), c.Hkv, c.d, u8(c.k), u8(c.v), u8(c.ks), u8(c.vs), c.pages,
+                         c.page, i32(c.table), c.blocks, i32(lens), i32(q0), integer(a[9], "max_new"), on.stream),
+       "wq_kv_append_e4m3");
+  Py_RETURN_NONE;
+}
+
+// k_cache, v_cache, k_scales, v_scales, block_table, starts, tokens, float16, out K, out V -> (K, V)
+PyObject* kv_read(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 10);
+  const at::Tensor& k = tensor(a[0], "k_cache");
+  if (!k.is_cuda()) refuse("k_cache must be a CUDA tensor");
+  const On on(k);
+  const Cache8 c = cache8(a, on.dev);
+  const at::Tensor& starts = tensor(a[5], "starts");
+  const int64_t T = integer(a[6], "tokens"), R = c.table.size(0);
+  const bool f16 = truth(a[7], "float16");
+  const at::ScalarType ty = f16 ? at::kHalf : at::kBFloat16;
+  need(starts, "starts", on.dev, at::kInt, {R + 1});
+  if (T < 1) refuse("tokens must be at least 1");
+  at::Tensor ko = optional(a[8], "out K"), vo = optional(a[9], "out V");
+  if (ko.defined()) need(ko, "out K", on.dev, ty, {T, c.Hkv, c.d});
+  else ko = on.empty({T, c.Hkv, c.d}, ty);
+  if (vo.defined()) need(vo, "out V", on.dev, ty, {T, c.Hkv, c.d});
+  else vo = on.empty({T, c.Hkv, c.d}, ty);
+  done(wq_kv_read_e4m3(f16 ? WQ_DTYPE_F16 : WQ_DTYPE_BF16, u8(c.k), u8(c.v), u8(c.ks), u8(c.vs), c.pages, c.page, c.Hkv, c.d,
+                       i32(c.table), c.blocks, i32(starts), R, T, u16(ko), u16(vo), on.stream),
+       "wq_kv_read_e4m3");
+  PyObject* t = PyTuple_New(2);
+  if (!t) return nullptr;
+  PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(ko));
+  PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(vo));
+  return t;
+}
+
+// Q, k_cache, v_cache, k_scales, v_scales, block_table, lens, q_start, max_new, scale, out O, out lse, workspace -> (O, lse)
+PyObject* attn8(PyObject* const* a, Py_ssize_t n) {
+  arity(n, 13);
+  const at::Tensor &Q = tensor(a[0], "Q"), &lens = tensor(a[6], "lens");
+  const at::Tensor q0 = optional(a[7], "q_start");
+  const wq_dtype dt = dtype16(Q, "Q");
+  const at::ScalarType ty = Q.scalar_type();
+  const int64_t qs = head_stride(Q, "Q"), T = Q.size(0), Hq = Q.size(1), d = Q.size(2);
+  const On on(Q);
+  const Cache8 c = cache8(a + 1, on.dev);
+  if (c.d != d) refuse("Q and k_cache must have heads of the same size");
+  rows_of(lens, q0, c, on.dev, T);
+  const int64_t R = c.table.size(0), max_new = integer(a[8], "max_new");
+  const float scale = a[9] == Py_None ? 1.0f / std::sqrt(static_cast<float>(d)) : static_cast<float>(number(a[9], "scale"));
+  at::Tensor o = optional(a[10], "out O"), lse = optional(a[11], "out lse");
+  if (o.defined()) need(o, "out O", on.dev, ty, {T, Hq, d});
+  else o = on.empty({T, Hq, d}, ty);
+  if (lse.defined()) need(lse, "out lse", on.dev, at::kFloat, {T, Hq});
+  else lse = on.empty({T, Hq}, at::kFloat);
+  const at::Tensor ws = on.workspace(a[12], wq_attn_e4m3_workspace_bytes(T, R, Hq, c.Hkv, d, max_new));
+  done(wq_attn_e4m3(dt, u16(Q), qs, T, R, Hq, c.Hkv, d, u8(c.k), u8(c.v), u8(c.ks), u8(c.vs), c.pages, c.page, i32(c.table), c.blocks,
+                    i32(lens), i32(q0), max_new, scale, u16(o), f32(lse), ws.data_ptr(), ws.nbytes(), on.stream),
+       "wq_attn_e4m3");
+  PyObject* t = PyTuple_New(2);
+  if (!t) return nullptr;
+  PyTuple_SET_ITEM(t, 0, THPVariable_Wrap(o));
+  PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(lse));
+  return t;
+}
+
 // Raw stream -> the number of the graph capture that it takes part in, 0: none.
 PyObject* capture_id(PyObject* const* a, Py_ssize_t n) {
   arity(n, 1);
@@ -381,7 +490,8 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define WQ_ENTRY(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {WQ_ENTRY("qk_norm_rope", rope), WQ_ENTRY("qk_norm_rope_cache", rope_cache),
                          WQ_ENTRY("attn_shared_prefix", attn), WQ_ENTRY("lora_add", lora_add),
-                         WQ_ENTRY("gemm_w4a16_lora", gemm_lora), WQ_ENTRY("capture_id", capture_id), {nullptr, nullptr, 0, nullptr}};
+                         WQ_ENTRY("gemm_w4a16_lora", gemm_lora), WQ_ENTRY("kv_append_e4m3", kv_append), WQ_ENTRY("kv_read_e4m3", kv_read),
+                         WQ_ENTRY("attn_e4m3", attn8), WQ_ENTRY("capture_id", capture_id), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -567,6 +567,87 @@ wq_status wq_gemm_w4a16_lora(wq_fmt fmt, const uint16_t* X, int64_t M, int64_t K
                              int64_t r, const int32_t* ranks, const int32_t* adapter, const float* lora_scales,
                              uint16_t* Y, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * The cache of keys and values in 8 bits: FP8 E4M3 codes in pages with a scale for each page and
+ * head (推理优化与量化算子深度技术调研 §1.6 and 量化与加速 name FP8 for the cache; the codes are the
+ * E4M3 of wq_quantize_fp8_weights, the scales E8M0 bytes as those of wq_quantize_mxfp4).
+ *
+ * Common to the three
+ *   - A cache is k_cache, v_cache [pages, Hkv, page_size, d] uint8 (E4M3) and k_scales, v_scales
+ *     [pages, Hkv] uint8: element = E4M3(code) * 2^(byte - 127).  page_size is 16, 32, 64 or 128,
+ *     d is 64 or 128.  wq_kv_append_e4m3 writes bytes 63 .. 191 (exponents -64 .. 64); what the calls
+ *     compute of other bytes is unspecified.
+ *   - block_table [R, max_blocks] int32: the pages of the requests' tokens in order (entries past a
+ *     request's length are not read).  lens [R] int32: tokens of each request with this call's, at most
+ *     max_blocks * page_size; the n new tokens of a request are its last ones.
+ *   - q_start [R + 1] int32, ascending from 0: request r's new tokens are rows q_start[r] ..
+ *     q_start[r + 1] - 1, at most max_new of them.  It may end before row T: rows behind it (a batch
+ *     padded for a captured graph) are not read, and the outputs' rows are left as they were.  NULL:
+ *     one token a request (T == R, max_new == 1).
+ *   - dtype, alignment (scales: any), index checks and the error word as for the attention block above:
+ *     where an index is out of range, what depends on it is unspecified or not written, and bit 1 << 7 is
+ *     set.
+ */
+
+/*
+ * New tokens quantized as they are written to their pages.  For every page that the call writes, per
+ * head, keys and values apart:
+ *   need = the lowest e in [-64, 64] with amax <= 448 * 2^e, amax over the finite elements of the
+ *          call's tokens of the page (64 where it is larger, -64 where they are all 0);
+ *   e'   = need where the call writes the page's first place, else max(need, the page's exponent);
+ *   code = E4M3(x * 2^-e'), nearest, ties to even, saturating at +-448; infinities and NaN become NaN;
+ *   the places before the call's first token of the page: code = E4M3(code * 2^(e - e')), alike.
+ * So a page starts afresh when its first place is written, and its scale otherwise only grows; a token
+ * written again (a rejected draft's place) keeps the page's scale.  Other places stay as they were.
+ *   K, V [T, Hkv, d] dtype: a token's heads contiguous, tokens k_stride / v_stride elements apart (multiples
+ *     of 8, at least Hkv d).
+ *   A request of length 0 writes nothing (a row that pads a batch); with 0 < length < n it writes
+ *     nothing either, and the error word is set.  A page belongs to one request of the call.
+ * Errors: WQ_ERR_ARG (dtype; overlapping arrays); WQ_ERR_NULL; WQ_ERR_SHAPE unless T, R, Hkv, pages, max_new,
+ *   max_blocks >= 1, T, R <= 2^24, Hkv <= 1024, pages * Hkv <= 2^31 - 1, max_blocks * page_size <= 2^30,
+ *   d, page_size, strides and q_start as above; WQ_ERR_ALIGN; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.
+ */
+wq_status wq_kv_append_e4m3(wq_dtype dtype, const uint16_t* K, int64_t k_stride, const uint16_t* V, int64_t v_stride,
+                            int64_t T, int64_t R, int64_t Hkv, int64_t d, uint8_t* k_cache, uint8_t* v_cache,
+                            uint8_t* k_scales, uint8_t* v_scales, int64_t pages, int64_t page_size,
+                            const int32_t* block_table, int64_t max_blocks, const int32_t* lens, const int32_t* q_start,
+                            int64_t max_new, void* stream);
+
+/*
+ * Tokens read back in 16 bits, one request after the other: the first starts[r + 1] - starts[r] tokens of
+ * request r to rows starts[r] .. starts[r + 1] - 1 of Ko, Vo [T, Hkv, d] dtype (contiguous).  starts [R + 1]
+ * int32 ascends from 0 and may end before T: rows behind it are left as they were.  Exact in bf16; in fp16
+ * rounded once, values beyond the type's range saturate.
+ * Errors as wq_kv_append_e4m3.
+ */
+wq_status wq_kv_read_e4m3(wq_dtype dtype, const uint8_t* k_cache, const uint8_t* v_cache, const uint8_t* k_scales,
+                          const uint8_t* v_scales, int64_t pages, int64_t page_size, int64_t Hkv, int64_t d,
+                          const int32_t* block_table, int64_t max_blocks, const int32_t* starts, int64_t R, int64_t T,
+                          uint16_t* Ko, uint16_t* Vo, void* stream);
+
+/*
+ * Attention of R requests over the cache in 8 bits:
+ *   O[t, h] = sum_j p_j v_j,  p = softmax_j(scale q[t, h] . k_j),  lse[t, h] = ln sum_j e^(scale q . k_j)
+ * Query head h uses key/value head h / (Hq / Hkv).  New token i of a request sees its keys j <= lens[r] - n + i
+ * (the new tokens are in the cache already).  A row that sees no key gives O = 0 and lse = -inf.
+ *   Q [T, Hq, d]: tokens q_stride elements apart (a multiple of 8, at least Hq d).
+ *   Places past a request's length are not used, whatever they hold.  A NaN among the request's values
+ *     reaches every row that sees it, and of its own new tokens may reach those before it.
+ *   O [T, Hq, d] dtype, lse [T, Hq] float32 (may be NULL): contiguous outputs, distinct from Q.
+ *   workspace / ws_bytes: at least wq_attn_e4m3_workspace_bytes(...) bytes, under the workspace rules of
+ *     wq_gemm_workspace_bytes (it starts with the same header, left at zero).
+ * The weights of the values are rounded to fp16 (11 bits), their sum is not; queries and codes are exact.
+ * Errors: WQ_ERR_ARG (dtype; scale not positive and finite); WQ_ERR_NULL; WQ_ERR_SHAPE unless T, R, Hq, Hkv, pages,
+ *   max_new, max_blocks >= 1, T, R <= 2^24, Hq <= 1024, Hq % Hkv == 0, Hq / Hkv <= 128, T * (Hq / Hkv) <= 2^30,
+ *   the cache as above; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.
+ */
+size_t wq_attn_e4m3_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new);
+wq_status wq_attn_e4m3(wq_dtype dtype, const uint16_t* Q, int64_t q_stride, int64_t T, int64_t R, int64_t Hq, int64_t Hkv,
+                       int64_t d, const uint8_t* k_cache, const uint8_t* v_cache, const uint8_t* k_scales,
+                       const uint8_t* v_scales, int64_t pages, int64_t page_size, const int32_t* block_table,
+                       int64_t max_blocks, const int32_t* lens, const int32_t* q_start, int64_t max_new, float scale,
+                       uint16_t* O, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 /* WQ_OK when the current device is a GB300-class part (compute capability 10.3). */
 wq_status wq_check_device(void);
 
