@@ -15,15 +15,19 @@
 // item (a segment) goes to the workspace, unnormalised, and the last CTA that is done with the item
 // joins its segments in line order.  A CTA has two such segments at most, its first and its last.
 //
-// The kernel: a warp has 16 rows and takes 16 keys at a time straight from global memory
-// into the registers that mma.sync wants them in: for S = Q K^T a thread's 4 bytes along d are one
-// fragment (Q is loaded in the same order of d), for O += P V the bytes of two keys are interleaved as
-// they are widened, so V needs no transposition, and the scores' registers are P's.  4 warps: the row
-// tiles of the item (1, 2 or 4), and the 16-key steps shared out among the warps of a row tile.
+// Few rows (k_attn_e4m3): a warp has 8 NR rows of the item (its row tile), and the warps of a row tile take the
+// steps of 16 keys (32 where d is 64) in turn, copied by the warp itself with cp.async two steps ahead: 512
+// contiguous bytes a copy, kept in that order but for a swizzle of the 16-byte chunks.  (With each thread copying what
+// it will read, in the fragments' order, a copy of 512 bytes took 26 passes of the shared memory instead of 4.)
+// Products are transposed, S^T = K Q^T and O^T = V^T P^T, so that eight rows fill a fragment of mma.sync: for the
+// first a thread's 4 bytes along d are a fragment of K (Q is loaded in the same order of d), for the second the
+// bytes of two keys are interleaved as they are widened, so V needs no transposition, and an 8 x 8 transposition in
+// registers turns the scores into the fragment of P.
 #include <algorithm>
 
 #include "internal.h"
 #include "kv_e4m3.cuh"
+#include "tcgen05.cuh"
 
 namespace wq {
 
@@ -39,18 +43,16 @@ uint32_t attn_e4m3_read_and_clear_error() {
 namespace {
 
 constexpr int kTile = 64;              // keys a tile of the line
-constexpr int kStep = 16;              // keys a warp takes at a time (a page holds whole steps)
-constexpr int kFewRows = 64;           // rows an item
-constexpr int kFewThreads = 128, kFewWarps = 4, kFewCtas = 3;     // CTAs an SM
 constexpr float kLazy = 8.f;           // the running maximum follows when it grew by more than 2^8 ...
 constexpr float kUp = 7.f;             // ... and weights stand 2^7 higher, up to 2^15: fp16 reaches 2^-31 of the largest
 
 struct Params {
   AttnE4m3Args a;
   int G, log_page;
+  int few;                   // requests of up to so many rows are the first kernel's
   float c;                   // scale * log2(e)
   int* count;                // segments of the item that begins in a CTA which are done [ctas]
-  float *po;                 // partials [cta][2][64][d], largest exponents and sums [cta][2][64][2]
+  float *po;                 // partials [cta][2][rows of an item][d], largest exponents and sums [cta][2][rows][2]
   float2 *ml;
 };
 
@@ -74,25 +76,45 @@ __device__ __forceinline__ Request request(const AttnE4m3Args& a, int r) {
 // Keys that row `row` of the request sees.
 __device__ __forceinline__ int keys_seen(const Request& q, int token) { return min(max(q.len - q.n + token + 1, 0), q.len); }
 
-// The items of one request and head: row tiles, their key tiles and line lengths.
+// A line's items: their rows, the weight of a tile (by the item's rows) and the constant of an item.
+// Weights are in units of some 20 cycles of an SM.
+template <int NR, int W>
+struct FewLine {
+  __device__ static bool takes(const Params& p, int rows) { return rows <= p.few; }
+  static constexpr int kThreads = 32 * W, kRows = 4 * 8 * NR, kItem = 60, kMost = 20;
+  __device__ static int weight(int rows) { return rows <= 8 * NR ? 8 : rows <= 16 * NR ? 12 : kMost; }
+};
+
+constexpr int kManyThreads = 512, kManyRows = 256;
+struct ManyLine {
+  __device__ static bool takes(const Params& p, int rows) { return rows > p.few; }
+  static constexpr int kThreads = kManyThreads, kRows = kManyRows, kItem = 30, kMost = 10;
+  __device__ static int weight(int rows) { return rows <= kManyRows / 2 ? 6 : kMost; }
+};
+
+// One item: row tile rt of a request and head.
 struct Shape {
   int rows, tiles, weight;
 };
-constexpr int kWItem = 12;
-__device__ __forceinline__ int tile_weight(int rows) { return rows <= 16 ? 8 : rows <= 32 ? 12 : 20; }
+template <class L>
+__device__ __forceinline__ int row_tiles(const Params& p, const Request& q) {
+  const int rows = q.n * p.G;
+  return L::takes(p, rows) ? (rows + L::kRows - 1) / L::kRows : 0;
+}
+template <class L>
 __device__ __forceinline__ Shape shape(const Params& p, const Request& q, int rt) {
   Shape s;
-  s.rows = min(kFewRows, q.n * p.G - rt * kFewRows);
-  s.tiles = max(1, (keys_seen(q, (rt * kFewRows + s.rows - 1) / p.G) + kTile - 1) / kTile);
-  s.weight = tile_weight(s.rows);
+  s.rows = min(L::kRows, q.n * p.G - rt * L::kRows);
+  s.tiles = max(1, (keys_seen(q, (rt * L::kRows + s.rows - 1) / p.G) + kTile - 1) / kTile);
+  s.weight = L::weight(s.rows);
   return s;
 }
-__device__ __forceinline__ int row_tiles(const Params& p, const Request& q) { return (q.n * p.G + kFewRows - 1) / kFewRows; }
+template <class L>
 __device__ __forceinline__ long long head_cost(const Params& p, const Request& q) {
   long long c = 0;
-  for (int rt = 0; rt < row_tiles(p, q); ++rt) {
-    const Shape s = shape(p, q, rt);
-    c += static_cast<long long>(s.tiles) * s.weight + kWItem;
+  for (int rt = 0; rt < row_tiles<L>(p, q); ++rt) {
+    const Shape s = shape<L>(p, q, rt);
+    c += static_cast<long long>(s.tiles) * s.weight + L::kItem;
   }
   return c;
 }
@@ -109,16 +131,43 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 16 bytes of the cache, read once.
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// The 8 x 8 transpose of a matrix of 16-bit elements held two a thread.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
-__device__ __forceinline__ uint2 load_codes8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+
+// Byte offset of the 16 bytes `c` of key `key` in a stage as TMA's 128-byte swizzle leaves them: rows of 128 bytes
+// (two keys where d is 64), the 8 chunks of a row exchanged by the row's number.
+template <int D>
+__device__ __forceinline__ int chunk_at(int key, int c) {
+  const int row = key / (128 / D), chunk = D == 128 ? c : 4 * (key & 1) + c;
+  return 128 * row + 16 * (chunk ^ (row & 7));
+}
+// The key of fragment row m among a piece's 16, chosen so that eight lanes' reads of K (keys of rows g) and of V
+// (keys of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9) fall on all banks.
+template <int D>
+__device__ __forceinline__ int key_of_row(int m) {
+  return D == 128 ? m : 4 * ((m & 7) >> 1) + 2 * (m >> 3) + (m & 1);
+}
+
+// A wait of a whole warp, bounded as mbar_wait_short is; once one has run out, all others give up too.
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* failed, uint32_t code) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, *failed != 0)) return false;
+    if (__any_sync(0xffffffffu, clock64() - t0 > 4000000000ll)) {
+      atomicOr(&g_attn8_err, code);
+      *failed = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
 
 // The line's length and the request in which position b0 lies; all threads of the CTA.
@@ -126,17 +175,19 @@ struct Place {
   long long share, b0, at;   // line units a CTA; where this CTA's begins; where request r begins
   int r;                     // -1: nothing for this CTA
 };
+template <class L>
 __device__ __forceinline__ Place find_place(const Params& p) {
-  __shared__ long long sums[kFewWarps];
+  constexpr int kWarps = L::kThreads / 32;
+  __shared__ long long sums[kWarps];
   __shared__ long long found_at;
   __shared__ int found_r;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long mine = 0, first_cost = 0;
-  for (int r = threadIdx.x; r < p.a.R; r += kFewThreads) {
+  for (int r = threadIdx.x; r < p.a.R; r += L::kThreads) {
     const Request q = request(p.a, r);
     if (q.bad && blockIdx.x == 0) atomicOr(&g_attn8_err, kErrIndex);
-    const long long c = p.a.Hkv * head_cost(p, q);
-    if (r < kFewThreads) first_cost = c;
+    const long long c = p.a.Hkv * head_cost<L>(p, q);
+    if (r < L::kThreads) first_cost = c;
     mine += c;
   }
 #pragma unroll
@@ -146,14 +197,14 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   __syncthreads();
   long long total = 0;
 #pragma unroll
-  for (int w = 0; w < kFewWarps; ++w) total += sums[w];
+  for (int w = 0; w < kWarps; ++w) total += sums[w];
   Place s;
-  s.share = max(static_cast<long long>(tile_weight(kFewRows)), (total + gridDim.x - 1) / gridDim.x);
+  s.share = max(static_cast<long long>(L::kMost), (total + gridDim.x - 1) / gridDim.x);
   s.b0 = blockIdx.x * s.share;
   long long before = 0;
-  for (int base = 0; base < p.a.R && before <= s.b0 && s.b0 < total; base += kFewThreads) {
+  for (int base = 0; base < p.a.R && before <= s.b0 && s.b0 < total; base += L::kThreads) {
     const int r = base + threadIdx.x;
-    const long long c = base == 0 ? first_cost : r < p.a.R ? p.a.Hkv * head_cost(p, request(p.a, r)) : 0;
+    const long long c = base == 0 ? first_cost : r < p.a.R ? p.a.Hkv * head_cost<L>(p, request(p.a, r)) : 0;
     long long in = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -165,7 +216,7 @@ __device__ __forceinline__ Place find_place(const Params& p) {
     __syncthreads();
     long long at = before + in - c;
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) at += sums[w];
       before += sums[w];
     }
@@ -183,72 +234,233 @@ __device__ __forceinline__ int tile_at(long long b, long long s, int n, int w) {
   return d >= static_cast<long long>(n) * w ? n : (static_cast<int>(d) + w - 1) / w;
 }
 
-template <int D>
+// Walks over the items of one CTA's share of the line; copying and computing warps alike.
+template <class L>
+struct Walk {
+  const Params& p;
+  long long b0, b1, line, start;   // the share, where the next item begins, where this one does
+  int r, kvh, rt;                  // of the next item
+  Request q;
+  // the item: its request's row tile `tile`, head, shape, and the key tiles of this share
+  int tile, head, lo, hi;
+  Shape it;
+
+  __device__ Walk(const Params& p_, const Place& s) : p(p_), b0(s.b0), b1(s.b0 + s.share), line(s.at), r(s.r), kvh(0), rt(0) {
+    q = request(p.a, r);
+    const long long cost = head_cost<L>(p, q);       // heads before the share
+    kvh = static_cast<int>((b0 - line) / cost);
+    line += kvh * cost;
+  }
+  __device__ bool next() {
+    while (line < b1) {
+      if (rt == row_tiles<L>(p, q)) {
+        rt = 0;
+        if (row_tiles<L>(p, q) == 0 || ++kvh == p.a.Hkv) {
+          kvh = 0;
+          if (++r == p.a.R) return false;
+          q = request(p.a, r);
+        }
+        continue;
+      }
+      it = shape<L>(p, q, rt);
+      tile = rt, head = kvh, start = line;
+      line += static_cast<long long>(it.tiles) * it.weight + L::kItem;
+      ++rt;
+      lo = tile_at(b0, start, it.tiles, it.weight), hi = tile_at(b1, start, it.tiles, it.weight);
+      if (lo < hi) return true;
+    }
+    return false;
+  }
+  // Stages of KEYS keys of this share of the item, up to the last key that its last row sees.
+  template <int KEYS>
+  __device__ int stages(int& first) const {
+    const int seen = keys_seen(q, (tile * L::kRows + it.rows - 1) / p.G);
+    first = lo * (kTile / KEYS);
+    return max(0, min(hi * (kTile / KEYS), (seen + KEYS - 1) / KEYS) - first);
+  }
+};
+
+// The warp that copies: stages of KEYS keys and values of all the CTA's items into a ring of N places (ring(i): where
+// stage i's keys go, its values follow), and the scales of the stage's boxes to scales(i).  A box is what one copy
+// takes: a page's run of up to KEYS keys.
+template <class L, int D, int KEYS, int N, class Ring, class Scales>
+__device__ __forceinline__ void copy_items(const Params& p, const Place& place, const CUtensorMap& tk, const CUtensorMap& tv,
+                                           const Ring& ring, uint64_t* full, uint64_t* empty, const Scales& scales, int* failed) {
+  const int lane = threadIdx.x & 31;
+  Walk<L> walk(p, place);
+  uint32_t stage = 0;                          // of all items so far
+  const uint64_t once = l2_policy_evict_first();
+  const int box = min(p.a.page_size, KEYS), boxes = KEYS / box, log_box = 31 - __clz(box);
+  bool ok = true;
+  while (ok && walk.next()) {
+    int first;
+    const int n = walk.template stages<KEYS>(first), len = walk.q.len;
+    const int32_t* table = p.a.block_table + static_cast<int64_t>(walk.r) * p.a.max_blocks;
+    // lane i has box base + i of the item; the table of the 32 after it is on its way
+    const auto table_at = [&](int base) {
+      const int key = first * KEYS + ((base + lane) << log_box);
+      return base + lane < n * boxes && key < len ? __ldg(table + (key >> p.log_page)) : 0;
+    };
+    int row = 0, ahead = table_at(0);
+    uint32_t scale = 0;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j, ++stage) {
+      const int b0 = j * boxes;
+      if ((b0 & 31) == 0) {
+        int page = ahead;
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.a.pages)) {
+          atomicOr(&g_attn8_err, kErrIndex);
+          page = 0;
+        }
+        row = page * p.a.Hkv + walk.head;
+        scale = __ldg(p.a.k_scales + row) | (static_cast<uint32_t>(__ldg(p.a.v_scales + row)) << 8);
+        ahead = table_at(b0 + 32);
+      }
+      const int s = stage % N;
+      ok = stage_wait(&empty[s], ((stage / N) & 1) ^ 1, failed, kErrWaitEmpty);
+      if (!ok) break;
+      const int mine = lane - (b0 & 31);
+      if (mine >= 0 && mine < boxes) scales(stage)[mine] = static_cast<uint16_t>(scale);
+      int rows[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows[i] = __shfl_sync(0xffffffffu, row, (b0 + i) & 31);
+      // boxes with a key of the request
+      const int count = min(boxes, (len - (first + j) * KEYS + box - 1) >> log_box);
+      __syncwarp();
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[s], 2 * count * box * D);
+        uint8_t* dst = ring(stage);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < count) {
+            const int in_page = (((first + j) * KEYS + (i << log_box)) & (p.a.page_size - 1)) * D / 128;
+            tma_load_4d(dst + i * box * D, &tk, 0, in_page, 0, rows[i], &full[s], once);
+            tma_load_4d(dst + KEYS * D + i * box * D, &tv, 0, in_page, 0, rows[i], &full[s], once);
+          }
+      }
+      __syncwarp();
+    }
+  }
+  // the last fill of each place has landed before the CTA's memory goes
+  for (uint32_t i = stage > N ? stage - N : 0; i < stage; ++i)
+    mbar_wait_short(&full[i % N], (i / N) & 1, &g_attn8_err, kErrDrain);
+}
+
+constexpr int kStages = 3;             // steps of a warp in shared memory, two of them under way
+constexpr int kStepBytes = 2048;       // of K, and of V
+template <int D, int NR, int W>
 struct FewSmem {
-  // a warp's outputs: [row][D / 32 quarters of 32 columns], padded so that stores of 16 bytes fall on all banks
-  static constexpr int kQuarter = D / 4 + 4, kRow = 4 * kQuarter;
-  float o[kFewWarps][16][kRow];
-  float2 ml[kFewWarps][16];
+  static constexpr int kRow = D + 4;
+  union {
+    uint8_t ring[W][kStages][2][kStepBytes];   // K, V
+    float o[W][8 * NR][kRow];                  // the warps' outputs, once their steps are done
+  };
+  float2 ml[W][8 * NR];
   int last;
 };
 
-template <bool F16, int D>
-__global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_e4m3(const __grid_constant__ Params p) {
-  constexpr int KS = D / 16;                   // 16-wide steps of d
-  constexpr int NT = D / 8;                    // 8-wide tiles of d
-  __shared__ FewSmem<D> sm;
+// Codes global -> shared memory.
+__device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Warps an SM: registers for 16 with eight rows a warp, for 12 with sixteen.
+constexpr int few_warps(int nr) { return nr == 1 ? 16 : 12; }
+
+template <bool F16, int D, int NR, int W>
+__global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const __grid_constant__ Params p) {
+  using L = FewLine<NR, W>;
+  using S = FewSmem<D, NR, W>;
+  constexpr int kKeys = kStepBytes / D;        // of a step
+  constexpr int kPieces = kKeys / 16;
+  constexpr int KS = D / 16;                   // 16-wide steps of d, and 16-row tiles of V^T
+  constexpr int R2 = 2 * NR;                   // rows that a thread has scores of: 2 t, 2 t + 1 (and 8 more each)
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const Place place = find_place(p);
+  // where this lane's copies go: chunk 32 i + lane of a step is chunk lane % 8 of row 4 i + lane / 8 of 128 bytes
+  const uint32_t ring = smem_u32(sm.ring[warp][0][0]);
+  const uint32_t to_even = 128 * (lane >> 3) + 16 * ((lane & 7) ^ (lane >> 3)), to_odd = to_even ^ 64;
+  const uint8_t *k_lane = p.a.k_cache + 16 * lane, *v_lane = p.a.v_cache + 16 * lane;
+  const Place place = find_place<L>(p);
   if (place.r < 0) return;
-  const long long b0 = place.b0, b1 = b0 + place.share;
-  long long line = place.at;
-  int r = place.r, kvh = 0, rt = 0;
-  Request q = request(p.a, r);
-  {                                            // heads before the share
-    const long long head = head_cost(p, q);
-    kvh = static_cast<int>((b0 - line) / head);
-    line += kvh * head;
-  }
+  Walk<L> walk(p, place);
 #pragma unroll 1
-  while (line < b1) {
-    if (rt == row_tiles(p, q)) {               // on to the next item
-      rt = 0;
-      if (q.n == 0 || ++kvh == p.a.Hkv) {
-        kvh = 0;
-        if (++r == p.a.R) break;
-        q = request(p.a, r);
-      }
-      continue;
-    }
-    const Shape it = shape(p, q, rt);
-    const long long start = line;
-    const int row0 = rt * kFewRows;
-    line += static_cast<long long>(it.tiles) * it.weight + kWItem;
-    ++rt;
-    const int lo = tile_at(b0, start, it.tiles, it.weight), hi = tile_at(b1, start, it.tiles, it.weight);
-    if (lo >= hi) continue;
-
+  while (walk.next()) {
+    const Request& q = walk.q;
+    const Shape& it = walk.it;
+    const int kvh = walk.head, row0 = walk.tile * L::kRows;
     // ------------------------------------------------------------------ this warp's rows
-    const int mt = it.rows <= 16 ? 1 : it.rows <= 32 ? 2 : 4, wk = kFewWarps / mt;
-    const int m_tile = warp & (mt - 1), phase = warp / mt;
-    const int row_base = m_tile * 16;          // within the item
-    int lim[2];                                // keys that rows g and g + 8 see
-    float crow[2];                             // c, times the power of two taken from the row's query
-    uint32_t qf[KS][4];
+    const int mt = it.rows <= 8 * NR ? 1 : it.rows <= 16 * NR ? 2 : 4, wk = W / mt;
+    const int row_base = (warp & (mt - 1)) * 8 * NR, phase = warp / mt;
+    // the most keys that a row of the warp sees, and the fewest
+    const int last_row = min(it.rows, row_base + 8 * NR) - 1;
+    const int lim_top = last_row < row_base ? 0 : keys_seen(q, (row0 + last_row) / p.G);
+    const int lim_low = keys_seen(q, (row0 + row_base) / p.G);
+    int first;
+    const int n_steps = walk.template stages<kKeys>(first);
+    const int s0 = first + phase, s1 = min(first + n_steps, (lim_top + kKeys - 1) / kKeys);
+    const int steps = s1 > s0 ? (s1 - s0 + wk - 1) / wk : 0;
+    const int32_t* table = p.a.block_table + static_cast<int64_t>(walk.r) * p.a.max_blocks;
+
+    // Lane i looks up piece i (16 keys) of a window of 32: its page, as the piece's place in the caches (16 D bytes
+    // each: as many as memory can hold fit 32 bits), and the page's scales; the table of the window after it is on its
+    // way, the scales of the one before it are kept for the steps that the copies are ahead.
+    const auto key_of = [&](int piece) { return (s0 + (piece / kPieces) * wk) * kKeys + 16 * (piece % kPieces); };
+    const auto table_at = [&](int base) {
+      const int key = key_of(base + lane);
+      return base + lane < steps * kPieces && key < q.len ? __ldg(table + (key >> p.log_page)) : 0;
+    };
+    int page_next = table_at(0);
+    uint32_t piece_i = 0, scale_i = 0, scale_before = 0;
+    const auto look_up = [&](int base) {
+      int page = page_next;
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.a.pages)) {
+        atomicOr(&g_attn8_err, kErrIndex);
+        page = 0;
+      }
+      const uint32_t at = static_cast<uint32_t>(page) * p.a.Hkv + kvh;
+      piece_i = (at << (p.log_page - 4)) + ((key_of(base + lane) & (p.a.page_size - 1)) >> 4);
+      scale_before = scale_i;
+      scale_i = __ldg(p.a.k_scales + at) | (static_cast<uint32_t>(__ldg(p.a.v_scales + at)) << 8);
+      page_next = table_at(base + 32);
+    };
+    const auto issue = [&](int j) {
+      if (j < steps) {
+        if (((j * kPieces) & 31) == 0) look_up(j * kPieces);
+        const uint32_t slot = ring + (j % kStages) * (2 * kStepBytes);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = row_base + g + 8 * h;
+        for (int h = 0; h < kPieces; ++h) {
+          const uint32_t piece = __shfl_sync(0xffffffffu, piece_i, (j * kPieces + h) & 31);
+          const uint8_t *k = k_lane + static_cast<uint64_t>(piece) * (16 * D), *v = v_lane + static_cast<uint64_t>(piece) * (16 * D);
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {   // 16 keys are D contiguous chunks
+            const uint32_t dst = slot + (i & 1 ? to_odd : to_even) + 16 * D * h + 512 * i;
+            copy_codes(dst, k + 512 * i);
+            copy_codes(dst + kStepBytes, v + 512 * i);
+          }
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll
+    for (int j = 0; j < kStages - 1; ++j) issue(j);
+    uint32_t qf[KS][NR][2];
+    float crow[R2];                            // c, times the power of two taken from the row's query
+    int lim[R2];                               // keys that the row sees
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int row = row_base + 8 * n + g;
       const bool valid = row < it.rows;
       const int tok = (row0 + row) / p.G, head = kvh * p.G + (row0 + row) - tok * p.G;
-      lim[h] = valid ? keys_seen(q, tok) : 0;
       uint4 x[D / 32];
       const uint16_t* src = p.a.Q + (q.first + tok) * p.a.q_stride + head * D;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)         // 16 elements at 16 t, and for d = 128 at 64 + 16 t
-        x[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src + 64 * (i >> 1) + 16 * t) + (i & 1)) : make_uint4(0, 0, 0, 0);
-      crow[h] = p.c;
+      for (int i = 0; i < D / 32; ++i)         // elements (D / 4) t .. of the row
+        x[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src + (D / 4) * t) + i) : make_uint4(0, 0, 0, 0);
+      float c = p.c;
       if (!F16) {
         uint32_t mx = 0;
 #pragma unroll
@@ -259,7 +471,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_e4m3(const __gri
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const int k = bf16_to_f16_exponent(mx);
         const float down = pow2_normal(-k);
-        crow[h] *= pow2_normal(k);
+        c *= pow2_normal(k);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -270,182 +482,188 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_e4m3(const __gri
       }
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        qf[s][h] = (&x[s >> 1].x)[2 * (s & 1)];
-        qf[s][2 + h] = (&x[s >> 1].x)[2 * (s & 1) + 1];
+        qf[s][n][0] = (&x[s >> 1].x)[2 * (s & 1)];
+        qf[s][n][1] = (&x[s >> 1].x)[2 * (s & 1) + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        crow[2 * n + i] = F16 ? p.c : __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
+        const int mine = row_base + 8 * n + 2 * t + i;
+        lim[2 * n + i] = mine < it.rows ? keys_seen(q, (row0 + mine) / p.G) : 0;
       }
     }
-    const int lim_top = __reduce_max_sync(0xffffffffu, max(lim[0], lim[1]));
-    // lowest limit among the rows that exist
-    const int lim_low = __reduce_min_sync(0xffffffffu, min(row_base + g < it.rows ? lim[0] : 0x7fffffff,
-                                                           row_base + g + 8 < it.rows ? lim[1] : 0x7fffffff));
 
-    // ------------------------------------------------------------------ its keys: steps of 16
-    float acc[NT][4];
+    // ------------------------------------------------------------------ its stages
+    float acc[KS][NR][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-    const int s0 = lo * (kTile / kStep) + phase, s1 = min(hi * (kTile / kStep), (lim_top + kStep - 1) / kStep);
-    const int steps = s1 > s0 ? (s1 - s0 + wk - 1) / wk : 0;
-    const int32_t* table = p.a.block_table + static_cast<int64_t>(r) * p.a.max_blocks;
-    const int steps_log = p.log_page - 4;      // steps a page, log2
-
-    // Lane i looks up step i of a window of 32: its page and the page's scales.
-    int page_i = 0;
-    uint32_t scale_i = 0;
-    const auto look_up = [&](int base) {
-      page_i = 0;
-      if (base + lane < steps) {
-        page_i = __ldg(table + ((s0 + (base + lane) * wk) >> steps_log));
-        if (static_cast<uint32_t>(page_i) >= static_cast<uint32_t>(p.a.pages)) {
-          atomicOr(&g_attn8_err, kErrIndex);
-          page_i = 0;
-        }
-      }
-      const int64_t at = static_cast<int64_t>(page_i) * p.a.Hkv + kvh;
-      scale_i = __ldg(p.a.k_scales + at) | (static_cast<uint32_t>(__ldg(p.a.v_scales + at)) << 8);
-    };
-    // Bytes of a step's first key within the caches.
-    const auto offset = [&](int j) {
-      const int64_t page = __shfl_sync(0xffffffffu, page_i, j & 31);
-      return (((page * p.a.Hkv + kvh) << p.log_page) + (((s0 + j * wk) << 4) & (p.a.page_size - 1))) * D;
-    };
-    uint4 kc[2][D / 64];                       // keys 4 (g / 2) + g % 2 and + 2; bytes 16 t and, for d = 128, 64 + 16 t
-    uint32_t vc[4][D / 32];                    // keys 4 t .. 4 t + 3; bytes (D / 8) g ..
-    const auto load_k = [&](int64_t at) {
-      const uint8_t* src = p.a.k_cache + at + (4 * (g >> 1) + (g & 1)) * D + 16 * t;
+    for (int j = 0; j < KS; ++j)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NR; ++n) acc[j][n][0] = acc[j][n][1] = acc[j][n][2] = acc[j][n][3] = 0.f;
+    float m[R2], sum[R2];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) kc[n][i] = load_codes(src + 2 * n * D + 64 * i);
-    };
-    const auto load_v = [&](int64_t at) {
-      const uint8_t* src = p.a.v_cache + at + 4 * t * D + (D / 8) * g;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (D == 128) {
-          const uint4 v = load_codes(src + i * D);
-          vc[i][0] = v.x, vc[i][1] = v.y, vc[i][2] = v.z, vc[i][3] = v.w;
-        } else {
-          const uint2 v = load_codes8(src + i * D);
-          vc[i][0] = v.x, vc[i][1] = v.y;
-        }
-      }
-    };
-    int64_t at = 0, at_next = 0;
-    uint32_t scales = 0;
-    if (steps > 0) {
-      look_up(0);
-      at = offset(0);
-      scales = __shfl_sync(0xffffffffu, scale_i, 0);
-      load_k(at);
-      load_v(at);
-    }
+    for (int i = 0; i < R2; ++i) m[i] = -INFINITY, sum[i] = 0.f;
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
-      const int key0 = (s0 + j * wk) << 4;
-      // S = Q K^T: c[n][0..1] row g, keys 4 t + 2 n, + 1; c[n][2..3] row g + 8
-      float s[2][4];
+      // the scales of step j: the look-ups may be a window ahead
+      uint32_t scales[kPieces];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      for (int h = 0; h < kPieces; ++h) {
+        const int piece = j * kPieces + h, ahead = min(j + kStages - 2, steps - 1) * kPieces;
+        scales[h] = __shfl_sync(0xffffffffu, (piece >> 5) == (ahead >> 5) ? scale_i : scale_before, piece & 31);
+      }
+      __syncwarp();                            // all lanes have read the step before
+      issue(j + kStages - 1);
+      copy_wait<kStages - 1>();
+      __syncwarp();                            // all lanes' copies are there
+      const uint8_t *k_at = sm.ring[warp][j % kStages][0], *v_at = sm.ring[warp][j % kStages][1];
+      const int key0 = (s0 + j * wk) * kKeys;
+      {
+        // S^T = K Q^T: s[h][n][0 .. 1] the key of row g, query rows 2 t, 2 t + 1; s[h][n][2 .. 3] that of row g + 8
+        float s[kPieces][NR][4];
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+        for (int h = 0; h < kPieces; ++h) {
+          uint4 k[2][D / 64];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const uint32_t w = (&kc[n][k >> 2].x)[k & 3];
-          mma16816(s[n], qf[k], e4m3_low(w), e4m3_high(w));
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w)
+              k[i][w] = *reinterpret_cast<const uint4*>(k_at + 16 * D * h + chunk_at<D>(key_of_row<D>(g + 8 * i), (D / 64) * t + w));
+          float odd[NR][4];                    // two sums, so that products need not wait for one another
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[h][n][i] = odd[n][i] = 0.f;
+#pragma unroll
+          for (int c = 0; c < KS; ++c) {
+            const uint32_t w0 = (&k[0][c >> 2].x)[c & 3], w1 = (&k[1][c >> 2].x)[c & 3];
+            const uint32_t a[4] = {e4m3_low(w0), e4m3_low(w1), e4m3_high(w0), e4m3_high(w1)};
+#pragma unroll
+            for (int n = 0; n < NR; ++n) mma16816(NR == 1 && (c & 1) ? odd[n] : s[h][n], a, qf[c][n][0], qf[c][n][1]);
+          }
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (NR == 1) s[h][n][i] += odd[n][i];
         }
-      uint32_t scales_next = 0;
-      if (j + 1 < steps) {
-        if (((j + 1) & 31) == 0) look_up(j + 1);
-        at_next = offset(j + 1);
-        scales_next = __shfl_sync(0xffffffffu, scale_i, (j + 1) & 31);
-        load_k(at_next);
-      }
-      const float k_scale = scale_value(scales & 0xffu), ev = static_cast<float>(static_cast<int>(scales >> 8) - kScaleBias);
-      const float inv_v = scale_value(2 * kScaleBias - (scales >> 8));
-      float x[2][4];                           // [row][key of the thread's four]
+        float x[kPieces][R2][2];               // [row][key of row g, g + 8]
+        const bool edge = key0 + 16 * kPieces > lim_low;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float ck = crow[h] * k_scale;
+        for (int h = 0; h < kPieces; ++h) {
+          const float k_scale = scale_value(scales[h] & 0xffu), ev = static_cast<float>(static_cast<int>(scales[h] >> 8) - kScaleBias);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[h][i] = fmaf(s[i >> 1][2 * h + (i & 1)], ck, ev);
-      }
-      if (key0 + kStep > lim_low) {
+          for (int i = 0; i < R2; ++i) {
+            const float ck = crow[i] * k_scale;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+            for (int e = 0; e < 2; ++e) x[h][i][e] = fmaf(s[h][i >> 1][2 * e + (i & 1)], ck, ev);
+          }
+        }
+        if (edge) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (key0 + 4 * t + i >= lim[h]) x[h][i] = -INFINITY;
-        if (key0 + kStep > q.len) {            // places behind the request's tokens hold anything
+          for (int h = 0; h < kPieces; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (key0 + 4 * t + i >= q.len) {
+            for (int i = 0; i < R2; ++i)
 #pragma unroll
-              for (int w = 0; w < D / 32; ++w) vc[i][w] = 0;
+              for (int e = 0; e < 2; ++e)
+                if (key0 + 16 * h + key_of_row<D>(g + 8 * e) >= lim[i]) x[h][i][e] = -INFINITY;
+        }
+        float top[R2];
+        bool grows = false;
+#pragma unroll
+        for (int i = 0; i < R2; ++i) {
+          top[i] = fmaxf(x[0][i][0], x[0][i][1]);
+          if (kPieces == 2) top[i] = fmaxf(top[i], fmaxf(x[kPieces - 1][i][0], x[kPieces - 1][i][1]));
+          grows |= top[i] > m[i] + kLazy;
+        }
+        if (__any_sync(0xffffffffu, grows)) {
+          float keep[R2];
+#pragma unroll
+          for (int i = 0; i < R2; ++i) {
+            float all = top[i];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+            const bool grow = all > m[i] + kLazy;
+            keep[i] = grow ? exp2_approx(m[i] - all) : 1.f;
+            if (grow) m[i] = all;
+            sum[i] *= keep[i];
+          }
+#pragma unroll
+          for (int c = 0; c < KS; ++c)
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[c][n][i] *= keep[2 * n + (i & 1)];
+        }
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) {
+          const float inv_v = scale_value(2 * kScaleBias - (scales[h] >> 8));
+          uint32_t pf[NR][2];
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            float w[2][2];                     // [key][row]
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float base = kUp - (m[2 * n + i] == -INFINITY ? 0.f : m[2 * n + i]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) w[e][i] = exp2_approx(x[h][2 * n + i][e] + base);
+              sum[2 * n + i] = fmaf(w[0][i] + w[1][i], inv_v, sum[2 * n + i]);
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) pf[n][e] = transposed(pack2<true>(w[e][0], w[e][1]));
+          }
+          uint32_t v[4][D / 32];               // keys of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9; bytes (D / 8) g ..
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = key_of_row<D>(2 * t + 8 * (i >> 1) + (i & 1));
+            const uint8_t* src = v_at + 16 * D * h + chunk_at<D>(key, D == 128 ? g : g >> 1);
+            if constexpr (D == 128) {
+              const uint4 c = *reinterpret_cast<const uint4*>(src);
+              v[i][0] = c.x, v[i][1] = c.y, v[i][2] = c.z, v[i][3] = c.w;
+            } else {
+              const uint2 c = reinterpret_cast<const uint2*>(src)[g & 1];
+              v[i][0] = c.x, v[i][1] = c.y;
+            }
+          }
+          if (edge && key0 + 16 * h + 16 > q.len) {      // places behind the request's tokens hold anything
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key0 + 16 * h + key_of_row<D>(2 * t + 8 * (i >> 1) + (i & 1)) >= q.len) {
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) v[i][w] = 0;
+              }
+          }
+          // O^T += V^T P^T: tile c has bytes 2 c and 2 c + 1 of the threads' runs of d
+#pragma unroll
+          for (int c = 0; c < KS; ++c) {
+            const uint32_t sel = c & 1 ? 0x7362u : 0x5140u;
+            const uint32_t w0 = __byte_perm(v[0][c >> 1], v[1][c >> 1], sel), w1 = __byte_perm(v[2][c >> 1], v[3][c >> 1], sel);
+            const uint32_t a[4] = {e4m3_low(w0), e4m3_high(w0), e4m3_low(w1), e4m3_high(w1)};
+#pragma unroll
+            for (int n = 0; n < NR; ++n) mma16816(acc[c][n], a, pf[n][0], pf[n][1]);
+          }
         }
-      }
-      const float top0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3]));
-      const float top1 = fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3]));
-      if (__any_sync(0xffffffffu, top0 > m[0] + kLazy || top1 > m[1] + kLazy)) {
-        float keep[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float top = h ? top1 : top0;
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const bool grow = top > m[h] + kLazy;
-          keep[h] = grow ? exp2_approx(m[h] - top) : 1.f;
-          if (grow) m[h] = top;
-          sum[h] *= keep[h];
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n][0] *= keep[0], acc[n][1] *= keep[0], acc[n][2] *= keep[1], acc[n][3] *= keep[1];
-      }
-      uint32_t pf[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float base = kUp - (m[h] == -INFINITY ? 0.f : m[h]);
-        float w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = exp2_approx(x[h][i] + base);
-        sum[h] = fmaf((w[0] + w[1]) + (w[2] + w[3]), inv_v, sum[h]);
-        pf[h] = pack2<true>(w[0], w[1]);
-        pf[2 + h] = pack2<true>(w[2], w[3]);
-      }
-      // O += P V: tile n has the thread's byte n, d = (D / 8) g + n of the fragment's column g
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7362u : 0x5140u;
-          const uint32_t a = __byte_perm(vc[0][w], vc[1][w], sel), b = __byte_perm(vc[2][w], vc[3][w], sel);
-          mma16816(acc[4 * w + 2 * half], pf, e4m3_low(a), e4m3_low(b));
-          mma16816(acc[4 * w + 2 * half + 1], pf, e4m3_high(a), e4m3_high(b));
-        }
-      }
-      if (j + 1 < steps) {
-        load_v(at_next);
-        scales = scales_next;
       }
     }
+    copy_wait<0>();
 
     // ------------------------------------------------------------------ the warps of a row tile
+    __syncthreads();                           // the ring becomes the outputs' place
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
-      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
-      if (t == 0) sm.ml[warp][g + 8 * h] = make_float2(m[h], sum[h]);
-      // columns (D / 4) t .. + D / 4 of the row: acc[n][2 h] at n, acc[n][2 h + 1] at D / 8 + n
-      float4* dst = reinterpret_cast<float4*>(&sm.o[warp][g + 8 * h][t * FewSmem<D>::kQuarter]);
+    for (int i = 0; i < R2; ++i) {
 #pragma unroll
-      for (int n = 0; n < NT; n += 4) {
-        dst[n / 4] = make_float4(acc[n][2 * h], acc[n + 1][2 * h], acc[n + 2][2 * h], acc[n + 3][2 * h]);
-        dst[(NT + n) / 4] = make_float4(acc[n][2 * h + 1], acc[n + 1][2 * h + 1], acc[n + 2][2 * h + 1], acc[n + 3][2 * h + 1]);
+      for (int o = 4; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+      const int row = 8 * (i >> 1) + 2 * t + (i & 1);
+      if (g == 0) sm.ml[warp][row] = make_float2(m[i], sum[i]);
+      float4* dst = reinterpret_cast<float4*>(&sm.o[warp][row][(D / 8) * g]);
+#pragma unroll
+      for (int c = 0; c < KS; c += 2) {
+        const float(&a)[4] = acc[c][i >> 1], (&b)[4] = acc[c + 1][i >> 1];
+        dst[c / 2] = make_float4(a[i & 1], a[2 + (i & 1)], b[i & 1], b[2 + (i & 1)]);
       }
     }
     __syncthreads();
-    const int c0 = static_cast<int>(start / place.share), c1 = static_cast<int>((start + static_cast<long long>(it.tiles - 1) * it.weight) / place.share);
+    const int c0 = static_cast<int>(walk.start / place.share);
+    const int c1 = static_cast<int>((walk.start + static_cast<long long>(it.tiles - 1) * it.weight) / place.share);
     const bool whole = c0 == c1;
     const int cta = blockIdx.x;
     const auto finish = [&](int row, int col, const float4& o, float top, float total) {
@@ -459,30 +677,30 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_e4m3(const __gri
     };
     const int units = it.rows * (D / 4);       // four columns of a row
 #pragma unroll 1
-    for (int u = threadIdx.x; u < units; u += kFewThreads) {
-      const int row = u / (D / 4), col = 4 * (u % (D / 4)), tile = row >> 4, in = row & 15;
+    for (int u = threadIdx.x; u < units; u += 32 * W) {
+      const int row = u / (D / 4), col = 4 * (u % (D / 4)), tile = row / (8 * NR), in = row % (8 * NR);
       float top = -INFINITY, total = 0.f;
-      for (int w = tile; w < kFewWarps; w += mt) top = fmaxf(top, sm.ml[w][in].x);
+      for (int w = tile; w < W; w += mt) top = fmaxf(top, sm.ml[w][in].x);
       const float ref = top == -INFINITY ? 0.f : top;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = tile; w < kFewWarps; w += mt) {
+      for (int w = tile; w < W; w += mt) {
         const float2 ml = sm.ml[w][in];
         const float f = exp2_approx(ml.x - ref);
         total = fmaf(ml.y, f, total);
-        const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][in][(col / (D / 4)) * FewSmem<D>::kQuarter + col % (D / 4)]);
+        const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][in][col]);
         o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
       }
       if (whole) {
         finish(row, col, o, top, total);
       } else {
-        const int64_t at_row = (2ll * cta + (cta == c0 ? 1 : 0)) * kFewRows + row;
+        const int64_t at_row = (2ll * cta + (cta == c0 ? 1 : 0)) * L::kRows + row;
         *reinterpret_cast<float4*>(p.po + at_row * D + col) = o;
         if (col == 0) p.ml[at_row] = make_float2(top, total);
       }
     }
+    __syncthreads();         // the outputs' places are free again
     if (!whole) {
       // the last CTA that is done with the item joins what all of them left, in line order
-      __syncthreads();
       if (threadIdx.x == 0) {
         __threadfence();
         const int done = atomicAdd(p.count + c0, 1);
@@ -493,14 +711,15 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_e4m3(const __gri
       __syncthreads();
       if (sm.last) {
 #pragma unroll 1
-        for (int u = threadIdx.x; u < units; u += kFewThreads) {
+        for (int u = threadIdx.x; u < units; u += 32 * W) {
           const int row = u / (D / 4), col = 4 * (u % (D / 4));
-          const auto slot = [&](int c) { return (2ll * c + (c == c0 ? 1 : 0)) * kFewRows + row; };
+          const auto slot = [&](int c) { return (2ll * c + (c == c0 ? 1 : 0)) * L::kRows + row; };
           float top = -INFINITY, total = 0.f;
+#pragma unroll 8
           for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.ml[slot(c)].x));
           const float ref = top == -INFINITY ? 0.f : top;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
           for (int c = c0; c <= c1; ++c) {
             const float2 ml = __ldcg(p.ml + slot(c));
             const float4 v = __ldcg(reinterpret_cast<const float4*>(p.po + slot(c) * D + col));
@@ -512,43 +731,527 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_e4m3(const __gri
         }
       }
     }
-    __syncthreads();                           // shared memory is free again
+    __syncthreads();                           // and the ring again
   }
 }
 
+// ------------------------------------------------------------------------------- many rows
+// Items of up to 256 rows on the tensor cores (tcgen05).  Two lanes of 128 rows, each with its own output and two
+// buffers of scores in tensor memory, its own warp that issues the products and its own four softmax warps, a row a
+// thread; both see every key tile.  A tile's codes come by TMA (128-byte swizzle), four warps widen them to fp16 tiles,
+// K first, and the tiles serve both lanes:
+//   S = Q K^T       both operands from shared memory; the softmax warps put Q there, in fp16
+//   W = 2^(x - m)   written over S in tensor memory, fp16
+//   O += W V        W from tensor memory, V from shared memory, d contiguous (transposed operand)
+// The products of a tile run while the softmax of the lane's tile before it, and of the other lane's, runs.
+constexpr int kRawStages = 3;          // tiles of codes, K and V
+constexpr int kWideStages = 3;         // tiles of fp16, of K and of V
+constexpr int kScaleRing = 16;         // tiles' scales: more than the copies are ahead of the softmax warps
+constexpr int kWWiden = 8, kWMma = 12, kWCopy = 14;    // first warps of a role; warps 0 .. 7: softmax; the last has none
+constexpr int kManyRegs = 168, kManyRegsOther = 88;    // of 128 a thread at launch
+constexpr int kTmemCols = 512, kColO = 256;            // two S of 64 columns a lane, then O of 128 a lane
+static_assert(8 * kManyRegs + 8 * kManyRegsOther == 128 * 16, "registers are those of the launch");
+
+template <int D>
+struct ManySmem {
+  uint8_t raw[kRawStages][2][kTile * D];       // codes of K, V
+  uint8_t wide[2][kWideStages][kTile * D * 2]; // fp16 K, V: [D / 64][64 keys][128 bytes], swizzled
+  uint8_t q[2][128 * D * 2];                   // [D / 64][128 rows][128 bytes], swizzled
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];
+  uint64_t full[2][kWideStages], empty[2][kWideStages];
+  uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
+  uint16_t scales[kScaleRing][4];
+  int last, failed;
+  uint32_t tmem_base;
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+template <bool F16, int D>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    k_attn_e4m3_many(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const __grid_constant__ Params p) {
+  using L = ManyLine;
+  using S = ManySmem<D>;
+  constexpr int CH = D / 64;
+  constexpr uint32_t kQChunk = 128 * 128, kKvChunk = kTile * 128;       // bytes of 64 elements of all rows / keys
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw + smem_align_pad(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRawStages; ++i) mbar_init(&sm.raw_full[i], 1), mbar_init(&sm.raw_empty[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      for (int s = 0; s < kWideStages; ++s) mbar_init(&sm.full[i][s], 4), mbar_init(&sm.empty[i][s], 2);
+      mbar_init(&sm.q_full[i], 4), mbar_init(&sm.q_empty[i], 1);
+      for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[i][b], 1), mbar_init(&sm.p_full[i][b], 4);
+      mbar_init(&sm.pv_done[i], 1), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.o_empty[i], 4), mbar_init(&sm.drain[i], 1);
+    }
+    sm.failed = 0;
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 32 * kWCopy) tma_prefetch_desc(&tk), tma_prefetch_desc(&tv);
+  pdl_launch_dependents();
+  pdl_wait();
+  const Place place = find_place<L>(p);        // with barriers of the CTA: those above are ready too
+  if (place.r < 0) return;
+  if (warp == kWMma) {
+    tmem_alloc(&sm.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  bool ok = true;
+
+  if (warp >= kWWiden) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyRegsOther));
+    if (warp == kWCopy) {
+      // ------------------------------------------------------------------ codes and scales
+      copy_items<L, D, kTile, kRawStages>(p, place, tk, tv, [&](uint32_t i) { return sm.raw[i % kRawStages][0]; }, sm.raw_full, sm.raw_empty,
+                                          [&](uint32_t i) { return sm.scales[i % kScaleRing]; }, &sm.failed);
+    } else if (warp < kWMma) {
+      // ------------------------------------------------------------------ codes -> fp16
+      // A thread widens 16 codes at a time.  Eight lanes have four chunks each of two keys, chosen (k and k ^ 5, or
+      // k ^ 1 where d is 64) so that what they read and what they write falls on all banks.
+      constexpr int kUnits = kTile * D / 16 / 128;      // of a thread
+      const int u0 = threadIdx.x - 32 * kWWiden;
+      Walk<L> walk(p, place);
+      uint32_t tile = 0;
+      while (ok && walk.next()) {
+        int first;
+        const int n = walk.stages<kTile>(first), len = walk.q.len;
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j, ++tile) {
+          const uint32_t rs = tile % kRawStages, ws = tile % kWideStages;
+          ok = stage_wait(&sm.raw_full[rs], (tile / kRawStages) & 1, &sm.failed, kErrWaitFull);
+          const int left = len - (first + j) * kTile;   // keys of the request in the tile
+#pragma unroll 1
+          for (int v = 0; v < 2 && ok; ++v) {
+            uint4 c[kUnits];
+            int key[kUnits], plane[kUnits];
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+              const int u = u0 + 128 * i, chunk = u & 3, sel = (u >> 2) & 1, pair = (u >> 3) & 31;
+              plane[i] = u >> 8;
+              key[i] = (2 * pair) ^ (sel * (D == 128 ? 5 : 1));
+              c[i] = *reinterpret_cast<const uint4*>(sm.raw[rs][v] + chunk_at<D>(key[i], 4 * plane[i] + chunk));
+              if (v && key[i] >= left) c[i] = make_uint4(0, 0, 0, 0);      // places behind the tokens hold anything
+            }
+            ok = stage_wait(&sm.empty[v][ws], ((tile / kWideStages) & 1) ^ 1, &sm.failed, kErrWaitEmpty);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+              uint8_t* dst = sm.wide[v][ws] + plane[i] * kKvChunk + key[i] * 128;
+              const int unit = 2 * (u0 & 3), x = key[i] & 7;
+              *reinterpret_cast<uint4*>(dst + 16 * (unit ^ x)) = make_uint4(e4m3_low(c[i].x), e4m3_high(c[i].x), e4m3_low(c[i].y), e4m3_high(c[i].y));
+              *reinterpret_cast<uint4*>(dst + 16 * ((unit + 1) ^ x)) = make_uint4(e4m3_low(c[i].z), e4m3_high(c[i].z), e4m3_low(c[i].w), e4m3_high(c[i].w));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[v][ws]);
+          }
+          if (ok && lane == 0) mbar_arrive(&sm.raw_empty[rs]);
+        }
+      }
+    } else if (warp < kWCopy) {
+      // ------------------------------------------------------------------ products of lane l
+      const int l = warp - kWMma;
+      constexpr uint32_t id_qk = (1u << 4) | ((kTile >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr uint32_t id_wv = (1u << 4) | (1u << 16) | ((D >> 3) << 17) | ((128u >> 4) << 24);
+      const uint32_t t_s = tmem + 128 * l, t_o = tmem + kColO + 128 * l;
+      const uint64_t k0 = smem_desc_sw128(smem_u32(sm.wide[0][0])), v0 = smem_desc_sw128_mn(smem_u32(sm.wide[1][0]), kKvChunk);
+      const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[l]));
+      constexpr uint32_t kWideBytes = kTile * D * 2;
+      uint32_t k_tile = 0, v_tile = 0, items = 0;       // tiles and items of this lane's own alike for all
+      uint32_t s_cnt = 0, p_cnt = 0;            // tiles of this lane whose S was issued / whose W was taken
+      Walk<L> walk(p, place);
+      while (ok && walk.next()) {
+        int first;
+        const int n = walk.stages<kTile>(first);
+        // Every place of the rings is waited for and given back by both lanes, also where one has no rows: a wait
+        // by parity is only sound if no phase is left out.
+        const bool mine = l == 0 || walk.it.rows > 128;
+        if (mine && n > 0) ok = stage_wait(&sm.q_full[l], items & 1, &sm.failed, kErrWaitFull);
+        const auto qk = [&](int) {
+          const uint32_t sl = k_tile % kWideStages;
+          ok = stage_wait(&sm.full[0][sl], (k_tile / kWideStages) & 1, &sm.failed, kErrWaitFull);
+          if (!ok) return;
+          ++k_tile;
+          if (!mine) {
+            if (lane == 0) mbar_arrive(&sm.empty[0][sl]);
+            __syncwarp();
+            return;
+          }
+          const uint64_t kd = k0 + sl * (kWideBytes >> 4);
+          const uint32_t b = s_cnt & 1, t = t_s + 64 * b;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4 * CH; ++k)
+              tc_mma_ss_f16(t, qd + (((k >> 2) * kQChunk + 32 * (k & 3)) >> 4), kd + (((k >> 2) * kKvChunk + 32 * (k & 3)) >> 4),
+                            id_qk, k ? 1u : 0u);
+            tc_commit(&sm.s_full[l][b]);
+            tc_commit(&sm.empty[0][sl]);
+          }
+          __syncwarp();
+          ++s_cnt;
+        };
+        const auto wv = [&](int j) {
+          const uint32_t sl = v_tile % kWideStages;
+          ok = stage_wait(&sm.full[1][sl], (v_tile / kWideStages) & 1, &sm.failed, kErrWaitFull);
+          if (!ok) return;
+          ++v_tile;
+          if (!mine) {
+            if (lane == 0) mbar_arrive(&sm.empty[1][sl]);
+            __syncwarp();
+            return;
+          }
+          // first: the lane's previous item has left the output columns
+          if (j == 0) ok = stage_wait(&sm.o_empty[l], (items & 1) ^ 1, &sm.failed, kErrWaitAccum);
+          const uint32_t b = p_cnt & 1, t = t_s + 64 * b;
+          ok = ok && stage_wait(&sm.p_full[l][b], (p_cnt >> 1) & 1, &sm.failed, kErrWaitFull);
+          if (!ok) return;
+          const uint64_t vd = v0 + sl * (kWideBytes >> 4);
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k) tc_mma_ts(t_o, t + 8 * k, vd + ((k * 2048) >> 4), id_wv, (j == 0 && k == 0) ? 0u : 1u);
+            tc_commit(&sm.pv_done[l]);
+            if (j + 1 == n) tc_commit(&sm.o_full[l]);
+            tc_commit(&sm.empty[1][sl]);
+          }
+          __syncwarp();
+          ++p_cnt;
+        };
+#pragma unroll 1
+        for (int j = 0; j < n + 2 && ok; ++j) {
+          if (j >= 2) wv(j - 2);
+          if (ok && j < n) qk(j);
+        }
+        if (!ok) break;
+        if (mine && n > 0) {
+          if (elect_one()) tc_commit(&sm.q_empty[l]);
+          __syncwarp();
+          ++items;
+        }
+      }
+      // every product and commit of this warp (elect.sync names the same lane each time) has completed before tensor memory and barriers go
+      if (elect_one()) tc_commit(&sm.drain[l]);
+      mbar_wait_short(&sm.drain[l], 0, &g_attn8_err, kErrDrain);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    // -------------------------------------------------------------------- softmax, one row a thread
+    const int l = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_o = tmem + lane_base + kColO + 128 * l;
+    const int log_box = 31 - __clz(min(p.a.page_size, kTile));
+    uint32_t cnt = 0, items = 0, tile = 0;      // tiles and items of this lane; tiles of all items
+    Walk<L> walk(p, place);
+    while (walk.next()) {
+      int first;
+      const int n = ok ? walk.stages<kTile>(first) : 0;
+      const int row_item = 128 * l + row, rows = walk.it.rows, row_all = walk.tile * kManyRows + row_item;
+      const bool mine = l == 0 || rows > 128, valid = row_item < rows, active = __any_sync(0xffffffffu, valid);
+      const int tok = row_all / p.G, head = walk.head * p.G + row_all - tok * p.G;
+      const int lim = valid ? keys_seen(walk.q, tok) : 0;
+      float m = -INFINITY, sum = 0.f;           // m: the largest x, in units of log2
+      float c = p.c;
+      if (mine && n > 0) {
+        // Q -> fp16, behind a power of two of the row where it is bf16
+        uint4 x[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(p.a.Q + (walk.q.first + tok) * p.a.q_stride + static_cast<int64_t>(head) * D);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        if (!F16) {
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu), __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+          const int k = bf16_to_f16_exponent(max(mx & 0xffffu, mx >> 16));
+          const float down = pow2_normal(-k);
+          c *= pow2_normal(k);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float2 f = unpack2<false>((&x[i].x)[w]);
+              (&x[i].x)[w] = pack2<true>(f.x * down, f.y * down);
+            }
+        }
+        ok = stage_wait(&sm.q_empty[l], (items & 1) ^ 1, &sm.failed, kErrWaitEmpty);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<uint4*>(sm.q[l] + (i >> 3) * kQChunk + row * 128 + 16 * ((i & 7) ^ (row & 7))) = x[i];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full[l]);
+      }
+#pragma unroll 1
+      for (int j = 0; j < n && ok && mine; ++j, ++cnt) {
+        const int key0 = (first + j) * kTile;
+        const uint32_t b = cnt & 1, t_s = tmem + lane_base + 128 * l + 64 * b, at = tile + j;
+        ok = stage_wait(&sm.s_full[l][b], (cnt >> 1) & 1, &sm.failed, kErrWaitAccum);
+        // the tile's V is there, and with it the scales; its place is not filled again before this tile's product
+        ok = ok && stage_wait(&sm.full[1][at % kWideStages], (at / kWideStages) & 1, &sm.failed, kErrWaitFull);
+        if (!ok) break;
+        tc_fence_after();
+        if (active) {
+          uint32_t v[2][32];
+          tmem_ld32(t_s, v[0]);
+          tmem_ld32(t_s + 32, v[1]);
+          float ck[4], ev[4], inv[4];           // of each 16 keys
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t sc = sm.scales[at % kScaleRing][(16 * q) >> log_box];
+            ck[q] = c * scale_value(sc & 0xffu), ev[q] = static_cast<float>(static_cast<int>(sc >> 8) - kScaleBias);
+            inv[q] = scale_value(2 * kScaleBias - (sc >> 8));
+          }
+          tc_wait_ld();
+          if (__builtin_expect(__any_sync(0xffffffffu, valid && key0 + kTile > lim), 0)) {
+            const int left = lim - key0;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * q + e >= left) v[q][e] = 0xff800000u;
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* w = &v[q >> 1][16 * (q & 1)];
+            float mq = fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) mq = max3(mq, __uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+            top = fmaxf(top, fmaf(mq, ck[q], ev[q]));
+          }
+          const bool grow = valid && top > m + kLazy;
+          if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+            const float keep = grow ? exp2_approx(m - top) : 1.f;
+            if (grow) m = top;
+            sum *= keep;
+            if (j > 0) {
+              // the lane's last product has left the output (one phase at most is outstanding: this tile's S was
+              // issued after the product before that one)
+              ok = stage_wait(&sm.pv_done[l], (cnt - 1) & 1, &sm.failed, kErrWaitAccum);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t keep2 = pair_f(keep, keep);
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tmem_ld32(t_o + 32 * q, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  const float2 f = unpair(mul_pair(pair(o[e], o[e + 1]), keep2));
+                  o[e] = __float_as_uint(f.x), o[e + 1] = __float_as_uint(f.y);
+                }
+                tmem_st32(t_o + 32 * q, o);
+              }
+            }
+          }
+          const float base = kUp - (m == -INFINITY ? 0.f : m);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint64_t c2 = pair_f(ck[q], ck[q]), b2 = pair_f(base + ev[q], base + ev[q]);
+            uint64_t part = 0;
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t* s = &v[q >> 1][16 * (q & 1) + 2 * e];
+              const float2 x = unpair(fma_pair(pair(s[0], s[1]), c2, b2));
+              const float a = exp2_approx(x.x), d = exp2_approx(x.y);
+              part = add_pair(part, pair_f(a, d));
+              w[e] = pack2<true>(a, d);
+            }
+            tmem_st8(t_s + 8 * q, w);
+            const float2 s2 = unpair(part);
+            sum = fmaf(s2.x + s2.y, inv[q], sum);
+          }
+          tc_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[l][b]);
+      }
+      tile += n;
+      // ------------------------------------------------------------------ the segment's output
+      uint32_t o[D / 32][32];
+      if (mine && n > 0 && ok) {
+        ok = stage_wait(&sm.o_full[l], items & 1, &sm.failed, kErrWaitAccum);
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) tmem_ld32(t_o + 32 * q, o[q]);
+        tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_empty[l]);
+        ++items;
+      } else {
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[q][e] = 0;
+      }
+      const int c0 = static_cast<int>(walk.start / place.share);
+      const int c1 = static_cast<int>((walk.start + static_cast<long long>(walk.it.tiles - 1) * walk.it.weight) / place.share);
+      const int cta = blockIdx.x;
+      const auto finish = [&](float top, float total) {
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const int64_t at_row = static_cast<int64_t>(walk.q.first + tok) * p.a.Hq + head;
+        uint4* dst = reinterpret_cast<uint4*>(p.a.O + at_row * D);
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = pack2<F16>(__uint_as_float(o[e >> 2][8 * (e & 3) + 2 * i]) * inv, __uint_as_float(o[e >> 2][8 * (e & 3) + 2 * i + 1]) * inv);
+          dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (p.a.lse)
+          p.a.lse[at_row] = total == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - kUp + log2f(total)) * 0.6931471805599453f;
+      };
+      if (c0 == c1) {
+        if (valid) finish(m, sum);
+        continue;
+      }
+      // partials [cta][2][d / 4][256 rows][4]: a warp writes and reads whole lines
+      const auto slot = [&](int at) { return 2ll * at + (at == c0 ? 1 : 0); };
+      if (valid) {
+        float4* po = reinterpret_cast<float4*>(p.po) + slot(cta) * (D / 4) * kManyRows + row_item;
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e)
+          po[e * kManyRows] = make_float4(__uint_as_float(o[e >> 3][4 * (e & 7)]), __uint_as_float(o[e >> 3][4 * (e & 7) + 1]),
+                                          __uint_as_float(o[e >> 3][4 * (e & 7) + 2]), __uint_as_float(o[e >> 3][4 * (e & 7) + 3]));
+        p.ml[slot(cta) * kManyRows + row_item] = make_float2(m, sum);
+      }
+      named_bar_sync(1, 256);
+      if (threadIdx.x == 0) {
+        __threadfence();
+        const int done = atomicAdd(p.count + c0, 1);
+        sm.last = done == c1 - c0;
+        if (sm.last) p.count[c0] = 0;
+        __threadfence();
+      }
+      named_bar_sync(1, 256);
+      if (sm.last && valid) {
+        float top = -INFINITY, total = 0.f;
+#pragma unroll 4
+        for (int at = c0; at <= c1; ++at) top = fmaxf(top, __ldcg(&p.ml[slot(at) * kManyRows + row_item].x));
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[q][e] = 0;
+#pragma unroll 1
+        for (int at = c0; at <= c1; ++at) {
+          const float2 ml = __ldcg(p.ml + slot(at) * kManyRows + row_item);
+          const float f = exp2_approx(ml.x - ref);
+          total = fmaf(ml.y, f, total);
+          const float4* po = reinterpret_cast<const float4*>(p.po) + slot(at) * (D / 4) * kManyRows + row_item;
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) {
+            const float4 v = __ldcg(po + e * kManyRows);
+            uint32_t* a = &o[e >> 3][4 * (e & 7)];
+            a[0] = __float_as_uint(fmaf(v.x, f, __uint_as_float(a[0]))), a[1] = __float_as_uint(fmaf(v.y, f, __uint_as_float(a[1])));
+            a[2] = __float_as_uint(fmaf(v.z, f, __uint_as_float(a[2]))), a[3] = __float_as_uint(fmaf(v.w, f, __uint_as_float(a[3])));
+          }
+        }
+        finish(top, total);
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == kWMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+constexpr int kFewMostRows = 64;       // of an item, either NR
 struct Layout {
-  int ctas;
+  int sms;
   size_t po, ml, bytes;
 };
 
 Layout layout(int64_t d) {
   Layout l{};
-  l.ctas = kFewCtas * device_sm_count();
+  l.sms = device_sm_count();
   size_t off = kWsHeaderBytes;
   const auto take = [&](size_t bytes) {
     const size_t at = off;
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t rows = static_cast<size_t>(l.ctas) * 2 * kFewRows;
-  l.po = take(rows * d * sizeof(float));
-  l.ml = take(rows * sizeof(float2));
+  // two segments of each CTA: up to four an SM with items of up to 64 rows, one with 256
+  const size_t slots = static_cast<size_t>(l.sms) * 2 * 4 * kFewMostRows;
+  static_assert(4 * kFewMostRows == kManyRows, "both kernels' segments");
+  l.po = take(slots * d * sizeof(float));
+  l.ml = take(slots * sizeof(float2));
   l.bytes = off;
   return l;
 }
 
+// The cache as rows of 128 bytes: a box is a page's run of up to `keys` keys.
+cudaError_t cache_map(CUtensorMap* map, const uint8_t* cache, const AttnE4m3Args& a, int keys) {
+  const uint64_t rows = static_cast<uint64_t>(a.page_size) * a.d / 128;
+  const uint64_t dims[4] = {128, rows, 1, static_cast<uint64_t>(a.pages) * a.Hkv};
+  const uint64_t strides[3] = {128, rows * 128, rows * 128};
+  const uint32_t box[4] = {128, static_cast<uint32_t>(std::min(a.page_size, keys) * a.d / 128), 1, 1};
+  return make_tmap_4d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+template <bool F16, int D, int NR, int W>
+cudaError_t launch_few(const Params& p, const Layout& l, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(FewSmem<D, NR, W>);
+  constexpr int ctas = few_warps(NR) / W;
+  static_assert(ctas * (smem + 1024 + 256) <= 227 * 1024, "CTAs of the kernel for few rows do not fit an SM");
+  const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(k_attn_e4m3<F16, D, NR, W>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_attn_e4m3<F16, D, NR, W>, dim3(l.sms * ctas), 32 * W, smem, stream, p);
+}
+
+template <bool F16, int D>
+cudaError_t launch_many(const Params& p, const Layout& l, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(ManySmem<D>) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of the kernel for many rows over the per-CTA limit");
+  CUtensorMap tk, tv;
+  cudaError_t e = cache_map(&tk, p.a.k_cache, p.a, kTile);
+  if (e == cudaSuccess) e = cache_map(&tv, p.a.v_cache, p.a, kTile);
+  if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(k_attn_e4m3_many<F16, D>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_attn_e4m3_many<F16, D>, dim3(l.sms), kManyThreads, smem, stream, tk, tv, p);
+}
+
 template <bool F16, int D>
 cudaError_t launch_t(const AttnE4m3Args& a, uint8_t* ws, cudaStream_t stream) {
-  const Layout l = layout(D);
   Params p{};
   p.a = a;
   p.G = a.Hq / a.Hkv;
+  const int64_t rows = static_cast<int64_t>(a.max_new) * p.G;
+  const Layout l = layout(D);
   p.log_page = 4;
   while ((1 << p.log_page) < a.page_size) ++p.log_page;
   p.c = a.scale * 1.4426950408889634f;
   p.count = reinterpret_cast<int*>(ws);        // the header's counters: zero, and left so
   p.po = reinterpret_cast<float*>(ws + l.po), p.ml = reinterpret_cast<float2*>(ws + l.ml);
-  return launch_pdl(k_attn_e4m3<F16, D>, dim3(l.ctas), kFewThreads, 0, stream, p);
+  // A request of more rows than a CTA's warps have is the tensor cores'; others in the same call stay with the first kernel.
+  p.few = kFewMostRows;
+  if (rows > kFewMostRows) {
+    const cudaError_t e = launch_many<F16, D>(p, l, stream);
+    if (e != cudaSuccess) return e;
+  }
+  // Few items: one CTA an SM, so that an item has fewer segments.
+  const bool few_items = static_cast<int64_t>(a.R) * a.Hkv <= l.sms;
+  if (rows <= 8) return few_items ? launch_few<F16, D, 1, 16>(p, l, stream) : launch_few<F16, D, 1, 4>(p, l, stream);
+  return few_items ? launch_few<F16, D, 2, 12>(p, l, stream) : launch_few<F16, D, 2, 4>(p, l, stream);
 }
 
 }  // namespace
