@@ -46,9 +46,29 @@ constexpr int kTile = 64;              // keys a tile of the line
 constexpr float kLazy = 8.f;           // the running maximum follows when it grew by more than 2^8 ...
 constexpr float kUp = 7.f;             // ... and weights stand 2^7 higher, up to 2^15: fp16 reaches 2^-31 of the largest
 
+// n / d for 0 <= n < 2^31 by a multiplication: q = (hi(n mul) + n) >> shift with mul = 2^32 (2^shift - d) / d + 1.
+struct Divisor {
+  uint32_t mul, shift;
+  explicit Divisor(uint32_t d = 1) : shift(0) {
+    while ((1u << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((static_cast<uint64_t>((1u << shift) - d) << 32) / d + 1);
+    if (d == 1) mul = 0;
+  }
+  __device__ int of(int n) const { return static_cast<int>((__umulhi(n, mul) + static_cast<uint32_t>(n)) >> shift); }
+};
+
+// a / b of positions on a line, exact where it is below 2^20 (a 64-bit division takes some hundred instructions).
+__device__ __forceinline__ int quotient(long long a, long long b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  if (q * b > a) --q;
+  else if ((q + 1) * b <= a) ++q;
+  return q;
+}
+
 struct Params {
   AttnE4m3Args a;
   int G, log_page;
+  Divisor by_G;
   int few;                   // requests of up to so many rows are the first kernel's
   float c;                   // scale * log2(e)
   int* count;                // segments of the item that begins in a CTA which are done [ctas]
@@ -105,7 +125,7 @@ template <class L>
 __device__ __forceinline__ Shape shape(const Params& p, const Request& q, int rt) {
   Shape s;
   s.rows = min(L::kRows, q.n * p.G - rt * L::kRows);
-  s.tiles = max(1, (keys_seen(q, (rt * L::kRows + s.rows - 1) / p.G) + kTile - 1) / kTile);
+  s.tiles = max(1, (keys_seen(q, p.by_G.of(rt * L::kRows + s.rows - 1)) + kTile - 1) / kTile);
   s.weight = L::weight(s.rows);
   return s;
 }
@@ -182,11 +202,37 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   __shared__ long long found_at;
   __shared__ int found_r;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long mine = 0, first_cost = 0;
-  for (int r = threadIdx.x; r < p.a.R; r += L::kThreads) {
+  // some more than an equal share, so that the shares cover the line
+  const auto take = [&](Place& s, long long total) {
+    s.share = max(static_cast<long long>(L::kMost),
+                  static_cast<long long>(__fdividef(static_cast<float>(total), static_cast<float>(gridDim.x)) * 1.000001f) + 1);
+    s.b0 = blockIdx.x * s.share;
+  };
+  const auto cost_of = [&](int r) {
     const Request q = request(p.a, r);
     if (q.bad && blockIdx.x == 0) atomicOr(&g_attn8_err, kErrIndex);
-    const long long c = p.a.Hkv * head_cost<L>(p, q);
+    return p.a.Hkv * head_cost<L>(p, q);
+  };
+  const auto scan = [&](long long c) {         // inclusive over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += v;
+    }
+    return c;
+  };
+  Place s;
+  if (p.a.R <= 32) {                           // every warp by itself
+    const long long c = lane < p.a.R ? cost_of(lane) : 0, in = scan(c);
+    take(s, __shfl_sync(0xffffffffu, in, 31));
+    const uint32_t here = __ballot_sync(0xffffffffu, in - c <= s.b0 && s.b0 < in);
+    s.r = here ? __ffs(here) - 1 : -1;
+    s.at = __shfl_sync(0xffffffffu, in - c, max(s.r, 0));
+    return s;
+  }
+  long long mine = 0, first_cost = 0;
+  for (int r = threadIdx.x; r < p.a.R; r += L::kThreads) {
+    const long long c = cost_of(r);
     if (r < L::kThreads) first_cost = c;
     mine += c;
   }
@@ -198,19 +244,11 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   long long total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += sums[w];
-  Place s;
-  s.share = max(static_cast<long long>(L::kMost), (total + gridDim.x - 1) / gridDim.x);
-  s.b0 = blockIdx.x * s.share;
+  take(s, total);
   long long before = 0;
   for (int base = 0; base < p.a.R && before <= s.b0 && s.b0 < total; base += L::kThreads) {
     const int r = base + threadIdx.x;
-    const long long c = base == 0 ? first_cost : r < p.a.R ? p.a.Hkv * head_cost<L>(p, request(p.a, r)) : 0;
-    long long in = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, in, o);
-      if (lane >= o) in += v;
-    }
+    const long long c = base == 0 ? first_cost : r < p.a.R ? p.a.Hkv * head_cost<L>(p, request(p.a, r)) : 0, in = scan(c);
     __syncthreads();
     if (lane == 31) sums[warp] = in;
     __syncthreads();
@@ -225,6 +263,16 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   __syncthreads();
   s.r = found_r, s.at = found_at;
   return s;
+}
+
+// Counts this CTA's segment of an item that CTAs c0 .. c1 share; true in the one that is last, which sees what the
+// others have written.  After a barrier of the CTA's writers, by one thread.
+__device__ __forceinline__ bool last_segment(int* count, int segments) {
+  int done;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(done) : "l"(count) : "memory");
+  if (done + 1 < segments) return false;
+  *count = 0;
+  return true;
 }
 
 // First tile of an item (line start s, tiles n of weight w) that starts at or after position b.
@@ -248,7 +296,7 @@ struct Walk {
   __device__ Walk(const Params& p_, const Place& s) : p(p_), b0(s.b0), b1(s.b0 + s.share), line(s.at), r(s.r), kvh(0), rt(0) {
     q = request(p.a, r);
     const long long cost = head_cost<L>(p, q);       // heads before the share
-    kvh = static_cast<int>((b0 - line) / cost);
+    kvh = quotient(b0 - line, cost);
     line += kvh * cost;
   }
   __device__ bool next() {
@@ -271,10 +319,15 @@ struct Walk {
     }
     return false;
   }
+  // The CTAs that have the item's first and last tile.
+  __device__ void ctas(int& c0, int& c1) const {
+    const long long share = b1 - b0;
+    c0 = quotient(start, share), c1 = quotient(start + static_cast<long long>(it.tiles - 1) * it.weight, share);
+  }
   // Stages of KEYS keys of this share of the item, up to the last key that its last row sees.
   template <int KEYS>
   __device__ int stages(int& first) const {
-    const int seen = keys_seen(q, (tile * L::kRows + it.rows - 1) / p.G);
+    const int seen = keys_seen(q, p.by_G.of(tile * L::kRows + it.rows - 1));
     first = lo * (kTile / KEYS);
     return max(0, min(hi * (kTile / KEYS), (seen + KEYS - 1) / KEYS) - first);
   }
@@ -397,8 +450,16 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
     const int row_base = (warp & (mt - 1)) * 8 * NR, phase = warp / mt;
     // the most keys that a row of the warp sees, and the fewest
     const int last_row = min(it.rows, row_base + 8 * NR) - 1;
-    const int lim_top = last_row < row_base ? 0 : keys_seen(q, (row0 + last_row) / p.G);
-    const int lim_low = keys_seen(q, (row0 + row_base) / p.G);
+    const int lim_top = last_row < row_base ? 0 : keys_seen(q, p.by_G.of(row0 + last_row));
+    const int lim_low = keys_seen(q, p.by_G.of(row0 + row_base));
+    uint4 raw[NR][D / 32];                     // elements (D / 4) t .. of rows g and g + 8
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int row = row_base + 8 * n + g, tok = p.by_G.of(row0 + row), head = kvh * p.G + (row0 + row) - tok * p.G;
+      const uint16_t* src = p.a.Q + (q.first + tok) * p.a.q_stride + head * D + (D / 4) * t;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) raw[n][i] = row < it.rows ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+    }
     int first;
     const int n_steps = walk.template stages<kKeys>(first);
     const int s0 = first + phase, s1 = min(first + n_steps, (lim_top + kKeys - 1) / kKeys);
@@ -452,14 +513,7 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
     int lim[R2];                               // keys that the row sees
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const int row = row_base + 8 * n + g;
-      const bool valid = row < it.rows;
-      const int tok = (row0 + row) / p.G, head = kvh * p.G + (row0 + row) - tok * p.G;
-      uint4 x[D / 32];
-      const uint16_t* src = p.a.Q + (q.first + tok) * p.a.q_stride + head * D;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i)         // elements (D / 4) t .. of the row
-        x[i] = valid ? __ldg(reinterpret_cast<const uint4*>(src + (D / 4) * t) + i) : make_uint4(0, 0, 0, 0);
+      uint4(&x)[D / 32] = raw[n];
       float c = p.c;
       if (!F16) {
         uint32_t mx = 0;
@@ -489,7 +543,7 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
       for (int i = 0; i < 2; ++i) {
         crow[2 * n + i] = F16 ? p.c : __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
         const int mine = row_base + 8 * n + 2 * t + i;
-        lim[2 * n + i] = mine < it.rows ? keys_seen(q, (row0 + mine) / p.G) : 0;
+        lim[2 * n + i] = mine < it.rows ? keys_seen(q, p.by_G.of(row0 + mine)) : 0;
       }
     }
 
@@ -662,13 +716,13 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
       }
     }
     __syncthreads();
-    const int c0 = static_cast<int>(walk.start / place.share);
-    const int c1 = static_cast<int>((walk.start + static_cast<long long>(it.tiles - 1) * it.weight) / place.share);
-    const bool whole = c0 == c1;
+    const bool whole = walk.lo == 0 && walk.hi == it.tiles;
     const int cta = blockIdx.x;
+    int c0, c1;
+    walk.ctas(c0, c1);
     const auto finish = [&](int row, int col, const float4& o, float top, float total) {
       const float inv = total == 0.f ? 0.f : 1.f / total;
-      const int tok = (row0 + row) / p.G, head = kvh * p.G + (row0 + row) - tok * p.G;
+      const int tok = p.by_G.of(row0 + row), head = kvh * p.G + (row0 + row) - tok * p.G;
       const int64_t at_row = static_cast<int64_t>(q.first + tok) * p.a.Hq + head;
       *reinterpret_cast<uint2*>(p.a.O + at_row * D + col) =
           make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
@@ -680,9 +734,11 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
     for (int u = threadIdx.x; u < units; u += 32 * W) {
       const int row = u / (D / 4), col = 4 * (u % (D / 4)), tile = row / (8 * NR), in = row % (8 * NR);
       float top = -INFINITY, total = 0.f;
+#pragma unroll 4
       for (int w = tile; w < W; w += mt) top = fmaxf(top, sm.ml[w][in].x);
       const float ref = top == -INFINITY ? 0.f : top;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
       for (int w = tile; w < W; w += mt) {
         const float2 ml = sm.ml[w][in];
         const float f = exp2_approx(ml.x - ref);
@@ -701,33 +757,50 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
     __syncthreads();         // the outputs' places are free again
     if (!whole) {
       // the last CTA that is done with the item joins what all of them left, in line order
-      if (threadIdx.x == 0) {
-        __threadfence();
-        const int done = atomicAdd(p.count + c0, 1);
-        sm.last = done == c1 - c0;
-        if (sm.last) p.count[c0] = 0;
-        __threadfence();
-      }
+      if (threadIdx.x == 0) sm.last = last_segment(p.count + c0, c1 - c0 + 1);
       __syncthreads();
       if (sm.last) {
+        // P neighbouring threads take a unit's segments in turn, eight at a time, so that few loads wait for others
+        const int parts = units * 8 <= 32 * W ? 8 : units * 4 <= 32 * W ? 4 : units * 2 <= 32 * W ? 2 : 1, part = threadIdx.x & (parts - 1);
 #pragma unroll 1
-        for (int u = threadIdx.x; u < units; u += 32 * W) {
-          const int row = u / (D / 4), col = 4 * (u % (D / 4));
+        for (int u0 = 0; u0 < units * parts; u0 += 32 * W) {
+          const int u = min((u0 + static_cast<int>(threadIdx.x)) / parts, units - 1), row = u / (D / 4), col = 4 * (u % (D / 4));
           const auto slot = [&](int c) { return (2ll * c + (c == c0 ? 1 : 0)) * L::kRows + row; };
           float top = -INFINITY, total = 0.f;
-#pragma unroll 8
-          for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(&p.ml[slot(c)].x));
-          const float ref = top == -INFINITY ? 0.f : top;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int c = c0; c <= c1; ++c) {
-            const float2 ml = __ldcg(p.ml + slot(c));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.po + slot(c) * D + col));
-            const float f = exp2_approx(ml.x - ref);
-            total = fmaf(ml.y, f, total);
-            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+#pragma unroll 1
+          for (int base = c0 + part; base <= c1; base += 8 * parts) {
+            float2 ml[8];
+            float4 v[8];
+            float now = top;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = min(base + i * parts, c1);
+              ml[i] = __ldcg(p.ml + slot(c));
+              v[i] = __ldcg(reinterpret_cast<const float4*>(p.po + slot(c) * D + col));
+              if (base + i * parts > c1) ml[i] = make_float2(-INFINITY, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              now = fmaxf(now, ml[i].x);
+            }
+            const float ref = now == -INFINITY ? 0.f : now, keep = exp2_approx(top - ref);
+            total *= keep, o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+            top = now;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float f = exp2_approx(ml[i].x - ref);
+              total = fmaf(ml[i].y, f, total);
+              o.x = fmaf(v[i].x, f, o.x), o.y = fmaf(v[i].y, f, o.y), o.z = fmaf(v[i].z, f, o.z), o.w = fmaf(v[i].w, f, o.w);
+            }
           }
-          finish(row, col, o, top, total);
+          for (int d = 1; d < parts; d <<= 1) {
+            const float other = __shfl_xor_sync(0xffffffffu, top, d), now = fmaxf(top, other), ref = now == -INFINITY ? 0.f : now;
+            const float f = exp2_approx(top - ref);
+            top = now;
+            total *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+            total += __shfl_xor_sync(0xffffffffu, total, d);
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, d), o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, d), o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+          }
+          if (part == 0 && u0 + static_cast<int>(threadIdx.x) < units * parts) finish(row, col, o, top, total);
         }
       }
     }
@@ -795,7 +868,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   if (threadIdx.x == 32 * kWCopy) tma_prefetch_desc(&tk), tma_prefetch_desc(&tv);
   pdl_launch_dependents();
   pdl_wait();
-  const Place place = find_place<L>(p);        // with barriers of the CTA: those above are ready too
+  const Place place = find_place<L>(p);
   if (place.r < 0) return;
   if (warp == kWMma) {
     tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -957,7 +1030,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int n = ok ? walk.stages<kTile>(first) : 0;
       const int row_item = 128 * l + row, rows = walk.it.rows, row_all = walk.tile * kManyRows + row_item;
       const bool mine = l == 0 || rows > 128, valid = row_item < rows, active = __any_sync(0xffffffffu, valid);
-      const int tok = row_all / p.G, head = walk.head * p.G + row_all - tok * p.G;
+      const int tok = p.by_G.of(row_all), head = walk.head * p.G + row_all - tok * p.G;
       const int lim = valid ? keys_seen(walk.q, tok) : 0;
       float m = -INFINITY, sum = 0.f;           // m: the largest x, in units of log2
       float c = p.c;
@@ -1098,8 +1171,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[q][e] = 0;
       }
-      const int c0 = static_cast<int>(walk.start / place.share);
-      const int c1 = static_cast<int>((walk.start + static_cast<long long>(walk.it.tiles - 1) * walk.it.weight) / place.share);
       const int cta = blockIdx.x;
       const auto finish = [&](float top, float total) {
         const float inv = total == 0.f ? 0.f : 1.f / total;
@@ -1116,10 +1187,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (p.a.lse)
           p.a.lse[at_row] = total == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - kUp + log2f(total)) * 0.6931471805599453f;
       };
-      if (c0 == c1) {
+      if (walk.lo == 0 && walk.hi == walk.it.tiles) {
         if (valid) finish(m, sum);
         continue;
       }
+      int c0, c1;
+      walk.ctas(c0, c1);
       // partials [cta][2][d / 4][256 rows][4]: a warp writes and reads whole lines
       const auto slot = [&](int at) { return 2ll * at + (at == c0 ? 1 : 0); };
       if (valid) {
@@ -1131,13 +1204,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         p.ml[slot(cta) * kManyRows + row_item] = make_float2(m, sum);
       }
       named_bar_sync(1, 256);
-      if (threadIdx.x == 0) {
-        __threadfence();
-        const int done = atomicAdd(p.count + c0, 1);
-        sm.last = done == c1 - c0;
-        if (sm.last) p.count[c0] = 0;
-        __threadfence();
-      }
+      if (threadIdx.x == 0) sm.last = last_segment(p.count + c0, c1 - c0 + 1);
       named_bar_sync(1, 256);
       if (sm.last && valid) {
         float top = -INFINITY, total = 0.f;
@@ -1235,6 +1302,7 @@ cudaError_t launch_t(const AttnE4m3Args& a, uint8_t* ws, cudaStream_t stream) {
   Params p{};
   p.a = a;
   p.G = a.Hq / a.Hkv;
+  p.by_G = Divisor(p.G);
   const int64_t rows = static_cast<int64_t>(a.max_new) * p.G;
   const Layout l = layout(D);
   p.log_page = 4;
