@@ -49,7 +49,7 @@ constexpr float kUp = 7.f;             // ... and weights stand 2^7 higher, up t
 // n / d for 0 <= n < 2^31 by a multiplication: q = (hi(n mul) + n) >> shift with mul = 2^32 (2^shift - d) / d + 1.
 struct Divisor {
   uint32_t mul, shift;
-  explicit Divisor(uint32_t d = 1) : shift(0) {
+  Divisor(uint32_t d = 1) : shift(0) {
     while ((1u << shift) < d) ++shift;
     mul = static_cast<uint32_t>((static_cast<uint64_t>((1u << shift) - d) << 32) / d + 1);
     if (d == 1) mul = 0;
@@ -108,7 +108,7 @@ struct FewLine {
 constexpr int kManyThreads = 512, kManyRows = 256;
 struct ManyLine {
   __device__ static bool takes(const Params& p, int rows) { return rows > p.few; }
-  static constexpr int kThreads = kManyThreads, kRows = kManyRows, kItem = 30, kMost = 10;
+  static constexpr int kThreads = kManyThreads, kRows = kManyRows, kItem = 100, kMost = 10;
   __device__ static int weight(int rows) { return rows <= kManyRows / 2 ? 6 : kMost; }
 };
 
@@ -129,12 +129,43 @@ __device__ __forceinline__ Shape shape(const Params& p, const Request& q, int rt
   s.weight = L::weight(s.rows);
   return s;
 }
+// Line length of row tile rt.
+template <class L>
+__device__ __forceinline__ long long item_cost(const Params& p, const Request& q, int rt) {
+  const Shape s = shape<L>(p, q, rt);
+  return static_cast<long long>(s.tiles) * s.weight + L::kItem;
+}
+// Line length of all row tiles of a head, by a thread.
 template <class L>
 __device__ __forceinline__ long long head_cost(const Params& p, const Request& q) {
   long long c = 0;
-  for (int rt = 0; rt < row_tiles<L>(p, q); ++rt) {
-    const Shape s = shape<L>(p, q, rt);
-    c += static_cast<long long>(s.tiles) * s.weight + L::kItem;
+  for (int rt = 0; rt < row_tiles<L>(p, q); ++rt) c += item_cost<L>(p, q, rt);
+  return c;
+}
+// The same where every lane of a warp has a request: those of many row tiles are added up by all lanes, one after the other.
+template <class L>
+__device__ __forceinline__ long long head_costs(const Params& p, const Request& q) {
+  constexpr int kAlone = 4;
+  const int rts = row_tiles<L>(p, q);
+  long long c = rts <= kAlone ? head_cost<L>(p, q) : 0;
+  for (uint32_t left = __ballot_sync(0xffffffffu, rts > kAlone); left; left &= left - 1) {
+    const int from = __ffs(left) - 1, n = __shfl_sync(0xffffffffu, rts, from), lane = threadIdx.x & 31;
+    Request x;
+    x.n = __shfl_sync(0xffffffffu, q.n, from), x.len = __shfl_sync(0xffffffffu, q.len, from);
+    long long sum = 0;
+    for (int rt = lane; rt < n; rt += 32) sum += item_cost<L>(p, x, rt);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == from) c = sum;
+  }
+  return c;
+}
+__device__ __forceinline__ long long warp_scan(long long c) {      // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, c, o);
+    if (lane >= o) c += v;
   }
   return c;
 }
@@ -172,11 +203,18 @@ __device__ __forceinline__ int key_of_row(int m) {
   return D == 128 ? m : 4 * ((m & 7) >> 1) + 2 * (m >> 3) + (m & 1);
 }
 
-// A wait of a whole warp, bounded as mbar_wait_short is; once one has run out, all others give up too.
-__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* failed, uint32_t code) {
+// `bytes` (a multiple of 16) from a 16-byte aligned address on their way to L2.
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// A wait of a whole warp, bounded as mbar_wait_short is; once one has run out, all others give up too.  `sleep_ns`: of
+// a warp that is far ahead, so that it leaves the issue slots to others.
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* failed, uint32_t code, uint32_t sleep_ns = 0) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
   while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+    if (sleep_ns) __nanosleep(sleep_ns);
     if (__any_sync(0xffffffffu, *failed != 0)) return false;
     if (__any_sync(0xffffffffu, clock64() - t0 > 4000000000ll)) {
       atomicOr(&g_attn8_err, code);
@@ -193,13 +231,14 @@ __device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) 
 // The line's length and the request in which position b0 lies; all threads of the CTA.
 struct Place {
   long long share, b0, at;   // line units a CTA; where this CTA's begins; where request r begins
+  long long head;            // line length of a head of it
   int r;                     // -1: nothing for this CTA
 };
 template <class L>
 __device__ __forceinline__ Place find_place(const Params& p) {
   constexpr int kWarps = L::kThreads / 32;
   __shared__ long long sums[kWarps];
-  __shared__ long long found_at;
+  __shared__ long long found_at, found_head;
   __shared__ int found_r;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // some more than an equal share, so that the shares cover the line
@@ -208,38 +247,33 @@ __device__ __forceinline__ Place find_place(const Params& p) {
                   static_cast<long long>(__fdividef(static_cast<float>(total), static_cast<float>(gridDim.x)) * 1.000001f) + 1);
     s.b0 = blockIdx.x * s.share;
   };
+  // line length of a head of request r (none past the last); all lanes of the warp
   const auto cost_of = [&](int r) {
-    const Request q = request(p.a, r);
+    Request q{0, 0, 0, false};
+    if (r < p.a.R) q = request(p.a, r);
     if (q.bad && blockIdx.x == 0) atomicOr(&g_attn8_err, kErrIndex);
-    return p.a.Hkv * head_cost<L>(p, q);
-  };
-  const auto scan = [&](long long c) {         // inclusive over the warp
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += v;
-    }
-    return c;
+    return head_costs<L>(p, q);
   };
   Place s;
   if (p.a.R <= 32) {                           // every warp by itself
-    const long long c = lane < p.a.R ? cost_of(lane) : 0, in = scan(c);
+    const long long h = cost_of(lane), c = p.a.Hkv * h, in = warp_scan(c);
     take(s, __shfl_sync(0xffffffffu, in, 31));
     const uint32_t here = __ballot_sync(0xffffffffu, in - c <= s.b0 && s.b0 < in);
     s.r = here ? __ffs(here) - 1 : -1;
     s.at = __shfl_sync(0xffffffffu, in - c, max(s.r, 0));
+    s.head = __shfl_sync(0xffffffffu, h, max(s.r, 0));
     return s;
   }
-  long long mine = 0, first_cost = 0;
-  for (int r = threadIdx.x; r < p.a.R; r += L::kThreads) {
-    const long long c = cost_of(r);
-    if (r < L::kThreads) first_cost = c;
-    mine += c;
+  long long mine = 0, first = 0;
+  for (int base = 0; base < p.a.R; base += L::kThreads) {
+    const long long h = cost_of(base + threadIdx.x);
+    if (base == 0) first = h;
+    mine += p.a.Hkv * h;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) sums[warp] = mine;
-  if (threadIdx.x == 0) found_r = -1, found_at = 0;
+  if (threadIdx.x == 0) found_r = -1, found_at = 0, found_head = 0;
   __syncthreads();
   long long total = 0;
 #pragma unroll
@@ -248,7 +282,7 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   long long before = 0;
   for (int base = 0; base < p.a.R && before <= s.b0 && s.b0 < total; base += L::kThreads) {
     const int r = base + threadIdx.x;
-    const long long c = base == 0 ? first_cost : r < p.a.R ? p.a.Hkv * head_cost<L>(p, request(p.a, r)) : 0, in = scan(c);
+    const long long h = base == 0 ? first : cost_of(r), c = p.a.Hkv * h, in = warp_scan(c);
     __syncthreads();
     if (lane == 31) sums[warp] = in;
     __syncthreads();
@@ -258,10 +292,10 @@ __device__ __forceinline__ Place find_place(const Params& p) {
       if (w < warp) at += sums[w];
       before += sums[w];
     }
-    if (at <= s.b0 && s.b0 < at + c) found_r = r, found_at = at;
+    if (at <= s.b0 && s.b0 < at + c) found_r = r, found_at = at, found_head = h;
   }
   __syncthreads();
-  s.r = found_r, s.at = found_at;
+  s.r = found_r, s.at = found_at, s.head = found_head;
   return s;
 }
 
@@ -282,73 +316,93 @@ __device__ __forceinline__ int tile_at(long long b, long long s, int n, int w) {
   return d >= static_cast<long long>(n) * w ? n : (static_cast<int>(d) + w - 1) / w;
 }
 
-// Walks over the items of one CTA's share of the line; copying and computing warps alike.
-template <class L>
-struct Walk {
-  const Params& p;
-  long long b0, b1, line, start;   // the share, where the next item begins, where this one does
-  int r, kvh, rt;                  // of the next item
+// A segment: what one CTA has of an item.
+struct Segment {
   Request q;
-  // the item: its request's row tile `tile`, head, shape, and the key tiles of this share
-  int tile, head, lo, hi;
+  int r, head, tile;               // request, key/value head, row tile
   Shape it;
+  int lo, hi;                      // key tiles
+  long long start;                 // the item's place on the line
 
-  __device__ Walk(const Params& p_, const Place& s) : p(p_), b0(s.b0), b1(s.b0 + s.share), line(s.at), r(s.r), kvh(0), rt(0) {
-    q = request(p.a, r);
-    const long long cost = head_cost<L>(p, q);       // heads before the share
-    kvh = quotient(b0 - line, cost);
-    line += kvh * cost;
-  }
-  __device__ bool next() {
-    while (line < b1) {
-      if (rt == row_tiles<L>(p, q)) {
-        rt = 0;
-        if (row_tiles<L>(p, q) == 0 || ++kvh == p.a.Hkv) {
-          kvh = 0;
-          if (++r == p.a.R) return false;
-          q = request(p.a, r);
-        }
-        continue;
-      }
-      it = shape<L>(p, q, rt);
-      tile = rt, head = kvh, start = line;
-      line += static_cast<long long>(it.tiles) * it.weight + L::kItem;
-      ++rt;
-      lo = tile_at(b0, start, it.tiles, it.weight), hi = tile_at(b1, start, it.tiles, it.weight);
-      if (lo < hi) return true;
-    }
-    return false;
-  }
+  __device__ bool whole() const { return lo == 0 && hi == it.tiles; }
   // The CTAs that have the item's first and last tile.
-  __device__ void ctas(int& c0, int& c1) const {
-    const long long share = b1 - b0;
+  __device__ void ctas(long long share, int& c0, int& c1) const {
     c0 = quotient(start, share), c1 = quotient(start + static_cast<long long>(it.tiles - 1) * it.weight, share);
   }
-  // Stages of KEYS keys of this share of the item, up to the last key that its last row sees.
-  template <int KEYS>
-  __device__ int stages(int& first) const {
+  // Its stages of KEYS keys, up to the last key that the item's last row sees.
+  template <class L, int KEYS>
+  __device__ int stages(const Params& p, int& first) const {
     const int seen = keys_seen(q, p.by_G.of(tile * L::kRows + it.rows - 1));
     first = lo * (kTile / KEYS);
     return max(0, min(hi * (kTile / KEYS), (seen + KEYS - 1) / KEYS) - first);
   }
 };
 
+// Walks over the segments of one CTA's share of the line; copying and computing warps alike.
+template <class L>
+struct Walk {
+  const Params& p;
+  long long b0, b1, line;          // the share, and where the next item begins
+  int r, kvh, rt, rts;             // the next item; row tiles of its request
+  Request q;
+
+  __device__ Walk(const Params& p_, const Place& s) : p(p_), b0(s.b0), b1(s.b0 + s.share), line(s.at), r(s.r), kvh(0), rt(0) {
+    q = request(p.a, r);
+    rts = row_tiles<L>(p, q);
+    kvh = quotient(b0 - line, s.head);               // heads before the share, and row tiles
+    line += kvh * s.head;
+    for (bool found = rts == 1; !found && rt < rts; rt += found ? 0 : 32) {
+      const int lane = threadIdx.x & 31;
+      const long long c = rt + lane < rts ? item_cost<L>(p, q, rt + lane) : 0, in = warp_scan(c);
+      const uint32_t past = __ballot_sync(0xffffffffu, line + in > b0);
+      found = past != 0;
+      const int at = found ? __ffs(past) - 1 : 31;
+      line += __shfl_sync(0xffffffffu, found ? in - c : in, at);
+      if (found) rt += at;
+    }
+  }
+  __device__ bool next(Segment& x) {
+    while (line < b1) {
+      if (rt == rts) {
+        rt = 0;
+        if (rts == 0 || ++kvh == p.a.Hkv) {
+          kvh = 0;
+          if (++r == p.a.R) return false;
+          q = request(p.a, r);
+          rts = row_tiles<L>(p, q);
+        }
+        continue;
+      }
+      const Shape it = shape<L>(p, q, rt);
+      const long long start = line;
+      line += static_cast<long long>(it.tiles) * it.weight + L::kItem;
+      ++rt;
+      x.lo = tile_at(b0, start, it.tiles, it.weight), x.hi = tile_at(b1, start, it.tiles, it.weight);
+      if (x.lo < x.hi) {
+        x.q = q, x.r = r, x.head = kvh, x.tile = rt - 1, x.it = it, x.start = start;
+        return true;
+      }
+    }
+    return false;
+  }
+};
+
 // The warp that copies: stages of KEYS keys and values of all the CTA's items into a ring of N places (ring(i): where
 // stage i's keys go, its values follow), and the scales of the stage's boxes to scales(i).  A box is what one copy
 // takes: a page's run of up to KEYS keys.
-template <class L, int D, int KEYS, int N, class Ring, class Scales>
-__device__ __forceinline__ void copy_items(const Params& p, const Place& place, const CUtensorMap& tk, const CUtensorMap& tv,
+template <class L, int D, int KEYS, int N, class Next, class Done, class Ring, class Scales>
+__device__ __forceinline__ void copy_items(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv, const Next& next, const Done& done,
                                            const Ring& ring, uint64_t* full, uint64_t* empty, const Scales& scales, int* failed) {
   const int lane = threadIdx.x & 31;
-  Walk<L> walk(p, place);
   uint32_t stage = 0;                          // of all items so far
   const uint64_t once = l2_policy_evict_first();
   const int box = min(p.a.page_size, KEYS), boxes = KEYS / box, log_box = 31 - __clz(box);
   bool ok = true;
-  while (ok && walk.next()) {
+  while (const Segment* seg = ok ? next() : nullptr) {
+    const Segment& x = *seg;
     int first;
-    const int n = walk.template stages<KEYS>(first), len = walk.q.len;
-    const int32_t* table = p.a.block_table + static_cast<int64_t>(walk.r) * p.a.max_blocks;
+    const int n = x.template stages<L, KEYS>(p, first), len = x.q.len;
+    const int32_t* table = p.a.block_table + static_cast<int64_t>(x.r) * p.a.max_blocks;
     // lane i has box base + i of the item; the table of the 32 after it is on its way
     const auto table_at = [&](int base) {
       const int key = first * KEYS + ((base + lane) << log_box);
@@ -365,7 +419,7 @@ __device__ __forceinline__ void copy_items(const Params& p, const Place& place, 
           atomicOr(&g_attn8_err, kErrIndex);
           page = 0;
         }
-        row = page * p.a.Hkv + walk.head;
+        row = page * p.a.Hkv + x.head;
         scale = __ldg(p.a.k_scales + row) | (static_cast<uint32_t>(__ldg(p.a.v_scales + row)) << 8);
         ahead = table_at(b0 + 32);
       }
@@ -393,6 +447,7 @@ __device__ __forceinline__ void copy_items(const Params& p, const Place& place, 
       }
       __syncwarp();
     }
+    if (ok) done();
   }
   // the last fill of each place has landed before the CTA's memory goes
   for (uint32_t i = stage > N ? stage - N : 0; i < stage; ++i)
@@ -440,11 +495,12 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
   const Place place = find_place<L>(p);
   if (place.r < 0) return;
   Walk<L> walk(p, place);
+  Segment seg;
 #pragma unroll 1
-  while (walk.next()) {
-    const Request& q = walk.q;
-    const Shape& it = walk.it;
-    const int kvh = walk.head, row0 = walk.tile * L::kRows;
+  while (walk.next(seg)) {
+    const Request& q = seg.q;
+    const Shape& it = seg.it;
+    const int kvh = seg.head, row0 = seg.tile * L::kRows;
     // ------------------------------------------------------------------ this warp's rows
     const int mt = it.rows <= 8 * NR ? 1 : it.rows <= 16 * NR ? 2 : 4, wk = W / mt;
     const int row_base = (warp & (mt - 1)) * 8 * NR, phase = warp / mt;
@@ -461,10 +517,10 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
       for (int i = 0; i < D / 32; ++i) raw[n][i] = row < it.rows ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
     }
     int first;
-    const int n_steps = walk.template stages<kKeys>(first);
+    const int n_steps = seg.template stages<L, kKeys>(p, first);
     const int s0 = first + phase, s1 = min(first + n_steps, (lim_top + kKeys - 1) / kKeys);
     const int steps = s1 > s0 ? (s1 - s0 + wk - 1) / wk : 0;
-    const int32_t* table = p.a.block_table + static_cast<int64_t>(walk.r) * p.a.max_blocks;
+    const int32_t* table = p.a.block_table + static_cast<int64_t>(seg.r) * p.a.max_blocks;
 
     // Lane i looks up piece i (16 keys) of a window of 32: its page, as the piece's place in the caches (16 D bytes
     // each: as many as memory can hold fit 32 bits), and the page's scales; the table of the window after it is on its
@@ -716,10 +772,10 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
       }
     }
     __syncthreads();
-    const bool whole = walk.lo == 0 && walk.hi == it.tiles;
+    const bool whole = seg.whole();
     const int cta = blockIdx.x;
     int c0, c1;
-    walk.ctas(c0, c1);
+    seg.ctas(place.share, c0, c1);
     const auto finish = [&](int row, int col, const float4& o, float top, float total) {
       const float inv = total == 0.f ? 0.f : 1.f / total;
       const int tok = p.by_G.of(row0 + row), head = kvh * p.G + (row0 + row) - tok * p.G;
@@ -820,7 +876,8 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
 constexpr int kRawStages = 3;          // tiles of codes, K and V
 constexpr int kWideStages = 3;         // tiles of fp16, of K and of V
 constexpr int kScaleRing = 16;         // tiles' scales: more than the copies are ahead of the softmax warps
-constexpr int kWWiden = 8, kWMma = 12, kWCopy = 14;    // first warps of a role; warps 0 .. 7: softmax; the last has none
+constexpr int kSegments = 4;           // segments that the walk is ahead of the other warps
+constexpr int kWWiden = 8, kWMma = 12, kWCopy = 14, kWWalk = 15;       // first warps of a role; warps 0 .. 7: softmax
 constexpr int kManyRegs = 168, kManyRegsOther = 88;    // of 128 a thread at launch
 constexpr int kTmemCols = 512, kColO = 256;            // two S of 64 columns a lane, then O of 128 a lane
 static_assert(8 * kManyRegs + 8 * kManyRegsOther == 128 * 16, "registers are those of the launch");
@@ -833,6 +890,8 @@ struct ManySmem {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   uint64_t full[2][kWideStages], empty[2][kWideStages];
   uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
+  Segment seg[kSegments];
   uint16_t scales[kScaleRing][4];
   int last, failed;
   uint32_t tmem_base;
@@ -862,6 +921,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[i][b], 1), mbar_init(&sm.p_full[i][b], 4);
       mbar_init(&sm.pv_done[i], 1), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.o_empty[i], 4), mbar_init(&sm.drain[i], 1);
     }
+    for (int i = 0; i < kSegments; ++i) mbar_init(&sm.seg_full[i], 1), mbar_init(&sm.seg_empty[i], kWWalk);
     sm.failed = 0;
     fence_barrier_init();
   }
@@ -879,12 +939,45 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   bool ok = true;
+  // The segment in its place in the ring, or null at the end or after a wait that ran out; given back when the warp is
+  // done with it.  `ahead`: the one after it.
+  uint32_t n_seg = 0;
+  const auto segment = [&](uint32_t ahead) -> const Segment* {
+    const uint32_t i = n_seg + ahead;
+    ok = ok && stage_wait(&sm.seg_full[i % kSegments], (i / kSegments) & 1, &sm.failed, kErrWaitFull);
+    return ok && sm.seg[i % kSegments].hi > 0 ? &sm.seg[i % kSegments] : nullptr;
+  };
+  const auto segment_done = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.seg_empty[n_seg % kSegments]);
+    ++n_seg;
+  };
 
   if (warp >= kWWiden) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kManyRegsOther));
-    if (warp == kWCopy) {
+    if (warp == kWWalk) {
+      // ------------------------------------------------------------------ the walk
+      Walk<L> walk(p, place);
+      bool more = true;
+      for (uint32_t i = 0; more && ok; ++i) {
+        Segment x;
+        more = walk.next(x);
+        if (!more) x.hi = 0;
+        if (more) {                             // its queries on their way to L2
+          const int row0 = x.tile * kManyRows, t0 = p.by_G.of(row0), tokens = p.by_G.of(row0 + x.it.rows - 1) - t0 + 1;
+          const uint32_t bytes = p.G * D * 2;
+          for (int t = lane; t < tokens; t += 32)
+            prefetch_l2(p.a.Q + (x.q.first + t0 + t) * p.a.q_stride + static_cast<int64_t>(x.head) * p.G * D, bytes);
+        }
+        ok = stage_wait(&sm.seg_empty[i % kSegments], ((i / kSegments) & 1) ^ 1, &sm.failed, kErrWaitEmpty, 500);
+        if (lane == 0 && ok) {
+          sm.seg[i % kSegments] = x;
+          mbar_arrive(&sm.seg_full[i % kSegments]);
+        }
+      }
+    } else if (warp == kWCopy) {
       // ------------------------------------------------------------------ codes and scales
-      copy_items<L, D, kTile, kRawStages>(p, place, tk, tv, [&](uint32_t i) { return sm.raw[i % kRawStages][0]; }, sm.raw_full, sm.raw_empty,
+      copy_items<L, D, kTile, kRawStages>(p, tk, tv, [&] { return segment(0); }, segment_done, [&](uint32_t i) { return sm.raw[i % kRawStages][0]; }, sm.raw_full, sm.raw_empty,
                                           [&](uint32_t i) { return sm.scales[i % kScaleRing]; }, &sm.failed);
     } else if (warp < kWMma) {
       // ------------------------------------------------------------------ codes -> fp16
@@ -892,11 +985,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       // k ^ 1 where d is 64) so that what they read and what they write falls on all banks.
       constexpr int kUnits = kTile * D / 16 / 128;      // of a thread
       const int u0 = threadIdx.x - 32 * kWWiden;
-      Walk<L> walk(p, place);
       uint32_t tile = 0;
-      while (ok && walk.next()) {
+      while (const Segment* x = segment(0)) {
         int first;
-        const int n = walk.stages<kTile>(first), len = walk.q.len;
+        const int n = x->stages<L, kTile>(p, first), len = x->q.len;
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j, ++tile) {
           const uint32_t rs = tile % kRawStages, ws = tile % kWideStages;
@@ -919,9 +1011,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
             for (int i = 0; i < kUnits; ++i) {
               uint8_t* dst = sm.wide[v][ws] + plane[i] * kKvChunk + key[i] * 128;
-              const int unit = 2 * (u0 & 3), x = key[i] & 7;
-              *reinterpret_cast<uint4*>(dst + 16 * (unit ^ x)) = make_uint4(e4m3_low(c[i].x), e4m3_high(c[i].x), e4m3_low(c[i].y), e4m3_high(c[i].y));
-              *reinterpret_cast<uint4*>(dst + 16 * ((unit + 1) ^ x)) = make_uint4(e4m3_low(c[i].z), e4m3_high(c[i].z), e4m3_low(c[i].w), e4m3_high(c[i].w));
+              const int unit = 2 * (u0 & 3), swap = key[i] & 7;
+              *reinterpret_cast<uint4*>(dst + 16 * (unit ^ swap)) = make_uint4(e4m3_low(c[i].x), e4m3_high(c[i].x), e4m3_low(c[i].y), e4m3_high(c[i].y));
+              *reinterpret_cast<uint4*>(dst + 16 * ((unit + 1) ^ swap)) = make_uint4(e4m3_low(c[i].z), e4m3_high(c[i].z), e4m3_low(c[i].w), e4m3_high(c[i].w));
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -929,6 +1021,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
           if (ok && lane == 0) mbar_arrive(&sm.raw_empty[rs]);
         }
+        if (!ok) break;
+        segment_done();
       }
     } else if (warp < kWCopy) {
       // ------------------------------------------------------------------ products of lane l
@@ -941,15 +1035,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       constexpr uint32_t kWideBytes = kTile * D * 2;
       uint32_t k_tile = 0, v_tile = 0, items = 0;       // tiles and items of this lane's own alike for all
       uint32_t s_cnt = 0, p_cnt = 0;            // tiles of this lane whose S was issued / whose W was taken
-      Walk<L> walk(p, place);
-      while (ok && walk.next()) {
+      while (const Segment* x = segment(0)) {
         int first;
-        const int n = walk.stages<kTile>(first);
+        const int n = x->stages<L, kTile>(p, first);
         // Every place of the rings is waited for and given back by both lanes, also where one has no rows: a wait
         // by parity is only sound if no phase is left out.
-        const bool mine = l == 0 || walk.it.rows > 128;
+        const bool mine = l == 0 || x->it.rows > 128;
         if (mine && n > 0) ok = stage_wait(&sm.q_full[l], items & 1, &sm.failed, kErrWaitFull);
-        const auto qk = [&](int) {
+        const auto qk = [&](int j) {
           const uint32_t sl = k_tile % kWideStages;
           ok = stage_wait(&sm.full[0][sl], (k_tile / kWideStages) & 1, &sm.failed, kErrWaitFull);
           if (!ok) return;
@@ -969,6 +1062,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                             id_qk, k ? 1u : 0u);
             tc_commit(&sm.s_full[l][b]);
             tc_commit(&sm.empty[0][sl]);
+            if (j + 1 == n) tc_commit(&sm.q_empty[l]);
           }
           __syncwarp();
           ++s_cnt;
@@ -1006,11 +1100,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (ok && j < n) qk(j);
         }
         if (!ok) break;
-        if (mine && n > 0) {
-          if (elect_one()) tc_commit(&sm.q_empty[l]);
-          __syncwarp();
-          ++items;
-        }
+        if (mine && n > 0) ++items;
+        segment_done();
       }
       // every product and commit of this warp (elect.sync names the same lane each time) has completed before tensor memory and barriers go
       if (elect_one()) tc_commit(&sm.drain[l]);
@@ -1024,46 +1115,80 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t t_o = tmem + lane_base + kColO + 128 * l;
     const int log_box = 31 - __clz(min(p.a.page_size, kTile));
     uint32_t cnt = 0, items = 0, tile = 0;      // tiles and items of this lane; tiles of all items
-    Walk<L> walk(p, place);
-    while (walk.next()) {
-      int first;
-      const int n = ok ? walk.stages<kTile>(first) : 0;
-      const int row_item = 128 * l + row, rows = walk.it.rows, row_all = walk.tile * kManyRows + row_item;
-      const bool mine = l == 0 || rows > 128, valid = row_item < rows, active = __any_sync(0xffffffffu, valid);
-      const int tok = p.by_G.of(row_all), head = walk.head * p.G + row_all - tok * p.G;
-      const int lim = valid ? keys_seen(walk.q, tok) : 0;
-      float m = -INFINITY, sum = 0.f;           // m: the largest x, in units of log2
-      float c = p.c;
-      if (mine && n > 0) {
-        // Q -> fp16, behind a power of two of the row where it is bf16
-        uint4 x[D / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(p.a.Q + (walk.q.first + tok) * p.a.q_stride + static_cast<int64_t>(head) * D);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        if (!F16) {
-          uint32_t mx = 0;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu), __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-          const int k = bf16_to_f16_exponent(max(mx & 0xffffu, mx >> 16));
-          const float down = pow2_normal(-k);
-          c *= pow2_normal(k);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float2 f = unpack2<false>((&x[i].x)[w]);
-              (&x[i].x)[w] = pack2<true>(f.x * down, f.y * down);
-            }
-        }
-        ok = stage_wait(&sm.q_empty[l], (items & 1) ^ 1, &sm.failed, kErrWaitEmpty);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint4*>(sm.q[l] + (i >> 3) * kQChunk + row * 128 + 16 * ((i & 7) ^ (row & 7))) = x[i];
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_full[l]);
+    uint32_t q_items = 0;                       // items of this lane whose Q is on its way
+    // What this thread's row of a segment needs.
+    struct Row {
+      bool mine, valid;                         // the lane has rows; this row is one
+      int tok, head, n, first;
+      float c;                                  // scale * log2(e), times the power of two taken from the query
+    };
+    const auto row_of = [&](const Segment& x) {
+      Row w;
+      const int row_item = 128 * l + row, row_all = x.tile * kManyRows + row_item;
+      w.mine = l == 0 || x.it.rows > 128, w.valid = row_item < x.it.rows;
+      w.tok = p.by_G.of(row_all), w.head = x.head * p.G + row_all - w.tok * p.G;
+      w.n = x.template stages<L, kTile>(p, w.first);
+      w.c = p.c;
+      return w;
+    };
+    // Q to shared memory, and there to fp16, behind a power of two of the row where it is bf16.  Loops that stay
+    // loops: code that runs once an item comes from L2, and unrolled it took 4 us an item.
+    const auto put_q = [&](const Segment& x, Row& w) {
+      if (!w.mine || w.n == 0) return;
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;      // lanes a row, rows a copy of the warp
+      uint8_t* const q = sm.q[l] + (warp & 3) * 32 * 128;       // the warp's 32 rows
+      const auto place_of = [&](int to, int unit) { return (unit >> 3) * kQChunk + to * 128 + 16 * ((unit & 7) ^ (to & 7)); };
+      const int64_t row_at = (x.q.first + w.tok) * p.a.q_stride + static_cast<int64_t>(w.head) * D;
+      const uint32_t rows = __ballot_sync(0xffffffffu, w.valid);
+      ok = ok && stage_wait(&sm.q_empty[l], (q_items & 1) ^ 1, &sm.failed, kErrWaitEmpty);
+#pragma unroll 1
+      for (int i = 0; i < kLanes; ++i) {
+        const int to = i * kAtOnce + lane / kLanes;
+        const int64_t at = __shfl_sync(0xffffffffu, row_at, to);
+        const bool on = (rows >> to) & 1;      // rows that do not exist: zeros
+        copy16(q + place_of(to, lane % kLanes), on ? p.a.Q + at + 8 * (lane % kLanes) : p.a.Q, on);
       }
+      copy_commit();
+      copy_wait<0>();
+      __syncwarp();
+      if (!F16) {
+        uint32_t mx = 0;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(q + place_of(lane, i));
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+        }
+        const int k = bf16_to_f16_exponent(max(mx & 0xffffu, mx >> 16));
+        const float down = pow2_normal(-k);
+        w.c *= pow2_normal(k);
+#pragma unroll 2
+        for (int i = 0; i < D / 8; ++i) {
+          uint4* at = reinterpret_cast<uint4*>(q + place_of(lane, i));
+          uint4 v = *at;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2<false>((&v.x)[e]);
+            (&v.x)[e] = pack2<true>(f.x * down, f.y * down);
+          }
+          *at = v;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full[l]);
+      ++q_items;
+    };
+    const Segment* seg = segment(0);
+    Row w{};
+    if (seg) w = row_of(*seg), put_q(*seg, w);
+#pragma unroll 1
+    while (seg) {
+      const Segment& x = *seg;
+      const int n = ok ? w.n : 0, first = w.first, row_item = 128 * l + row;
+      const bool mine = w.mine, valid = w.valid, active = __any_sync(0xffffffffu, valid);
+      const int lim = valid ? keys_seen(x.q, w.tok) : 0;
+      const float c = w.c;
+      float m = -INFINITY, sum = 0.f;           // m: the largest x, in units of log2
 #pragma unroll 1
       for (int j = 0; j < n && ok && mine; ++j, ++cnt) {
         const int key0 = (first + j) * kTile;
@@ -1137,8 +1262,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const uint32_t* s = &v[q >> 1][16 * (q & 1) + 2 * e];
-              const float2 x = unpair(fma_pair(pair(s[0], s[1]), c2, b2));
-              const float a = exp2_approx(x.x), d = exp2_approx(x.y);
+              const float2 y = unpair(fma_pair(pair(s[0], s[1]), c2, b2));
+              const float a = exp2_approx(y.x), d = exp2_approx(y.y);
               part = add_pair(part, pair_f(a, d));
               w[e] = pack2<true>(a, d);
             }
@@ -1153,6 +1278,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (lane == 0) mbar_arrive(&sm.p_full[l][b]);
       }
       tile += n;
+      // the next segment's Q is put in place before this one's output is taken, so that its first products run beside that
+      const Segment* next = segment(1);
+      const Row done = w;
+      if (next) w = row_of(*next), put_q(*next, w);
       // ------------------------------------------------------------------ the segment's output
       uint32_t o[D / 32][32];
       if (mine && n > 0 && ok) {
@@ -1171,66 +1300,91 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[q][e] = 0;
       }
-      const int cta = blockIdx.x;
-      const auto finish = [&](float top, float total) {
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        const int64_t at_row = static_cast<int64_t>(walk.q.first + tok) * p.a.Hq + head;
-        uint4* dst = reinterpret_cast<uint4*>(p.a.O + at_row * D);
+      const int64_t at_row = static_cast<int64_t>(x.q.first + done.tok) * p.a.Hq + done.head;
+      // 32 columns of the row, given as the sums' bits
+      const auto finish = [&](int q, const uint32_t (&o)[32], float inv) {
+        uint32_t h[16];
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          uint32_t w[4];
+        for (int i = 0; i < 16; ++i) h[i] = pack2<F16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+        uint4* dst = reinterpret_cast<uint4*>(p.a.O + at_row * D + 32 * q);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = pack2<F16>(__uint_as_float(o[e >> 2][8 * (e & 3) + 2 * i]) * inv, __uint_as_float(o[e >> 2][8 * (e & 3) + 2 * i + 1]) * inv);
-          dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+      };
+      const auto finish_lse = [&](float top, float total) {
         if (p.a.lse)
           p.a.lse[at_row] = total == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - kUp + log2f(total)) * 0.6931471805599453f;
       };
-      if (walk.lo == 0 && walk.hi == walk.it.tiles) {
-        if (valid) finish(m, sum);
-        continue;
-      }
-      int c0, c1;
-      walk.ctas(c0, c1);
-      // partials [cta][2][d / 4][256 rows][4]: a warp writes and reads whole lines
-      const auto slot = [&](int at) { return 2ll * at + (at == c0 ? 1 : 0); };
-      if (valid) {
-        float4* po = reinterpret_cast<float4*>(p.po) + slot(cta) * (D / 4) * kManyRows + row_item;
+      if (x.whole()) {
+        if (valid) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int e = 0; e < D / 4; ++e)
-          po[e * kManyRows] = make_float4(__uint_as_float(o[e >> 3][4 * (e & 7)]), __uint_as_float(o[e >> 3][4 * (e & 7) + 1]),
-                                          __uint_as_float(o[e >> 3][4 * (e & 7) + 2]), __uint_as_float(o[e >> 3][4 * (e & 7) + 3]));
-        p.ml[slot(cta) * kManyRows + row_item] = make_float2(m, sum);
-      }
-      named_bar_sync(1, 256);
-      if (threadIdx.x == 0) sm.last = last_segment(p.count + c0, c1 - c0 + 1);
-      named_bar_sync(1, 256);
-      if (sm.last && valid) {
-        float top = -INFINITY, total = 0.f;
+          for (int q = 0; q < D / 32; ++q) finish(q, o[q], inv);
+          finish_lse(m, sum);
+        }
+      } else {
+        int c0, c1;
+        x.ctas(place.share, c0, c1);
+        // partials [cta][2][d / 4][256 rows][4]: a warp writes and reads whole lines
+        const auto slot = [&](int at) { return 2ll * at + (at == c0 ? 1 : 0); };
+        const auto part = [&](int at) { return reinterpret_cast<float4*>(p.po) + slot(at) * (D / 4) * kManyRows + row_item; };
+        if (valid) {
+          float4* po = part(blockIdx.x);
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e)
+            po[e * kManyRows] = make_float4(__uint_as_float(o[e >> 3][4 * (e & 7)]), __uint_as_float(o[e >> 3][4 * (e & 7) + 1]),
+                                            __uint_as_float(o[e >> 3][4 * (e & 7) + 2]), __uint_as_float(o[e >> 3][4 * (e & 7) + 3]));
+          p.ml[slot(blockIdx.x) * kManyRows + row_item] = make_float2(m, sum);
+        }
+        named_bar_sync(1, 256);
+        if (threadIdx.x == 0) sm.last = last_segment(p.count + c0, c1 - c0 + 1);
+        named_bar_sync(1, 256);
+        if (sm.last && valid) {
+          float top = -INFINITY, total = 0.f;
 #pragma unroll 4
-        for (int at = c0; at <= c1; ++at) top = fmaxf(top, __ldcg(&p.ml[slot(at) * kManyRows + row_item].x));
-        const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[q][e] = 0;
+          for (int at = c0; at <= c1; ++at) top = fmaxf(top, __ldcg(&p.ml[slot(at) * kManyRows + row_item].x));
+          const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+          for (int at = c0; at <= c1; ++at) {
+            const float2 ml = __ldcg(p.ml + slot(at) * kManyRows + row_item);
+            total = fmaf(ml.y, exp2_approx(ml.x - ref), total);
+          }
+          const float inv = total == 0.f ? 0.f : 1.f / total;
+          finish_lse(top, total);
+          // 32 columns at a time, two segments' loads under way
 #pragma unroll 1
-        for (int at = c0; at <= c1; ++at) {
-          const float2 ml = __ldcg(p.ml + slot(at) * kManyRows + row_item);
-          const float f = exp2_approx(ml.x - ref);
-          total = fmaf(ml.y, f, total);
-          const float4* po = reinterpret_cast<const float4*>(p.po) + slot(at) * (D / 4) * kManyRows + row_item;
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t sums[32];
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e) {
-            const float4 v = __ldcg(po + e * kManyRows);
-            uint32_t* a = &o[e >> 3][4 * (e & 7)];
-            a[0] = __float_as_uint(fmaf(v.x, f, __uint_as_float(a[0]))), a[1] = __float_as_uint(fmaf(v.y, f, __uint_as_float(a[1])));
-            a[2] = __float_as_uint(fmaf(v.z, f, __uint_as_float(a[2]))), a[3] = __float_as_uint(fmaf(v.w, f, __uint_as_float(a[3])));
+            for (int e = 0; e < 32; ++e) sums[e] = 0;
+#pragma unroll 1
+            for (int at = c0; at <= c1; at += 2) {
+              float4 v[2][8];
+              float f[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int a = min(at + i, c1);
+                f[i] = __ldcg(&p.ml[slot(a) * kManyRows + row_item].x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = __ldcg(part(a) + (8 * q + e) * kManyRows);
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (at + i > c1) break;
+                const float scale = exp2_approx(f[i] - ref);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  uint32_t* a = &sums[4 * e];
+                  a[0] = __float_as_uint(fmaf(v[i][e].x, scale, __uint_as_float(a[0]))), a[1] = __float_as_uint(fmaf(v[i][e].y, scale, __uint_as_float(a[1])));
+                  a[2] = __float_as_uint(fmaf(v[i][e].z, scale, __uint_as_float(a[2]))), a[3] = __float_as_uint(fmaf(v[i][e].w, scale, __uint_as_float(a[3])));
+                }
+              }
+            }
+            finish(q, sums, inv);
           }
         }
-        finish(top, total);
       }
+      segment_done();
+      seg = next;
     }
   }
   __syncwarp();
