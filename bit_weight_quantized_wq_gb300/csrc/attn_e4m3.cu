@@ -71,7 +71,7 @@ struct Params {
   Divisor by_G;
   int few;                   // requests of up to so many rows are the first kernel's
   float c;                   // scale * log2(e)
-  int* count;                // segments of the item that begins in a CTA which are done [ctas]
+  int* count;                // segments (or groups) that are done of the item that begins in a CTA, and of the group [2][ctas]
   float *po;                 // partials [cta][2][rows of an item][d], largest exponents and sums [cta][2][rows][2]
   float2 *ml;
 };
@@ -224,10 +224,6 @@ __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volat
   }
   return true;
 }
-__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-
 // The line's length and the request in which position b0 lies; all threads of the CTA.
 struct Place {
   long long share, b0, at;   // line units a CTA; where this CTA's begins; where request r begins
@@ -298,6 +294,10 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   s.r = found_r, s.at = found_at, s.head = found_head;
   return s;
 }
+
+// An item's segments are joined in line order by the last CTA that is done with it, or, where there are more of them
+// than kGroup, in two steps: groups of kGroup neighbours, each joined in the place of its first, then the groups.
+constexpr int kGroup = 8;
 
 // Counts this CTA's segment of an item that CTAs c0 .. c1 share; true in the one that is last, which sees what the
 // others have written.  After a barrier of the CTA's writers, by one thread.
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
   constexpr int kPieces = kKeys / 16;
   constexpr int KS = D / 16;                   // 16-wide steps of d, and 16-row tiles of V^T
   constexpr int R2 = 2 * NR;                   // rows that a thread has scores of: 2 t, 2 t + 1 (and 8 more each)
-  extern __shared__ __align__(128) uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
@@ -812,29 +812,44 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
     }
     __syncthreads();         // the outputs' places are free again
     if (!whole) {
-      // the last CTA that is done with the item joins what all of them left, in line order
-      if (threadIdx.x == 0) sm.last = last_segment(p.count + c0, c1 - c0 + 1);
-      __syncthreads();
-      if (sm.last) {
+      const int segments = c1 - c0 + 1, group = (cta - c0) / kGroup;
+      const auto last = [&](int* count, int n) {
+        __syncthreads();
+        if (threadIdx.x == 0) sm.last = last_segment(count, n);
+        __syncthreads();
+        return sm.last != 0;
+      };
+      int first = c0, step = 1, n = segments;
+      bool final = true, mine;
+      if (segments > kGroup) {
+        first = c0 + group * kGroup, n = min(kGroup, c1 - first + 1), final = false;
+        mine = last(p.count + gridDim.x + first, n);
+      } else {
+        mine = last(p.count + c0, n);
+      }
+      while (mine) {
         // P neighbouring threads take a unit's segments in turn, eight at a time, so that few loads wait for others
         const int parts = units * 8 <= 32 * W ? 8 : units * 4 <= 32 * W ? 4 : units * 2 <= 32 * W ? 2 : 1, part = threadIdx.x & (parts - 1);
 #pragma unroll 1
         for (int u0 = 0; u0 < units * parts; u0 += 32 * W) {
           const int u = min((u0 + static_cast<int>(threadIdx.x)) / parts, units - 1), row = u / (D / 4), col = 4 * (u % (D / 4));
-          const auto slot = [&](int c) { return (2ll * c + (c == c0 ? 1 : 0)) * L::kRows + row; };
+          const auto slot = [&](int i) {
+            const int c = first + i * step;
+            return (2ll * c + (c == c0 ? 1 : 0)) * L::kRows + row;
+          };
           float top = -INFINITY, total = 0.f;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-          for (int base = c0 + part; base <= c1; base += 8 * parts) {
+          for (int base = part; base < n; base += 8 * parts) {
             float2 ml[8];
             float4 v[8];
             float now = top;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int c = min(base + i * parts, c1);
-              ml[i] = __ldcg(p.ml + slot(c));
-              v[i] = __ldcg(reinterpret_cast<const float4*>(p.po + slot(c) * D + col));
-              if (base + i * parts > c1) ml[i] = make_float2(-INFINITY, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              const long long at = slot(min(base + i * parts, n - 1));
+              ml[i] = __ldcg(p.ml + at);
+              v[i] = __ldcg(reinterpret_cast<const float4*>(p.po + at * D + col));
+              if (base + i * parts >= n) ml[i] = make_float2(-INFINITY, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
               now = fmaxf(now, ml[i].x);
             }
             const float ref = now == -INFINITY ? 0.f : now, keep = exp2_approx(top - ref);
@@ -856,8 +871,21 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
             o.x += __shfl_xor_sync(0xffffffffu, o.x, d), o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
             o.z += __shfl_xor_sync(0xffffffffu, o.z, d), o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
           }
-          if (part == 0 && u0 + static_cast<int>(threadIdx.x) < units * parts) finish(row, col, o, top, total);
+          if (part == 0 && u0 + static_cast<int>(threadIdx.x) < units * parts) {
+            if (final) {
+              finish(row, col, o, top, total);
+            } else {
+              *reinterpret_cast<float4*>(p.po + slot(0) * D + col) = o;
+              if (col == 0) sm.ml[row / (8 * NR)][row % (8 * NR)] = make_float2(top, total);
+            }
+          }
         }
+        if (final) break;
+        __syncthreads();                       // all have read what the group's first CTA left
+        for (int row = threadIdx.x; row < it.rows; row += 32 * W)
+          p.ml[(2ll * first + (first == c0 ? 1 : 0)) * L::kRows + row] = sm.ml[row / (8 * NR)][row % (8 * NR)];
+        first = c0, step = kGroup, n = (segments + kGroup - 1) / kGroup, final = true;
+        mine = last(p.count + c0, n);
       }
     }
     __syncthreads();                           // and the ring again
@@ -1335,52 +1363,78 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                                             __uint_as_float(o[e >> 3][4 * (e & 7) + 2]), __uint_as_float(o[e >> 3][4 * (e & 7) + 3]));
           p.ml[slot(blockIdx.x) * kManyRows + row_item] = make_float2(m, sum);
         }
-        named_bar_sync(1, 256);
-        if (threadIdx.x == 0) sm.last = last_segment(p.count + c0, c1 - c0 + 1);
-        named_bar_sync(1, 256);
-        if (sm.last && valid) {
-          float top = -INFINITY, total = 0.f;
+        const int segments = c1 - c0 + 1, cta = blockIdx.x;
+        const auto last = [&](int* count, int n) {
+          named_bar_sync(1, 256);
+          if (threadIdx.x == 0) sm.last = last_segment(count, n);
+          named_bar_sync(1, 256);
+          return sm.last != 0;
+        };
+        int first = c0, step = 1, n_parts = segments;
+        bool final = true, joins;
+        if (segments > kGroup) {
+          first = c0 + (cta - c0) / kGroup * kGroup, n_parts = min(kGroup, c1 - first + 1), final = false;
+          joins = last(p.count + gridDim.x + first, n_parts);
+        } else {
+          joins = last(p.count + c0, n_parts);
+        }
+        while (joins) {
+          if (valid) {                         // a row's partials are read and written by its thread alone
+            float top = -INFINITY, total = 0.f;
 #pragma unroll 4
-          for (int at = c0; at <= c1; ++at) top = fmaxf(top, __ldcg(&p.ml[slot(at) * kManyRows + row_item].x));
-          const float ref = top == -INFINITY ? 0.f : top;
+            for (int i = 0; i < n_parts; ++i) top = fmaxf(top, __ldcg(&p.ml[slot(first + i * step) * kManyRows + row_item].x));
+            const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
-          for (int at = c0; at <= c1; ++at) {
-            const float2 ml = __ldcg(p.ml + slot(at) * kManyRows + row_item);
-            total = fmaf(ml.y, exp2_approx(ml.x - ref), total);
-          }
-          const float inv = total == 0.f ? 0.f : 1.f / total;
-          finish_lse(top, total);
-          // 32 columns at a time, two segments' loads under way
+            for (int i = 0; i < n_parts; ++i) {
+              const float2 ml = __ldcg(p.ml + slot(first + i * step) * kManyRows + row_item);
+              total = fmaf(ml.y, exp2_approx(ml.x - ref), total);
+            }
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            // 32 columns at a time, two segments' loads under way
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t sums[32];
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t sums[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) sums[e] = 0;
+              for (int e = 0; e < 32; ++e) sums[e] = 0;
 #pragma unroll 1
-            for (int at = c0; at <= c1; at += 2) {
-              float4 v[2][8];
-              float f[2];
+              for (int i0 = 0; i0 < n_parts; i0 += 2) {
+                float4 v[2][8];
+                float f[2];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int a = min(at + i, c1);
-                f[i] = __ldcg(&p.ml[slot(a) * kManyRows + row_item].x);
+                for (int i = 0; i < 2; ++i) {
+                  const int at = first + min(i0 + i, n_parts - 1) * step;
+                  f[i] = __ldcg(&p.ml[slot(at) * kManyRows + row_item].x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = __ldcg(part(a) + (8 * q + e) * kManyRows);
-              }
+                  for (int e = 0; e < 8; ++e) v[i][e] = __ldcg(part(at) + (8 * q + e) * kManyRows);
+                }
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (at + i > c1) break;
-                const float scale = exp2_approx(f[i] - ref);
+                for (int i = 0; i < 2; ++i) {
+                  if (i0 + i >= n_parts) break;
+                  const float scale = exp2_approx(f[i] - ref);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  uint32_t* a = &sums[4 * e];
-                  a[0] = __float_as_uint(fmaf(v[i][e].x, scale, __uint_as_float(a[0]))), a[1] = __float_as_uint(fmaf(v[i][e].y, scale, __uint_as_float(a[1])));
-                  a[2] = __float_as_uint(fmaf(v[i][e].z, scale, __uint_as_float(a[2]))), a[3] = __float_as_uint(fmaf(v[i][e].w, scale, __uint_as_float(a[3])));
+                  for (int e = 0; e < 8; ++e) {
+                    uint32_t* a = &sums[4 * e];
+                    a[0] = __float_as_uint(fmaf(v[i][e].x, scale, __uint_as_float(a[0]))), a[1] = __float_as_uint(fmaf(v[i][e].y, scale, __uint_as_float(a[1])));
+                    a[2] = __float_as_uint(fmaf(v[i][e].z, scale, __uint_as_float(a[2]))), a[3] = __float_as_uint(fmaf(v[i][e].w, scale, __uint_as_float(a[3])));
+                  }
                 }
               }
+              if (final) {
+                finish(q, sums, inv);
+              } else {
+                float4* po = part(first) + 8 * q * kManyRows;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  po[e * kManyRows] = make_float4(__uint_as_float(sums[4 * e]), __uint_as_float(sums[4 * e + 1]), __uint_as_float(sums[4 * e + 2]),
+                                                  __uint_as_float(sums[4 * e + 3]));
+              }
             }
-            finish(q, sums, inv);
+            if (final) finish_lse(top, total);
+            else p.ml[slot(first) * kManyRows + row_item] = make_float2(top, total);
           }
+          if (final) break;
+          first = c0, step = kGroup, n_parts = (segments + kGroup - 1) / kGroup, final = true;
+          joins = last(p.count + c0, n_parts);
         }
       }
       segment_done();
@@ -1470,10 +1524,8 @@ cudaError_t launch_t(const AttnE4m3Args& a, uint8_t* ws, cudaStream_t stream) {
     const cudaError_t e = launch_many<F16, D>(p, l, stream);
     if (e != cudaSuccess) return e;
   }
-  // Few items: one CTA an SM, so that an item has fewer segments.
-  const bool few_items = static_cast<int64_t>(a.R) * a.Hkv <= l.sms;
-  if (rows <= 8) return few_items ? launch_few<F16, D, 1, 16>(p, l, stream) : launch_few<F16, D, 1, 4>(p, l, stream);
-  return few_items ? launch_few<F16, D, 2, 12>(p, l, stream) : launch_few<F16, D, 2, 4>(p, l, stream);
+  if (rows <= 8) return launch_few<F16, D, 1, 4>(p, l, stream);
+  return launch_few<F16, D, 2, 4>(p, l, stream);
 }
 
 }  // namespace
