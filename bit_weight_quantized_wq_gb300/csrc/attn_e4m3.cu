@@ -65,6 +65,8 @@ __device__ __forceinline__ int quotient(long long a, long long b) {
   return q;
 }
 
+constexpr int kFewWarps = 4;           // of a CTA of the kernel for few rows
+
 struct Params {
   AttnE4m3Args a;
   int G, log_page;
@@ -98,18 +100,19 @@ __device__ __forceinline__ int keys_seen(const Request& q, int token) { return m
 
 // A line's items: their rows, the weight of a tile (by the item's rows) and the constant of an item.
 // Weights are in units of some 20 cycles of an SM.
-template <int NR, int W>
+constexpr int kFewMostRows = 16;       // of a request's head in the kernel for few rows
+template <int NR>
 struct FewLine {
   __device__ static bool takes(const Params& p, int rows) { return rows <= p.few; }
-  static constexpr int kThreads = 32 * W, kRows = 4 * 8 * NR, kItem = 60, kMost = 20;
-  __device__ static int weight(int rows) { return rows <= 8 * NR ? 8 : rows <= 16 * NR ? 12 : kMost; }
+  static constexpr int kThreads = 32 * kFewWarps, kRows = 8 * NR, kItem = 60, kMost = 8;
+  __device__ static int weight(int) { return kMost; }
 };
 
 constexpr int kManyThreads = 512, kManyRows = 256;
 struct ManyLine {
   __device__ static bool takes(const Params& p, int rows) { return rows > p.few; }
   static constexpr int kThreads = kManyThreads, kRows = kManyRows, kItem = 100, kMost = 10;
-  __device__ static int weight(int rows) { return rows <= kManyRows / 2 ? 6 : kMost; }
+  __device__ static int weight(int rows) { return rows <= kManyRows / 2 ? 5 : kMost; }
 };
 
 // One item: row tile rt of a request and head.
@@ -456,14 +459,14 @@ __device__ __forceinline__ void copy_items(const Params& p, const CUtensorMap& t
 
 constexpr int kStages = 3;             // steps of a warp in shared memory, two of them under way
 constexpr int kStepBytes = 2048;       // of K, and of V
-template <int D, int NR, int W>
+template <int D, int NR>
 struct FewSmem {
   static constexpr int kRow = D + 4;
   union {
-    uint8_t ring[W][kStages][2][kStepBytes];   // K, V
-    float o[W][8 * NR][kRow];                  // the warps' outputs, once their steps are done
+    uint8_t ring[kFewWarps][kStages][2][kStepBytes];   // K, V
+    float o[kFewWarps][8 * NR][kRow];                  // the warps' outputs, once their steps are done
   };
-  float2 ml[W][8 * NR];
+  float2 ml[kFewWarps][8 * NR];
   int last;
 };
 
@@ -472,13 +475,14 @@ __device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Warps an SM: registers for 16 with eight rows a warp, for 12 with sixteen.
-constexpr int few_warps(int nr) { return nr == 1 ? 16 : 12; }
+// CTAs an SM: as many as there are registers for (with 12 warps of 168 registers for eight rows, 64 requests over up to
+// 16384 keys took 204 us instead of 174: the kernel is bound by what its warps wait for).
+constexpr int few_ctas(int nr) { return nr == 1 ? 4 : 3; }
 
-template <bool F16, int D, int NR, int W>
-__global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const __grid_constant__ Params p) {
-  using L = FewLine<NR, W>;
-  using S = FewSmem<D, NR, W>;
+template <bool F16, int D, int NR>
+__global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4m3(const __grid_constant__ Params p) {
+  using L = FewLine<NR>;
+  using S = FewSmem<D, NR>;
   constexpr int kKeys = kStepBytes / D;        // of a step
   constexpr int kPieces = kKeys / 16;
   constexpr int KS = D / 16;                   // 16-wide steps of d, and 16-row tiles of V^T
@@ -500,32 +504,27 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
   while (walk.next(seg)) {
     const Request& q = seg.q;
     const Shape& it = seg.it;
-    const int kvh = seg.head, row0 = seg.tile * L::kRows;
-    // ------------------------------------------------------------------ this warp's rows
-    const int mt = it.rows <= 8 * NR ? 1 : it.rows <= 16 * NR ? 2 : 4, wk = W / mt;
-    const int row_base = (warp & (mt - 1)) * 8 * NR, phase = warp / mt;
-    // the most keys that a row of the warp sees, and the fewest
-    const int last_row = min(it.rows, row_base + 8 * NR) - 1;
-    const int lim_top = last_row < row_base ? 0 : keys_seen(q, p.by_G.of(row0 + last_row));
-    const int lim_low = keys_seen(q, p.by_G.of(row0 + row_base));
+    const int kvh = seg.head;
+    // the most keys that a row sees, and the fewest
+    const int lim_top = keys_seen(q, p.by_G.of(it.rows - 1)), lim_low = keys_seen(q, 0);
     uint4 raw[NR][D / 32];                     // elements (D / 4) t .. of rows g and g + 8
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const int row = row_base + 8 * n + g, tok = p.by_G.of(row0 + row), head = kvh * p.G + (row0 + row) - tok * p.G;
+      const int row = 8 * n + g, tok = p.by_G.of(row), head = kvh * p.G + row - tok * p.G;
       const uint16_t* src = p.a.Q + (q.first + tok) * p.a.q_stride + head * D + (D / 4) * t;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) raw[n][i] = row < it.rows ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
     }
     int first;
     const int n_steps = seg.template stages<L, kKeys>(p, first);
-    const int s0 = first + phase, s1 = min(first + n_steps, (lim_top + kKeys - 1) / kKeys);
-    const int steps = s1 > s0 ? (s1 - s0 + wk - 1) / wk : 0;
+    const int s0 = first + warp, s1 = min(first + n_steps, (lim_top + kKeys - 1) / kKeys);
+    const int steps = s1 > s0 ? (s1 - s0 + kFewWarps - 1) / kFewWarps : 0;
     const int32_t* table = p.a.block_table + static_cast<int64_t>(seg.r) * p.a.max_blocks;
 
     // Lane i looks up piece i (16 keys) of a window of 32: its page, as the piece's place in the caches (16 D bytes
     // each: as many as memory can hold fit 32 bits), and the page's scales; the table of the window after it is on its
     // way, the scales of the one before it are kept for the steps that the copies are ahead.
-    const auto key_of = [&](int piece) { return (s0 + (piece / kPieces) * wk) * kKeys + 16 * (piece % kPieces); };
+    const auto key_of = [&](int piece) { return (s0 + (piece / kPieces) * kFewWarps) * kKeys + 16 * (piece % kPieces); };
     const auto table_at = [&](int base) {
       const int key = key_of(base + lane);
       return base + lane < steps * kPieces && key < q.len ? __ldg(table + (key >> p.log_page)) : 0;
@@ -598,8 +597,8 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         crow[2 * n + i] = F16 ? p.c : __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
-        const int mine = row_base + 8 * n + 2 * t + i;
-        lim[2 * n + i] = mine < it.rows ? keys_seen(q, p.by_G.of(row0 + mine)) : 0;
+        const int mine = 8 * n + 2 * t + i;
+        lim[2 * n + i] = mine < it.rows ? keys_seen(q, p.by_G.of(mine)) : 0;
       }
     }
 
@@ -626,7 +625,7 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
       copy_wait<kStages - 1>();
       __syncwarp();                            // all lanes' copies are there
       const uint8_t *k_at = sm.ring[warp][j % kStages][0], *v_at = sm.ring[warp][j % kStages][1];
-      const int key0 = (s0 + j * wk) * kKeys;
+      const int key0 = (s0 + j * kFewWarps) * kKeys;
       {
         // S^T = K Q^T: s[h][n][0 .. 1] the key of row g, query rows 2 t, 2 t + 1; s[h][n][2 .. 3] that of row g + 8
         float s[kPieces][NR][4];
@@ -756,7 +755,7 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
     }
     copy_wait<0>();
 
-    // ------------------------------------------------------------------ the warps of a row tile
+    // ------------------------------------------------------------------ the warps' outputs
     __syncthreads();                           // the ring becomes the outputs' place
 #pragma unroll
     for (int i = 0; i < R2; ++i) {
@@ -778,7 +777,7 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
     seg.ctas(place.share, c0, c1);
     const auto finish = [&](int row, int col, const float4& o, float top, float total) {
       const float inv = total == 0.f ? 0.f : 1.f / total;
-      const int tok = p.by_G.of(row0 + row), head = kvh * p.G + (row0 + row) - tok * p.G;
+      const int tok = p.by_G.of(row), head = kvh * p.G + row - tok * p.G;
       const int64_t at_row = static_cast<int64_t>(q.first + tok) * p.a.Hq + head;
       *reinterpret_cast<uint2*>(p.a.O + at_row * D + col) =
           make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
@@ -787,19 +786,19 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
     };
     const int units = it.rows * (D / 4);       // four columns of a row
 #pragma unroll 1
-    for (int u = threadIdx.x; u < units; u += 32 * W) {
-      const int row = u / (D / 4), col = 4 * (u % (D / 4)), tile = row / (8 * NR), in = row % (8 * NR);
+    for (int u = threadIdx.x; u < units; u += L::kThreads) {
+      const int row = u / (D / 4), col = 4 * (u % (D / 4));
       float top = -INFINITY, total = 0.f;
-#pragma unroll 4
-      for (int w = tile; w < W; w += mt) top = fmaxf(top, sm.ml[w][in].x);
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sm.ml[w][row].x);
       const float ref = top == -INFINITY ? 0.f : top;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int w = tile; w < W; w += mt) {
-        const float2 ml = sm.ml[w][in];
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float2 ml = sm.ml[w][row];
         const float f = exp2_approx(ml.x - ref);
         total = fmaf(ml.y, f, total);
-        const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][in][col]);
+        const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][row][col]);
         o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
       }
       if (whole) {
@@ -829,9 +828,9 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
       }
       while (mine) {
         // P neighbouring threads take a unit's segments in turn, eight at a time, so that few loads wait for others
-        const int parts = units * 8 <= 32 * W ? 8 : units * 4 <= 32 * W ? 4 : units * 2 <= 32 * W ? 2 : 1, part = threadIdx.x & (parts - 1);
+        const int parts = units * 8 <= L::kThreads ? 8 : units * 4 <= L::kThreads ? 4 : units * 2 <= L::kThreads ? 2 : 1, part = threadIdx.x & (parts - 1);
 #pragma unroll 1
-        for (int u0 = 0; u0 < units * parts; u0 += 32 * W) {
+        for (int u0 = 0; u0 < units * parts; u0 += L::kThreads) {
           const int u = min((u0 + static_cast<int>(threadIdx.x)) / parts, units - 1), row = u / (D / 4), col = 4 * (u % (D / 4));
           const auto slot = [&](int i) {
             const int c = first + i * step;
@@ -876,14 +875,14 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
               finish(row, col, o, top, total);
             } else {
               *reinterpret_cast<float4*>(p.po + slot(0) * D + col) = o;
-              if (col == 0) sm.ml[row / (8 * NR)][row % (8 * NR)] = make_float2(top, total);
+              if (col == 0) sm.ml[0][row] = make_float2(top, total);
             }
           }
         }
         if (final) break;
         __syncthreads();                       // all have read what the group's first CTA left
-        for (int row = threadIdx.x; row < it.rows; row += 32 * W)
-          p.ml[(2ll * first + (first == c0 ? 1 : 0)) * L::kRows + row] = sm.ml[row / (8 * NR)][row % (8 * NR)];
+        for (int row = threadIdx.x; row < it.rows; row += L::kThreads)
+          p.ml[(2ll * first + (first == c0 ? 1 : 0)) * L::kRows + row] = sm.ml[0][row];
         first = c0, step = kGroup, n = (segments + kGroup - 1) / kGroup, final = true;
         mine = last(p.count + c0, n);
       }
@@ -895,7 +894,8 @@ __global__ void __launch_bounds__(32 * W, few_warps(NR) / W) k_attn_e4m3(const _
 // ------------------------------------------------------------------------------- many rows
 // Items of up to 256 rows on the tensor cores (tcgen05).  Two lanes of 128 rows, each with its own output and two
 // buffers of scores in tensor memory, its own warp that issues the products and its own four softmax warps, a row a
-// thread; both see every key tile.  A tile's codes come by TMA (128-byte swizzle), four warps widen them to fp16 tiles,
+// thread.  With more than 128 rows in the item both lanes see every key tile; with up to 128 both have the same rows and
+// take the tiles in turn, and the first adds up the outputs (in one lane of tensor memory a row has both).  A tile's codes come by TMA (128-byte swizzle), four warps widen them to fp16 tiles,
 // K first, and the tiles serve both lanes:
 //   S = Q K^T       both operands from shared memory; the softmax warps put Q there, in fp16
 //   W = 2^(x - m)   written over S in tensor memory, fp16
@@ -918,7 +918,8 @@ struct ManySmem {
   uint64_t raw_full[kRawStages], raw_empty[kRawStages];
   uint64_t full[2][kWideStages], empty[2][kWideStages];
   uint64_t q_full[2], q_empty[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
-  uint64_t seg_full[kSegments], seg_empty[kSegments];
+  float2 ml[128];                              // the second lane's statistics, where it has the first one's rows
+  uint64_t seg_full[kSegments], seg_empty[kSegments], meet;
   Segment seg[kSegments];
   uint16_t scales[kScaleRing][4];
   int last, failed;
@@ -930,6 +931,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+
+// The key tiles of an item of n tiles that lane l takes.
+struct Turns {
+  int first, step, n;
+  __device__ Turns(int rows, int n_, int l) : first(rows > 128 ? 0 : l), step(rows > 128 ? 1 : 2), n(n_) {}
+  __device__ bool mine(int j) const { return step == 1 || ((j ^ first) & 1) == 0; }
+  __device__ bool any() const { return first < n; }
+};
 
 template <bool F16, int D>
 __global__ void __launch_bounds__(kManyThreads, 1)
@@ -950,6 +959,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(&sm.pv_done[i], 1), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.o_empty[i], 4), mbar_init(&sm.drain[i], 1);
     }
     for (int i = 0; i < kSegments; ++i) mbar_init(&sm.seg_full[i], 1), mbar_init(&sm.seg_empty[i], kWWalk);
+    mbar_init(&sm.meet, kWWiden);
     sm.failed = 0;
     fence_barrier_init();
   }
@@ -1066,16 +1076,18 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       while (const Segment* x = segment(0)) {
         int first;
         const int n = x->stages<L, kTile>(p, first);
-        // Every place of the rings is waited for and given back by both lanes, also where one has no rows: a wait
-        // by parity is only sound if no phase is left out.
-        const bool mine = l == 0 || x->it.rows > 128;
-        if (mine && n > 0) ok = stage_wait(&sm.q_full[l], items & 1, &sm.failed, kErrWaitFull);
+        // Every place of the rings is waited for and given back by both lanes, also where only the other one uses it: a
+        // wait by parity is only sound if no phase is left out.
+        const Turns turns(x->it.rows, n, l);
+        // S runs ahead by two tiles of the lane's own: the next two, or two of the next three
+        const int ahead = turns.step == 1 ? 2 : 3;
+        if (turns.any()) ok = stage_wait(&sm.q_full[l], items & 1, &sm.failed, kErrWaitFull);
         const auto qk = [&](int j) {
           const uint32_t sl = k_tile % kWideStages;
           ok = stage_wait(&sm.full[0][sl], (k_tile / kWideStages) & 1, &sm.failed, kErrWaitFull);
           if (!ok) return;
           ++k_tile;
-          if (!mine) {
+          if (!turns.mine(j)) {
             if (lane == 0) mbar_arrive(&sm.empty[0][sl]);
             __syncwarp();
             return;
@@ -1090,7 +1102,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                             id_qk, k ? 1u : 0u);
             tc_commit(&sm.s_full[l][b]);
             tc_commit(&sm.empty[0][sl]);
-            if (j + 1 == n) tc_commit(&sm.q_empty[l]);
+            if (j + turns.step >= n) tc_commit(&sm.q_empty[l]);
           }
           __syncwarp();
           ++s_cnt;
@@ -1100,13 +1112,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           ok = stage_wait(&sm.full[1][sl], (v_tile / kWideStages) & 1, &sm.failed, kErrWaitFull);
           if (!ok) return;
           ++v_tile;
-          if (!mine) {
+          if (!turns.mine(j)) {
             if (lane == 0) mbar_arrive(&sm.empty[1][sl]);
             __syncwarp();
             return;
           }
           // first: the lane's previous item has left the output columns
-          if (j == 0) ok = stage_wait(&sm.o_empty[l], (items & 1) ^ 1, &sm.failed, kErrWaitAccum);
+          const bool begins = j == turns.first;
+          if (begins) ok = stage_wait(&sm.o_empty[l], (items & 1) ^ 1, &sm.failed, kErrWaitAccum);
           const uint32_t b = p_cnt & 1, t = t_s + 64 * b;
           ok = ok && stage_wait(&sm.p_full[l][b], (p_cnt >> 1) & 1, &sm.failed, kErrWaitFull);
           if (!ok) return;
@@ -1114,21 +1127,21 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) tc_mma_ts(t_o, t + 8 * k, vd + ((k * 2048) >> 4), id_wv, (j == 0 && k == 0) ? 0u : 1u);
+            for (int k = 0; k < kTile / 16; ++k) tc_mma_ts(t_o, t + 8 * k, vd + ((k * 2048) >> 4), id_wv, (begins && k == 0) ? 0u : 1u);
             tc_commit(&sm.pv_done[l]);
-            if (j + 1 == n) tc_commit(&sm.o_full[l]);
+            if (j + turns.step >= n) tc_commit(&sm.o_full[l]);
             tc_commit(&sm.empty[1][sl]);
           }
           __syncwarp();
           ++p_cnt;
         };
 #pragma unroll 1
-        for (int j = 0; j < n + 2 && ok; ++j) {
-          if (j >= 2) wv(j - 2);
+        for (int j = 0; j < n + ahead && ok; ++j) {
+          if (j >= ahead) wv(j - ahead);
           if (ok && j < n) qk(j);
         }
         if (!ok) break;
-        if (mine && n > 0) ++items;
+        if (turns.any()) ++items;
         segment_done();
       }
       // every product and commit of this warp (elect.sync names the same lane each time) has completed before tensor memory and barriers go
@@ -1146,14 +1159,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     uint32_t q_items = 0;                       // items of this lane whose Q is on its way
     // What this thread's row of a segment needs.
     struct Row {
-      bool mine, valid;                         // the lane has rows; this row is one
+      bool both, valid;                         // both lanes have the same rows; this row is one
       int tok, head, n, first;
       float c;                                  // scale * log2(e), times the power of two taken from the query
     };
     const auto row_of = [&](const Segment& x) {
       Row w;
-      const int row_item = 128 * l + row, row_all = x.tile * kManyRows + row_item;
-      w.mine = l == 0 || x.it.rows > 128, w.valid = row_item < x.it.rows;
+      w.both = x.it.rows <= 128;
+      const int row_item = w.both ? row : 128 * l + row, row_all = x.tile * kManyRows + row_item;
+      w.valid = row_item < x.it.rows;
       w.tok = p.by_G.of(row_all), w.head = x.head * p.G + row_all - w.tok * p.G;
       w.n = x.template stages<L, kTile>(p, w.first);
       w.c = p.c;
@@ -1162,7 +1176,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // Q to shared memory, and there to fp16, behind a power of two of the row where it is bf16.  Loops that stay
     // loops: code that runs once an item comes from L2, and unrolled it took 4 us an item.
     const auto put_q = [&](const Segment& x, Row& w) {
-      if (!w.mine || w.n == 0) return;
+      if (!Turns(x.it.rows, w.n, l).any()) return;
       constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;      // lanes a row, rows a copy of the warp
       uint8_t* const q = sm.q[l] + (warp & 3) * 32 * 128;       // the warp's 32 rows
       const auto place_of = [&](int to, int unit) { return (unit >> 3) * kQChunk + to * 128 + 16 * ((unit & 7) ^ (to & 7)); };
@@ -1206,19 +1220,27 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       if (lane == 0) mbar_arrive(&sm.q_full[l]);
       ++q_items;
     };
+    // All softmax warps meet, by a wait that is bounded as the others are: one that gave up leaves none behind.
+    uint32_t meets = 0;
+    const auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.meet);
+      ok = stage_wait(&sm.meet, meets++ & 1, &sm.failed, kErrWaitReduce) && ok;
+    };
     const Segment* seg = segment(0);
     Row w{};
     if (seg) w = row_of(*seg), put_q(*seg, w);
 #pragma unroll 1
     while (seg) {
       const Segment& x = *seg;
-      const int n = ok ? w.n : 0, first = w.first, row_item = 128 * l + row;
-      const bool mine = w.mine, valid = w.valid, active = __any_sync(0xffffffffu, valid);
+      const int n = ok ? w.n : 0, first = w.first;
+      const bool valid = w.valid, active = __any_sync(0xffffffffu, valid);
+      const Turns turns(x.it.rows, n, l);
       const int lim = valid ? keys_seen(x.q, w.tok) : 0;
       const float c = w.c;
       float m = -INFINITY, sum = 0.f;           // m: the largest x, in units of log2
 #pragma unroll 1
-      for (int j = 0; j < n && ok && mine; ++j, ++cnt) {
+      for (int j = turns.first; j < n && ok; j += turns.step, ++cnt) {
         const int key0 = (first + j) * kTile;
         const uint32_t b = cnt & 1, t_s = tmem + lane_base + 128 * l + 64 * b, at = tile + j;
         ok = stage_wait(&sm.s_full[l][b], (cnt >> 1) & 1, &sm.failed, kErrWaitAccum);
@@ -1260,7 +1282,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             const float keep = grow ? exp2_approx(m - top) : 1.f;
             if (grow) m = top;
             sum *= keep;
-            if (j > 0) {
+            if (j != turns.first) {
               // the lane's last product has left the output (one phase at most is outstanding: this tile's S was
               // issued after the product before that one)
               ok = stage_wait(&sm.pv_done[l], (cnt - 1) & 1, &sm.failed, kErrWaitAccum);
@@ -1311,22 +1333,27 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const Row done = w;
       if (next) w = row_of(*next), put_q(*next, w);
       // ------------------------------------------------------------------ the segment's output
-      uint32_t o[D / 32][32];
-      if (mine && n > 0 && ok) {
+      bool out = valid;                         // this thread has a row's output
+      const int row_item = done.both ? row : 128 * l + row;
+      const bool had = turns.any() && ok;
+      if (had) {
         ok = stage_wait(&sm.o_full[l], items & 1, &sm.failed, kErrWaitAccum);
         tc_fence_after();
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) tmem_ld32(t_o + 32 * q, o[q]);
-        tc_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_empty[l]);
         ++items;
-      } else {
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[q][e] = 0;
+      }
+      float f0 = 1.f, f1 = 0.f;                 // of this lane's output, and of the second lane's
+      if (done.both) {                          // the first lane adds up both
+        if (l == 1) sm.ml[row] = make_float2(m, sum);
+        tc_fence_before();
+        meet();
+        tc_fence_after();
+        out = valid && l == 0;
+        if (l == 0) {
+          const float2 other = sm.ml[row];
+          const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+          f0 = exp2_approx(m - ref), f1 = exp2_approx(other.x - ref);
+          sum = fmaf(other.y, f1, sum * f0), m = top;
+        }
       }
       const int64_t at_row = static_cast<int64_t>(x.q.first + done.tok) * p.a.Hq + done.head;
       // 32 columns of the row, given as the sums' bits
@@ -1342,32 +1369,57 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (p.a.lse)
           p.a.lse[at_row] = total == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) - kUp + log2f(total)) * 0.6931471805599453f;
       };
-      if (x.whole()) {
-        if (valid) {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      int c0, c1;
+      x.ctas(place.share, c0, c1);
+      // partials [cta][2][d / 4][256 rows][4]: a warp writes and reads whole lines
+      const auto slot = [&](int at) { return 2ll * at + (at == c0 ? 1 : 0); };
+      const auto part = [&](int at) { return reinterpret_cast<float4*>(p.po) + slot(at) * (D / 4) * kManyRows + row_item; };
+      const auto put_part = [&](int at, int q, const uint32_t (&o)[32]) {
+        float4* po = part(at) + 8 * q * kManyRows;
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) finish(q, o[q], inv);
-          finish_lse(m, sum);
-        }
-      } else {
-        int c0, c1;
-        x.ctas(place.share, c0, c1);
-        // partials [cta][2][d / 4][256 rows][4]: a warp writes and reads whole lines
-        const auto slot = [&](int at) { return 2ll * at + (at == c0 ? 1 : 0); };
-        const auto part = [&](int at) { return reinterpret_cast<float4*>(p.po) + slot(at) * (D / 4) * kManyRows + row_item; };
-        if (valid) {
-          float4* po = part(blockIdx.x);
+        for (int e = 0; e < 8; ++e)
+          po[e * kManyRows] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                          __uint_as_float(o[4 * e + 3]));
+      };
+      const bool whole = x.whole();
+      if (__any_sync(0xffffffffu, out)) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          if (n > 0) tmem_ld32(t_o + 32 * q, o);
+          if (done.both && n > 1) {
+            uint32_t o1[32];
+            tmem_ld32(t_o + 128 + 32 * q, o1);
+            tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e)
-            po[e * kManyRows] = make_float4(__uint_as_float(o[e >> 3][4 * (e & 7)]), __uint_as_float(o[e >> 3][4 * (e & 7) + 1]),
-                                            __uint_as_float(o[e >> 3][4 * (e & 7) + 2]), __uint_as_float(o[e >> 3][4 * (e & 7) + 3]));
-          p.ml[slot(blockIdx.x) * kManyRows + row_item] = make_float2(m, sum);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e]) * f0));
+          } else if (n > 0) {
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0;
+          }
+          if (out) {
+            if (whole) finish(q, o, inv);
+            else put_part(blockIdx.x, q, o);
+          }
         }
+        if (out) {
+          if (whole) finish_lse(m, sum);
+          else p.ml[slot(blockIdx.x) * kManyRows + row_item] = make_float2(m, sum);
+        }
+      }
+      tc_fence_before();
+      if (done.both) meet();                    // the first lane has read the second one's
+      else __syncwarp();
+      if (had && lane == 0) mbar_arrive(&sm.o_empty[l]);
+      if (!whole) {
         const int segments = c1 - c0 + 1, cta = blockIdx.x;
         const auto last = [&](int* count, int n) {
-          named_bar_sync(1, 256);
+          meet();
           if (threadIdx.x == 0) sm.last = last_segment(count, n);
-          named_bar_sync(1, 256);
+          meet();
           return sm.last != 0;
         };
         int first = c0, step = 1, n_parts = segments;
@@ -1379,7 +1431,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           joins = last(p.count + c0, n_parts);
         }
         while (joins) {
-          if (valid) {                         // a row's partials are read and written by its thread alone
+          if (out) {                           // a row's partials are read and written by its thread alone
             float top = -INFINITY, total = 0.f;
 #pragma unroll 4
             for (int i = 0; i < n_parts; ++i) top = fmaxf(top, __ldcg(&p.ml[slot(first + i * step) * kManyRows + row_item].x));
@@ -1422,11 +1474,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               if (final) {
                 finish(q, sums, inv);
               } else {
-                float4* po = part(first) + 8 * q * kManyRows;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  po[e * kManyRows] = make_float4(__uint_as_float(sums[4 * e]), __uint_as_float(sums[4 * e + 1]), __uint_as_float(sums[4 * e + 2]),
-                                                  __uint_as_float(sums[4 * e + 3]));
+                put_part(first, q, sums);
               }
             }
             if (final) finish_lse(top, total);
@@ -1449,7 +1497,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
 }
 
-constexpr int kFewMostRows = 64;       // of an item, either NR
 struct Layout {
   int sms;
   size_t po, ml, bytes;
@@ -1464,9 +1511,9 @@ Layout layout(int64_t d) {
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  // two segments of each CTA: up to four an SM with items of up to 64 rows, one with 256
-  const size_t slots = static_cast<size_t>(l.sms) * 2 * 4 * kFewMostRows;
-  static_assert(4 * kFewMostRows == kManyRows, "both kernels' segments");
+  // two segments of each CTA: up to four an SM with items of up to 16 rows, one with 256
+  const size_t slots = static_cast<size_t>(l.sms) * 2 * kManyRows;
+  static_assert(4 * kFewMostRows <= kManyRows, "both kernels' segments");
   l.po = take(slots * d * sizeof(float));
   l.ml = take(slots * sizeof(float2));
   l.bytes = off;
@@ -1483,14 +1530,14 @@ cudaError_t cache_map(CUtensorMap* map, const uint8_t* cache, const AttnE4m3Args
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
-template <bool F16, int D, int NR, int W>
+template <bool F16, int D, int NR>
 cudaError_t launch_few(const Params& p, const Layout& l, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(FewSmem<D, NR, W>);
-  constexpr int ctas = few_warps(NR) / W;
-  static_assert(ctas * (smem + 1024 + 256) <= 227 * 1024, "CTAs of the kernel for few rows do not fit an SM");
-  const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(k_attn_e4m3<F16, D, NR, W>), smem);
+  constexpr size_t smem = sizeof(FewSmem<D, NR>);
+  constexpr int ctas = few_ctas(NR);
+  static_assert(ctas * (smem + 1024 + 1024) <= 227 * 1024, "CTAs of the kernel for few rows do not fit an SM");
+  const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(k_attn_e4m3<F16, D, NR>), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_attn_e4m3<F16, D, NR, W>, dim3(l.sms * ctas), 32 * W, smem, stream, p);
+  return launch_pdl(k_attn_e4m3<F16, D, NR>, dim3(l.sms * ctas), FewLine<NR>::kThreads, smem, stream, p);
 }
 
 template <bool F16, int D>
@@ -1518,14 +1565,14 @@ cudaError_t launch_t(const AttnE4m3Args& a, uint8_t* ws, cudaStream_t stream) {
   p.c = a.scale * 1.4426950408889634f;
   p.count = reinterpret_cast<int*>(ws);        // the header's counters: zero, and left so
   p.po = reinterpret_cast<float*>(ws + l.po), p.ml = reinterpret_cast<float2*>(ws + l.ml);
-  // A request of more rows than a CTA's warps have is the tensor cores'; others in the same call stay with the first kernel.
-  p.few = kFewMostRows;
+  // Requests of up to 16 rows a head, or of up to 8 where a call also has longer ones and a single token's rows are no
+  // more (the decoding requests beside prompts), go to the first kernel.  First / second kernel, G = 8, in us: FIGURES.
+  p.few = rows <= kFewMostRows || p.G > 8 ? kFewMostRows : 8;
   if (rows > kFewMostRows) {
     const cudaError_t e = launch_many<F16, D>(p, l, stream);
     if (e != cudaSuccess) return e;
   }
-  if (rows <= 8) return launch_few<F16, D, 1, 4>(p, l, stream);
-  return launch_few<F16, D, 2, 4>(p, l, stream);
+  return std::min<int64_t>(rows, p.few) <= 8 ? launch_few<F16, D, 1>(p, l, stream) : launch_few<F16, D, 2>(p, l, stream);
 }
 
 }  // namespace
