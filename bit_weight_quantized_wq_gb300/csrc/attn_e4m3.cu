@@ -15,7 +15,7 @@
 // item (a segment) goes to the workspace, unnormalised, and the last CTA that is done with the item
 // joins its segments in line order.  A CTA has two such segments at most, its first and its last.
 //
-// Few rows (k_attn_e4m3): a warp has 8 NR rows of the item (its row tile), and the warps of a row tile take the
+// Few rows (k_attn_e4m3): a warp has 8 NR rows of the item (its row tile, one of two at most), and the warps of a row tile take the
 // steps of 16 keys (32 where d is 64) in turn, copied by the warp itself with cp.async two steps ahead: 512
 // contiguous bytes a copy, kept in that order but for a swizzle of the 16-byte chunks.  (With each thread copying what
 // it will read, in the fragments' order, a copy of 512 bytes took 26 passes of the shared memory instead of 4.)
@@ -100,12 +100,13 @@ __device__ __forceinline__ int keys_seen(const Request& q, int token) { return m
 
 // A line's items: their rows, the weight of a tile (by the item's rows) and the constant of an item.
 // Weights are in units of some 20 cycles of an SM.
-constexpr int kFewMostRows = 16;       // of a request's head in the kernel for few rows
+constexpr int kFewMostRows = 32;       // of a request's head in the kernel for few rows
 template <int NR>
 struct FewLine {
   __device__ static bool takes(const Params& p, int rows) { return rows <= p.few; }
-  static constexpr int kThreads = 32 * kFewWarps, kRows = 8 * NR, kItem = 60, kMost = 8;
-  __device__ static int weight(int) { return kMost; }
+  // eight rows a warp: one row tile; sixteen: two, each with half of the warps
+  static constexpr int kThreads = 32 * kFewWarps, kRows = NR == 1 ? 8 : 32, kItem = 60, kMost = NR == 1 ? 8 : 12;
+  __device__ static int weight(int rows) { return rows <= 8 * NR ? 8 : kMost; }
 };
 
 constexpr int kManyThreads = 512, kManyRows = 256;
@@ -505,26 +506,29 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
     const Request& q = seg.q;
     const Shape& it = seg.it;
     const int kvh = seg.head;
-    // the most keys that a row sees, and the fewest
-    const int lim_top = keys_seen(q, p.by_G.of(it.rows - 1)), lim_low = keys_seen(q, 0);
+    // ------------------------------------------------------------------ this warp's rows
+    const int mt = NR > 1 && it.rows > 8 * NR ? 2 : 1, wk = kFewWarps / mt;
+    const int row_base = (warp & (mt - 1)) * 8 * NR, phase = warp / mt;
+    // the most keys that a row of the warp sees, and the fewest
+    const int lim_top = keys_seen(q, p.by_G.of(min(it.rows, row_base + 8 * NR) - 1)), lim_low = keys_seen(q, p.by_G.of(row_base));
     uint4 raw[NR][D / 32];                     // elements (D / 4) t .. of rows g and g + 8
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const int row = 8 * n + g, tok = p.by_G.of(row), head = kvh * p.G + row - tok * p.G;
+      const int row = row_base + 8 * n + g, tok = p.by_G.of(row), head = kvh * p.G + row - tok * p.G;
       const uint16_t* src = p.a.Q + (q.first + tok) * p.a.q_stride + head * D + (D / 4) * t;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) raw[n][i] = row < it.rows ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
     }
     int first;
     const int n_steps = seg.template stages<L, kKeys>(p, first);
-    const int s0 = first + warp, s1 = min(first + n_steps, (lim_top + kKeys - 1) / kKeys);
-    const int steps = s1 > s0 ? (s1 - s0 + kFewWarps - 1) / kFewWarps : 0;
+    const int s0 = first + phase, s1 = min(first + n_steps, (lim_top + kKeys - 1) / kKeys);
+    const int steps = s1 > s0 ? (s1 - s0 + wk - 1) / wk : 0;
     const int32_t* table = p.a.block_table + static_cast<int64_t>(seg.r) * p.a.max_blocks;
 
     // Lane i looks up piece i (16 keys) of a window of 32: its page, as the piece's place in the caches (16 D bytes
     // each: as many as memory can hold fit 32 bits), and the page's scales; the table of the window after it is on its
     // way, the scales of the one before it are kept for the steps that the copies are ahead.
-    const auto key_of = [&](int piece) { return (s0 + (piece / kPieces) * kFewWarps) * kKeys + 16 * (piece % kPieces); };
+    const auto key_of = [&](int piece) { return (s0 + (piece / kPieces) * wk) * kKeys + 16 * (piece % kPieces); };
     const auto table_at = [&](int base) {
       const int key = key_of(base + lane);
       return base + lane < steps * kPieces && key < q.len ? __ldg(table + (key >> p.log_page)) : 0;
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         crow[2 * n + i] = F16 ? p.c : __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
-        const int mine = 8 * n + 2 * t + i;
+        const int mine = row_base + 8 * n + 2 * t + i;
         lim[2 * n + i] = mine < it.rows ? keys_seen(q, p.by_G.of(mine)) : 0;
       }
     }
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
       copy_wait<kStages - 1>();
       __syncwarp();                            // all lanes' copies are there
       const uint8_t *k_at = sm.ring[warp][j % kStages][0], *v_at = sm.ring[warp][j % kStages][1];
-      const int key0 = (s0 + j * kFewWarps) * kKeys;
+      const int key0 = (s0 + j * wk) * kKeys;
       {
         // S^T = K Q^T: s[h][n][0 .. 1] the key of row g, query rows 2 t, 2 t + 1; s[h][n][2 .. 3] that of row g + 8
         float s[kPieces][NR][4];
@@ -787,18 +791,20 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
     const int units = it.rows * (D / 4);       // four columns of a row
 #pragma unroll 1
     for (int u = threadIdx.x; u < units; u += L::kThreads) {
-      const int row = u / (D / 4), col = 4 * (u % (D / 4));
+      const int row = u / (D / 4), col = 4 * (u % (D / 4)), tile = row / (8 * NR), in = row % (8 * NR);
       float top = -INFINITY, total = 0.f;
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sm.ml[w][row].x);
+      for (int w = 0; w < kFewWarps; ++w)
+        if ((w & (mt - 1)) == tile) top = fmaxf(top, sm.ml[w][in].x);
       const float ref = top == -INFINITY ? 0.f : top;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) {
-        const float2 ml = sm.ml[w][row];
+        if ((w & (mt - 1)) != tile) continue;
+        const float2 ml = sm.ml[w][in];
         const float f = exp2_approx(ml.x - ref);
         total = fmaf(ml.y, f, total);
-        const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][row][col]);
+        const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][in][col]);
         o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
       }
       if (whole) {
@@ -875,14 +881,14 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
               finish(row, col, o, top, total);
             } else {
               *reinterpret_cast<float4*>(p.po + slot(0) * D + col) = o;
-              if (col == 0) sm.ml[0][row] = make_float2(top, total);
+              if (col == 0) sm.ml[row / (8 * NR)][row % (8 * NR)] = make_float2(top, total);
             }
           }
         }
         if (final) break;
         __syncthreads();                       // all have read what the group's first CTA left
         for (int row = threadIdx.x; row < it.rows; row += L::kThreads)
-          p.ml[(2ll * first + (first == c0 ? 1 : 0)) * L::kRows + row] = sm.ml[0][row];
+          p.ml[(2ll * first + (first == c0 ? 1 : 0)) * L::kRows + row] = sm.ml[row / (8 * NR)][row % (8 * NR)];
         first = c0, step = kGroup, n = (segments + kGroup - 1) / kGroup, final = true;
         mine = last(p.count + c0, n);
       }
@@ -953,7 +959,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRawStages; ++i) mbar_init(&sm.raw_full[i], 1), mbar_init(&sm.raw_empty[i], 4);
     for (int i = 0; i < 2; ++i) {
-      for (int s = 0; s < kWideStages; ++s) mbar_init(&sm.full[i][s], 4), mbar_init(&sm.empty[i][s], 2);
+      for (int s = 0; s < kWideStages; ++s) mbar_init(&sm.full[i][s], 2), mbar_init(&sm.empty[i][s], 2);
       mbar_init(&sm.q_full[i], 4), mbar_init(&sm.q_empty[i], 1);
       for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[i][b], 1), mbar_init(&sm.p_full[i][b], 4);
       mbar_init(&sm.pv_done[i], 1), mbar_init(&sm.o_full[i], 1), mbar_init(&sm.o_empty[i], 4), mbar_init(&sm.drain[i], 1);
@@ -1019,10 +1025,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                                           [&](uint32_t i) { return sm.scales[i % kScaleRing]; }, &sm.failed);
     } else if (warp < kWMma) {
       // ------------------------------------------------------------------ codes -> fp16
-      // A thread widens 16 codes at a time.  Eight lanes have four chunks each of two keys, chosen (k and k ^ 5, or
-      // k ^ 1 where d is 64) so that what they read and what they write falls on all banks.
-      constexpr int kUnits = kTile * D / 16 / 128;      // of a thread
-      const int u0 = threadIdx.x - 32 * kWWiden;
+      // Two warps widen K, two V, so that neither waits for the other's barriers.  A thread widens 16 codes at a time, of
+      // keys 16 apart.  Eight lanes have four chunks each of two keys, chosen (k and k ^ 5, or k ^ 1 where d is 64) so
+      // that what they read and what they write falls on all banks.
+      const int v = (warp - kWWiden) >> 1, u = threadIdx.x & 63, chunk = u & 3;
+      const int key = (2 * (u >> 3)) ^ (((u >> 2) & 1) * (D == 128 ? 5 : 1));    // 0 .. 15
+      const uint32_t from = chunk_at<D>(key, chunk), to = 128 * key + 16 * ((2 * chunk) ^ (key & 7));
       uint32_t tile = 0;
       while (const Segment* x = segment(0)) {
         int first;
@@ -1031,33 +1039,32 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         for (int j = 0; j < n && ok; ++j, ++tile) {
           const uint32_t rs = tile % kRawStages, ws = tile % kWideStages;
           ok = stage_wait(&sm.raw_full[rs], (tile / kRawStages) & 1, &sm.failed, kErrWaitFull);
-          const int left = len - (first + j) * kTile;   // keys of the request in the tile
-#pragma unroll 1
-          for (int v = 0; v < 2 && ok; ++v) {
-            uint4 c[kUnits];
-            int key[kUnits], plane[kUnits];
+          ok = ok && stage_wait(&sm.empty[v][ws], ((tile / kWideStages) & 1) ^ 1, &sm.failed, kErrWaitEmpty);
+          if (!ok) break;
+          const uint8_t* src = sm.raw[rs][v];
+          uint8_t* dst = sm.wide[v][ws];
+          const int left = len - (first + j) * kTile;
+          const bool tail = v && left < kTile;          // V's places behind the tokens hold anything: zeros
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
-              const int u = u0 + 128 * i, chunk = u & 3, sel = (u >> 2) & 1, pair = (u >> 3) & 31;
-              plane[i] = u >> 8;
-              key[i] = (2 * pair) ^ (sel * (D == 128 ? 5 : 1));
-              c[i] = *reinterpret_cast<const uint4*>(sm.raw[rs][v] + chunk_at<D>(key[i], 4 * plane[i] + chunk));
-              if (v && key[i] >= left) c[i] = make_uint4(0, 0, 0, 0);      // places behind the tokens hold anything
-            }
-            ok = stage_wait(&sm.empty[v][ws], ((tile / kWideStages) & 1) ^ 1, &sm.failed, kErrWaitEmpty);
-            if (!ok) break;
+          for (int plane = 0; plane < CH; ++plane) {
+            uint4 c[4];
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
-              uint8_t* dst = sm.wide[v][ws] + plane[i] * kKvChunk + key[i] * 128;
-              const int unit = 2 * (u0 & 3), swap = key[i] & 7;
-              *reinterpret_cast<uint4*>(dst + 16 * (unit ^ swap)) = make_uint4(e4m3_low(c[i].x), e4m3_high(c[i].x), e4m3_low(c[i].y), e4m3_high(c[i].y));
-              *reinterpret_cast<uint4*>(dst + 16 * ((unit + 1) ^ swap)) = make_uint4(e4m3_low(c[i].z), e4m3_high(c[i].z), e4m3_low(c[i].w), e4m3_high(c[i].w));
+            for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(src + (from ^ (64 * plane)) + 16 * D * i);
+            if (__builtin_expect(tail, 0)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (key + 16 * i >= left) c[i] = make_uint4(0, 0, 0, 0);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.full[v][ws]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint8_t* at = dst + plane * kKvChunk + 2048 * i;
+              *reinterpret_cast<uint4*>(at + to) = make_uint4(e4m3_low(c[i].x), e4m3_high(c[i].x), e4m3_low(c[i].y), e4m3_high(c[i].y));
+              *reinterpret_cast<uint4*>(at + (to ^ 16)) = make_uint4(e4m3_low(c[i].z), e4m3_high(c[i].z), e4m3_low(c[i].w), e4m3_high(c[i].w));
+            }
           }
-          if (ok && lane == 0) mbar_arrive(&sm.raw_empty[rs]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.full[v][ws]), mbar_arrive(&sm.raw_empty[rs]);
         }
         if (!ok) break;
         segment_done();
@@ -1511,7 +1518,7 @@ Layout layout(int64_t d) {
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  // two segments of each CTA: up to four an SM with items of up to 16 rows, one with 256
+  // two segments of each CTA: up to four an SM with items of up to 32 rows, one with 256
   const size_t slots = static_cast<size_t>(l.sms) * 2 * kManyRows;
   static_assert(4 * kFewMostRows <= kManyRows, "both kernels' segments");
   l.po = take(slots * d * sizeof(float));
@@ -1565,8 +1572,10 @@ cudaError_t launch_t(const AttnE4m3Args& a, uint8_t* ws, cudaStream_t stream) {
   p.c = a.scale * 1.4426950408889634f;
   p.count = reinterpret_cast<int*>(ws);        // the header's counters: zero, and left so
   p.po = reinterpret_cast<float*>(ws + l.po), p.ml = reinterpret_cast<float2*>(ws + l.ml);
-  // Requests of up to 16 rows a head, or of up to 8 where a call also has longer ones and a single token's rows are no
-  // more (the decoding requests beside prompts), go to the first kernel.  First / second kernel, G = 8, in us: FIGURES.
+  // Requests of up to 32 rows a head, or of up to 8 where a call also has longer ones and a single token's rows are no
+  // more (the decoding requests beside prompts), go to the first kernel.  First / second kernel, 64 heads of 128 on 8, in
+  // us: 4 requests over up to 40000 keys, 3 new tokens 58 / 73, 4 63 / 73, 6 103 / 73, 8 114 / 72; 48 requests over up to
+  // 4096, 3 70 / 93, 4 77 / 92, 6 124 / 93; heads of 64, 3 39 / 77, 4 42 / 78, 6 66 / 77, 8 73 / 77.
   p.few = rows <= kFewMostRows || p.G > 8 ? kFewMostRows : 8;
   if (rows > kFewMostRows) {
     const cudaError_t e = launch_many<F16, D>(p, l, stream);
