@@ -10,6 +10,7 @@
 // written token by token holds what one written at once holds, but for those steps.  (A free float32
 // scale rounds every code again at each growth.)
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv_e4m3.cuh"
@@ -48,11 +49,35 @@ __device__ __forceinline__ int touched_pages(const KvAppendArgs& a, int r, int& 
   return ((len - 1) >> a.log_page) - ((len - n) >> a.log_page) + 1;
 }
 
-// The index-th page that the call writes, in the order of the requests.  All threads of the CTA.
-__device__ __forceinline__ Touched find_touched(const KvAppendArgs& a, int index) {
+// Request r's index-th page of those that the call writes.
+__device__ __forceinline__ Touched touched_page(const KvAppendArgs& a, int r, int first, int n, int len, int index) {
+  Touched u;
+  const int start = len - n, block = (start >> a.log_page) + index, lo = max(start, block << a.log_page);
+  u.row = first + lo - start;
+  u.count = min(len, (block + 1) << a.log_page) - lo;
+  u.place = lo & (a.page_size - 1);
+  u.page = __ldg(a.block_table + static_cast<int64_t>(r) * a.max_blocks + block);
+  if (static_cast<uint32_t>(u.page) >= static_cast<uint32_t>(a.pages)) {
+    atomicOr(&g_kv_err, kErrIndex);
+    u.page = -1;
+  }
+  return u;
+}
+
+// The index-th page that the call writes.  With `each` pages for every request, whether it has them or not, each thread
+// finds it by itself; else the CTA counts them in the order of the requests.
+__device__ __forceinline__ Touched find_touched(const KvAppendArgs& a, int index, int each) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (each) {
+    const int r = each == 1 ? index : index / each, j = index - r * each;
+    int first, n, len;
+    bool bad;
+    const int c = touched_pages(a, r, first, n, len, bad);
+    if (bad) atomicOr(&g_kv_err, kErrIndex);
+    return j < c ? touched_page(a, r, first, n, len, j) : Touched{0, 0, 0, -1};
+  }
   __shared__ int sums[kAppendThreads / 32];
   __shared__ Touched out;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) out.page = -1;
   int before = 0;
   const bool checks = blockIdx.x == 0 && blockIdx.y == 0;    // one CTA looks at every request
@@ -78,16 +103,7 @@ __device__ __forceinline__ Touched find_touched(const KvAppendArgs& a, int index
       if (w < warp) at += sums[w];
       before += sums[w];
     }
-    if (at <= index && index < at + c) {
-      const int start = len - n, block = (start >> a.log_page) + index - at, lo = max(start, block << a.log_page);
-      out.row = first + lo - start;
-      out.count = min(len, (block + 1) << a.log_page) - lo;
-      out.place = lo & (a.page_size - 1);
-      const int page = __ldg(a.block_table + static_cast<int64_t>(r) * a.max_blocks + block);
-      const bool fine = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages);
-      if (!fine) atomicOr(&g_kv_err, kErrIndex);
-      out.page = fine ? page : -1;
-    }
+    if (at <= index && index < at + c) out = touched_page(a, r, first, n, len, index - at);
     __syncthreads();
   }
   return out;
@@ -104,13 +120,13 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // Bound by the bytes (2 read, 1 written an element) for prompts, by launch and dependent loads for
 // decoding (starts and lengths, then the page and the tokens).
 template <bool F16, int D, int N, int P>
-__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs a, int each) {
   constexpr int kRow = D / 8;                  // pieces a token
   constexpr uint32_t kInf = F16 ? 0x7c00u : 0x7f80u;
   __shared__ uint32_t tops[kAppendThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
-  const Touched u = find_touched(a, blockIdx.x);
+  const Touched u = find_touched(a, blockIdx.x, each);
   if (u.page < 0) return;
   const int unit = blockIdx.y * (kAppendThreads / N) + threadIdx.x / N, j = threadIdx.x % N;
   const bool on = unit < 2 * a.Hkv;            // with N = 128 always
@@ -194,28 +210,54 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs
 
 template <bool F16, int D>
 cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
-  const int64_t most = std::min<int64_t>(a.T, a.T / a.page_size + 2ll * a.R);      // pages that T tokens of R requests lie in
+  // pages that T tokens of R requests lie in, and that max_new tokens of one do
+  const int64_t most = std::min<int64_t>(a.T, a.T / a.page_size + 2ll * a.R);
+  const int one = 1 + (a.max_new + a.page_size - 2) / a.page_size;
+  // Where no request can have more than two, CTAs for as many each: 512 requests of one token 8.3 us counted, 6.0 so.
+  const int each = one <= 2 && static_cast<int64_t>(a.R) * one < 0x7fffffff ? one : 0;
+  const unsigned pages = static_cast<unsigned>(each ? a.R * one : most);
   const int pieces = std::min(a.page_size, a.max_new) * D / 8;
   if (pieces <= 4 * 32)
-    return launch_pdl(k_kv_append<F16, D, 32, 4>, dim3(static_cast<unsigned>(most), (2 * a.Hkv + 3) / 4), kAppendThreads, 0, stream, a);
-  const dim3 grid(static_cast<unsigned>(most), 2 * a.Hkv);
-  if (pieces <= 8 * 128) return launch_pdl(k_kv_append<F16, D, 128, 8>, grid, kAppendThreads, 0, stream, a);
-  return launch_pdl(k_kv_append<F16, D, 128, 16>, grid, kAppendThreads, 0, stream, a);
+    return launch_pdl(k_kv_append<F16, D, 32, 4>, dim3(pages, (2 * a.Hkv + 3) / 4), kAppendThreads, 0, stream, a, each);
+  const dim3 grid(pages, 2 * a.Hkv);
+  if (pieces <= 8 * 128) return launch_pdl(k_kv_append<F16, D, 128, 8>, grid, kAppendThreads, 0, stream, a, each);
+  return launch_pdl(k_kv_append<F16, D, 128, 16>, grid, kAppendThreads, 0, stream, a, each);
 }
 
 // ------------------------------------------------------------------------------- reading back
-constexpr int kReadThreads = 256, kReadTokens = 16, kReadAhead = 4;
+constexpr int kReadThreads = 256, kReadAhead = 2;
 
-// A CTA has 16 rows of the output, K or V; a thread 16 elements at a time (16 bytes in, 32 out).
-template <bool F16, int D>
+// Codes at scale byte `byte` as two packed elements of the output's type.  Most scales are exact in fp16 and reach no
+// infinity (2^-14 .. 2^7): one product there.
+template <bool F16>
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t f16x2, uint32_t byte, bool plain) {
+  if (F16 && plain) {
+    const __half2 s = __half2half2(__ushort_as_half(static_cast<uint16_t>((byte - kScaleBias + 15) << 10)));
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&f16x2), s);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+  const float s = scale_value(byte);
+  float2 f = unpack2<true>(f16x2);
+  f.x *= s, f.y *= s;
+  if (F16) {                                   // past the type's largest value: that value (NaN stays NaN)
+    if (fabsf(f.x) > 65504.f) f.x = copysignf(65504.f, f.x);
+    if (fabsf(f.y) > 65504.f) f.y = copysignf(65504.f, f.y);
+  }
+  return pack2<F16>(f.x, f.y);
+}
+
+// A CTA has TOK rows of the output, K or V; a thread 16 elements at a time (16 bytes in, 32 out).  Bound by reads and writes
+// of HBM mixed once its instructions are few: with divisions for every unit, and fp16 by way of float32 and a clamp, the
+// ALU was at 65% and 24 requests of up to 8191 tokens took 118 us.
+template <bool F16, int D, int TOK>
 __global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvReadArgs a) {
   constexpr int kPieces = D / 16;
-  __shared__ int64_t where[kReadTokens];       // of each row: its token of head 0, counted in tokens of the cache; -1: none
-  __shared__ int pages[kReadTokens];
+  __shared__ int64_t where[TOK];               // of each row: its token of head 0, counted in tokens of the cache; -1: none
+  __shared__ int pages[TOK], requests[TOK], places[TOK];
   pdl_launch_dependents();
   pdl_wait();
-  const int t0 = blockIdx.x * kReadTokens, count = min(kReadTokens, a.T - t0);
-  if (threadIdx.x < kReadTokens) where[threadIdx.x] = -1;
+  const int t0 = blockIdx.x * TOK, count = min(TOK, a.T - t0);
+  if (threadIdx.x < TOK) requests[threadIdx.x] = -1;
   __syncthreads();
   for (int r = threadIdx.x; r < a.R; r += kReadThreads) {
     const int lo = __ldg(a.starts + r), hi = __ldg(a.starts + r + 1);
@@ -223,54 +265,58 @@ __global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvReadArgs a) {
       if (blockIdx.x == 0) atomicOr(&g_kv_err, kErrIndex);
       continue;
     }
-    for (int t = max(lo, t0); t < min(hi, t0 + count); ++t) {
-      const int pos = t - lo, block = pos >> a.log_page;
+    for (int t = max(lo, t0); t < min(hi, t0 + count); ++t) requests[t - t0] = r, places[t - t0] = t - lo;
+  }
+  __syncthreads();
+  if (threadIdx.x < TOK) {
+    const int r = requests[threadIdx.x], pos = places[threadIdx.x], block = pos >> a.log_page;
+    int64_t at = -1;
+    if (r >= 0) {
       const int page = block < a.max_blocks ? __ldg(a.block_table + static_cast<int64_t>(r) * a.max_blocks + block) : -1;
-      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pages)) {
+      if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pages)) {
+        at = ((static_cast<int64_t>(page) * a.Hkv) << a.log_page) + (pos & (a.page_size - 1));
+        pages[threadIdx.x] = page;
+      } else {
         atomicOr(&g_kv_err, kErrIndex);
-        continue;
       }
-      pages[t - t0] = page;
-      where[t - t0] = ((static_cast<int64_t>(page) * a.Hkv) << a.log_page) + (pos & (a.page_size - 1));
     }
+    where[threadIdx.x] = at;
   }
   __syncthreads();
   const uint8_t* cache = blockIdx.y ? a.v_cache : a.k_cache;
   const uint8_t* scales = blockIdx.y ? a.v_scales : a.k_scales;
   uint16_t* out = (blockIdx.y ? a.Vo : a.Ko) + static_cast<int64_t>(t0) * a.Hkv * D;
   const int per_token = a.Hkv * kPieces, units = count * per_token;
+  const int step_t = kReadThreads / per_token, step_u = kReadThreads - step_t * per_token;
+  int t = threadIdx.x / per_token, u = threadIdx.x - t * per_token;      // the unit's token, and its place among the token's
   for (int base = threadIdx.x; base < units; base += kReadThreads * kReadAhead) {
     uint4 c[kReadAhead];
     uint32_t byte[kReadAhead];
     bool on[kReadAhead];
 #pragma unroll
     for (int i = 0; i < kReadAhead; ++i) {
-      const int u = base + i * kReadThreads, t = u / per_token, h = (u - t * per_token) / kPieces, piece = u % kPieces;
-      const int64_t at = u < units ? where[t] : -1;
+      const int h = u / kPieces;
+      const int64_t at = base + i * kReadThreads < units ? where[t] : -1;
       on[i] = at >= 0;
       c[i] = make_uint4(0, 0, 0, 0), byte[i] = kScaleBias;
       if (on[i]) {
-        c[i] = __ldg(reinterpret_cast<const uint4*>(cache + (at + (static_cast<int64_t>(h) << a.log_page)) * D) + piece);
+        c[i] = __ldg(reinterpret_cast<const uint4*>(cache + (at + (static_cast<int64_t>(h) << a.log_page)) * D) + u % kPieces);
         byte[i] = __ldg(scales + static_cast<int64_t>(pages[t]) * a.Hkv + h);
       }
+      t += step_t, u += step_u;
+      if (u >= per_token) u -= per_token, ++t;
     }
 #pragma unroll
     for (int i = 0; i < kReadAhead; ++i) {
       if (!on[i]) continue;
-      const float s = scale_value(byte[i]);
+      const bool plain = byte[i] - (kScaleBias - 14) <= 14 + 7;
       uint32_t w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t word = (&c[i].x)[k >> 1];
-        float2 f = unpack2<true>(k & 1 ? e4m3_high(word) : e4m3_low(word));
-        f.x *= s, f.y *= s;
-        if (F16) {                             // past the type's largest value: that value (NaN stays NaN)
-          if (fabsf(f.x) > 65504.f) f.x = copysignf(65504.f, f.x);
-          if (fabsf(f.y) > 65504.f) f.y = copysignf(65504.f, f.y);
-        }
-        w[k] = pack2<F16>(f.x, f.y);
+        w[k] = scaled_pair<F16>(k & 1 ? e4m3_high(word) : e4m3_low(word), byte[i], plain);
       }
-      uint4* dst = reinterpret_cast<uint4*>(out + static_cast<int64_t>(base + i * kReadThreads) * 16);
+      uint4* dst = reinterpret_cast<uint4*>(out) + 2ll * (base + i * kReadThreads);
       dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
       dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
@@ -279,7 +325,17 @@ __global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvReadArgs a) {
 
 template <bool F16, int D>
 cudaError_t launch_read_t(const KvReadArgs& a, cudaStream_t stream) {
-  return launch_pdl(k_kv_read<F16, D>, dim3((a.T + kReadTokens - 1) / kReadTokens, 2), kReadThreads, 0, stream, a);
+  // A CTA's threads have a unit each, so that a short call is over in one round of loads; 32 rows from 2^22 units on.
+  // 4 / 16 / 32 rows, 8 heads of 128 (64 units a row), in us: 1000 rows 4.0 / 5.2 / 8.3, 12000 16.8 / 18.1 / 24, 30000 40 /
+  // 39 / 43, 98000 116 / 109 / 102; 2 heads of 64 (8 units), 9000 rows 8.7 / 5.0 / 6.8, 45000 32 / 17.6 / 17.4.
+  const int per_row = a.Hkv * D / 16;
+  const auto read = [&](auto rows) {
+    constexpr int n = decltype(rows)::value;
+    return launch_pdl(k_kv_read<F16, D, n>, dim3((a.T + n - 1) / n, 2), kReadThreads, 0, stream, a);
+  };
+  if (per_row <= 12 || static_cast<int64_t>(a.T) * per_row >= 1 << 22) return read(std::integral_constant<int, 32>());
+  if (per_row <= 40) return read(std::integral_constant<int, 16>());
+  return read(std::integral_constant<int, 4>());
 }
 
 int log2_of(int page_size) {
