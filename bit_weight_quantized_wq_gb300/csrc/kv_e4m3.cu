@@ -225,7 +225,7 @@ cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------------------- reading back
-constexpr int kReadThreads = 256, kReadAhead = 2;
+constexpr int kReadThreads = 256;
 
 // Codes at scale byte `byte` as two packed elements of the output's type.  Most scales are exact in fp16 and reach no
 // infinity (2^-14 .. 2^7): one product there.
@@ -248,8 +248,9 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t f16x2, uint32_t byte, b
 
 // A CTA has TOK rows of the output, K or V; a thread 16 elements at a time (16 bytes in, 32 out).  Bound by reads and writes
 // of HBM mixed once its instructions are few: with divisions for every unit, and fp16 by way of float32 and a clamp, the
-// ALU was at 65% and 24 requests of up to 8191 tokens took 118 us.
-template <bool F16, int D, int TOK>
+// ALU was at 65%, and with a thread looking up its request's pages one after the other: 24 requests of up to 8191 tokens took
+// 118 us, now 94 (6.4 TB/s of reads and writes).
+template <bool F16, int D, int TOK, int kReadAhead>
 __global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvReadArgs a) {
   constexpr int kPieces = D / 16;
   __shared__ int64_t where[TOK];               // of each row: its token of head 0, counted in tokens of the cache; -1: none
@@ -325,17 +326,19 @@ __global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvReadArgs a) {
 
 template <bool F16, int D>
 cudaError_t launch_read_t(const KvReadArgs& a, cudaStream_t stream) {
-  // A CTA's threads have a unit each, so that a short call is over in one round of loads; 32 rows from 2^22 units on.
-  // 4 / 16 / 32 rows, 8 heads of 128 (64 units a row), in us: 1000 rows 4.0 / 5.2 / 8.3, 12000 16.8 / 18.1 / 24, 30000 40 /
-  // 39 / 43, 98000 116 / 109 / 102; 2 heads of 64 (8 units), 9000 rows 8.7 / 5.0 / 6.8, 45000 32 / 17.6 / 17.4.
+  // A CTA's threads have a unit each, so that a call is over in one round of loads, until there are enough CTAs for the
+  // chain of loads before it to matter: 16 rows a CTA from 700000 units on.  4 / 16 / 32 rows, 8 heads of 128 (64 units a
+  // row), in us: 700 rows 3.1 / 3.8 / 5.2, 6000 9.1 / 11.3 / 13.5, 12000 15.0 / 14.9 / 21, 30000 37 / 35 / 37, 98000 118 /
+  // 94 / 97; 2 heads of 64 (8 units), 9000 rows 7.5 / 3.6 / 3.9, 18000 12.5 / 5.8 / 4.8, 45000 28 / 10.8 / 8.7.
   const int per_row = a.Hkv * D / 16;
-  const auto read = [&](auto rows) {
+  const auto read = [&](auto rows, auto ahead) {
     constexpr int n = decltype(rows)::value;
-    return launch_pdl(k_kv_read<F16, D, n>, dim3((a.T + n - 1) / n, 2), kReadThreads, 0, stream, a);
+    return launch_pdl(k_kv_read<F16, D, n, decltype(ahead)::value>, dim3((a.T + n - 1) / n, 2), kReadThreads, 0, stream, a);
   };
-  if (per_row <= 12 || static_cast<int64_t>(a.T) * per_row >= 1 << 22) return read(std::integral_constant<int, 32>());
-  if (per_row <= 40) return read(std::integral_constant<int, 16>());
-  return read(std::integral_constant<int, 4>());
+  using One = std::integral_constant<int, 1>;
+  if (per_row <= 12) return read(std::integral_constant<int, 32>(), One());
+  if (static_cast<int64_t>(a.T) * per_row >= 700000) return read(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
+  return read(std::integral_constant<int, 4>(), One());
 }
 
 int log2_of(int page_size) {
