@@ -129,6 +129,18 @@ def test_append_many_requests_one_token_each(B, dtype):
     c.check()
 
 
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (64, 128)])
+@pytest.mark.parametrize("most", [2, 16, 17, 18, 65, 130, 131])
+def test_append_up_to_a_number_of_tokens(B, d, page, most):
+    """One, two and more pages a request; requests with fewer than the most, none, or all of their tokens new."""
+    lens = [most, 5 * page, 3 * page + 1, most + page - 1, 1, 2 * page, most + 1]
+    c = Cache(12, lens, 3, d, page, spread=1.0).fill(B, [max(0, n - most) for n in lens])
+    news = [most, most, most, most, 1, 0, max(1, most - 1)]
+    news = [min(a, b) for a, b in zip(news, lens)]
+    c.append(B, c.new(2, sum(news), "bf16", 4.0), lens, news)
+    c.check()
+
+
 @pytest.mark.parametrize("page,d", [(16, 128), (64, 64), (128, 128)])
 def test_append_extreme_values(B, page, d):
     c = Cache(5, [page + 9], 2, d, page)
@@ -214,6 +226,26 @@ def test_read(B, dtype, Hkv, d, page):
         assert torch.equal(got[i].cpu(), want.to(_dt(dtype)))
 
 
+@pytest.mark.parametrize("Hkv,d,page,lens", [(1, 128, 16, [700, 2, 0, 301]), (3, 64, 32, [999, 46]), (8, 128, 64, [9001, 1, 2047]),
+                                             (40, 128, 16, [1500, 0, 723])])
+def test_read_calls_of_all_sizes(B, Hkv, d, page, lens):
+    import torch
+    c = Cache(11, lens, Hkv, d, page)
+    for i in (2, 3):                               # scales of a prompt's pages, some beyond fp16's exact powers
+        c.host[i][:] = 127 + c.rng.integers(-17, 10, c.host[i].shape)
+        c.dev[i].copy_(torch.from_numpy(c.host[i]))
+    starts = np.concatenate(([0], np.cumsum(lens)))
+    T = int(starts[-1])
+    for dt in (torch.bfloat16, torch.float16):
+        got = B.kv_read_e4m3(*c.dev, i32(c.table), i32(starts), T, dtype=dt)
+        for i in (0, 1):
+            want = np.concatenate([c8.tokens(c.host[i], c.host[i + 2], c.table[r], n) for r, n in enumerate(lens)])
+            want = torch.from_numpy(want)
+            want = (want.clamp(-65504.0, 65504.0) if dt == torch.float16 else want).to(dt)
+            x = got[i].cpu()
+            assert torch.equal(x.isnan(), want.isnan()) and torch.equal(x.nan_to_num(), want.nan_to_num())
+
+
 def test_read_every_code_and_scale(B):
     """bf16 exactly (the largest binades of 2^64 * 448 are inside its range), fp16 rounded once and saturated."""
     import torch
@@ -257,7 +289,10 @@ def _lse_limit(lse, reach, n):
 def _within(got, ref, limit, what):
     assert got.shape == ref.shape
     assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(np.isinf(got), np.isinf(ref)), what
-    err = np.where(np.isfinite(ref), np.abs(got - ref), 0)
+    assert np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)]), what
+    err = np.zeros_like(ref)
+    np.subtract(got, ref, out=err, where=np.isfinite(ref))
+    err = np.abs(err)
     bad = ~(err <= limit)
     assert not bad.any(), "%s: %d of %d outside, worst %g of its limit" % (what, bad.sum(), bad.size, np.nanmax(err / np.maximum(limit, 1e-300)))
 
@@ -304,6 +339,42 @@ def test_attend(B, case, dtype, d, page):
     lens, news, Hq, Hkv = ATTN[case]
     c = Cache(20 + case, lens, Hkv, d, page, spread=0.5).fill(B, lens)
     _attend(B, c, lens, news, Hq, dtype, case)
+
+
+ROWS = [  # lens, new tokens, Hq, Hkv: rows of a head (new tokens x Hq / Hkv) on both sides of the kernels' limits
+    ([200, 90, 64], [6, 8, 5], 8, 2),                              # 24, 32, 20: two row tiles
+    ([300, 5, 70], [4, 4, 1], 16, 2),                              # 32 and 8 of the same call
+    ([64, 60, 700], [10, 33, 12], 8, 2),                           # 40, 132, 48: key tiles in turn, and not
+    ([5, 64, 63, 65, 129], [5, 9, 16, 10, 7], 16, 2),              # 40 .. 128 over one key tile, or two or three
+    ([140, 300, 40], [32, 65, 33], 8, 2),                          # 128, 260, 132: on both sides of a lane and of an item
+    ([400, 60, 300, 90, 17], [100, 1, 1, 2, 1], 14, 2),            # decoding requests beside a prompt
+    ([300, 40, 5, 260], [30, 1, 0, 2], 20, 1),                     # 600, 20, none, 40
+    ([33, 2, 1, 500], [33, 2, 1, 0], 8, 1),                        # as long as the request
+]
+
+
+@pytest.mark.parametrize("dtype,d,page", [("bf16", 128, 16), ("bf16", 64, 32), ("f16", 128, 128), ("f16", 64, 64)])
+@pytest.mark.parametrize("case", range(len(ROWS)))
+def test_attend_rows_of_all_kinds(B, case, dtype, d, page):
+    lens, news, Hq, Hkv = ROWS[case]
+    c = Cache(60 + case, lens, Hkv, d, page, spread=0.5).fill(B, lens)
+    _attend(B, c, lens, news, Hq, dtype, case)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("lens,news,Hq", [([9000], [1], 4), ([20001, 30], [7, 2], 4), ([9000, 77], [20, 1], 4), ([6000], [130], 2)])
+def test_attend_few_requests_cut_in_many_pieces(B, dtype, d, lens, news, Hq):
+    """Their pieces are joined by groups, then the groups."""
+    c = Cache(70, lens, 1, d, 64, spread=0.5).fill(B, lens)
+    _attend(B, c, lens, news, Hq, dtype, 1)
+
+
+def test_attend_many_requests_of_both_kinds(B):
+    rng = np.random.default_rng(6)
+    news = [int(n) for n in rng.integers(0, 40, 90)]
+    lens = [int(n + m) for n, m in zip(news, rng.integers(0, 90, 90))]
+    c = Cache(71, lens, 2, 64, 16).fill(B, lens)
+    _attend(B, c, lens, news, 8, "bf16")
 
 
 def test_attend_many_requests(B):
