@@ -657,3 +657,14 @@ def test_run_together_as_a_decoder_uses_them(B):
     o16, _ = B.attn_shared_prefix(q, wide[0], wide[1], None, 0, i32([[0, 1, 2, 3]]), i32([n]))
     # both round the weights (2^-11, 2^-8) and the output (2^-8): sums of |v| p, at most max |v|
     assert (o16.float() - o.float()).abs().max() <= (2 * 2.0 ** -8 + 2.0 ** -8 + 2.0 ** -11) * float(v16.float().abs().max()) * 1.5
+
+
+def test_example_of_a_served_block(B):
+    """Prompts in pieces beside decoding requests, then a captured step with places whose request is done."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "quantized_cache_block.py")
+    spec = importlib.util.spec_from_file_location("quantized_cache_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main() < 2.0 ** -4
