@@ -216,6 +216,10 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// The scales of keys behind a request's tokens, K | V << 8: 1.  (A page that is not the request's holds any bytes, and
+// 0 and 255 times a weight of 0 are not 0.)
+constexpr uint32_t kNoScale = kScaleBias | (kScaleBias << 8);
+
 // A wait of a whole warp on a barrier in a ring, bounded as mbar_wait_short is; once one has run out, all others give up too.  `sleep_ns`: of
 // a warp that is far ahead, so that it leaves the issue slots to others.
 __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* failed, uint32_t code, uint32_t sleep_ns = 0) {
@@ -413,10 +417,9 @@ __device__ __forceinline__ void copy_items(const Params& p, const CUtensorMap& t
     const int n = x.template stages<L, KEYS>(p, first), len = x.q.len;
     const int32_t* table = p.a.block_table + static_cast<int64_t>(x.r) * p.a.max_blocks;
     // lane i has box base + i of the item; the table of the 32 after it is on its way
-    const auto table_at = [&](int base) {
-      const int key = first * KEYS + ((base + lane) << log_box);
-      return base + lane < n * boxes && key < len ? __ldg(table + (key >> p.log_page)) : 0;
-    };
+    const auto key_of = [&](int base) { return first * KEYS + ((base + lane) << log_box); };
+    const auto held = [&](int base) { return base + lane < n * boxes && key_of(base) < len; };
+    const auto table_at = [&](int base) { return held(base) ? __ldg(table + (key_of(base) >> p.log_page)) : 0; };
     int row = 0, ahead = table_at(0);
     uint32_t scale = 0;
 #pragma unroll 1
@@ -429,7 +432,8 @@ __device__ __forceinline__ void copy_items(const Params& p, const CUtensorMap& t
           page = 0;
         }
         row = page * p.a.Hkv + x.head;
-        scale = __ldg(p.a.k_scales + row) | (static_cast<uint32_t>(__ldg(p.a.v_scales + row)) << 8);
+        scale = kNoScale;
+        if (held(b0)) scale = __ldg(p.a.k_scales + row) | (static_cast<uint32_t>(__ldg(p.a.v_scales + row)) << 8);
         ahead = table_at(b0 + 32);
       }
       const int s = stage % N;
@@ -534,10 +538,8 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
     // each: as many as memory can hold fit 32 bits), and the page's scales; the table of the window after it is on its
     // way, the scales of the one before it are kept for the steps that the copies are ahead.
     const auto key_of = [&](int piece) { return (s0 + (piece / kPieces) * wk) * kKeys + 16 * (piece % kPieces); };
-    const auto table_at = [&](int base) {
-      const int key = key_of(base + lane);
-      return base + lane < steps * kPieces && key < q.len ? __ldg(table + (key >> p.log_page)) : 0;
-    };
+    const auto held = [&](int base) { return base + lane < steps * kPieces && key_of(base + lane) < q.len; };
+    const auto table_at = [&](int base) { return held(base) ? __ldg(table + (key_of(base + lane) >> p.log_page)) : 0; };
     int page_next = table_at(0);
     uint32_t piece_i = 0, scale_i = 0, scale_before = 0;
     const auto look_up = [&](int base) {
@@ -549,7 +551,8 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
       const uint32_t at = static_cast<uint32_t>(page) * p.a.Hkv + kvh;
       piece_i = (at << (p.log_page - 4)) + ((key_of(base + lane) & (p.a.page_size - 1)) >> 4);
       scale_before = scale_i;
-      scale_i = __ldg(p.a.k_scales + at) | (static_cast<uint32_t>(__ldg(p.a.v_scales + at)) << 8);
+      scale_i = kNoScale;
+      if (held(base)) scale_i = __ldg(p.a.k_scales + at) | (static_cast<uint32_t>(__ldg(p.a.v_scales + at)) << 8);
       page_next = table_at(base + 32);
     };
     const auto issue = [&](int j) {
@@ -1268,7 +1271,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t sc = sm.scales[at % kScaleRing][(16 * q) >> log_box];
-            ck[q] = c * scale_value(sc & 0xffu), ev[q] = static_cast<float>(static_cast<int>(sc >> 8) - kScaleBias);
+            // not 0, which the masked scores' infinities turn into NaN; what this changes of x is below 2^-94
+            ck[q] = fmaxf(c * scale_value(sc & 0xffu), 1.17549435e-38f), ev[q] = static_cast<float>(static_cast<int>(sc >> 8) - kScaleBias);
             inv[q] = scale_value(2 * kScaleBias - (sc >> 8));
           }
           tc_wait_ld();

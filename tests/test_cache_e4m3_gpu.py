@@ -485,6 +485,36 @@ def test_attend_nan_of_visible_keys_and_values_only(B, news):
         c.dev[i].copy_(torch.from_numpy(c.host[i]))
 
 
+@pytest.mark.parametrize("byte", [0, 255])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (64, 32), (128, 128)])
+@pytest.mark.parametrize("news", [1, 9, 70])
+def test_attend_pages_of_no_request_reach_nothing(B, d, page, byte, news):
+    """Pages that nothing was written to hold anything, scale bytes 0 and 255 too, the first page among them."""
+    import torch
+    lens = [news, news + 8, news + 67]
+    c = Cache(72, lens, 2, d, page, spare=4)
+    free = [p for p in range(c.host[0].shape[0]) if p not in c.table]
+    c.table[c.table == 0] = free[0] if free[0] else 0
+    c.fill(B, lens)
+    free = [p for p in range(c.host[0].shape[0]) if p not in c.table]
+    assert 0 in free
+    for i, b in enumerate((0x7F, 0x7F, byte, byte)):
+        c.host[i][free] = b
+        c.dev[i].copy_(torch.from_numpy(c.host[i]))
+    for dtype in ("bf16", "f16"):
+        _attend(B, c, lens, [news] * 3, 8, dtype)
+
+
+@pytest.mark.parametrize("news", [1, 9, 70])
+def test_attend_scores_that_underflow(B, news):
+    """scale times a query below float32's range: all visible keys weigh alike, the others still nothing."""
+    import torch
+    lens = [news + 30]
+    c = Cache(73, lens, 1, 128, 16).fill(B, lens)
+    q = (torch.randn(news, 4, 128, generator=torch.Generator().manual_seed(1)) * 2.0 ** -100).bfloat16().cuda()
+    _attend(B, c, lens, [news], 4, "bf16", q=q, scale=float(np.float32(1e-30)))
+
+
 def test_attend_and_append_beyond_32_bit_offsets(B):
     import torch
     pages, Hkv, page, d = 36000, 8, 128, 128                              # 4.7e9 codes
