@@ -77,6 +77,7 @@ struct Params {
   int* count;                // segments (or groups) that are done of the item that begins in a CTA, and of the group [2][ctas]
   float *po;                 // partials [cta][2][rows of an item][d], largest exponents and sums [cta][2][rows][2]
   float2 *ml;
+  bool beside;               // the kernel for few rows: behind the other one of the same call
 };
 
 // One request's new tokens and keys, forced into range.
@@ -501,13 +502,18 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
   S& sm = *reinterpret_cast<S*>(smem_raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
-  pdl_wait();
+  // Behind the kernel for many rows this one need not wait: that one lets it start after its own wait, and the two share
+  // nothing.  It does not end before that one, so that what waits for this call waits for both.
+  if (!p.beside) pdl_wait();
   // where this lane's copies go: chunk 32 i + lane of a step is chunk lane % 8 of row 4 i + lane / 8 of 128 bytes
   const uint32_t ring = smem_u32(sm.ring[warp][0][0]);
   const uint32_t to_even = 128 * (lane >> 3) + 16 * ((lane & 7) ^ (lane >> 3)), to_odd = to_even ^ 64;
   const uint8_t *k_lane = p.a.k_cache + 16 * lane, *v_lane = p.a.v_cache + 16 * lane;
   const Place place = find_place<L>(p);
-  if (place.r < 0) return;
+  if (place.r < 0) {
+    pdl_wait();
+    return;
+  }
   Walk<L> walk(p, place);
   Segment seg;
 #pragma unroll 1
@@ -900,6 +906,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
     }
     __syncthreads();                           // and the ring again
   }
+  pdl_wait();
 }
 
 // ------------------------------------------------------------------------------- many rows
@@ -978,8 +985,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     fence_barrier_init();
   }
   if (threadIdx.x == 32 * kWCopy) tma_prefetch_desc(&tk), tma_prefetch_desc(&tv);
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();                     // not before: the kernel for few rows reads what this one waited for
   const Place place = find_place<L>(p);
   if (place.r < 0) return;
   if (warp == kWMma) {
@@ -1513,10 +1520,16 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   }
 }
 
+// Of each kernel: counters, two segments of each CTA.
 struct Layout {
   int sms;
-  size_t po, ml, bytes;
+  size_t count[2], po[2], ml[2], bytes;
+  void give(Params& p, int i, uint8_t* ws) const {
+    p.count = reinterpret_cast<int*>(ws + count[i]);       // in the header: zero, and left so
+    p.po = reinterpret_cast<float*>(ws + po[i]), p.ml = reinterpret_cast<float2*>(ws + ml[i]);
+  }
 };
+constexpr int kMany = 0, kFew = 1;
 
 Layout layout(int64_t d) {
   Layout l{};
@@ -1527,11 +1540,12 @@ Layout layout(int64_t d) {
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  // two segments of each CTA: up to four an SM with items of up to 32 rows, one with 256
-  const size_t slots = static_cast<size_t>(l.sms) * 2 * kManyRows;
-  static_assert(4 * kFewMostRows <= kManyRows, "both kernels' segments");
-  l.po = take(slots * d * sizeof(float));
-  l.ml = take(slots * sizeof(float2));
+  const size_t rows[2] = {kManyRows, static_cast<size_t>(std::max(few_ctas(1) * FewLine<1>::kRows, few_ctas(2) * FewLine<2>::kRows))};
+  l.count[kMany] = 0, l.count[kFew] = 2 * l.sms * sizeof(int);
+  for (int i : {kMany, kFew}) {
+    l.po[i] = take(2 * l.sms * rows[i] * d * sizeof(float));
+    l.ml[i] = take(2 * l.sms * rows[i] * sizeof(float2));
+  }
   l.bytes = off;
   return l;
 }
@@ -1547,17 +1561,18 @@ cudaError_t cache_map(CUtensorMap* map, const uint8_t* cache, const AttnE4m3Args
 }
 
 template <bool F16, int D, int NR>
-cudaError_t launch_few(const Params& p, const Layout& l, cudaStream_t stream) {
+cudaError_t launch_few(Params p, const Layout& l, uint8_t* ws, cudaStream_t stream) {
   constexpr size_t smem = sizeof(FewSmem<D, NR>);
   constexpr int ctas = few_ctas(NR);
   static_assert(ctas * (smem + 1024 + 1024) <= 227 * 1024, "CTAs of the kernel for few rows do not fit an SM");
   const cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(k_attn_e4m3<F16, D, NR>), smem);
   if (e != cudaSuccess) return e;
+  l.give(p, kFew, ws);
   return launch_pdl(k_attn_e4m3<F16, D, NR>, dim3(l.sms * ctas), FewLine<NR>::kThreads, smem, stream, p);
 }
 
 template <bool F16, int D>
-cudaError_t launch_many(const Params& p, const Layout& l, cudaStream_t stream) {
+cudaError_t launch_many(Params p, const Layout& l, uint8_t* ws, cudaStream_t stream) {
   constexpr size_t smem = sizeof(ManySmem<D>) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of the kernel for many rows over the per-CTA limit");
   CUtensorMap tk, tv;
@@ -1565,6 +1580,7 @@ cudaError_t launch_many(const Params& p, const Layout& l, cudaStream_t stream) {
   if (e == cudaSuccess) e = cache_map(&tv, p.a.v_cache, p.a, kTile);
   if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(k_attn_e4m3_many<F16, D>), smem);
   if (e != cudaSuccess) return e;
+  l.give(p, kMany, ws);
   return launch_pdl(k_attn_e4m3_many<F16, D>, dim3(l.sms), kManyThreads, smem, stream, tk, tv, p);
 }
 
@@ -1579,18 +1595,17 @@ cudaError_t launch_t(const AttnE4m3Args& a, uint8_t* ws, cudaStream_t stream) {
   p.log_page = 4;
   while ((1 << p.log_page) < a.page_size) ++p.log_page;
   p.c = a.scale * 1.4426950408889634f;
-  p.count = reinterpret_cast<int*>(ws);        // the header's counters: zero, and left so
-  p.po = reinterpret_cast<float*>(ws + l.po), p.ml = reinterpret_cast<float2*>(ws + l.ml);
   // Requests of up to 32 rows a head, or of up to 8 where a call also has longer ones and a single token's rows are no
   // more (the decoding requests beside prompts), go to the first kernel.  First / second kernel, 64 heads of 128 on 8, in
   // us: 4 requests over up to 40000 keys, 3 new tokens 58 / 73, 4 63 / 73, 6 103 / 73, 8 114 / 72; 48 requests over up to
   // 4096, 3 70 / 93, 4 77 / 92, 6 124 / 93; heads of 64, 3 39 / 77, 4 42 / 78, 6 66 / 77, 8 73 / 77.
   p.few = rows <= kFewMostRows || p.G > 8 ? kFewMostRows : 8;
-  if (rows > kFewMostRows) {
-    const cudaError_t e = launch_many<F16, D>(p, l, stream);
+  p.beside = rows > kFewMostRows;
+  if (p.beside) {
+    const cudaError_t e = launch_many<F16, D>(p, l, ws, stream);
     if (e != cudaSuccess) return e;
   }
-  return std::min<int64_t>(rows, p.few) <= 8 ? launch_few<F16, D, 1>(p, l, stream) : launch_few<F16, D, 2>(p, l, stream);
+  return std::min<int64_t>(rows, p.few) <= 8 ? launch_few<F16, D, 1>(p, l, ws, stream) : launch_few<F16, D, 2>(p, l, ws, stream);
 }
 
 }  // namespace
