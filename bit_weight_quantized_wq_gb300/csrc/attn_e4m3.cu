@@ -1022,16 +1022,16 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         Segment x;
         more = walk.next(x);
         if (!more) x.hi = 0;
-        if (more) {                             // its queries on their way to L2
-          const int row0 = x.tile * kManyRows, t0 = p.by_G.of(row0), tokens = p.by_G.of(row0 + x.it.rows - 1) - t0 + 1;
-          const uint32_t bytes = p.G * D * 2;
-          for (int t = lane; t < tokens; t += 32)
-            prefetch_l2(p.a.Q + (x.q.first + t0 + t) * p.a.q_stride + static_cast<int64_t>(x.head) * p.G * D, bytes);
-        }
         ok = stage_wait(&sm.seg_empty[i % kSegments], ((i / kSegments) & 1) ^ 1, &sm.failed, kErrWaitEmpty, 500);
         if (lane == 0 && ok) {
           sm.seg[i % kSegments] = x;
           mbar_arrive(&sm.seg_full[i % kSegments]);
+        }
+        if (more && i > 0) {                    // its queries on their way to L2; the first ones are asked for right away
+          const int row0 = x.tile * kManyRows, t0 = p.by_G.of(row0), tokens = p.by_G.of(row0 + x.it.rows - 1) - t0 + 1;
+          const uint32_t bytes = p.G * D * 2;
+          for (int t = lane; t < tokens; t += 32)
+            prefetch_l2(p.a.Q + (x.q.first + t0 + t) * p.a.q_stride + static_cast<int64_t>(x.head) * p.G * D, bytes);
         }
       }
     } else if (warp == kWCopy) {
@@ -1205,7 +1205,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int64_t row_at = (x.q.first + w.tok) * p.a.q_stride + static_cast<int64_t>(w.head) * D;
       const uint32_t rows = __ballot_sync(0xffffffffu, w.valid);
       ok = ok && stage_wait(&sm.q_empty[l], (q_items & 1) ^ 1, &sm.failed, kErrWaitEmpty);
-#pragma unroll 1
+#pragma unroll 4
       for (int i = 0; i < kLanes; ++i) {
         const int to = i * kAtOnce + lane / kLanes;
         const int64_t at = __shfl_sync(0xffffffffu, row_at, to);
