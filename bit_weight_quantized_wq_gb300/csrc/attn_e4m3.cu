@@ -103,7 +103,8 @@ __device__ __forceinline__ int keys_seen(const Request& q, int token) { return m
 // The lines: rows of an item, the weight of a tile (by the item's rows) and the constant of an item, which stands for
 // its set-up, its output and its part of a join.  Measured: first line, 20 / 60 / 120 / 240, 48 requests of up to 4 new
 // tokens 57.8 / 45.2 / 46.3 / 47.1 us and 64 single tokens over long caches 174.5 / 173.8 / 175.0 / 181.4; second line,
-// 25 / 50 / 100 / 200, pieces of 3 prompts 467 / 437 / 420 / 435 us and prompts beside single tokens 80 / 79 / 80 / 86.
+// 60 / 80 / 100 / 130 / 160, pieces of 3 prompts 405 / 399 / 402 / 405 / 408 us, prompts beside single tokens 72.8 / 73.3 /
+// 73.5 / 74.1 / 74.6, 48 requests of up to 8 new tokens 85 / 87 / 89 / 92 / 96, 100 items of 1024 keys 44 / 39 / 37 / 38 / 38.
 constexpr int kFewWarps = 4;           // of a CTA of the kernel for few rows
 constexpr int kFewMostRows = 32;       // of a request's head in it
 template <int NR>
@@ -117,7 +118,7 @@ struct FewLine {
 constexpr int kManyThreads = 512, kManyRows = 256;
 struct ManyLine {
   __device__ static bool takes(const Params& p, int rows) { return rows > p.few; }
-  static constexpr int kThreads = kManyThreads, kRows = kManyRows, kItem = 100, kMost = 10;
+  static constexpr int kThreads = kManyThreads, kRows = kManyRows, kItem = 80, kMost = 10;
   __device__ static int weight(int rows) { return rows <= kManyRows / 2 ? 5 : kMost; }
 };
 
@@ -251,10 +252,14 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   __shared__ long long found_at, found_head;
   __shared__ int found_r;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // some more than an equal share, so that the shares cover the line
+  // An equal share, rounded up so that the shares cover the line; for many rows by no more than has to be, or cuts drift
+  // into items that fit the CTAs: 152 items of 512 keys 37 us, exactly 23.  (For few rows that took 0.2 us and gave none.)
   const auto take = [&](Place& s, long long total) {
+    const long long ctas = gridDim.x;
     s.share = max(static_cast<long long>(L::kMost),
-                  static_cast<long long>(__fdividef(static_cast<float>(total), static_cast<float>(gridDim.x)) * 1.000001f) + 1);
+                  static_cast<long long>(__fdividef(static_cast<float>(total), static_cast<float>(ctas)) * 1.000001f) + 1);
+    if constexpr (L::kRows == kManyRows)
+      while (s.share > L::kMost && (s.share - 1) * ctas >= total) --s.share;
     s.b0 = blockIdx.x * s.share;
   };
   // line length of a head of request r (none past the last); all lanes of the warp
@@ -921,7 +926,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
 // The products of a tile run while the softmax of the lane's tile before it, and of the other lane's, runs.  A warp walks
 // over the segments ahead of the others.  Bound by the products: a tile of 256 rows takes some 1820 cycles, and the
 // tensor core's part of them is 1760 (S has to read Q from shared memory for every 64 keys, as attn.cu says).  Pieces of
-// 3 prompts, 5119 new tokens over up to 10007 keys, 32 heads on 8: 420 us, 1027 TFLOP/s of what the rows see.
+// 3 prompts, 5119 new tokens over up to 10007 keys, 32 heads on 8: 399 us, 1081 TFLOP/s of what the rows see.
 constexpr int kRawStages = 3;          // tiles of codes, K and V
 constexpr int kWideStages = 3;         // tiles of fp16, of K and of V
 constexpr int kScaleRing = 16;         // tiles' scales: more than the copies are ahead of the softmax warps
@@ -1225,7 +1230,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         const int k = bf16_to_f16_exponent(max(mx & 0xffffu, mx >> 16));
         const float down = pow2_normal(-k);
         w.c *= pow2_normal(k);
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
           uint4* at = reinterpret_cast<uint4*>(q + place_of(lane, i));
           uint4 v = *at;
@@ -1596,9 +1601,9 @@ cudaError_t launch_t(const AttnE4m3Args& a, uint8_t* ws, cudaStream_t stream) {
   while ((1 << p.log_page) < a.page_size) ++p.log_page;
   p.c = a.scale * 1.4426950408889634f;
   // Requests of up to 32 rows a head, or of up to 8 where a call also has longer ones and a single token's rows are no
-  // more (the decoding requests beside prompts), go to the first kernel.  First / second kernel, 64 heads of 128 on 8, in
-  // us: 4 requests over up to 40000 keys, 3 new tokens 58 / 73, 4 63 / 73, 6 103 / 73, 8 114 / 72; 48 requests over up to
-  // 4096, 3 70 / 93, 4 77 / 92, 6 124 / 93; heads of 64, 3 39 / 77, 4 42 / 78, 6 66 / 77, 8 73 / 77.
+  // more (the decoding requests beside prompts), go to the first kernel.  64 heads of 128 on 8, in us, first kernel with
+  // 3 / 4 / 6 / 8 new tokens (24 .. 64 rows) and second one with 6 .. 12: 4 requests over up to 40000 keys 55 / 59 / 103 /
+  // 114 and 69; 48 requests over up to 4096 66 / 72 / 124 / 138 and 87; the same with heads of 64 38 / 41 / 66 / 73 and 81.
   p.few = rows <= kFewMostRows || p.G > 8 ? kFewMostRows : 8;
   p.beside = rows > kFewMostRows;
   if (p.beside) {
