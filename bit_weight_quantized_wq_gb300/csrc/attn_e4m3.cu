@@ -958,6 +958,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// 32 bytes to an address that is a multiple of 32.
+__device__ __forceinline__ void store32(void* to, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // The key tiles of an item of n tiles that lane l takes.
 struct Turns {
   int first, step, n;
@@ -1384,14 +1391,19 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
       }
       const int64_t at_row = static_cast<int64_t>(x.q.first + done.tok) * p.a.Hq + done.head;
+      const bool wide_rows = (reinterpret_cast<uintptr_t>(p.a.O) & 31) == 0;
       // 32 columns of the row, given as the sums' bits
       const auto finish = [&](int q, const uint32_t (&o)[32], float inv) {
         uint32_t h[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) h[i] = pack2<F16>(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-        uint4* dst = reinterpret_cast<uint4*>(p.a.O + at_row * D + 32 * q);
+        uint16_t* dst = p.a.O + at_row * D + 32 * q;
+        if (wide_rows) {                        // whole sectors: 304 items of 512 keys 39.4 -> 37.7 us
+          store32(dst, &h[0]), store32(dst + 16, &h[8]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+          for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+        }
       };
       const auto finish_lse = [&](float top, float total) {
         if (p.a.lse)

@@ -444,6 +444,26 @@ def test_attend_one_token_each_without_q_start_strided_q_given_outputs(B):
     check(c, q, o, lse, lens, [0, 1, 2, 3], None, "bf16")
 
 
+@pytest.mark.parametrize("news", [1, 70])
+def test_attend_inputs_and_outputs_aligned_to_16_bytes_only(B, news):
+    import torch
+    lens = [news + 90, news + 7]
+    c = Cache(74, lens, 2, 128, 32).fill(B, lens)
+    T = 2 * news
+
+    def at16(like):
+        flat = torch.empty(like.numel() + 8, dtype=like.dtype, device="cuda")
+        assert flat.data_ptr() % 32 == 0
+        t = flat[16 // like.element_size():][:like.numel()].view(like.shape)
+        t.copy_(like)
+        return t
+    q = at16(torch.randn(T, 8, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda())
+    c.dev[0], c.dev[1] = (torch.cat((torch.zeros(16, dtype=torch.uint8, device="cuda"), x.flatten()))[16:].view(x.shape) for x in c.dev[:2])
+    out = at16(torch.zeros(T, 8, 128, dtype=torch.bfloat16, device="cuda")), torch.empty(T * 8 + 1, device="cuda")[1:].view(T, 8)
+    _, o, _ = _attend(B, c, lens, [news] * 2, 8, "bf16", q=q, out=out)
+    assert o is out[0] and o.data_ptr() % 32 == 16
+
+
 def test_attend_leaves_rows_behind_the_requests_alone(B):
     import torch
     lens = [90, 200]
