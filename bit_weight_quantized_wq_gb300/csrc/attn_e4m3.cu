@@ -27,6 +27,7 @@
 // 16384 keys, 64 heads on 8, 174 us, 6.2 TB/s; a short call by its chain of loads, barriers and the join: one request
 // over 500 keys 6.6 us, one over 131071 54 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv_e4m3.cuh"
@@ -849,58 +850,84 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
         mine = last(p.count + c0, n);
       }
       while (mine) {
-        // P neighbouring threads take a unit's segments in turn, eight at a time, so that few loads wait for others
+        // Few loads wait for others: neighbouring threads (`parts` of them) take a unit's segments in turn, or a thread has
+        // two units where there are more than threads, eight segments at a time.  (One unit after the other: 8 requests of 4
+        // new tokens over up to 8192 keys, 32 heads on 8, 25.6 us, so 22.0; two also where there is one: one request over 500
+        // keys 6.7, so 7.1.)
         const int parts = units * 8 <= L::kThreads ? 8 : units * 4 <= L::kThreads ? 4 : units * 2 <= L::kThreads ? 2 : 1, part = threadIdx.x & (parts - 1);
+        const auto join = [&](auto each) {
+          constexpr int U = decltype(each)::value, kApart = L::kThreads / (D / 4);      // rows from a thread's unit to its next
 #pragma unroll 1
-        for (int u0 = 0; u0 < units * parts; u0 += L::kThreads) {
-          const int u = min((u0 + static_cast<int>(threadIdx.x)) / parts, units - 1), row = u / (D / 4), col = 4 * (u % (D / 4));
-          const auto slot = [&](int i) {
-            const int c = first + i * step;
-            return (2ll * c + (c == c0 ? 1 : 0)) * L::kRows + row;
-          };
-          float top = -INFINITY, total = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int u0 = 0; u0 < units * parts; u0 += U * L::kThreads) {
+            const int u = min((u0 + static_cast<int>(threadIdx.x)) / parts, units - 1), row = u / (D / 4), col = 4 * (u % (D / 4));
+            const bool two = U == 2 && row + kApart < it.rows;
+            const auto slot = [&](int i) {
+              const int c = first + i * step;
+              return (2ll * c + (c == c0 ? 1 : 0)) * L::kRows + row;
+            };
+            float top[U], total[U];
+            float4 o[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) top[k] = -INFINITY, total[k] = 0.f, o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-          for (int base = part; base < n; base += 8 * parts) {
-            float2 ml[8];
-            float4 v[8];
-            float now = top;
+            for (int base = part; base < n; base += 8 * parts) {
+              float2 ml[U][8];
+              float4 v[U][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const long long at = slot(min(base + i * parts, n - 1));
-              ml[i] = __ldcg(p.ml + at);
-              v[i] = __ldcg(reinterpret_cast<const float4*>(p.po + at * D + col));
-              if (base + i * parts >= n) ml[i] = make_float2(-INFINITY, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-              now = fmaxf(now, ml[i].x);
-            }
-            const float ref = now == -INFINITY ? 0.f : now, keep = exp2_approx(top - ref);
-            total *= keep, o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
-            top = now;
+              for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float f = exp2_approx(ml[i].x - ref);
-              total = fmaf(ml[i].y, f, total);
-              o.x = fmaf(v[i].x, f, o.x), o.y = fmaf(v[i].y, f, o.y), o.z = fmaf(v[i].z, f, o.z), o.w = fmaf(v[i].w, f, o.w);
+                for (int k = 0; k < U; ++k) {
+                  ml[k][i] = make_float2(-INFINITY, 0.f), v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (base + i * parts < n && (k == 0 || two)) {
+                    const long long at = slot(base + i * parts) + k * kApart;
+                    ml[k][i] = __ldcg(p.ml + at);
+                    v[k][i] = __ldcg(reinterpret_cast<const float4*>(p.po + at * D + col));
+                  }
+                }
+#pragma unroll
+              for (int k = 0; k < U; ++k) {
+                float now = top[k];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) now = fmaxf(now, ml[k][i].x);
+                const float ref = now == -INFINITY ? 0.f : now, keep = exp2_approx(top[k] - ref);
+                total[k] *= keep, o[k].x *= keep, o[k].y *= keep, o[k].z *= keep, o[k].w *= keep;
+                top[k] = now;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float f = exp2_approx(ml[k][i].x - ref);
+                  const float4& x = v[k][i];
+                  total[k] = fmaf(ml[k][i].y, f, total[k]);
+                  o[k].x = fmaf(x.x, f, o[k].x), o[k].y = fmaf(x.y, f, o[k].y), o[k].z = fmaf(x.z, f, o[k].z), o[k].w = fmaf(x.w, f, o[k].w);
+                }
+              }
+            }
+            if (U == 1)
+              for (int d = 1; d < parts; d <<= 1) {
+                const float other = __shfl_xor_sync(0xffffffffu, top[0], d), now = fmaxf(top[0], other), ref = now == -INFINITY ? 0.f : now;
+                const float f = exp2_approx(top[0] - ref);
+                top[0] = now;
+                total[0] *= f, o[0].x *= f, o[0].y *= f, o[0].z *= f, o[0].w *= f;
+                total[0] += __shfl_xor_sync(0xffffffffu, total[0], d);
+                o[0].x += __shfl_xor_sync(0xffffffffu, o[0].x, d), o[0].y += __shfl_xor_sync(0xffffffffu, o[0].y, d);
+                o[0].z += __shfl_xor_sync(0xffffffffu, o[0].z, d), o[0].w += __shfl_xor_sync(0xffffffffu, o[0].w, d);
+              }
+            if (part == 0 && u0 + static_cast<int>(threadIdx.x) < units * parts) {
+#pragma unroll
+              for (int k = 0; k < U; ++k) {
+                if (k == 1 && !two) break;
+                const int r = row + k * kApart;
+                if (final) {
+                  finish(r, col, o[k], top[k], total[k]);
+                } else {
+                  *reinterpret_cast<float4*>(p.po + (slot(0) + k * kApart) * D + col) = o[k];
+                  if (col == 0) sm.ml[r / (8 * NR)][r % (8 * NR)] = make_float2(top[k], total[k]);
+                }
+              }
             }
           }
-          for (int d = 1; d < parts; d <<= 1) {
-            const float other = __shfl_xor_sync(0xffffffffu, top, d), now = fmaxf(top, other), ref = now == -INFINITY ? 0.f : now;
-            const float f = exp2_approx(top - ref);
-            top = now;
-            total *= f, o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-            total += __shfl_xor_sync(0xffffffffu, total, d);
-            o.x += __shfl_xor_sync(0xffffffffu, o.x, d), o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
-            o.z += __shfl_xor_sync(0xffffffffu, o.z, d), o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
-          }
-          if (part == 0 && u0 + static_cast<int>(threadIdx.x) < units * parts) {
-            if (final) {
-              finish(row, col, o, top, total);
-            } else {
-              *reinterpret_cast<float4*>(p.po + slot(0) * D + col) = o;
-              if (col == 0) sm.ml[row / (8 * NR)][row % (8 * NR)] = make_float2(top, total);
-            }
-          }
-        }
+        };
+        if (units <= L::kThreads) join(std::integral_constant<int, 1>());
+        else join(std::integral_constant<int, 2>());
         if (final) break;
         __syncthreads();                       // all have read what the group's first CTA left
         for (int row = threadIdx.x; row < it.rows; row += L::kThreads)
