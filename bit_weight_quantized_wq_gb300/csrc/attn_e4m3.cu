@@ -14,7 +14,7 @@
 // one for each CTA.  A CTA's run of tiles may begin and end inside items: what it computes of such an
 // item (a segment) goes to the workspace, unnormalised, and the last CTA that is done with the item
 // joins its segments in line order.  A CTA has two such segments at most, its first and its last.
-// Two kernels share a call's requests, each with a line of its own: up to 32 rows a head, and more.
+// Two kernels share a call's requests, each with a line of its own: up to 32 rows a head (64 with heads of 64), and more.
 //
 // Few rows (k_attn_e4m3): a warp has 8 NR rows of the item (its row tile, one of two at most), and the warps of a
 // row tile take the steps of 16 keys (32 where d is 64) in turn, copied by the warp itself with cp.async two steps
@@ -107,11 +107,11 @@ __device__ __forceinline__ int keys_seen(const Request& q, int token) { return m
 // 60 / 80 / 100 / 130 / 160, pieces of 3 prompts 405 / 399 / 402 / 405 / 408 us, prompts beside single tokens 72.8 / 73.3 /
 // 73.5 / 74.1 / 74.6, 48 requests of up to 8 new tokens 85 / 87 / 89 / 92 / 96, 100 items of 1024 keys 44 / 39 / 37 / 38 / 38.
 constexpr int kFewWarps = 4;           // of a CTA of the kernel for few rows
-constexpr int kFewMostRows = 32;       // of a request's head in it
+constexpr int few_most_rows(int d) { return d == 64 ? 64 : 32; }       // of a request's head in it
 template <int NR>
 struct FewLine {
   __device__ static bool takes(const Params& p, int rows) { return rows <= p.few; }
-  // eight rows a warp: one row tile; sixteen: two, each with half of the warps
+  // eight rows a warp: one row tile; sixteen: one or two, each with half of the warps, and items of up to 32 rows
   static constexpr int kThreads = 32 * kFewWarps, kRows = NR == 1 ? 8 : 32, kItem = 60, kMost = NR == 1 ? 8 : 12;
   __device__ static int weight(int rows) { return rows <= 8 * NR ? 8 : kMost; }
 };
@@ -529,13 +529,15 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
     const int kvh = seg.head;
     // ------------------------------------------------------------------ this warp's rows
     const int mt = NR > 1 && it.rows > 8 * NR ? 2 : 1, wk = kFewWarps / mt;
+    // the item's first row (below, rows are counted from it); 0 where one item has all
+    const int row0 = NR > 1 && few_most_rows(D) > L::kRows ? seg.tile * L::kRows : 0;
     const int row_base = (warp & (mt - 1)) * 8 * NR, phase = warp / mt;
     // the most keys that a row of the warp sees, and the fewest
-    const int lim_top = keys_seen(q, p.by_G.of(min(it.rows, row_base + 8 * NR) - 1)), lim_low = keys_seen(q, p.by_G.of(row_base));
+    const int lim_top = keys_seen(q, p.by_G.of(row0 + min(it.rows, row_base + 8 * NR) - 1)), lim_low = keys_seen(q, p.by_G.of(row0 + row_base));
     uint4 raw[NR][D / 32];                     // elements (D / 4) t .. of rows g and g + 8
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      const int row = row_base + 8 * n + g, tok = p.by_G.of(row), head = kvh * p.G + row - tok * p.G;
+      const int row = row_base + 8 * n + g, tok = p.by_G.of(row0 + row), head = kvh * p.G + row0 + row - tok * p.G;
       const uint16_t* src = p.a.Q + (q.first + tok) * p.a.q_stride + head * D + (D / 4) * t;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) raw[n][i] = row < it.rows ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
       for (int i = 0; i < 2; ++i) {
         crow[2 * n + i] = F16 ? p.c : __shfl_sync(0xffffffffu, c, 4 * (2 * t + i));
         const int mine = row_base + 8 * n + 2 * t + i;
-        lim[2 * n + i] = mine < it.rows ? keys_seen(q, p.by_G.of(mine)) : 0;
+        lim[2 * n + i] = mine < it.rows ? keys_seen(q, p.by_G.of(row0 + mine)) : 0;
       }
     }
 
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
     seg.ctas(place.share, c0, c1);
     const auto finish = [&](int row, int col, const float4& o, float top, float total) {
       const float inv = total == 0.f ? 0.f : 1.f / total;
-      const int tok = p.by_G.of(row), head = kvh * p.G + row - tok * p.G;
+      const int tok = p.by_G.of(row0 + row), head = kvh * p.G + row0 + row - tok * p.G;
       const int64_t at_row = static_cast<int64_t>(q.first + tok) * p.a.Hq + head;
       *reinterpret_cast<uint2*>(p.a.O + at_row * D + col) =
           make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
@@ -1639,12 +1641,14 @@ cudaError_t launch_t(const AttnE4m3Args& a, uint8_t* ws, cudaStream_t stream) {
   p.log_page = 4;
   while ((1 << p.log_page) < a.page_size) ++p.log_page;
   p.c = a.scale * 1.4426950408889634f;
-  // Requests of up to 32 rows a head, or of up to 8 where a call also has longer ones and a single token's rows are no
-  // more (the decoding requests beside prompts), go to the first kernel.  64 heads of 128 on 8, in us, first kernel with
-  // 3 / 4 / 6 / 8 new tokens (24 .. 64 rows) and second one with 6 .. 12: 4 requests over up to 40000 keys 55 / 59 / 103 /
-  // 114 and 69; 48 requests over up to 4096 66 / 72 / 124 / 138 and 87; the same with heads of 64 38 / 41 / 66 / 73 and 81.
-  p.few = rows <= kFewMostRows || p.G > 8 ? kFewMostRows : 8;
-  p.beside = rows > kFewMostRows;
+  // Requests of up to 32 rows a head (64 with heads of 64), or of up to 8 where a call also has longer ones and a single
+  // token's rows are no more (the decoding requests beside prompts), go to the first kernel.  First / second kernel with
+  // 24, 32, 40, 48, 64, 96 rows (8 heads a key head), in us: 4 requests over up to 40000 keys 50 / 71, 53 / 72, 72 / 72,
+  // 72 / 73, 80 / 71, 114 / 73; 48 over up to 4096 63 / 88, 68 / 88, 89 / 89, 94 / 89, 110 / 88, 154 / 90; heads of 64: the
+  // latter 38 / 80, 41 / 79, 52 / 81, 55 / 81, 65 / 81, 89 / 85.
+  constexpr int kMost = few_most_rows(D);
+  p.few = rows <= kMost || p.G > 8 ? kMost : 8;
+  p.beside = rows > kMost;
   if (p.beside) {
     const cudaError_t e = launch_many<F16, D>(p, l, ws, stream);
     if (e != cudaSuccess) return e;

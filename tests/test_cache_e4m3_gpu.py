@@ -347,6 +347,8 @@ ROWS = [  # lens, new tokens, Hq, Hkv: rows of a head (new tokens x Hq / Hkv) on
     ([64, 60, 700], [10, 33, 12], 8, 2),                           # 40, 132, 48: key tiles in turn, and not
     ([5, 64, 63, 65, 129], [5, 9, 16, 10, 7], 16, 2),              # 40 .. 128 over one key tile, or two or three
     ([140, 300, 40], [32, 65, 33], 8, 2),                          # 128, 260, 132: on both sides of a lane and of an item
+    ([200, 90, 300], [16, 13, 9], 8, 2),                           # 64, 52, 36
+    ([70, 1100], [5, 6], 30, 3),                                   # 50, 60 of ten heads
     ([400, 60, 300, 90, 17], [100, 1, 1, 2, 1], 14, 2),            # decoding requests beside a prompt
     ([300, 40, 5, 260], [30, 1, 0, 2], 20, 1),                     # 600, 20, none, 40
     ([33, 2, 1, 500], [33, 2, 1, 0], 8, 1),                        # as long as the request
