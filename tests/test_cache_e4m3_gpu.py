@@ -651,6 +651,77 @@ def test_captured_and_replayed_over_growing_requests(B):
         check(c, q, o, lse, now, [0, 1, 2, 3], None, "bf16")
 
 
+@pytest.mark.parametrize("dtype,Hq,d", [("bf16", 8, 128), ("f16", 24, 64)])
+def test_decoding_requests_beside_prompts_call_after_call(B, dtype, Hq, d):
+    """Appends and attention of both kinds of requests with nothing between the calls, eager and replayed: the same bits as
+    with a synchronisation after each (the tokens that a call reads change with every step)."""
+    import torch
+    rng = np.random.default_rng(8)
+    news = [1, 150, 1, 1, 2, 70, 1, 1]
+    lens = [int(n) for n in 150 + rng.integers(0, 3000, 8)]
+    T, starts = sum(news), i32(np.concatenate(([0], np.cumsum(news))))
+    c = Cache(75, lens, 2, d, 64)
+    c.append(B, c.new(1, sum(lens), dtype), lens, lens)
+    table, n = i32(c.table), i32(lens)
+    steps = [c.new(100 + i, T, dtype, 1.0 + i)[0] for i in range(12)]
+    q = torch.randn(T, Hq, d, generator=torch.Generator().manual_seed(1)).to(_dt(dtype)).cuda()
+    ws = torch.zeros(B.load_library().wq_attn_e4m3_workspace_bytes(T, 8, Hq, 2, d, 150), dtype=torch.uint8, device="cuda")
+    fresh = [x.clone() for x in c.dev]
+
+    def go(each, wait=False):
+        for x, saved in zip(c.dev, fresh):
+            x.copy_(saved)
+        torch.cuda.synchronize()
+        got = []
+        for k, v in steps:
+            got.append(each(k, v))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return got
+
+    def call(k, v):
+        B.kv_append_e4m3(k, v, *c.dev, table, n, starts, 150)
+        return B.attn_e4m3(q, *c.dev, table, n, starts, 150, workspace=ws)
+
+    want = go(call, wait=True)
+    assert not torch.equal(want[0][0], want[1][0])
+    kv = [x.clone() for x in steps[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = call(*kv)
+
+    def replayed(k, v):
+        kv[0].copy_(k), kv[1].copy_(v)
+        graph.replay()
+        return o.clone(), lse.clone()
+    for _ in range(5):
+        for got in (go(call), go(replayed)):
+            assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))
+    assert not ws[:64 * 1024].any()
+    c.host = [x.cpu().numpy() for x in c.dev]
+    check(c, q, *want[-1], lens, starts.cpu().numpy(), None, dtype)
+
+
+@pytest.mark.parametrize("news", [1, 3, 70])
+def test_attend_non_finite_queries_stay_in_their_rows(B, news):
+    import torch
+    lens = [news + 90, news + 300]
+    c = Cache(76, lens, 2, 64, 32).fill(B, lens)
+    for dtype in ("bf16", "f16"):
+        q = torch.randn(2 * news, 8, 64, generator=torch.Generator().manual_seed(1)).to(_dt(dtype)).cuda()
+        starts = [0, news, 2 * news]
+        want = B.attn_e4m3(q, *c.dev, i32(c.table), i32(lens), i32(starts), news)
+        bad = q.clone()
+        bad[0, 1, 3], bad[-1, 6, 0], bad[-1, 7, 63] = float("nan"), float("inf"), -float("inf")
+        got = B.attn_e4m3(bad, *c.dev, i32(c.table), i32(lens), i32(starts), news)
+        hit = torch.zeros(2 * news, 8, dtype=torch.bool, device="cuda")
+        hit[0, 1] = hit[-1, 6] = hit[-1, 7] = True
+        for a, b in zip(got, want):
+            assert torch.equal(a[~hit], b[~hit])
+        assert not torch.isfinite(got[0][hit]).any()
+
+
 def test_rejects_bad_arguments(B):
     import torch
     c = Cache(55, [40, 33], 2, 64, 16)
