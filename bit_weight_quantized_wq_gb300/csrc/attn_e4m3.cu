@@ -6,7 +6,8 @@
 // so a page's scales cost one multiply-add a score, and the weights w of the second product are largest
 // where their products with the codes are, whatever the scales are: m follows the largest x, not the
 // largest score.  Codes are exact in fp16.  A bf16 query is too, behind a power of two a row; w is rounded
-// to fp16 (11 bits) for the second product, its sum kept in float32 unrounded.
+// to fp16 (11 bits) for the second product, its sum kept in float32 unrounded.  (Float32 ends 2^-133 below the largest
+// w, so with exponents ev 100 apart what the sum loses of a key is below 2^-33 of the whole.)
 //
 // Work.  An item is a tile of query rows of one request and key/value head (row = new token * G + query
 // head of the group, G = Hq / Hkv) against the keys that its last row sees, in tiles of 64.  All items'
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
       }
     }
 
-    // ------------------------------------------------------------------ its stages
+    // ------------------------------------------------------------------ its steps
     float acc[KS][NR][4];
 #pragma unroll
     for (int j = 0; j < KS; ++j)
@@ -856,7 +857,8 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
         // two units where there are more than threads, eight segments at a time.  (One unit after the other: 8 requests of 4
         // new tokens over up to 8192 keys, 32 heads on 8, 25.6 us, so 22.0; two also where there is one: one request over 500
         // keys 6.7, so 7.1.)
-        const int parts = units * 8 <= L::kThreads ? 8 : units * 4 <= L::kThreads ? 4 : units * 2 <= L::kThreads ? 2 : 1, part = threadIdx.x & (parts - 1);
+        const int parts = units * 8 <= L::kThreads ? 8 : units * 4 <= L::kThreads ? 4 : units * 2 <= L::kThreads ? 2 : 1;
+        const int part = threadIdx.x & (parts - 1);
         const auto join = [&](auto each) {
           constexpr int U = decltype(each)::value, kApart = L::kThreads / (D / 4);      // rows from a thread's unit to its next
 #pragma unroll 1
@@ -1077,8 +1079,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       }
     } else if (warp == kWCopy) {
       // ------------------------------------------------------------------ codes and scales
-      copy_items<L, D, kTile, kRawStages>(p, tk, tv, [&] { return segment(0); }, segment_done, [&](uint32_t i) { return sm.raw[i % kRawStages][0]; }, sm.raw_full, sm.raw_empty,
-                                          [&](uint32_t i) { return sm.scales[i % kScaleRing]; }, &sm.failed);
+      copy_items<L, D, kTile, kRawStages>(
+          p, tk, tv, [&] { return segment(0); }, segment_done, [&](uint32_t i) { return sm.raw[i % kRawStages][0]; }, sm.raw_full,
+          sm.raw_empty, [&](uint32_t i) { return sm.scales[i % kScaleRing]; }, &sm.failed);
     } else if (warp < kWMma) {
       // ------------------------------------------------------------------ codes -> fp16
       // Two warps widen K, two V, so that neither waits for the other's barriers.  A thread widens 16 codes at a time, of
@@ -1535,8 +1538,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
 #pragma unroll
                   for (int e = 0; e < 8; ++e) {
                     uint32_t* a = &sums[4 * e];
-                    a[0] = __float_as_uint(fmaf(v[i][e].x, scale, __uint_as_float(a[0]))), a[1] = __float_as_uint(fmaf(v[i][e].y, scale, __uint_as_float(a[1])));
-                    a[2] = __float_as_uint(fmaf(v[i][e].z, scale, __uint_as_float(a[2]))), a[3] = __float_as_uint(fmaf(v[i][e].w, scale, __uint_as_float(a[3])));
+                    const float4& x4 = v[i][e];
+                    a[0] = __float_as_uint(fmaf(x4.x, scale, __uint_as_float(a[0])));
+                    a[1] = __float_as_uint(fmaf(x4.y, scale, __uint_as_float(a[1])));
+                    a[2] = __float_as_uint(fmaf(x4.z, scale, __uint_as_float(a[2])));
+                    a[3] = __float_as_uint(fmaf(x4.w, scale, __uint_as_float(a[3])));
                   }
                 }
               }

@@ -401,6 +401,26 @@ def test_attend_scales_that_differ_widely_between_pages(B, dtype, d, news):
     _attend(B, c, lens, [news, news], 8, dtype, scale=4.0)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("news", [1, 5, 70])
+def test_attend_value_scales_a_hundred_powers_of_two_apart(B, dtype, d, news):
+    """What a sum loses of a key is below 2^-33 of it here: in the limit's n 2^-32 of the largest value."""
+    import torch
+    lens = [news + 220, news + 64]
+    c = Cache(77, lens, 2, d, 16).fill(B, lens)
+    rng = np.random.default_rng(1)
+    c.host[2][:] = 127 - 8 + rng.integers(-3, 2, c.host[2].shape)
+    c.host[3][:] = 127 + rng.choice([-50, -49, 0, 49, 50], c.host[3].shape)
+    for i in (2, 3):
+        c.dev[i].copy_(torch.from_numpy(c.host[i]))
+    # the output's type ends before the largest values do: those of fp16 are taken out by a page's exponent
+    if dtype == "f16":
+        c.host[3][:] -= 50
+        c.host[3][:] = np.maximum(c.host[3], 63)
+        c.dev[3].copy_(torch.from_numpy(c.host[3]))
+    _attend(B, c, lens, [news, news], 8, dtype)
+
+
 @pytest.mark.parametrize("where", [63, 191])
 def test_attend_scales_at_their_limits(B, where):
     import torch
