@@ -117,8 +117,9 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 
 // N threads (a warp or the CTA) have a page of one head's keys or values: P pieces of 8 elements each.
-// Bound by the bytes (2 read, 1 written an element) for prompts, by launch and dependent loads for
-// decoding (starts and lengths, then the page and the tokens).
+// Bound by the bytes (2 read, 1 written an element) for prompts: 11006 tokens of 8 heads of 128 in pages of 64 take
+// 12.5 us, 5.4 TB/s (256 threads a page and head 13.6, 512 20.8: fewer bytes under way before a page's maximum is
+// known); by launch and dependent loads for decoding (starts and lengths, then the page and the tokens): one token 2.1 us.
 template <bool F16, int D, int N, int P>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs a, int each) {
   constexpr int kRow = D / 8;                  // pieces a token
