@@ -32,6 +32,7 @@
 
 #include "internal.h"
 #include "kv_e4m3.cuh"
+#include "line.cuh"
 #include "tcgen05.cuh"
 
 namespace wq {
@@ -62,21 +63,13 @@ struct Divisor {
   __device__ int of(int n) const { return static_cast<int>((__umulhi(n, mul) + static_cast<uint32_t>(n)) >> shift); }
 };
 
-// a / b of positions on a line, exact where it is below 2^20 (a 64-bit division takes some hundred instructions).
-__device__ __forceinline__ int quotient(long long a, long long b) {
-  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
-  if (q * b > a) --q;
-  else if ((q + 1) * b <= a) ++q;
-  return q;
-}
-
 struct Params {
   AttnE4m3Args a;
   int G, log_page;
   Divisor by_G;
   int few;                   // requests of up to so many rows are the first kernel's
   float c;                   // scale * log2(e)
-  int* count;                // segments (or groups) that are done of the item that begins in a CTA, and of the group [2][ctas]
+  int* count;                // segments (or groups) that are done of the item, and of the group, that begins in a CTA [2][ctas]
   float *po;                 // partials [cta][2][rows of an item][d], largest exponents and sums [cta][2][rows][2]
   float2 *ml;
   bool beside;               // the kernel for few rows: behind the other one of the same call
@@ -254,14 +247,10 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   __shared__ long long found_at, found_head;
   __shared__ int found_r;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // An equal share, rounded up so that the shares cover the line; for many rows by no more than has to be, or cuts drift
-  // into items that fit the CTAs: 152 items of 512 keys 37 us, exactly 23.  (For few rows that took 0.2 us and gave none.)
+  // Shares rounded up exactly for many rows, or cuts drift into items that fit the CTAs: 152 items of 512 keys 37 us, exactly
+  // 23.  (For few rows that took 0.2 us and gave none.)
   const auto take = [&](Place& s, long long total) {
-    const long long ctas = gridDim.x;
-    s.share = max(static_cast<long long>(L::kMost),
-                  static_cast<long long>(__fdividef(static_cast<float>(total), static_cast<float>(ctas)) * 1.000001f) + 1);
-    if constexpr (L::kRows == kManyRows)
-      while (s.share > L::kMost && (s.share - 1) * ctas >= total) --s.share;
+    s.share = line_share(total, gridDim.x, L::kMost, L::kRows == kManyRows);
     s.b0 = blockIdx.x * s.share;
   };
   // line length of a head of request r (none past the last); all lanes of the warp
@@ -316,25 +305,14 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   return s;
 }
 
-// An item's segments are joined in line order by the last CTA that is done with it, or, where there are more of them
-// than kGroup, in two steps: groups of kGroup neighbours, each joined in the place of its first, then the groups.
-constexpr int kGroup = 8;
-
-// Counts this CTA's segment of an item that CTAs c0 .. c1 share; true in the one that is last, which sees what the
-// others have written.  After a barrier of the CTA's writers, by one thread.
-__device__ __forceinline__ bool last_segment(int* count, int segments) {
+// Counts this CTA's part of one step of a join; true in the CTA that is the last of n, which sees what the others have
+// written, and leaves the counter at 0.  After a barrier of the CTA's writers, by one thread.
+__device__ __forceinline__ bool last_part(int* count, int n) {
   int done;
   asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(done) : "l"(count) : "memory");
-  if (done + 1 < segments) return false;
+  if (done + 1 < n) return false;
   *count = 0;
   return true;
-}
-
-// First tile of an item (line start s, tiles n of weight w) that starts at or after position b.
-__device__ __forceinline__ int tile_at(long long b, long long s, int n, int w) {
-  if (b <= s) return 0;
-  const long long d = b - s;
-  return d >= static_cast<long long>(n) * w ? n : (static_cast<int>(d) + w - 1) / w;
 }
 
 // A segment: what one CTA has of an item.
@@ -837,22 +815,15 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
       }
     }
     if (!whole) {
-      const int segments = c1 - c0 + 1, group = (cta - c0) / kGroup;
-      const auto last = [&](int* count, int n) {
+      const auto last = [&](const Join& j) {
         __syncthreads();
-        if (threadIdx.x == 0) sm.last = last_segment(count, n);
+        if (threadIdx.x == 0) sm.last = last_part(p.count + j.counter, j.n);
         __syncthreads();
         return sm.last != 0;
       };
-      int first = c0, step = 1, n = segments;
-      bool final = true, mine;
-      if (segments > kGroup) {
-        first = c0 + group * kGroup, n = min(kGroup, c1 - first + 1), final = false;
-        mine = last(p.count + gridDim.x + first, n);
-      } else {
-        mine = last(p.count + c0, n);
-      }
-      while (mine) {
+      Join round = first_join(c0, c1, cta, gridDim.x);
+      while (last(round)) {
+        const int first = round.first, step = round.step, n = round.n;
         // Few loads wait for others: neighbouring threads (`parts` of them) take a unit's segments in turn, or a thread has
         // two units where there are more than threads, eight segments at a time.  (One unit after the other: 8 requests of 4
         // new tokens over up to 8192 keys, 32 heads on 8, 25.6 us, so 22.0; two also where there is one: one request over 500
@@ -920,7 +891,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
               for (int k = 0; k < U; ++k) {
                 if (k == 1 && !two) break;
                 const int r = row + k * kApart;
-                if (final) {
+                if (round.final) {
                   finish(r, col, o[k], top[k], total[k]);
                 } else {
                   *reinterpret_cast<float4*>(p.po + (slot(0) + k * kApart) * D + col) = o[k];
@@ -932,12 +903,11 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
         };
         if (units <= L::kThreads) join(std::integral_constant<int, 1>());
         else join(std::integral_constant<int, 2>());
-        if (final) break;
+        if (round.final) break;
         __syncthreads();                       // all have read what the group's first CTA left
         for (int row = threadIdx.x; row < it.rows; row += L::kThreads)
           p.ml[(2ll * first + (first == c0 ? 1 : 0)) * L::kRows + row] = sm.ml[row / (8 * NR)][row % (8 * NR)];
-        first = c0, step = kGroup, n = (segments + kGroup - 1) / kGroup, final = true;
-        mine = last(p.count + c0, n);
+        round = final_join(c0, c1);
       }
     }
     __syncthreads();                           // and the ring again
@@ -1487,22 +1457,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       else __syncwarp();
       if (had && lane == 0) mbar_arrive(&sm.o_empty[l]);
       if (!whole) {
-        const int segments = c1 - c0 + 1, cta = blockIdx.x;
-        const auto last = [&](int* count, int n) {
+        const auto last = [&](const Join& j) {
           meet();
-          if (threadIdx.x == 0) sm.last = last_segment(count, n);
+          if (threadIdx.x == 0) sm.last = last_part(p.count + j.counter, j.n);
           meet();
           return sm.last != 0;
         };
-        int first = c0, step = 1, n_parts = segments;
-        bool final = true, joins;
-        if (segments > kGroup) {
-          first = c0 + (cta - c0) / kGroup * kGroup, n_parts = min(kGroup, c1 - first + 1), final = false;
-          joins = last(p.count + gridDim.x + first, n_parts);
-        } else {
-          joins = last(p.count + c0, n_parts);
-        }
-        while (joins) {
+        Join round = first_join(c0, c1, blockIdx.x, gridDim.x);
+        while (last(round)) {
+          const int first = round.first, step = round.step, n_parts = round.n;
           if (out) {                           // a row's partials are read and written by its thread alone
             float top = -INFINITY, total = 0.f;
 #pragma unroll 4
@@ -1546,18 +1509,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
                   }
                 }
               }
-              if (final) {
+              if (round.final) {
                 finish(q, sums, inv);
               } else {
                 put_part(first, q, sums);
               }
             }
-            if (final) finish_lse(top, total);
+            if (round.final) finish_lse(top, total);
             else p.ml[slot(first) * kManyRows + row_item] = make_float2(top, total);
           }
-          if (final) break;
-          first = c0, step = kGroup, n_parts = (segments + kGroup - 1) / kGroup, final = true;
-          joins = last(p.count + c0, n_parts);
+          if (round.final) break;
+          round = final_join(c0, c1);
         }
       }
       segment_done();

@@ -811,3 +811,93 @@ def test_example_of_a_served_block(B):
     example = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(example)
     assert example.main() < 2.0 ** -4
+
+
+# ------------------------------------------------------------- items cut over many CTAs, neighbours in one of them
+class LongCache:
+    """Random codes and scales made on the GPU, for caches too long for the host's oracle."""
+
+    def __init__(self, seed, lens, Hkv, d, page):
+        import torch
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        blocks = [-(-n // page) for n in lens]
+        pages = sum(blocks) + 3
+        perm = torch.randperm(pages, generator=g, device="cuda").int().cpu().numpy()
+        self.table, at = np.full((len(lens), max(blocks)), -1, np.int32), 0
+        for r, b in enumerate(blocks):
+            self.table[r, :b] = perm[at:at + b]
+            at += b
+        self.dev = []
+        for _ in range(2):
+            codes = torch.empty(pages, Hkv, page, d, dtype=torch.uint8, device="cuda")
+            for i in range(0, pages, 512):
+                x = torch.randn(codes[i:i + 512].shape, generator=g, device="cuda") * 64
+                codes[i:i + 512] = x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            self.dev.append(codes)
+        self.dev += [torch.randint(119, 122, (pages, Hkv), generator=g, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        self.d, self.Hkv = d, Hkv
+
+    def tokens(self, i, r, h, n):
+        """Keys (i = 0) or values of the first n tokens of a request's head, float64."""
+        import torch
+        page = self.dev[i].shape[2]
+        p = torch.from_numpy(self.table[r, :-(-n // page)]).long().cuda()
+        x = torch.from_numpy(c8.VALUES).cuda()[self.dev[i][p, h].long()] * torch.exp2(self.dev[i + 2][p, h].double() - c8.BIAS)[:, None, None]
+        return x.reshape(-1, self.d)[:n]
+
+    def check(self, q, o, lse, lens, news, dtype):
+        """All rows against float64, computed on the GPU."""
+        import torch
+        group, scale, t = q.shape[1] // self.Hkv, self.d ** -0.5, 0
+        for r, (n, new) in enumerate(zip(lens, news)):
+            for h in range(self.Hkv):
+                k, v = self.tokens(0, r, h, n), self.tokens(1, r, h, n)
+                heads = slice(h * group, (h + 1) * group)
+                x = q[t:t + new, heads].double().reshape(-1, self.d)
+                score = scale * (x @ k.T)
+                hidden = torch.arange(n, device="cuda") > (n - new + torch.arange(new, device="cuda").repeat_interleave(group))[:, None]
+                reach = scale * (x.abs() @ k.abs().T).amax(1)
+                score.masked_fill_(hidden, -float("inf"))
+                ref_lse, p = torch.logsumexp(score, 1), torch.softmax(score, 1)
+                ref, oabs = (_host((p @ w).view(new, group, -1)) for w in (v, v.abs()))
+                ref_lse, reach = _host(ref_lse.view(new, group)), _host(reach.view(new, group))
+                what = "request %d, head %d: " % (r, h)
+                _within(_host(o[t:t + new, heads]), ref, _limit(ref, oabs, reach, n, float(v.abs().max()), dtype), what + "O")
+                _within(_host(lse[t:t + new, heads]), ref_lse, _lse_limit(ref_lse, reach, n), what + "lse")
+            t += new
+
+
+CUT = [  # lens, new tokens, Hq, Hkv, d, dtype: items of more than eight segments, the next one beginning where one ends
+    ([74000], [1], 40, 5, 128, "bf16"),
+    ([131071 - 997 * i for i in range(9)], [1] * 9, 64, 8, 128, "bf16"),
+    ([int(32768 * 4 ** (i / 11)) for i in range(12)], [1] * 12, 64, 8, 128, "f16"),
+    ([8000 + 8000 * i for i in range(8)], [4] * 8, 64, 8, 128, "bf16"),
+    ([65000, 30011, 50000, 41000], [3, 2, 4, 1], 16, 16, 64, "f16"),
+    ([25500], [128], 40, 5, 128, "bf16"),
+    ([32663, 52569], [16, 64], 64, 8, 128, "bf16"),
+    ([120000, 90000, 131071, 3000, 65536], [1, 1, 1, 200, 1], 64, 8, 128, "bf16"),
+    ([11489, 18484, 42577, 49181], [1, 64, 24, 40], 24, 3, 64, "f16"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CUT)))
+def test_attend_neighbouring_items_cut_in_groups(B, case):
+    """Every row of every call is written, the same each time, and the workspace's header is left at zero."""
+    import torch
+    lens, news, Hq, Hkv, d, dtype = CUT[case]
+    c = LongCache(80 + case, lens, Hkv, d, 64)
+    T = sum(news)
+    q = torch.randn(T, Hq, d, generator=torch.Generator().manual_seed(case)).to(_dt(dtype)).cuda()
+    table, n, starts = i32(c.table), i32(lens), i32(np.concatenate(([0], np.cumsum(news))))
+    ws = torch.zeros(B.load_library().wq_attn_e4m3_workspace_bytes(T, len(lens), Hq, Hkv, d, max(news)), dtype=torch.uint8, device="cuda")
+    outs = [(torch.full((T, Hq, d), float("nan"), dtype=_dt(dtype), device="cuda"), torch.full((T, Hq), float("nan"), device="cuda"))
+            for _ in range(30)]
+    for i, out in enumerate(outs):                    # some with nothing between them, some each by itself
+        B.attn_e4m3(q, *c.dev, table, n, starts, max(news), out=out, workspace=ws)
+        if i >= 20:
+            assert not ws[:64 * 1024].any()
+    torch.cuda.synchronize()
+    assert not ws[:64 * 1024].any()
+    for o, lse in outs:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+    c.check(q, *outs[0], lens, news, dtype)
