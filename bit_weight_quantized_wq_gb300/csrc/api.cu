@@ -914,8 +914,10 @@ wq_status wq_attn_e4m3(wq_dtype dtype, const uint16_t* Q, int64_t q_stride, int6
   wq_status st = check_cache8(c, T, R, block_table, max_blocks);
   if (st != WQ_OK) return st;
   if (!aligned16(Q) || !aligned16(O) || odd4(lse) || odd4(lens) || odd4(q_start)) return WQ_ERR_ALIGN;
-  const size_t out = static_cast<size_t>(T) * Hq * d * 2;
-  if (overlap(Q, (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2, O, out) || c.overlaps(O, out)) return WQ_ERR_ARG;
+  const size_t in = (static_cast<size_t>(T - 1) * q_stride + Hq * d) * 2, out = static_cast<size_t>(T) * Hq * d * 2;
+  const size_t stats = static_cast<size_t>(T) * Hq * sizeof(float);
+  if (overlap(Q, in, O, out) || c.overlaps(O, out)) return WQ_ERR_ARG;
+  if (lse && (overlap(Q, in, lse, stats) || overlap(O, out, lse, stats) || c.overlaps(lse, stats))) return WQ_ERR_ARG;
   if (!workspace || ws_bytes < wq_attn_e4m3_workspace_bytes(T, R, Hq, Hkv, d, max_new)) return WQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return WQ_ERR_ALIGN;
   st = check_device_cached();

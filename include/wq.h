@@ -633,15 +633,15 @@ wq_status wq_kv_read_e4m3(wq_dtype dtype, const uint8_t* k_cache, const uint8_t*
  *   Q [T, Hq, d]: tokens q_stride elements apart (a multiple of 8, at least Hq d).
  *   Places past a request's length are not used, whatever they hold.  A NaN among the request's values
  *     reaches every row that sees it, and of its own new tokens may reach those before it.
- *   O [T, Hq, d] dtype, lse [T, Hq] float32 (may be NULL): contiguous outputs, distinct from Q.
+ *   O [T, Hq, d] dtype, lse [T, Hq] float32 (may be NULL): contiguous outputs, distinct from Q, the cache and each other.
  *   workspace / ws_bytes: at least wq_attn_e4m3_workspace_bytes(...) bytes, under the workspace rules of
  *     wq_gemm_workspace_bytes (it starts with the same header, left at zero).
  * The weights of the values are rounded to fp16 (11 bits), their sum is not; queries and codes are exact.
  * A key whose weight times its page's value scale is below 2^-133 of the largest such product counts as nothing:
  * that shows in no result where the value scales of a request's head are within 2^100 of one another.
- * Errors: WQ_ERR_ARG (dtype; scale not positive and finite); WQ_ERR_NULL; WQ_ERR_SHAPE unless T, R, Hq, Hkv, pages,
- *   max_new, max_blocks >= 1, T, R <= 2^24, Hq <= 1024, Hq % Hkv == 0, Hq / Hkv <= 128, T * (Hq / Hkv) <= 2^30,
- *   the cache as above; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.
+ * Errors: WQ_ERR_ARG (dtype; scale not positive and finite; O or lse overlapping Q, the cache or each other); WQ_ERR_NULL;
+ *   WQ_ERR_SHAPE unless T, R, Hq, Hkv, pages, max_new, max_blocks >= 1, T, R <= 2^24, Hq <= 1024, Hq % Hkv == 0,
+ *   Hq / Hkv <= 128, T * (Hq / Hkv) <= 2^30, the cache as above; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.
  */
 size_t wq_attn_e4m3_workspace_bytes(int64_t T, int64_t R, int64_t Hq, int64_t Hkv, int64_t d, int64_t max_new);
 wq_status wq_attn_e4m3(wq_dtype dtype, const uint16_t* Q, int64_t q_stride, int64_t T, int64_t R, int64_t Hq, int64_t Hkv,

@@ -164,3 +164,12 @@ def test_attend_refusals(lib):
     assert _attend(lib, lse=_p(5, 2)) == 3 and _attend(lib, qs=_p(3, 2)) == 3
     assert _attend(lib, O=_p(0)) == 7 and _attend(lib, O=_p(0, 1024)) == 7 and _attend(lib, O=_p(10)) == 7 and _attend(lib, O=_p(12)) == 7
     assert lib.wq_attn_e4m3_workspace_bytes(4, 2, 7, 2, 128, 1) == 0 and lib.wq_attn_e4m3_workspace_bytes(4, 2, 8, 2, 96, 1) == 0
+
+
+def test_attend_refuses_outputs_that_overlap(lib):
+    """lse is stored while other CTAs still read queries and codes: it shares no byte with them, nor with O."""
+    stats, last = 4 * 8 * 4, 3 * 1024 * 2 + 8 * 128 * 2                   # bytes of lse, and of Q from its first to its last element
+    for name, at in (("Q", 0), ("O", 4), ("k_cache", 10), ("v_cache", 11), ("k_scales", 12), ("v_scales", 13)):
+        assert _attend(lib, lse=_p(at)) == 7, name
+        assert _attend(lib, lse=ctypes.c_void_p(_p(at).value - stats + 4)) == 7, name
+    assert _attend(lib, lse=_p(0, last - 4)) == 7 and _attend(lib, lse=_p(4, 4 * 8 * 128 * 2 - 4)) == 7
