@@ -901,3 +901,71 @@ def test_attend_neighbouring_items_cut_in_groups(B, case):
     for o, lse in outs:
         assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
     c.check(q, *outs[0], lens, news, dtype)
+
+
+# ---------------------------------------------------------------------------------- calls of many requests
+def _read_directly(c, starts, T, dtype):
+    """What a read gives, by indexing on the GPU; rows of no request are -1."""
+    import torch
+    rows, out = torch.arange(T, device="cuda"), []
+    s = torch.tensor(starts, device="cuda")
+    r = (torch.searchsorted(s, rows, right=True) - 1).clamp(0, len(starts) - 2)
+    place, mine = rows - s[r], (rows >= s[0]) & (rows < s[-1])
+    page = c.table[r, (place // 16).clamp(0, c.table.shape[1] - 1)].long().clamp(min=0)
+    for i in (0, 1):
+        x = torch.from_numpy(c8.VALUES).cuda()[c.dev[i][page, :, place % 16].long()] * torch.exp2(c.dev[i + 2][page].double() - c8.BIAS)[..., None]
+        out.append(torch.where(mine[:, None, None], x, -1.0).to(dtype))
+    return out
+
+
+class ManyRequests:
+    """Requests of random tokens in pages of 16, on the GPU alone."""
+
+    def __init__(self, seed, lens, Hkv, d):
+        import torch
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        blocks = -(-torch.tensor(lens) // 16)
+        pages = int(blocks.sum()) + 1
+        perm = torch.randperm(pages, generator=g, device="cuda").int()
+        most = max(1, int(blocks.max()))
+        at = torch.arange(most)[None] < blocks[:, None]
+        self.table = torch.full((len(lens), most), -1, dtype=torch.int32)
+        self.table[at] = perm[:int(blocks.sum())].cpu()
+        self.table = self.table.cuda()
+        codes = torch.randint(0, 254, (2, pages, Hkv, 16, d), generator=g, device="cuda", dtype=torch.uint8)
+        codes[(codes & 127) == 127] = 5
+        scales = torch.randint(110, 130, (2, pages, Hkv), generator=g, device="cuda", dtype=torch.uint8)
+        self.dev = [codes[0], codes[1], scales[0], scales[1]]
+
+
+@pytest.mark.parametrize("Hkv,d", [(2, 64), (1, 64), (8, 128)])
+@pytest.mark.parametrize("R", [256, 257, 1000, 70000])
+def test_read_of_many_requests(B, R, Hkv, d):
+    """Empty ones among them, rows before the first and behind the last left as they were."""
+    import torch
+    rng = np.random.default_rng(R)
+    lens = rng.choice([0, 0, 1, 1, 2, 3, 17, 40], R) if R < 10000 else rng.choice([0, 1, 2], R)
+    lens[rng.integers(0, R, 3)] = 300
+    lens[R // 3:R // 3 + 400] = 0                     # more empty ones in a row than threads
+    c = ManyRequests(R, lens.tolist(), Hkv, d)
+    for lead in (0, 5):
+        starts = np.concatenate(([lead], lead + np.cumsum(lens)))
+        T = int(starts[-1]) + 7
+        want = _read_directly(c, starts.tolist(), T, torch.bfloat16)
+        out = [torch.full((T, Hkv, d), -1.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        B.kv_read_e4m3(*c.dev, c.table, i32(starts), T, out=out)
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_read_of_many_requests_reports_starts_out_of_range(B):
+    import torch
+    lens = [3] * 900
+    c = ManyRequests(1, lens, 2, 64)
+    good = np.concatenate(([0], np.cumsum(lens)))
+    for at, value in ((0, -1), (1, -5), (450, 0), (450, 1 << 30), (899, 2), (900, 2701), (900, 5)):
+        starts = good.copy()
+        starts[at] = value
+        B.kv_read_e4m3(*c.dev, c.table, i32(starts), 2700)
+        assert B.read_error_flags() == 1 << 7, (at, value)
+    B.kv_read_e4m3(*c.dev, c.table, i32(good), 2700)
+    assert B.read_error_flags() == 0
