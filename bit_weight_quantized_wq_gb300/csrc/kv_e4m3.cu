@@ -78,30 +78,45 @@ __device__ __forceinline__ Touched touched_page(const KvAppendArgs& a, int r, in
   return u;
 }
 
-// The index-th page that the call writes.  With `each` pages for every request, whether it has them or not, each thread
-// finds it by itself; else the CTA counts them in the order of the requests.
-__device__ __forceinline__ Touched find_touched(const KvAppendArgs& a, int index, int each) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (each) {
-    const int r = each == 1 ? index : index / each, j = index - r * each;
-    int first, n, len;
-    bool bad;
+// How a CTA finds its page: each request has as many places (one, or two) whether it has pages for them or not; requests of
+// up to a CTA's threads have their pages counted; more have places that begin at first_place, and the CTA searches.
+enum class Find { kEach, kCount, kSearch };
+
+// Where request r's places begin: n tokens lie in at most n / page_size + 2 pages, and in at most n.
+__device__ __forceinline__ int first_place(const KvAppendArgs& a, int r, bool by_token) {
+  const int row = __ldg(a.q_start + r);
+  return by_token ? row : (row >> a.log_page) + 2 * r;
+}
+
+// The page of place `index`, if there is one; `places`: of each request (kEach), or 1: places by tokens (kSearch).
+template <Find HOW>
+__device__ __forceinline__ Touched find_touched(const KvAppendArgs& a, int index, int places) {
+  int first = 0, n = 0, len = 0;
+  bool bad = false;
+  if constexpr (HOW == Find::kEach) {
+    const int r = places == 1 ? index : index / places, j = index - r * places;
     const int c = touched_pages(a, r, first, n, len, bad);
     if (bad) atomicOr(&g_kv_err, kErrIndex);
     return j < c ? touched_page(a, r, first, n, len, j) : Touched{0, 0, 0, -1};
-  }
-  __shared__ int sums[kAppendThreads / 32];
-  __shared__ Touched out;
-  if (threadIdx.x == 0) out.page = -1;
-  int before = 0;
-  const bool checks = blockIdx.x == 0 && blockIdx.y == 0;    // one CTA looks at every request
-  for (int base = 0; base < a.R && (before <= index || checks); base += kAppendThreads) {
-    const int r = base + threadIdx.x;
-    int first = 0, n = 0, len = 0, c = 0;
+  } else if constexpr (HOW == Find::kSearch) {
+    if (blockIdx.y == 0)                       // each CTA checks some of the requests
+      for (int r = blockIdx.x * kAppendThreads + threadIdx.x; r < a.R; r += gridDim.x * kAppendThreads) {
+        touched_pages(a, r, first, n, len, bad);
+        if (bad) atomicOr(&g_kv_err, kErrIndex);
+      }
+    const int r = count_up_to<kAppendThreads>(a.R, index, [&](int i) { return first_place(a, i, places); }) - 1;
+    if (r < 0) return Touched{0, 0, 0, -1};
+    const int j = index - first_place(a, r, places), c = touched_pages(a, r, first, n, len, bad);
+    return 0 <= j && j < c ? touched_page(a, r, first, n, len, j) : Touched{0, 0, 0, -1};
+  } else {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = threadIdx.x;
+    __shared__ int sums[kAppendThreads / 32];
+    __shared__ Touched out;
+    if (threadIdx.x == 0) out.page = -1;
+    int c = 0;
     if (r < a.R) {
-      bool bad;
       c = touched_pages(a, r, first, n, len, bad);
-      if (bad && checks) atomicOr(&g_kv_err, kErrIndex);
+      if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(&g_kv_err, kErrIndex);
     }
     int in = c;
 #pragma unroll
@@ -111,16 +126,14 @@ __device__ __forceinline__ Touched find_touched(const KvAppendArgs& a, int index
     }
     if (lane == 31) sums[warp] = in;
     __syncthreads();
-    int at = before + in - c;
+    int at = in - c;
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 32; ++w) {
+    for (int w = 0; w < kAppendThreads / 32; ++w)
       if (w < warp) at += sums[w];
-      before += sums[w];
-    }
     if (at <= index && index < at + c) out = touched_page(a, r, first, n, len, index - at);
     __syncthreads();
+    return out;
   }
-  return out;
 }
 
 // The lowest exponent with amax <= 448 * 2^e = 1.75 * 2^(e + 8), kept in the range.
@@ -134,14 +147,14 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // Bound by the bytes (2 read, 1 written an element) for prompts: 11006 tokens of 8 heads of 128 in pages of 64 take
 // 12.5 us, 5.4 TB/s (256 threads a page and head 13.6, 512 20.8: fewer bytes under way before a page's maximum is
 // known); by launch and dependent loads for decoding (starts and lengths, then the page and the tokens): one token 2.1 us.
-template <bool F16, int D, int N, int P>
-__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs a, int each) {
+template <bool F16, int D, int N, int P, Find HOW>
+__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs a, int places) {
   constexpr int kRow = D / 8;                  // pieces a token
   constexpr uint32_t kInf = F16 ? 0x7c00u : 0x7f80u;
   __shared__ uint32_t tops[kAppendThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
-  const Touched u = find_touched(a, blockIdx.x, each);
+  const Touched u = find_touched<HOW>(a, blockIdx.x, places);
   if (u.page < 0) return;
   const int unit = blockIdx.y * (kAppendThreads / N) + threadIdx.x / N, j = threadIdx.x % N;
   const bool on = unit < 2 * a.Hkv;            // with N = 128 always
@@ -223,20 +236,27 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs
   }
 }
 
-template <bool F16, int D>
-cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
-  // pages that T tokens of R requests lie in, and that max_new tokens of one do
-  const int64_t most = std::min<int64_t>(a.T, a.T / a.page_size + 2ll * a.R);
-  const int one = 1 + (a.max_new + a.page_size - 2) / a.page_size;
-  // Where no request can have more than two, CTAs for as many each: 512 requests of one token 8.3 us counted, 6.0 so.
-  const int each = one <= 2 && static_cast<int64_t>(a.R) * one < 0x7fffffff ? one : 0;
-  const unsigned pages = static_cast<unsigned>(each ? a.R * one : most);
+template <bool F16, int D, Find HOW>
+cudaError_t launch_append_t(const KvAppendArgs& a, unsigned pages, int places, cudaStream_t stream) {
   const int pieces = std::min(a.page_size, a.max_new) * D / 8;
   if (pieces <= 4 * 32)
-    return launch_pdl(k_kv_append<F16, D, 32, 4>, dim3(pages, (2 * a.Hkv + 3) / 4), kAppendThreads, 0, stream, a, each);
+    return launch_pdl(k_kv_append<F16, D, 32, 4, HOW>, dim3(pages, (2 * a.Hkv + 3) / 4), kAppendThreads, 0, stream, a, places);
   const dim3 grid(pages, 2 * a.Hkv);
-  if (pieces <= 8 * 128) return launch_pdl(k_kv_append<F16, D, 128, 8>, grid, kAppendThreads, 0, stream, a, each);
-  return launch_pdl(k_kv_append<F16, D, 128, 16>, grid, kAppendThreads, 0, stream, a, each);
+  if (pieces <= 8 * 128) return launch_pdl(k_kv_append<F16, D, 128, 8, HOW>, grid, kAppendThreads, 0, stream, a, places);
+  return launch_pdl(k_kv_append<F16, D, 128, 16, HOW>, grid, kAppendThreads, 0, stream, a, places);
+}
+
+// Where no request can have more than two pages, as many places each: 512 requests of one token 8.3 us counted, 6.0 so.
+// Counting, which every CTA does for itself, is a load less than a search while it is one round of a CTA's threads (7
+// prompts 12.3 / 12.8 us); 512 requests with two pieces of 512 tokens among them 38 / 25 us, 4096 677 / 136.
+template <bool F16, int D>
+cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
+  const int each = 1 + (a.max_new + a.page_size - 2) / a.page_size;      // pages that max_new tokens of a request lie in
+  if (each <= 2) return launch_append_t<F16, D, Find::kEach>(a, static_cast<unsigned>(a.R) * each, each, stream);
+  const int64_t by_pages = a.T / a.page_size + 2ll * a.R;
+  const unsigned pages = static_cast<unsigned>(std::min<int64_t>(a.T, by_pages));
+  if (a.R <= kAppendThreads) return launch_append_t<F16, D, Find::kCount>(a, pages, 0, stream);
+  return launch_append_t<F16, D, Find::kSearch>(a, pages, a.T <= by_pages, stream);
 }
 
 // ------------------------------------------------------------------------------- reading back

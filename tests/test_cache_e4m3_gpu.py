@@ -969,3 +969,45 @@ def test_read_of_many_requests_reports_starts_out_of_range(B):
         assert B.read_error_flags() == 1 << 7, (at, value)
     B.kv_read_e4m3(*c.dev, c.table, i32(good), 2700)
     assert B.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("R", [128, 129, 700, 3000])
+@pytest.mark.parametrize("kind", ["single tokens and prompts", "pieces", "nearly all empty"])
+def test_append_to_many_requests(B, R, kind):
+    """More requests than a CTA's threads: empty ones, single tokens and pieces of several pages among them, a padded batch."""
+    rng = np.random.default_rng(R)
+    if kind == "single tokens and prompts":
+        news = np.ones(R, int)
+        news[rng.integers(0, R, 4)] = [200, 77, 16, 129]
+    elif kind == "pieces":
+        news = rng.integers(0, 60, R) if R < 1000 else rng.integers(0, 20, R)
+        news[R // 2] = 64
+    else:
+        news = np.zeros(R, int)
+        news[rng.integers(0, R, 5)] = [300, 1, 40, 17, 2]
+        news[0], news[-1] = 0, 33
+    news = [int(n) for n in news]
+    lens = [int(n + m) for n, m in zip(news, rng.integers(0, 40, R))]
+    c = Cache(90, lens, 1, 64, 16, spread=1.0).fill(B, [n - m for n, m in zip(lens, news)])
+    c.append(B, c.new(2, sum(news) + 3, "bf16", 4.0), lens, news)
+    c.check()
+    c.append(B, c.new(3, sum(news), "bf16", 4.0), [0] * R, news)          # all of them padding: nothing is written
+    c.check()
+
+
+def test_append_to_many_requests_reports_indices_out_of_range(B):
+    import torch
+    R = 600
+    news, lens = [1] * R, [30] * R
+    news[7] = 25
+    c = Cache(91, lens, 1, 64, 16).fill(B, lens)
+    kv, _ = c.new(1, sum(news), "bf16")
+    starts = np.concatenate(([0], np.cumsum(news)))
+    for which, at, value in (("starts", 300, 0), ("starts", 300, 1 << 30), ("starts", 0, -1), ("starts", R, sum(news) + 1), ("starts", 301, 360),
+                             ("lens", 599, -1), ("lens", 0, 1 << 20), ("lens", 7, 24), ("table", 599, -1), ("table", 0, 1 << 20)):
+        a = dict(starts=starts.copy(), lens=np.array(lens), table=c.table.copy())
+        a[which][(at, 1) if which == "table" else at] = value
+        B.kv_append_e4m3(*kv, *c.dev, i32(a["table"]), i32(a["lens"]), i32(a["starts"]), 25)
+        assert B.read_error_flags() == 1 << 7, (which, at, value)
+    B.kv_append_e4m3(*kv, *c.dev, i32(c.table), i32(lens), i32(starts), 25)
+    assert B.read_error_flags() == 0
