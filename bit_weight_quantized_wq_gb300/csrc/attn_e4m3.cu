@@ -236,7 +236,8 @@ __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volat
 
 // The line's length and the request in which position b0 lies; all threads of the CTA.
 struct Place {
-  long long share, b0, at;   // line units a CTA; where this CTA's begins; where request r begins
+  long long share, b0, b1;   // line units a CTA; where this CTA's begin and end
+  long long at;              // where request r begins
   long long head;            // line length of a head of it
   int r;                     // -1: nothing for this CTA
 };
@@ -251,7 +252,7 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   // 23.  (For few rows that took 0.2 us and gave none.)
   const auto take = [&](Place& s, long long total) {
     s.share = line_share(total, gridDim.x, L::kMost, L::kRows == kManyRows);
-    s.b0 = blockIdx.x * s.share;
+    s.b0 = blockIdx.x * s.share, s.b1 = min(s.b0 + s.share, total);
   };
   // line length of a head of request r (none past the last); all lanes of the warp
   const auto cost_of = [&](int r) {
@@ -345,7 +346,7 @@ struct Walk {
   int r, kvh, rt, rts;             // the next item; row tiles of its request
   Request q;
 
-  __device__ Walk(const Params& p_, const Place& s) : p(p_), b0(s.b0), b1(s.b0 + s.share), line(s.at), r(s.r), kvh(0), rt(0) {
+  __device__ Walk(const Params& p_, const Place& s) : p(p_), b0(s.b0), b1(s.b1), line(s.at), r(s.r), kvh(0), rt(0) {
     q = request(p.a, r);
     rts = row_tiles<L>(p, q);
     kvh = quotient(b0 - line, s.head);               // heads before the share, and row tiles
@@ -360,17 +361,33 @@ struct Walk {
       if (found) rt += at;
     }
   }
+  // To the first request from r on that has rows on this line, 32 at a time: a thousand of the other line lie between two
+  // prompts of a batch (one at a time, prompts at both ends of 1024 decoding requests took 278 us, so 107).
+  __device__ bool to_request() {
+    for (; r < p.a.R; r += 32) {
+      Request x{0, 0, 0, false};
+      const int lane = threadIdx.x & 31;
+      if (r + lane < p.a.R) x = request(p.a, r + lane);
+      const uint32_t here = __ballot_sync(0xffffffffu, row_tiles<L>(p, x) > 0);
+      if (here) {
+        const int at = __ffs(here) - 1;
+        r += at;
+        q.first = __shfl_sync(0xffffffffu, x.first, at), q.n = __shfl_sync(0xffffffffu, x.n, at);
+        q.len = __shfl_sync(0xffffffffu, x.len, at);
+        rts = row_tiles<L>(p, q);
+        return true;
+      }
+    }
+    return false;
+  }
   __device__ bool next(Segment& x) {
     while (line < b1) {
       if (rt == rts) {
         rt = 0;
-        if (rts == 0 || ++kvh == p.a.Hkv) {
-          kvh = 0;
-          if (++r == p.a.R) return false;
-          q = request(p.a, r);
-          rts = row_tiles<L>(p, q);
+        if (++kvh == p.a.Hkv) {
+          kvh = 0, ++r;
+          if (!to_request()) return false;
         }
-        continue;
       }
       const Shape it = shape<L>(p, q, rt);
       const long long start = line;

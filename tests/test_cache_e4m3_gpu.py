@@ -1011,3 +1011,17 @@ def test_append_to_many_requests_reports_indices_out_of_range(B):
         assert B.read_error_flags() == 1 << 7, (which, at, value)
     B.kv_append_e4m3(*kv, *c.dev, i32(c.table), i32(lens), i32(starts), 25)
     assert B.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("prompts", [{0: 60, 399: 90}, {0: 33}, {399: 100}, {31: 40, 32: 41, 33: 42, 300: 70}, {200: 50}])
+def test_attend_prompts_far_apart_among_many_requests(B, dtype, d, prompts):
+    """Hundreds of single tokens and of empty requests lie between, before and behind them."""
+    news = [1] * 400
+    for r in list(range(40, 120)) + list(range(330, 399)):
+        news[r] = 0
+    for r, n in prompts.items():
+        news[r] = n
+    lens = [n + m for n, m in zip(news, np.random.default_rng(9).integers(0, 40, 400).tolist())]
+    c = Cache(92, lens, 2, d, 16).fill(B, lens)
+    _attend(B, c, lens, news, 8, dtype)
