@@ -6,8 +6,11 @@
 // so a page's scales cost one multiply-add a score, and the weights w of the second product are largest
 // where their products with the codes are, whatever the scales are: m follows the largest x, not the
 // largest score.  Codes are exact in fp16.  A bf16 query is too, behind a power of two a row; w is rounded
-// to fp16 (11 bits) for the second product, its sum kept in float32 unrounded.  (Float32 ends 2^-133 below the largest
-// w, so with exponents ev 100 apart what the sum loses of a key is below 2^-33 of the whole.)
+// to fp16 for the second product, to 11 bits down to 2^-21 of the row's largest w and to steps of 2^-31 of that below: tensor
+// cores take 16 bits, and float32 weights in two parts would double a product that prompts are bound by.  It shows where
+// all that an element's result comes from has a w so small: pages of scales 2^21 below that of a page with zeros there.
+// The sum of the w stays in float32, unrounded.  (Float32 ends 2^-133 below the largest w, so with exponents ev 100 apart
+// what the sum loses of a key is below 2^-33 of the whole.)
 //
 // Work.  An item is a tile of query rows of one request and key/value head (row = new token * G + query
 // head of the group, G = Hq / Hkv) against the keys that its last row sees, in tiles of 64.  All items'

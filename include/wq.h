@@ -636,9 +636,12 @@ wq_status wq_kv_read_e4m3(wq_dtype dtype, const uint8_t* k_cache, const uint8_t*
  *   O [T, Hq, d] dtype, lse [T, Hq] float32 (may be NULL): contiguous outputs, distinct from Q, the cache and each other.
  *   workspace / ws_bytes: at least wq_attn_e4m3_workspace_bytes(...) bytes, under the workspace rules of
  *     wq_gemm_workspace_bytes (it starts with the same header, left at zero).
- * The weights of the values are rounded to fp16 (11 bits), their sum is not; queries and codes are exact.
- * A key whose weight times its page's value scale is below 2^-133 of the largest such product counts as nothing:
- * that shows in no result where the value scales of a request's head are within 2^100 of one another.
+ * Queries and codes are exact.  The second product takes each key's weight times its page's value scale in fp16: off by up
+ * to 2^-11 of itself, or, below 2^-21 of the row's largest such product, by up to 2^-32 of that one, so O by up to
+ * 2^-11 sum p |v| + n 2^-32 * 448 max_j p_j 2^e_j (n keys, e_j their value exponents).  Values in pages whose scale is 2^21
+ * or more below another page's so lose bits, also in elements where that page holds zeros (all of them at 2^32).
+ * The sum of the weights and lse are not rounded so: a key counts as nothing there below 2^-133 of the largest product, which
+ * shows in no result where the value scales of a request's head are within 2^100 of one another.
  * Errors: WQ_ERR_ARG (dtype; scale not positive and finite; O or lse overlapping Q, the cache or each other); WQ_ERR_NULL;
  *   WQ_ERR_SHAPE unless T, R, Hq, Hkv, pages, max_new, max_blocks >= 1, T, R <= 2^24, Hq <= 1024, Hq % Hkv == 0,
  *   Hq / Hkv <= 128, T * (Hq / Hkv) <= 2^30, the cache as above; WQ_ERR_ALIGN; WQ_ERR_WORKSPACE; WQ_ERR_UNSUPPORTED_ARCH; WQ_ERR_CUDA.

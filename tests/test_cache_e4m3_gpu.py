@@ -1025,3 +1025,36 @@ def test_attend_prompts_far_apart_among_many_requests(B, dtype, d, prompts):
     lens = [n + m for n, m in zip(news, np.random.default_rng(9).integers(0, 40, 400).tolist())]
     c = Cache(92, lens, 2, d, 16).fill(B, lens)
     _attend(B, c, lens, news, 8, dtype)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("news", [1, 5, 70])
+@pytest.mark.parametrize("apart", [10, 20, 30, 60])
+def test_attend_elements_where_a_page_of_large_scale_holds_zeros(B, dtype, d, news, apart):
+    """One value of the first page raises its scale by 2^apart, its others are zeros: the outputs' other elements come from
+    the other pages alone, to what wq.h says: 2^-11 of sum p |v| and n 2^-32 * 448 max p 2^e."""
+    import torch
+    lens = [news + 150, news + 60]
+    c = Cache(93, lens, 2, d, 16).fill(B, lens)
+    c.host[2][:] = 127 - 8
+    c.host[3][:] = 127 - 8 - (apart if dtype == "f16" else 0)
+    first = c.table[:, 0]
+    c.host[1][first] = 0
+    c.host[1][first, :, 3, 7] = 0x7E                                     # 448
+    c.host[3][first] += apart
+    for i in (1, 2, 3):
+        c.dev[i].copy_(torch.from_numpy(c.host[i]))
+    starts = [0, news, 2 * news]
+    q = torch.randn(2 * news, 8, d, generator=torch.Generator().manual_seed(1)).to(_dt(dtype)).cuda()
+    o, lse = B.attn_e4m3(q, *c.dev, i32(c.table), i32(lens), i32(starts), news)
+    ref, ref_lse, oabs, reach = c8.attend(_host(q), *c.host, c.table, lens, starts, d ** -0.5)
+    # 2^e of the largest scale for max p 2^e: p is at most 1
+    largest = 2.0 ** (int(c.host[3].max()) - 127)
+    eps = 2.0 ** -22 * (10 * reach[..., None] + 64) * 1.4427
+    n = max(lens)
+    limit = U[dtype] * np.abs(ref) + (2.0 ** -11 + 2 * eps + (n / 16 + 8) * 2.0 ** -22) * oabs + n * 2.0 ** -32 * 448 * largest
+    if dtype == "f16":
+        limit += 2.0 ** -25                                              # half the lowest step of the output's type
+    others = np.arange(d) != 7
+    _within(_host(o)[..., others], ref[..., others], limit[..., others], "O")
+    _within(_host(lse), ref_lse, _lse_limit(ref_lse, reach, n), "lse")
