@@ -220,6 +220,17 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
 // 0 and 255 times a weight of 0 are not 0.)
 constexpr uint32_t kNoScale = kScaleBias | (kScaleBias << 8);
 
+// 0xff in the bytes of four codes that are NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+// Four codes of a key's values from element `col` on; 0 where its page is out of range.
+__device__ __forceinline__ uint32_t value_codes(const Params& p, const int32_t* table, int head, int key, int d, int col) {
+  const int page = __ldg(table + (key >> p.log_page));
+  if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.a.pages)) return 0;
+  const int64_t at = ((static_cast<int64_t>(page) * p.a.Hkv + head) << p.log_page) + (key & (p.a.page_size - 1));
+  return __ldg(reinterpret_cast<const uint32_t*>(p.a.v_cache + at * d + col));
+}
+
 // A wait of a whole warp on a barrier in a ring, bounded as mbar_wait_short is; once one has run out, all others give up too.  `sleep_ns`: of
 // a warp that is far ahead, so that it leaves the issue slots to others.
 __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* failed, uint32_t code, uint32_t sleep_ns = 0) {
@@ -636,6 +647,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
     float m[R2], sum[R2];
 #pragma unroll
     for (int i = 0; i < R2; ++i) m[i] = -INFINITY, sum[i] = 0.f;
+    uint32_t odd = 0;                          // NaN that were taken out of values
 #pragma unroll 1
     for (int j = 0; j < steps; ++j) {
       // the scales of step j: the look-ups may be a window ahead
@@ -765,6 +777,17 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
               for (int w = 0; w < D / 32; ++w) v[i][w] = 0;
             }
         }
+        // A NaN among values that not all rows see would reach those rows too, as 0 times it: it is taken out, and put into
+        // the rows that see it with their output.
+        if (edge && lim_low < lim_top) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+              const uint32_t nan = nan_codes(v[i][w]);
+              v[i][w] &= ~nan, odd |= nan;
+            }
+        }
         // O^T += V^T P^T: tile c has bytes 2 c and 2 c + 1 of the threads' runs of d
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
@@ -793,7 +816,7 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
         dst[c / 2] = make_float4(a[i & 1], a[2 + (i & 1)], b[i & 1], b[2 + (i & 1)]);
       }
     }
-    __syncthreads();
+    const bool put_nan = __syncthreads_or(odd != 0);
     const bool whole = seg.whole();
     const int cta = blockIdx.x;
     int c0, c1;
@@ -825,6 +848,18 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
         total = fmaf(ml.y, f, total);
         const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][in][col]);
         o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+      }
+      if (__builtin_expect(put_nan, 0)) {      // the segment's keys that the row sees, of the steps that not all rows see
+        const int from = max(first, keys_seen(q, p.by_G.of(row0)) / kKeys);
+        const int end = min(keys_seen(q, p.by_G.of(row0 + row)), (first + n_steps) * kKeys);
+#pragma unroll 1
+        for (int key = from * kKeys; key < end; ++key) {
+          const uint32_t nan = nan_codes(value_codes(p, table, kvh, key, D, col));
+          if (nan & 0xffu) o.x = NAN;
+          if (nan & 0xff00u) o.y = NAN;
+          if (nan & 0xff0000u) o.z = NAN;
+          if (nan & 0xff000000u) o.w = NAN;
+        }
       }
       if (whole) {
         finish(row, col, o, top, total);
@@ -968,6 +1003,7 @@ struct ManySmem {
   float2 ml[128];                              // the second lane's statistics, where it has the first one's rows
   uint64_t seg_full[kSegments], seg_empty[kSegments], meet;
   Segment seg[kSegments];
+  int odd[kSegments];                          // NaN were taken out of a segment's values
   uint16_t scales[kScaleRing][4];
   int last, failed;
   uint32_t tmem_base;
@@ -984,6 +1020,11 @@ __device__ __forceinline__ void store32(void* to, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
                "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
+}
+
+// The first key of the key tiles of an item of many rows that not all its rows see whole.
+__device__ __forceinline__ int seen_by_all(const Params& p, const Segment& x) {
+  return keys_seen(x.q, p.by_G.of(x.tile * kManyRows)) / kTile * kTile;
 }
 
 // The key tiles of an item of n tiles that lane l takes.
@@ -1057,7 +1098,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (!more) x.hi = 0;
         ok = stage_wait(&sm.seg_empty[i % kSegments], ((i / kSegments) & 1) ^ 1, &sm.failed, kErrWaitEmpty, 500);
         if (lane == 0 && ok) {
-          sm.seg[i % kSegments] = x;
+          sm.seg[i % kSegments] = x, sm.odd[i % kSegments] = 0;
           mbar_arrive(&sm.seg_full[i % kSegments]);
         }
         if (more && i > 0) {                    // its queries on their way to L2; the first ones are asked for right away
@@ -1083,7 +1124,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       uint32_t tile = 0;
       while (const Segment* x = segment(0)) {
         int first;
-        const int n = x->stages<L, kTile>(p, first), len = x->q.len;
+        const int n = x->stages<L, kTile>(p, first), len = x->q.len, all_see = seen_by_all(p, *x);
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j, ++tile) {
           const uint32_t rs = tile % kRawStages, ws = tile % kWideStages;
@@ -1094,6 +1135,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           uint8_t* dst = sm.wide[v][ws];
           const int left = len - (first + j) * kTile;
           const bool tail = v && left < kTile;          // V's places behind the tokens hold anything: zeros
+          // A NaN among values that not all rows see would reach those rows too, as 0 times it: it is taken out, and put into
+          // the rows that see it with their output.
+          const bool edge = v && (first + j) * kTile >= all_see;
+          uint32_t odd = 0;
 #pragma unroll
           for (int plane = 0; plane < CH; ++plane) {
             uint4 c[4];
@@ -1104,6 +1149,16 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               for (int i = 0; i < 4; ++i)
                 if (key + 16 * i >= left) c[i] = make_uint4(0, 0, 0, 0);
             }
+            if (__builtin_expect(edge, 0)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint32_t& w = (&c[i].x)[e];
+                  const uint32_t nan = nan_codes(w);
+                  w &= ~nan, odd |= nan;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint8_t* at = dst + plane * kKvChunk + 2048 * i;
@@ -1111,6 +1166,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
               *reinterpret_cast<uint4*>(at + (to ^ 16)) = make_uint4(e4m3_low(c[i].z), e4m3_high(c[i].z), e4m3_low(c[i].w), e4m3_high(c[i].w));
             }
           }
+          if (odd) sm.odd[n_seg % kSegments] = 1;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.full[v][ws]), mbar_arrive(&sm.raw_empty[rs]);
@@ -1470,6 +1526,24 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (out) {
           if (whole) finish_lse(m, sum);
           else p.ml[slot(blockIdx.x) * kManyRows + row_item] = make_float2(m, sum);
+        }
+        // NaN that were taken out of the values: over the row's elements, of the keys that it sees of those that not all rows do
+        if (__builtin_expect(sm.odd[n_seg % kSegments] != 0 && out, 0)) {
+          const int32_t* table = p.a.block_table + static_cast<int64_t>(x.r) * p.a.max_blocks;
+          const int from = max(first * kTile, seen_by_all(p, x)), end = min(lim, (first + n) * kTile);
+#pragma unroll 1
+          for (int key = from; key < end; ++key) {
+#pragma unroll 1
+            for (int col = 0; col < D; col += 4) {
+              uint32_t nan = nan_codes(value_codes(p, table, x.head, key, D, col));
+#pragma unroll 1
+              for (int e = 0; nan != 0; ++e, nan >>= 8) {
+                if (!(nan & 1)) continue;
+                if (whole) p.a.O[at_row * D + col + e] = 0x7fff;         // a NaN in both types
+                else reinterpret_cast<float*>(part(blockIdx.x) + (col / 4) * kManyRows)[e] = NAN;
+              }
+            }
+          }
         }
       }
       tc_fence_before();

@@ -631,8 +631,8 @@ wq_status wq_kv_read_e4m3(wq_dtype dtype, const uint8_t* k_cache, const uint8_t*
  * Query head h uses key/value head h / (Hq / Hkv).  New token i of a request sees its keys j <= lens[r] - n + i
  * (the new tokens are in the cache already).  A row that sees no key gives O = 0 and lse = -inf.
  *   Q [T, Hq, d]: tokens q_stride elements apart (a multiple of 8, at least Hq d).
- *   Places past a request's length are not used, whatever they hold.  A NaN among the request's values
- *     reaches every row that sees it, and of its own new tokens may reach those before it.
+ *   Places past a request's length are not used, whatever they hold.  A NaN among the request's values reaches every
+ *     row that sees its token, also where the weight is 0, and no other; one among its keys those rows whole, and lse.
  *   O [T, Hq, d] dtype, lse [T, Hq] float32 (may be NULL): contiguous outputs, distinct from Q, the cache and each other.
  *   workspace / ws_bytes: at least wq_attn_e4m3_workspace_bytes(...) bytes, under the workspace rules of
  *     wq_gemm_workspace_bytes (it starts with the same header, left at zero).

@@ -1058,3 +1058,45 @@ def test_attend_elements_where_a_page_of_large_scale_holds_zeros(B, dtype, d, ne
     others = np.arange(d) != 7
     _within(_host(o)[..., others], ref[..., others], limit[..., others], "O")
     _within(_host(lse), ref_lse, _lse_limit(ref_lse, reach, n), "lse")
+
+
+@pytest.mark.parametrize("dtype,d,page", [("bf16", 128, 16), ("f16", 64, 64), ("bf16", 64, 32), ("f16", 128, 128)])
+@pytest.mark.parametrize("lens,news", [([40, 90], [3, 6]), ([33, 700], [8, 16]), ([100, 64], [30, 7]), ([150, 400], [70, 130]), ([20000, 70], [70, 70])])
+def test_attend_nan_among_new_values_reaches_no_row_before_them(B, dtype, d, page, lens, news):
+    """A NaN in the value of a new token makes that element NaN in the rows that see the token, and changes no other bit."""
+    import torch
+    c = Cache(94, lens, 2, d, page).fill(B, lens)
+    T, table, n, starts = sum(news), i32(c.table), i32(lens), i32([0, news[0], sum(news)])
+    q = torch.randn(T, 8, d, generator=torch.Generator().manual_seed(1)).to(_dt(dtype)).cuda()
+    clean = c.dev[1].clone()
+    want = B.attn_e4m3(q, *c.dev, table, n, starts, max(news))
+    first = [0, news[0]]
+    for marks in ([(1, -1, 0, 5)], [(0, -1, 1, d - 1)], [(1, 0, 1, 0)], [(0, news[0] // 2, 0, 17), (0, news[0] - 1, 0, 18), (1, news[1] // 3, 1, 33)],
+                  [(1, -2, 0, 62), (0, 1, 1, 40)]):
+        c.dev[1].copy_(clean)
+        nan = torch.zeros(T, 8, d, dtype=torch.bool, device="cuda")
+        for r, i, h, col in marks:                    # request, new token, key/value head, element
+            i %= news[r]
+            at = lens[r] - news[r] + i
+            c.dev[1][int(c.table[r, at // page]), h, at % page, col] = 0x7F if (i & 1) else 0xFF
+            nan[first[r] + i:first[r] + news[r], 4 * h:4 * h + 4, col] = True
+        o, lse = B.attn_e4m3(q, *c.dev, table, n, starts, max(news))
+        assert torch.equal(torch.isnan(o), nan), marks
+        assert torch.equal(o[~nan], want[0][~nan]) and torch.equal(lse, want[1])
+
+
+def test_attend_nan_values_of_new_tokens_in_items_that_are_joined(B):
+    """The same where the rows' keys are cut over many CTAs, for few rows and for many."""
+    import torch
+    for lens, news, Hq in (([30000], [4], 8), ([26000], [40], 16), ([26000], [200], 4)):
+        c = LongCache(95, lens, 1, 128, 64)
+        q = torch.randn(news[0], Hq, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+        args = i32(c.table), i32(lens), i32([0, news[0]]), news[0]
+        want = B.attn_e4m3(q, *c.dev, *args)
+        i = 2 * news[0] // 3
+        at = lens[0] - news[0] + i
+        c.dev[1][int(c.table[0, at // 64]), 0, at % 64, 70] = 0x7F
+        o, lse = B.attn_e4m3(q, *c.dev, *args)
+        nan = torch.zeros_like(o, dtype=torch.bool)
+        nan[i:, :, 70] = True
+        assert torch.equal(torch.isnan(o), nan) and torch.equal(o[~nan], want[0][~nan]) and torch.equal(lse, want[1])
