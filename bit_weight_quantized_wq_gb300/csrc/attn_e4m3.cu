@@ -29,7 +29,7 @@
 // bytes of two keys are interleaved as they are widened, so V needs no transposition, and an 8 x 8 transposition in
 // registers turns the scores into the fragment of P.  Bound by the bytes where requests are long: 64 requests over up to
 // 16384 keys, 64 heads on 8, 174 us, 6.2 TB/s; a short call by its chain of loads, barriers and the join: one request
-// over 500 keys 6.6 us, one over 131071 54 us.
+// over 500 keys 6.8 us, one over 131071 54 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -982,7 +982,8 @@ __global__ void __launch_bounds__(FewLine<NR>::kThreads, few_ctas(NR)) k_attn_e4
 // The products of a tile run while the softmax of the lane's tile before it, and of the other lane's, runs.  A warp walks
 // over the segments ahead of the others.  Bound by the products: a tile of 256 rows takes some 1820 cycles, and the
 // tensor core's part of them is 1760 (S has to read Q from shared memory for every 64 keys, as attn.cu says).  Pieces of
-// 3 prompts, 5119 new tokens over up to 10007 keys, 32 heads on 8: 399 us, 1081 TFLOP/s of what the rows see.
+// 3 prompts, 5119 new tokens over up to 10007 keys, 32 heads on 8: 338 to 413 us by how deep each lies, 1128 to 1165 TFLOP/s of
+// what the rows see.
 constexpr int kRawStages = 3;          // tiles of codes, K and V
 constexpr int kWideStages = 3;         // tiles of fp16, of K and of V
 constexpr int kScaleRing = 16;         // tiles' scales: more than the copies are ahead of the softmax warps

@@ -144,9 +144,11 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 
 // N threads (a warp or the CTA) have a page of one head's keys or values: P pieces of 8 elements each.
-// Bound by the bytes (2 read, 1 written an element) for prompts: 11006 tokens of 8 heads of 128 in pages of 64 take
-// 12.5 us, 5.4 TB/s (256 threads a page and head 13.6, 512 20.8: fewer bytes under way before a page's maximum is
-// known); by launch and dependent loads for decoding (starts and lengths, then the page and the tokens): one token 2.1 us.
+// Large calls of prompts come near the bytes (2 read, 1 written an element): 31850 tokens of 8 heads of 128 in pages of 64 35.7
+// us, 5.5 TB/s.  11006 tokens are two waves of CTAs, each of which loads a page, waits for its maximum, stores and ends: 18.8
+// us, 3.6 TB/s, and some 12 where the tokens are in L2 still (there 256 threads a page and head took 13.6, 512 20.8: fewer
+// bytes under way before a page's maximum is known).  Decoding is bound by launch and dependent loads (starts and
+// lengths, then the page and the tokens): one token 2.1 us.
 template <bool F16, int D, int N, int P, Find HOW>
 __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvAppendArgs a, int places) {
   constexpr int kRow = D / 8;                  // pieces a token
@@ -248,7 +250,7 @@ cudaError_t launch_append_t(const KvAppendArgs& a, unsigned pages, int places, c
 
 // Where no request can have more than two pages, as many places each: 512 requests of one token 8.3 us counted, 6.0 so.
 // Counting, which every CTA does for itself, is a load less than a search while it is one round of a CTA's threads (7
-// prompts 12.3 / 12.8 us); 512 requests with two pieces of 512 tokens among them 38 / 25 us, 4096 677 / 136.
+// prompts in L2 12.3 / 12.8 us); 512 requests with two pieces of 512 tokens among them 38 / 25 us, 4096 677 / 136.
 template <bool F16, int D>
 cudaError_t launch_append_t(const KvAppendArgs& a, cudaStream_t stream) {
   const int each = 1 + (a.max_new + a.page_size - 2) / a.page_size;      // pages that max_new tokens of a request lie in
