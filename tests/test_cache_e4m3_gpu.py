@@ -1100,3 +1100,71 @@ def test_attend_nan_values_of_new_tokens_in_items_that_are_joined(B):
         nan = torch.zeros_like(o, dtype=torch.bool)
         nan[i:, :, 70] = True
         assert torch.equal(torch.isnan(o), nan) and torch.equal(o[~nan], want[0][~nan]) and torch.equal(lse, want[1])
+
+
+# ------------------------------------------------------------------------------ calls of unusual shape
+@pytest.mark.parametrize("dtype,d,page", [("bf16", 128, 16), ("f16", 64, 128)])
+@pytest.mark.parametrize("lens,news,Hq,Hkv", [([20, 0, 300], [70, 40, 50], 8, 2), ([1, 64, 65], [300, 65, 64], 4, 4), ([0], [90], 8, 1),
+                                              ([250, 40], [3, 1], 128, 1), ([130], [130], 7, 7)])
+def test_attend_more_new_tokens_than_keys_and_wide_groups(B, dtype, d, page, lens, news, Hq, Hkv):
+    c = Cache(96, lens, Hkv, d, page).fill(B, lens) if sum(lens) else Cache(96, lens, Hkv, d, page)
+    _attend(B, c, lens, news, Hq, dtype)
+
+
+@pytest.mark.parametrize("news", [1, 6, 90])
+def test_attend_queries_inside_a_fused_projection(B, news):
+    import torch
+    lens = [news + 70, news + 3]
+    c = Cache(97, lens, 2, 128, 32).fill(B, lens)
+    x = torch.randn(2 * news, 8 + 4 + 1, 128, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    x[:, 8:] = float("nan")
+    _attend(B, c, lens, [news, news], 8, "bf16", q=x[:, :8])
+
+
+@pytest.mark.parametrize("most", [1, 100])
+def test_calls_of_requests_without_new_tokens(B, most):
+    """A batch that is all padding: nothing is written, nothing reported."""
+    import torch
+    lens = [40, 0, 7]
+    c = Cache(98, lens, 2, 64, 16).fill(B, lens)
+    before = [x.clone() for x in c.dev]
+    starts, table, n = i32([0, 0, 0, 0]), i32(c.table), i32(lens)
+    out = torch.full((5, 8, 64), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((5, 8), 4.0, device="cuda")
+    q = torch.randn(5, 8, 64).bfloat16().cuda()
+    B.attn_e4m3(q, *c.dev, table, n, starts, most, out=out)
+    B.kv_append_e4m3(q[:, :2], q[:, 2:4], *c.dev, table, n, starts, most)
+    read = [torch.full((5, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    B.kv_read_e4m3(*c.dev, table, starts, 5, out=read)
+    torch.cuda.synchronize()
+    assert torch.all(out[0] == 3) and torch.all(out[1] == 4) and all(torch.all(x == 5) for x in read)
+    assert all(torch.equal(a, b) for a, b in zip(before, c.dev))
+
+
+@pytest.mark.parametrize("lens,news", [([90, 200], [1, 1]), ([90, 9000], [40, 3])])
+def test_attend_without_lse(B, lens, news):
+    """The C call may leave lse out; O is the same."""
+    import ctypes
+
+    import torch
+    c = Cache(99, lens, 2, 64, 32).fill(B, lens)
+    T, most = sum(news), max(news)
+    q = torch.randn(T, 8, 64, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    table, n, starts = i32(c.table), i32(lens), i32(np.concatenate(([0], np.cumsum(news))))
+    want, _ = B.attn_e4m3(q, *c.dev, table, n, starts, most)
+    lib, o = B.load_library(), torch.empty_like(q)
+    ws = torch.zeros(lib.wq_attn_e4m3_workspace_bytes(T, 2, 8, 2, 64, most), dtype=torch.uint8, device="cuda")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())   # noqa: E731
+    st = lib.wq_attn_e4m3(0, p(q), 512, T, 2, 8, 2, 64, *[p(x) for x in c.dev], c.dev[0].shape[0], 32, p(table), c.table.shape[1], p(n), p(starts),
+                          most, 0.125, p(o), None, p(ws), ws.numel(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and torch.equal(o, want)
+
+
+@pytest.mark.parametrize("prompts", [{0: 40, 700: 50, 1299: 60}, {600: 300}])
+def test_attend_more_requests_than_a_cta_has_threads(B, prompts):
+    news = [1] * 1300
+    for r, n in prompts.items():
+        news[r] = n
+    lens = [n + m for n, m in zip(news, np.random.default_rng(10).integers(0, 30, 1300).tolist())]
+    c = Cache(100, lens, 1, 64, 16).fill(B, lens)
+    _attend(B, c, lens, news, 4, "bf16")
